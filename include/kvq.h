@@ -372,6 +372,195 @@ KVQ_API kvq_status kv_attend_decode_static(const kvq_cache *cache, const void *q
                                            void *out, int32_t out_dtype, int32_t *dev_status,
                                            kvq_stream_t stream);
 
+/*
+ * Rotary positions. Pair i of a head (of rotary_dim / 2 pairs) turns by the
+ * angle pos * f_i, f_i = base^(-2 i / rotary_dim) before scaling; features past
+ * rotary_dim pass through. KVQ_ROPE_HALF pairs features i and
+ * i + rotary_dim / 2, KVQ_ROPE_INTERLEAVED features 2i and 2i + 1.
+ * Scaling for contexts longer than the trained one:
+ *   NONE    f_i as above; the other fields are ignored.
+ *   LINEAR  f_i / factor.
+ *   BASE    base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *           (rotary_dim >= 4).
+ *   RAMP    pairs that turn often over the original context keep f_i, pairs
+ *           that turn seldom take f_i / factor, linear in i between
+ *           floor(x(p0)) and ceil(x(p1)) (clamped to [0, rotary_dim - 1]),
+ *           x(r) = rotary_dim ln(original / (2 pi r)) / (2 ln base) the pair
+ *           that makes r turns; the rotation is multiplied by
+ *           0.1 ln(factor) + 1.
+ *   BANDS   with r = original f_i / (2 pi) turns, w = (r - p0) / (p1 - p0)
+ *           clamped to [0, 1]: w f_i + (1 - w) f_i / factor.
+ */
+typedef enum { KVQ_ROPE_HALF = 0, KVQ_ROPE_INTERLEAVED = 1 } kvq_rope_layout;
+typedef enum {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_BASE = 2,
+  KVQ_ROPE_RAMP = 3,
+  KVQ_ROPE_BANDS = 4
+} kvq_rope_scaling_kind;
+
+typedef struct kvq_rope_scaling {
+  int32_t kind;    /* kvq_rope_scaling_kind */
+  double factor;   /* >= 1 */
+  double original; /* RAMP, BANDS: tokens of the trained context (> 0) */
+  double p0, p1;   /* RAMP: turns kept from / scaled to, p0 > p1 > 0; BANDS: p1 > p0 >= 0 */
+} kvq_rope_scaling;
+
+/*
+ * The frequency table of kv_rope: turns[i] = f_i / (2 pi) as a 64-bit binary
+ * fraction of a turn, so that pos * turns[i] modulo 2^64 is the phase of any
+ * position with no loss at far ones. turns: HOST array of rotary_dim / 2
+ * entries (the caller copies it to the device once); *amplitude receives the
+ * factor on the rotation. scaling may be NULL (NONE). Host only. KVQ_ERR_ARG
+ * for an odd or non-positive rotary_dim, one above 256, base <= 1 or a
+ * scaling outside the limits above.
+ */
+KVQ_API kvq_status kvq_rope_turns(int32_t rotary_dim, double base, const kvq_rope_scaling *scaling,
+                                  uint64_t *turns, float *amplitude);
+
+/* One tensor of kv_rope: element (b, h, t, d) of the input lies at
+ * in[b * stride_b + h * stride_h + t * stride_t + d] (strides in elements);
+ * the output is dense [batch][heads][n][head_dim], as the other calls read q
+ * and new keys and values. rotate == 0 only copies (values that come out of
+ * the same projection). in == out is allowed with the dense strides; other
+ * overlaps are not. */
+typedef struct kvq_rope_tensor {
+  const void *in;
+  void *out;
+  int32_t heads;
+  int32_t rotate;
+  int64_t stride_b, stride_h, stride_t;
+} kvq_rope_tensor;
+
+/*
+ * kv_rope -- rotary positions of up to three tensors (q, k and, copied, v of
+ * one projection) in one kernel: y0 = a (x0 cos - x1 sin), y1 = a (x0 sin +
+ * x1 cos) per pair, a the amplitude, computed in fp32 and rounded once.
+ * tensors: HOST array of n_tensors (1..3) entries, all of `dtype` (F32 or
+ * BF16), read before the call returns. positions: device int32 [batch][n], any
+ * values (negative ones turn backwards). turns: device copy of kvq_rope_turns'
+ * table. inverse != 0 applies the transposed rotation (angle negated, same
+ * amplitude): the gradient of the call with respect to its input, and with
+ * amplitude 1 what takes a position off a key.
+ * rotary_dim: even, 2 <= rotary_dim <= head_dim; head_dim as everywhere.
+ * Strides must be >= 0 and multiples of 16 bytes (KVQ_ERR_ALIGN).
+ * KVQ_ERR_UNSUPPORTED when batch * n exceeds 2^31 - 1. n == 0 and batch == 0
+ * are valid and enqueue nothing.
+ */
+KVQ_API kvq_status kv_rope(const kvq_rope_tensor *tensors, int32_t n_tensors, int32_t dtype,
+                           int32_t batch, int32_t n, int32_t head_dim, int32_t rotary_dim,
+                           int32_t layout, const uint64_t *turns, float amplitude,
+                           int32_t inverse, const int32_t *positions, int32_t *dev_status,
+                           kvq_stream_t stream);
+
+/*
+ * kv_attend_tree -- attention of drafted tokens that are not in the cache yet:
+ * n_tree (T) tokens per sequence, a forest given by parents: device int32
+ * [batch][T]. parents[b][i] is the drafted token that token i follows (below
+ * i), -1 when it follows the cache's last token, or -2 when row i holds no
+ * token (a smaller tree in a padded batch): such a row's output is left as it
+ * was and no row sees it. Token i attends every token of the cache, itself
+ * and its ancestors, with K and V of the drafted tokens taken from
+ * k_tree, v_tree: [batch][kv_heads][T][D] in tree_dtype (F32 or BF16). A
+ * chain (parents[i] = i - 1) is causal attention of T new tokens.
+ * q: [batch][q_heads][T][D], out likewise, as kv_attend (their row i is token
+ * i). Contents of k_tree, v_tree and q where a row holds no token, and of any
+ * drafted token for the rows that do not see it, never reach an output,
+ * infinities and NaN included.
+ * A parent outside [-2, i), or that is itself no token, is flagged
+ * KVQ_DEV_INDEX and its row treated as holding no token.
+ * 1 <= T <= KVQ_TREE_MAX (else KVQ_ERR_ARG); an MXFP8 K window rounds Q to
+ * MXFP8 for every key, drafted ones included.
+ * workspace/ws_bytes as kv_attend.
+ * Kernel choice: D = 128, bf16 q and tree and a bf16 window (or none) run on
+ * the tensor cores with fp16 operands: the int4 part as code * scale (the
+ * scale and the product each rounded once to fp16, 11 bits), q, window and
+ * drafted rows converted from bf16 (exact within fp16's normal range, 6e-5 to
+ * 65504; larger finite values are clamped to it), products and sums in fp32.
+ * Other shapes run an fp32 kernel (q_heads and batch <= 65,535).
+ */
+#define KVQ_TREE_MAX 256
+KVQ_API kvq_status kv_attend_tree(const kvq_cache *cache, const void *q, int32_t q_dtype,
+                                  int32_t q_heads, int32_t n_tree, const void *k_tree,
+                                  const void *v_tree, int32_t tree_dtype, const int32_t *parents,
+                                  float sm_scale, void *out, int32_t out_dtype, void *workspace,
+                                  size_t *ws_bytes, int32_t *dev_status, kvq_stream_t stream);
+
+/*
+ * Block summaries: for every block of `block` (32, 64 or 128) consecutive
+ * tokens of a cache's int4 part one int8 mean key, from which
+ * kv_select_blocks scores the block. There are n_blocks = ceil((N - R) / block)
+ * of them; the last may hold fewer tokens.
+ *   codes  [batch][kv_heads][cap_blocks][D]  int8, in [-127, 127]
+ *   scales [batch][kv_heads][cap_blocks]     float
+ * Entries past n_blocks are not read or written.
+ */
+typedef struct kvq_summary {
+  int8_t *codes;
+  float *scales;
+  int32_t block;
+  int32_t cap_blocks;
+} kvq_summary;
+
+/*
+ * kv_block_summary -- (re)compute the summaries of blocks [first_block,
+ * n_blocks) from the cache's K codes and scales. With c the int4 codes of a
+ * group and s its scale of a channel: part_g = fl(s * sum c) per 32-token
+ * group, the groups' parts added in order in fp32, mean = fl(sum / tokens),
+ * scale = fl(max over D of |mean| / 127), code = rint(fl(mean / scale)), ties
+ * to even (0 for a zero scale): integers and single fp32 roundings, so the
+ * result does not depend on the order of the work. After kv_append moved
+ * groups out of the window, the blocks from floor(old cut / block) on are
+ * new; first_block >= n_blocks enqueues nothing.
+ * KVQ_ERR_ARG: block not 32, 64 or 128, first_block < 0; KVQ_ERR_WORKSPACE:
+ * cap_blocks < n_blocks.
+ */
+KVQ_API kvq_status kv_block_summary(const kvq_cache *cache, const kvq_summary *summary,
+                                    int32_t first_block, int32_t *dev_status,
+                                    kvq_stream_t stream);
+
+/*
+ * kv_select_blocks -- for each query token of each KV head the top_k blocks by
+ * a cheap score. Each query row is rounded to int8 (scale s_q = fl(max|q| /
+ * 127), code = rint(fl(q / s_q))); a block's score for a head is
+ * fl(fl(s_q * s_b) * d), d the integer product of the codes, and its score
+ * for the KV head the largest over the query heads that share it. Equal
+ * scores: the lower block first. The first n_sink blocks are always taken
+ * (before the others, n_sink <= top_k). Every step is exact or a single fp32
+ * rounding, so the choice is the same whatever the order of the work.
+ * q: [batch][q_heads][n_q][D] in q_dtype (F32 or BF16), finite.
+ * selected: device int32 [batch][kv_heads][n_q][top_k], the chosen blocks in
+ * increasing order, then -1 when the cache has fewer than top_k blocks.
+ * workspace/ws_bytes as kv_attend. KVQ_ERR_UNSUPPORTED for q_heads / kv_heads
+ * above 64, batch * kv_heads * n_q above 65,535.
+ */
+KVQ_API kvq_status kv_select_blocks(const kvq_cache *cache, const kvq_summary *summary,
+                                    const void *q, int32_t q_dtype, int32_t q_heads, int32_t n_q,
+                                    int32_t top_k, int32_t n_sink, int32_t *selected,
+                                    void *workspace, size_t *ws_bytes, int32_t *dev_status,
+                                    kvq_stream_t stream);
+
+/*
+ * kv_attend_blocks -- exact attention of each query token over the tokens of
+ * its listed blocks and the whole window. selected: device int32
+ * [batch][kv_heads][n_q][top_k] as kv_select_blocks writes it (any list of
+ * increasing blocks in [0, n_blocks), closed by -1 entries, may be passed).
+ * All query heads of a KV head share a list. An entry outside the blocks
+ * (other than -1) is skipped and flagged KVQ_DEV_INDEX; one that does not
+ * exceed the entry before it is skipped and flagged KVQ_DEV_DUP (the list's
+ * rows are then invalid). Rows with no key at all (no window, an empty list)
+ * are zero. q, out, workspace/ws_bytes as kv_attend.
+ * Kernel choice: D = 128, bf16 q, a bf16 window (or none) and at most 8 query
+ * heads per KV head run the decode kernels over the listed blocks; other
+ * shapes run an fp32 kernel (q_heads and batch <= 65,535).
+ */
+KVQ_API kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32_t q_dtype,
+                                    int32_t q_heads, int32_t n_q, const int32_t *selected,
+                                    int32_t top_k, int32_t block, float sm_scale, void *out,
+                                    int32_t out_dtype, void *workspace, size_t *ws_bytes,
+                                    int32_t *dev_status, kvq_stream_t stream);
+
 /* Number of kernel launches the last successful call on this thread enqueued. */
 KVQ_API int32_t kvq_last_launch_count(void);
 

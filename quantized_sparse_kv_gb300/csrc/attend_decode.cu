@@ -28,6 +28,15 @@
 // bf16 MMAs with q and P split into hi + lo bf16 parts. Softmax runs in the
 // log2 domain with fp32 state.
 //
+// Listed blocks (kv_attend_blocks, the kList variant). A unit is then one query
+// token of a (sequence, KV head); its int4 items are its listed blocks' groups
+// taken four at a time, so the four groups of an item come from up to four
+// places: lanes 0-3 of the loader warp each copy one group (and note how many
+// of its tokens exist, 0 for a skipped entry), from list entries the whole warp
+// reads eight items ahead. Everything behind the copies is the same code; with
+// fewer than 8 query heads per KV head the missing rows of the MMA are zero and
+// not stored.
+//
 // Feature order. Within a thread, features are visited in a fixed permutation
 // (the one that makes a 16-byte row slice of nibbles a ready MMA operand); the
 // same permutation is used for q and K, and the output is written back in
@@ -37,6 +46,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "int4_dequant.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -82,7 +92,20 @@ struct DecodeArgs {
   float scale_log2;
   float *partials;                  // [units][max_ctas_per_unit][8][132]
   KernelCtl ctl;
+  // listed blocks: lists [unit][top_k], groups per block, blocks of the cache,
+  // query tokens per (sequence, KV head), query heads per KV head
+  const int32_t *list;
+  int top_k, gpb, n_blocks, n_q, heads;
 };
+
+// Query (and output) row of head g of unit u; kList: unit = (sequence, KV
+// head, query token).
+template <bool kList>
+__device__ __forceinline__ long q_row(const DecodeArgs &a, int u, int g) {
+  if (!kList) return static_cast<long>(u) * kHeads + g;
+  const int un = u / a.n_q;
+  return (static_cast<long>(un) * a.heads + g) * a.n_q + (u - un * a.n_q);
+}
 
 // ------------------------------------------------------------------ PTX wrappers
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -93,40 +116,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
-
-// (w & kMask) | kMagic as one three-input logic op.
-template <uint32_t kMask, uint32_t kMagic>
-__device__ __forceinline__ uint32_t and_or(uint32_t w) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(kMask), "n"(kMagic));
-  return d;
-}
-
-// Nibbles at bits 0-3 and 16-19 -> fp16 codes: 0x6400 | n is 1024 + n, n = code + 8.
-__device__ __forceinline__ uint32_t dq_lo(uint32_t w) {
-  const uint32_t x = and_or<0x000F000Fu, 0x64006400u>(w);
-  return as_u32(__hsub2(as_h2(x), as_h2(0x64086408u)));  // 1032
-}
-// Nibbles at bits 4-7 and 20-23: 0x5400 | n << 4 is 64 + n.
-__device__ __forceinline__ uint32_t dq_hi(uint32_t w) {
-  const uint32_t x = and_or<0x00F000F0u, 0x54005400u>(w);
-  return as_u32(__hsub2(as_h2(x), as_h2(0x54805480u)));  // 72
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  return as_u32(__floats2half2_rn(lo, hi));
-}
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
 // ------------------------------------------------------------------ per-warp state
 struct WarpState {
@@ -357,11 +346,13 @@ struct __align__(16) DecodeSmem {
   uint64_t full[kStages];
   uint64_t empty[kStages];
   int abort_flag;
+  int valid[kStages][kConsumers];   // kList: tokens of each group of the item
 };
 
+template <bool kList>
 __device__ __forceinline__ void load_q(const DecodeArgs &a, int u, int g, int t,
                                        uint32_t (&qh)[4][4]) {
-  const long row = static_cast<long>(u) * kHeads + g;  // query head kvh * 8 + g of sequence b
+  const long row = q_row<kList>(a, u, g);  // query head kvh * 8 + g of sequence b
   float qr[32];
   if (a.q_dtype == KVQ_F32) {
     const float *q = static_cast<const float *>(a.q) + row * kD + 32 * t;
@@ -387,21 +378,23 @@ struct QRaw {
   uint4 w[4];
 };
 
+template <bool kList>
 __device__ __forceinline__ void load_q_raw(const DecodeArgs &a, int u, int g, int t, QRaw &r) {
-  if (a.q_dtype == KVQ_F32) return;  // fp32 rows are loaded when converted
-  const long row = static_cast<long>(u) * kHeads + g;
+  if (!kList && a.q_dtype == KVQ_F32) return;  // fp32 rows are loaded when converted
+  const long row = q_row<kList>(a, u, g);
   const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + row * kD +
                                                    32 * t);
-  const bool ok = in_bounds(a.ctl, p, 4 * sizeof(uint4));
+  const bool ok = (!kList || g < a.heads) && in_bounds(a.ctl, p, 4 * sizeof(uint4));
 #pragma unroll
   for (int i = 0; i < 4; ++i) r.w[i] = ok ? p[i] : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // load_q from a prefetched bf16 slice (the same values).
+template <bool kList>
 __device__ __forceinline__ void q_from_raw(const DecodeArgs &a, int u, int g, int t,
                                            const QRaw &r, uint32_t (&qh)[4][4]) {
-  if (a.q_dtype == KVQ_F32) {
-    load_q(a, u, g, t, qh);
+  if (!kList && a.q_dtype == KVQ_F32) {  // (lists come with bf16 queries)
+    load_q<kList>(a, u, g, t, qh);
     return;
   }
   float qr[32];
@@ -458,6 +451,66 @@ __device__ __forceinline__ void load_item(const DecodeArgs &a, int u, int j, uin
   }
 }
 
+// kList: the cache group that group slot w of the CTA's item k holds, or -1 (a
+// window item, past the list, or a skipped entry, which is flagged).
+__device__ __forceinline__ int listed_group(const DecodeArgs &a, int x, int w) {
+  const int u = x / a.ipu, j = x - u * a.ipu;
+  if (j >= a.Gi) return -1;
+  const int gl = kGroupsPerItem * j + w, e = gl / a.gpb, sub = gl - e * a.gpb;
+  if (e >= a.top_k) return -1;
+  const int32_t *l = a.list + static_cast<long>(u) * a.top_k + e;
+  if (!in_bounds(a.ctl, e > 0 ? l - 1 : l, sizeof(int32_t) * (e > 0 ? 2 : 1))) return -1;
+  const int blk = *l, prev = e > 0 ? l[-1] : -2;
+  if (blk == -1) return -1;
+  int bit = 0;
+  if (blk < 0 || blk >= a.n_blocks || prev == -1)
+    bit = KVQ_DEV_INDEX;
+  else if (blk <= prev)
+    bit = KVQ_DEV_DUP;
+  if (bit) {
+    if (sub == 0) flag_error(a.ctl, bit);
+    return -1;
+  }
+  const int g = blk * a.gpb + sub;
+  return g < a.Gk ? g : -1;  // (the last block may hold fewer groups)
+}
+
+// kList: lane w's share of item j of unit u, group grp of the cache (or -1),
+// or of a window item.
+__device__ __forceinline__ void load_listed(const DecodeArgs &a, DecodeSmem &sm, int u, int j,
+                                            int grp, int w, int st) {
+  const uint32_t dst = smem_u32(sm.stage[st]), bar = smem_u32(&sm.full[st]);
+  const int cu = u / a.n_q;
+  if (j >= a.Gi) {
+    const int w0 = kWinItem * (j - a.Gi);
+    const long wi = static_cast<long>(cu) * a.Ws + w0;
+    const uint32_t bytes = 256u * min(kWinItem, a.R - w0);
+    // lane 0 copies K, lane 1 V
+    const uint16_t *src = w == 0 ? a.k_window + wi * 128 : a.v_window + wi * 128;
+    const bool ok = w < 2 && in_bounds(a.ctl, src, bytes);
+    mbar_arrive_expect_tx(bar, ok ? bytes : 0u);
+    if (ok) bulk_g2s(dst + (w == 0 ? 0 : kOffVWin), src, bytes, bar);
+    return;
+  }
+  const int nt = grp < 0 ? 0 : min(32, a.cut - 32 * grp);
+  sm.valid[st][w] = nt;
+  if (nt <= 0) {
+    mbar_arrive_expect_tx(bar, 0u);
+    return;
+  }
+  const long gi = static_cast<long>(cu) * a.Gs + grp, ti = static_cast<long>(cu) * a.Vs + 32 * grp;
+  const uint32_t vb = 64u * nt, wb = 16u * nt;
+  const bool ok0 = in_bounds(a.ctl, a.k_codes + gi * 2048, 2048);
+  const bool ok1 = in_bounds(a.ctl, a.k_scales + gi * 128, 512);
+  const bool ok2 = in_bounds(a.ctl, a.v_codes + ti * 64, vb);
+  const bool ok3 = in_bounds(a.ctl, a.v_scales + ti * 4, wb);
+  mbar_arrive_expect_tx(bar, (ok0 ? 2048u : 0u) + (ok1 ? 512u : 0u) + (ok2 ? vb : 0u) + (ok3 ? wb : 0u));
+  if (ok0) bulk_g2s(dst + 2048u * w, a.k_codes + gi * 2048, 2048u, bar);
+  if (ok1) bulk_g2s(dst + kOffKScale + 512u * w, a.k_scales + gi * 128, 512u, bar);
+  if (ok2) bulk_g2s(dst + kOffVCode + 2048u * w, a.v_codes + ti * 64, vb, bar);
+  if (ok3) bulk_g2s(dst + kOffVScale + 512u * w, a.v_scales + ti * 4, wb, bar);
+}
+
 // First CTA of the persistent grid whose slice holds item x: the largest c
 // with floor(c * T / C) <= x.
 __device__ __forceinline__ int cta_of_item(const DecodeArgs &a, int x) {
@@ -468,6 +521,7 @@ __device__ __forceinline__ float *partial_of(const DecodeArgs &a, int u, int slo
   return a.partials + (static_cast<long>(u) * a.max_ctas_per_unit + slot) * (kHeads * kPartFloats);
 }
 
+template <bool kList>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   DecodeSmem &sm = *reinterpret_cast<DecodeSmem *>(smem_raw);
@@ -484,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.full[s]), kList ? kGroupsPerItem : 1);
       mbar_init(smem_u32(&sm.empty[s]), kConsumers);
     }
     sm.abort_flag = 0;
@@ -497,7 +551,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
 
   if (warp == kConsumers) {
     // ---------------- loader: one lane walks the CTA's items in order
-    if (lane == 0) {
+    if constexpr (kList) {
+      // lanes 0-3 copy, all 32 read the list entries of the next eight items
+      const int w = lane & 3;
+      int k = 0, u = u_first, j = lo - u_first * a.ipu, ents = 0;
+      for (; k < n_items; ++k) {
+        const int st = k % kStages;
+        if ((k & 7) == 0) {
+          const int kk = k + (lane >> 2);
+          ents = kk < n_items ? listed_group(a, lo + kk, w) : -1;
+        }
+        const int grp = __shfl_sync(0xffffffffu, ents, 4 * (k & 7) + w);
+        bool go = true;
+        if (k >= kStages) {
+          const uint32_t par = static_cast<uint32_t>((k / kStages - 1) & 1);
+          go = mbar_wait(smem_u32(&sm.empty[st]), par, a.ctl.wait_limit_ns);
+          if (!go) {
+            flag_error(a.ctl, KVQ_DEV_TIMEOUT);
+            *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+          }
+        }
+        if (__any_sync(0xffffffffu, !go || aborted_flag(sm))) break;
+        if (lane < kGroupsPerItem && lo + k != a.ctl.drop_item)
+          load_listed(a, sm, u, j, grp, w, st);
+        if (++j == a.ipu) {
+          j = 0;
+          ++u;
+        }
+      }
+      for (int d = max(0, k - kStages); d < k; ++d) {
+        if (lo + d == a.ctl.drop_item) continue;
+        mbar_wait(smem_u32(&sm.full[d % kStages]), static_cast<uint32_t>((d / kStages) & 1),
+                  2000000000ull);
+      }
+    } else if (lane == 0) {
       int k = 0, u = u_first, j = lo - u_first * a.ipu;
       for (; k < n_items; ++k) {
         const int st = k % kStages;
@@ -532,11 +619,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
   WarpState st;
   uint32_t qh[4][4];
   QRaw qraw;
-  load_q_raw(a, u_first, g, t, qraw);
+  load_q_raw<kList>(a, u_first, g, t, qraw);
   int k = 0;  // CTA-relative item index
   for (int u = u_first; u * a.ipu < hi; ++u) {
     state_reset(st);
-    q_from_raw(a, u, g, t, qraw, qh);
+    q_from_raw<kList>(a, u, g, t, qraw, qh);
     const int u_end = min(hi, (u + 1) * a.ipu) - lo;  // CTA-relative end of unit u
     int j = lo + k - u * a.ipu;                        // item index within unit u
     bool aborted = false;
@@ -558,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
       const uint8_t *stg = sm.stage[s];
       if (j < a.Gi) {
         const int grp = kGroupsPerItem * j + warp;
-        const int valid = a.cut - 32 * grp;
+        const int valid = kList ? sm.valid[s][warp] : a.cut - 32 * grp;
         const uint8_t *kc = stg + warp * 2048, *vc = stg + kOffVCode + warp * 2048;
         const float *ks = reinterpret_cast<const float *>(stg + kOffKScale + warp * 512);
         const float *vs = reinterpret_cast<const float *>(stg + kOffVScale + warp * 512);
@@ -577,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
       if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
     }
     // the next unit's query rows are in flight during the merge
-    if ((u + 1) * a.ipu < hi) load_q_raw(a, u + 1, g, t, qraw);
+    if ((u + 1) * a.ipu < hi) load_q_raw<kList>(a, u + 1, g, t, qraw);
     // ---- merge the 4 warps' states for unit u and write one partial
     float l0 = st.l[0], l1 = st.l[1];
 #pragma unroll
@@ -649,20 +736,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
 // slices overlap the unit (log-sum-exp), normalise, store. The partials of
 // unit u sit in consecutive slots, one per overlapping CTA; they are read
 // sixteen at a time with all loads of a batch in flight together.
-template <typename OT>
+template <typename OT, bool kList>
 __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__restrict__ out) {
   wait_prior_grid();
   allow_next_grid();  // the next call's decode grid may be placed while this one runs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = blockIdx.x;
   const int h = warp;
+  if (kList && h >= a.heads) return;
   const int n = cta_of_item(a, (u + 1) * a.ipu - 1) - cta_of_item(a, u * a.ipu) + 1;
   const float *base = partial_of(a, u, 0) + h * kPartFloats;
   constexpr int kSlot = kHeads * kPartFloats;
 #ifdef KVQ_DEBUG
   // the unit's partial slots and this head's output row (the same in every lane)
   if (!in_bounds(a.ctl, base - h * kPartFloats, sizeof(float) * n * kSlot) ||
-      !in_bounds(a.ctl, out + (static_cast<long>(u) * kHeads + h) * kD, kD * sizeof(OT)))
+      !in_bounds(a.ctl, out + q_row<kList>(a, u, h) * kD, kD * sizeof(OT)))
     return;
 #endif
   constexpr int kBatch = 16;
@@ -700,8 +788,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__
     }
     m = nm;
   }
-  const float inv = 1.0f / l;
-  OT *o = out + (static_cast<long>(u) * kHeads + h) * kD + 4 * lane;
+  const float inv = kList && l == 0.0f ? 0.0f : 1.0f / l;  // a list may hold no key
+  OT *o = out + q_row<kList>(a, u, h) * kD + 4 * lane;
   store_from_f32(o + 0, acc.x * inv);
   store_from_f32(o + 1, acc.y * inv);
   store_from_f32(o + 2, acc.z * inv);
@@ -714,7 +802,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__
 // warps' states merged through shared memory.
 constexpr int kWideCombineAbove = 32;  // slots per unit above which it is used
 
-template <typename OT>
+template <typename OT, bool kList>
 __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
                                                            OT *__restrict__ out) {
   wait_prior_grid();
@@ -723,12 +811,13 @@ __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
   __shared__ float4 sm_acc[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = blockIdx.x, h = blockIdx.y;
+  if (kList && h >= a.heads) return;
   const int n = cta_of_item(a, (u + 1) * a.ipu - 1) - cta_of_item(a, u * a.ipu) + 1;
   const float *base = partial_of(a, u, 0) + h * kPartFloats;
   constexpr int kSlot = kHeads * kPartFloats;
 #ifdef KVQ_DEBUG
   if (!in_bounds(a.ctl, base - h * kPartFloats, sizeof(float) * n * kSlot) ||
-      !in_bounds(a.ctl, out + (static_cast<long>(u) * kHeads + h) * kD, kD * sizeof(OT)))
+      !in_bounds(a.ctl, out + q_row<kList>(a, u, h) * kD, kD * sizeof(OT)))
     return;
 #endif
   constexpr int kBatch = 8;
@@ -789,8 +878,8 @@ __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
     o4.z += c * x.z;
     o4.w += c * x.w;
   }
-  const float inv = 1.0f / ls;
-  OT *o = out + (static_cast<long>(u) * kHeads + h) * kD + 4 * lane;
+  const float inv = kList && ls == 0.0f ? 0.0f : 1.0f / ls;
+  OT *o = out + q_row<kList>(a, u, h) * kD + 4 * lane;
   store_from_f32(o + 0, o4.x * inv);
   store_from_f32(o + 1, o4.y * inv);
   store_from_f32(o + 2, o4.z * inv);
@@ -803,13 +892,13 @@ struct Plan {
   long units;
 };
 
-Plan make_plan(const kvq_cache &c, int num_sms) {
-  const CacheDims d = dims_of(c);
+// `groups` int4 groups and R window tokens for each of `units` units.
+Plan plan_of(long units, int groups, int R, int num_sms) {
   Plan p;
-  p.Gi = (d.Gk + kGroupsPerItem - 1) / kGroupsPerItem;
-  p.Wt = (d.R + kWinItem - 1) / kWinItem;
+  p.Gi = (groups + kGroupsPerItem - 1) / kGroupsPerItem;
+  p.Wt = (R + kWinItem - 1) / kWinItem;
   p.ipu = p.Gi + p.Wt;
-  p.units = static_cast<long>(d.B) * d.Hkv;
+  p.units = units;
   const long total = p.units * p.ipu;
   p.total_items = static_cast<int>(std::min<long>(total, 1L << 30));
   p.num_ctas = static_cast<int>(std::min<long>(total, static_cast<long>(kCtasPerSm) * num_sms));
@@ -820,28 +909,21 @@ Plan make_plan(const kvq_cache &c, int num_sms) {
   return p;
 }
 
-}  // namespace
-
-bool decode_supported(const kvq_cache &c, int q_dtype, int Hq, int n_q) {
-  const bool win_ok = c.recent == 0 || (c.kwin_dtype == KVQ_BF16 && c.vwin_dtype == KVQ_BF16);
-  const long items = static_cast<long>(c.batch) * c.kv_heads *
-                    ((c.n_tokens - c.recent + 32 * kGroupsPerItem - 1) / (32 * kGroupsPerItem) +
-                     (c.recent + kWinItem - 1) / kWinItem);
-  return c.head_dim == kD && n_q == 1 && Hq == kHeads * c.kv_heads && win_ok &&
-         (q_dtype == KVQ_BF16 || q_dtype == KVQ_F32) && c.n_tokens > 0 && items < (1L << 30);
-}
-
-size_t decode_workspace_bytes(const kvq_cache &c, int, int num_sms) {
-  const Plan p = make_plan(c, num_sms);
-  return sizeof(float) * static_cast<size_t>(p.units) * p.max_ctas_per_unit * kHeads * kPartFloats;
-}
-
-int launch_attend_decode(const kvq_cache &c, const void *q, int q_dtype, float scale_log2,
-                         void *out, int out_dtype, void *ws, const KernelCtl &ctl, int num_sms,
-                         cudaStream_t s) {
+Plan make_plan(const kvq_cache &c, int num_sms) {
   const CacheDims d = dims_of(c);
-  const Plan p = make_plan(c, num_sms);
-  DecodeArgs a;
+  return plan_of(static_cast<long>(d.B) * d.Hkv, d.Gk, d.R, num_sms);
+}
+
+// A list longer than the cache's blocks can hold no more groups than the cache.
+int listed_groups(const CacheDims &d, int top_k, int gpb) {
+  return static_cast<int>(std::min<long>(static_cast<long>(top_k) * gpb,
+                                         static_cast<long>((d.Gk + gpb - 1) / gpb) * gpb));
+}
+
+DecodeArgs make_args(const kvq_cache &c, const void *q, int q_dtype, float scale_log2, void *ws,
+                     const KernelCtl &ctl, const Plan &p) {
+  const CacheDims d = dims_of(c);
+  DecodeArgs a = {};
   a.k_codes = c.k_codes;
   a.k_scales = c.k_scales;
   a.v_codes = c.v_codes;
@@ -867,27 +949,95 @@ int launch_attend_decode(const kvq_cache &c, const void *q, int q_dtype, float s
   a.scale_log2 = scale_log2;
   a.partials = static_cast<float *>(ws);
   a.ctl = ctl;
+  return a;
+}
+
+template <bool kList>
+int launch_decode(const DecodeArgs &a, const Plan &p, void *out, int out_dtype, cudaStream_t s) {
   const size_t smem = sizeof(DecodeSmem);
-  opt_in_smem(decode_kernel, smem);
+  opt_in_smem(decode_kernel<kList>, smem);
   // The combine grid's blocks may be placed while the decode grid drains; they
   // wait for it on the device.
-  launch_dependent(decode_kernel, dim3(p.num_ctas), dim3(kThreads), smem, s, a);
+  launch_dependent(decode_kernel<kList>, dim3(p.num_ctas), dim3(kThreads), smem, s, a);
   if (p.max_ctas_per_unit > kWideCombineAbove) {
-    const dim3 grid(static_cast<unsigned>(p.units), kHeads);
+    const dim3 grid(static_cast<unsigned>(p.units), kList ? a.heads : kHeads);
     if (out_dtype == KVQ_F32)
-      launch_dependent(combine_wide_kernel<float>, grid, dim3(256), 0, s, a,
+      launch_dependent(combine_wide_kernel<float, kList>, grid, dim3(256), 0, s, a,
                        static_cast<float *>(out));
     else
-      launch_dependent(combine_wide_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a,
+      launch_dependent(combine_wide_kernel<__nv_bfloat16, kList>, grid, dim3(256), 0, s, a,
                        static_cast<__nv_bfloat16 *>(out));
   } else if (out_dtype == KVQ_F32) {
-    launch_dependent(combine_kernel<float>, dim3(p.units), dim3(kHeads * 32), 0, s, a,
+    launch_dependent(combine_kernel<float, kList>, dim3(p.units), dim3(kHeads * 32), 0, s, a,
                      static_cast<float *>(out));
   } else {
-    launch_dependent(combine_kernel<__nv_bfloat16>, dim3(p.units), dim3(kHeads * 32), 0, s, a,
-                     static_cast<__nv_bfloat16 *>(out));
+    launch_dependent(combine_kernel<__nv_bfloat16, kList>, dim3(p.units), dim3(kHeads * 32), 0, s,
+                     a, static_cast<__nv_bfloat16 *>(out));
   }
   return 2;
+}
+
+}  // namespace
+
+bool decode_supported(const kvq_cache &c, int q_dtype, int Hq, int n_q) {
+  const bool win_ok = c.recent == 0 || (c.kwin_dtype == KVQ_BF16 && c.vwin_dtype == KVQ_BF16);
+  const long items = static_cast<long>(c.batch) * c.kv_heads *
+                    ((c.n_tokens - c.recent + 32 * kGroupsPerItem - 1) / (32 * kGroupsPerItem) +
+                     (c.recent + kWinItem - 1) / kWinItem);
+  return c.head_dim == kD && n_q == 1 && Hq == kHeads * c.kv_heads && win_ok &&
+         (q_dtype == KVQ_BF16 || q_dtype == KVQ_F32) && c.n_tokens > 0 && items < (1L << 30);
+}
+
+size_t decode_workspace_bytes(const kvq_cache &c, int, int num_sms) {
+  const Plan p = make_plan(c, num_sms);
+  return sizeof(float) * static_cast<size_t>(p.units) * p.max_ctas_per_unit * kHeads * kPartFloats;
+}
+
+int launch_attend_decode(const kvq_cache &c, const void *q, int q_dtype, float scale_log2,
+                         void *out, int out_dtype, void *ws, const KernelCtl &ctl, int num_sms,
+                         cudaStream_t s) {
+  const Plan p = make_plan(c, num_sms);
+  return launch_decode<false>(make_args(c, q, q_dtype, scale_log2, ws, ctl, p), p, out, out_dtype,
+                              s);
+}
+
+// ------------------------------------------------------------------ listed blocks
+bool blocks_decode_supported(const kvq_cache &c, int q_dtype, int Hq, int n_q, int top_k,
+                             int block) {
+  const CacheDims d = dims_of(c);
+  const bool win_ok = c.recent == 0 || (c.kwin_dtype == KVQ_BF16 && c.vwin_dtype == KVQ_BF16);
+  const long units = static_cast<long>(d.B) * d.Hkv * n_q;
+  const long ipu = (listed_groups(d, top_k, block / kGroup) + kGroupsPerItem - 1) / kGroupsPerItem +
+                   (d.R + kWinItem - 1) / kWinItem;
+  // (an MXFP8 window type rounds q even when the window is empty)
+  return d.D == kD && win_ok && c.kwin_dtype != KVQ_MXFP8 && q_dtype == KVQ_BF16 &&
+         Hq <= kHeads * d.Hkv && units * ipu < (1L << 30);
+}
+
+size_t blocks_decode_workspace_bytes(const kvq_cache &c, int n_q, int top_k, int block,
+                                     int num_sms) {
+  const CacheDims d = dims_of(c);
+  const Plan p = plan_of(static_cast<long>(d.B) * d.Hkv * n_q,
+                         listed_groups(d, top_k, block / kGroup), d.R, num_sms);
+  return sizeof(float) * static_cast<size_t>(p.units) * p.max_ctas_per_unit * kHeads * kPartFloats;
+}
+
+int launch_attend_blocks(const kvq_cache &c, const void *q, int Hq, int n_q,
+                         const int32_t *selected, int top_k, int block, int n_blocks,
+                         float scale_log2, void *out, int out_dtype, void *ws,
+                         const KernelCtl &ctl, int num_sms, cudaStream_t s) {
+  const CacheDims d = dims_of(c);
+  const int gpb = block / kGroup;
+  const Plan p = plan_of(static_cast<long>(d.B) * d.Hkv * n_q, listed_groups(d, top_k, gpb), d.R,
+                         num_sms);
+  DecodeArgs a = make_args(c, q, KVQ_BF16, scale_log2, ws, ctl, p);
+  a.list = selected;
+  a.top_k = top_k;
+  a.gpb = gpb;
+  a.n_blocks = n_blocks;
+  a.n_q = n_q;
+  a.heads = Hq / d.Hkv;
+  return launch_decode<true>(a, p, out, out_dtype, s);
 }
 
 // ------------------------------------------------------------------ library-owned scratch

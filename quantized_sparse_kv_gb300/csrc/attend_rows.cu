@@ -1,0 +1,348 @@
+// fp32 attention of single rows over chosen keys, for any supported shape: the
+// path of kv_attend_tree and kv_attend_blocks for the shapes and types their
+// tensor-core kernels do not take (fp32 queries, other head dims, fp32 or MXFP8
+// windows).
+//
+// One CTA of 8 warps per (query token, query head, sequence). The row's keys are
+// walked in chunks of 32: the cache's tokens and then the drafted ones (tree), or
+// the listed blocks' groups and then the window (blocks); warp w takes chunks w,
+// w + 8, ... Lane j of a warp scores key j of the chunk against the whole q row in
+// shared memory, the warp keeps an online softmax (running maximum, rescaled sum)
+// and each lane owns D / 32 output features. The warps' states meet in shared
+// memory. Keys a row does not see are never read into a sum, so their contents
+// do not matter. It is bound by its instructions, about 2 D + 100 per key.
+#include <math_constants.h>
+
+#include "kvq_internal.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kRowWarps = 8;
+
+struct RowsArgs {
+  const uint8_t *k_codes;
+  const float *k_scales;
+  const uint8_t *v_codes;
+  const float *v_scales;
+  const void *k_window;
+  const void *v_window;
+  const uint8_t *k_e8m0;
+  int kwin, vwin;
+  int Hkv, N, R, cut, Gs, Vs, Ws;
+  int Hq, group, n_q;
+  const void *q;
+  int q_dtype;
+  void *out;
+  int out_dtype;
+  float scale;
+  // tree
+  const void *k_tree, *v_tree;
+  int tree_dtype;
+  const int32_t *parents;
+  // blocks
+  const int32_t *selected;
+  int top_k, block, n_blocks;
+  KernelCtl ctl;
+};
+
+__device__ __forceinline__ float nibble(uint32_t byte, int odd) {
+  return static_cast<float>(static_cast<int>(odd ? (byte >> 4) & 15u : byte & 15u) - 8);
+}
+__device__ __forceinline__ float elem(const void *p, int dtype, long i) {
+  return dtype == KVQ_F32 ? static_cast<const float *>(p)[i]
+                          : bf16_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+__device__ __forceinline__ size_t elem_size(int dtype) {
+  return dtype == KVQ_F32 ? 4 : dtype == KVQ_BF16 ? 2 : 1;
+}
+
+// q . (row `row` of a dense [rows][D] tensor)
+template <int D>
+__device__ __forceinline__ float dot_row(const KernelCtl &ctl, const void *p, int dtype, long row,
+                                         const float *q) {
+  float s = 0.0f;
+  if (!in_bounds(ctl, static_cast<const uint8_t *>(p) + row * D * elem_size(dtype),
+                 D * elem_size(dtype)))
+    return s;
+#pragma unroll 8
+  for (int d = 0; d < D; ++d) s = fmaf(q[d], elem(p, dtype, row * D + d), s);
+  return s;
+}
+
+// q . K of cache token t
+template <int D>
+__device__ __forceinline__ float dot_cache(const RowsArgs &a, long u, int t, const float *q) {
+  float s = 0.0f;
+  if (t < a.cut) {
+    const long g = u * a.Gs + t / kGroup;
+    const uint32_t *c =
+        reinterpret_cast<const uint32_t *>(a.k_codes + (g * kGroup + t % kGroup) * (D / 2));
+    const float *sc = a.k_scales + g * D;
+    if (!in_bounds(a.ctl, c, D / 2) || !in_bounds(a.ctl, sc, D * sizeof(float))) return s;
+#pragma unroll 4
+    for (int w = 0; w < D / 8; ++w) {
+      const uint32_t x = c[w];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        s = fmaf(q[8 * w + e], nibble(x >> (8 * (e / 2)), e & 1) * sc[8 * w + e], s);
+    }
+    return s;
+  }
+  const long row = u * a.Ws + (t - a.cut);
+  if (a.kwin != KVQ_MXFP8) return dot_row<D>(a.ctl, a.k_window, a.kwin, row, q);
+  const uint8_t *c = static_cast<const uint8_t *>(a.k_window) + row * D;
+  const uint8_t *e8 = a.k_e8m0 + row * (D / 32);
+  if (!in_bounds(a.ctl, c, D) || !in_bounds(a.ctl, e8, D / 32)) return s;
+  for (int d = 0; d < D; ++d) s = fmaf(q[d], mxfp8_value(c[d], e8[d / 32]), s);
+  return s;
+}
+
+// Element d of V of cache token t
+template <int D>
+__device__ __forceinline__ float v_cache(const RowsArgs &a, long u, int t, int d) {
+  if (t < a.cut) {
+    const long row = u * a.Vs + t;
+    const uint8_t *c = a.v_codes + row * (D / 2) + d / 2;
+    const float *sc = a.v_scales + row * (D / 32) + d / 32;
+    if (!in_bounds(a.ctl, c, 1) || !in_bounds(a.ctl, sc, sizeof(float))) return 0.0f;
+    return nibble(*c, d & 1) * *sc;
+  }
+  const long i = (u * a.Ws + (t - a.cut)) * D + d;
+  if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.v_window) + i * elem_size(a.vwin),
+                 elem_size(a.vwin)))
+    return 0.0f;
+  return elem(a.v_window, a.vwin, i);
+}
+
+template <int DPL, bool kTree>
+__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  constexpr int D = 32 * DPL;
+  __shared__ float qs[D];
+  __shared__ float wo[kRowWarps][D], wm[kRowWarps], wl[kRowWarps];
+  __shared__ int par[KVQ_TREE_MAX];
+  __shared__ uint32_t seen[KVQ_TREE_MAX / 32];
+  __shared__ int row_ok;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const long kvh = h / a.group;
+  const long u = static_cast<long>(b) * a.Hkv + kvh;
+  const long row = (static_cast<long>(b) * a.Hq + h) * a.n_q + i;
+  const size_t qe = elem_size(a.q_dtype), oe = elem_size(a.out_dtype);
+  const bool io_ok =
+      in_bounds(a.ctl, static_cast<const uint8_t *>(a.q) + row * D * qe, D * qe) &&
+      in_bounds(a.ctl, static_cast<uint8_t *>(a.out) + row * D * oe, D * oe);
+  for (int d = tid; d < D; d += kRowWarps * 32) qs[d] = io_ok ? elem(a.q, a.q_dtype, row * D + d) : 0.0f;
+  if (kTree) {
+    const int32_t *p = a.parents + static_cast<long>(b) * a.n_q;
+    const bool ok = in_bounds(a.ctl, p, sizeof(int32_t) * a.n_q);
+    for (int j = tid; j < a.n_q; j += kRowWarps * 32) par[j] = ok ? p[j] : -2;
+    if (tid < KVQ_TREE_MAX / 32) seen[tid] = 0u;
+  }
+  __syncthreads();
+  if (kTree && tid == 0) {
+    // up the parents, each below its child, to the cache (-1); a row that
+    // meets anything else holds no token
+    int j = i;
+    bool bad = false;
+    for (;;) {
+      const int p = par[j];
+      if (p < -1 || p >= j) {
+        bad = p != -2 || j != i;  // -2 on the row itself: an unused row
+        row_ok = 0;
+        break;
+      }
+      seen[j >> 5] |= 1u << (j & 31);
+      if (p == -1) {
+        row_ok = 1;
+        break;
+      }
+      j = p;
+    }
+    if (bad) flag_error(a.ctl, KVQ_DEV_INDEX);
+  }
+  if (a.kwin == KVQ_MXFP8) {  // Q takes the same MXFP8 rounding as the K window
+    for (int j = warp; j < DPL; j += kRowWarps)
+      qs[32 * j + lane] = mxfp8_round_warp(qs[32 * j + lane]);
+  }
+  __syncthreads();
+  if (kTree && row_ok == 0) return;  // the output of a row without a token stays
+
+  float m = -CUDART_INF_F, l = 0.0f, o[DPL];
+#pragma unroll
+  for (int k = 0; k < DPL; ++k) o[k] = 0.0f;
+
+  const int32_t *list = nullptr;
+  int per_block = 1, list_chunks = 0;
+  if (!kTree) {
+    list = a.selected + (u * a.n_q + i) * a.top_k;
+    per_block = a.block / 32;
+    list_chunks = in_bounds(a.ctl, list, sizeof(int32_t) * a.top_k) ? a.top_k * per_block : 0;
+  }
+  const int cache_chunks = kTree ? (a.N + 31) / 32 : list_chunks;
+  const int tail_keys = kTree ? i + 1 : a.R;  // a drafted token sees none after itself
+  const int chunks = cache_chunks + (tail_keys + 31) / 32;
+  for (int c = warp; c < chunks; c += kRowWarps) {
+    int t = -1, tj = -1;  // this lane's cache token, or drafted token
+    if (c < cache_chunks) {
+      if (kTree) {
+        t = 32 * c + lane < a.N ? 32 * c + lane : -1;
+      } else {
+        const int e = c / per_block, blk = list[e];
+        const int prev = e > 0 ? list[e - 1] : -1;
+        int bit = 0;
+        if (blk != -1 && (blk < 0 || blk >= a.n_blocks)) bit = KVQ_DEV_INDEX;
+        else if (blk != -1 && e > 0 && blk <= prev) bit = KVQ_DEV_DUP;
+        else if (blk != -1 && e > 0 && prev == -1) bit = KVQ_DEV_INDEX;
+        if (bit != 0 && lane == 0 && c % per_block == 0) flag_error(a.ctl, bit);
+        if (blk == -1 || bit != 0) continue;
+        const int t0 = blk * a.block + 32 * (c % per_block);
+        t = t0 + lane < a.cut ? t0 + lane : -1;
+      }
+    } else {
+      const int k = 32 * (c - cache_chunks) + lane;
+      if (kTree) {
+        if (k < tail_keys && (seen[k >> 5] >> (k & 31) & 1u)) tj = k;
+      } else {
+        t = k < a.R ? a.cut + k : -1;
+      }
+    }
+    float s = -CUDART_INF_F;
+    if (t >= 0) s = dot_cache<D>(a, u, t, qs) * a.scale;
+    if (tj >= 0) s = dot_row<D>(a.ctl, a.k_tree, a.tree_dtype, u * a.n_q + tj, qs) * a.scale;
+    const bool live = t >= 0 || tj >= 0;
+    const uint32_t lives = __ballot_sync(0xffffffffu, live);
+    if (lives == 0u) continue;
+    const float mx = warp_max(s);
+    // (all scores -inf: probabilities against 0 are exp(-inf) = 0)
+    const float m_new = fmaxf(m, mx), ref = m_new == -CUDART_INF_F ? 0.0f : m_new;
+    const float corr = m == -CUDART_INF_F ? 0.0f : expf(m - ref);
+    const float p = live ? expf(s - ref) : 0.0f;
+    l = l * corr + warp_sum(p);
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) o[k] *= corr;
+    m = m_new;
+    for (int j = 0; j < 32; ++j) {
+      if (!(lives >> j & 1u)) continue;
+      const float pj = __shfl_sync(0xffffffffu, p, j);
+      const int tt = __shfl_sync(0xffffffffu, t, j), tr = __shfl_sync(0xffffffffu, tj, j);
+#pragma unroll
+      for (int k = 0; k < DPL; ++k) {
+        const int d = lane + 32 * k;
+        float v = 0.0f;
+        if (tr >= 0) {
+          const long e = (u * a.n_q + tr) * D + d;
+          if (in_bounds(a.ctl, static_cast<const uint8_t *>(a.v_tree) + e * elem_size(a.tree_dtype),
+                        elem_size(a.tree_dtype)))
+            v = elem(a.v_tree, a.tree_dtype, e);
+        } else {
+          v = v_cache<D>(a, u, tt, d);
+        }
+        o[k] = fmaf(pj, v, o[k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < DPL; ++k) wo[warp][lane + 32 * k] = o[k];
+  if (lane == 0) {
+    wm[warp] = m;
+    wl[warp] = l;
+  }
+  __syncthreads();
+  float mx = -CUDART_INF_F;
+#pragma unroll
+  for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, wm[w]);
+  if (!io_ok) return;
+  for (int d = tid; d < D; d += kRowWarps * 32) {
+    float ls = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+      if (wl[w] == 0.0f) continue;  // no key (a NaN sum stays in)
+      const float f = wm[w] == -CUDART_INF_F ? 1.0f : expf(wm[w] - mx);
+      ls += f * wl[w];
+      acc += f * wo[w][d];
+    }
+    const float x = ls == 0.0f ? 0.0f : acc / ls;  // no key at all: zero
+    if (a.out_dtype == KVQ_F32)
+      static_cast<float *>(a.out)[row * D + d] = x;
+    else
+      static_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(x);
+  }
+}
+
+template <bool kTree>
+int launch_rows(const RowsArgs &a, int D, int batch, cudaStream_t s) {
+  const dim3 grid(a.n_q, a.Hq, batch), block(kRowWarps * 32);
+  switch (D / 32) {
+    case 1: launch_dependent(rows_kernel<1, kTree>, grid, block, 0, s, a); break;
+    case 2: launch_dependent(rows_kernel<2, kTree>, grid, block, 0, s, a); break;
+    case 3: launch_dependent(rows_kernel<3, kTree>, grid, block, 0, s, a); break;
+    case 4: launch_dependent(rows_kernel<4, kTree>, grid, block, 0, s, a); break;
+    case 5: launch_dependent(rows_kernel<5, kTree>, grid, block, 0, s, a); break;
+    case 6: launch_dependent(rows_kernel<6, kTree>, grid, block, 0, s, a); break;
+    case 7: launch_dependent(rows_kernel<7, kTree>, grid, block, 0, s, a); break;
+    default: launch_dependent(rows_kernel<8, kTree>, grid, block, 0, s, a); break;
+  }
+  return 1;
+}
+
+RowsArgs rows_args(const kvq_cache &c, const void *q, int q_dtype, int Hq, int n_q, float scale,
+                   void *out, int out_dtype, const KernelCtl &ctl) {
+  const CacheDims d = dims_of(c);
+  RowsArgs a = {};
+  a.k_codes = c.k_codes;
+  a.k_scales = c.k_scales;
+  a.v_codes = c.v_codes;
+  a.v_scales = c.v_scales;
+  a.k_window = c.k_window;
+  a.v_window = c.v_window;
+  a.k_e8m0 = c.k_window_e8m0;
+  a.kwin = c.kwin_dtype;
+  a.vwin = c.vwin_dtype;
+  a.Hkv = d.Hkv;
+  a.N = d.N;
+  a.R = d.R;
+  a.cut = d.cut;
+  a.Gs = d.Gs;
+  a.Vs = d.Vs;
+  a.Ws = d.Ws;
+  a.Hq = Hq;
+  a.group = Hq / d.Hkv;
+  a.n_q = n_q;
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.scale = scale;
+  a.ctl = ctl;
+  return a;
+}
+
+}  // namespace
+
+int launch_tree_rows(const kvq_cache &c, const void *q, int q_dtype, int Hq, int T,
+                     const void *k_tree, const void *v_tree, int tree_dtype,
+                     const int32_t *parents, float scale, void *out, int out_dtype,
+                     const KernelCtl &ctl, cudaStream_t s) {
+  RowsArgs a = rows_args(c, q, q_dtype, Hq, T, scale, out, out_dtype, ctl);
+  a.k_tree = k_tree;
+  a.v_tree = v_tree;
+  a.tree_dtype = tree_dtype;
+  a.parents = parents;
+  return launch_rows<true>(a, c.head_dim, c.batch, s);
+}
+
+int launch_block_rows(const kvq_cache &c, const void *q, int q_dtype, int Hq, int n_q,
+                      const int32_t *selected, int top_k, int block, int n_blocks, float scale,
+                      void *out, int out_dtype, const KernelCtl &ctl, cudaStream_t s) {
+  RowsArgs a = rows_args(c, q, q_dtype, Hq, n_q, scale, out, out_dtype, ctl);
+  a.selected = selected;
+  a.top_k = top_k;
+  a.block = block;
+  a.n_blocks = n_blocks;
+  return launch_rows<false>(a, c.head_dim, c.batch, s);
+}
+
+}  // namespace kvq

@@ -1,0 +1,968 @@
+// Attention of drafted tokens over a packed cache and their own ancestors
+// (kv_attend_tree) on the fifth-generation tensor cores: D = 128, bf16 q.
+//
+// Mathematics. The T drafted tokens of a sequence times the G query heads of a KV
+// head are T * G query rows that attend the same keys: the cache's tokens, all of
+// them, and the drafted ones, under a mask. O = softmax(c Q K^T) V is computed
+// key tile by key tile with a running reference and sum per row; partial results
+// of a row over different key ranges are merged by the log-sum-exp rule.
+//
+// Work split. A unit is one (sequence, KV head); its rows are cut into row blocks
+// of 256 (two MMA tiles of 128), its keys into tiles of 128: the int4 part, then
+// the bf16 window and the drafted tokens laid end to end. All (unit, row block,
+// tile) items are laid end to end too and one CTA per SM takes an equal contiguous
+// slice, so a call with few rows still uses every SM. A CTA writes a partial
+// per row block it touches (or the output itself when its slice covers the whole
+// row block), tree_combine_kernel merges them.
+//
+// Inside a CTA (17 warps):
+//   warps 0-3, 4-7   softmax groups A and B, a thread per query row;
+//   warps 8-15       dequantization: packed tile -> registers (one tile ahead)
+//                    -> fp16 K and V tiles in shared memory, 128B-swizzled, two
+//                    stages each;
+//   warp 16          TMEM allocation; one lane issues the MMAs.
+// With more than 128 rows in the row block group A takes rows 0-127 and group B
+// rows 128-255 of every tile (each dequantized tile feeds both); with fewer, both
+// work on the same rows and take alternate tiles, so that one exponentiates
+// while the tensor core works for the other; their sums and outputs are merged at
+// the end of the slice. Per tile and group: S = Q K^T (MMA, both operands in
+// shared memory), softmax in registers, P written as fp16 over S in TMEM, O += P V
+// (MMA, A operand from TMEM). S of the next tile is issued once that MMA has
+// completed. The issuing lane polls both groups and issues whatever is ready.
+//
+// Precision: fp16 operands (11 bits; K and V are code * scale), fp32 sums and
+// softmax state. P is taken against the reference, raised when a tile's
+// maximum passes it by more than 2^8, so P stays below 2^8 in fp16.
+//
+// Feature order: a nibble word gives features (0,4)(1,5)(2,6)(3,7) of eight in
+// pairs without shuffling, so Q, K and V tiles hold every eight features in the
+// order 0 4 1 5 2 6 3 7; the output is written back in natural order.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "int4_dequant.cuh"
+#include "kvq_internal.h"
+#include "tc_common.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kBM = 128;           // rows of an MMA tile
+constexpr int kBN = 128;           // keys of a tile
+constexpr int kRowBlock = 2 * kBM;
+constexpr int kSoftWarps = 8, kDqWarps = 8;
+constexpr int kThreads = (kSoftWarps + kDqWarps + 1) * 32;
+constexpr uint32_t kHalf = 128u * 128u;      // 16 KB: 128 rows x 64 fp16 features
+constexpr uint32_t kTileBytes = 2u * kHalf;
+constexpr int kStages = 2;                   // K and V tiles in shared memory, each
+constexpr int kMaskWords = KVQ_TREE_MAX / 32;
+constexpr float kLazy = 8.0f;                // log2 units the maximum may pass the reference
+constexpr int kPartStride = kD + 4;          // floats of a partial row: O[128], m, l, padding
+
+struct __align__(1024) TreeSmem {
+  uint8_t q[2][kTileBytes];
+  uint8_t k[kStages][kTileBytes];
+  uint8_t v[kStages][kTileBytes];
+  int par[KVQ_TREE_MAX];                     // parents of the sequence
+  uint32_t seen[KVQ_TREE_MAX][kMaskWords];   // ancestor bits of every drafted token
+  uint32_t live[kMaskWords];                 // drafted tokens that exist
+  uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
+  float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full, s_full[2], p_full[2], o_done[2], mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct TreeArgs {
+  const uint8_t *k_codes;
+  const float *k_scales;
+  const uint8_t *v_codes;
+  const float *v_scales;
+  const uint16_t *k_window, *v_window;  // bf16
+  const uint16_t *k_tree, *v_tree;      // bf16 [unit][T][128]
+  const uint16_t *q;                    // bf16 [batch][Hq][T][128]
+  const int32_t *parents;
+  int Hkv, G, T, R, cut, Gk, Gs, Vs, Ws;
+  int rows, row_blocks;                 // T * G, and per unit
+  int int4_tiles, tiles;                // key tiles per unit
+  long items;                           // units * row_blocks * tiles
+  int ctas, slots;                      // slots: partials reserved per row block
+  float scale_log2;
+  void *out;
+  int out_dtype;
+  float *partials;                      // [unit * row_blocks][slots][256][132]
+  KernelCtl ctl;
+};
+
+// ------------------------------------------------------------------ PTX wrappers
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// O += P V with P (A operand, fp16 pairs, one lane per row) in TMEM.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 words to 16 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, M = N =
+// 128, A K-major, B K-major (0) or MN-major (1).
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t b_mn_major) {
+  return (1u << 4) | (b_mn_major << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Two floats to fp16, finite values beyond its range clamped to it (infinities
+// and NaN stay).
+__device__ __forceinline__ float clamp_h(float x) {
+  const float c = fminf(fmaxf(x, -65504.0f), 65504.0f);
+  return fabsf(x) <= 3.40282347e38f ? c : x;
+}
+
+// Eight bf16 (four words, natural order) as fp16 in the tiles' feature order.
+__device__ __forceinline__ uint4 bf8_to_h8(const uint4 &w) {
+  const float x0 = clamp_h(bf_lo(w.x)), x1 = clamp_h(bf_hi(w.x));
+  const float x2 = clamp_h(bf_lo(w.y)), x3 = clamp_h(bf_hi(w.y));
+  const float x4 = clamp_h(bf_lo(w.z)), x5 = clamp_h(bf_hi(w.z));
+  const float x6 = clamp_h(bf_lo(w.w)), x7 = clamp_h(bf_hi(w.w));
+  return make_uint4(pack_h2(x0, x4), pack_h2(x1, x5), pack_h2(x2, x6), pack_h2(x3, x7));
+}
+
+// Place of 16-byte chunk c (0..15, eight features each) of row r in a tile.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
+  return (c >> 3) * kHalf + swz(r, c & 7u);
+}
+
+// Slice of CTA c: items [items * c / ctas, items * (c + 1) / ctas).
+__device__ __forceinline__ long slice_lo(const TreeArgs &a, int c) { return a.items * c / a.ctas; }
+// CTA whose slice holds item x.
+__device__ __forceinline__ int cta_of(const TreeArgs &a, long x) {
+  return static_cast<int>(((x + 1) * a.ctas - 1) / a.items);
+}
+
+// ------------------------------------------------------------------ dequantization
+// Thread's part of a tile: 16 B of codes (32 features, block cb) of rows r and
+// r + 16 of group grp. A quarter-warp takes eight consecutive rows of one
+// feature block, so its swizzled 16-byte stores meet all banks; a warp's code
+// loads are 512 contiguous bytes.
+struct DqMap {
+  int grp, r, cb;
+};
+
+struct KRaw {
+  uint4 c[2];
+  float4 s[8];
+};
+struct VRaw {
+  uint4 c[2];
+  float s[2];
+};
+
+__device__ __forceinline__ void load_k(const TreeArgs &a, long u, int tile, const DqMap &d, KRaw &x) {
+  const int g = 4 * tile + d.grp;
+  const bool have = g < a.Gk;
+  const long gi = u * a.Gs + g;
+  const uint8_t *p = a.k_codes + (gi * 32 + d.r) * 64 + 16 * d.cb;
+  const float *s = a.k_scales + gi * 128 + 32 * d.cb;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    x.c[i] = have && in_bounds(a.ctl, p + 1024 * i, 16)
+                 ? *reinterpret_cast<const uint4 *>(p + 1024 * i)
+                 : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+  const bool ok = have && in_bounds(a.ctl, s, 128);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x.s[i] = ok ? reinterpret_cast<const float4 *>(s)[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+__device__ __forceinline__ void load_v(const TreeArgs &a, long u, int tile, const DqMap &d, VRaw &x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = 128 * tile + 32 * d.grp + d.r + 16 * i;
+    const long row = u * a.Vs + t;
+    const uint8_t *p = a.v_codes + row * 64 + 16 * d.cb;
+    const float *s = a.v_scales + row * 4 + d.cb;
+    const bool ok = t < a.cut && in_bounds(a.ctl, p, 16) && in_bounds(a.ctl, s, 4);
+    x.c[i] = ok ? *reinterpret_cast<const uint4 *>(p)
+                : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+    x.s[i] = ok ? *s : 0.0f;
+  }
+}
+
+// Eight codes of a word times their scales (pairs in the tiles' feature order).
+__device__ __forceinline__ uint4 dq8(uint32_t w, __half2 s04, __half2 s15, __half2 s26,
+                                     __half2 s37) {
+  const uint32_t h = w >> 8;
+  return make_uint4(as_u32(__hmul2(as_h2(dq_lo(w)), s04)), as_u32(__hmul2(as_h2(dq_hi(w)), s15)),
+                    as_u32(__hmul2(as_h2(dq_lo(h)), s26)), as_u32(__hmul2(as_h2(dq_hi(h)), s37)));
+}
+
+__device__ __forceinline__ void store_k(const KRaw &x, const DqMap &d, uint8_t *tile) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 s0 = x.s[2 * j], s1 = x.s[2 * j + 1];
+    const __half2 a = __floats2half2_rn(s0.x, s1.x), b = __floats2half2_rn(s0.y, s1.y);
+    const __half2 c = __floats2half2_rn(s0.z, s1.z), e = __floats2half2_rn(s0.w, s1.w);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = j == 0 ? x.c[i].x : j == 1 ? x.c[i].y : j == 2 ? x.c[i].z : x.c[i].w;
+      *reinterpret_cast<uint4 *>(tile + chunk_at(32 * d.grp + d.r + 16 * i, 4 * d.cb + j)) =
+          dq8(w, a, b, c, e);
+    }
+  }
+}
+
+__device__ __forceinline__ void store_v(const VRaw &x, const DqMap &d, uint8_t *tile) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 s = __float2half2_rn(x.s[i]);
+    const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4 *>(tile + chunk_at(32 * d.grp + d.r + 16 * i, 4 * d.cb + j)) =
+          dq8(w[j], s, s, s, s);
+  }
+}
+
+// Rows of the tail (window, then drafted tokens) from key k0 on, zeros past
+// its end; non-finite V elements of drafted tokens become zero (they are added
+// for the rows that see them when the output is written).
+__device__ __forceinline__ void copy_tail(const TreeArgs &a, long u, int k0, const DqMap &d,
+                                          const uint16_t *win, const uint16_t *tree, bool is_v,
+                                          uint8_t *tile) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 32 * d.grp + d.r + 16 * i, key = k0 + r;
+    const uint16_t *p = key < a.R ? win + (u * a.Ws + key) * kD
+                                  : tree + (u * a.T + (key - a.R)) * kD;
+    const bool ok = key < a.R + a.T && in_bounds(a.ctl, p, 2 * kD);
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = ok ? reinterpret_cast<const uint4 *>(p + 32 * d.cb)[j] : make_uint4(0u, 0u, 0u, 0u);
+    if (is_v && key >= a.R) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t *e = reinterpret_cast<uint32_t *>(&w[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u;
+          if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4 *>(tile + chunk_at(r, 4 * d.cb + j)) = bf8_to_h8(w[j]);
+  }
+}
+
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ the kernel
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The same barrier, returning in every thread whether any thread passed true:
+// the one place where the softmax threads agree to stop.
+__device__ __forceinline__ bool soft_sync_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// A bounded wait of a whole warp: true only when every lane's wait ended in time.
+__device__ __forceinline__ bool warp_wait(int *abort_flag, uint32_t bar, uint32_t parity,
+                                          const KernelCtl &ctl) {
+  return __all_sync(0xffffffffu, wait_or_abort(abort_flag, bar, parity, ctl));
+}
+
+// Sum of v[e] over the drafted tokens j of this row whose V has non-finite
+// elements: what their zeroed elements would have added (feature d0 + e).
+__device__ __noinline__ void add_odd_values(const TreeArgs &a, const TreeSmem &sm, long u, int tok,
+                                            int k_lo, int k_hi, int d0, float (&v)[32]) {
+  for (int j = max(0, k_lo - a.R); j < min(a.T, k_hi - a.R); ++j) {
+    if (!((sm.odd_v[j >> 5] & sm.seen[tok][j >> 5]) >> (j & 31) & 1u)) continue;
+    const uint16_t *p = a.v_tree + (u * a.T + j) * kD + d0;
+    if (!in_bounds(a.ctl, p, 64)) continue;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float x = bf16_to_f32(p[e]);
+      if (!(fabsf(x) <= 3.40282347e38f)) v[e] += x;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  TreeSmem &sm = *reinterpret_cast<TreeSmem *>(smem_raw + (((base + 1023u) & ~1023u) - base));
+  int *const abort_flag = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long lo = slice_lo(a, blockIdx.x), hi = slice_lo(a, blockIdx.x + 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sm.k_full[s]), kDqWarps);
+      mbar_init(smem_u32(&sm.v_full[s]), kDqWarps);
+      mbar_init(smem_u32(&sm.k_empty[s]), 1);
+      mbar_init(smem_u32(&sm.v_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sm.q_full), 2 * kBM);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(smem_u32(&sm.s_full[g]), 1);
+      mbar_init(smem_u32(&sm.p_full[g]), kBM);
+      mbar_init(smem_u32(&sm.o_done[g]), 1);
+    }
+    mbar_init(smem_u32(&sm.mma_done), 1);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kSoftWarps + kDqWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&sm.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  wait_prior_grid();
+  allow_next_grid();
+  const uint32_t tmem = sm.tmem_base;
+  auto t_s = [&](int g) { return tmem + 256u * g; };
+  auto t_o = [&](int g) { return tmem + 256u * g + 128u; };
+
+  if (warp >= kSoftWarps && warp < kSoftWarps + kDqWarps) {
+    // ------------------------------------------------ dequantization
+    const int w = warp - kSoftWarps;
+    DqMap d;
+    d.grp = w >> 1;
+    d.r = 8 * (w & 1) + (lane & 7);
+    d.cb = lane >> 3;
+    KRaw kx;
+    VRaw vx;
+    long x = lo;
+    long rb = x / a.tiles;
+    int tile = static_cast<int>(x - rb * a.tiles);
+    long u = rb / a.row_blocks;
+    int rbu = static_cast<int>(rb - u * a.row_blocks);
+    if (x < hi && tile < a.int4_tiles) {
+      load_k(a, u, tile, d, kx);
+      load_v(a, u, tile, d, vx);
+    }
+    for (int j = 0; x < hi; ++x, ++j) {
+      const int st = j % kStages;
+      const uint32_t par = static_cast<uint32_t>((j / kStages - 1) & 1);
+      // where the next item is
+      long nu = u;
+      int nt = tile + 1, nrb = rbu;
+      if (nt == a.tiles) {
+        nt = 0;
+        if (++nrb == a.row_blocks) {
+          nrb = 0;
+          ++nu;
+        }
+      }
+      const bool next4 = x + 1 < hi && nt < a.int4_tiles;
+      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.k_empty[st]), par, a.ctl)) break;
+      if (__any_sync(0xffffffffu, cta_aborted(abort_flag))) break;
+      if (tile < a.int4_tiles)
+        store_k(kx, d, sm.k[st]);
+      else
+        copy_tail(a, u, kBN * (tile - a.int4_tiles), d, a.k_window, a.k_tree, false, sm.k[st]);
+      fence_async_smem();
+      __syncwarp();
+      // (test hook: a dropped item's keys never arrive)
+      if (lane == 0 && x != a.ctl.drop_item) mbar_arrive(smem_u32(&sm.k_full[st]));
+      if (next4) load_k(a, nu, nt, d, kx);
+      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.v_empty[st]), par, a.ctl)) break;
+      if (tile < a.int4_tiles)
+        store_v(vx, d, sm.v[st]);
+      else
+        copy_tail(a, u, kBN * (tile - a.int4_tiles), d, a.v_window, a.v_tree, true, sm.v[st]);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[st]));
+      if (next4) load_v(a, nu, nt, d, vx);
+      u = nu;
+      tile = nt;
+      rbu = nrb;
+    }
+  } else if (warp == kSoftWarps + kDqWarps) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f16(0), id_pv = idesc_f16(1);
+      int base_j = 0;            // tiles of the CTA before this segment
+      int seg = 0;
+      int done[2] = {0, 0};      // PV MMAs issued by each group so far
+      bool ok = true;
+      for (long x = lo; ok && x < hi; ++seg) {
+        const long rb = x / a.tiles;
+        const int t_lo = static_cast<int>(x - rb * a.tiles);
+        const int n = static_cast<int>(min(static_cast<long>(a.tiles - t_lo), hi - x));
+        const int rows = min(kRowBlock, a.rows - kRowBlock * static_cast<int>(rb % a.row_blocks));
+        const bool two = rows > kBM;
+        if (!wait_or_abort(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
+        // Group g's next tile and whether its S is out; group g takes tiles
+        // 0, 1, 2, ... of the segment (two) or g, g + 2, ... (shared rows).
+        int at[2] = {0, two ? 0 : 1};
+        bool s_out[2] = {false, false}, first[2] = {true, true};
+        int s_left[kStages] = {0, 0}, v_left[kStages] = {0, 0};
+        const int stride = two ? 1 : 2;
+        uint64_t t0 = 0;
+        int idle = 0;
+        while (at[0] < n || at[1] < n) {
+          bool moved = false;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int j = at[g];
+            if (j >= n) continue;
+            const int jj = base_j + j, st = jj % kStages;
+            const uint32_t par = static_cast<uint32_t>((jj / kStages) & 1);
+            if (!s_out[g]) {
+              // S of tile j: K is there and the group's last PV has read P
+              if (!mbar_test(smem_u32(&sm.k_full[st]), par)) continue;
+              if (!first[g] &&
+                  !mbar_test(smem_u32(&sm.o_done[g]), static_cast<uint32_t>((done[g] - 1) & 1)))
+                continue;
+              tc_fence_after();
+              const uint32_t qa = smem_u32(sm.q[two ? g : 0]), ka = smem_u32(sm.k[st]);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32u;
+                tc_mma_f16(t_s(g), smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024),
+                           id_qk, kk > 0 ? 1u : 0u);
+              }
+              tc_commit(smem_u32(&sm.s_full[g]));
+              if (!two || ++s_left[st] == 2) {
+                tc_commit(smem_u32(&sm.k_empty[st]));
+                s_left[st] = 0;
+              }
+              s_out[g] = true;
+              moved = true;
+            } else {
+              // O += P V of tile j
+              if (!mbar_test(smem_u32(&sm.p_full[g]), static_cast<uint32_t>(done[g] & 1)))
+                continue;
+              if (!mbar_test(smem_u32(&sm.v_full[st]), par)) continue;
+              tc_fence_after();
+              const uint32_t va = smem_u32(sm.v[st]);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_f16_ta(t_o(g), t_s(g) + 8u * kk, smem_desc(va + kk * 2048u, kHalf, 1024),
+                              id_pv, (!first[g] || kk > 0) ? 1u : 0u);
+              tc_commit(smem_u32(&sm.o_done[g]));
+              if (!two || ++v_left[st] == 2) {
+                tc_commit(smem_u32(&sm.v_empty[st]));
+                v_left[st] = 0;
+              }
+              ++done[g];
+              first[g] = false;
+              s_out[g] = false;
+              at[g] = j + stride;
+              moved = true;
+            }
+          }
+          if (moved) {
+            idle = 0;
+          } else if ((++idle & 1023) == 0) {
+            const uint64_t now = global_ns();
+            if (idle == 1024) t0 = now;
+            if (cta_aborted(abort_flag) || now - t0 > a.ctl.wait_limit_ns) {
+              flag_error(a.ctl, KVQ_DEV_TIMEOUT);
+              *reinterpret_cast<volatile int *>(abort_flag) = 1;
+              ok = false;
+              break;
+            }
+          }
+        }
+        base_j += n;
+        x += n;
+      }
+      // all MMAs of this CTA complete before TMEM is released
+      tc_commit(smem_u32(&sm.mma_done));
+      mbar_wait(smem_u32(&sm.mma_done), 0, 2000000000ull);
+    }
+  } else {
+    // ------------------------------------------------ softmax groups
+    const int g = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_row = t_s(g) + lane_off, o_row = t_o(g) + lane_off;
+    int s_seen = 0, pv_seen = 0;  // S tiles and PV MMAs of this group so far
+    bool ok = true;
+    for (long x = lo; x < hi;) {
+      const long rb = x / a.tiles;
+      const int t_lo = static_cast<int>(x - rb * a.tiles);
+      const int n = static_cast<int>(min(static_cast<long>(a.tiles - t_lo), hi - x));
+      const long u = rb / a.row_blocks;
+      const int row0 = kRowBlock * static_cast<int>(rb - u * a.row_blocks);
+      const bool two = a.rows - row0 > kBM;
+      const long b = u / a.Hkv;
+      const int kvh = static_cast<int>(u - b * a.Hkv);
+      const int r = row0 + (two ? kBM * g : 0) + row;  // row of the unit: token r / G, head r % G
+      const int tok = r < a.rows ? r / a.G : 0, head = r - tok * a.G;
+      x += n;
+      // ---- the tree's masks and this segment's queries
+      const int tid = threadIdx.x;  // 0..255
+      {
+        const int32_t *p = a.parents + b * a.T;
+        const bool pok = in_bounds(a.ctl, p, sizeof(int32_t) * a.T);
+        if (tid < a.T) sm.par[tid] = pok ? p[tid] : -2;
+        if (tid < kMaskWords) sm.live[tid] = sm.odd_v[tid] = 0u;
+      }
+      soft_sync();
+      if (tid < a.T) {
+#pragma unroll
+        for (int w = 0; w < kMaskWords; ++w) sm.seen[tid][w] = 0u;
+        // up the parents (each below its child) to the cache; anything else
+        // met on the way: no token
+        int j = tid;
+        for (;;) {
+          const int p = sm.par[j];
+          if (p < -1 || p >= j) {
+            if ((p != -2 || j != tid) && t_lo == 0 && row0 == 0 && kvh == 0)
+              flag_error(a.ctl, KVQ_DEV_INDEX);
+            break;
+          }
+          sm.seen[tid][j >> 5] |= 1u << (j & 31);
+          if (p == -1) {
+            atomicOr(&sm.live[tid >> 5], 1u << (tid & 31));
+            break;
+          }
+          j = p;
+        }
+      }
+      const bool has_tail = t_lo + n > a.int4_tiles;
+      const int tail_lo = kBN * max(0, t_lo - a.int4_tiles);        // tail keys of this segment
+      const int tail_hi = kBN * (t_lo + n - a.int4_tiles);
+      if (has_tail) {
+        for (int j = max(0, tail_lo - a.R) + warp; j < min(a.T, tail_hi - a.R); j += kSoftWarps) {
+          const uint16_t *p = a.v_tree + (u * a.T + j) * kD + 4 * lane;
+          uint2 w = in_bounds(a.ctl, p, 8) ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
+          const bool odd = (w.x & 0x7f80u) == 0x7f80u || (w.x & 0x7f800000u) == 0x7f800000u ||
+                           (w.y & 0x7f80u) == 0x7f80u || (w.y & 0x7f800000u) == 0x7f800000u;
+          if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sm.odd_v[j >> 5], 1u << (j & 31));
+        }
+      }
+      soft_sync();
+      const bool mine = r < a.rows && (sm.live[tok >> 5] >> (tok & 31) & 1u);
+      const long qrow = ((b * a.Hkv + kvh) * a.G + head) * a.T + tok;
+      {
+        const uint16_t *p = a.q + qrow * kD;
+        const bool qok = mine && in_bounds(a.ctl, p, 2 * kD);
+        // two: each group its own tile; shared rows: one half of the features each
+        uint8_t *q = sm.q[two ? g : 0];
+        const int c0 = two ? 0 : 8 * g, c1 = two ? 16 : 8 * g + 8;
+#pragma unroll 4
+        for (int c = c0; c < c1; ++c)
+          *reinterpret_cast<uint4 *>(q + chunk_at(row, c)) =
+              qok ? bf8_to_h8(reinterpret_cast<const uint4 *>(p)[c]) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      mbar_arrive(smem_u32(&sm.q_full));
+
+      float m = -CUDART_INF_F, l = 0.0f;
+      int mine_tiles = 0;
+      for (int j = two ? 0 : g; j < n; j += two ? 1 : 2, ++mine_tiles) {
+        if (!warp_wait(abort_flag, smem_u32(&sm.s_full[g]), s_seen & 1, a.ctl)) {
+          ok = false;
+          break;
+        }
+        ++s_seen;
+        tc_fence_after();
+        const int tile = t_lo + j;
+        // keys of the tile this row sees: all, the first `valid`, or by bits
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        bool all = true;
+        if (tile < a.int4_tiles) {
+          const int valid = a.cut - kBN * tile;
+          if (valid < kBN) {
+            all = false;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int k = valid - 32 * c;
+              see[c] = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
+            }
+          }
+        } else {
+          const int k0 = kBN * (tile - a.int4_tiles);
+          all = k0 + kBN <= a.R;
+          if (!all) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              // key k0 + 32c + e is drafted token s + e
+              const int s = k0 + 32 * c - a.R;
+              uint32_t bits = s <= -32 ? ~0u : 0u;
+              if (s > -32) {
+                if (s < 0) bits = (1u << -s) - 1u;  // window keys
+                const int w = s >= 0 ? s >> 5 : -1, sh = s & 31;
+                const uint32_t w0 = w >= 0 && w < kMaskWords ? sm.seen[tok][w] : 0u;
+                const uint32_t w1 = w + 1 < kMaskWords ? sm.seen[tok][w + 1] : 0u;
+                bits |= sh == 0 ? w0 : __funnelshift_r(w0, w1, sh);
+              }
+              see[c] = bits;
+            }
+          }
+        }
+        // ---- the tile's maximum
+        float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(s_row + 32u * c, v);
+          tmem_wait_ld();
+          reg_fence(v);
+          if (all) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              mx0 = fmaxf(mx0, v[e]);
+              mx1 = fmaxf(mx1, v[e + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              mx0 = fmaxf(mx0, see[c] >> e & 1u ? v[e] : -CUDART_INF_F);
+              mx1 = fmaxf(mx1, see[c] >> (e + 1) & 1u ? v[e + 1] : -CUDART_INF_F);
+            }
+          }
+        }
+        const float mx = fmaxf(mx0, mx1) * a.scale_log2;
+        // The reference is raised when the maximum passes it by 2^kLazy (and
+        // set by the first tile with a key); O and l follow.
+        const bool raise = mx > m + kLazy || (m == -CUDART_INF_F && mx > -CUDART_INF_F);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? fast_exp2(m - mx) : 1.0f;
+          if (raise) {
+            m = mx;
+            l *= f;
+          }
+          if (mine_tiles > 0) scale_tmem_row(o_row, f);  // the group's last PV has completed
+        }
+        const float neg_m = m == -CUDART_INF_F ? 0.0f : -m;
+        // ---- P over S: 32 scores at columns 32c become 16 words at 16c
+        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(s_row + 32u * c, v);
+          tmem_wait_ld();
+          reg_fence(v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            fma2(v[e], v[e + 1], v[e], v[e + 1], a.scale_log2, neg_m);
+            v[e] = fast_exp2(v[e]);
+            v[e + 1] = fast_exp2(v[e + 1]);
+          }
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = see[c] >> e & 1u ? v[e] : 0.0f;
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            add2(sum0, sum1, v[2 * e], v[2 * e + 1]);
+            p[e] = pack_h2(v[2 * e], v[2 * e + 1]);
+          }
+          tmem_st16(s_row + 16u * c, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.p_full[g]));
+        l += sum0 + sum1;
+      }
+      // (after a wait that ran out: on to the barrier below, where all stop)
+      pv_seen += mine_tiles;
+      if (ok && mine_tiles > 0 &&
+          !warp_wait(abort_flag, smem_u32(&sm.o_done[g]), (pv_seen - 1) & 1, a.ctl))
+        ok = false;
+      // ---- write the segment's rows: the output when the slice covers all
+      // of the row block's tiles, else a partial
+      if (!two) {
+        sm.mm[g][row] = mine_tiles > 0 ? m : -CUDART_INF_F;
+        sm.ml[g][row] = mine_tiles > 0 ? l : 0.0f;
+      }
+      tc_fence_before();
+      // both groups' last PV is done and their states are there
+      if (soft_sync_any(!ok || cta_aborted(abort_flag))) break;
+      tc_fence_after();
+      float fa = 1.0f, fb = 0.0f;
+      const bool have_b = !two && n > 1;
+      if (!two) {
+        const float ma = sm.mm[0][row], mb = sm.mm[1][row];
+        m = fmaxf(ma, mb);
+        fa = ma == -CUDART_INF_F ? 0.0f : fast_exp2(ma - m);
+        fb = mb == -CUDART_INF_F ? 0.0f : fast_exp2(mb - m);
+        l = fa * sm.ml[0][row] + (have_b ? fb * sm.ml[1][row] : 0.0f);
+      }
+      const bool whole = n == a.tiles;
+      const float inv = whole ? 1.0f / l : 1.0f;
+      float *part = nullptr;
+      if (!whole) {
+        const int slot = static_cast<int>(blockIdx.x) - cta_of(a, rb * a.tiles);
+        part = a.partials +
+               ((rb * a.slots + slot) * kRowBlock + (r - row0)) * static_cast<long>(kPartStride);
+      }
+      // (two: all four chunks of this group's rows; shared rows: half of them each)
+      for (int c = two ? 0 : 2 * g; c < (two ? 4 : 2 * g + 2); ++c) {
+        float v[32];
+        if (two) {
+          tmem_ld32(o_row + 32u * c, v);
+          tmem_wait_ld();
+          reg_fence(v);
+        } else {
+          tmem_ld32(t_o(0) + lane_off + 32u * c, v);
+          tmem_wait_ld();
+          reg_fence(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= fa;
+          if (have_b) {
+            float w[32];
+            tmem_ld32(t_o(1) + lane_off + 32u * c, w);
+            tmem_wait_ld();
+            reg_fence(w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(fb, w[e], v[e]);
+          }
+        }
+        if (!mine) continue;
+        // back to natural feature order: column 8k + i holds feature 8k + nat[i]
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int i = e & 7, nat = (i >> 1) + 4 * (i & 1);
+          y[(e & ~7) + nat] = v[e] * inv;
+        }
+        if (has_tail) {
+          bool odd = false;
+#pragma unroll
+          for (int w = 0; w < kMaskWords; ++w) odd |= (sm.odd_v[w] & sm.seen[tok][w]) != 0u;
+          if (odd) add_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c, y);
+        }
+        if (!whole) {
+          float4 *o = reinterpret_cast<float4 *>(part + 32 * c);
+          if (!in_bounds(a.ctl, part, sizeof(float) * kPartStride)) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          if (c == 0) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
+        } else if (a.out_dtype == KVQ_F32) {
+          float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + qrow * kD + 32 * c);
+          if (!in_bounds(a.ctl, o, 128)) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        } else {
+          uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + qrow * kD + 32 * c);
+          if (!in_bounds(a.ctl, o, 64)) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = make_uint4(pack_bf2(y[8 * e], y[8 * e + 1]), pack_bf2(y[8 * e + 2], y[8 * e + 3]),
+                              pack_bf2(y[8 * e + 4], y[8 * e + 5]),
+                              pack_bf2(y[8 * e + 6], y[8 * e + 7]));
+        }
+      }
+      // a row without a token leaves a partial that says so
+      if (!mine && !whole && r < a.rows && (two || g == 0) &&
+          in_bounds(a.ctl, part, sizeof(float) * kPartStride))
+        *reinterpret_cast<float2 *>(part + kD) = make_float2(-CUDART_INF_F, 0.0f);
+      tc_fence_before();
+      soft_sync();  // O, masks and states are read before the next segment rewrites them
+      tc_fence_after();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + kDqWarps) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// One warp per query row: merge the partials of the CTAs whose slices overlap
+// its row block (log-sum-exp), normalise, store. Row blocks inside one slice
+// were written by the kernel itself.
+constexpr int kCombineWarps = 8;
+
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const TreeArgs a,
+                                                                          long total_rows) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const long id = static_cast<long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+  if (id >= total_rows) return;
+  const long u = id / a.rows;
+  const int r = static_cast<int>(id - u * a.rows);
+  const long rb = u * a.row_blocks + r / kRowBlock;
+  const int c0 = cta_of(a, rb * a.tiles), c1 = cta_of(a, (rb + 1) * a.tiles - 1);
+  const int n = c1 - c0 + 1;
+  if (n == 1) return;
+  const long slot = static_cast<long>(kRowBlock) * kPartStride;
+  const float *p = a.partials + (rb * a.slots * kRowBlock + r % kRowBlock) * static_cast<long>(kPartStride);
+#ifdef KVQ_DEBUG
+  for (int i = 0; i < n; ++i)
+    if (!in_bounds(a.ctl, p + i * slot, sizeof(float) * kPartStride)) return;
+#endif
+  // the largest reference of the slots, then weights against it
+  float m = -CUDART_INF_F;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p[i * slot + kD]);
+  m = warp_max(m);
+  float l = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  bool any = false;
+  constexpr int kBatch = 8;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 o[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float *s = p + min(i0 + i, n - 1) * slot;
+      ml[i] = *reinterpret_cast<const float2 *>(s + kD);
+      o[i] = *reinterpret_cast<const float4 *>(s + 4 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i >= n || ml[i].y == 0.0f) continue;  // (a NaN sum stays in)
+      any = true;
+      const float w = ml[i].x == -CUDART_INF_F ? 1.0f : exp2f(ml[i].x - m);
+      l += w * ml[i].y;
+      acc.x += w * o[i].x;
+      acc.y += w * o[i].y;
+      acc.z += w * o[i].z;
+      acc.w += w * o[i].w;
+    }
+  }
+  if (!any) return;  // the row holds no token
+  const float inv = 1.0f / l;
+  const int tok = r / a.G, head = r - tok * a.G;
+  const long row = (u * a.G + head) * a.T + tok;
+  if (a.out_dtype == KVQ_F32) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kD) + lane;
+    if (in_bounds(a.ctl, o, 16))
+      *o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  } else {
+    uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD) + lane;
+    if (in_bounds(a.ctl, o, 8))
+      *o = make_uint2(pack_bf2(acc.x * inv, acc.y * inv), pack_bf2(acc.z * inv, acc.w * inv));
+  }
+}
+
+struct TreePlan {
+  int rows, row_blocks, int4_tiles, tiles, ctas, slots;
+  long units, items;
+};
+
+TreePlan tree_plan(const kvq_cache &c, int Hq, int T, int num_sms) {
+  const CacheDims d = dims_of(c);
+  TreePlan p;
+  p.rows = T * (Hq / d.Hkv);
+  p.row_blocks = (p.rows + kRowBlock - 1) / kRowBlock;
+  p.int4_tiles = (d.cut + kBN - 1) / kBN;
+  p.tiles = p.int4_tiles + (d.R + T + kBN - 1) / kBN;
+  p.units = static_cast<long>(d.B) * d.Hkv;
+  p.items = p.units * p.row_blocks * p.tiles;
+  p.ctas = static_cast<int>(std::min<long>(p.items, num_sms));
+  // a row block's tiles meet at most (tiles - 2) / min_per + 2 slices
+  const long min_per = p.items / p.ctas;
+  p.slots = p.tiles >= 2 ? static_cast<int>((p.tiles - 2) / min_per + 2) : 1;
+  return p;
+}
+
+}  // namespace
+
+bool tree_tensor_supported(const kvq_cache &c, int q_dtype, int tree_dtype, int Hq, int T) {
+  const bool win = c.recent == 0 || (c.kwin_dtype == KVQ_BF16 && c.vwin_dtype == KVQ_BF16);
+  // an MXFP8 window type rounds Q even when the window is empty
+  return c.head_dim == kD && win && c.kwin_dtype != KVQ_MXFP8 && q_dtype == KVQ_BF16 &&
+         tree_dtype == KVQ_BF16 &&
+         static_cast<long>(T) * (Hq / c.kv_heads) <= (1L << 24) &&
+         static_cast<long>(c.n_tokens) + T < (1L << 30);
+}
+
+size_t tree_workspace_bytes(const kvq_cache &c, int Hq, int T, int num_sms) {
+  const TreePlan p = tree_plan(c, Hq, T, num_sms);
+  return sizeof(float) * static_cast<size_t>(p.units) * p.row_blocks * p.slots * kRowBlock *
+         kPartStride;
+}
+
+int launch_attend_tree(const kvq_cache &c, const void *q, int Hq, int T, const void *k_tree,
+                       const void *v_tree, const int32_t *parents, float scale_log2, void *out,
+                       int out_dtype, void *ws, const KernelCtl &ctl, int num_sms,
+                       cudaStream_t s) {
+  const CacheDims d = dims_of(c);
+  const TreePlan p = tree_plan(c, Hq, T, num_sms);
+  TreeArgs a;
+  a.k_codes = c.k_codes;
+  a.k_scales = c.k_scales;
+  a.v_codes = c.v_codes;
+  a.v_scales = c.v_scales;
+  a.k_window = static_cast<const uint16_t *>(c.k_window);
+  a.v_window = static_cast<const uint16_t *>(c.v_window);
+  a.k_tree = static_cast<const uint16_t *>(k_tree);
+  a.v_tree = static_cast<const uint16_t *>(v_tree);
+  a.q = static_cast<const uint16_t *>(q);
+  a.parents = parents;
+  a.Hkv = d.Hkv;
+  a.G = Hq / d.Hkv;
+  a.T = T;
+  a.R = d.R;
+  a.cut = d.cut;
+  a.Gk = d.Gk;
+  a.Gs = d.Gs;
+  a.Vs = d.Vs;
+  a.Ws = d.Ws;
+  a.rows = p.rows;
+  a.row_blocks = p.row_blocks;
+  a.int4_tiles = p.int4_tiles;
+  a.tiles = p.tiles;
+  a.items = p.items;
+  a.ctas = p.ctas;
+  a.slots = p.slots;
+  a.scale_log2 = scale_log2;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.partials = static_cast<float *>(ws);
+  a.ctl = ctl;
+  const size_t smem = sizeof(TreeSmem) + 1024;
+  if (opt_in_smem(tree_kernel, smem) != cudaSuccess) return -1;
+  launch_dependent(tree_kernel, dim3(p.ctas), dim3(kThreads), smem, s, a);
+  const long total_rows = p.units * p.rows;
+  launch_dependent(tree_combine_kernel,
+                   dim3(static_cast<unsigned>((total_rows + kCombineWarps - 1) / kCombineWarps)),
+                   dim3(kCombineWarps * 32), 0, s, a, total_rows);
+  return 2;
+}
+
+}  // namespace kvq

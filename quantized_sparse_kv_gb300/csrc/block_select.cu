@@ -1,0 +1,471 @@
+// Block summaries of a packed cache (kv_block_summary) and the choice of
+// blocks from them (kv_select_blocks).
+//
+// Mathematics. A block's summary is the mean of its dequantized keys, rounded
+// to int8 with one scale: with c the codes of a 32-token group and s its
+// per-channel scale the group's sum is fl(s * sum c), sum c an integer; the
+// groups' sums are added in order. A query row is rounded to int8 the same
+// way, the product of the two code vectors is an integer below 2^24, and the
+// score is two fp32 multiplications. Nothing depends on the order of the
+// additions, so the chosen blocks are a function of the inputs alone.
+//
+// What bounds them. The summary reads 20 D bytes of K codes and scales per
+// group and writes D + 4 per block: memory. Scoring reads D + 4 bytes per
+// block, about 1/40 of the block itself, and needs heads * D / 4 dp4a
+// instructions for it; choosing is a radix selection over one score row and
+// bound by latency.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "kvq_internal.h"
+
+namespace kvq {
+namespace {
+
+// fl(x / s) rounded to an integer, 0 for a zero scale.
+__device__ __forceinline__ int int8_code(float x, float s) {
+  return s > 0.0f ? __float2int_rn(__fdiv_rn(x, s)) : 0;
+}
+
+struct SummaryArgs {
+  const uint8_t *k_codes;
+  const float *k_scales;
+  int8_t *codes;
+  float *scales;
+  int D, cut, Gk, Gs;      // Gs: K groups per unit (stride)
+  int m;                   // groups per block
+  int first, blocks, cap;  // blocks [first, blocks) are computed; cap: stride
+  long units;
+  KernelCtl ctl;
+};
+
+// ------------------------------------------------------------------ D = 128
+// One warp per block. A lane reads 16 bytes (32 channels) of a token row, so
+// four loads of a warp take a whole group's codes (2 KB) and one more its
+// scales. Nibbles are summed as bytes: two masks split a word into its even
+// and odd channels, four tokens a lane and three lane exchanges give the 32
+// tokens' sums (a byte holds 16 tokens' worth, 240; the last exchange is on
+// 16-bit halves). Each exchange also halves what a lane keeps, so a lane ends
+// with the four channels whose scales it loaded.
+constexpr int kSumWarps = 8;
+
+__device__ __forceinline__ uint32_t prmt_u(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
+// Sums of the codes of one group in this lane's channels: 32 (lane & 3) +
+// 16 b2 + 8 b3 + 4 b4 + 0..3, b2..b4 the lane's upper bits.
+__device__ __forceinline__ int4 group_sums(const uint4 (&w)[4], int lane) {
+  uint32_t lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};  // word j: channels 8j + 0,2,4,6 / 1,3,5,7
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] += x[j] & 0x0F0F0F0Fu;
+      hi[j] += (x[j] >> 4) & 0x0F0F0F0Fu;
+    }
+  }
+  const bool b2 = lane & 4, b3 = lane & 8, b4 = lane & 16;
+  uint32_t l2[2], h2[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {  // keep words 0,1 (b2 = 0) or 2,3
+    l2[j] = (b2 ? lo[2 + j] : lo[j]) + __shfl_xor_sync(0xffffffffu, b2 ? lo[j] : lo[2 + j], 4);
+    h2[j] = (b2 ? hi[2 + j] : hi[j]) + __shfl_xor_sync(0xffffffffu, b2 ? hi[j] : hi[2 + j], 4);
+  }
+  const uint32_t l1 = (b3 ? l2[1] : l2[0]) + __shfl_xor_sync(0xffffffffu, b3 ? l2[0] : l2[1], 8);
+  const uint32_t h1 = (b3 ? h2[1] : h2[0]) + __shfl_xor_sync(0xffffffffu, b3 ? h2[0] : h2[1], 8);
+  // widen: channels (0, 2) and (4, 6) of the word, (1, 3) and (5, 7)
+  const uint32_t la = prmt_u(l1, 0u, 0x4140u), lb = prmt_u(l1, 0u, 0x4342u);
+  const uint32_t ha = prmt_u(h1, 0u, 0x4140u), hb = prmt_u(h1, 0u, 0x4342u);
+  const uint32_t e = (b4 ? lb : la) + __shfl_xor_sync(0xffffffffu, b4 ? la : lb, 16);
+  const uint32_t o = (b4 ? hb : ha) + __shfl_xor_sync(0xffffffffu, b4 ? ha : hb, 16);
+  // 32 tokens of code + 8: padding tokens hold code 0
+  return make_int4(static_cast<int>(e & 0xffffu) - 256, static_cast<int>(o & 0xffffu) - 256,
+                   static_cast<int>(e >> 16) - 256, static_cast<int>(o >> 16) - 256);
+}
+
+template <int M>
+__global__ void __launch_bounds__(kSumWarps * 32) summary128_kernel(const SummaryArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const long per = a.blocks - a.first;
+  const long id = static_cast<long>(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
+  if (id >= per * a.units) return;
+  const long u = id / per;
+  const int blk = a.first + static_cast<int>(id - u * per);
+  const int g0 = blk * M;
+  const int ch = 32 * (lane & 3) + ((lane & 4) << 2) + (lane & 8) + ((lane & 16) >> 2);
+  uint4 w[M][4];
+  float4 sc[M];
+#pragma unroll
+  for (int g = 0; g < M; ++g) {
+    const bool have = g0 + g < a.Gk;
+    const long gi = u * a.Gs + g0 + g;
+    const uint8_t *p = a.k_codes + gi * 2048 + 16 * lane;
+    const float *s = a.k_scales + gi * 128 + ch;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // lane reads token 8i + lane / 4, bytes 16 (lane & 3)..
+      w[g][i] = have && in_bounds(a.ctl, p + 512 * i, 16)
+                    ? __ldcs(reinterpret_cast<const uint4 *>(p + 512 * i))
+                    : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+    sc[g] = have && in_bounds(a.ctl, s, 16) ? __ldcs(reinterpret_cast<const float4 *>(s))
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  float acc[4];
+#pragma unroll
+  for (int g = 0; g < M; ++g) {
+    const int4 c = group_sums(w[g], lane);
+    const float p[4] = {__fmul_rn(sc[g].x, static_cast<float>(c.x)),
+                        __fmul_rn(sc[g].y, static_cast<float>(c.y)),
+                        __fmul_rn(sc[g].z, static_cast<float>(c.z)),
+                        __fmul_rn(sc[g].w, static_cast<float>(c.w))};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = g == 0 ? p[j] : __fadd_rn(acc[j], p[j]);
+  }
+  const float tokens = static_cast<float>(min(32 * M, a.cut - 32 * M * blk));
+  float mx = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    acc[j] = __fdiv_rn(acc[j], tokens);
+    mx = fmaxf(mx, fabsf(acc[j]));
+  }
+  const float scale = __fdiv_rn(warp_max(mx), 127.0f);
+  uint32_t out = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    out |= (static_cast<uint32_t>(int8_code(acc[j], scale)) & 0xffu) << (8 * j);
+  const long row = u * a.cap + blk;
+  if (in_bounds(a.ctl, a.codes + row * 128 + ch, 4))
+    *reinterpret_cast<uint32_t *>(a.codes + row * 128 + ch) = out;
+  if (lane == 0 && in_bounds(a.ctl, a.scales + row, 4)) a.scales[row] = scale;
+}
+
+// ------------------------------------------------------------------ any D
+// One CTA per block: D / 8 threads share a token row (4 bytes, 8 channels
+// each), the other threads further rows; integer sums meet in shared memory.
+constexpr int kSumThreads = 256;
+
+__global__ void __launch_bounds__(kSumThreads) summary_kernel(const SummaryArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ int sums[4][256];
+  __shared__ float red[kSumThreads / 32];
+  const int tid = threadIdx.x, D = a.D;
+  const int blk = a.first + static_cast<int>(blockIdx.x);
+  const int per_row = D / 8, rows = kSumThreads / per_row;
+  const int piece = tid % per_row, r0 = tid / per_row;
+  for (long u = blockIdx.y; u < a.units; u += gridDim.y) {
+    for (int i = tid; i < a.m * D; i += kSumThreads) sums[i / D][i % D] = 0;
+    __syncthreads();
+    for (int g = 0; g < a.m; ++g) {
+      const long gi = u * a.Gs + blk * a.m + g;
+      if (blk * a.m + g >= a.Gk || r0 >= rows) continue;
+      uint32_t lo = 0u, hi = 0u;  // at most 32 / rows + 1 <= 5 tokens a byte (rows >= 8)
+      for (int t = r0; t < 32; t += rows) {
+        const uint8_t *p = a.k_codes + (gi * 32 + t) * (D / 2) + 4 * piece;
+        const uint32_t x = in_bounds(a.ctl, p, 4) ? *reinterpret_cast<const uint32_t *>(p)
+                                                  : 0x88888888u;
+        lo += x & 0x0F0F0F0Fu;
+        hi += (x >> 4) & 0x0F0F0F0Fu;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (r0 >= 32) break;
+        atomicAdd(&sums[g][8 * piece + 2 * j], static_cast<int>((lo >> (8 * j)) & 0xffu));
+        atomicAdd(&sums[g][8 * piece + 2 * j + 1], static_cast<int>((hi >> (8 * j)) & 0xffu));
+      }
+    }
+    __syncthreads();
+    const float tokens = static_cast<float>(min(32 * a.m, a.cut - 32 * a.m * blk));
+    float mean = 0.0f;
+    if (tid < D) {
+      float acc = 0.0f;
+      for (int g = 0; g < a.m && blk * a.m + g < a.Gk; ++g) {
+        const float *s = a.k_scales + (u * a.Gs + blk * a.m + g) * D + tid;
+        const float p = __fmul_rn(in_bounds(a.ctl, s, 4) ? *s : 0.0f,
+                                  static_cast<float>(sums[g][tid] - 256));
+        acc = g == 0 ? p : __fadd_rn(acc, p);
+      }
+      mean = __fdiv_rn(acc, tokens);
+    }
+    const float wm = warp_max(fabsf(mean));
+    if ((tid & 31) == 0) red[tid >> 5] = wm;
+    __syncthreads();
+    float mx = red[0];
+#pragma unroll
+    for (int w = 1; w < kSumThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+    const float scale = __fdiv_rn(mx, 127.0f);
+    const long row = u * a.cap + blk;
+    if (tid < D && in_bounds(a.ctl, a.codes + row * D + tid, 1))
+      a.codes[row * D + tid] = static_cast<int8_t>(int8_code(mean, scale));
+    if (tid == 0 && in_bounds(a.ctl, a.scales + row, 4)) a.scales[row] = scale;
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ scores
+struct SelectArgs {
+  const int8_t *codes;
+  const float *scales;
+  const void *q;
+  int q_dtype;
+  int D, Hkv, G, n_q;   // G: query heads per KV head
+  int blocks, cap, top_k, sink;
+  float *scores;        // [unit][n_q][blocks]
+  int32_t *selected;
+  KernelCtl ctl;
+};
+
+constexpr int kScoreThreads = 128;
+constexpr int kMaxGroup = 64;  // query heads per KV head
+
+// One thread per block of a (unit, query token); q of the G heads as int8 in
+// shared memory, read by broadcast. A thread reads its block's D codes 16
+// bytes at a time and keeps eight heads' products at once.
+__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  extern __shared__ __align__(16) int8_t qs[];  // [ceil(G / 8) * 8][D]
+  __shared__ float sq[kMaxGroup];
+  const int D = a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int uq = blockIdx.y;  // unit * n_q + query token
+  const long u = uq / a.n_q;
+  const int iq = uq % a.n_q;
+  const int Gp = (a.G + 7) / 8 * 8;
+  for (int h = warp; h < Gp; h += kScoreThreads / 32) {
+    const long row = (u * a.G + h) * a.n_q + iq;  // [batch][q_heads][n_q], q head = kv * G + h
+    float x[8], mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int d = lane + 32 * i;
+      x[i] = 0.0f;
+      if (h < a.G && d < D) {
+        if (a.q_dtype == KVQ_F32) {
+          const float *p = static_cast<const float *>(a.q) + row * D + d;
+          if (in_bounds(a.ctl, p, 4)) x[i] = *p;
+        } else {
+          const uint16_t *p = static_cast<const uint16_t *>(a.q) + row * D + d;
+          if (in_bounds(a.ctl, p, 2)) x[i] = bf16_to_f32(*p);
+        }
+      }
+      mx = fmaxf(mx, fabsf(x[i]));
+    }
+    const float s = __fdiv_rn(warp_max(mx), 127.0f);
+    if (lane == 0 && h < a.G) sq[h] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < D)
+        qs[h * D + lane + 32 * i] = static_cast<int8_t>(int8_code(x[i], s));
+  }
+  __syncthreads();
+  const int blk = blockIdx.x * kScoreThreads + threadIdx.x;
+  if (blk >= a.blocks) return;
+  const long row = u * a.cap + blk;
+  float score = -CUDART_INF_F;
+  if (in_bounds(a.ctl, a.codes + row * D, D) && in_bounds(a.ctl, a.scales + row, 4)) {
+    const float sb = a.scales[row];
+    const uint4 *kp = reinterpret_cast<const uint4 *>(a.codes + row * D);
+    for (int h0 = 0; h0 < Gp; h0 += 8) {
+      int dot[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 k = kp[c];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const int4 q = *reinterpret_cast<const int4 *>(qs + (h0 + h) * D + 16 * c);
+          dot[h] = __dp4a(static_cast<int>(k.x), q.x, dot[h]);
+          dot[h] = __dp4a(static_cast<int>(k.y), q.y, dot[h]);
+          dot[h] = __dp4a(static_cast<int>(k.z), q.z, dot[h]);
+          dot[h] = __dp4a(static_cast<int>(k.w), q.w, dot[h]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (h0 + h < a.G)
+          score = fmaxf(score, __fmul_rn(__fmul_rn(sq[h0 + h], sb), static_cast<float>(dot[h])));
+    }
+  }
+  float *o = a.scores + static_cast<long>(uq) * a.blocks + blk;
+  if (in_bounds(a.ctl, o, 4)) *o = blk < a.sink ? CUDART_INF_F : score;
+}
+
+// ------------------------------------------------------------------ selection
+// One CTA per (unit, query token): radix selection of the top_k-th largest
+// score over order-preserving keys (8 bits a round, histogram in shared
+// memory), then the blocks above it and the lowest-numbered ones equal to it
+// are written in increasing order.
+constexpr int kSelThreads = 256;
+
+// Larger score, larger key; -0 counts as +0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Exclusive prefix sum of v over the CTA and its total.
+__device__ __forceinline__ int cta_scan(int v, int *warp_sums, int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ int hist[256], warp_sums[kSelThreads / 32];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_left;
+  const int tid = threadIdx.x;
+  const long uq = blockIdx.x;
+  const float *sc = a.scores + uq * a.blocks;
+  int32_t *out = a.selected + uq * a.top_k;
+  const int k = min(a.top_k, a.blocks);
+  if (!in_bounds(a.ctl, out, sizeof(int32_t) * a.top_k) ||
+      (a.blocks > 0 && !in_bounds(a.ctl, sc, sizeof(float) * a.blocks)))
+    return;
+  for (int i = k + tid; i < a.top_k; i += kSelThreads) out[i] = -1;
+  if (a.blocks <= a.top_k) {
+    for (int i = tid; i < a.blocks; i += kSelThreads) out[i] = i;
+    return;
+  }
+  uint32_t prefix = 0u, mask = 0u;
+  int left = k;  // how many of the keys matching the prefix are to be taken
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.blocks; i += kSelThreads) {
+      const uint32_t key = order_key(sc[i]);
+      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    // the digit at which the count from the top reaches `left`: thread i
+    // counts the digits above 255 - i
+    int total;
+    const int c = hist[255 - tid];
+    const int above = cta_scan(c, warp_sums, total);
+    if (above < left && above + c >= left) {
+      s_prefix = prefix | (static_cast<uint32_t>(255 - tid) << shift);
+      s_left = left - above;
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
+    mask |= 255u << shift;
+    __syncthreads();
+  }
+  // keys above `prefix` all, keys equal to it the first `left`
+  int written = 0, equal_before = 0;
+  for (int base = 0; base < a.blocks; base += kSelThreads) {
+    const int i = base + tid;
+    const uint32_t key = i < a.blocks ? order_key(sc[i]) : 0u;
+    const bool gt = i < a.blocks && key > prefix, eq = i < a.blocks && key == prefix;
+    int total;
+    // one scan for both counts: at most 256 of each
+    const int both = cta_scan((gt ? 1 : 0) | (eq ? 1 << 16 : 0), warp_sums, total);
+    const int eq_rank = equal_before + (both >> 16);
+    // equal ones written before this thread: those with rank < left
+    const int eq_taken_before = min(eq_rank, left) - min(equal_before, left);
+    const int pos = written + (both & 0xffff) + eq_taken_before;
+    if (gt || (eq && eq_rank < left)) out[pos] = i;
+    const int eq_total = total >> 16;
+    written += (total & 0xffff) + min(equal_before + eq_total, left) - min(equal_before, left);
+    equal_before += eq_total;
+  }
+}
+
+}  // namespace
+
+int launch_block_summary(const kvq_cache &c, const kvq_summary &sm, int first, int blocks,
+                         const KernelCtl &ctl, cudaStream_t s) {
+  const CacheDims d = dims_of(c);
+  SummaryArgs a;
+  a.k_codes = c.k_codes;
+  a.k_scales = c.k_scales;
+  a.codes = sm.codes;
+  a.scales = sm.scales;
+  a.D = d.D;
+  a.cut = d.cut;
+  a.Gk = d.Gk;
+  a.Gs = d.Gs;
+  a.m = sm.block / kGroup;
+  a.first = first;
+  a.blocks = blocks;
+  a.cap = sm.cap_blocks;
+  a.units = static_cast<long>(d.B) * d.Hkv;
+  a.ctl = ctl;
+  if (d.D == 128) {
+    const long warps = a.units * (blocks - first);
+    const dim3 grid(static_cast<unsigned>((warps + kSumWarps - 1) / kSumWarps));
+    if (a.m == 1)
+      launch_dependent(summary128_kernel<1>, grid, dim3(kSumWarps * 32), 0, s, a);
+    else if (a.m == 2)
+      launch_dependent(summary128_kernel<2>, grid, dim3(kSumWarps * 32), 0, s, a);
+    else
+      launch_dependent(summary128_kernel<4>, grid, dim3(kSumWarps * 32), 0, s, a);
+    return 1;
+  }
+  const dim3 grid(static_cast<unsigned>(blocks - first),
+                  static_cast<unsigned>(std::min<long>(a.units, 65535)));
+  launch_dependent(summary_kernel, grid, dim3(kSumThreads), 0, s, a);
+  return 1;
+}
+
+size_t select_workspace_bytes(const kvq_cache &c, int blocks, int n_q) {
+  return sizeof(float) * static_cast<size_t>(c.batch) * c.kv_heads * n_q * blocks;
+}
+
+int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, const void *q,
+                         int q_dtype, int Hq, int n_q, int top_k, int n_sink, int32_t *selected,
+                         void *ws, const KernelCtl &ctl, cudaStream_t s) {
+  SelectArgs a;
+  a.codes = sm.codes;
+  a.scales = sm.scales;
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.D = c.head_dim;
+  a.Hkv = c.kv_heads;
+  a.G = Hq / c.kv_heads;
+  a.n_q = n_q;
+  a.blocks = blocks;
+  a.cap = sm.cap_blocks;
+  a.top_k = top_k;
+  a.sink = n_sink;
+  a.scores = static_cast<float *>(ws);
+  a.selected = selected;
+  a.ctl = ctl;
+  const unsigned units = static_cast<unsigned>(c.batch) * c.kv_heads * n_q;
+  int launches = 0;
+  if (blocks > top_k) {
+    const size_t smem = static_cast<size_t>((a.G + 7) / 8 * 8) * a.D;
+    launch_dependent(block_scores_kernel,
+                     dim3((blocks + kScoreThreads - 1) / kScoreThreads, units),
+                     dim3(kScoreThreads), smem, s, a);
+    ++launches;
+  }
+  launch_dependent(select_kernel, dim3(units), dim3(kSelThreads), 0, s, a);
+  return launches + 1;
+}
+
+int select_max_group() { return kMaxGroup; }
+
+}  // namespace kvq

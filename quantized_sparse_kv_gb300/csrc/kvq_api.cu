@@ -144,6 +144,29 @@ void ctl_add_cache(kvq::KernelCtl &c, const kvq_cache &k) {
 #endif
 }
 
+// Blocks of the int4 part.
+int summary_blocks(const kvq_cache &c, int block) {
+  return (c.n_tokens - c.recent + block - 1) / block;
+}
+
+kvq_status check_summary(const kvq_cache *c, const kvq_summary *s) {
+  if (!s) return KVQ_ERR_ARG;
+  if (s->block != 32 && s->block != 64 && s->block != 128) return KVQ_ERR_ARG;
+  const int blocks = summary_blocks(*c, s->block);
+  if (s->cap_blocks < blocks) return KVQ_ERR_WORKSPACE;
+  if (blocks > 0) {
+    if (!s->codes || !s->scales) return KVQ_ERR_ARG;
+    if (!aligned16(s->codes) || !aligned16(s->scales)) return KVQ_ERR_ALIGN;
+  }
+  return KVQ_OK;
+}
+
+void ctl_add_summary(kvq::KernelCtl &c, const kvq_cache &k, const kvq_summary &s) {
+  const size_t rows = static_cast<size_t>(k.batch) * k.kv_heads * s.cap_blocks;
+  ctl_add(c, s.codes, rows * k.head_dim);
+  ctl_add(c, s.scales, rows * sizeof(float));
+}
+
 }  // namespace
 
 extern "C" {
@@ -596,6 +619,242 @@ kvq_status kv_attend_decode_static(const kvq_cache *cache, const void *q, int32_
                                           out, out_dtype, scratch, ctl, sms,
                                           reinterpret_cast<cudaStream_t>(stream));
   return finish(n, "decode_static");
+}
+
+kvq_status kvq_rope_turns(int32_t rotary_dim, double base, const kvq_rope_scaling *scaling,
+                          uint64_t *turns, float *amplitude) {
+  if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 || !turns || !amplitude)
+    return KVQ_ERR_ARG;
+  return kvq::rope_turns(rotary_dim, base, scaling, turns, amplitude) ? KVQ_OK : KVQ_ERR_ARG;
+}
+
+kvq_status kv_rope(const kvq_rope_tensor *tensors, int32_t n_tensors, int32_t dtype,
+                   int32_t batch, int32_t n, int32_t head_dim, int32_t rotary_dim, int32_t layout,
+                   const uint64_t *turns, float amplitude, int32_t inverse,
+                   const int32_t *positions, int32_t *dev_status, kvq_stream_t stream) {
+  if (!tensors || n_tensors < 1 || n_tensors > 3) return KVQ_ERR_ARG;
+  if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_ARG;
+  if (batch < 0 || n < 0 || head_dim < 32 || head_dim > 256 || head_dim % 32) return KVQ_ERR_ARG;
+  if (rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2) return KVQ_ERR_ARG;
+  if (layout != KVQ_ROPE_HALF && layout != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_ARG;
+  if (!turns || !(amplitude > 0.0f)) return KVQ_ERR_ARG;
+  const int64_t unit = dtype == KVQ_F32 ? 4 : 8;  // elements in 16 bytes
+  kvq::RopeTensors t = {};
+  t.n = n_tensors;
+  int64_t heads = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const kvq_rope_tensor &x = tensors[i];
+    if (x.heads < 1 || x.stride_b < 0 || x.stride_h < 0 || x.stride_t < 0) return KVQ_ERR_ARG;
+    heads += x.heads;
+  }
+  if (heads > 0x7fffffffL) return KVQ_ERR_ARG;
+  if (batch == 0 || n == 0) {
+    g_last_launches = 0;
+    g_last_path = "rope";
+    return KVQ_OK;
+  }
+  if (static_cast<int64_t>(batch) * n > 0x7fffffffL) return KVQ_ERR_UNSUPPORTED;
+  if (!positions) return KVQ_ERR_ARG;
+  for (int i = 0; i < n_tensors; ++i)
+    if (!tensors[i].in || !tensors[i].out) return KVQ_ERR_ARG;
+  if (!aligned16(turns) || !aligned16(positions) || (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  for (int i = 0; i < n_tensors; ++i) {
+    const kvq_rope_tensor &x = tensors[i];
+    if (!aligned16(x.in) || !aligned16(x.out) || x.stride_b % unit || x.stride_h % unit ||
+        x.stride_t % unit)
+      return KVQ_ERR_ALIGN;
+    t.in[i] = x.in;
+    t.out[i] = x.out;
+    t.heads[i] = x.heads;
+    t.rotate[i] = x.rotate;
+    t.sb[i] = x.stride_b;
+    t.sh[i] = x.stride_h;
+    t.st[i] = x.stride_t;
+    ctl_add(ctl, x.in,
+            rows_bytes((batch - 1) * x.stride_b + (x.heads - 1) * x.stride_h +
+                           (n - 1) * x.stride_t + head_dim, 1, dtype));
+    ctl_add(ctl, x.out, rows_bytes(static_cast<long>(batch) * x.heads * n, head_dim, dtype));
+  }
+  t.total_heads = static_cast<int>(heads);
+  ctl_add(ctl, turns, static_cast<size_t>(rotary_dim) * 4);
+  ctl_add(ctl, positions, static_cast<size_t>(batch) * n * 4);
+  const int k = kvq::launch_rope(t, dtype, batch, n, head_dim, rotary_dim, layout, turns,
+                                 amplitude, inverse, positions, ctl, sm_count(),
+                                 reinterpret_cast<cudaStream_t>(stream));
+  return finish(k, "rope");
+}
+
+kvq_status kv_attend_tree(const kvq_cache *cache, const void *q, int32_t q_dtype,
+                          int32_t q_heads, int32_t n_tree, const void *k_tree,
+                          const void *v_tree, int32_t tree_dtype, const int32_t *parents,
+                          float sm_scale, void *out, int32_t out_dtype, void *workspace,
+                          size_t *ws_bytes, int32_t *dev_status, kvq_stream_t stream) {
+  const kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!ws_bytes) return KVQ_ERR_ARG;
+  if (q_heads < 1 || q_heads % cache->kv_heads) return KVQ_ERR_ARG;
+  if (n_tree < 1 || n_tree > KVQ_TREE_MAX) return KVQ_ERR_ARG;
+  if ((q_dtype != KVQ_F32 && q_dtype != KVQ_BF16) ||
+      (tree_dtype != KVQ_F32 && tree_dtype != KVQ_BF16) ||
+      (out_dtype != KVQ_F32 && out_dtype != KVQ_BF16))
+    return KVQ_ERR_ARG;
+  const int sms = sm_count();
+  const bool tensor = kvq::tree_tensor_supported(*cache, q_dtype, tree_dtype, q_heads, n_tree);
+  if (!tensor && (q_heads > 65535 || cache->batch > 65535)) return KVQ_ERR_UNSUPPORTED;
+  const size_t need = tensor ? kvq::tree_workspace_bytes(*cache, q_heads, n_tree, sms) : 0;
+  if (!workspace) {
+    *ws_bytes = need;
+    return KVQ_OK;
+  }
+  if (*ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (!q || !out || !k_tree || !v_tree || !parents) return KVQ_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_tree) || !aligned16(v_tree) ||
+      !aligned16(parents) || !aligned16(workspace) || (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  const float scale = resolve_scale(sm_scale, cache->head_dim);
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  {
+    const long rows = static_cast<long>(cache->batch) * q_heads * n_tree;
+    const long tree = static_cast<long>(cache->batch) * cache->kv_heads * n_tree;
+    ctl_add_cache(ctl, *cache);
+    ctl_add(ctl, q, rows_bytes(rows, cache->head_dim, q_dtype));
+    ctl_add(ctl, out, rows_bytes(rows, cache->head_dim, out_dtype));
+    ctl_add(ctl, k_tree, rows_bytes(tree, cache->head_dim, tree_dtype));
+    ctl_add(ctl, v_tree, rows_bytes(tree, cache->head_dim, tree_dtype));
+    ctl_add(ctl, parents, rows_bytes(cache->batch, n_tree, KVQ_F32));
+    ctl_add(ctl, workspace, *ws_bytes);
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (tensor) {
+    const int n = kvq::launch_attend_tree(*cache, q, q_heads, n_tree, k_tree, v_tree, parents,
+                                          static_cast<float>(scale * kLog2e), out, out_dtype,
+                                          workspace, ctl, sms, s);
+    if (n < 0) return KVQ_ERR_CUDA;
+    return finish(n, "tree_tensor");
+  }
+  const int n = kvq::launch_tree_rows(*cache, q, q_dtype, q_heads, n_tree, k_tree, v_tree,
+                                      tree_dtype, parents, scale, out, out_dtype, ctl, s);
+  return finish(n, "tree_rows");
+}
+
+kvq_status kv_block_summary(const kvq_cache *cache, const kvq_summary *summary,
+                            int32_t first_block, int32_t *dev_status, kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  st = check_summary(cache, summary);
+  if (st != KVQ_OK) return st;
+  if (first_block < 0) return KVQ_ERR_ARG;
+  if (dev_status && !aligned16(dev_status)) return KVQ_ERR_ALIGN;
+  const int blocks = summary_blocks(*cache, summary->block);
+  if (first_block >= blocks) {
+    g_last_launches = 0;
+    g_last_path = "block_summary";
+    return KVQ_OK;
+  }
+  // one warp per block: the grid's x holds 2^31 - 1 CTAs of eight
+  if (static_cast<long>(cache->batch) * cache->kv_heads * blocks > 0x7fffffffL)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  ctl_add_cache(ctl, *cache);
+  ctl_add_summary(ctl, *cache, *summary);
+  const int n = kvq::launch_block_summary(*cache, *summary, first_block, blocks, ctl,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return finish(n, "block_summary");
+}
+
+kvq_status kv_select_blocks(const kvq_cache *cache, const kvq_summary *summary, const void *q,
+                            int32_t q_dtype, int32_t q_heads, int32_t n_q, int32_t top_k,
+                            int32_t n_sink, int32_t *selected, void *workspace, size_t *ws_bytes,
+                            int32_t *dev_status, kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  st = check_summary(cache, summary);
+  if (st != KVQ_OK) return st;
+  if (!ws_bytes) return KVQ_ERR_ARG;
+  if (q_heads < 1 || q_heads % cache->kv_heads || n_q < 1) return KVQ_ERR_ARG;
+  if (q_dtype != KVQ_F32 && q_dtype != KVQ_BF16) return KVQ_ERR_ARG;
+  if (top_k < 1 || n_sink < 0 || n_sink > top_k) return KVQ_ERR_ARG;
+  if (q_heads / cache->kv_heads > kvq::select_max_group()) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<long>(cache->batch) * cache->kv_heads * n_q > 65535) return KVQ_ERR_UNSUPPORTED;
+  const int blocks = summary_blocks(*cache, summary->block);
+  const size_t need = blocks > top_k ? kvq::select_workspace_bytes(*cache, blocks, n_q) : 0;
+  if (!workspace) {
+    *ws_bytes = need;
+    return KVQ_OK;
+  }
+  if (*ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (!q || !selected) return KVQ_ERR_ARG;
+  if (!aligned16(q) || !aligned16(selected) || !aligned16(workspace) ||
+      (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  {
+    const long rows = static_cast<long>(cache->batch) * q_heads * n_q;
+    ctl_add_summary(ctl, *cache, *summary);
+    ctl_add(ctl, q, rows_bytes(rows, cache->head_dim, q_dtype));
+    ctl_add(ctl, selected,
+            rows_bytes(static_cast<long>(cache->batch) * cache->kv_heads * n_q, top_k, KVQ_F32));
+    ctl_add(ctl, workspace, *ws_bytes);
+  }
+  const int n = kvq::launch_select_blocks(*cache, *summary, blocks, q, q_dtype, q_heads, n_q,
+                                          top_k, n_sink, selected, workspace, ctl,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return finish(n, "select_blocks");
+}
+
+kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32_t q_dtype,
+                            int32_t q_heads, int32_t n_q, const int32_t *selected, int32_t top_k,
+                            int32_t block, float sm_scale, void *out, int32_t out_dtype,
+                            void *workspace, size_t *ws_bytes, int32_t *dev_status,
+                            kvq_stream_t stream) {
+  const kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!ws_bytes) return KVQ_ERR_ARG;
+  if (q_heads < 1 || q_heads % cache->kv_heads || n_q < 1 || top_k < 1) return KVQ_ERR_ARG;
+  if (block != 32 && block != 64 && block != 128) return KVQ_ERR_ARG;
+  if ((q_dtype != KVQ_F32 && q_dtype != KVQ_BF16) ||
+      (out_dtype != KVQ_F32 && out_dtype != KVQ_BF16))
+    return KVQ_ERR_ARG;
+  const int sms = sm_count();
+  const bool decode = kvq::blocks_decode_supported(*cache, q_dtype, q_heads, n_q, top_k, block);
+  if (!decode && (q_heads > 65535 || cache->batch > 65535)) return KVQ_ERR_UNSUPPORTED;
+  // the fp32 kernel counts a list's 32-token groups in 32 bits
+  if (!decode && static_cast<long>(top_k) * (block / 32) > (1L << 30)) return KVQ_ERR_UNSUPPORTED;
+  const size_t need =
+      decode ? kvq::blocks_decode_workspace_bytes(*cache, n_q, top_k, block, sms) : 0;
+  if (!workspace) {
+    *ws_bytes = need;
+    return KVQ_OK;
+  }
+  if (*ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (!q || !out || !selected) return KVQ_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(selected) || !aligned16(workspace) ||
+      (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  const float scale = resolve_scale(sm_scale, cache->head_dim);
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  {
+    const long rows = static_cast<long>(cache->batch) * q_heads * n_q;
+    ctl_add_cache(ctl, *cache);
+    ctl_add(ctl, q, rows_bytes(rows, cache->head_dim, q_dtype));
+    ctl_add(ctl, out, rows_bytes(rows, cache->head_dim, out_dtype));
+    ctl_add(ctl, selected,
+            rows_bytes(static_cast<long>(cache->batch) * cache->kv_heads * n_q, top_k, KVQ_F32));
+    ctl_add(ctl, workspace, *ws_bytes);
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int blocks = summary_blocks(*cache, block);
+  if (decode) {
+    const int n = kvq::launch_attend_blocks(*cache, q, q_heads, n_q, selected, top_k, block,
+                                            blocks, static_cast<float>(scale * kLog2e), out,
+                                            out_dtype, workspace, ctl, sms, s);
+    return finish(n, "blocks_decode");
+  }
+  const int n = kvq::launch_block_rows(*cache, q, q_dtype, q_heads, n_q, selected, top_k, block,
+                                       blocks, scale, out, out_dtype, ctl, s);
+  return finish(n, "blocks_rows");
 }
 
 int32_t kvq_last_launch_count(void) { return g_last_launches; }

@@ -76,6 +76,16 @@ int launch_attend_decode(const kvq_cache &c, const void *q, int q_dtype, float s
 size_t decode_static_scratch_limit();
 cudaError_t decode_static_scratch(void **ptr);
 
+// attend_decode.cu: the decode kernels over listed blocks (kv_attend_blocks).
+bool blocks_decode_supported(const kvq_cache &c, int q_dtype, int Hq, int n_q, int top_k,
+                             int block);
+size_t blocks_decode_workspace_bytes(const kvq_cache &c, int n_q, int top_k, int block,
+                                     int num_sms);
+int launch_attend_blocks(const kvq_cache &c, const void *q, int Hq, int n_q,
+                         const int32_t *selected, int top_k, int block, int n_blocks,
+                         float scale_log2, void *out, int out_dtype, void *ws,
+                         const KernelCtl &ctl, int num_sms, cudaStream_t s);
+
 // attend_candidates.cu
 // top_k > 0: attend only the top_k listed keys by exact score (selected, if
 // not null, receives their positions); n_cand <= candidates_topk_max() then.
@@ -113,6 +123,46 @@ int chunk_max_regions();
 int launch_attend_chunk(const kvq_cache &c, const void *q, int Hq, int n_q, float scale_log2,
                         void *out, int out_dtype, const int32_t *bounds, int n_regions,
                         float *mass, void *ws, const KernelCtl &ctl, cudaStream_t s);
+
+// rope.cu: up to three tensors of one kv_rope call (heads counted over all of
+// them in total_heads).
+struct RopeTensors {
+  const void *in[3];
+  void *out[3];
+  int heads[3], rotate[3];
+  int64_t sb[3], sh[3], st[3];
+  int n, total_heads;
+};
+int launch_rope(const RopeTensors &t, int dtype, int batch, int n, int D, int rot, int layout,
+                const uint64_t *turns, float amplitude, int inverse, const int32_t *positions,
+                const KernelCtl &ctl, int num_sms, cudaStream_t s);
+bool rope_turns(int rot, double base, const kvq_rope_scaling *sc, uint64_t *turns, float *amp);
+
+// attend_tree.cu: drafted tokens over the cache and their ancestors, tensor cores.
+bool tree_tensor_supported(const kvq_cache &c, int q_dtype, int tree_dtype, int Hq, int T);
+size_t tree_workspace_bytes(const kvq_cache &c, int Hq, int T, int num_sms);
+int launch_attend_tree(const kvq_cache &c, const void *q, int Hq, int T, const void *k_tree,
+                       const void *v_tree, const int32_t *parents, float scale_log2, void *out,
+                       int out_dtype, void *ws, const KernelCtl &ctl, int num_sms,
+                       cudaStream_t s);
+
+// attend_rows.cu: fp32 rows over chosen keys, any supported shape.
+int launch_tree_rows(const kvq_cache &c, const void *q, int q_dtype, int Hq, int T,
+                     const void *k_tree, const void *v_tree, int tree_dtype,
+                     const int32_t *parents, float scale, void *out, int out_dtype,
+                     const KernelCtl &ctl, cudaStream_t s);
+int launch_block_rows(const kvq_cache &c, const void *q, int q_dtype, int Hq, int n_q,
+                      const int32_t *selected, int top_k, int block, int n_blocks, float scale,
+                      void *out, int out_dtype, const KernelCtl &ctl, cudaStream_t s);
+
+// block_select.cu: block summaries [first, blocks) and the choice of blocks.
+int launch_block_summary(const kvq_cache &c, const kvq_summary &sm, int first, int blocks,
+                         const KernelCtl &ctl, cudaStream_t s);
+size_t select_workspace_bytes(const kvq_cache &c, int blocks, int n_q);
+int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, const void *q,
+                         int q_dtype, int Hq, int n_q, int top_k, int n_sink, int32_t *selected,
+                         void *ws, const KernelCtl &ctl, cudaStream_t s);
+int select_max_group();
 
 // attend_stats.cu: observer statistics of attention rows (kv_attend_stats).
 int stats_max_tokens();

@@ -51,6 +51,22 @@ class KvqCacheStruct(ctypes.Structure):
     ]
 
 
+class KvqRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("p0", ctypes.c_double), ("p1", ctypes.c_double)]
+
+
+class KvqRopeTensor(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("rotate", ctypes.c_int32), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_t", ctypes.c_int64)]
+
+
+class KvqSummary(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("block", ctypes.c_int32), ("cap_blocks", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -94,6 +110,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kv_attend_candidates.argtypes = [cp, vp, i32, i32, i32, vp, i32, i32, f32, vp, i32, vp,
                                          ctypes.POINTER(sz), vp, vp]
     lib.kv_attend_candidates.restype = i32
+    lib.kvq_rope_turns.argtypes = [i32, ctypes.c_double, ctypes.POINTER(KvqRopeScaling),
+                                   ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(f32)]
+    lib.kvq_rope_turns.restype = i32
+    lib.kv_rope.argtypes = [ctypes.POINTER(KvqRopeTensor), i32, i32, i32, i32, i32, i32, i32, vp,
+                            f32, i32, vp, vp, vp]
+    lib.kv_rope.restype = i32
+    lib.kv_attend_tree.argtypes = [cp, vp, i32, i32, i32, vp, vp, i32, vp, f32, vp, i32, vp,
+                                   ctypes.POINTER(sz), vp, vp]
+    lib.kv_attend_tree.restype = i32
+    sp = ctypes.POINTER(KvqSummary)
+    lib.kv_block_summary.argtypes = [cp, sp, i32, vp, vp]
+    lib.kv_block_summary.restype = i32
+    lib.kv_select_blocks.argtypes = [cp, sp, vp, i32, i32, i32, i32, i32, vp, vp,
+                                     ctypes.POINTER(sz), vp, vp]
+    lib.kv_select_blocks.restype = i32
+    lib.kv_attend_blocks.argtypes = [cp, vp, i32, i32, i32, vp, i32, i32, f32, vp, i32, vp,
+                                     ctypes.POINTER(sz), vp, vp]
+    lib.kv_attend_blocks.restype = i32
     lib.kvq_last_launch_count.argtypes = []
     lib.kvq_last_launch_count.restype = i32
     lib.kvq_last_path.argtypes = []
@@ -508,3 +542,330 @@ class AttendRegionDrop:
     def run(self) -> torch.Tensor:
         self._call(_ptr(self.ws), self.ws_bytes)
         return self.out
+
+
+# ------------------------------------------------------------------ rotary positions
+TREE_MAX = 256   # KVQ_TREE_MAX
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+# scaling kinds and the keyword arguments that fill (original, p0, p1)
+ROPE_SCALINGS = {"none": (0, ()), "linear": (1, ()), "base": (2, ()),
+                 "ramp": (3, ("original", "fast", "slow")),
+                 "bands": (4, ("original", "low", "high"))}
+
+
+class RopePlan:
+    """Frequency table of kv_rope on the device (kvq_rope_turns): made once per
+    model. ``scaling``: none, linear, base (``factor``), ramp (``factor``,
+    ``original``, ``fast``, ``slow``) or bands (``factor``, ``original``,
+    ``low``, ``high``); see include/kvq.h."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, device="cuda", **params):
+        if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+            raise ValueError("unknown layout or scaling")
+        kind, names = ROPE_SCALINGS[scaling]
+        if set(params) != set(names):
+            raise TypeError(f"scaling {scaling!r} takes {('factor',) + names if kind else ()}")
+        sc = KvqRopeScaling(kind, float(factor), *([float(params[n]) for n in names] or [0.0] * 3))
+        self.rotary_dim, self.layout = int(rotary_dim), ROPE_LAYOUTS[layout]
+        host = (ctypes.c_uint64 * max(1, self.rotary_dim // 2))()
+        amp = ctypes.c_float(0.0)
+        _check(load_library().kvq_rope_turns(self.rotary_dim, float(base), ctypes.byref(sc), host,
+                                             ctypes.byref(amp)), "kvq_rope_turns")
+        self.amplitude = float(amp.value)
+        self.turns_host = list(host)
+        signed = [x - (1 << 64) if x >> 63 else x for x in self.turns_host]
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+def _static(copies: list, x: torch.Tensor, dtype=None) -> torch.Tensor:
+    """x itself when a prepared call can read it in place, else a dense buffer
+    (of ``dtype``) that every run() fills from x again."""
+    y = x.to(dtype or x.dtype).contiguous()
+    if y.data_ptr() % 16:
+        y = y.clone()
+    if y is not x:
+        copies.append((y, x))
+    return y
+
+
+def _refresh(copies: list):
+    for buf, src in copies:
+        buf.copy_(src)
+
+
+def _rope_view(copies: list, x: torch.Tensor) -> torch.Tensor:
+    """x if kv_rope can read it in place (unit feature stride, 16-byte rows), else as _static."""
+    unit = 16 // x.element_size()
+    ok = (x.stride(3) == 1 and x.data_ptr() % 16 == 0 and
+          all(s >= 0 and (s % unit == 0 or n == 1) for s, n in zip(x.stride()[:3], x.shape[:3])))
+    return x if ok else _static(copies, x)
+
+
+class Rope:
+    """A prepared kv_rope call: q (batch, heads, n, D) and optionally k of the
+    same batch, n and D, at any strides (views of a projection's rows are read
+    in place when their rows start on 16 bytes); ``v`` is only copied to the
+    dense layout. ``run()`` returns the outputs, dense (batch, heads, n, D)."""
+
+    def __init__(self, plan: RopePlan, q: torch.Tensor, k: torch.Tensor | None,
+                 positions: torch.Tensor, v: torch.Tensor | None = None, inverse: bool = False,
+                 out=None):
+        self.lib = load_library()
+        self.plan, self.inverse = plan, int(bool(inverse))
+        src = [x for x in (q, k, v) if x is not None]
+        if any(x.dim() != 4 or x.dtype != q.dtype for x in src):
+            raise TypeError("q, k and v must be (batch, heads, n, D) of one type")
+        if q.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("q, k and v must be float32 or bfloat16")
+        b, _, n, d = q.shape
+        if any((x.shape[0], x.shape[2], x.shape[3]) != (b, n, d) for x in src):
+            raise ValueError("q, k and v must have the same batch, tokens and head dim")
+        if tuple(positions.shape) != (b, n):
+            raise ValueError("positions must be (batch, n)")
+        if plan.rotary_dim > d:
+            raise ValueError("rotary_dim is larger than the head dim")
+        self._copies = []
+        self.src = [_rope_view(self._copies, x) for x in src]
+        self.positions = _static(self._copies, positions, torch.int32)
+        if out is None:
+            out = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in src]
+        if len(out) != len(src) or any(o.shape != x.shape or o.dtype != x.dtype or
+                                       not o.is_contiguous() for o, x in zip(out, src)):
+            raise ValueError("out must hold one dense tensor per input")
+        self.out = list(out)
+        self.dt = F32 if q.dtype == torch.float32 else BF16
+        self.b, self.n, self.d = b, n, d
+        arr = (KvqRopeTensor * len(src))()
+        for i, (x, o) in enumerate(zip(self.src, self.out)):
+            st = [s if m > 1 else 0 for s, m in zip(x.stride()[:3], x.shape[:3])]
+            arr[i] = KvqRopeTensor(_ptr(x), _ptr(o), x.shape[1],
+                                   0 if v is not None and i == len(src) - 1 else 1,
+                                   st[0], st[1], st[2])
+        self.arr = arr
+
+    def run(self):
+        _refresh(self._copies)
+        st = self.lib.kv_rope(self.arr, len(self.src), self.dt, self.b, self.n, self.d,
+                              self.plan.rotary_dim, self.plan.layout, _ptr(self.plan.turns),
+                              self.plan.amplitude, self.inverse, _ptr(self.positions), None,
+                              _stream())
+        _check(st, "kv_rope")
+        return self.out
+
+    def launches(self) -> int:
+        return int(self.lib.kvq_last_launch_count())
+
+
+def rope(plan: RopePlan, q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
+         v: torch.Tensor | None = None, inverse: bool = False):
+    """kv_rope; returns the outputs (q, and k, v if given). ``inverse`` turns by
+    the negated angle: the gradient of the call."""
+    return Rope(plan, q, k, positions, v, inverse).run()
+
+
+# ------------------------------------------------------------------ drafted tokens
+class AttendTree:
+    """A prepared kv_attend_tree call (see Attend): q (batch, q_heads, T, D),
+    k_tree, v_tree (batch, kv_heads, T, D) of the drafted tokens, parents
+    (batch, T): the drafted token a token follows, -1 for the cache's last
+    token, -2 for no token (its output row stays as it was)."""
+
+    def __init__(self, cache: PackedCache, q: torch.Tensor, k_tree: torch.Tensor,
+                 v_tree: torch.Tensor, parents: torch.Tensor, sm_scale: float = 0.0,
+                 out_dtype=None, out=None):
+        self.lib = load_library()
+        self.cache = cache
+        self._copies = []
+        self.q, self.k, self.v = (_static(self._copies, x) for x in (q, k_tree, v_tree))
+        if self.q.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("q must be float32 or bfloat16")
+        if self.k.dtype not in (torch.float32, torch.bfloat16) or self.v.dtype != self.k.dtype:
+            raise TypeError("k_tree and v_tree must both be float32 or bfloat16")
+        b, hq, t, d = self.q.shape
+        if b != cache.batch or d != cache.head_dim:
+            raise ValueError("q does not match the cache")
+        if tuple(self.k.shape) != (b, cache.kv_heads, t, d) or self.v.shape != self.k.shape:
+            raise ValueError("k_tree and v_tree must be (batch, kv_heads, T, D)")
+        if tuple(parents.shape) != (b, t):
+            raise ValueError("parents must be (batch, T)")
+        self.parents = _static(self._copies, parents, torch.int32)
+        self.q_dt = F32 if self.q.dtype == torch.float32 else BF16
+        self.t_dt = F32 if self.k.dtype == torch.float32 else BF16
+        self.out_dt = (_dtype(out_dtype) if out_dtype is not None else
+                       self.q_dt if out is None else
+                       F32 if out.dtype == torch.float32 else BF16)
+        # rows without a token are never written: zeros unless the caller gives the buffer
+        self.out = out if out is not None else torch.zeros(
+            (b, hq, t, d), dtype=TORCH_OF[self.out_dt], device=self.q.device)
+        if (self.out.shape != self.q.shape or self.out.dtype != TORCH_OF[self.out_dt] or
+                not self.out.is_contiguous()):
+            raise ValueError("out must be a dense tensor of q's shape")
+        self.hq, self.t, self.sm_scale = hq, t, float(sm_scale or 0.0)
+        self.status = new_status(self.q.device)
+        self.ws = None
+        self._reserve()
+        self.path = None
+
+    def _reserve(self):
+        """Workspace for the cache's present length (it grows with appends)."""
+        need = ctypes.c_size_t(0)
+        self._call(None, need)
+        self._n = self.cache.n_tokens
+        if self.ws is None or int(need.value) > self.ws.numel():
+            self.ws = torch.empty(max(int(need.value), 256), dtype=torch.uint8,
+                                  device=self.q.device)
+            self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+
+    def _call(self, ws, ws_bytes):
+        st = self.lib.kv_attend_tree(self.cache.ref, _ptr(self.q), self.q_dt, self.hq, self.t,
+                                     _ptr(self.k), _ptr(self.v), self.t_dt, _ptr(self.parents),
+                                     self.sm_scale, _ptr(self.out), self.out_dt, ws,
+                                     ctypes.byref(ws_bytes), _ptr(self.status), _stream())
+        _check(st, "kv_attend_tree")
+
+    def run(self) -> torch.Tensor:
+        if self.cache.n_tokens != self._n:
+            self._reserve()
+        _refresh(self._copies)
+        self._call(_ptr(self.ws), self.ws_bytes)
+        self.path = self.lib.kvq_last_path().decode()
+        return self.out
+
+    def launches(self) -> int:
+        return int(self.lib.kvq_last_launch_count())
+
+
+def attend_tree(cache: PackedCache, q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor,
+                parents: torch.Tensor, sm_scale: float = 0.0, out_dtype=None):
+    """kv_attend_tree; returns (out, status tensor)."""
+    a = AttendTree(cache, q, k_tree, v_tree, parents, sm_scale, out_dtype)
+    a.run()
+    return a.out, a.status
+
+
+# ------------------------------------------------------------------ block-sparse attention
+class BlockSummary:
+    """int8 mean keys of the blocks of ``block`` tokens of a cache's int4 part
+    (kv_block_summary), with room for the blocks the cache can grow to."""
+
+    def __init__(self, cache: PackedCache, block: int = 64):
+        if block not in (32, 64, 128):
+            raise ValueError("block must be 32, 64 or 128")
+        self.lib = load_library()
+        self.cache, self.block = cache, block
+        groups = cache.reserve[0] or cache.gk
+        self.cap_blocks = -(-groups * 32 // block)
+        dev = cache.k_codes.device
+        b, h, d = cache.batch, cache.kv_heads, cache.head_dim
+        self.codes = torch.empty((b, h, self.cap_blocks, d), dtype=torch.int8, device=dev)
+        self.scales = torch.empty((b, h, self.cap_blocks), dtype=torch.float32, device=dev)
+        self.struct = KvqSummary(_ptr(self.codes), _ptr(self.scales), block, self.cap_blocks)
+        self.ref = ctypes.byref(self.struct)
+
+    @property
+    def blocks(self) -> int:
+        return -(-(self.cache.n_tokens - self.cache.recent) // self.block)
+
+    def update(self, first: int = 0) -> "BlockSummary":
+        """Recompute the blocks from ``first`` on (all of them by default)."""
+        _check(self.lib.kv_block_summary(self.cache.ref, self.ref, int(first), None, _stream()),
+               "kv_block_summary")
+        return self
+
+    def values(self, first: int = 0) -> torch.Tensor:
+        """The mean keys the codes stand for, fp32 (batch, kv_heads, blocks - first, D)."""
+        n = self.blocks
+        return self.codes[:, :, first:n] * self.scales[:, :, first:n].unsqueeze(-1)
+
+
+class AttendBlocks:
+    """A prepared pair of calls, kv_select_blocks and kv_attend_blocks: each
+    query token of a KV head attends the ``top_k`` blocks its summary scores
+    highest and the whole window. ``selected`` (batch, kv_heads, n_q, top_k)
+    holds the chosen blocks after ``run()``; ``select=False`` attends the lists
+    already there (``selected`` may be passed)."""
+
+    def __init__(self, cache: PackedCache, q: torch.Tensor, summary: BlockSummary | None,
+                 top_k: int, n_sink: int = 0, sm_scale: float = 0.0, out_dtype=None, out=None,
+                 selected: torch.Tensor | None = None, block: int | None = None):
+        self.lib = load_library()
+        self.cache, self.summary = cache, summary
+        self._copies = []
+        self.q = _static(self._copies, q)
+        if self.q.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("q must be float32 or bfloat16")
+        b, hq, nq, d = self.q.shape
+        if b != cache.batch or d != cache.head_dim:
+            raise ValueError("q does not match the cache")
+        if summary is not None and summary.cache is not cache:
+            raise ValueError("the summary is another cache's")
+        if summary is None and (selected is None or block is None):
+            raise ValueError("without a summary, selected and block are needed")
+        self.block = summary.block if summary is not None else int(block)
+        self.top_k, self.n_sink = int(top_k), int(n_sink)
+        shape = (b, cache.kv_heads, nq, self.top_k)
+        if selected is None:
+            selected = torch.full(shape, -1, dtype=torch.int32, device=self.q.device)
+        if (tuple(selected.shape) != shape or selected.dtype != torch.int32 or
+                not selected.is_contiguous()):
+            raise ValueError("selected must be int32 (batch, kv_heads, n_q, top_k), dense")
+        self.selected = selected
+        self.q_dt = F32 if self.q.dtype == torch.float32 else BF16
+        self.out_dt = _dtype(out_dtype) if out_dtype is not None else self.q_dt
+        self.out = out if out is not None else torch.empty(
+            (b, hq, nq, d), dtype=TORCH_OF[self.out_dt], device=self.q.device)
+        if (self.out.shape != self.q.shape or self.out.dtype != TORCH_OF[self.out_dt] or
+                not self.out.is_contiguous()):
+            raise ValueError("out must be a dense tensor of q's shape")
+        self.hq, self.nq, self.sm_scale = hq, nq, float(sm_scale or 0.0)
+        self.status = new_status(self.q.device)
+        self.ws = None
+        self._reserve()
+        self.path = None
+
+    def _reserve(self):
+        """Workspace for the cache's present length (it grows with appends)."""
+        need = ctypes.c_size_t(0)
+        self._attend(None, need)
+        most = int(need.value)
+        if self.summary is not None:
+            self._select(None, need)
+            most = max(most, int(need.value))
+        self._n = self.cache.n_tokens
+        # the calls run one after the other and may share their workspace
+        if self.ws is None or most > self.ws.numel():
+            self.ws = torch.empty(max(most, 256), dtype=torch.uint8, device=self.q.device)
+            self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+
+    def _select(self, ws, ws_bytes):
+        st = self.lib.kv_select_blocks(self.cache.ref, self.summary.ref, _ptr(self.q), self.q_dt,
+                                       self.hq, self.nq, self.top_k, self.n_sink,
+                                       _ptr(self.selected), ws, ctypes.byref(ws_bytes),
+                                       _ptr(self.status), _stream())
+        _check(st, "kv_select_blocks")
+
+    def _attend(self, ws, ws_bytes):
+        st = self.lib.kv_attend_blocks(self.cache.ref, _ptr(self.q), self.q_dt, self.hq, self.nq,
+                                       _ptr(self.selected), self.top_k, self.block, self.sm_scale,
+                                       _ptr(self.out), self.out_dt, ws, ctypes.byref(ws_bytes),
+                                       _ptr(self.status), _stream())
+        _check(st, "kv_attend_blocks")
+
+    def run(self, select: bool = True) -> torch.Tensor:
+        if self.cache.n_tokens != self._n:
+            self._reserve()
+        _refresh(self._copies)
+        if select and self.summary is not None:
+            self._select(_ptr(self.ws), self.ws_bytes)
+        self._attend(_ptr(self.ws), self.ws_bytes)
+        self.path = self.lib.kvq_last_path().decode()
+        return self.out
+
+
+def attend_blocks(cache: PackedCache, q: torch.Tensor, summary: BlockSummary, top_k: int,
+                  n_sink: int = 0, sm_scale: float = 0.0, out_dtype=None):
+    """kv_select_blocks and kv_attend_blocks; returns (out, selected, status tensor)."""
+    a = AttendBlocks(cache, q, summary, top_k, n_sink, sm_scale, out_dtype)
+    a.run()
+    return a.out, a.selected, a.status
