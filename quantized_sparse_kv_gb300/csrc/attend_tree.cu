@@ -15,12 +15,13 @@
 // per row block it touches (or the output itself when its slice covers the whole
 // row block), tree_combine_kernel merges them.
 //
-// Inside a CTA (17 warps):
+// Inside a CTA (20 warps, 18 of them busy):
 //   warps 0-3, 4-7   softmax groups A and B, a thread per query row;
 //   warps 8-15       dequantization: packed tile -> registers (one tile ahead)
 //                    -> fp16 K and V tiles in shared memory, 128B-swizzled, two
 //                    stages each;
-//   warp 16          TMEM allocation; one lane issues the MMAs.
+//   warps 16, 17     the MMAs of group A and of group B (16 also allocates TMEM).
+// Registers move from the other roles to the softmax groups (setmaxnreg).
 // With more than 128 rows in the row block group A takes rows 0-127 and group B
 // rows 128-255 of every tile (each dequantized tile feeds both); with fewer, both
 // work on the same rows and take alternate tiles, so that one exponentiates
@@ -28,11 +29,11 @@
 // the end of the slice. Per tile and group: S = Q K^T (MMA, both operands in
 // shared memory), softmax in registers, P written as fp16 over S in TMEM, O += P V
 // (MMA, A operand from TMEM). S of the next tile is issued once that MMA has
-// completed. The issuing lane polls both groups and issues whatever is ready.
+// completed.
 //
 // Precision: fp16 operands (11 bits; K and V are code * scale), fp32 sums and
-// softmax state. P is taken against the reference, raised when a tile's
-// maximum passes it by more than 2^8, so P stays below 2^8 in fp16.
+// softmax state. P is taken against the reference, raised when 64 keys' P sum
+// to more than 2^12, so P stays below 2^12 in fp16.
 //
 // Feature order: a nibble word gives features (0,4)(1,5)(2,6)(3,7) of eight in
 // pairs without shuffling, so Q, K and V tiles hold every eight features in the
@@ -53,12 +54,17 @@ constexpr int kBM = 128;           // rows of an MMA tile
 constexpr int kBN = 128;           // keys of a tile
 constexpr int kRowBlock = 2 * kBM;
 constexpr int kSoftWarps = 8, kDqWarps = 8;
-constexpr int kThreads = (kSoftWarps + kDqWarps + 1) * 32;
+constexpr int kThreads = (kSoftWarps + kDqWarps + 4) * 32;  // whole warpgroups (setmaxnreg)
+// Registers a thread of each role: the launch gives 96 to all 640 (65,536 / 640,
+// rounded down to a multiple of 8); the softmax groups take what the others
+// leave: 2 * 120 + 2 * 88 + 64 <= 5 * 96.
+constexpr int kLaunchRegs = 96, kSoftRegs = 120, kDqRegs = 88, kMmaRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kDqRegs + kMmaRegs <= 5 * kLaunchRegs, "register split");
 constexpr uint32_t kHalf = 128u * 128u;      // 16 KB: 128 rows x 64 fp16 features
 constexpr uint32_t kTileBytes = 2u * kHalf;
 constexpr int kStages = 2;                   // K and V tiles in shared memory, each
 constexpr int kMaskWords = KVQ_TREE_MAX / 32;
-constexpr float kLazy = 8.0f;                // log2 units the maximum may pass the reference
+constexpr float kSumBound = 4096.0f;         // sum of 64 P above which the reference is raised
 constexpr int kPartStride = kD + 4;          // floats of a partial row: O[128], m, l, padding
 
 struct __align__(1024) TreeSmem {
@@ -71,7 +77,7 @@ struct __align__(1024) TreeSmem {
   uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
   float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full, s_full[2], p_full[2], o_done[2], mma_done;
+  uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][half]
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -121,20 +127,63 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// 16 words to 16 consecutive TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// True in one lane of a fully active warp, always the same one. MMAs are issued
+// under it from code the whole warp runs, with operands the compiler can see to
+// be warp-uniform: a batch of eight (N = 128) then issues in the 512 cycles
+// it executes in, against 1,026 under `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// A bounded wait by testing the barrier in a loop: the two MMA warps do nothing
+// else, and waking from a suspended wait takes longer.
+__device__ __forceinline__ bool spin_wait(int *abort_flag, uint32_t bar, uint32_t parity,
+                                          const KernelCtl &ctl) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_test(bar, parity)); ++i) {
+    if ((i & 1023u) != 0) continue;
+    const uint64_t now = global_ns();
+    if (i == 1024u) t0 = now;
+    if (__any_sync(0xffffffffu, cta_aborted(abort_flag) || now - t0 > ctl.wait_limit_ns)) {
+      flag_error(ctl, KVQ_DEV_TIMEOUT);
+      *reinterpret_cast<volatile int *>(abort_flag) = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// The value of lane 0, which the compiler then knows to be warp-uniform.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// A shared-memory descriptor (smem_desc) from its low word, which holds the
+// address / 16 and the leading offset, and its constant high word.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1,024, version 1, 128B swizzle
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// 32 words to 32 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
       : "memory");
 }
 
-// Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, M = N =
-// 128, A K-major, B K-major (0) or MN-major (1).
-__host__ __device__ constexpr uint32_t idesc_f16(uint32_t b_mn_major) {
-  return (1u << 4) | (b_mn_major << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, M = 128,
+// N = n, A K-major, B K-major (0) or MN-major (1).
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t b_mn_major, uint32_t n) {
+  return (1u << 4) | (b_mn_major << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // Two floats to fp16, finite values beyond its range clamped to it (infinities
@@ -176,7 +225,7 @@ struct DqMap {
 
 struct KRaw {
   uint4 c[2];
-  float4 s[8];
+  float4 s;  // scales 4 (lane & 7) .. + 3 of the feature block; the eight lanes share theirs
 };
 struct VRaw {
   uint4 c[2];
@@ -188,16 +237,14 @@ __device__ __forceinline__ void load_k(const TreeArgs &a, long u, int tile, cons
   const bool have = g < a.Gk;
   const long gi = u * a.Gs + g;
   const uint8_t *p = a.k_codes + (gi * 32 + d.r) * 64 + 16 * d.cb;
-  const float *s = a.k_scales + gi * 128 + 32 * d.cb;
+  const float *s = a.k_scales + gi * 128 + 32 * d.cb + 4 * (d.r & 7);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     x.c[i] = have && in_bounds(a.ctl, p + 1024 * i, 16)
                  ? *reinterpret_cast<const uint4 *>(p + 1024 * i)
                  : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-  const bool ok = have && in_bounds(a.ctl, s, 128);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x.s[i] = ok ? reinterpret_cast<const float4 *>(s)[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  x.s = have && in_bounds(a.ctl, s, 16) ? *reinterpret_cast<const float4 *>(s)
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
 __device__ __forceinline__ void load_v(const TreeArgs &a, long u, int tile, const DqMap &d, VRaw &x) {
@@ -223,11 +270,17 @@ __device__ __forceinline__ uint4 dq8(uint32_t w, __half2 s04, __half2 s15, __hal
 }
 
 __device__ __forceinline__ void store_k(const KRaw &x, const DqMap &d, uint8_t *tile) {
+  const uint32_t h01 = pack_h2(x.s.x, x.s.y), h23 = pack_h2(x.s.z, x.s.w);
+  const int lane0 = 8 * d.cb;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 s0 = x.s[2 * j], s1 = x.s[2 * j + 1];
-    const __half2 a = __floats2half2_rn(s0.x, s1.x), b = __floats2half2_rn(s0.y, s1.y);
-    const __half2 c = __floats2half2_rn(s0.z, s1.z), e = __floats2half2_rn(s0.w, s1.w);
+    // word j's scales: 0-3 from lane 2j of the eight, 4-7 from lane 2j + 1
+    const uint32_t p01 = __shfl_sync(0xffffffffu, h01, lane0 + 2 * j);
+    const uint32_t p23 = __shfl_sync(0xffffffffu, h23, lane0 + 2 * j);
+    const uint32_t p45 = __shfl_sync(0xffffffffu, h01, lane0 + 2 * j + 1);
+    const uint32_t p67 = __shfl_sync(0xffffffffu, h23, lane0 + 2 * j + 1);
+    const __half2 a = as_h2(prmt(p01, p45, 0x5410u)), b = as_h2(prmt(p01, p45, 0x7632u));
+    const __half2 c = as_h2(prmt(p23, p67, 0x5410u)), e = as_h2(prmt(p23, p67, 0x7632u));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w = j == 0 ? x.c[i].x : j == 1 ? x.c[i].y : j == 2 ? x.c[i].z : x.c[i].w;
@@ -308,19 +361,24 @@ __device__ __forceinline__ bool warp_wait(int *abort_flag, uint32_t bar, uint32_
   return __all_sync(0xffffffffu, wait_or_abort(abort_flag, bar, parity, ctl));
 }
 
-// Sum of v[e] over the drafted tokens j of this row whose V has non-finite
-// elements: what their zeroed elements would have added (feature d0 + e).
-__device__ __noinline__ void add_odd_values(const TreeArgs &a, const TreeSmem &sm, long u, int tok,
-                                            int k_lo, int k_hi, int d0, float (&v)[32]) {
-  for (int j = max(0, k_lo - a.R); j < min(a.T, k_hi - a.R); ++j) {
-    if (!((sm.odd_v[j >> 5] & sm.seen[tok][j >> 5]) >> (j & 31) & 1u)) continue;
-    const uint16_t *p = a.v_tree + (u * a.T + j) * kD + d0;
-    if (!in_bounds(a.ctl, p, 64)) continue;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float x = bf16_to_f32(p[e]);
-      if (!(fabsf(x) <= 3.40282347e38f)) v[e] += x;
+// Features d0 .. d0 + 31 of a row just written to dst whose seen drafted tokens
+// hold infinities or NaN in V there (zeroed in the tiles): the sum of those is
+// the result. k_lo, k_hi: the tail keys the row's sum covers.
+__device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &sm, long u, int tok,
+                                            int k_lo, int k_hi, int d0, void *dst, bool bf16) {
+  for (int e = d0; e < d0 + 32; ++e) {
+    float s = 0.0f;
+    for (int j = max(0, k_lo - a.R); j < min(a.T, k_hi - a.R); ++j) {
+      if (!((sm.odd_v[j >> 5] & sm.seen[tok][j >> 5]) >> (j & 31) & 1u)) continue;
+      const uint16_t *p = a.v_tree + (u * a.T + j) * kD + e;
+      const float x = in_bounds(a.ctl, p, 2) ? bf16_to_f32(*p) : 0.0f;
+      if (!(fabsf(x) <= 3.40282347e38f)) s += x;
     }
+    if (s == 0.0f) continue;
+    if (bf16)
+      static_cast<__nv_bfloat16 *>(dst)[e] = __float2bfloat16_rn(s);
+    else
+      static_cast<float *>(dst)[e] = s;
   }
 }
 
@@ -329,23 +387,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   const uint32_t base = smem_u32(smem_raw);
   TreeSmem &sm = *reinterpret_cast<TreeSmem *>(smem_raw + (((base + 1023u) & ~1023u) - base));
   int *const abort_flag = &sm.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const long lo = slice_lo(a, blockIdx.x), hi = slice_lo(a, blockIdx.x + 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm.k_full[s]), kDqWarps);
       mbar_init(smem_u32(&sm.v_full[s]), kDqWarps);
-      mbar_init(smem_u32(&sm.k_empty[s]), 1);
-      mbar_init(smem_u32(&sm.v_empty[s]), 1);
+      mbar_init(smem_u32(&sm.k_empty[s]), 4);
+      mbar_init(smem_u32(&sm.v_empty[s]), 4);
     }
     mbar_init(smem_u32(&sm.q_full), 2 * kBM);
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(smem_u32(&sm.s_full[g]), 1);
-      mbar_init(smem_u32(&sm.p_full[g]), kBM);
-      mbar_init(smem_u32(&sm.o_done[g]), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&sm.p_full[i >> 1][i & 1]), kBM / 32);
+      mbar_init(smem_u32(&sm.o_done[i >> 1][i & 1]), 1);
     }
-    mbar_init(smem_u32(&sm.mma_done), 1);
+    mbar_init(smem_u32(&sm.mma_done), 4);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -366,162 +424,165 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kDqWarps) {
     // ------------------------------------------------ dequantization
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
     const int w = warp - kSoftWarps;
     DqMap d;
     d.grp = w >> 1;
     d.r = 8 * (w & 1) + (lane & 7);
     d.cb = lane >> 3;
-    KRaw kx;
-    VRaw vx;
-    long x = lo;
-    long rb = x / a.tiles;
-    int tile = static_cast<int>(x - rb * a.tiles);
-    long u = rb / a.row_blocks;
-    int rbu = static_cast<int>(rb - u * a.row_blocks);
-    if (x < hi && tile < a.int4_tiles) {
-      load_k(a, u, tile, d, kx);
-      load_v(a, u, tile, d, vx);
-    }
-    for (int j = 0; x < hi; ++x, ++j) {
-      const int st = j % kStages;
-      const uint32_t par = static_cast<uint32_t>((j / kStages - 1) & 1);
-      // where the next item is
-      long nu = u;
-      int nt = tile + 1, nrb = rbu;
-      if (nt == a.tiles) {
-        nt = 0;
-        if (++nrb == a.row_blocks) {
-          nrb = 0;
-          ++nu;
+    // Items in order, each with its codes and scales loaded two items earlier
+    // (two register sets in turn: one tile's conversion is shorter than the
+    // loads' latency).
+    struct Pos {
+      long u;
+      int rb, tile;
+    };
+    auto next = [&](Pos &p) {
+      if (++p.tile == a.tiles) {
+        p.tile = 0;
+        if (++p.rb == a.row_blocks) {
+          p.rb = 0;
+          ++p.u;
         }
       }
-      const bool next4 = x + 1 < hi && nt < a.int4_tiles;
-      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.k_empty[st]), par, a.ctl)) break;
-      if (__any_sync(0xffffffffu, cta_aborted(abort_flag))) break;
-      if (tile < a.int4_tiles)
+    };
+    KRaw k0, k1;
+    VRaw v0, v1;
+    Pos cur, ahead;
+    cur.tile = static_cast<int>(lo % a.tiles);
+    cur.rb = static_cast<int>(lo / a.tiles % a.row_blocks);
+    cur.u = lo / a.tiles / a.row_blocks;
+    ahead = cur;
+    int left = static_cast<int>(hi - lo);  // items from `ahead` on
+    auto load = [&](KRaw *k, VRaw *v) {
+      if (left > 0 && ahead.tile < a.int4_tiles) {
+        if (k) load_k(a, ahead.u, ahead.tile, d, *k);
+        if (v) load_v(a, ahead.u, ahead.tile, d, *v);
+      }
+      if (v) {
+        next(ahead);
+        --left;
+      }
+    };
+    load(&k0, &v0);
+    load(&k1, &v1);
+    const int n_items = static_cast<int>(hi - lo);
+    auto item = [&](int j, KRaw &kx, VRaw &vx) -> bool {
+      const int st = j % kStages;
+      const uint32_t par = static_cast<uint32_t>((j / kStages - 1) & 1);
+      const bool int4 = cur.tile < a.int4_tiles;
+      const int tail0 = kBN * (cur.tile - a.int4_tiles);
+      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.k_empty[st]), par, a.ctl)) return false;
+      if (__any_sync(0xffffffffu, cta_aborted(abort_flag))) return false;
+      if (int4)
         store_k(kx, d, sm.k[st]);
       else
-        copy_tail(a, u, kBN * (tile - a.int4_tiles), d, a.k_window, a.k_tree, false, sm.k[st]);
+        copy_tail(a, cur.u, tail0, d, a.k_window, a.k_tree, false, sm.k[st]);
       fence_async_smem();
       __syncwarp();
       // (test hook: a dropped item's keys never arrive)
-      if (lane == 0 && x != a.ctl.drop_item) mbar_arrive(smem_u32(&sm.k_full[st]));
-      if (next4) load_k(a, nu, nt, d, kx);
-      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.v_empty[st]), par, a.ctl)) break;
-      if (tile < a.int4_tiles)
+      if (lane == 0 && lo + j != a.ctl.drop_item) mbar_arrive(smem_u32(&sm.k_full[st]));
+      load(&kx, nullptr);
+      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.v_empty[st]), par, a.ctl)) return false;
+      if (int4)
         store_v(vx, d, sm.v[st]);
       else
-        copy_tail(a, u, kBN * (tile - a.int4_tiles), d, a.v_window, a.v_tree, true, sm.v[st]);
+        copy_tail(a, cur.u, tail0, d, a.v_window, a.v_tree, true, sm.v[st]);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[st]));
-      if (next4) load_v(a, nu, nt, d, vx);
-      u = nu;
-      tile = nt;
-      rbu = nrb;
+      load(nullptr, &vx);
+      next(cur);
+      return true;
+    };
+    for (int j = 0; j < n_items; j += 2) {
+      if (!item(j, k0, v0)) break;
+      if (j + 1 < n_items && !item(j + 1, k1, v1)) break;
     }
-  } else if (warp == kSoftWarps + kDqWarps) {
+  } else if (warp >= kSoftWarps + kDqWarps) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16(0), id_pv = idesc_f16(1);
-      int base_j = 0;            // tiles of the CTA before this segment
-      int seg = 0;
-      int done[2] = {0, 0};      // PV MMAs issued by each group so far
-      bool ok = true;
-      for (long x = lo; ok && x < hi; ++seg) {
-        const long rb = x / a.tiles;
-        const int t_lo = static_cast<int>(x - rb * a.tiles);
-        const int n = static_cast<int>(min(static_cast<long>(a.tiles - t_lo), hi - x));
-        const int rows = min(kRowBlock, a.rows - kRowBlock * static_cast<int>(rb % a.row_blocks));
-        const bool two = rows > kBM;
-        if (!wait_or_abort(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
-        // Group g's next tile and whether its S is out; group g takes tiles
-        // 0, 1, 2, ... of the segment (two) or g, g + 2, ... (shared rows).
-        int at[2] = {0, two ? 0 : 1};
-        bool s_out[2] = {false, false}, first[2] = {true, true};
-        int s_left[kStages] = {0, 0}, v_left[kStages] = {0, 0};
-        const int stride = two ? 1 : 2;
-        uint64_t t0 = 0;
-        int idle = 0;
-        while (at[0] < n || at[1] < n) {
-          bool moved = false;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int j = at[g];
-            if (j >= n) continue;
-            const int jj = base_j + j, st = jj % kStages;
-            const uint32_t par = static_cast<uint32_t>((jj / kStages) & 1);
-            if (!s_out[g]) {
-              // S of tile j: K is there and the group's last PV has read P
-              if (!mbar_test(smem_u32(&sm.k_full[st]), par)) continue;
-              if (!first[g] &&
-                  !mbar_test(smem_u32(&sm.o_done[g]), static_cast<uint32_t>((done[g] - 1) & 1)))
-                continue;
-              tc_fence_after();
-              const uint32_t qa = smem_u32(sm.q[two ? g : 0]), ka = smem_u32(sm.k[st]);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32u;
-                tc_mma_f16(t_s(g), smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024),
-                           id_qk, kk > 0 ? 1u : 0u);
-              }
-              tc_commit(smem_u32(&sm.s_full[g]));
-              if (!two || ++s_left[st] == 2) {
-                tc_commit(smem_u32(&sm.k_empty[st]));
-                s_left[st] = 0;
-              }
-              s_out[g] = true;
-              moved = true;
-            } else {
-              // O += P V of tile j
-              if (!mbar_test(smem_u32(&sm.p_full[g]), static_cast<uint32_t>(done[g] & 1)))
-                continue;
-              if (!mbar_test(smem_u32(&sm.v_full[st]), par)) continue;
-              tc_fence_after();
-              const uint32_t va = smem_u32(sm.v[st]);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16_ta(t_o(g), t_s(g) + 8u * kk, smem_desc(va + kk * 2048u, kHalf, 1024),
-                              id_pv, (!first[g] || kk > 0) ? 1u : 0u);
-              tc_commit(smem_u32(&sm.o_done[g]));
-              if (!two || ++v_left[st] == 2) {
-                tc_commit(smem_u32(&sm.v_empty[st]));
-                v_left[st] = 0;
-              }
-              ++done[g];
-              first[g] = false;
-              s_out[g] = false;
-              at[g] = j + stride;
-              moved = true;
-            }
-          }
-          if (moved) {
-            idle = 0;
-          } else if ((++idle & 1023) == 0) {
-            const uint64_t now = global_ns();
-            if (idle == 1024) t0 = now;
-            if (cta_aborted(abort_flag) || now - t0 > a.ctl.wait_limit_ns) {
-              flag_error(a.ctl, KVQ_DEV_TIMEOUT);
-              *reinterpret_cast<volatile int *>(abort_flag) = 1;
-              ok = false;
-              break;
-            }
-          }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    // Warp 16 + 2g + h: half h (64 keys) of group g's tiles.
+    constexpr uint32_t id_qk = idesc_f16(0, 64), id_pv = idesc_f16(1, 128);
+    const uint32_t g = uniform((warp - (kSoftWarps + kDqWarps)) >> 1), h = uniform(warp & 1);
+    const uint32_t to = uniform(tmem) + 256u * g + 128u, ts = uniform(tmem) + 256u * g + 64u * h;
+    const uint32_t q_lo = uniform((smem_u32(sm.q[0]) >> 4) | (1u << 16));   // leading offset 16
+    const uint32_t k_lo = uniform(((smem_u32(sm.k[0]) + 8192u * h) >> 4) | (1u << 16));
+    const uint32_t v_lo = uniform(((smem_u32(sm.v[0]) + 8192u * h) >> 4) | (kHalf >> 4) << 16);
+    const uint32_t s_bar = smem_u32(&sm.s_full[g][h]), p_bar = smem_u32(&sm.p_full[g][h]);
+    const uint32_t o_bar = smem_u32(&sm.o_done[g][h]);
+    uint32_t base_j = 0;  // tiles of the CTA before this segment
+    uint32_t seg = 0;
+    uint32_t done = 0;    // PV MMAs issued so far
+    bool ok = true;
+    for (long x = lo; ok && x < hi; ++seg) {
+      const long rb = x / a.tiles;
+      const int t_lo = static_cast<int>(x - rb * a.tiles);
+      const int n = static_cast<int>(min(static_cast<long>(a.tiles - t_lo), hi - x));
+      const bool two =
+          uniform(a.rows - kRowBlock * static_cast<int>(rb % a.row_blocks) > kBM ? 1u : 0u) != 0u;
+      const uint32_t qd = q_lo + (two ? g : 0u) * (kTileBytes >> 4);
+      if (!spin_wait(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
+      // group g takes tiles 0, 1, 2, ... of the segment (two) or g, g + 2, ...
+      // (shared rows; a stage's four arrivals then come from one group)
+      bool first = true;
+      for (int at = two ? 0 : static_cast<int>(g); at < n; at += two ? 1 : 2) {
+        const uint32_t jj = base_j + at, st = uniform(jj % kStages), par = (jj / kStages) & 1;
+        // S: K is there and this half's last PV has read P
+        if (!spin_wait(abort_flag, smem_u32(&sm.k_full[st]), par, a.ctl) ||
+            (!first && !spin_wait(abort_flag, o_bar, (done - 1) & 1, a.ctl))) {
+          ok = false;
+          break;
         }
-        base_j += n;
-        x += n;
+        tc_fence_after();
+        const uint32_t kd = k_lo + st * (kTileBytes >> 4);
+        const uint32_t k_bar = smem_u32(&sm.k_empty[st]), v_bar = smem_u32(&sm.v_empty[st]);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {  // (descriptor addresses count 16 bytes)
+            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4;
+            tc_mma_f16(ts, desc_of(qd + off), desc_of(kd + off), id_qk, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(s_bar);
+          tc_commit(k_bar);
+          if (!two) tc_commit(k_bar);
+        }
+        __syncwarp();
+        // O += P V
+        if (!spin_wait(abort_flag, smem_u32(&sm.v_full[st]), par, a.ctl) ||
+            !spin_wait(abort_flag, p_bar, done & 1, a.ctl)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t vd = v_lo + st * (kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_ta(to, ts + 8u * kk, desc_of(vd + (kk * 2048u >> 4)), id_pv, 1u);
+          tc_commit(o_bar);
+          tc_commit(v_bar);
+          if (!two) tc_commit(v_bar);
+        }
+        __syncwarp();
+        ++done;
+        first = false;
       }
-      // all MMAs of this CTA complete before TMEM is released
-      tc_commit(smem_u32(&sm.mma_done));
-      mbar_wait(smem_u32(&sm.mma_done), 0, 2000000000ull);
+      base_j += n;
+      x += n;
     }
+    // all MMAs of this CTA complete before TMEM is released
+    if (elect_one()) tc_commit(smem_u32(&sm.mma_done));
+    __syncwarp();
+    mbar_wait(smem_u32(&sm.mma_done), 0, 2000000000ull);
   } else {
     // ------------------------------------------------ softmax groups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int g = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_row = t_s(g) + lane_off, o_row = t_o(g) + lane_off;
-    int s_seen = 0, pv_seen = 0;  // S tiles and PV MMAs of this group so far
+    int pv_seen = 0;  // tiles of this group so far
     bool ok = true;
     for (long x = lo; x < hi;) {
       const long rb = x / a.tiles;
@@ -591,123 +652,129 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           *reinterpret_cast<uint4 *>(q + chunk_at(row, c)) =
               qok ? bf8_to_h8(reinterpret_cast<const uint4 *>(p)[c]) : make_uint4(0u, 0u, 0u, 0u);
       }
+      // O starts at zero: the halves' first PVs may come in either order
+      {
+        float z[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) z[e] = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) tmem_st32(o_row + 32u * c, z);
+        tmem_wait_st();
+      }
       fence_async_smem();
+      tc_fence_before();
       mbar_arrive(smem_u32(&sm.q_full));
 
       float m = -CUDART_INF_F, l = 0.0f;
       int mine_tiles = 0;
       for (int j = two ? 0 : g; j < n; j += two ? 1 : 2, ++mine_tiles) {
-        if (!warp_wait(abort_flag, smem_u32(&sm.s_full[g]), s_seen & 1, a.ctl)) {
-          ok = false;
-          break;
-        }
-        ++s_seen;
-        tc_fence_after();
         const int tile = t_lo + j;
-        // keys of the tile this row sees: all, the first `valid`, or by bits
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        bool all = true;
-        if (tile < a.int4_tiles) {
-          const int valid = a.cut - kBN * tile;
-          if (valid < kBN) {
-            all = false;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int k = valid - 32 * c;
-              see[c] = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
-            }
+        // Keys of the tile this row sees: all of them, else by bits (word c:
+        // keys 32c .. 32c + 31): the first ones of the int4 part's last tile;
+        // in the tail the window and the row's drafted tokens.
+        const bool int4 = tile < a.int4_tiles;
+        const int k0 = kBN * (int4 ? tile : tile - a.int4_tiles);
+        const int plain = (int4 ? a.cut : a.R) - k0;  // keys from the tile's first seen by every row
+        const bool all = plain >= kBN;
+        auto see_word = [&](int c) -> uint32_t {
+          const int s = 32 * c - plain;  // word c's first key counted from the end of those
+          if (s <= -32) return ~0u;
+          uint32_t bits = s < 0 ? (1u << -s) - 1u : 0u;
+          if (!int4) {
+            // keys past the window: drafted tokens s, s + 1, ...
+            const int w = s >> 5, sh = s & 31;
+            const uint32_t w0 = w >= 0 && w < kMaskWords ? sm.seen[tok][w] : 0u;
+            const uint32_t w1 = w + 1 < kMaskWords ? sm.seen[tok][w + 1] : 0u;
+            bits |= sh == 0 ? w0 : __funnelshift_r(w0, w1, sh);
           }
-        } else {
-          const int k0 = kBN * (tile - a.int4_tiles);
-          all = k0 + kBN <= a.R;
-          if (!all) {
+          return bits;
+        };
+        // ---- P over S, 64 keys at a time (32 words over 64 scores). No maximum
+        // is taken as long as a half's sum of P stays below kSumBound, which
+        // bounds every P of it (fp16 holds 2^15); above that (and for a row's
+        // first keys) the half is redone with its maximum as the new
+        // reference, and O and l follow.
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!warp_wait(abort_flag, smem_u32(&sm.s_full[g][h]), pv_seen & 1, a.ctl)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          bool with_max = __any_sync(0xffffffffu, m == -CUDART_INF_F);
+          uint32_t p[32];
+          float s;
+          for (;;) {
+            float v[32], w[32];
+            tmem_ld32(s_row + 64u * h, v);
+            tmem_ld32(s_row + 64u * h + 32u, w);
+            tmem_wait_ld();
+            reg_fence(v);
+            reg_fence(w);
+            if (!all) {
+              const uint32_t see0 = see_word(2 * h), see1 = see_word(2 * h + 1);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              // key k0 + 32c + e is drafted token s + e
-              const int s = k0 + 32 * c - a.R;
-              uint32_t bits = s <= -32 ? ~0u : 0u;
-              if (s > -32) {
-                if (s < 0) bits = (1u << -s) - 1u;  // window keys
-                const int w = s >= 0 ? s >> 5 : -1, sh = s & 31;
-                const uint32_t w0 = w >= 0 && w < kMaskWords ? sm.seen[tok][w] : 0u;
-                const uint32_t w1 = w + 1 < kMaskWords ? sm.seen[tok][w + 1] : 0u;
-                bits |= sh == 0 ? w0 : __funnelshift_r(w0, w1, sh);
+              for (int e = 0; e < 32; ++e) {
+                v[e] = see0 >> e & 1u ? v[e] : -CUDART_INF_F;
+                w[e] = see1 >> e & 1u ? w[e] : -CUDART_INF_F;
               }
-              see[c] = bits;
             }
-          }
-        }
-        // ---- the tile's maximum
-        float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+            if (with_max) {
+              float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(s_row + 32u * c, v);
-          tmem_wait_ld();
-          reg_fence(v);
-          if (all) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              mx0 = fmaxf(mx0, v[e]);
-              mx1 = fmaxf(mx1, v[e + 1]);
+              for (int e = 0; e < 32; ++e) mx = fmaxf(fmaxf(mx, v[e]), w[e]);
+              mx *= a.scale_log2;
+              const float f = mx > m ? fast_exp2(m - mx) : 1.0f;
+              m = fmaxf(m, mx);
+              l *= f;
+              sum *= f;
+              // O holds still once the other half's last PV is done (this
+              // half's was before its S was issued)
+              if (h == 1 || pv_seen > 0)
+                ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][h ^ 1]),
+                               (h == 1 ? pv_seen : pv_seen - 1) & 1, a.ctl);
+              if (!ok) break;
+              tc_fence_after();
+              scale_tmem_row(o_row, f);
             }
-          } else {
+            const float neg_m = m == -CUDART_INF_F ? 0.0f : -m;
+            float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              mx0 = fmaxf(mx0, see[c] >> e & 1u ? v[e] : -CUDART_INF_F);
-              mx1 = fmaxf(mx1, see[c] >> (e + 1) & 1u ? v[e + 1] : -CUDART_INF_F);
+            for (int e = 0; e < 16; ++e) {
+              float y0, y1, z0, z1;
+              fma2(y0, y1, v[2 * e], v[2 * e + 1], a.scale_log2, neg_m);
+              fma2(z0, z1, w[2 * e], w[2 * e + 1], a.scale_log2, neg_m);
+              y0 = fast_exp2(y0);
+              y1 = fast_exp2(y1);
+              z0 = fast_exp2(z0);
+              z1 = fast_exp2(z1);
+              add2(s0, s1, y0, y1);
+              add2(s2, s3, z0, z1);
+              p[e] = pack_h2(y0, y1);
+              p[16 + e] = pack_h2(z0, z1);
             }
+            s = (s0 + s1) + (s2 + s3);
+            if (with_max || !__any_sync(0xffffffffu, !(s <= kSumBound))) break;
+            with_max = true;
           }
+          if (!ok) break;
+          sum += s;
+          tmem_st32u(s_row + 64u * h, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g][h]));
         }
-        const float mx = fmaxf(mx0, mx1) * a.scale_log2;
-        // The reference is raised when the maximum passes it by 2^kLazy (and
-        // set by the first tile with a key); O and l follow.
-        const bool raise = mx > m + kLazy || (m == -CUDART_INF_F && mx > -CUDART_INF_F);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? fast_exp2(m - mx) : 1.0f;
-          if (raise) {
-            m = mx;
-            l *= f;
-          }
-          if (mine_tiles > 0) scale_tmem_row(o_row, f);  // the group's last PV has completed
-        }
-        const float neg_m = m == -CUDART_INF_F ? 0.0f : -m;
-        // ---- P over S: 32 scores at columns 32c become 16 words at 16c
-        float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(s_row + 32u * c, v);
-          tmem_wait_ld();
-          reg_fence(v);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            fma2(v[e], v[e + 1], v[e], v[e + 1], a.scale_log2, neg_m);
-            v[e] = fast_exp2(v[e]);
-            v[e + 1] = fast_exp2(v[e + 1]);
-          }
-          if (!all) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = see[c] >> e & 1u ? v[e] : 0.0f;
-          }
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            add2(sum0, sum1, v[2 * e], v[2 * e + 1]);
-            p[e] = pack_h2(v[2 * e], v[2 * e + 1]);
-          }
-          tmem_st16(s_row + 16u * c, p);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sm.p_full[g]));
-        l += sum0 + sum1;
+        if (!ok) break;
+        ++pv_seen;
+        l += sum;
       }
       // (after a wait that ran out: on to the barrier below, where all stop)
-      pv_seen += mine_tiles;
-      if (ok && mine_tiles > 0 &&
-          !warp_wait(abort_flag, smem_u32(&sm.o_done[g]), (pv_seen - 1) & 1, a.ctl))
-        ok = false;
+      for (int h = 0; h < 2; ++h)
+        if (ok && mine_tiles > 0 &&
+            !warp_wait(abort_flag, smem_u32(&sm.o_done[g][h]), (pv_seen - 1) & 1, a.ctl))
+          ok = false;
       // ---- write the segment's rows: the output when the slice covers all
       // of the row block's tiles, else a partial
       if (!two) {
@@ -734,6 +801,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         const int slot = static_cast<int>(blockIdx.x) - cta_of(a, rb * a.tiles);
         part = a.partials +
                ((rb * a.slots + slot) * kRowBlock + (r - row0)) * static_cast<long>(kPartStride);
+      }
+      bool odd = false;  // a seen drafted token with a non-finite V
+      if (has_tail) {
+#pragma unroll
+        for (int w = 0; w < kMaskWords; ++w) odd |= (sm.odd_v[w] & sm.seen[tok][w]) != 0u;
       }
       // (two: all four chunks of this group's rows; shared rows: half of them each)
       for (int c = two ? 0 : 2 * g; c < (two ? 4 : 2 * g + 2); ++c) {
@@ -765,12 +837,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           const int i = e & 7, nat = (i >> 1) + 4 * (i & 1);
           y[(e & ~7) + nat] = v[e] * inv;
         }
-        if (has_tail) {
-          bool odd = false;
-#pragma unroll
-          for (int w = 0; w < kMaskWords; ++w) odd |= (sm.odd_v[w] & sm.seen[tok][w]) != 0u;
-          if (odd) add_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c, y);
-        }
         if (!whole) {
           float4 *o = reinterpret_cast<float4 *>(part + 32 * c);
           if (!in_bounds(a.ctl, part, sizeof(float) * kPartStride)) continue;
@@ -778,12 +844,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           for (int e = 0; e < 8; ++e)
             o[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           if (c == 0) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
+          if (odd) put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c, part, false);
         } else if (a.out_dtype == KVQ_F32) {
           float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + qrow * kD + 32 * c);
           if (!in_bounds(a.ctl, o, 128)) continue;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             o[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          if (odd)
+            put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c,
+                           static_cast<float *>(a.out) + qrow * kD, false);
         } else {
           uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + qrow * kD + 32 * c);
           if (!in_bounds(a.ctl, o, 64)) continue;
@@ -792,6 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
             o[e] = make_uint4(pack_bf2(y[8 * e], y[8 * e + 1]), pack_bf2(y[8 * e + 2], y[8 * e + 3]),
                               pack_bf2(y[8 * e + 4], y[8 * e + 5]),
                               pack_bf2(y[8 * e + 6], y[8 * e + 7]));
+          if (odd)
+            put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c,
+                           static_cast<uint16_t *>(a.out) + qrow * kD, true);
         }
       }
       // a row without a token leaves a partial that says so
