@@ -15,21 +15,24 @@
 // per row block it touches (or the output itself when its slice covers the whole
 // row block), tree_combine_kernel merges them.
 //
-// Inside a CTA (20 warps, 18 of them busy):
+// Inside a CTA (20 warps):
 //   warps 0-3, 4-7   softmax groups A and B, a thread per query row;
-//   warps 8-15       dequantization: packed tile -> registers (one tile ahead)
-//                    -> fp16 K and V tiles in shared memory, 128B-swizzled, two
-//                    stages each;
-//   warps 16, 17     the MMAs of group A and of group B (16 also allocates TMEM).
+//   warps 8-11, 12-15  dequantization of K and of V: packed tile -> registers
+//                    (a tile ahead) -> fp16 tile in shared memory,
+//                    128B-swizzled, two stages each;
+//   warps 16-19      the MMAs, a warp per group and half tile (16 also
+//                    allocates TMEM).
 // Registers move from the other roles to the softmax groups (setmaxnreg).
 // With more than 128 rows in the row block group A takes rows 0-127 and group B
 // rows 128-255 of every tile (each dequantized tile feeds both); with fewer, both
 // work on the same rows and take alternate tiles, so that one exponentiates
 // while the tensor core works for the other; their sums and outputs are merged at
-// the end of the slice. Per tile and group: S = Q K^T (MMA, both operands in
-// shared memory), softmax in registers, P written as fp16 over S in TMEM, O += P V
-// (MMA, A operand from TMEM). S of the next tile is issued once that MMA has
-// completed.
+// the end of the slice. Per group and half tile (64 keys): S = Q K^T (MMA, both
+// operands in shared memory), softmax in registers, P written as fp16 over S in
+// TMEM, O += P V (MMA, A operand from TMEM), and the next S once that MMA has
+// completed. Each step hands over through a barrier, and two such chains per
+// group (four in all) keep the tensor core and the softmax warps busy across
+// those hand-overs.
 //
 // Precision: fp16 operands (11 bits; K and V are code * scale), fp32 sums and
 // softmax state. P is taken against the reference, raised when 64 keys' P sum
@@ -57,8 +60,8 @@ constexpr int kSoftWarps = 8, kDqWarps = 8;
 constexpr int kThreads = (kSoftWarps + kDqWarps + 4) * 32;  // whole warpgroups (setmaxnreg)
 // Registers a thread of each role: the launch gives 96 to all 640 (65,536 / 640,
 // rounded down to a multiple of 8); the softmax groups take what the others
-// leave: 2 * 120 + 2 * 88 + 64 <= 5 * 96.
-constexpr int kLaunchRegs = 96, kSoftRegs = 120, kDqRegs = 88, kMmaRegs = 64;
+// leave: 2 * 128 + 2 * 80 + 64 <= 5 * 96.
+constexpr int kLaunchRegs = 96, kSoftRegs = 128, kDqRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kDqRegs + kMmaRegs <= 5 * kLaunchRegs, "register split");
 constexpr uint32_t kHalf = 128u * 128u;      // 16 KB: 128 rows x 64 fp16 features
 constexpr uint32_t kTileBytes = 2u * kHalf;
@@ -76,7 +79,7 @@ struct __align__(1024) TreeSmem {
   uint32_t live[kMaskWords];                 // drafted tokens that exist
   uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
   float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kStages][2], k_empty[kStages][2], v_full[kStages][2], v_empty[kStages][2];  // [half]
   uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][half]
   uint32_t tmem_base;
   int abort_flag;
@@ -215,49 +218,62 @@ __device__ __forceinline__ int cta_of(const TreeArgs &a, long x) {
 }
 
 // ------------------------------------------------------------------ dequantization
-// Thread's part of a tile: 16 B of codes (32 features, block cb) of rows r and
-// r + 16 of group grp. A quarter-warp takes eight consecutive rows of one
-// feature block, so its swizzled 16-byte stores meet all banks; a warp's code
-// loads are 512 contiguous bytes.
-struct DqMap {
-  int grp, r, cb;
+// Four warps make the K tiles and four the V tiles. Warp grp of either takes
+// the tile's rows 32 grp .. 32 grp + 31 (one K group), lane (r, cb) the 32
+// features of block cb of rows r, r + 8, r + 16, r + 24 (16 bytes of codes
+// each): a quarter-warp stores eight consecutive rows of one feature block, so
+// its swizzled 16-byte stores meet all banks, and a warp's code loads are 512
+// contiguous bytes.
+struct Raw {
+  uint4 c[4];
+  float4 s;  // K: scales 4r .. 4r + 3 of the block (eight lanes share theirs); V: one per row
 };
 
-struct KRaw {
-  uint4 c[2];
-  float4 s;  // scales 4 (lane & 7) .. + 3 of the feature block; the eight lanes share theirs
-};
-struct VRaw {
-  uint4 c[2];
-  float s[2];
+// Where a warp's next tile lies (its lane's first 16 bytes and scale).
+struct RawPtr {
+  const uint8_t *c;
+  const float *s;
 };
 
-__device__ __forceinline__ void load_k(const TreeArgs &a, long u, int tile, const DqMap &d, KRaw &x) {
-  const int g = 4 * tile + d.grp;
-  const bool have = g < a.Gk;
-  const long gi = u * a.Gs + g;
-  const uint8_t *p = a.k_codes + (gi * 32 + d.r) * 64 + 16 * d.cb;
-  const float *s = a.k_scales + gi * 128 + 32 * d.cb + 4 * (d.r & 7);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    x.c[i] = have && in_bounds(a.ctl, p + 1024 * i, 16)
-                 ? *reinterpret_cast<const uint4 *>(p + 1024 * i)
-                 : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-  x.s = have && in_bounds(a.ctl, s, 16) ? *reinterpret_cast<const float4 *>(s)
-                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+template <bool kV>
+__device__ __forceinline__ RawPtr raw_ptr(const TreeArgs &a, long u, int tile, int grp, int r,
+                                          int cb) {
+  RawPtr p;
+  if (kV) {
+    const long row = u * a.Vs + kBN * tile + 32 * grp + r;
+    p.c = a.v_codes + row * 64 + 16 * cb;
+    p.s = a.v_scales + row * 4 + cb;
+  } else {
+    const long gi = u * a.Gs + 4 * tile + grp;
+    p.c = a.k_codes + (gi * 32 + r) * 64 + 16 * cb;
+    p.s = a.k_scales + gi * 128 + 32 * cb + 4 * r;
+  }
+  return p;
 }
 
-__device__ __forceinline__ void load_v(const TreeArgs &a, long u, int tile, const DqMap &d, VRaw &x) {
+template <bool kV>
+__device__ __forceinline__ void load_raw(const TreeArgs &a, const RawPtr &p, int tile, int grp,
+                                         int r, Raw &x) {
+  const uint4 zero = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // code 0
+  if (kV) {
+    float *s = reinterpret_cast<float *>(&x.s);
+    const int left = a.cut - (kBN * tile + 32 * grp + r);  // rows from this lane's first on
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = 128 * tile + 32 * d.grp + d.r + 16 * i;
-    const long row = u * a.Vs + t;
-    const uint8_t *p = a.v_codes + row * 64 + 16 * d.cb;
-    const float *s = a.v_scales + row * 4 + d.cb;
-    const bool ok = t < a.cut && in_bounds(a.ctl, p, 16) && in_bounds(a.ctl, s, 4);
-    x.c[i] = ok ? *reinterpret_cast<const uint4 *>(p)
-                : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-    x.s[i] = ok ? *s : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const bool ok = 8 * i < left && in_bounds(a.ctl, p.c + 512 * i, 16) &&
+                      in_bounds(a.ctl, p.s + 32 * i, 4);
+      x.c[i] = ok ? *reinterpret_cast<const uint4 *>(p.c + 512 * i) : zero;
+      s[i] = ok ? p.s[32 * i] : 0.0f;
+    }
+  } else {
+    const bool have = 4 * tile + grp < a.Gk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x.c[i] = have && in_bounds(a.ctl, p.c + 512 * i, 16)
+                   ? *reinterpret_cast<const uint4 *>(p.c + 512 * i)
+                   : zero;
+    x.s = have && in_bounds(a.ctl, p.s, 16) ? *reinterpret_cast<const float4 *>(p.s)
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
 }
 
@@ -269,56 +285,52 @@ __device__ __forceinline__ uint4 dq8(uint32_t w, __half2 s04, __half2 s15, __hal
                     as_u32(__hmul2(as_h2(dq_lo(h)), s26)), as_u32(__hmul2(as_h2(dq_hi(h)), s37)));
 }
 
-__device__ __forceinline__ void store_k(const KRaw &x, const DqMap &d, uint8_t *tile) {
+// The lane's part of a tile to shared memory; `row` is the lane's first row's
+// place and sw its swizzle (the rows differ by multiples of eight).
+template <bool kV>
+__device__ __forceinline__ void store_raw(const Raw &x, int r, int cb, uint8_t *row) {
   const uint32_t h01 = pack_h2(x.s.x, x.s.y), h23 = pack_h2(x.s.z, x.s.w);
-  const int lane0 = 8 * d.cb;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    // word j's scales: 0-3 from lane 2j of the eight, 4-7 from lane 2j + 1
-    const uint32_t p01 = __shfl_sync(0xffffffffu, h01, lane0 + 2 * j);
-    const uint32_t p23 = __shfl_sync(0xffffffffu, h23, lane0 + 2 * j);
-    const uint32_t p45 = __shfl_sync(0xffffffffu, h01, lane0 + 2 * j + 1);
-    const uint32_t p67 = __shfl_sync(0xffffffffu, h23, lane0 + 2 * j + 1);
-    const __half2 a = as_h2(prmt(p01, p45, 0x5410u)), b = as_h2(prmt(p01, p45, 0x7632u));
-    const __half2 c = as_h2(prmt(p23, p67, 0x5410u)), e = as_h2(prmt(p23, p67, 0x7632u));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w = j == 0 ? x.c[i].x : j == 1 ? x.c[i].y : j == 2 ? x.c[i].z : x.c[i].w;
-      *reinterpret_cast<uint4 *>(tile + chunk_at(32 * d.grp + d.r + 16 * i, 4 * d.cb + j)) =
-          dq8(w, a, b, c, e);
+    uint8_t *dst = row + (cb >> 1) * kHalf + ((((4 * cb + j) & 7) ^ r) << 4);
+    __half2 s0, s1, s2, s3;
+    if (!kV) {
+      // word j's scales: 0-3 from lane 2j of the eight, 4-7 from lane 2j + 1
+      const int from = 8 * cb + 2 * j;
+      const uint32_t p01 = __shfl_sync(0xffffffffu, h01, from);
+      const uint32_t p23 = __shfl_sync(0xffffffffu, h23, from);
+      const uint32_t p45 = __shfl_sync(0xffffffffu, h01, from + 1);
+      const uint32_t p67 = __shfl_sync(0xffffffffu, h23, from + 1);
+      s0 = as_h2(prmt(p01, p45, 0x5410u)), s1 = as_h2(prmt(p01, p45, 0x7632u));
+      s2 = as_h2(prmt(p23, p67, 0x5410u)), s3 = as_h2(prmt(p23, p67, 0x7632u));
     }
-  }
-}
-
-__device__ __forceinline__ void store_v(const VRaw &x, const DqMap &d, uint8_t *tile) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 s = __float2half2_rn(x.s[i]);
-    const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4 *>(tile + chunk_at(32 * d.grp + d.r + 16 * i, 4 * d.cb + j)) =
-          dq8(w[j], s, s, s, s);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = j == 0 ? x.c[i].x : j == 1 ? x.c[i].y : j == 2 ? x.c[i].z : x.c[i].w;
+      if (kV) s0 = s1 = s2 = s3 = as_h2(prmt(i < 2 ? h01 : h23, 0u, i & 1 ? 0x3232u : 0x1010u));
+      *reinterpret_cast<uint4 *>(dst + 1024 * i) = dq8(w, s0, s1, s2, s3);
+    }
   }
 }
 
 // Rows of the tail (window, then drafted tokens) from key k0 on, zeros past
 // its end; non-finite V elements of drafted tokens become zero (they are added
 // for the rows that see them when the output is written).
-__device__ __forceinline__ void copy_tail(const TreeArgs &a, long u, int k0, const DqMap &d,
-                                          const uint16_t *win, const uint16_t *tree, bool is_v,
+template <bool kV>
+__device__ __noinline__ void copy_tail(const TreeArgs &a, long u, int k0, int grp, int r, int cb,
                                           uint8_t *tile) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 32 * d.grp + d.r + 16 * i, key = k0 + r;
+  const uint16_t *win = kV ? a.v_window : a.k_window, *tree = kV ? a.v_tree : a.k_tree;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int row = 32 * grp + r + 8 * i, key = k0 + row;
     const uint16_t *p = key < a.R ? win + (u * a.Ws + key) * kD
                                   : tree + (u * a.T + (key - a.R)) * kD;
     const bool ok = key < a.R + a.T && in_bounds(a.ctl, p, 2 * kD);
     uint4 w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      w[j] = ok ? reinterpret_cast<const uint4 *>(p + 32 * d.cb)[j] : make_uint4(0u, 0u, 0u, 0u);
-    if (is_v && key >= a.R) {
+      w[j] = ok ? reinterpret_cast<const uint4 *>(p + 32 * cb)[j] : make_uint4(0u, 0u, 0u, 0u);
+    if (kV && key >= a.R) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t *e = reinterpret_cast<uint32_t *>(&w[j]);
@@ -331,7 +343,7 @@ __device__ __forceinline__ void copy_tail(const TreeArgs &a, long u, int k0, con
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4 *>(tile + chunk_at(r, 4 * d.cb + j)) = bf8_to_h8(w[j]);
+      *reinterpret_cast<uint4 *>(tile + chunk_at(row, 4 * cb + j)) = bf8_to_h8(w[j]);
   }
 }
 
@@ -382,6 +394,58 @@ __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &s
   }
 }
 
+// One dequantization warp: its rows of every K (or V) tile of the CTA's items, each
+// with codes and scales loaded a tile earlier. (Loading two tiles ahead needs the
+// loop twice; the code of all roles then no longer fits the instruction caches
+// and the call takes half as long again.)
+template <bool kV>
+__device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, long lo, long hi,
+                                             int grp, int lane) {
+  const int r = lane & 7, cb = lane >> 3;
+  const int n = static_cast<int>(hi - lo);
+  // Only tiles are followed; a unit is found by division where one begins.
+  // (32-bit: a 64-bit division is a call, around which registers spill)
+  const uint32_t lo32 = static_cast<uint32_t>(lo);
+  auto unit_of = [&](int j) {
+    return static_cast<long>((lo32 + j) / static_cast<uint32_t>(a.tiles) /
+                             static_cast<uint32_t>(a.row_blocks));
+  };
+  int cur = static_cast<int>(lo32 % static_cast<uint32_t>(a.tiles)), ahead = cur, ahead_j = 0;
+  RawPtr ptr = raw_ptr<kV>(a, unit_of(0), cur, grp, r, cb);
+  auto load = [&](Raw &x) {
+    if (ahead_j < n && ahead < a.int4_tiles) load_raw<kV>(a, ptr, ahead, grp, r, x);
+    ++ahead_j;
+    ptr.c += 8192;
+    ptr.s += 512;
+    if (++ahead == a.tiles) {
+      ahead = 0;
+      ptr = raw_ptr<kV>(a, unit_of(ahead_j), 0, grp, r, cb);
+    }
+  };
+  Raw x;
+  load(x);
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int st = j % kStages;
+    uint64_t *empty = kV ? &sm.v_empty[st][grp >> 1] : &sm.k_empty[st][grp >> 1];
+    uint64_t *full = kV ? &sm.v_full[st][grp >> 1] : &sm.k_full[st][grp >> 1];
+    uint8_t *tile = kV ? sm.v[st] : sm.k[st];
+    if (j >= kStages && !warp_wait(&sm.abort_flag, smem_u32(empty),
+                                   static_cast<uint32_t>((j / kStages - 1) & 1), a.ctl))
+      break;
+    if (cur < a.int4_tiles)
+      store_raw<kV>(x, r, cb, tile + (32 * grp + r) * 128);
+    else
+      copy_tail<kV>(a, unit_of(j), kBN * (cur - a.int4_tiles), grp, r, cb, tile);
+    fence_async_smem();
+    __syncwarp();
+    // (test hook: a dropped item's keys never arrive)
+    if (lane == 0 && (kV || lo + j != a.ctl.drop_item)) mbar_arrive(smem_u32(full));
+    load(x);
+    if (++cur == a.tiles) cur = 0;
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = smem_u32(smem_raw);
@@ -391,11 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   const long lo = slice_lo(a, blockIdx.x), hi = slice_lo(a, blockIdx.x + 1);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&sm.k_full[s]), kDqWarps);
-      mbar_init(smem_u32(&sm.v_full[s]), kDqWarps);
-      mbar_init(smem_u32(&sm.k_empty[s]), 4);
-      mbar_init(smem_u32(&sm.v_empty[s]), 4);
+    for (int i = 0; i < 2 * kStages; ++i) {
+      mbar_init(smem_u32(&sm.k_full[i >> 1][i & 1]), kDqWarps / 4);
+      mbar_init(smem_u32(&sm.v_full[i >> 1][i & 1]), kDqWarps / 4);
+      mbar_init(smem_u32(&sm.k_empty[i >> 1][i & 1]), 2);
+      mbar_init(smem_u32(&sm.v_empty[i >> 1][i & 1]), 2);
     }
     mbar_init(smem_u32(&sm.q_full), 2 * kBM);
     for (int i = 0; i < 4; ++i) {
@@ -425,80 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   if (warp >= kSoftWarps && warp < kSoftWarps + kDqWarps) {
     // ------------------------------------------------ dequantization
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
-    const int w = warp - kSoftWarps;
-    DqMap d;
-    d.grp = w >> 1;
-    d.r = 8 * (w & 1) + (lane & 7);
-    d.cb = lane >> 3;
-    // Items in order, each with its codes and scales loaded two items earlier
-    // (two register sets in turn: one tile's conversion is shorter than the
-    // loads' latency).
-    struct Pos {
-      long u;
-      int rb, tile;
-    };
-    auto next = [&](Pos &p) {
-      if (++p.tile == a.tiles) {
-        p.tile = 0;
-        if (++p.rb == a.row_blocks) {
-          p.rb = 0;
-          ++p.u;
-        }
-      }
-    };
-    KRaw k0, k1;
-    VRaw v0, v1;
-    Pos cur, ahead;
-    cur.tile = static_cast<int>(lo % a.tiles);
-    cur.rb = static_cast<int>(lo / a.tiles % a.row_blocks);
-    cur.u = lo / a.tiles / a.row_blocks;
-    ahead = cur;
-    int left = static_cast<int>(hi - lo);  // items from `ahead` on
-    auto load = [&](KRaw *k, VRaw *v) {
-      if (left > 0 && ahead.tile < a.int4_tiles) {
-        if (k) load_k(a, ahead.u, ahead.tile, d, *k);
-        if (v) load_v(a, ahead.u, ahead.tile, d, *v);
-      }
-      if (v) {
-        next(ahead);
-        --left;
-      }
-    };
-    load(&k0, &v0);
-    load(&k1, &v1);
-    const int n_items = static_cast<int>(hi - lo);
-    auto item = [&](int j, KRaw &kx, VRaw &vx) -> bool {
-      const int st = j % kStages;
-      const uint32_t par = static_cast<uint32_t>((j / kStages - 1) & 1);
-      const bool int4 = cur.tile < a.int4_tiles;
-      const int tail0 = kBN * (cur.tile - a.int4_tiles);
-      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.k_empty[st]), par, a.ctl)) return false;
-      if (__any_sync(0xffffffffu, cta_aborted(abort_flag))) return false;
-      if (int4)
-        store_k(kx, d, sm.k[st]);
-      else
-        copy_tail(a, cur.u, tail0, d, a.k_window, a.k_tree, false, sm.k[st]);
-      fence_async_smem();
-      __syncwarp();
-      // (test hook: a dropped item's keys never arrive)
-      if (lane == 0 && lo + j != a.ctl.drop_item) mbar_arrive(smem_u32(&sm.k_full[st]));
-      load(&kx, nullptr);
-      if (j >= kStages && !warp_wait(abort_flag, smem_u32(&sm.v_empty[st]), par, a.ctl)) return false;
-      if (int4)
-        store_v(vx, d, sm.v[st]);
-      else
-        copy_tail(a, cur.u, tail0, d, a.v_window, a.v_tree, true, sm.v[st]);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[st]));
-      load(nullptr, &vx);
-      next(cur);
-      return true;
-    };
-    for (int j = 0; j < n_items; j += 2) {
-      if (!item(j, k0, v0)) break;
-      if (j + 1 < n_items && !item(j + 1, k1, v1)) break;
-    }
+    if (warp < kSoftWarps + kDqWarps / 2)
+      dequant_warp<false>(a, sm, lo, hi, warp & 3, lane);
+    else
+      dequant_warp<true>(a, sm, lo, hi, warp & 3, lane);
   } else if (warp >= kSoftWarps + kDqWarps) {
     // ------------------------------------------------ MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
@@ -524,19 +518,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const uint32_t qd = q_lo + (two ? g : 0u) * (kTileBytes >> 4);
       if (!spin_wait(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
       // group g takes tiles 0, 1, 2, ... of the segment (two) or g, g + 2, ...
-      // (shared rows; a stage's four arrivals then come from one group)
+      // (shared rows; a half stage's two arrivals then come from one group)
       bool first = true;
       for (int at = two ? 0 : static_cast<int>(g); at < n; at += two ? 1 : 2) {
         const uint32_t jj = base_j + at, st = uniform(jj % kStages), par = (jj / kStages) & 1;
         // S: K is there and this half's last PV has read P
-        if (!spin_wait(abort_flag, smem_u32(&sm.k_full[st]), par, a.ctl) ||
+        if (!spin_wait(abort_flag, smem_u32(&sm.k_full[st][h]), par, a.ctl) ||
             (!first && !spin_wait(abort_flag, o_bar, (done - 1) & 1, a.ctl))) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t kd = k_lo + st * (kTileBytes >> 4);
-        const uint32_t k_bar = smem_u32(&sm.k_empty[st]), v_bar = smem_u32(&sm.v_empty[st]);
+        const uint32_t k_bar = smem_u32(&sm.k_empty[st][h]), v_bar = smem_u32(&sm.v_empty[st][h]);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {  // (descriptor addresses count 16 bytes)
@@ -549,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         }
         __syncwarp();
         // O += P V
-        if (!spin_wait(abort_flag, smem_u32(&sm.v_full[st]), par, a.ctl) ||
+        if (!spin_wait(abort_flag, smem_u32(&sm.v_full[st][h]), par, a.ctl) ||
             !spin_wait(abort_flag, p_bar, done & 1, a.ctl)) {
           ok = false;
           break;
@@ -981,7 +975,10 @@ bool tree_tensor_supported(const kvq_cache &c, int q_dtype, int tree_dtype, int 
   return c.head_dim == kD && win && c.kwin_dtype != KVQ_MXFP8 && q_dtype == KVQ_BF16 &&
          tree_dtype == KVQ_BF16 &&
          static_cast<long>(T) * (Hq / c.kv_heads) <= (1L << 24) &&
-         static_cast<long>(c.n_tokens) + T < (1L << 30);
+         static_cast<long>(c.n_tokens) + T < (1L << 30) &&
+         // items (32-bit in the kernel): row blocks of 256, tiles of 128 keys and two partial ones
+         static_cast<long>(c.batch) * c.kv_heads * (static_cast<long>(T) * (Hq / c.kv_heads) / 256 + 1) *
+                 (c.n_tokens / 128 + 4) < (1L << 30);
 }
 
 size_t tree_workspace_bytes(const kvq_cache &c, int Hq, int T, int num_sms) {
