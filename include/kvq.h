@@ -477,7 +477,8 @@ KVQ_API kvq_status kv_rope(const kvq_rope_tensor *tensors, int32_t n_tensors, in
  * the tensor cores with fp16 operands: the int4 part as code * scale (the
  * scale and the product each rounded once to fp16, 11 bits), q, window and
  * drafted rows converted from bf16 (exact within fp16's normal range, 6e-5 to
- * 65504; larger finite values are clamped to it), products and sums in fp32.
+ * 65504; larger values, infinite ones too, count as 65504), products and sums
+ * in fp32.
  * Other shapes run an fp32 kernel (q_heads and batch <= 65,535).
  */
 #define KVQ_TREE_MAX 256

@@ -67,8 +67,11 @@ constexpr uint32_t kHalf = 128u * 128u;      // 16 KB: 128 rows x 64 fp16 featur
 constexpr uint32_t kTileBytes = 2u * kHalf;
 constexpr int kStages = 2;                   // K and V tiles in shared memory, each
 constexpr int kMaskWords = KVQ_TREE_MAX / 32;
+constexpr int kLead = 3;                     // tiles' worth of time a row block's start and end take
 constexpr float kSumBound = 4096.0f;         // sum of 64 P above which the reference is raised
-constexpr int kPartStride = kD + 4;          // floats of a partial row: O[128], m, l, padding
+// A partial: O of 256 rows as [32 pieces][256 rows] float4 (a warp's store is
+// consecutive rows of one piece), then (m, l) of the rows.
+constexpr long kPartFloats = kRowBlock * (kD + 2);
 
 struct __align__(1024) TreeSmem {
   uint8_t q[2][kTileBytes];
@@ -97,12 +100,16 @@ struct TreeArgs {
   int Hkv, G, T, R, cut, Gk, Gs, Vs, Ws;
   int rows, row_blocks;                 // T * G, and per unit
   int int4_tiles, tiles;                // key tiles per unit
-  long items;                           // units * row_blocks * tiles
+  // Items are laid out as if every row block began with `lead` more tiles (the
+  // time its queries, masks and output take), so that slices that begin a row
+  // block get fewer tiles.
+  int lead, span;                       // span = lead + tiles
+  long items;                           // units * row_blocks * span
   int ctas, slots;                      // slots: partials reserved per row block
   float scale_log2;
   void *out;
   int out_dtype;
-  float *partials;                      // [unit * row_blocks][slots][256][132]
+  float *partials;                      // [unit * row_blocks][slots][kPartFloats]
   KernelCtl ctl;
 };
 
@@ -189,20 +196,18 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t b_mn_major, uint32_t n
   return (1u << 4) | (b_mn_major << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Two floats to fp16, finite values beyond its range clamped to it (infinities
-// and NaN stay).
-__device__ __forceinline__ float clamp_h(float x) {
-  const float c = fminf(fmaxf(x, -65504.0f), 65504.0f);
-  return fabsf(x) <= 3.40282347e38f ? c : x;
+// Two floats to fp16, values beyond its range (infinities too) clamped to it; NaN
+// stays.
+__device__ __forceinline__ uint32_t pack_h2_sat(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 // Eight bf16 (four words, natural order) as fp16 in the tiles' feature order.
 __device__ __forceinline__ uint4 bf8_to_h8(const uint4 &w) {
-  const float x0 = clamp_h(bf_lo(w.x)), x1 = clamp_h(bf_hi(w.x));
-  const float x2 = clamp_h(bf_lo(w.y)), x3 = clamp_h(bf_hi(w.y));
-  const float x4 = clamp_h(bf_lo(w.z)), x5 = clamp_h(bf_hi(w.z));
-  const float x6 = clamp_h(bf_lo(w.w)), x7 = clamp_h(bf_hi(w.w));
-  return make_uint4(pack_h2(x0, x4), pack_h2(x1, x5), pack_h2(x2, x6), pack_h2(x3, x7));
+  return make_uint4(pack_h2_sat(bf_lo(w.x), bf_lo(w.z)), pack_h2_sat(bf_hi(w.x), bf_hi(w.z)),
+                    pack_h2_sat(bf_lo(w.y), bf_lo(w.w)), pack_h2_sat(bf_hi(w.y), bf_hi(w.w)));
 }
 
 // Place of 16-byte chunk c (0..15, eight features each) of row r in a tile.
@@ -210,8 +215,31 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
   return (c >> 3) * kHalf + swz(r, c & 7u);
 }
 
-// Slice of CTA c: items [items * c / ctas, items * (c + 1) / ctas).
-__device__ __forceinline__ long slice_lo(const TreeArgs &a, int c) { return a.items * c / a.ctas; }
+// Slice of CTA c: items [items * c / ctas, items * (c + 1) / ctas), moved to the
+// first tile of a row block where it begins in the lead of one.
+__device__ __forceinline__ uint32_t slice_lo(const TreeArgs &a, int c) {
+  return static_cast<uint32_t>(a.items * c / a.ctas);
+}
+// A CTA's work: segments of consecutive tiles of one row block each.
+struct Segment {
+  uint32_t rb;       // unit * row_blocks + row block
+  int t_lo, n;       // first tile, tiles (> 0)
+};
+// The segment that begins at or after item x (moved behind it); false when
+// the slice ending at hi holds no further tile.
+__device__ __forceinline__ bool next_segment(const TreeArgs &a, uint32_t &x, uint32_t hi,
+                                             Segment &s) {
+  while (x < hi) {
+    s.rb = x / static_cast<uint32_t>(a.span);
+    const uint32_t start = s.rb * a.span, end = min(start + a.span, hi);
+    const int lo = max(0, static_cast<int>(x - start) - a.lead);
+    s.t_lo = lo;
+    s.n = static_cast<int>(end - start) - a.lead - lo;
+    x = end;
+    if (s.n > 0) return true;
+  }
+  return false;
+}
 // CTA whose slice holds item x.
 __device__ __forceinline__ int cta_of(const TreeArgs &a, long x) {
   return static_cast<int>(((x + 1) * a.ctas - 1) / a.items);
@@ -320,7 +348,7 @@ template <bool kV>
 __device__ __noinline__ void copy_tail(const TreeArgs &a, long u, int k0, int grp, int r, int cb,
                                           uint8_t *tile) {
   const uint16_t *win = kV ? a.v_window : a.k_window, *tree = kV ? a.v_tree : a.k_tree;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = 0; i < 4; ++i) {
     const int row = 32 * grp + r + 8 * i, key = k0 + row;
     const uint16_t *p = key < a.R ? win + (u * a.Ws + key) * kD
@@ -375,9 +403,10 @@ __device__ __forceinline__ bool warp_wait(int *abort_flag, uint32_t bar, uint32_
 
 // Features d0 .. d0 + 31 of a row just written to dst whose seen drafted tokens
 // hold infinities or NaN in V there (zeroed in the tiles): the sum of those is
-// the result. k_lo, k_hi: the tail keys the row's sum covers.
+// the result. k_lo, k_hi: the tail keys the row's sum covers; step: elements from
+// one piece of four features to the next.
 __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &sm, long u, int tok,
-                                            int k_lo, int k_hi, int d0, void *dst, bool bf16) {
+                                            int k_lo, int k_hi, int d0, void *dst, int step, bool bf16) {
   for (int e = d0; e < d0 + 32; ++e) {
     float s = 0.0f;
     for (int j = max(0, k_lo - a.R); j < min(a.T, k_hi - a.R); ++j) {
@@ -387,10 +416,11 @@ __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &s
       if (!(fabsf(x) <= 3.40282347e38f)) s += x;
     }
     if (s == 0.0f) continue;
+    const long at = static_cast<long>(e >> 2) * step + (e & 3);
     if (bf16)
-      static_cast<__nv_bfloat16 *>(dst)[e] = __float2bfloat16_rn(s);
+      static_cast<__nv_bfloat16 *>(dst)[at] = __float2bfloat16_rn(s);
     else
-      static_cast<float *>(dst)[e] = s;
+      static_cast<float *>(dst)[at] = s;
   }
 }
 
@@ -399,33 +429,34 @@ __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &s
 // loop twice; the code of all roles then no longer fits the instruction caches
 // and the call takes half as long again.)
 template <bool kV>
-__device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, long lo, long hi,
-                                             int grp, int lane) {
+__device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, uint32_t lo,
+                                             uint32_t hi, int grp, int lane) {
   const int r = lane & 7, cb = lane >> 3;
-  const int n = static_cast<int>(hi - lo);
-  // Only tiles are followed; a unit is found by division where one begins.
-  // (32-bit: a 64-bit division is a call, around which registers spill)
-  const uint32_t lo32 = static_cast<uint32_t>(lo);
-  auto unit_of = [&](int j) {
-    return static_cast<long>((lo32 + j) / static_cast<uint32_t>(a.tiles) /
-                             static_cast<uint32_t>(a.row_blocks));
+  auto unit_of = [&](uint32_t rb) {
+    return static_cast<long>(rb / static_cast<uint32_t>(a.row_blocks));
   };
-  int cur = static_cast<int>(lo32 % static_cast<uint32_t>(a.tiles)), ahead = cur, ahead_j = 0;
-  RawPtr ptr = raw_ptr<kV>(a, unit_of(0), cur, grp, r, cb);
-  auto load = [&](Raw &x) {
-    if (ahead_j < n && ahead < a.int4_tiles) load_raw<kV>(a, ptr, ahead, grp, r, x);
-    ++ahead_j;
+  // the tile at hand and the one loaded ahead: segment, tile, tiles left
+  Segment cur, ahead;
+  uint32_t cur_x = lo, ahead_x = lo;
+  bool more = next_segment(a, ahead_x, hi, ahead);
+  if (!more) return;
+  next_segment(a, cur_x, hi, cur);
+  RawPtr ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp, r, cb);
+  Raw x;
+  auto load = [&]() {
+    if (!more) return;
+    if (ahead.t_lo < a.int4_tiles) load_raw<kV>(a, ptr, ahead.t_lo, grp, r, x);
     ptr.c += 8192;
     ptr.s += 512;
-    if (++ahead == a.tiles) {
-      ahead = 0;
-      ptr = raw_ptr<kV>(a, unit_of(ahead_j), 0, grp, r, cb);
+    ++ahead.t_lo;
+    if (--ahead.n == 0) {
+      more = next_segment(a, ahead_x, hi, ahead);
+      if (more) ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp, r, cb);
     }
   };
-  Raw x;
-  load(x);
+  load();
 #pragma unroll 1
-  for (int j = 0; j < n; ++j) {
+  for (int j = 0;; ++j) {
     const int st = j % kStages;
     uint64_t *empty = kV ? &sm.v_empty[st][grp >> 1] : &sm.k_empty[st][grp >> 1];
     uint64_t *full = kV ? &sm.v_full[st][grp >> 1] : &sm.k_full[st][grp >> 1];
@@ -433,16 +464,18 @@ __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, lo
     if (j >= kStages && !warp_wait(&sm.abort_flag, smem_u32(empty),
                                    static_cast<uint32_t>((j / kStages - 1) & 1), a.ctl))
       break;
-    if (cur < a.int4_tiles)
+    if (cur.t_lo < a.int4_tiles)
       store_raw<kV>(x, r, cb, tile + (32 * grp + r) * 128);
     else
-      copy_tail<kV>(a, unit_of(j), kBN * (cur - a.int4_tiles), grp, r, cb, tile);
+      copy_tail<kV>(a, unit_of(cur.rb), kBN * (cur.t_lo - a.int4_tiles), grp, r, cb, tile);
     fence_async_smem();
     __syncwarp();
-    // (test hook: a dropped item's keys never arrive)
-    if (lane == 0 && (kV || lo + j != a.ctl.drop_item)) mbar_arrive(smem_u32(full));
-    load(x);
-    if (++cur == a.tiles) cur = 0;
+    // (test hook: the keys of a dropped tile never arrive)
+    if (lane == 0 && (kV || static_cast<int>(cur.rb) * a.tiles + cur.t_lo != a.ctl.drop_item))
+      mbar_arrive(smem_u32(full));
+    load();
+    ++cur.t_lo;
+    if (--cur.n == 0 && !next_segment(a, cur_x, hi, cur)) break;
   }
 }
 
@@ -452,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   TreeSmem &sm = *reinterpret_cast<TreeSmem *>(smem_raw + (((base + 1023u) & ~1023u) - base));
   int *const abort_flag = &sm.abort_flag;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const long lo = slice_lo(a, blockIdx.x), hi = slice_lo(a, blockIdx.x + 1);
+  const uint32_t lo = slice_lo(a, blockIdx.x), hi = slice_lo(a, blockIdx.x + 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * kStages; ++i) {
@@ -489,10 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   if (warp >= kSoftWarps && warp < kSoftWarps + kDqWarps) {
     // ------------------------------------------------ dequantization
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
-    if (warp < kSoftWarps + kDqWarps / 2)
-      dequant_warp<false>(a, sm, lo, hi, warp & 3, lane);
+    // K on the schedulers (warp % 4) 0 and 1, V on 2 and 3: each holds one's code
+    const int grp = (warp & 1) + ((warp & 4) >> 1);
+    if (warp & 2)
+      dequant_warp<true>(a, sm, lo, hi, grp, lane);
     else
-      dequant_warp<true>(a, sm, lo, hi, warp & 3, lane);
+      dequant_warp<false>(a, sm, lo, hi, grp, lane);
   } else if (warp >= kSoftWarps + kDqWarps) {
     // ------------------------------------------------ MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
@@ -509,12 +544,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     uint32_t seg = 0;
     uint32_t done = 0;    // PV MMAs issued so far
     bool ok = true;
-    for (long x = lo; ok && x < hi; ++seg) {
-      const long rb = x / a.tiles;
-      const int t_lo = static_cast<int>(x - rb * a.tiles);
-      const int n = static_cast<int>(min(static_cast<long>(a.tiles - t_lo), hi - x));
-      const bool two =
-          uniform(a.rows - kRowBlock * static_cast<int>(rb % a.row_blocks) > kBM ? 1u : 0u) != 0u;
+    uint32_t x = lo;
+    for (Segment sg; ok && next_segment(a, x, hi, sg); ++seg) {
+      const int n = uniform(sg.n);
+      const int row0 = kRowBlock * static_cast<int>(sg.rb % static_cast<uint32_t>(a.row_blocks));
+      const bool two = uniform(a.rows - row0 > kBM ? 1u : 0u) != 0u;
       const uint32_t qd = q_lo + (two ? g : 0u) * (kTileBytes >> 4);
       if (!spin_wait(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
       // group g takes tiles 0, 1, 2, ... of the segment (two) or g, g + 2, ...
@@ -563,7 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         first = false;
       }
       base_j += n;
-      x += n;
     }
     // all MMAs of this CTA complete before TMEM is released
     if (elect_one()) tc_commit(smem_u32(&sm.mma_done));
@@ -578,20 +611,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     const uint32_t s_row = t_s(g) + lane_off, o_row = t_o(g) + lane_off;
     int pv_seen = 0;  // tiles of this group so far
     bool ok = true;
-    for (long x = lo; x < hi;) {
-      const long rb = x / a.tiles;
-      const int t_lo = static_cast<int>(x - rb * a.tiles);
-      const int n = static_cast<int>(min(static_cast<long>(a.tiles - t_lo), hi - x));
-      const long u = rb / a.row_blocks;
-      const int row0 = kRowBlock * static_cast<int>(rb - u * a.row_blocks);
+    uint32_t x = lo;
+    for (Segment sg; next_segment(a, x, hi, sg);) {
+      const long rb = sg.rb;
+      const int t_lo = sg.t_lo, n = sg.n;
+      const uint32_t u32 = sg.rb / static_cast<uint32_t>(a.row_blocks);
+      const long u = u32;
+      const int row0 = kRowBlock * static_cast<int>(sg.rb - u32 * a.row_blocks);
       const bool two = a.rows - row0 > kBM;
-      const long b = u / a.Hkv;
-      const int kvh = static_cast<int>(u - b * a.Hkv);
+      const long b = u32 / static_cast<uint32_t>(a.Hkv);
+      const int kvh = static_cast<int>(u32 - static_cast<uint32_t>(b) * a.Hkv);
       const int r = row0 + (two ? kBM * g : 0) + row;  // row of the unit: token r / G, head r % G
       const int tok = r < a.rows ? r / a.G : 0, head = r - tok * a.G;
-      x += n;
-      // ---- the tree's masks and this segment's queries
+      // ---- the tree's masks and this segment's queries. Half a warp loads a
+      // query row; the first eight pairs of rows are in flight while the
+      // masks are made. Two groups of rows: a group loads its own 128, else
+      // both load 64 of the shared ones.
       const int tid = threadIdx.x;  // 0..255
+      const int q_first = two ? 32 * (warp & 3) : 16 * warp;  // within the MMA tile
+      const int q_base = row0 + (two ? kBM * g : 0) + q_first + (lane >> 4);
+      uint8_t *const q_tile = sm.q[two ? g : 0];
+      uint4 qw[8];
+      auto load_q = [&](int i) -> uint4 {
+        const int qr = q_base + 2 * i, qt = qr / a.G;
+        const uint16_t *p =
+            a.q + ((u * a.G + (qr - qt * a.G)) * a.T + qt) * kD + 8 * (lane & 15);
+        return qr < a.rows && in_bounds(a.ctl, p, 16) ? *reinterpret_cast<const uint4 *>(p)
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+      };
+      auto store_q = [&](int i, const uint4 &w) {  // zeros for a row without a token
+        const int qr = q_base + 2 * i, qt = qr / a.G;
+        const bool on = qr < a.rows && (sm.live[qt >> 5] >> (qt & 31) & 1u);
+        *reinterpret_cast<uint4 *>(q_tile + chunk_at(q_first + (lane >> 4) + 2 * i, lane & 15)) =
+            on ? bf8_to_h8(w) : make_uint4(0u, 0u, 0u, 0u);
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qw[i] = load_q(i);
       {
         const int32_t *p = a.parents + b * a.T;
         const bool pok = in_bounds(a.ctl, p, sizeof(int32_t) * a.T);
@@ -624,27 +679,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const int tail_lo = kBN * max(0, t_lo - a.int4_tiles);        // tail keys of this segment
       const int tail_hi = kBN * (t_lo + n - a.int4_tiles);
       if (has_tail) {
-        for (int j = max(0, tail_lo - a.R) + warp; j < min(a.T, tail_hi - a.R); j += kSoftWarps) {
-          const uint16_t *p = a.v_tree + (u * a.T + j) * kD + 4 * lane;
-          uint2 w = in_bounds(a.ctl, p, 8) ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
-          const bool odd = (w.x & 0x7f80u) == 0x7f80u || (w.x & 0x7f800000u) == 0x7f800000u ||
-                           (w.y & 0x7f80u) == 0x7f80u || (w.y & 0x7f800000u) == 0x7f800000u;
-          if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sm.odd_v[j >> 5], 1u << (j & 31));
+        // drafted tokens with a non-finite V: a warp per token, four at a time
+        const int j1 = min(a.T, tail_hi - a.R);
+        for (int j0 = max(0, tail_lo - a.R) + warp; j0 < j1; j0 += 4 * kSoftWarps) {
+          uint2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + i * kSoftWarps;
+            const uint16_t *p = a.v_tree + (u * a.T + j) * kD + 4 * lane;
+            w[i] = j < j1 && in_bounds(a.ctl, p, 8) ? *reinterpret_cast<const uint2 *>(p)
+                                                    : make_uint2(0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + i * kSoftWarps;
+            const bool odd =
+                (w[i].x & 0x7f80u) == 0x7f80u || (w[i].x & 0x7f800000u) == 0x7f800000u ||
+                (w[i].y & 0x7f80u) == 0x7f80u || (w[i].y & 0x7f800000u) == 0x7f800000u;
+            if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sm.odd_v[j >> 5], 1u << (j & 31));
+          }
         }
       }
       soft_sync();
       const bool mine = r < a.rows && (sm.live[tok >> 5] >> (tok & 31) & 1u);
-      const long qrow = ((b * a.Hkv + kvh) * a.G + head) * a.T + tok;
-      {
-        const uint16_t *p = a.q + qrow * kD;
-        const bool qok = mine && in_bounds(a.ctl, p, 2 * kD);
-        // two: each group its own tile; shared rows: one half of the features each
-        uint8_t *q = sm.q[two ? g : 0];
-        const int c0 = two ? 0 : 8 * g, c1 = two ? 16 : 8 * g + 8;
-#pragma unroll 4
-        for (int c = c0; c < c1; ++c)
-          *reinterpret_cast<uint4 *>(q + chunk_at(row, c)) =
-              qok ? bf8_to_h8(reinterpret_cast<const uint4 *>(p)[c]) : make_uint4(0u, 0u, 0u, 0u);
+      const long qrow = (u * a.G + head) * a.T + tok;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) store_q(i, qw[i]);
+      if (two) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qw[i] = load_q(8 + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store_q(8 + i, qw[i]);
       }
       // O starts at zero: the halves' first PVs may come in either order
       {
@@ -790,11 +855,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       }
       const bool whole = n == a.tiles;
       const float inv = whole ? 1.0f / l : 1.0f;
-      float *part = nullptr;
+      float *part = nullptr;  // this row's first float4, pieces kRowBlock apart
+      float2 *part_ml = nullptr;
       if (!whole) {
-        const int slot = static_cast<int>(blockIdx.x) - cta_of(a, rb * a.tiles);
-        part = a.partials +
-               ((rb * a.slots + slot) * kRowBlock + (r - row0)) * static_cast<long>(kPartStride);
+        const int slot = static_cast<int>(blockIdx.x) - cta_of(a, rb * a.span + a.lead);
+        float *p = a.partials + (rb * a.slots + slot) * kPartFloats;
+        part = p + 4 * (r - row0);
+        part_ml = reinterpret_cast<float2 *>(p + kRowBlock * kD) + (r - row0);
+        if (!in_bounds(a.ctl, p, sizeof(float) * kPartFloats)) part = nullptr;
       }
       bool odd = false;  // a seen drafted token with a non-finite V
       if (has_tail) {
@@ -832,13 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           y[(e & ~7) + nat] = v[e] * inv;
         }
         if (!whole) {
-          float4 *o = reinterpret_cast<float4 *>(part + 32 * c);
-          if (!in_bounds(a.ctl, part, sizeof(float) * kPartStride)) continue;
+          if (!part) continue;
+          float4 *o = reinterpret_cast<float4 *>(part) + static_cast<long>(8 * c) * kRowBlock;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            o[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-          if (c == 0) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
-          if (odd) put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c, part, false);
+            o[e * kRowBlock] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          if (odd) put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c, part, 4 * kRowBlock, false);
         } else if (a.out_dtype == KVQ_F32) {
           float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + qrow * kD + 32 * c);
           if (!in_bounds(a.ctl, o, 128)) continue;
@@ -847,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
             o[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           if (odd)
             put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c,
-                           static_cast<float *>(a.out) + qrow * kD, false);
+                           static_cast<float *>(a.out) + qrow * kD, 4, false);
         } else {
           uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + qrow * kD + 32 * c);
           if (!in_bounds(a.ctl, o, 64)) continue;
@@ -858,13 +925,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
                               pack_bf2(y[8 * e + 6], y[8 * e + 7]));
           if (odd)
             put_odd_values(a, sm, u, tok, tail_lo, tail_hi, 32 * c,
-                           static_cast<uint16_t *>(a.out) + qrow * kD, true);
+                           static_cast<uint16_t *>(a.out) + qrow * kD, 4, true);
         }
       }
-      // a row without a token leaves a partial that says so
-      if (!mine && !whole && r < a.rows && (two || g == 0) &&
-          in_bounds(a.ctl, part, sizeof(float) * kPartStride))
-        *reinterpret_cast<float2 *>(part + kD) = make_float2(-CUDART_INF_F, 0.0f);
+      // (a row without a token leaves a partial that says so)
+      if (part && r < a.rows && (two || g == 0))
+        *part_ml = mine ? make_float2(m, l) : make_float2(-CUDART_INF_F, 0.0f);
       tc_fence_before();
       soft_sync();  // O, masks and states are read before the next segment rewrites them
       tc_fence_after();
@@ -878,76 +944,115 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   }
 }
 
-// One warp per query row: merge the partials of the CTAs whose slices overlap
-// its row block (log-sum-exp), normalise, store. Row blocks inside one slice
-// were written by the kernel itself.
+// Merge of the partials of the CTAs whose slices overlap a row block (log-sum-exp),
+// for 32 rows (lane = row) and, per warp, 16 features: a warp's loads are
+// consecutive rows of one piece, and each thread stores whole 32-byte sectors.
+// Row blocks inside one slice were written by the kernel itself. kWide (few row
+// blocks, each over many CTAs): one block per 16 features, its warps take every
+// eighth slot and meet in shared memory.
 constexpr int kCombineWarps = 8;
+constexpr int kWideAbove = 12;  // slots per row block
 
-__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const TreeArgs a,
-                                                                          long total_rows) {
+struct RowState {
+  float m, l, o[16];
+};
+__device__ __forceinline__ void merge_slot(RowState &s, const float2 &ml, const float4 (&o)[4]) {
+  if (ml.y == 0.0f) return;  // no key (a NaN sum stays in)
+  const float mn = fmaxf(s.m, ml.x);
+  const float ws = s.m == -CUDART_INF_F ? 0.0f : exp2f(s.m - mn);
+  const float w = ml.x == -CUDART_INF_F ? 1.0f : exp2f(ml.x - mn);
+  s.l = s.l * ws + ml.y * w;
+  s.m = mn;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s.o[4 * i] = s.o[4 * i] * ws + o[i].x * w;
+    s.o[4 * i + 1] = s.o[4 * i + 1] * ws + o[i].y * w;
+    s.o[4 * i + 2] = s.o[4 * i + 2] * ws + o[i].z * w;
+    s.o[4 * i + 3] = s.o[4 * i + 3] * ws + o[i].w * w;
+  }
+}
+
+template <bool kWide>
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const TreeArgs a) {
   wait_prior_grid();
   allow_next_grid();
-  const int lane = threadIdx.x & 31;
-  const long id = static_cast<long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  if (id >= total_rows) return;
-  const long u = id / a.rows;
-  const int r = static_cast<int>(id - u * a.rows);
-  const long rb = u * a.row_blocks + r / kRowBlock;
-  const int c0 = cta_of(a, rb * a.tiles), c1 = cta_of(a, (rb + 1) * a.tiles - 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rb = blockIdx.x;
+  const uint32_t u = rb / static_cast<uint32_t>(a.row_blocks);
+  const int row0 = kRowBlock * static_cast<int>(rb - u * a.row_blocks);
+  const int in_rb = 32 * blockIdx.y + lane, r = row0 + in_rb;
+  if (row0 + 32 * static_cast<int>(blockIdx.y) >= a.rows) return;
+  const int c0 = cta_of(a, static_cast<long>(rb) * a.span + a.lead);
+  const int c1 = cta_of(a, static_cast<long>(rb + 1) * a.span - 1);
   const int n = c1 - c0 + 1;
   if (n == 1) return;
-  const long slot = static_cast<long>(kRowBlock) * kPartStride;
-  const float *p = a.partials + (rb * a.slots * kRowBlock + r % kRowBlock) * static_cast<long>(kPartStride);
-#ifdef KVQ_DEBUG
-  for (int i = 0; i < n; ++i)
-    if (!in_bounds(a.ctl, p + i * slot, sizeof(float) * kPartStride)) return;
-#endif
-  // the largest reference of the slots, then weights against it
-  float m = -CUDART_INF_F;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, p[i * slot + kD]);
-  m = warp_max(m);
-  float l = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  bool any = false;
-  constexpr int kBatch = 8;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    float2 ml[kBatch];
-    float4 o[kBatch];
+  const int grp = kWide ? blockIdx.z : warp;  // features 16 grp .. + 15
+  const float *p = a.partials + static_cast<long>(rb) * a.slots * kPartFloats;
+  if (!in_bounds(a.ctl, p, sizeof(float) * kPartFloats * n)) return;
+  const float4 *po = reinterpret_cast<const float4 *>(p) + 4 * grp * kRowBlock + in_rb;
+  const float2 *pml = reinterpret_cast<const float2 *>(p + kRowBlock * kD) + in_rb;
+  RowState s;
+  s.m = -CUDART_INF_F;
+  s.l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float *s = p + min(i0 + i, n - 1) * slot;
-      ml[i] = *reinterpret_cast<const float2 *>(s + kD);
-      o[i] = *reinterpret_cast<const float4 *>(s + 4 * lane);
+  for (int e = 0; e < 16; ++e) s.o[e] = 0.0f;
+  constexpr int kBatch = 3;  // slots in flight
+  const int first = kWide ? warp : 0, step = kWide ? kCombineWarps : 1;
+  for (int i0 = first; i0 < n; i0 += kBatch * step) {
+    float2 ml[kBatch];
+    float4 o[kBatch][4];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * step;
+      ml[k] = make_float2(-CUDART_INF_F, 0.0f);
+      if (i < n) {
+        ml[k] = pml[i * (kPartFloats / 2)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][e] = po[i * (kPartFloats / 4) + e * kRowBlock];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (i0 + i >= n || ml[i].y == 0.0f) continue;  // (a NaN sum stays in)
-      any = true;
-      const float w = ml[i].x == -CUDART_INF_F ? 1.0f : exp2f(ml[i].x - m);
-      l += w * ml[i].y;
-      acc.x += w * o[i].x;
-      acc.y += w * o[i].y;
-      acc.z += w * o[i].z;
-      acc.w += w * o[i].w;
+    for (int k = 0; k < kBatch; ++k) merge_slot(s, ml[k], o[k]);
+  }
+  if (kWide) {
+    __shared__ float2 sml[kCombineWarps][32];
+    __shared__ float4 so[kCombineWarps][4][32];
+    sml[warp][lane] = make_float2(s.m, s.l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      so[warp][e][lane] = make_float4(s.o[4 * e], s.o[4 * e + 1], s.o[4 * e + 2], s.o[4 * e + 3]);
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < kCombineWarps; ++w) {
+      const float4 o[4] = {so[w][0][lane], so[w][1][lane], so[w][2][lane], so[w][3][lane]};
+      merge_slot(s, sml[w][lane], o);
     }
   }
-  if (!any) return;  // the row holds no token
-  const float inv = 1.0f / l;
+  if (r >= a.rows || s.l == 0.0f) return;  // (l == 0: the row holds no token)
+  const float inv = 1.0f / s.l;
   const int tok = r / a.G, head = r - tok * a.G;
-  const long row = (u * a.G + head) * a.T + tok;
+  const long at = ((static_cast<long>(u) * a.G + head) * a.T + tok) * kD + 16 * grp;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) s.o[e] *= inv;
   if (a.out_dtype == KVQ_F32) {
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kD) + lane;
-    if (in_bounds(a.ctl, o, 16))
-      *o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+    if (!in_bounds(a.ctl, o, 64)) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      o[e] = make_float4(s.o[4 * e], s.o[4 * e + 1], s.o[4 * e + 2], s.o[4 * e + 3]);
   } else {
-    uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD) + lane;
-    if (in_bounds(a.ctl, o, 8))
-      *o = make_uint2(pack_bf2(acc.x * inv, acc.y * inv), pack_bf2(acc.z * inv, acc.w * inv));
+    uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
+    if (!in_bounds(a.ctl, o, 32)) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      o[e] = make_uint4(pack_bf2(s.o[8 * e], s.o[8 * e + 1]), pack_bf2(s.o[8 * e + 2], s.o[8 * e + 3]),
+                        pack_bf2(s.o[8 * e + 4], s.o[8 * e + 5]),
+                        pack_bf2(s.o[8 * e + 6], s.o[8 * e + 7]));
   }
 }
 
 struct TreePlan {
-  int rows, row_blocks, int4_tiles, tiles, ctas, slots;
+  int rows, row_blocks, int4_tiles, tiles, lead, span, ctas, slots;
   long units, items;
 };
 
@@ -959,8 +1064,13 @@ TreePlan tree_plan(const kvq_cache &c, int Hq, int T, int num_sms) {
   p.int4_tiles = (d.cut + kBN - 1) / kBN;
   p.tiles = p.int4_tiles + (d.R + T + kBN - 1) / kBN;
   p.units = static_cast<long>(d.B) * d.Hkv;
-  p.items = p.units * p.row_blocks * p.tiles;
-  p.ctas = static_cast<int>(std::min<long>(p.items, num_sms));
+  const long work = p.units * p.row_blocks * p.tiles;
+  p.ctas = static_cast<int>(std::min<long>(work, num_sms));
+  // The lead only balances calls whose slices hold several tiles: with a tile or
+  // two a CTA every row block is split over many anyway.
+  p.lead = work >= 4L * num_sms ? kLead : 0;
+  p.span = p.lead + p.tiles;
+  p.items = p.units * p.row_blocks * p.span;
   // a row block's tiles meet at most (tiles - 2) / min_per + 2 slices
   const long min_per = p.items / p.ctas;
   p.slots = p.tiles >= 2 ? static_cast<int>((p.tiles - 2) / min_per + 2) : 1;
@@ -978,13 +1088,12 @@ bool tree_tensor_supported(const kvq_cache &c, int q_dtype, int tree_dtype, int 
          static_cast<long>(c.n_tokens) + T < (1L << 30) &&
          // items (32-bit in the kernel): row blocks of 256, tiles of 128 keys and two partial ones
          static_cast<long>(c.batch) * c.kv_heads * (static_cast<long>(T) * (Hq / c.kv_heads) / 256 + 1) *
-                 (c.n_tokens / 128 + 4) < (1L << 30);
+                 (c.n_tokens / 128 + 4 + kLead) < (1L << 30);
 }
 
 size_t tree_workspace_bytes(const kvq_cache &c, int Hq, int T, int num_sms) {
   const TreePlan p = tree_plan(c, Hq, T, num_sms);
-  return sizeof(float) * static_cast<size_t>(p.units) * p.row_blocks * p.slots * kRowBlock *
-         kPartStride;
+  return sizeof(float) * static_cast<size_t>(p.units) * p.row_blocks * p.slots * kPartFloats;
 }
 
 int launch_attend_tree(const kvq_cache &c, const void *q, int Hq, int T, const void *k_tree,
@@ -1017,6 +1126,8 @@ int launch_attend_tree(const kvq_cache &c, const void *q, int Hq, int T, const v
   a.row_blocks = p.row_blocks;
   a.int4_tiles = p.int4_tiles;
   a.tiles = p.tiles;
+  a.lead = p.lead;
+  a.span = p.span;
   a.items = p.items;
   a.ctas = p.ctas;
   a.slots = p.slots;
@@ -1028,10 +1139,14 @@ int launch_attend_tree(const kvq_cache &c, const void *q, int Hq, int T, const v
   const size_t smem = sizeof(TreeSmem) + 1024;
   if (opt_in_smem(tree_kernel, smem) != cudaSuccess) return -1;
   launch_dependent(tree_kernel, dim3(p.ctas), dim3(kThreads), smem, s, a);
-  const long total_rows = p.units * p.rows;
-  launch_dependent(tree_combine_kernel,
-                   dim3(static_cast<unsigned>((total_rows + kCombineWarps - 1) / kCombineWarps)),
-                   dim3(kCombineWarps * 32), 0, s, a, total_rows);
+  const unsigned blocks = static_cast<unsigned>(p.units * p.row_blocks);
+  const unsigned groups = static_cast<unsigned>(std::min(p.rows, kRowBlock) + 31) / 32;
+  if (p.slots > kWideAbove)
+    launch_dependent(tree_combine_kernel<true>, dim3(blocks, groups, kD / 16),
+                     dim3(kCombineWarps * 32), 0, s, a);
+  else
+    launch_dependent(tree_combine_kernel<false>, dim3(blocks, groups), dim3(kCombineWarps * 32), 0,
+                     s, a);
   return 2;
 }
 
