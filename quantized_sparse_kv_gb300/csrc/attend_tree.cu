@@ -67,7 +67,9 @@ constexpr uint32_t kHalf = 128u * 128u;      // 16 KB: 128 rows x 64 fp16 featur
 constexpr uint32_t kTileBytes = 2u * kHalf;
 constexpr int kStages = 2;                   // K and V tiles in shared memory, each
 constexpr int kMaskWords = KVQ_TREE_MAX / 32;
-constexpr int kLead = 3;                     // tiles' worth of time a row block's start and end take
+// Tiles' worth of time that starting and ending one more row block takes (12 us
+// against 1.9 us a tile of two groups, 1 us a tile of shared rows).
+constexpr int kLeadTwo = 6, kLeadShared = 10;
 constexpr float kSumBound = 4096.0f;         // sum of 64 P above which the reference is raised
 // A partial: O of 256 rows as [32 pieces][256 rows] float4 (a warp's store is
 // consecutive rows of one piece), then (m, l) of the rows.
@@ -624,35 +626,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const int r = row0 + (two ? kBM * g : 0) + row;  // row of the unit: token r / G, head r % G
       const int tok = r < a.rows ? r / a.G : 0, head = r - tok * a.G;
       // ---- the tree's masks and this segment's queries. Half a warp loads a
-      // query row; the first eight pairs of rows are in flight while the
-      // masks are made. Two groups of rows: a group loads its own 128, else
+      // query row; the first four pairs of rows are in flight while the masks
+      // are made. Two groups of rows: a group loads its own 128, else
       // both load 64 of the shared ones.
       const int tid = threadIdx.x;  // 0..255
       const int q_first = two ? 32 * (warp & 3) : 16 * warp;  // within the MMA tile
-      const int q_base = row0 + (two ? kBM * g : 0) + q_first + (lane >> 4);
+      const int q_r = row0 + (two ? kBM * g : 0) + q_first + (lane >> 4);
+      int q_tok = q_r / a.G, q_head = q_r - q_tok * a.G, q_left = a.rows - q_r;
       uint8_t *const q_tile = sm.q[two ? g : 0];
-      uint4 qw[8];
-      auto load_q = [&](int i) -> uint4 {
-        const int qr = q_base + 2 * i, qt = qr / a.G;
-        const uint16_t *p =
-            a.q + ((u * a.G + (qr - qt * a.G)) * a.T + qt) * kD + 8 * (lane & 15);
-        return qr < a.rows && in_bounds(a.ctl, p, 16) ? *reinterpret_cast<const uint4 *>(p)
-                                                      : make_uint4(0u, 0u, 0u, 0u);
-      };
-      auto store_q = [&](int i, const uint4 &w) {  // zeros for a row without a token
-        const int qr = q_base + 2 * i, qt = qr / a.G;
-        const bool on = qr < a.rows && (sm.live[qt >> 5] >> (qt & 31) & 1u);
-        *reinterpret_cast<uint4 *>(q_tile + chunk_at(q_first + (lane >> 4) + 2 * i, lane & 15)) =
-            on ? bf8_to_h8(w) : make_uint4(0u, 0u, 0u, 0u);
-      };
+      const uint16_t *const q_unit = a.q + u * a.G * a.T * kD + 8 * (lane & 15);
+      // four rows of the lane, two apart, into w; their tokens into tk (-1: none)
+      auto load_q = [&](uint4 (&w)[4], int (&tk)[4]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) qw[i] = load_q(i);
+        for (int i = 0; i < 4; ++i) {
+          const uint16_t *p = q_unit + (q_head * a.T + q_tok) * kD;
+          const bool on = q_left > 0 && in_bounds(a.ctl, p, 16);
+          w[i] = on ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
+          tk[i] = on ? q_tok : -1;
+          q_left -= 2;
+          q_head += 2;
+          while (q_head >= a.G) q_head -= a.G, ++q_tok;
+        }
+      };
+      uint4 qw[4];
+      int qt[4];
       {
         const int32_t *p = a.parents + b * a.T;
         const bool pok = in_bounds(a.ctl, p, sizeof(int32_t) * a.T);
         if (tid < a.T) sm.par[tid] = pok ? p[tid] : -2;
         if (tid < kMaskWords) sm.live[tid] = sm.odd_v[tid] = 0u;
       }
+      load_q(qw, qt);
       soft_sync();
       if (tid < a.T) {
 #pragma unroll
@@ -703,13 +707,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       soft_sync();
       const bool mine = r < a.rows && (sm.live[tok >> 5] >> (tok & 31) & 1u);
       const long qrow = (u * a.G + head) * a.T + tok;
+#pragma unroll 1
+      for (int i0 = q_first + (lane >> 4);;) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) store_q(i, qw[i]);
-      if (two) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) qw[i] = load_q(8 + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) store_q(8 + i, qw[i]);
+        for (int i = 0; i < 4; ++i) {  // zeros for a row without a token
+          const bool on = qt[i] >= 0 && (sm.live[qt[i] >> 5] >> (qt[i] & 31) & 1u);
+          *reinterpret_cast<uint4 *>(q_tile + chunk_at(i0 + 2 * i, lane & 15)) =
+              on ? bf8_to_h8(qw[i]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        i0 += 8;
+        if (i0 >= q_first + (two ? 32 : 16)) break;
+        load_q(qw, qt);
       }
       // O starts at zero: the halves' first PVs may come in either order
       {
@@ -1068,7 +1076,7 @@ TreePlan tree_plan(const kvq_cache &c, int Hq, int T, int num_sms) {
   p.ctas = static_cast<int>(std::min<long>(work, num_sms));
   // The lead only balances calls whose slices hold several tiles: with a tile or
   // two a CTA every row block is split over many anyway.
-  p.lead = work >= 4L * num_sms ? kLead : 0;
+  p.lead = work < 4L * num_sms ? 0 : p.rows > kBM ? kLeadTwo : kLeadShared;
   p.span = p.lead + p.tiles;
   p.items = p.units * p.row_blocks * p.span;
   // a row block's tiles meet at most (tiles - 2) / min_per + 2 slices
@@ -1088,7 +1096,7 @@ bool tree_tensor_supported(const kvq_cache &c, int q_dtype, int tree_dtype, int 
          static_cast<long>(c.n_tokens) + T < (1L << 30) &&
          // items (32-bit in the kernel): row blocks of 256, tiles of 128 keys and two partial ones
          static_cast<long>(c.batch) * c.kv_heads * (static_cast<long>(T) * (Hq / c.kv_heads) / 256 + 1) *
-                 (c.n_tokens / 128 + 4 + kLead) < (1L << 30);
+                 (c.n_tokens / 128 + 4 + kLeadShared) < (1L << 30);
 }
 
 size_t tree_workspace_bytes(const kvq_cache &c, int Hq, int T, int num_sms) {
