@@ -522,6 +522,15 @@ KVQ_API kvq_status kv_block_summary(const kvq_cache *cache, const kvq_summary *s
                                     kvq_stream_t stream);
 
 /*
+ * kv_block_values -- the mean keys that the summaries of blocks [first_block,
+ * n_blocks) stand for, code * scale: values, device float
+ * [batch][kv_heads][n_blocks - first_block][D]. Errors as kv_block_summary.
+ */
+KVQ_API kvq_status kv_block_values(const kvq_cache *cache, const kvq_summary *summary,
+                                   int32_t first_block, float *values, int32_t *dev_status,
+                                   kvq_stream_t stream);
+
+/*
  * kv_select_blocks -- for each query token of each KV head the top_k blocks by
  * a cheap score. Each query row is rounded to int8 (scale s_q = fl(max|q| /
  * 127), code = rint(fl(q / s_q))); a block's score for a head is

@@ -208,6 +208,46 @@ __global__ void __launch_bounds__(kSumThreads) summary_kernel(const SummaryArgs 
   }
 }
 
+// ------------------------------------------------------------------ values
+// code * scale of every summary from `first` on, dense: a thread takes four codes of
+// four rows at a time, so a warp stores 512 consecutive bytes and keeps eight
+// loads in flight. Memory: 1.25 D bytes read, 4 D written per block.
+constexpr int kValThreads = 256, kValRows = 4;
+
+__global__ void __launch_bounds__(kValThreads) values_kernel(const SummaryArgs a, float *out) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int D4 = a.D / 4, rows = a.blocks - a.first;
+  const int per = kValThreads / D4;  // rows the CTA takes at once
+  const int piece = threadIdx.x % D4, r0 = threadIdx.x / D4;
+  if (r0 >= per) return;
+  for (long u = blockIdx.y; u < a.units; u += gridDim.y) {
+    const int base = static_cast<int>(blockIdx.x) * per * kValRows + r0;
+    uint32_t c[kValRows];
+    float s[kValRows];
+#pragma unroll
+    for (int i = 0; i < kValRows; ++i) {
+      const int row = base + i * per;
+      const long from = u * a.cap + a.first + row;
+      const bool ok = row < rows && in_bounds(a.ctl, a.codes + from * a.D + 4 * piece, 4) &&
+                      in_bounds(a.ctl, a.scales + from, 4);
+      c[i] = ok ? *reinterpret_cast<const uint32_t *>(a.codes + from * a.D + 4 * piece) : 0u;
+      s[i] = ok ? a.scales[from] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kValRows; ++i) {
+      const int row = base + i * per;
+      float4 *o = reinterpret_cast<float4 *>(out + (u * rows + row) * a.D) + piece;
+      if (row >= rows || !in_bounds(a.ctl, o, 16)) continue;
+      __stcs(o, make_float4(
+                    static_cast<float>(static_cast<int8_t>(c[i] & 0xffu)) * s[i],
+                    static_cast<float>(static_cast<int8_t>(c[i] >> 8 & 0xffu)) * s[i],
+                    static_cast<float>(static_cast<int8_t>(c[i] >> 16 & 0xffu)) * s[i],
+                    static_cast<float>(static_cast<int8_t>(c[i] >> 24)) * s[i]));
+    }
+  }
+}
+
 // ------------------------------------------------------------------ scores
 struct SelectArgs {
   const int8_t *codes;
@@ -216,7 +256,8 @@ struct SelectArgs {
   int q_dtype;
   int D, Hkv, G, n_q;   // G: query heads per KV head
   int blocks, cap, top_k, sink;
-  float *scores;        // [unit][n_q][blocks]
+  float *scores;        // [unit][n_q][stride], stride = blocks rounded up to 4
+  int stride;
   int32_t *selected;
   KernelCtl ctl;
 };
@@ -225,23 +266,39 @@ constexpr int kScoreThreads = 128;
 constexpr int kMaxGroup = 64;  // query heads per KV head
 
 // One thread per block of a (unit, query token); q of the G heads as int8 in
-// shared memory, read by broadcast. A thread reads its block's D codes 16
-// bytes at a time and keeps eight heads' products at once.
+// shared memory, read by broadcast. For D = 128 (k128) a thread's whole block
+// row is in flight while q is rounded, so the two loads' latencies, which are
+// most of the time, overlap; other D read it 16 bytes at a time.
+template <bool k128>
 __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectArgs a) {
   wait_prior_grid();
   allow_next_grid();
   extern __shared__ __align__(16) int8_t qs[];  // [ceil(G / 8) * 8][D]
   __shared__ float sq[kMaxGroup];
-  const int D = a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = k128 ? 128 : a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int uq = blockIdx.y;  // unit * n_q + query token
   const long u = uq / a.n_q;
-  const int iq = uq % a.n_q;
+  const int iq = uq - static_cast<int>(u) * a.n_q;
   const int Gp = (a.G + 7) / 8 * 8;
+  const int blk = blockIdx.x * kScoreThreads + threadIdx.x;
+  const long brow = u * a.cap + blk;
+  const bool have = blk < a.blocks && in_bounds(a.ctl, a.codes + brow * D, D) &&
+                    in_bounds(a.ctl, a.scales + brow, 4);
+  const uint4 *kp = reinterpret_cast<const uint4 *>(a.codes + brow * D);
+  uint4 kk[k128 ? 8 : 1];
+  float sb = 0.0f;
+  if (have) {
+    sb = a.scales[brow];
+    if (k128) {
+#pragma unroll
+      for (int c = 0; c < (k128 ? 8 : 1); ++c) kk[c] = kp[c];
+    }
+  }
   for (int h = warp; h < Gp; h += kScoreThreads / 32) {
     const long row = (u * a.G + h) * a.n_q + iq;  // [batch][q_heads][n_q], q head = kv * G + h
     float x[8], mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < (k128 ? 4 : 8); ++i) {
       const int d = lane + 32 * i;
       x[i] = 0.0f;
       if (h < a.G && d < D) {
@@ -258,23 +315,17 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
     const float s = __fdiv_rn(warp_max(mx), 127.0f);
     if (lane == 0 && h < a.G) sq[h] = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < (k128 ? 4 : 8); ++i)
       if (lane + 32 * i < D)
         qs[h * D + lane + 32 * i] = static_cast<int8_t>(int8_code(x[i], s));
   }
   __syncthreads();
-  const int blk = blockIdx.x * kScoreThreads + threadIdx.x;
   if (blk >= a.blocks) return;
-  const long row = u * a.cap + blk;
   float score = -CUDART_INF_F;
-  if (in_bounds(a.ctl, a.codes + row * D, D) && in_bounds(a.ctl, a.scales + row, 4)) {
-    const float sb = a.scales[row];
-    const uint4 *kp = reinterpret_cast<const uint4 *>(a.codes + row * D);
+  if (have) {
     for (int h0 = 0; h0 < Gp; h0 += 8) {
       int dot[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 k = kp[c];
+      auto piece = [&](const uint4 &k, int c) {
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           const int4 q = *reinterpret_cast<const int4 *>(qs + (h0 + h) * D + 16 * c);
@@ -283,6 +334,13 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
           dot[h] = __dp4a(static_cast<int>(k.z), q.z, dot[h]);
           dot[h] = __dp4a(static_cast<int>(k.w), q.w, dot[h]);
         }
+      };
+      if (k128) {
+#pragma unroll
+        for (int c = 0; c < (k128 ? 8 : 1); ++c) piece(kk[c], c);
+      } else {
+#pragma unroll 4
+        for (int c = 0; c < D / 16; ++c) piece(kp[c], c);
       }
 #pragma unroll
       for (int h = 0; h < 8; ++h)
@@ -290,7 +348,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
           score = fmaxf(score, __fmul_rn(__fmul_rn(sq[h0 + h], sb), static_cast<float>(dot[h])));
     }
   }
-  float *o = a.scores + static_cast<long>(uq) * a.blocks + blk;
+  float *o = a.scores + static_cast<long>(uq) * a.stride + blk;
   if (in_bounds(a.ctl, o, 4)) *o = blk < a.sink ? CUDART_INF_F : score;
 }
 
@@ -298,8 +356,13 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
 // One CTA per (unit, query token): radix selection of the top_k-th largest
 // score over order-preserving keys (8 bits a round, histogram in shared
 // memory), then the blocks above it and the lowest-numbered ones equal to it
-// are written in increasing order.
+// are written in increasing order. The rounds end as soon as a whole digit is
+// taken, which with scores that differ is after two or three. Up to kSelThreads *
+// kSelKeys blocks every thread keeps the keys of consecutive blocks in
+// registers, so one prefix sum places the output; more blocks go through the
+// same code in pieces of that many, re-read from the workspace.
 constexpr int kSelThreads = 256;
+constexpr int kSelKeys = 8;
 
 // Larger score, larger key; -0 counts as +0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -307,8 +370,10 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Exclusive prefix sum of v over the CTA and its total.
-__device__ __forceinline__ int cta_scan(int v, int *warp_sums, int &total) {
+// Exclusive prefix sum of v over the CTA and its total. Two copies of warp_sums,
+// used in turn (`turn`), spare the barrier before the next scan.
+__device__ __forceinline__ int cta_scan(int v, int (*warp_sums)[kSelThreads / 32], int turn,
+                                        int &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -316,77 +381,111 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sums, int &total) {
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) warp_sums[turn & 1][warp] = x;
   __syncthreads();
   int before = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < kSelThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
+    const int s = warp_sums[turn & 1][w];
+    if (w < warp) before += s;
+    total += s;
   }
   return before + x - v;
+}
+
+// Keys of blocks base + kSelKeys * thread .. + 7 (0, below every key, past the last).
+__device__ __forceinline__ void load_keys(const float *sc, int base, int blocks,
+                                          uint32_t (&key)[kSelKeys]) {
+  const int i = base + kSelKeys * static_cast<int>(threadIdx.x);
+#pragma unroll
+  for (int j = 0; j < kSelKeys; j += 4) {
+    // (rows are padded to four scores; a padding score is not looked at)
+    const float4 f = i + j < blocks ? *reinterpret_cast<const float4 *>(sc + i + j)
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    key[j] = i + j < blocks ? order_key(f.x) : 0u;
+    key[j + 1] = i + j + 1 < blocks ? order_key(f.y) : 0u;
+    key[j + 2] = i + j + 2 < blocks ? order_key(f.z) : 0u;
+    key[j + 3] = i + j + 3 < blocks ? order_key(f.w) : 0u;
+  }
 }
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
   wait_prior_grid();
   allow_next_grid();
-  __shared__ int hist[256], warp_sums[kSelThreads / 32];
+  __shared__ int hist[2][256], warp_sums[2][kSelThreads / 32];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
+  __shared__ int s_left, s_whole;
   const int tid = threadIdx.x;
   const long uq = blockIdx.x;
-  const float *sc = a.scores + uq * a.blocks;
+  const float *sc = a.scores + uq * a.stride;
   int32_t *out = a.selected + uq * a.top_k;
   const int k = min(a.top_k, a.blocks);
-  if (!in_bounds(a.ctl, out, sizeof(int32_t) * a.top_k) ||
-      (a.blocks > 0 && !in_bounds(a.ctl, sc, sizeof(float) * a.blocks)))
-    return;
+  if (!in_bounds(a.ctl, out, sizeof(int32_t) * a.top_k)) return;
   for (int i = k + tid; i < a.top_k; i += kSelThreads) out[i] = -1;
   if (a.blocks <= a.top_k) {
     for (int i = tid; i < a.blocks; i += kSelThreads) out[i] = i;
     return;
   }
+  if (!in_bounds(a.ctl, sc, sizeof(float) * a.stride)) return;
+  constexpr int kPiece = kSelThreads * kSelKeys;
+  const bool one = a.blocks <= kPiece;
+  uint32_t key[kSelKeys];
+  load_keys(sc, 0, a.blocks, key);
   uint32_t prefix = 0u, mask = 0u;
   int left = k;  // how many of the keys matching the prefix are to be taken
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+  int turn = 0;
+  hist[0][tid] = 0;
+  for (int shift = 24; shift >= 0; shift -= 8, ++turn) {
+    int *h = hist[turn & 1];
+    hist[(turn + 1) & 1][tid] = 0;
     __syncthreads();
-    for (int i = tid; i < a.blocks; i += kSelThreads) {
-      const uint32_t key = order_key(sc[i]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+    for (int base = 0; base < a.blocks; base += kPiece) {
+      if (!one) load_keys(sc, base, a.blocks, key);
+#pragma unroll
+      for (int j = 0; j < kSelKeys; ++j)
+        if (key[j] != 0u && (key[j] & mask) == prefix) atomicAdd(&h[(key[j] >> shift) & 255u], 1);
     }
     __syncthreads();
     // the digit at which the count from the top reaches `left`: thread i
     // counts the digits above 255 - i
     int total;
-    const int c = hist[255 - tid];
-    const int above = cta_scan(c, warp_sums, total);
+    const int c = h[255 - tid];
+    const int above = cta_scan(c, warp_sums, turn, total);
     if (above < left && above + c >= left) {
       s_prefix = prefix | (static_cast<uint32_t>(255 - tid) << shift);
       s_left = left - above;
+      s_whole = above + c == left;
     }
     __syncthreads();
     prefix = s_prefix;
     left = s_left;
     mask |= 255u << shift;
-    __syncthreads();
+    if (s_whole) break;  // every key with this prefix is taken
   }
-  // keys above `prefix` all, keys equal to it the first `left`
+  // keys above the prefix all, keys with it the first `left`
   int written = 0, equal_before = 0;
-  for (int base = 0; base < a.blocks; base += kSelThreads) {
-    const int i = base + tid;
-    const uint32_t key = i < a.blocks ? order_key(sc[i]) : 0u;
-    const bool gt = i < a.blocks && key > prefix, eq = i < a.blocks && key == prefix;
+  for (int base = 0; base < a.blocks; base += kPiece) {
+    if (!one) load_keys(sc, base, a.blocks, key);
+    int gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < kSelKeys; ++j) {
+      gt += (key[j] & mask) > prefix;
+      eq += key[j] != 0u && (key[j] & mask) == prefix;
+    }
     int total;
-    // one scan for both counts: at most 256 of each
-    const int both = cta_scan((gt ? 1 : 0) | (eq ? 1 << 16 : 0), warp_sums, total);
-    const int eq_rank = equal_before + (both >> 16);
-    // equal ones written before this thread: those with rank < left
-    const int eq_taken_before = min(eq_rank, left) - min(equal_before, left);
-    const int pos = written + (both & 0xffff) + eq_taken_before;
-    if (gt || (eq && eq_rank < left)) out[pos] = i;
+    ++turn;
+    // one scan for both counts: at most kPiece of each, below 2^16
+    const int both = cta_scan(gt | eq << 16, warp_sums, turn, total);
+    int eq_rank = equal_before + (both >> 16);
+    int pos = written + (both & 0xffff) + min(eq_rank, left) - min(equal_before, left);
+#pragma unroll
+    for (int j = 0; j < kSelKeys; ++j) {
+      const bool above = (key[j] & mask) > prefix;
+      const bool equal = key[j] != 0u && (key[j] & mask) == prefix;
+      if ((above || (equal && eq_rank < left)) && pos < k) out[pos++] = base + kSelKeys * tid + j;
+      if (equal) ++eq_rank;
+    }
     const int eq_total = total >> 16;
     written += (total & 0xffff) + min(equal_before + eq_total, left) - min(equal_before, left);
     equal_before += eq_total;
@@ -430,8 +529,26 @@ int launch_block_summary(const kvq_cache &c, const kvq_summary &sm, int first, i
   return 1;
 }
 
+int launch_block_values(const kvq_cache &c, const kvq_summary &sm, int first, int blocks,
+                        float *values, const KernelCtl &ctl, cudaStream_t s) {
+  SummaryArgs a = {};
+  a.codes = sm.codes;
+  a.scales = sm.scales;
+  a.D = c.head_dim;
+  a.first = first;
+  a.blocks = blocks;
+  a.cap = sm.cap_blocks;
+  a.units = static_cast<long>(c.batch) * c.kv_heads;
+  a.ctl = ctl;
+  const int rows = kValThreads / (a.D / 4) * kValRows;
+  const dim3 grid(static_cast<unsigned>((blocks - first + rows - 1) / rows),
+                  static_cast<unsigned>(std::min<long>(a.units, 65535)));
+  launch_dependent(values_kernel, grid, dim3(kValThreads), 0, s, a, values);
+  return 1;
+}
+
 size_t select_workspace_bytes(const kvq_cache &c, int blocks, int n_q) {
-  return sizeof(float) * static_cast<size_t>(c.batch) * c.kv_heads * n_q * blocks;
+  return sizeof(float) * static_cast<size_t>(c.batch) * c.kv_heads * n_q * ((blocks + 3) / 4 * 4);
 }
 
 int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, const void *q,
@@ -451,15 +568,18 @@ int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, 
   a.top_k = top_k;
   a.sink = n_sink;
   a.scores = static_cast<float *>(ws);
+  a.stride = (blocks + 3) / 4 * 4;
   a.selected = selected;
   a.ctl = ctl;
   const unsigned units = static_cast<unsigned>(c.batch) * c.kv_heads * n_q;
   int launches = 0;
   if (blocks > top_k) {
     const size_t smem = static_cast<size_t>((a.G + 7) / 8 * 8) * a.D;
-    launch_dependent(block_scores_kernel,
-                     dim3((blocks + kScoreThreads - 1) / kScoreThreads, units),
-                     dim3(kScoreThreads), smem, s, a);
+    const dim3 grid((blocks + kScoreThreads - 1) / kScoreThreads, units);
+    if (a.D == 128)
+      launch_dependent(block_scores_kernel<true>, grid, dim3(kScoreThreads), smem, s, a);
+    else
+      launch_dependent(block_scores_kernel<false>, grid, dim3(kScoreThreads), smem, s, a);
     ++launches;
   }
   launch_dependent(select_kernel, dim3(units), dim3(kSelThreads), 0, s, a);

@@ -764,6 +764,35 @@ kvq_status kv_block_summary(const kvq_cache *cache, const kvq_summary *summary,
   return finish(n, "block_summary");
 }
 
+kvq_status kv_block_values(const kvq_cache *cache, const kvq_summary *summary,
+                           int32_t first_block, float *values, int32_t *dev_status,
+                           kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  st = check_summary(cache, summary);
+  if (st != KVQ_OK) return st;
+  if (first_block < 0) return KVQ_ERR_ARG;
+  if (dev_status && !aligned16(dev_status)) return KVQ_ERR_ALIGN;
+  const int blocks = summary_blocks(*cache, summary->block);
+  if (first_block >= blocks) {
+    g_last_launches = 0;
+    g_last_path = "block_values";
+    return KVQ_OK;
+  }
+  if (!values) return KVQ_ERR_ARG;
+  if (!aligned16(values)) return KVQ_ERR_ALIGN;
+  if (static_cast<long>(cache->batch) * cache->kv_heads * blocks > 0x7fffffffL)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  ctl_add_summary(ctl, *cache, *summary);
+  ctl_add(ctl, values,
+          rows_bytes(static_cast<long>(cache->batch) * cache->kv_heads * (blocks - first_block),
+                     cache->head_dim, KVQ_F32));
+  const int n = kvq::launch_block_values(*cache, *summary, first_block, blocks, values, ctl,
+                                         reinterpret_cast<cudaStream_t>(stream));
+  return finish(n, "block_values");
+}
+
 kvq_status kv_select_blocks(const kvq_cache *cache, const kvq_summary *summary, const void *q,
                             int32_t q_dtype, int32_t q_heads, int32_t n_q, int32_t top_k,
                             int32_t n_sink, int32_t *selected, void *workspace, size_t *ws_bytes,

@@ -158,6 +158,8 @@ int launch_block_rows(const kvq_cache &c, const void *q, int q_dtype, int Hq, in
 // block_select.cu: block summaries [first, blocks) and the choice of blocks.
 int launch_block_summary(const kvq_cache &c, const kvq_summary &sm, int first, int blocks,
                          const KernelCtl &ctl, cudaStream_t s);
+int launch_block_values(const kvq_cache &c, const kvq_summary &sm, int first, int blocks,
+                        float *values, const KernelCtl &ctl, cudaStream_t s);
 size_t select_workspace_bytes(const kvq_cache &c, int blocks, int n_q);
 int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, const void *q,
                          int q_dtype, int Hq, int n_q, int top_k, int n_sink, int32_t *selected,

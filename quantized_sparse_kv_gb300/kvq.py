@@ -122,6 +122,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     sp = ctypes.POINTER(KvqSummary)
     lib.kv_block_summary.argtypes = [cp, sp, i32, vp, vp]
     lib.kv_block_summary.restype = i32
+    lib.kv_block_values.argtypes = [cp, sp, i32, vp, vp, vp]
+    lib.kv_block_values.restype = i32
     lib.kv_select_blocks.argtypes = [cp, sp, vp, i32, i32, i32, i32, i32, vp, vp,
                                      ctypes.POINTER(sz), vp, vp]
     lib.kv_select_blocks.restype = i32
@@ -775,8 +777,12 @@ class BlockSummary:
 
     def values(self, first: int = 0) -> torch.Tensor:
         """The mean keys the codes stand for, fp32 (batch, kv_heads, blocks - first, D)."""
-        n = self.blocks
-        return self.codes[:, :, first:n] * self.scales[:, :, first:n].unsqueeze(-1)
+        c = self.cache
+        out = torch.empty((c.batch, c.kv_heads, max(0, self.blocks - first), c.head_dim),
+                          dtype=torch.float32, device=self.codes.device)
+        _check(self.lib.kv_block_values(c.ref, self.ref, int(first), _ptr(out), None, _stream()),
+               "kv_block_values")
+        return out
 
 
 class AttendBlocks:

@@ -38,11 +38,19 @@ def test_refusals(kvq):  # noqa: F811
     assert build(summary(codes=ctypes.c_void_p((1 << 20) + 8))) == 2
     assert build(summary(), first=-1) == 1
 
+    def values(s, first=0, out=ADDR):
+        return lib.kv_block_values(ctypes.byref(c), ctypes.byref(s) if s else None, first, out,
+                                   None, None)
+    assert values(summary(), first=15, out=None) == 0 and lib.kvq_last_launch_count() == 0
+    assert values(None) == 1 and values(summary(), first=-1) == 1
+    assert values(summary(), out=None) == 1
+    assert values(summary(), out=ctypes.c_void_p((1 << 20) + 4)) == 2
+
     def select(cc=c, hq=16, nq=1, top=4, sink=1, dt=1, ws=None, size=sz, sel=ADDR, q=ADDR):
         return lib.kv_select_blocks(ctypes.byref(cc), ctypes.byref(summary()), q, dt, hq, nq, top,
                                     sink, sel, ws, ctypes.byref(size) if size is not None else None,
                                     None, None)
-    assert select() == 0 and sz.value == 4 * 2 * 15
+    assert select() == 0 and sz.value == 4 * 2 * 16  # rows padded to four scores
     assert select(top=15) == 0 and sz.value == 0          # every block: nothing to score
     for kw in (dict(top=0), dict(sink=-1), dict(sink=5), dict(hq=3), dict(nq=0), dict(dt=2),
                dict(size=None)):
