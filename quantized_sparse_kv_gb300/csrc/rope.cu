@@ -24,6 +24,7 @@ namespace kvq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeHeads = 3;  // heads a thread has in flight
 
 struct RopeArgs {
   RopeTensors t;
@@ -36,15 +37,30 @@ struct RopeArgs {
   KernelCtl ctl;
 };
 
-// Eight elements as floats, and back.
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Eight elements of a row, as loaded and as floats.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 w;
+};
+__device__ __forceinline__ void load8(const float *p, Raw8<float> &r) {
+  r.a = *reinterpret_cast<const float4 *>(p);
+  r.b = *reinterpret_cast<const float4 *>(p + 4);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, Raw8<__nv_bfloat16> &r) {
+  r.w = *reinterpret_cast<const uint4 *>(p);
+}
+__device__ __forceinline__ void to_floats(const Raw8<float> &r, float (&x)[8]) {
+  x[0] = r.a.x, x[1] = r.a.y, x[2] = r.a.z, x[3] = r.a.w;
+  x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
+}
+__device__ __forceinline__ void to_floats(const Raw8<__nv_bfloat16> &r, float (&x)[8]) {
+  const uint32_t u[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
@@ -103,6 +119,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   const int half = a.rot / 2;
   const int d0 = kHalf ? (u < a.rot / 16 ? 8 * u : a.rot + 8 * (u - a.rot / 16)) : 8 * u;
   const bool pairs = kHalf ? u < a.rot / 16 : d0 < a.rot;
+  // Heads go kRopeHeads at a time, all loads of a batch in flight together; the
+  // first batch's are issued before the sines and cosines are made.
+  Raw8<T> rx[kRopeHeads], ry[kHalf ? kRopeHeads : 1];
+  T *out[kRopeHeads];
+  bool turn[kRopeHeads];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int k = 0; k < kRopeHeads; ++k, h += a.splits) {
+      out[k] = nullptr;
+      if (h >= a.t.total_heads) continue;
+      const T *in;
+      head_ptrs(a, h, b, t, in, out[k], turn[k]);
+      if (!in_bounds(a.ctl, in, a.D * sizeof(T)) || !in_bounds(a.ctl, out[k], a.D * sizeof(T))) {
+        out[k] = nullptr;
+        continue;
+      }
+      load8(in + d0, rx[k]);
+      if (kHalf && pairs) load8(in + d0 + half, ry[kHalf ? k : 0]);
+    }
+  };
+  load(h0);
   float c[kPairs], s[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
@@ -111,33 +148,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     const int p = kHalf ? d0 + i : d0 / 2 + i;
     if (pairs && p < half && in_bounds(a.ctl, a.turns + p, 8)) phase_cs(a, p, pos, c[i], s[i]);
   }
-#pragma unroll 2
-  for (int h = h0; h < a.t.total_heads; h += a.splits) {
-    const T *in;
-    T *out;
-    bool rotate;
-    head_ptrs(a, h, b, t, in, out, rotate);
-    if (!in_bounds(a.ctl, in, a.D * sizeof(T)) || !in_bounds(a.ctl, out, a.D * sizeof(T))) continue;
-    float x[8], y[8];
-    load8(in + d0, x);
-    if (kHalf) {
-      if (!pairs) {
-        store8(out + d0, x);
-        continue;
-      }
-      load8(in + d0 + half, y);
-      if (rotate) {
+#pragma unroll 1
+  for (int h = h0;;) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x0 = x[i], x1 = y[i];
-          x[i] = x0 * c[i % kPairs] - x1 * s[i % kPairs];
-          y[i] = x0 * s[i % kPairs] + x1 * c[i % kPairs];
+    for (int k = 0; k < kRopeHeads; ++k) {
+      if (!out[k]) continue;
+      float x[8], y[8];
+      to_floats(rx[k], x);
+      if (kHalf && pairs) {
+        to_floats(ry[kHalf ? k : 0], y);
+        if (turn[k]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x0 = x[i], x1 = y[i];
+            x[i] = x0 * c[i % kPairs] - x1 * s[i % kPairs];
+            y[i] = x0 * s[i % kPairs] + x1 * c[i % kPairs];
+          }
         }
-      }
-      store8(out + d0, x);
-      store8(out + d0 + half, y);
-    } else {
-      if (rotate && pairs) {
+        store8(out[k] + d0 + half, y);
+      } else if (!kHalf && pairs && turn[k]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x0 = x[2 * i], x1 = x[2 * i + 1];
@@ -147,8 +176,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
           }
         }
       }
-      store8(out + d0, x);
+      store8(out[k] + d0, x);
     }
+    h += kRopeHeads * a.splits;
+    if (h >= a.t.total_heads) break;
+    load(h);
   }
 }
 

@@ -182,6 +182,37 @@ def _stream() -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _one_device(*tensors) -> torch.device:
+    """The CUDA device all the tensors (None left out) live on."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError("all tensors must live on one CUDA device")
+    return next(iter(devs))
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+class _Prepared:
+    """Base of the prepared calls below: ``run()`` issues them on the current
+    stream of their tensors' device, with the arguments marshalled once (a
+    decoding step is bound by the host as much as by the GPU)."""
+
+    def run(self, *args, **kw):
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._run(*args, **kw)
+        return self._run(*args, **kw)
+
+    def _raw_stream(self) -> int:
+        # the handle without the Stream object around it, about 2 us a call cheaper
+        return _current_raw_stream(self.device.index)
+
+    def launches(self) -> int:
+        return int(self.lib.kvq_last_launch_count())
+
+
 def _ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() else None)
 
@@ -604,7 +635,7 @@ def _rope_view(copies: list, x: torch.Tensor) -> torch.Tensor:
     return x if ok else _static(copies, x)
 
 
-class Rope:
+class Rope(_Prepared):
     """A prepared kv_rope call: q (batch, heads, n, D) and optionally k of the
     same batch, n and D, at any strides (views of a projection's rows are read
     in place when their rows start on 16 bytes); ``v`` is only copied to the
@@ -616,6 +647,7 @@ class Rope:
         self.lib = load_library()
         self.plan, self.inverse = plan, int(bool(inverse))
         src = [x for x in (q, k, v) if x is not None]
+        self.device = _one_device(plan.turns, positions, *src, *(out or ()))
         if any(x.dim() != 4 or x.dtype != q.dtype for x in src):
             raise TypeError("q, k and v must be (batch, heads, n, D) of one type")
         if q.dtype not in (torch.float32, torch.bfloat16):
@@ -645,18 +677,14 @@ class Rope:
                                    0 if v is not None and i == len(src) - 1 else 1,
                                    st[0], st[1], st[2])
         self.arr = arr
+        self._args = (arr, len(src), self.dt, b, n, d, plan.rotary_dim, plan.layout,
+                      _ptr(plan.turns), plan.amplitude, self.inverse, _ptr(self.positions), None)
 
-    def run(self):
-        _refresh(self._copies)
-        st = self.lib.kv_rope(self.arr, len(self.src), self.dt, self.b, self.n, self.d,
-                              self.plan.rotary_dim, self.plan.layout, _ptr(self.plan.turns),
-                              self.plan.amplitude, self.inverse, _ptr(self.positions), None,
-                              _stream())
-        _check(st, "kv_rope")
+    def _run(self):
+        if self._copies:
+            _refresh(self._copies)
+        _check(self.lib.kv_rope(*self._args, self._raw_stream()), "kv_rope")
         return self.out
-
-    def launches(self) -> int:
-        return int(self.lib.kvq_last_launch_count())
 
 
 def rope(plan: RopePlan, q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
@@ -667,7 +695,7 @@ def rope(plan: RopePlan, q: torch.Tensor, k: torch.Tensor | None, positions: tor
 
 
 # ------------------------------------------------------------------ drafted tokens
-class AttendTree:
+class AttendTree(_Prepared):
     """A prepared kv_attend_tree call (see Attend): q (batch, q_heads, T, D),
     k_tree, v_tree (batch, kv_heads, T, D) of the drafted tokens, parents
     (batch, T): the drafted token a token follows, -1 for the cache's last
@@ -678,6 +706,7 @@ class AttendTree:
                  out_dtype=None, out=None):
         self.lib = load_library()
         self.cache = cache
+        self.device = _one_device(cache.k_scales, q, k_tree, v_tree, parents, out)
         self._copies = []
         self.q, self.k, self.v = (_static(self._copies, x) for x in (q, k_tree, v_tree))
         if self.q.dtype not in (torch.float32, torch.bfloat16):
@@ -707,35 +736,33 @@ class AttendTree:
         self.status = new_status(self.q.device)
         self.ws = None
         self._reserve()
-        self.path = None
 
     def _reserve(self):
         """Workspace for the cache's present length (it grows with appends)."""
+        args = (self.cache.ref, _ptr(self.q), self.q_dt, self.hq, self.t, _ptr(self.k),
+                _ptr(self.v), self.t_dt, _ptr(self.parents), self.sm_scale, _ptr(self.out),
+                self.out_dt)
         need = ctypes.c_size_t(0)
-        self._call(None, need)
+        with torch.cuda.device(self.device):
+            _check(self.lib.kv_attend_tree(*args, None, ctypes.byref(need), None, None),
+                   "kv_attend_tree")
         self._n = self.cache.n_tokens
         if self.ws is None or int(need.value) > self.ws.numel():
             self.ws = torch.empty(max(int(need.value), 256), dtype=torch.uint8,
                                   device=self.q.device)
-            self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+        self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+        self._args = (*args, _ptr(self.ws), ctypes.byref(self.ws_bytes), _ptr(self.status))
+        self.path = None
 
-    def _call(self, ws, ws_bytes):
-        st = self.lib.kv_attend_tree(self.cache.ref, _ptr(self.q), self.q_dt, self.hq, self.t,
-                                     _ptr(self.k), _ptr(self.v), self.t_dt, _ptr(self.parents),
-                                     self.sm_scale, _ptr(self.out), self.out_dt, ws,
-                                     ctypes.byref(ws_bytes), _ptr(self.status), _stream())
-        _check(st, "kv_attend_tree")
-
-    def run(self) -> torch.Tensor:
+    def _run(self) -> torch.Tensor:
         if self.cache.n_tokens != self._n:
             self._reserve()
-        _refresh(self._copies)
-        self._call(_ptr(self.ws), self.ws_bytes)
-        self.path = self.lib.kvq_last_path().decode()
+        if self._copies:
+            _refresh(self._copies)
+        _check(self.lib.kv_attend_tree(*self._args, self._raw_stream()), "kv_attend_tree")
+        if self.path is None:
+            self.path = self.lib.kvq_last_path().decode()
         return self.out
-
-    def launches(self) -> int:
-        return int(self.lib.kvq_last_launch_count())
 
 
 def attend_tree(cache: PackedCache, q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor,
@@ -747,7 +774,7 @@ def attend_tree(cache: PackedCache, q: torch.Tensor, k_tree: torch.Tensor, v_tre
 
 
 # ------------------------------------------------------------------ block-sparse attention
-class BlockSummary:
+class BlockSummary(_Prepared):
     """int8 mean keys of the blocks of ``block`` tokens of a cache's int4 part
     (kv_block_summary), with room for the blocks the cache can grow to."""
 
@@ -758,7 +785,7 @@ class BlockSummary:
         self.cache, self.block = cache, block
         groups = cache.reserve[0] or cache.gk
         self.cap_blocks = -(-groups * 32 // block)
-        dev = cache.k_codes.device
+        self.device = dev = _one_device(cache.k_scales)
         b, h, d = cache.batch, cache.kv_heads, cache.head_dim
         self.codes = torch.empty((b, h, self.cap_blocks, d), dtype=torch.int8, device=dev)
         self.scales = torch.empty((b, h, self.cap_blocks), dtype=torch.float32, device=dev)
@@ -771,21 +798,27 @@ class BlockSummary:
 
     def update(self, first: int = 0) -> "BlockSummary":
         """Recompute the blocks from ``first`` on (all of them by default)."""
-        _check(self.lib.kv_block_summary(self.cache.ref, self.ref, int(first), None, _stream()),
-               "kv_block_summary")
+        self.run("update", first)
         return self
 
     def values(self, first: int = 0) -> torch.Tensor:
         """The mean keys the codes stand for, fp32 (batch, kv_heads, blocks - first, D)."""
+        return self.run("values", first)
+
+    def _run(self, what: str, first: int):
         c = self.cache
+        if what == "update":
+            _check(self.lib.kv_block_summary(c.ref, self.ref, first, None, self._raw_stream()),
+                   "kv_block_summary")
+            return None
         out = torch.empty((c.batch, c.kv_heads, max(0, self.blocks - first), c.head_dim),
-                          dtype=torch.float32, device=self.codes.device)
-        _check(self.lib.kv_block_values(c.ref, self.ref, int(first), _ptr(out), None, _stream()),
-               "kv_block_values")
+                          dtype=torch.float32, device=self.device)
+        _check(self.lib.kv_block_values(c.ref, self.ref, first, _ptr(out), None,
+                                        self._raw_stream()), "kv_block_values")
         return out
 
 
-class AttendBlocks:
+class AttendBlocks(_Prepared):
     """A prepared pair of calls, kv_select_blocks and kv_attend_blocks: each
     query token of a KV head attends the ``top_k`` blocks its summary scores
     highest and the whole window. ``selected`` (batch, kv_heads, n_q, top_k)
@@ -797,6 +830,7 @@ class AttendBlocks:
                  selected: torch.Tensor | None = None, block: int | None = None):
         self.lib = load_library()
         self.cache, self.summary = cache, summary
+        self.device = _one_device(cache.k_scales, q, out, selected)
         self._copies = []
         self.q = _static(self._copies, q)
         if self.q.dtype not in (torch.float32, torch.bfloat16):
@@ -828,44 +862,44 @@ class AttendBlocks:
         self.status = new_status(self.q.device)
         self.ws = None
         self._reserve()
-        self.path = None
 
     def _reserve(self):
         """Workspace for the cache's present length (it grows with appends)."""
+        select = None
         need = ctypes.c_size_t(0)
-        self._attend(None, need)
-        most = int(need.value)
-        if self.summary is not None:
-            self._select(None, need)
-            most = max(most, int(need.value))
+        attend = (self.cache.ref, _ptr(self.q), self.q_dt, self.hq, self.nq, _ptr(self.selected),
+                  self.top_k, self.block, self.sm_scale, _ptr(self.out), self.out_dt)
+        with torch.cuda.device(self.device):
+            _check(self.lib.kv_attend_blocks(*attend, None, ctypes.byref(need), None, None),
+                   "kv_attend_blocks")
+            most = int(need.value)
+            if self.summary is not None:
+                select = (self.cache.ref, self.summary.ref, _ptr(self.q), self.q_dt, self.hq,
+                          self.nq, self.top_k, self.n_sink, _ptr(self.selected))
+                _check(self.lib.kv_select_blocks(*select, None, ctypes.byref(need), None, None),
+                       "kv_select_blocks")
+                most = max(most, int(need.value))
         self._n = self.cache.n_tokens
         # the calls run one after the other and may share their workspace
         if self.ws is None or most > self.ws.numel():
             self.ws = torch.empty(max(most, 256), dtype=torch.uint8, device=self.q.device)
-            self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+        self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+        tail = (_ptr(self.ws), ctypes.byref(self.ws_bytes), _ptr(self.status))
+        self._attend_args = (*attend, *tail)
+        self._select_args = (*select, *tail) if select else None
+        self.path = None
 
-    def _select(self, ws, ws_bytes):
-        st = self.lib.kv_select_blocks(self.cache.ref, self.summary.ref, _ptr(self.q), self.q_dt,
-                                       self.hq, self.nq, self.top_k, self.n_sink,
-                                       _ptr(self.selected), ws, ctypes.byref(ws_bytes),
-                                       _ptr(self.status), _stream())
-        _check(st, "kv_select_blocks")
-
-    def _attend(self, ws, ws_bytes):
-        st = self.lib.kv_attend_blocks(self.cache.ref, _ptr(self.q), self.q_dt, self.hq, self.nq,
-                                       _ptr(self.selected), self.top_k, self.block, self.sm_scale,
-                                       _ptr(self.out), self.out_dt, ws, ctypes.byref(ws_bytes),
-                                       _ptr(self.status), _stream())
-        _check(st, "kv_attend_blocks")
-
-    def run(self, select: bool = True) -> torch.Tensor:
+    def _run(self, select: bool = True) -> torch.Tensor:
         if self.cache.n_tokens != self._n:
             self._reserve()
-        _refresh(self._copies)
-        if select and self.summary is not None:
-            self._select(_ptr(self.ws), self.ws_bytes)
-        self._attend(_ptr(self.ws), self.ws_bytes)
-        self.path = self.lib.kvq_last_path().decode()
+        if self._copies:
+            _refresh(self._copies)
+        stream = self._raw_stream()
+        if select and self._select_args:
+            _check(self.lib.kv_select_blocks(*self._select_args, stream), "kv_select_blocks")
+        _check(self.lib.kv_attend_blocks(*self._attend_args, stream), "kv_attend_blocks")
+        if self.path is None:
+            self.path = self.lib.kvq_last_path().decode()
         return self.out
 
 
