@@ -20,19 +20,19 @@
 //   warps 8-11, 12-15  dequantization of K and of V: packed tile -> registers
 //                    (a tile ahead) -> fp16 tile in shared memory,
 //                    128B-swizzled, two stages each;
-//   warps 16-19      the MMAs, a warp per group and half tile (16 also
+//   warps 16-19      the MMAs, a warp per group and score buffer (16 also
 //                    allocates TMEM).
 // Registers move from the other roles to the softmax groups (setmaxnreg).
 // With more than 128 rows in the row block group A takes rows 0-127 and group B
 // rows 128-255 of every tile (each dequantized tile feeds both); with fewer, both
-// work on the same rows and take alternate tiles, so that one exponentiates
-// while the tensor core works for the other; their sums and outputs are merged at
-// the end of the slice. Per group and half tile (64 keys): S = Q K^T (MMA, both
-// operands in shared memory), softmax in registers, P written as fp16 over S in
-// TMEM, O += P V (MMA, A operand from TMEM), and the next S once that MMA has
-// completed. Each step hands over through a barrier, and two such chains per
-// group (four in all) keep the tensor core and the softmax warps busy across
-// those hand-overs.
+// work on the same rows, A on the first and B on the second half of every tile,
+// and their sums and outputs are merged at the end of the slice. A group's step
+// is a half tile (64 keys): S = Q K^T (MMA, both operands in shared memory),
+// softmax in registers, P written as fp16 over S in TMEM, O += P V (MMA, A operand
+// from TMEM). Its steps alternate between two score buffers, each with an MMA warp
+// of its own: S of the step after next is issued once the PV that reads the
+// buffer has completed, so the softmax warps find the next scores ready while
+// the hand-overs of the last step run.
 //
 // Precision: fp16 operands (11 bits; K and V are code * scale), fp32 sums and
 // softmax state. P is taken against the reference, raised when 64 keys' P sum
@@ -85,7 +85,7 @@ struct __align__(1024) TreeSmem {
   uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
   float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
   uint64_t k_full[kStages][2], k_empty[kStages][2], v_full[kStages][2], v_empty[kStages][2];  // [half]
-  uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][half]
+  uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][buffer]
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -533,15 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   } else if (warp >= kSoftWarps + kDqWarps) {
     // ------------------------------------------------ MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    // Warp 16 + 2g + h: half h (64 keys) of group g's tiles.
+    // Warp 16 + 2g + b: buffer b of group g, that is the group's steps b, b + 2, ...
     constexpr uint32_t id_qk = idesc_f16(0, 64), id_pv = idesc_f16(1, 128);
-    const uint32_t g = uniform((warp - (kSoftWarps + kDqWarps)) >> 1), h = uniform(warp & 1);
-    const uint32_t to = uniform(tmem) + 256u * g + 128u, ts = uniform(tmem) + 256u * g + 64u * h;
+    const uint32_t g = uniform((warp - (kSoftWarps + kDqWarps)) >> 1), buf = uniform(warp & 1);
+    const uint32_t to = uniform(tmem) + 256u * g + 128u, ts = uniform(tmem) + 256u * g + 64u * buf;
     const uint32_t q_lo = uniform((smem_u32(sm.q[0]) >> 4) | (1u << 16));   // leading offset 16
-    const uint32_t k_lo = uniform(((smem_u32(sm.k[0]) + 8192u * h) >> 4) | (1u << 16));
-    const uint32_t v_lo = uniform(((smem_u32(sm.v[0]) + 8192u * h) >> 4) | (kHalf >> 4) << 16);
-    const uint32_t s_bar = smem_u32(&sm.s_full[g][h]), p_bar = smem_u32(&sm.p_full[g][h]);
-    const uint32_t o_bar = smem_u32(&sm.o_done[g][h]);
+    const uint32_t k_lo = uniform((smem_u32(sm.k[0]) >> 4) | (1u << 16));
+    const uint32_t v_lo = uniform((smem_u32(sm.v[0]) >> 4) | (kHalf >> 4) << 16);
+    const uint32_t s_bar = smem_u32(&sm.s_full[g][buf]), p_bar = smem_u32(&sm.p_full[g][buf]);
+    const uint32_t o_bar = smem_u32(&sm.o_done[g][buf]);
     uint32_t base_j = 0;  // tiles of the CTA before this segment
     uint32_t seg = 0;
     uint32_t done = 0;    // PV MMAs issued so far
@@ -553,19 +553,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const bool two = uniform(a.rows - row0 > kBM ? 1u : 0u) != 0u;
       const uint32_t qd = q_lo + (two ? g : 0u) * (kTileBytes >> 4);
       if (!spin_wait(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
-      // group g takes tiles 0, 1, 2, ... of the segment (two) or g, g + 2, ...
-      // (shared rows; a half stage's two arrivals then come from one group)
+      // Two groups of rows: step s is half s & 1 of tile s / 2, and each half of a
+      // stage is freed by both groups. Shared rows: step s is half g of tile s,
+      // freed by that group alone, in both arrivals.
       bool first = true;
-      for (int at = two ? 0 : static_cast<int>(g); at < n; at += two ? 1 : 2) {
-        const uint32_t jj = base_j + at, st = uniform(jj % kStages), par = (jj / kStages) & 1;
-        // S: K is there and this half's last PV has read P
+      for (int at = static_cast<int>(buf); at < (two ? 2 * n : n); at += 2) {
+        const uint32_t h = two ? buf : g;
+        const uint32_t jj = base_j + (two ? at >> 1 : at), st = uniform(jj % kStages);
+        const uint32_t par = (jj / kStages) & 1;
+        // S: K is there and this buffer's last PV has read P
         if (!spin_wait(abort_flag, smem_u32(&sm.k_full[st][h]), par, a.ctl) ||
             (!first && !spin_wait(abort_flag, o_bar, (done - 1) & 1, a.ctl))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t kd = k_lo + st * (kTileBytes >> 4);
+        const uint32_t kd = k_lo + st * (kTileBytes >> 4) + h * (8192u >> 4);
         const uint32_t k_bar = smem_u32(&sm.k_empty[st][h]), v_bar = smem_u32(&sm.v_empty[st][h]);
         if (elect_one()) {
 #pragma unroll
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           break;
         }
         tc_fence_after();
-        const uint32_t vd = v_lo + st * (kTileBytes >> 4);
+        const uint32_t vd = v_lo + st * (kTileBytes >> 4) + h * (8192u >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_row = t_s(g) + lane_off, o_row = t_o(g) + lane_off;
-    int pv_seen = 0;  // tiles of this group so far
+    uint32_t used0 = 0, used1 = 0;  // steps of this group so far, by buffer
     bool ok = true;
     uint32_t x = lo;
     for (Segment sg; next_segment(a, x, hi, sg);) {
@@ -733,9 +736,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mbar_arrive(smem_u32(&sm.q_full));
 
       float m = -CUDART_INF_F, l = 0.0f;
-      int mine_tiles = 0;
-      for (int j = two ? 0 : g; j < n; j += two ? 1 : 2, ++mine_tiles) {
-        const int tile = t_lo + j;
+#pragma unroll 1
+      for (int step = 0; step < (two ? 2 * n : n); ++step) {
+        const int buf = step & 1, h = two ? buf : g;
+        const int tile = t_lo + (two ? step >> 1 : step);
+        const uint32_t used = buf ? used1 : used0, used_other = buf ? used0 : used1;
+        if (!warp_wait(abort_flag, smem_u32(&sm.s_full[g][buf]), used & 1, a.ctl)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
         // Keys of the tile this row sees: all of them, else by bits (word c:
         // keys 32c .. 32c + 31): the first ones of the int4 part's last tile;
         // in the tail the window and the row's drafted tokens.
@@ -756,110 +766,100 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           }
           return bits;
         };
-        // ---- P over S, 64 keys at a time (32 words over 64 scores). No maximum
-        // is taken as long as a half's sum of P stays below kSumBound, which
-        // bounds every P of it (fp16 holds 2^15); above that (and for a row's
-        // first keys) the half is redone with its maximum as the new
-        // reference, and O and l follow.
-        float sum = 0.0f;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (!warp_wait(abort_flag, smem_u32(&sm.s_full[g][h]), pv_seen & 1, a.ctl)) {
-            ok = false;
-            break;
+        // ---- P over S (32 words over 64 scores). No maximum is taken as long as
+        // the 64 keys' sum of P stays below kSumBound, which bounds every P of
+        // it (fp16 holds 2^15); above that (and for a row's first keys) the
+        // step is redone with its maximum as the new reference, and O and l
+        // follow.
+        bool with_max = __any_sync(0xffffffffu, m == -CUDART_INF_F);
+        uint32_t p[32];
+        float s;
+        for (;;) {
+          float v[32], w[32];
+          tmem_ld32(s_row + 64u * buf, v);
+          tmem_ld32(s_row + 64u * buf + 32u, w);
+          tmem_wait_ld();
+          reg_fence(v);
+          reg_fence(w);
+          if (!all) {
+            const uint32_t see0 = see_word(2 * h), see1 = see_word(2 * h + 1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              v[e] = see0 >> e & 1u ? v[e] : -CUDART_INF_F;
+              w[e] = see1 >> e & 1u ? w[e] : -CUDART_INF_F;
+            }
           }
-          tc_fence_after();
-          bool with_max = __any_sync(0xffffffffu, m == -CUDART_INF_F);
-          uint32_t p[32];
-          float s;
-          for (;;) {
-            float v[32], w[32];
-            tmem_ld32(s_row + 64u * h, v);
-            tmem_ld32(s_row + 64u * h + 32u, w);
-            tmem_wait_ld();
-            reg_fence(v);
-            reg_fence(w);
-            if (!all) {
-              const uint32_t see0 = see_word(2 * h), see1 = see_word(2 * h + 1);
+          if (with_max) {
+            float mx = -CUDART_INF_F;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                v[e] = see0 >> e & 1u ? v[e] : -CUDART_INF_F;
-                w[e] = see1 >> e & 1u ? w[e] : -CUDART_INF_F;
-              }
-            }
-            if (with_max) {
-              float mx = -CUDART_INF_F;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) mx = fmaxf(fmaxf(mx, v[e]), w[e]);
-              mx *= a.scale_log2;
-              const float f = mx > m ? fast_exp2(m - mx) : 1.0f;
-              m = fmaxf(m, mx);
-              l *= f;
-              sum *= f;
-              // O holds still once the other half's last PV is done (this
-              // half's was before its S was issued)
-              if (h == 1 || pv_seen > 0)
-                ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][h ^ 1]),
-                               (h == 1 ? pv_seen : pv_seen - 1) & 1, a.ctl);
-              if (!ok) break;
-              tc_fence_after();
-              scale_tmem_row(o_row, f);
-            }
-            const float neg_m = m == -CUDART_INF_F ? 0.0f : -m;
-            float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float y0, y1, z0, z1;
-              fma2(y0, y1, v[2 * e], v[2 * e + 1], a.scale_log2, neg_m);
-              fma2(z0, z1, w[2 * e], w[2 * e + 1], a.scale_log2, neg_m);
-              y0 = fast_exp2(y0);
-              y1 = fast_exp2(y1);
-              z0 = fast_exp2(z0);
-              z1 = fast_exp2(z1);
-              add2(s0, s1, y0, y1);
-              add2(s2, s3, z0, z1);
-              p[e] = pack_h2(y0, y1);
-              p[16 + e] = pack_h2(z0, z1);
-            }
-            s = (s0 + s1) + (s2 + s3);
-            if (with_max || !__any_sync(0xffffffffu, !(s <= kSumBound))) break;
-            with_max = true;
+            for (int e = 0; e < 32; ++e) mx = fmaxf(fmaxf(mx, v[e]), w[e]);
+            mx *= a.scale_log2;
+            const float f = mx > m ? fast_exp2(m - mx) : 1.0f;
+            m = fmaxf(m, mx);
+            l *= f;
+            // O holds still once the other buffer's last PV is done (this
+            // one's was before its S was issued)
+            if (used_other > 0)
+              ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][buf ^ 1]), (used_other - 1) & 1,
+                             a.ctl);
+            if (!ok) break;
+            tc_fence_after();
+            scale_tmem_row(o_row, f);
           }
-          if (!ok) break;
-          sum += s;
-          tmem_st32u(s_row + 64u * h, p);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g][h]));
+          const float neg_m = m == -CUDART_INF_F ? 0.0f : -m;
+          float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float y0, y1, z0, z1;
+            fma2(y0, y1, v[2 * e], v[2 * e + 1], a.scale_log2, neg_m);
+            fma2(z0, z1, w[2 * e], w[2 * e + 1], a.scale_log2, neg_m);
+            y0 = fast_exp2(y0);
+            y1 = fast_exp2(y1);
+            z0 = fast_exp2(z0);
+            z1 = fast_exp2(z1);
+            add2(s0, s1, y0, y1);
+            add2(s2, s3, z0, z1);
+            p[e] = pack_h2(y0, y1);
+            p[16 + e] = pack_h2(z0, z1);
+          }
+          s = (s0 + s1) + (s2 + s3);
+          if (with_max || !__any_sync(0xffffffffu, !(s <= kSumBound))) break;
+          with_max = true;
         }
         if (!ok) break;
-        ++pv_seen;
-        l += sum;
+        l += s;
+        tmem_st32u(s_row + 64u * buf, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g][buf]));
+        if (buf)
+          ++used1;
+        else
+          ++used0;
       }
       // (after a wait that ran out: on to the barrier below, where all stop)
-      for (int h = 0; h < 2; ++h)
-        if (ok && mine_tiles > 0 &&
-            !warp_wait(abort_flag, smem_u32(&sm.o_done[g][h]), (pv_seen - 1) & 1, a.ctl))
-          ok = false;
+      if (ok && used0 > 0)
+        ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][0]), (used0 - 1) & 1, a.ctl);
+      if (ok && used1 > 0)
+        ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][1]), (used1 - 1) & 1, a.ctl);
       // ---- write the segment's rows: the output when the slice covers all
       // of the row block's tiles, else a partial
       if (!two) {
-        sm.mm[g][row] = mine_tiles > 0 ? m : -CUDART_INF_F;
-        sm.ml[g][row] = mine_tiles > 0 ? l : 0.0f;
+        sm.mm[g][row] = m;
+        sm.ml[g][row] = l;
       }
       tc_fence_before();
       // both groups' last PV is done and their states are there
       if (soft_sync_any(!ok || cta_aborted(abort_flag))) break;
       tc_fence_after();
       float fa = 1.0f, fb = 0.0f;
-      const bool have_b = !two && n > 1;
       if (!two) {
         const float ma = sm.mm[0][row], mb = sm.mm[1][row];
         m = fmaxf(ma, mb);
         fa = ma == -CUDART_INF_F ? 0.0f : fast_exp2(ma - m);
         fb = mb == -CUDART_INF_F ? 0.0f : fast_exp2(mb - m);
-        l = fa * sm.ml[0][row] + (have_b ? fb * sm.ml[1][row] : 0.0f);
+        l = fa * sm.ml[0][row] + fb * sm.ml[1][row];
       }
       const bool whole = n == a.tiles;
       const float inv = whole ? 1.0f / l : 1.0f;
@@ -890,14 +890,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           reg_fence(v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] *= fa;
-          if (have_b) {
-            float w[32];
-            tmem_ld32(t_o(1) + lane_off + 32u * c, w);
-            tmem_wait_ld();
-            reg_fence(w);
+          float w[32];
+          tmem_ld32(t_o(1) + lane_off + 32u * c, w);
+          tmem_wait_ld();
+          reg_fence(w);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = fmaf(fb, w[e], v[e]);
-          }
+          for (int e = 0; e < 32; ++e) v[e] = fmaf(fb, w[e], v[e]);
         }
         if (!mine) continue;
         // back to natural feature order: column 8k + i holds feature 8k + nat[i]
