@@ -17,9 +17,9 @@
 //
 // Inside a CTA (20 warps):
 //   warps 0-3, 4-7   softmax groups A and B, a thread per query row;
-//   warps 8-11, 12-15  dequantization of K and of V: packed tile -> registers
-//                    (a tile ahead) -> fp16 tile in shared memory,
-//                    128B-swizzled, two stages each;
+//   warps 8-15       dequantization, four of K and four of V: packed tile by bulk
+//                    copies, a tile ahead -> registers -> fp16 tile in
+//                    shared memory, 128B-swizzled, two stages each;
 //   warps 16-19      the MMAs, a warp per group and score buffer (16 also
 //                    allocates TMEM).
 // Registers move from the other roles to the softmax groups (setmaxnreg).
@@ -79,12 +79,14 @@ struct __align__(1024) TreeSmem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kStages][kTileBytes];
   uint8_t v[kStages][kTileBytes];
+  uint8_t raw[2][4][2560];                   // packed part of the next tile of each K and V warp
   int par[KVQ_TREE_MAX];                     // parents of the sequence
   uint32_t seen[KVQ_TREE_MAX][kMaskWords];   // ancestor bits of every drafted token
   uint32_t live[kMaskWords];                 // drafted tokens that exist
   uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
   float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
   uint64_t k_full[kStages][2], k_empty[kStages][2], v_full[kStages][2], v_empty[kStages][2];  // [half]
+  uint64_t raw_full[2][4];
   uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][buffer]
   uint32_t tmem_base;
   int abort_flag;
@@ -252,59 +254,69 @@ __device__ __forceinline__ int cta_of(const TreeArgs &a, long x) {
 // the tile's rows 32 grp .. 32 grp + 31 (one K group), lane (r, cb) the 32
 // features of block cb of rows r, r + 8, r + 16, r + 24 (16 bytes of codes
 // each): a quarter-warp stores eight consecutive rows of one feature block, so
-// its swizzled 16-byte stores meet all banks, and a warp's code loads are 512
-// contiguous bytes.
+// its swizzled 16-byte stores meet all banks.
 struct Raw {
   uint4 c[4];
   float4 s;  // K: scales 4r .. 4r + 3 of the block (eight lanes share theirs); V: one per row
 };
 
-// Where a warp's next tile lies (its lane's first 16 bytes and scale).
+// Where a warp's part of a tile lies.
 struct RawPtr {
   const uint8_t *c;
   const float *s;
 };
 
 template <bool kV>
-__device__ __forceinline__ RawPtr raw_ptr(const TreeArgs &a, long u, int tile, int grp, int r,
-                                          int cb) {
+__device__ __forceinline__ RawPtr raw_ptr(const TreeArgs &a, long u, int tile, int grp) {
   RawPtr p;
   if (kV) {
-    const long row = u * a.Vs + kBN * tile + 32 * grp + r;
-    p.c = a.v_codes + row * 64 + 16 * cb;
-    p.s = a.v_scales + row * 4 + cb;
+    const long row = u * a.Vs + kBN * tile + 32 * grp;
+    p.c = a.v_codes + row * 64;
+    p.s = a.v_scales + row * 4;
   } else {
     const long gi = u * a.Gs + 4 * tile + grp;
-    p.c = a.k_codes + (gi * 32 + r) * 64 + 16 * cb;
-    p.s = a.k_scales + gi * 128 + 32 * cb + 4 * r;
+    p.c = a.k_codes + gi * 2048;
+    p.s = a.k_scales + gi * 128;
   }
   return p;
 }
 
+// Rows of a warp's part of a tile that exist (K: a group is whole, its padding
+// rows hold code 0).
 template <bool kV>
-__device__ __forceinline__ void load_raw(const TreeArgs &a, const RawPtr &p, int tile, int grp,
-                                         int r, Raw &x) {
+__device__ __forceinline__ int raw_rows(const TreeArgs &a, int tile, int grp) {
+  const int left = a.cut - (kBN * tile + 32 * grp);
+  return kV ? max(0, min(32, left)) : left > 0 ? 32 : 0;
+}
+
+// The warp's part of a tile into its raw stage (2 KB codes, 512 B scales): two
+// bulk copies completing on bar (one lane calls).
+template <bool kV>
+__device__ __forceinline__ void fetch_raw(const TreeArgs &a, const RawPtr &p, int rows,
+                                          uint32_t stage, uint32_t bar) {
+  const uint32_t cb = 64u * rows, sb = kV ? 16u * rows : 512u;
+  const bool ok = in_bounds(a.ctl, p.c, cb) && in_bounds(a.ctl, p.s, sb);
+  mbar_arrive_expect_tx(bar, ok ? cb + sb : 0u);
+  if (!ok) return;
+  bulk_g2s(stage, p.c, cb, bar);
+  bulk_g2s(stage + 2048u, p.s, sb, bar);
+}
+
+// The lane's part of the stage to registers.
+template <bool kV>
+__device__ __forceinline__ void take_raw(const uint8_t *stage, int rows, int r, int cb, Raw &x) {
   const uint4 zero = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // code 0
-  if (kV) {
-    float *s = reinterpret_cast<float *>(&x.s);
-    const int left = a.cut - (kBN * tile + 32 * grp + r);  // rows from this lane's first on
+  float *s = reinterpret_cast<float *>(&x.s);
+  const float *sc = reinterpret_cast<const float *>(stage + 2048);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool ok = 8 * i < left && in_bounds(a.ctl, p.c + 512 * i, 16) &&
-                      in_bounds(a.ctl, p.s + 32 * i, 4);
-      x.c[i] = ok ? *reinterpret_cast<const uint4 *>(p.c + 512 * i) : zero;
-      s[i] = ok ? p.s[32 * i] : 0.0f;
-    }
-  } else {
-    const bool have = 4 * tile + grp < a.Gk;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x.c[i] = have && in_bounds(a.ctl, p.c + 512 * i, 16)
-                   ? *reinterpret_cast<const uint4 *>(p.c + 512 * i)
-                   : zero;
-    x.s = have && in_bounds(a.ctl, p.s, 16) ? *reinterpret_cast<const float4 *>(p.s)
-                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = 0; i < 4; ++i) {
+    const bool ok = r + 8 * i < rows;
+    x.c[i] = ok ? *reinterpret_cast<const uint4 *>(stage + (r + 8 * i) * 64 + 16 * cb) : zero;
+    if (kV) s[i] = ok ? sc[(r + 8 * i) * 4 + cb] : 0.0f;
   }
+  if (!kV)
+    x.s = rows > 0 ? *reinterpret_cast<const float4 *>(sc + 32 * cb + 4 * r)
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
 // Eight codes of a word times their scales (pairs in the tiles' feature order).
@@ -426,10 +438,9 @@ __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &s
   }
 }
 
-// One dequantization warp: its rows of every K (or V) tile of the CTA's items, each
-// with codes and scales loaded a tile earlier. (Loading two tiles ahead needs the
-// loop twice; the code of all roles then no longer fits the instruction caches
-// and the call takes half as long again.)
+// One dequantization warp: its rows of every K (or V) tile of the CTA's items. The
+// tile at hand is in registers, the next one in the warp's raw stage or on its
+// way there, so a tile's copy has the time of a whole tile to arrive.
 template <bool kV>
 __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, uint32_t lo,
                                              uint32_t hi, int grp, int lane) {
@@ -437,35 +448,52 @@ __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, ui
   auto unit_of = [&](uint32_t rb) {
     return static_cast<long>(rb / static_cast<uint32_t>(a.row_blocks));
   };
-  // the tile at hand and the one loaded ahead: segment, tile, tiles left
+  // the tile at hand and the one being fetched: segment, tile, tiles left
   Segment cur, ahead;
   uint32_t cur_x = lo, ahead_x = lo;
   bool more = next_segment(a, ahead_x, hi, ahead);
   if (!more) return;
   next_segment(a, cur_x, hi, cur);
-  RawPtr ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp, r, cb);
-  Raw x;
-  auto load = [&]() {
+  RawPtr ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp);
+  uint8_t *const raw = sm.raw[kV ? 1 : 0][grp];
+  const uint32_t raw_bar = smem_u32(&sm.raw_full[kV ? 1 : 0][grp]);
+  uint32_t fetched = 0, taken = 0;  // copies started and used
+  auto fetch = [&]() {  // the tile `ahead` to the raw stage; on to the next
     if (!more) return;
-    if (ahead.t_lo < a.int4_tiles) load_raw<kV>(a, ptr, ahead.t_lo, grp, r, x);
+    const int rows = raw_rows<kV>(a, ahead.t_lo, grp);
+    if (rows > 0) {
+      if (lane == 0) fetch_raw<kV>(a, ptr, rows, smem_u32(raw), raw_bar);
+      ++fetched;
+    }
     ptr.c += 8192;
     ptr.s += 512;
     ++ahead.t_lo;
     if (--ahead.n == 0) {
       more = next_segment(a, ahead_x, hi, ahead);
-      if (more) ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp, r, cb);
+      if (more) ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp);
     }
   };
-  load();
+  Raw x;
+  bool ok = true;
+  fetch();
 #pragma unroll 1
-  for (int j = 0;; ++j) {
+  for (int j = 0; ok; ++j) {
+    const int rows = raw_rows<kV>(a, cur.t_lo, grp);
+    if (rows > 0) {
+      ok = warp_wait(&sm.abort_flag, raw_bar, taken & 1u, a.ctl);
+      if (!ok) break;
+      ++taken;
+    }
+    take_raw<kV>(raw, rows, r, cb, x);
+    __syncwarp();  // the stage has been read
+    fetch();
     const int st = j % kStages;
     uint64_t *empty = kV ? &sm.v_empty[st][grp >> 1] : &sm.k_empty[st][grp >> 1];
     uint64_t *full = kV ? &sm.v_full[st][grp >> 1] : &sm.k_full[st][grp >> 1];
     uint8_t *tile = kV ? sm.v[st] : sm.k[st];
-    if (j >= kStages && !warp_wait(&sm.abort_flag, smem_u32(empty),
-                                   static_cast<uint32_t>((j / kStages - 1) & 1), a.ctl))
-      break;
+    if (j >= kStages) ok = warp_wait(&sm.abort_flag, smem_u32(empty),
+                                     static_cast<uint32_t>((j / kStages - 1) & 1), a.ctl);
+    if (!ok) break;
     if (cur.t_lo < a.int4_tiles)
       store_raw<kV>(x, r, cb, tile + (32 * grp + r) * 128);
     else
@@ -475,10 +503,11 @@ __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, ui
     // (test hook: the keys of a dropped tile never arrive)
     if (lane == 0 && (kV || static_cast<int>(cur.rb) * a.tiles + cur.t_lo != a.ctl.drop_item))
       mbar_arrive(smem_u32(full));
-    load();
     ++cur.t_lo;
     if (--cur.n == 0 && !next_segment(a, cur_x, hi, cur)) break;
   }
+  // a copy still on its way lands before the CTA exits
+  if (fetched != taken) mbar_wait(raw_bar, taken & 1u, 2000000000ull);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
@@ -496,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mbar_init(smem_u32(&sm.k_empty[i >> 1][i & 1]), 2);
       mbar_init(smem_u32(&sm.v_empty[i >> 1][i & 1]), 2);
     }
+    for (int i = 0; i < kDqWarps; ++i) mbar_init(smem_u32(&sm.raw_full[i >> 2][i & 3]), 1);
     mbar_init(smem_u32(&sm.q_full), 2 * kBM);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sm.s_full[i >> 1][i & 1]), 1);
