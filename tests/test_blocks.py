@@ -50,7 +50,7 @@ def test_refusals(kvq):  # noqa: F811
         return lib.kv_select_blocks(ctypes.byref(cc), ctypes.byref(summary()), q, dt, hq, nq, top,
                                     sink, sel, ws, ctypes.byref(size) if size is not None else None,
                                     None, None)
-    assert select() == 0 and sz.value == 4 * 2 * 16  # rows padded to four scores
+    assert select() == 0 and sz.value == 4 * 2 * 16        # score rows padded to four
     assert select(top=15) == 0 and sz.value == 0          # every block: nothing to score
     for kw in (dict(top=0), dict(sink=-1), dict(sink=5), dict(hq=3), dict(nq=0), dict(dt=2),
                dict(size=None)):
@@ -205,6 +205,13 @@ SELECT = [
     (1, 2, 8, 1, 300, 44, 128, 64, 64, 1, torch.bfloat16),    # fewer blocks than top_k
     (1, 2, 8, 1, 60, 60, 128, 64, 3, 1, torch.bfloat16),      # no block at all
     (1, 1, 8, 1, 40000, 0, 96, 32, 256, 3, torch.bfloat16),
+    (1, 1, 8, 2, 40000, 0, 128, 32, 100, 1, torch.bfloat16),   # one piece of keys
+    (1, 2, 4, 1, 131072, 60, 128, 32, 33, 0, torch.bfloat16),
+    (1, 1, 8, 1, 400000, 0, 128, 32, 64, 2, torch.bfloat16),   # several pieces
+    (1, 1, 2, 1, 600000, 0, 128, 32, 40, 1, torch.bfloat16),
+    (1, 1, 9, 1, 8195, 3, 128, 64, 31, 0, torch.bfloat16),
+    (2, 1, 8, 1, 32 * 256, 0, 128, 32, 255, 0, torch.float32),
+    (2, 1, 8, 1, 32 * 257, 0, 128, 32, 256, 0, torch.float32),
 ]
 
 
