@@ -710,9 +710,11 @@ __device__ __forceinline__ void chunk_body(const CUtensorMap &tm_q, const CUtens
                                    sm.p[g], row, cs, psum, racc, v3, mx, set_ref, m_used);
         // A chunk sum bounds each of its P values: chunks 0-2 are checked by
         // their sums, chunk 3 by its raw maximum.
+        // (Sums that pass the bound are +inf at most; a NaN one comes from a NaN
+        // score, which no reference mends, and asks for nothing.)
         const float big = fmaxf(fmaxf(cs[0], cs[1]), cs[2]);
         if (!__any_sync(0xffffffffu,
-                        !(big <= kRedoBound) || mx * a.scale_log2 > m_used + kRedoThreshold))
+                        big > kRedoBound || mx * a.scale_log2 > m_used + kRedoThreshold))
           break;
         // far above the reference for some row (P could overflow): the warp
         // takes the tile maxima now and redoes the tile from its scores, still
