@@ -384,7 +384,8 @@ KVQ_API kvq_status kv_attend_decode_static(const kvq_cache *cache, const void *q
  *           (rotary_dim >= 4).
  *   RAMP    pairs that turn often over the original context keep f_i, pairs
  *           that turn seldom take f_i / factor, linear in i between
- *           floor(x(p0)) and ceil(x(p1)) (clamped to [0, rotary_dim - 1]),
+ *           floor(x(p0)) and ceil(x(p1)) (both clamped to [0, rotary_dim - 1];
+ *           a step behind that pair where they meet),
  *           x(r) = rotary_dim ln(original / (2 pi r)) / (2 ln base) the pair
  *           that makes r turns; the rotation is multiplied by
  *           0.1 ln(factor) + 1.

@@ -292,8 +292,10 @@ bool rope_turns(int rot, double base, const kvq_rope_scaling *sc, uint64_t *turn
     auto pair_of = [&](double t) {
       return r * std::log(sc->original / (kTwoPi * t)) / (2.0 * std::log(b));
     };
-    lo = std::max(0.0, std::floor(pair_of(sc->p0)));
-    hi = std::min(r - 1.0, std::ceil(pair_of(sc->p1)));
+    // (both ends inside the range: a context so long, or so short, that every
+    // pair lies on one side of the ramp must not turn it around)
+    lo = std::min(r - 1.0, std::max(0.0, std::floor(pair_of(sc->p0))));
+    hi = std::min(r - 1.0, std::max(0.0, std::ceil(pair_of(sc->p1))));
     if (hi == lo) hi += 0.001;  // a step instead of a ramp
     *amp = static_cast<float>(0.1 * std::log(sc->factor) + 1.0);
   }

@@ -95,6 +95,29 @@ def test_turns_refusals(kvq):
         kvq.RopePlan(64, layout="other", device="cpu")
 
 
+def test_ramp_outside_the_pairs(kvq):
+    """A ramp that lies past the last pair leaves every frequency alone, one before
+    the first pair scales all but that one (both ends are clamped to the pairs)."""
+    r, base, factor = 64, 10.0, 4.0
+
+    def turns(original):
+        out, amp = (ctypes.c_uint64 * (r // 2))(), ctypes.c_float()
+        sc = kvq.KvqRopeScaling(3, factor, original, 32.0, 1.0)
+        assert kvq.load_library().kvq_rope_turns(r, base, ctypes.byref(sc), out,
+                                                 ctypes.byref(amp)) == 0
+        return [x / 2.0 ** 64 * 2 * math.pi for x in out]
+
+    plain = [base ** (-2.0 * i / r) for i in range(r // 2)]
+    # x(32) = 64 ln(original / 201) / (2 ln 10) is above 63 from about 19,000 on
+    for got, want in zip(turns(1e6), plain):
+        assert abs(got - want) <= 1e-14 * want
+    # x(1) is below 0 up to 6 tokens
+    short = turns(4.0)
+    assert abs(short[0] - plain[0]) <= 1e-14
+    for got, want in zip(short[1:], plain[1:]):
+        assert abs(got - want / factor) <= 1e-14 * want
+
+
 def test_call_refusals(kvq):
     lib = kvq.load_library()
 
