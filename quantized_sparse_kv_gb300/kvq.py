@@ -197,7 +197,9 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 class _Prepared:
     """Base of the prepared calls below: ``run()`` issues them on the current
     stream of their tensors' device, with the arguments marshalled once (a
-    decoding step is bound by the host as much as by the GPU)."""
+    decoding step is bound by the host as much as by the GPU). A prepared call
+    has one workspace: runs that may overlap, on several streams or from
+    captured graphs, each need an object of their own."""
 
     def run(self, *args, **kw):
         if torch.cuda.current_device() != self.device.index:
@@ -211,6 +213,17 @@ class _Prepared:
 
     def launches(self) -> int:
         return int(self.lib.kvq_last_launch_count())
+
+    def _workspace(self, need: int):
+        """Workspace of at least ``need`` bytes. A larger one (the cache grew)
+        takes half as much again as the last, and the last stays: a graph
+        captured before may still be replayed and write to it."""
+        if self.ws is None or need > self.ws.numel():
+            if self.ws is not None:
+                self._kept.append(self.ws)
+                need = max(need, self.ws.numel() * 3 // 2)
+            self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        self.ws_bytes = ctypes.c_size_t(self.ws.numel())
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -734,7 +747,7 @@ class AttendTree(_Prepared):
             raise ValueError("out must be a dense tensor of q's shape")
         self.hq, self.t, self.sm_scale = hq, t, float(sm_scale or 0.0)
         self.status = new_status(self.q.device)
-        self.ws = None
+        self.ws, self._kept = None, []
         self._reserve()
 
     def _reserve(self):
@@ -747,10 +760,7 @@ class AttendTree(_Prepared):
             _check(self.lib.kv_attend_tree(*args, None, ctypes.byref(need), None, None),
                    "kv_attend_tree")
         self._n = self.cache.n_tokens
-        if self.ws is None or int(need.value) > self.ws.numel():
-            self.ws = torch.empty(max(int(need.value), 256), dtype=torch.uint8,
-                                  device=self.q.device)
-        self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+        self._workspace(int(need.value))
         self._args = (*args, _ptr(self.ws), ctypes.byref(self.ws_bytes), _ptr(self.status))
         self.path = None
 
@@ -860,7 +870,7 @@ class AttendBlocks(_Prepared):
             raise ValueError("out must be a dense tensor of q's shape")
         self.hq, self.nq, self.sm_scale = hq, nq, float(sm_scale or 0.0)
         self.status = new_status(self.q.device)
-        self.ws = None
+        self.ws, self._kept = None, []
         self._reserve()
 
     def _reserve(self):
@@ -881,9 +891,7 @@ class AttendBlocks(_Prepared):
                 most = max(most, int(need.value))
         self._n = self.cache.n_tokens
         # the calls run one after the other and may share their workspace
-        if self.ws is None or most > self.ws.numel():
-            self.ws = torch.empty(max(most, 256), dtype=torch.uint8, device=self.q.device)
-        self.ws_bytes = ctypes.c_size_t(self.ws.numel())
+        self._workspace(most)
         tail = (_ptr(self.ws), ctypes.byref(self.ws_bytes), _ptr(self.status))
         self._attend_args = (*attend, *tail)
         self._select_args = (*select, *tail) if select else None

@@ -388,3 +388,26 @@ def test_wait_that_runs_out_is_reported(kvq):
     call.status.zero_()
     assert torch.equal(call.run(), want)
     assert kvq.read_status(call.status) == 0
+
+
+@pytest.mark.gpu
+def test_outgrown_workspace_is_kept_for_captured_graphs(kvq):
+    """A graph captured before the cache grew writes to the workspace of that time."""
+    import weakref
+    b, hq, hkv, t = 2, 16, 2, 8
+    c = make(kvq, b, hkv, 256, 128, 128, reserve=(600, 512))
+    q, kt, vt = inputs(b, hq, hkv, t, 128)
+    par = random_tree(b, t, 3)
+    calls = [kvq.AttendTree(c, q, kt, vt, par),
+             kvq.AttendBlocks(c, q, kvq.BlockSummary(c, 32).update(), 512)]
+    refs = [weakref.ref(a.ws) for a in calls]
+    sizes = [a.ws.numel() for a in calls]
+    new = torch.randn((b, hkv, 320, 128), device="cuda", dtype=torch.bfloat16)
+    for _ in range(50):
+        kvq.append(c, new, new, 128)
+    calls[1].summary.update()
+    for a in calls:
+        a.run()
+    torch.cuda.synchronize()
+    for a, ref, size in zip(calls, refs, sizes):
+        assert a.ws.numel() >= size * 3 // 2 and ref() is not None
