@@ -626,7 +626,9 @@ class RopePlan:
 
 def _static(copies: list, x: torch.Tensor, dtype=None) -> torch.Tensor:
     """x itself when a prepared call can read it in place, else a dense buffer
-    (of ``dtype``) that every run() fills from x again."""
+    (of ``dtype``) that every run() fills from x again. The calls record no
+    gradients, nor do these copies."""
+    x = x.detach()
     y = x.to(dtype or x.dtype).contiguous()
     if y.data_ptr() % 16:
         y = y.clone()

@@ -411,3 +411,27 @@ def test_outgrown_workspace_is_kept_for_captured_graphs(kvq):
     torch.cuda.synchronize()
     for a, ref, size in zip(calls, refs, sizes):
         assert a.ws.numel() >= size * 3 // 2 and ref() is not None
+
+
+@pytest.mark.gpu
+def test_leaves_that_are_copied_record_nothing(kvq):
+    """Inputs a call cannot read in place are copied again each run, without a
+    gradient history that would grow with the runs."""
+    b, hq, hkv, t = 1, 16, 2, 4
+    c = make(kvq, b, hkv, 160, 128, 128)
+    q, kt, vt = inputs(b, hq, hkv, t, 128)
+    par = random_tree(b, t, 3)
+    want = kvq.AttendTree(c, q, kt, vt, par).run()
+    leaf = q.transpose(1, 2).contiguous().requires_grad_()
+    a = kvq.AttendTree(c, leaf.transpose(1, 2), kt, vt, par)
+    s = kvq.AttendBlocks(c, leaf.transpose(1, 2), kvq.BlockSummary(c, 32).update(), 1)
+    wide = torch.zeros((b, 2, 64, 8), device="cuda", requires_grad=True)
+    r = kvq.Rope(kvq.RopePlan(64), wide.transpose(2, 3), None,
+                 torch.zeros((b, 8), device="cuda", dtype=torch.int64))
+    for x in (a, s, r):
+        x.run()
+        assert len(x._copies) > 0 and not any(y.requires_grad for y, _ in x._copies)
+    assert torch.equal(a.out, want)
+    with torch.no_grad():
+        leaf.mul_(0.0)  # the next run reads the leaf's new values
+    assert not torch.equal(a.run(), want)
