@@ -26,7 +26,10 @@
  *    detects are OR-ed as KVQ_DEV_* bits into *dev_status (a device int32 the
  *    caller zeroes beforehand and reads after synchronising); kernels never
  *    trap and every wait in them is bounded.
- *  - sm_scale <= 0 selects 1/sqrt(head_dim). There is no mask.
+ *  - sm_scale <= 0 selects 1/sqrt(head_dim). Only kv_attend_tree masks keys.
+ *  - Calls that may run at the same time (on several streams, or replayed from
+ *    several captured graphs) need a workspace each, and their outputs and a
+ *    summary or list that one of them writes must not overlap.
  *  - head_dim is a multiple of 32 in [32, 256].
  */
 #ifndef KVQ_H
@@ -58,8 +61,10 @@ typedef enum {
 
 /* Bits OR-ed into *dev_status by kernels. */
 enum {
-  KVQ_DEV_INDEX = 1,   /* a candidate index outside [0, n_tokens) (that key is skipped) */
-  KVQ_DEV_DUP = 2,     /* a candidate list holds the same index twice (validate only) */
+  KVQ_DEV_INDEX = 1,   /* a candidate index outside [0, n_tokens), a listed block or a parent
+                          that does not exist (that key, block or row is skipped) */
+  KVQ_DEV_DUP = 2,     /* a candidate list holds the same index twice (validate only), or a
+                          list of blocks does not increase */
   KVQ_DEV_TIMEOUT = 4, /* a bounded wait ran out; the outputs of that launch are invalid */
   KVQ_DEV_BOUNDS = 8   /* an address range a kernel derived lay outside the call's buffers
                           (checked in the KVQ_DEBUG build, kvq_debug_checks); outputs invalid */
@@ -479,7 +484,8 @@ KVQ_API kvq_status kv_rope(const kvq_rope_tensor *tensors, int32_t n_tensors, in
  * scale and the product each rounded once to fp16, 11 bits), q, window and
  * drafted rows converted from bf16 (exact within fp16's normal range, 6e-5 to
  * 65504; larger values, infinite ones too, count as 65504), products and sums
- * in fp32.
+ * in fp32. Scales of the int4 part belong in that range too: smaller ones keep
+ * fewer bits, and 7 * scale above 65504 overflows.
  * Other shapes run an fp32 kernel (q_heads and batch <= 65,535).
  */
 #define KVQ_TREE_MAX 256
@@ -560,8 +566,9 @@ KVQ_API kvq_status kv_select_blocks(const kvq_cache *cache, const kvq_summary *s
  * All query heads of a KV head share a list. An entry outside the blocks
  * (other than -1) is skipped and flagged KVQ_DEV_INDEX; one that does not
  * exceed the entry before it is skipped and flagged KVQ_DEV_DUP (the list's
- * rows are then invalid). Rows with no key at all (no window, an empty list)
- * are zero. q, out, workspace/ws_bytes as kv_attend.
+ * rows are then invalid). Entries past the n_blocks-th are not looked at (a
+ * valid list holds -1 there). Rows with no key at all (no window, an empty
+ * list) are zero. q, out, workspace/ws_bytes as kv_attend.
  * Kernel choice: D = 128, bf16 q, a bf16 window (or none) and at most 8 query
  * heads per KV head run the decode kernels over the listed blocks; other
  * shapes run an fp32 kernel (q_heads and batch <= 65,535).
@@ -576,16 +583,18 @@ KVQ_API kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32
 KVQ_API int32_t kvq_last_launch_count(void);
 
 /* Name of the kernel family the last successful call on this thread used
- * ("pack", "decode", "chunk_bf16", "chunk_mxfp8", "generic", "candidates");
- * a static string. */
+ * ("pack", "decode", "chunk_bf16", "chunk_mxfp8", "generic", "candidates",
+ * "rope", "tree_tensor", "tree_rows", "block_summary", "block_values",
+ * "select_blocks", "blocks_decode", "blocks_rows", ...); a static string. */
 KVQ_API const char *kvq_last_path(void);
 
 /*
  * Test hook: bound every mbarrier wait of the next launches on this thread to
  * `wait_limit_ns` nanoseconds (0 restores the default of one second), and,
- * when drop_item >= 0, make the loader of the decode kernel and of the bf16
- * kv_pack kernel skip the copy of that work item so that the wait on it can
- * only run out. Used by the failure tests.
+ * when drop_item >= 0, make the loader of the decode kernel (over listed
+ * blocks too) and of the bf16 kv_pack kernel skip the copy of that work item,
+ * and the tree kernel withhold the keys of that one (row block * tiles + tile),
+ * so that the wait on it can only run out. Used by the failure tests.
  */
 KVQ_API void kvq_debug_set(uint32_t wait_limit_ns, int32_t drop_item);
 

@@ -179,7 +179,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a) 
   if (!kTree) {
     list = a.selected + (u * a.n_q + i) * a.top_k;
     per_block = a.block / 32;
-    list_chunks = in_bounds(a.ctl, list, sizeof(int32_t) * a.top_k) ? a.top_k * per_block : 0;
+    // (increasing blocks: a list's entries past the n_blocks-th hold none)
+    const int ents = min(a.top_k, a.n_blocks);
+    list_chunks = in_bounds(a.ctl, list, sizeof(int32_t) * a.top_k) ? ents * per_block : 0;
   }
   const int cache_chunks = kTree ? (a.N + 31) / 32 : list_chunks;
   const int tail_keys = kTree ? i + 1 : a.R;  // a drafted token sees none after itself

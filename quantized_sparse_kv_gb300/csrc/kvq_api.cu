@@ -849,8 +849,6 @@ kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32_t q_dty
   const int sms = sm_count();
   const bool decode = kvq::blocks_decode_supported(*cache, q_dtype, q_heads, n_q, top_k, block);
   if (!decode && (q_heads > 65535 || cache->batch > 65535)) return KVQ_ERR_UNSUPPORTED;
-  // the fp32 kernel counts a list's 32-token groups in 32 bits
-  if (!decode && static_cast<long>(top_k) * (block / 32) > (1L << 30)) return KVQ_ERR_UNSUPPORTED;
   const size_t need =
       decode ? kvq::blocks_decode_workspace_bytes(*cache, n_q, top_k, block, sms) : 0;
   if (!workspace) {

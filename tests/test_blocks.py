@@ -73,6 +73,7 @@ def test_refusals(kvq):  # noqa: F811
     assert attend(ws=ADDR, size=big, sel=None) == 1
     assert attend(ws=ADDR, size=ctypes.c_size_t(8)) == 4
     assert attend(hq=131072, dt=0) == 3
+    assert attend(top=0x7fffffff, dt=0) == 0 and attend(top=0x7fffffff) == 0
 
 
 def test_binding_refusals(kvq):  # noqa: F811
@@ -320,6 +321,10 @@ def test_lists_of_the_caller(kvq, dt):  # noqa: F811
     out, st = run([[0, -1, 3], [4, 5, 6]])                  # an entry behind the end
     assert st == kvq.DEV_INDEX
     assert rel(out, want([[0, -1, -1], [4, 5, 6]])) <= tol
+    # entries past the tenth (as many as there are blocks) are not looked at
+    long = list(range(10)) + [99, 3]
+    out, st = run([long, long])
+    assert st == 0 and rel(out, want([long[:10] + [-1, -1]] * 2)) <= tol
     # the same index twice, or a list that is not increasing
     for rows in ([[3, 3, -1], [4, 5, 6]], [[5, 3, -1], [4, 5, 6]]):
         _, st = run(rows)
