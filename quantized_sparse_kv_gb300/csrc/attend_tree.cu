@@ -17,9 +17,9 @@
 //
 // Inside a CTA (20 warps):
 //   warps 0-3, 4-7   softmax groups A and B, a thread per query row;
-//   warps 8-15       dequantization, four of K and four of V: packed tile by bulk
-//                    copies, a tile ahead -> registers -> fp16 tile in
-//                    shared memory, 128B-swizzled, two stages each;
+//   warps 8-15       dequantization, four of K and four of V: packed tile ->
+//                    registers (a tile ahead) -> fp16 tile in shared
+//                    memory, 128B-swizzled, two stages each;
 //   warps 16-19      the MMAs, a warp per group and score buffer (16 also
 //                    allocates TMEM).
 // Registers move from the other roles to the softmax groups (setmaxnreg).
@@ -67,9 +67,10 @@ constexpr uint32_t kHalf = 128u * 128u;      // 16 KB: 128 rows x 64 fp16 featur
 constexpr uint32_t kTileBytes = 2u * kHalf;
 constexpr int kStages = 2;                   // K and V tiles in shared memory, each
 constexpr int kMaskWords = KVQ_TREE_MAX / 32;
-// Tiles' worth of time that starting and ending one more row block takes (12 us
-// against 1.9 us a tile of two groups, 1 us a tile of shared rows).
-constexpr int kLeadTwo = 6, kLeadShared = 10;
+// Tiles' worth of time that starting a row block takes (queries, masks, first
+// scores) and that ending one does (the tail's slower tiles, the output), with two
+// groups of rows and with shared ones (a tile takes 1.8 us, or 1.1 us).
+constexpr int kLeadTwo = 5, kLeadShared = 4, kTrail = 2;
 constexpr float kSumBound = 4096.0f;         // sum of 64 P above which the reference is raised
 // A partial: O of 256 rows as [32 pieces][256 rows] float4 (a warp's store is
 // consecutive rows of one piece), then (m, l) of the rows.
@@ -79,14 +80,12 @@ struct __align__(1024) TreeSmem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kStages][kTileBytes];
   uint8_t v[kStages][kTileBytes];
-  uint8_t raw[2][4][2560];                   // packed part of the next tile of each K and V warp
   int par[KVQ_TREE_MAX];                     // parents of the sequence
   uint32_t seen[KVQ_TREE_MAX][kMaskWords];   // ancestor bits of every drafted token
   uint32_t live[kMaskWords];                 // drafted tokens that exist
   uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
   float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
   uint64_t k_full[kStages][2], k_empty[kStages][2], v_full[kStages][2], v_empty[kStages][2];  // [half]
-  uint64_t raw_full[2][4];
   uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][buffer]
   uint32_t tmem_base;
   int abort_flag;
@@ -104,10 +103,10 @@ struct TreeArgs {
   int Hkv, G, T, R, cut, Gk, Gs, Vs, Ws;
   int rows, row_blocks;                 // T * G, and per unit
   int int4_tiles, tiles;                // key tiles per unit
-  // Items are laid out as if every row block began with `lead` more tiles (the
-  // time its queries, masks and output take), so that slices that begin a row
-  // block get fewer tiles.
-  int lead, span;                       // span = lead + tiles
+  // Items are laid out as if every row block had `lead` more tiles before its
+  // first and some behind its last (the time its queries, masks, tail and
+  // output take), so that slices that begin or end a row block get fewer tiles.
+  int lead, span;                       // span = lead + tiles + those behind
   long items;                           // units * row_blocks * span
   int ctas, slots;                      // slots: partials reserved per row block
   float scale_log2;
@@ -219,8 +218,8 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
   return (c >> 3) * kHalf + swz(r, c & 7u);
 }
 
-// Slice of CTA c: items [items * c / ctas, items * (c + 1) / ctas), moved to the
-// first tile of a row block where it begins in the lead of one.
+// Slice of CTA c: items [items * c / ctas, items * (c + 1) / ctas), of which the
+// ones before a row block's first tile and behind its last are no work.
 __device__ __forceinline__ uint32_t slice_lo(const TreeArgs &a, int c) {
   return static_cast<uint32_t>(a.items * c / a.ctas);
 }
@@ -238,7 +237,7 @@ __device__ __forceinline__ bool next_segment(const TreeArgs &a, uint32_t &x, uin
     const uint32_t start = s.rb * a.span, end = min(start + a.span, hi);
     const int lo = max(0, static_cast<int>(x - start) - a.lead);
     s.t_lo = lo;
-    s.n = static_cast<int>(end - start) - a.lead - lo;
+    s.n = min(static_cast<int>(end - start) - a.lead, a.tiles) - lo;
     x = end;
     if (s.n > 0) return true;
   }
@@ -260,63 +259,52 @@ struct Raw {
   float4 s;  // K: scales 4r .. 4r + 3 of the block (eight lanes share theirs); V: one per row
 };
 
-// Where a warp's part of a tile lies.
+// Where a warp's next tile lies (its lane's first 16 bytes and scale).
 struct RawPtr {
   const uint8_t *c;
   const float *s;
 };
 
 template <bool kV>
-__device__ __forceinline__ RawPtr raw_ptr(const TreeArgs &a, long u, int tile, int grp) {
+__device__ __forceinline__ RawPtr raw_ptr(const TreeArgs &a, long u, int tile, int grp, int r,
+                                          int cb) {
   RawPtr p;
   if (kV) {
-    const long row = u * a.Vs + kBN * tile + 32 * grp;
-    p.c = a.v_codes + row * 64;
-    p.s = a.v_scales + row * 4;
+    const long row = u * a.Vs + kBN * tile + 32 * grp + r;
+    p.c = a.v_codes + row * 64 + 16 * cb;
+    p.s = a.v_scales + row * 4 + cb;
   } else {
     const long gi = u * a.Gs + 4 * tile + grp;
-    p.c = a.k_codes + gi * 2048;
-    p.s = a.k_scales + gi * 128;
+    p.c = a.k_codes + (gi * 32 + r) * 64 + 16 * cb;
+    p.s = a.k_scales + gi * 128 + 32 * cb + 4 * r;
   }
   return p;
 }
 
-// Rows of a warp's part of a tile that exist (K: a group is whole, its padding
-// rows hold code 0).
 template <bool kV>
-__device__ __forceinline__ int raw_rows(const TreeArgs &a, int tile, int grp) {
-  const int left = a.cut - (kBN * tile + 32 * grp);
-  return kV ? max(0, min(32, left)) : left > 0 ? 32 : 0;
-}
-
-// The warp's part of a tile into its raw stage (2 KB codes, 512 B scales): two
-// bulk copies completing on bar (one lane calls).
-template <bool kV>
-__device__ __forceinline__ void fetch_raw(const TreeArgs &a, const RawPtr &p, int rows,
-                                          uint32_t stage, uint32_t bar) {
-  const uint32_t cb = 64u * rows, sb = kV ? 16u * rows : 512u;
-  const bool ok = in_bounds(a.ctl, p.c, cb) && in_bounds(a.ctl, p.s, sb);
-  mbar_arrive_expect_tx(bar, ok ? cb + sb : 0u);
-  if (!ok) return;
-  bulk_g2s(stage, p.c, cb, bar);
-  bulk_g2s(stage + 2048u, p.s, sb, bar);
-}
-
-// The lane's part of the stage to registers.
-template <bool kV>
-__device__ __forceinline__ void take_raw(const uint8_t *stage, int rows, int r, int cb, Raw &x) {
+__device__ __forceinline__ void load_raw(const TreeArgs &a, const RawPtr &p, int tile, int grp,
+                                         int r, Raw &x) {
   const uint4 zero = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // code 0
-  float *s = reinterpret_cast<float *>(&x.s);
-  const float *sc = reinterpret_cast<const float *>(stage + 2048);
+  if (kV) {
+    float *s = reinterpret_cast<float *>(&x.s);
+    const int left = a.cut - (kBN * tile + 32 * grp + r);  // rows from this lane's first on
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool ok = r + 8 * i < rows;
-    x.c[i] = ok ? *reinterpret_cast<const uint4 *>(stage + (r + 8 * i) * 64 + 16 * cb) : zero;
-    if (kV) s[i] = ok ? sc[(r + 8 * i) * 4 + cb] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const bool ok = 8 * i < left && in_bounds(a.ctl, p.c + 512 * i, 16) &&
+                      in_bounds(a.ctl, p.s + 32 * i, 4);
+      x.c[i] = ok ? *reinterpret_cast<const uint4 *>(p.c + 512 * i) : zero;
+      s[i] = ok ? p.s[32 * i] : 0.0f;
+    }
+  } else {
+    const bool have = 4 * tile + grp < a.Gk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x.c[i] = have && in_bounds(a.ctl, p.c + 512 * i, 16)
+                   ? *reinterpret_cast<const uint4 *>(p.c + 512 * i)
+                   : zero;
+    x.s = have && in_bounds(a.ctl, p.s, 16) ? *reinterpret_cast<const float4 *>(p.s)
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
-  if (!kV)
-    x.s = rows > 0 ? *reinterpret_cast<const float4 *>(sc + 32 * cb + 4 * r)
-                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
 // Eight codes of a word times their scales (pairs in the tiles' feature order).
@@ -438,9 +426,12 @@ __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &s
   }
 }
 
-// One dequantization warp: its rows of every K (or V) tile of the CTA's items. The
-// tile at hand is in registers, the next one in the warp's raw stage or on its
-// way there, so a tile's copy has the time of a whole tile to arrive.
+// One dequantization warp: its rows of every K (or V) tile of the CTA's items, each
+// with codes and scales loaded a tile earlier. (Loading two tiles ahead needs the
+// loop twice; the code of all roles then no longer fits the instruction caches
+// and the call takes half as long again. Bulk copies to a raw stage per warp,
+// the next one issued when a fence has shown that every lane has read the stage, take
+// 219 us where this takes 208: 16 sequences of 64 drafted tokens, 32K keys.)
 template <bool kV>
 __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, uint32_t lo,
                                              uint32_t hi, int grp, int lane) {
@@ -448,52 +439,35 @@ __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, ui
   auto unit_of = [&](uint32_t rb) {
     return static_cast<long>(rb / static_cast<uint32_t>(a.row_blocks));
   };
-  // the tile at hand and the one being fetched: segment, tile, tiles left
+  // the tile at hand and the one loaded ahead: segment, tile, tiles left
   Segment cur, ahead;
   uint32_t cur_x = lo, ahead_x = lo;
   bool more = next_segment(a, ahead_x, hi, ahead);
   if (!more) return;
   next_segment(a, cur_x, hi, cur);
-  RawPtr ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp);
-  uint8_t *const raw = sm.raw[kV ? 1 : 0][grp];
-  const uint32_t raw_bar = smem_u32(&sm.raw_full[kV ? 1 : 0][grp]);
-  uint32_t fetched = 0, taken = 0;  // copies started and used
-  auto fetch = [&]() {  // the tile `ahead` to the raw stage; on to the next
+  RawPtr ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp, r, cb);
+  Raw x;
+  auto load = [&]() {
     if (!more) return;
-    const int rows = raw_rows<kV>(a, ahead.t_lo, grp);
-    if (rows > 0) {
-      if (lane == 0) fetch_raw<kV>(a, ptr, rows, smem_u32(raw), raw_bar);
-      ++fetched;
-    }
+    if (ahead.t_lo < a.int4_tiles) load_raw<kV>(a, ptr, ahead.t_lo, grp, r, x);
     ptr.c += 8192;
     ptr.s += 512;
     ++ahead.t_lo;
     if (--ahead.n == 0) {
       more = next_segment(a, ahead_x, hi, ahead);
-      if (more) ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp);
+      if (more) ptr = raw_ptr<kV>(a, unit_of(ahead.rb), ahead.t_lo, grp, r, cb);
     }
   };
-  Raw x;
-  bool ok = true;
-  fetch();
+  load();
 #pragma unroll 1
-  for (int j = 0; ok; ++j) {
-    const int rows = raw_rows<kV>(a, cur.t_lo, grp);
-    if (rows > 0) {
-      ok = warp_wait(&sm.abort_flag, raw_bar, taken & 1u, a.ctl);
-      if (!ok) break;
-      ++taken;
-    }
-    take_raw<kV>(raw, rows, r, cb, x);
-    __syncwarp();  // the stage has been read
-    fetch();
+  for (int j = 0;; ++j) {
     const int st = j % kStages;
     uint64_t *empty = kV ? &sm.v_empty[st][grp >> 1] : &sm.k_empty[st][grp >> 1];
     uint64_t *full = kV ? &sm.v_full[st][grp >> 1] : &sm.k_full[st][grp >> 1];
     uint8_t *tile = kV ? sm.v[st] : sm.k[st];
-    if (j >= kStages) ok = warp_wait(&sm.abort_flag, smem_u32(empty),
-                                     static_cast<uint32_t>((j / kStages - 1) & 1), a.ctl);
-    if (!ok) break;
+    if (j >= kStages && !warp_wait(&sm.abort_flag, smem_u32(empty),
+                                   static_cast<uint32_t>((j / kStages - 1) & 1), a.ctl))
+      break;
     if (cur.t_lo < a.int4_tiles)
       store_raw<kV>(x, r, cb, tile + (32 * grp + r) * 128);
     else
@@ -503,11 +477,10 @@ __device__ __forceinline__ void dequant_warp(const TreeArgs &a, TreeSmem &sm, ui
     // (test hook: the keys of a dropped tile never arrive)
     if (lane == 0 && (kV || static_cast<int>(cur.rb) * a.tiles + cur.t_lo != a.ctl.drop_item))
       mbar_arrive(smem_u32(full));
+    load();
     ++cur.t_lo;
     if (--cur.n == 0 && !next_segment(a, cur_x, hi, cur)) break;
   }
-  // a copy still on its way lands before the CTA exits
-  if (fetched != taken) mbar_wait(raw_bar, taken & 1u, 2000000000ull);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
@@ -525,7 +498,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mbar_init(smem_u32(&sm.k_empty[i >> 1][i & 1]), 2);
       mbar_init(smem_u32(&sm.v_empty[i >> 1][i & 1]), 2);
     }
-    for (int i = 0; i < kDqWarps; ++i) mbar_init(smem_u32(&sm.raw_full[i >> 2][i & 3]), 1);
     mbar_init(smem_u32(&sm.q_full), 2 * kBM);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sm.s_full[i >> 1][i & 1]), 1);
@@ -827,14 +799,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
             const float f = mx > m ? fast_exp2(m - mx) : 1.0f;
             m = fmaxf(m, mx);
             l *= f;
-            // O holds still once the other buffer's last PV is done (this
-            // one's was before its S was issued)
-            if (used_other > 0)
-              ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][buf ^ 1]), (used_other - 1) & 1,
-                             a.ctl);
-            if (!ok) break;
-            tc_fence_after();
-            scale_tmem_row(o_row, f);
+            if (step > 0) {  // (before the first step O is zero)
+              // O holds still once the other buffer's last PV is done (this
+              // one's was before its S was issued)
+              if (used_other > 0)
+                ok = warp_wait(abort_flag, smem_u32(&sm.o_done[g][buf ^ 1]), (used_other - 1) & 1,
+                               a.ctl);
+              if (!ok) break;
+              tc_fence_after();
+              scale_tmem_row(o_row, f);
+            }
           }
           const float neg_m = m == -CUDART_INF_F ? 0.0f : -m;
           float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
@@ -1019,7 +993,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   const int in_rb = 32 * blockIdx.y + lane, r = row0 + in_rb;
   if (row0 + 32 * static_cast<int>(blockIdx.y) >= a.rows) return;
   const int c0 = cta_of(a, static_cast<long>(rb) * a.span + a.lead);
-  const int c1 = cta_of(a, static_cast<long>(rb + 1) * a.span - 1);
+  const int c1 = cta_of(a, static_cast<long>(rb) * a.span + a.lead + a.tiles - 1);
   const int n = c1 - c0 + 1;
   if (n == 1) return;
   const int grp = kWide ? blockIdx.z : warp;  // features 16 grp .. + 15
@@ -1102,10 +1076,13 @@ TreePlan tree_plan(const kvq_cache &c, int Hq, int T, int num_sms) {
   p.units = static_cast<long>(d.B) * d.Hkv;
   const long work = p.units * p.row_blocks * p.tiles;
   p.ctas = static_cast<int>(std::min<long>(work, num_sms));
-  // The lead only balances calls whose slices hold several tiles: with a tile or
+  // They only balance calls whose slices hold several tiles: with a tile or
   // two a CTA every row block is split over many anyway.
-  p.lead = work < 4L * num_sms ? 0 : p.rows > kBM ? kLeadTwo : kLeadShared;
-  p.span = p.lead + p.tiles;
+  // Without them: 16 sequences of 8 tokens over 8K keys 33.5 -> 39.2 us, 16 of 64
+  // over 32K 210 -> 217 us, 64 of 21 over 8K 127 -> 129 us.
+  const bool several = work >= 4L * num_sms;
+  p.lead = !several ? 0 : p.rows > kBM ? kLeadTwo : kLeadShared;
+  p.span = p.lead + p.tiles + (several ? kTrail : 0);
   p.items = p.units * p.row_blocks * p.span;
   // a row block's tiles meet at most (tiles - 2) / min_per + 2 slices
   const long min_per = p.items / p.ctas;
@@ -1124,7 +1101,7 @@ bool tree_tensor_supported(const kvq_cache &c, int q_dtype, int tree_dtype, int 
          static_cast<long>(c.n_tokens) + T < (1L << 30) &&
          // items (32-bit in the kernel): row blocks of 256, tiles of 128 keys and two partial ones
          static_cast<long>(c.batch) * c.kv_heads * (static_cast<long>(T) * (Hq / c.kv_heads) / 256 + 1) *
-                 (c.n_tokens / 128 + 4 + kLeadShared) < (1L << 30);
+                 (c.n_tokens / 128 + 4 + kLeadTwo + kTrail) < (1L << 30);
 }
 
 size_t tree_workspace_bytes(const kvq_cache &c, int Hq, int T, int num_sms) {

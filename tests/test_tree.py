@@ -435,3 +435,22 @@ def test_leaves_that_are_copied_record_nothing(kvq):
     with torch.no_grad():
         leaf.mul_(0.0)  # the next run reads the leaf's new values
     assert not torch.equal(a.run(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(3, 2, 8, 4100, 100, 16), (1, 2, 8, 16384, 128, 33),
+                                  (8, 2, 8, 6000, 112, 8)])
+def test_many_runs_agree(kvq, case):
+    """The hand-overs between the kernel's warps leave nothing to timing: each of many
+    runs back to back gives the same bits (two tiles a block, and several)."""
+    b, hkv, g, n, recent, t = case
+    c = make(kvq, b, hkv, n, 128, recent)
+    q, k, v = inputs(b, g * hkv, hkv, t, 128)
+    par = random_tree(b, t, n + t)
+    call = kvq.AttendTree(c, q, k, v, par, out_dtype="f32")
+    first = call.run().clone()
+    compare(first, plain(c, kvq, q, k, v, par), par, TOL_TENSOR)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        differ += (call.run() != first).any()
+    assert int(differ) == 0 and kvq.read_status(call.status) == 0
