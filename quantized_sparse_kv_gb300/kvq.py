@@ -825,7 +825,8 @@ class BlockSummary(_Prepared):
             return None
         out = torch.empty((c.batch, c.kv_heads, max(0, self.blocks - first), c.head_dim),
                           dtype=torch.float32, device=self.device)
-        _check(self.lib.kv_block_values(c.ref, self.ref, first, _ptr(out), None,
+        # (the address as an int: about 1 us a call cheaper than a ctypes pointer)
+        _check(self.lib.kv_block_values(c.ref, self.ref, first, out.data_ptr() or None, None,
                                         self._raw_stream()), "kv_block_values")
         return out
 
