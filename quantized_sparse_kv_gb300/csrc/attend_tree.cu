@@ -543,10 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     const uint32_t k_lo = uniform((smem_u32(sm.k[0]) >> 4) | (1u << 16));
     const uint32_t v_lo = uniform((smem_u32(sm.v[0]) >> 4) | (kHalf >> 4) << 16);
     const uint32_t s_bar = smem_u32(&sm.s_full[g][buf]), p_bar = smem_u32(&sm.p_full[g][buf]);
-    const uint32_t o_bar = smem_u32(&sm.o_done[g][buf]);
+    const uint32_t o_bar = smem_u32(&sm.o_done[g][buf]), o_other = smem_u32(&sm.o_done[g][buf ^ 1]);
     uint32_t base_j = 0;  // tiles of the CTA before this segment
     uint32_t seg = 0;
     uint32_t done = 0;    // PV MMAs issued so far
+    uint32_t other = 0;   // the other buffer's in earlier segments
     bool ok = true;
     uint32_t x = lo;
     for (Segment sg; ok && next_segment(a, x, hi, sg); ++seg) {
@@ -558,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       // Two groups of rows: step s is half s & 1 of tile s / 2, and each half of a
       // stage is freed by both groups. Shared rows: step s is half g of tile s,
       // freed by that group alone, in both arrivals.
+      const int steps = two ? 2 * n : n;
       bool first = true;
-      for (int at = static_cast<int>(buf); at < (two ? 2 * n : n); at += 2) {
+      for (int at = static_cast<int>(buf); at < steps; at += 2) {
         const uint32_t h = two ? buf : g;
         const uint32_t jj = base_j + (two ? at >> 1 : at), st = uniform(jj % kStages);
         const uint32_t par = (jj / kStages) & 1;
@@ -583,9 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           if (!two) tc_commit(k_bar);
         }
         __syncwarp();
-        // O += P V
+        // O += P V, step after step (the last one's PV is the other buffer's): the sums'
+        // order, and so the result, does not depend on which warp comes first
         if (!spin_wait(abort_flag, smem_u32(&sm.v_full[st][h]), par, a.ctl) ||
-            !spin_wait(abort_flag, p_bar, done & 1, a.ctl)) {
+            !spin_wait(abort_flag, p_bar, done & 1, a.ctl) ||
+            (at > 0 && !spin_wait(abort_flag, o_other, (other + ((at + 1) >> 1) - 1) & 1, a.ctl))) {
           ok = false;
           break;
         }
@@ -594,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16_ta(to, ts + 8u * kk, desc_of(vd + (kk * 2048u >> 4)), id_pv, 1u);
+            tc_mma_f16_ta(to, ts + 8u * kk, desc_of(vd + (kk * 2048u >> 4)), id_pv,
+                          at > 0 || kk > 0 ? 1u : 0u);
           tc_commit(o_bar);
           tc_commit(v_bar);
           if (!two) tc_commit(v_bar);
@@ -604,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         first = false;
       }
       base_j += n;
+      other += (steps + buf) >> 1;
     }
     // all MMAs of this CTA complete before TMEM is released
     if (elect_one()) tc_commit(smem_u32(&sm.mma_done));
@@ -724,15 +730,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         if (i0 >= q_first + (two ? 32 : 16)) break;
         load_q(qw, qt);
       }
-      // O starts at zero: the halves' first PVs may come in either order
-      {
-        float z[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) z[e] = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) tmem_st32(o_row + 32u * c, z);
-        tmem_wait_st();
-      }
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(smem_u32(&sm.q_full));
@@ -799,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
             const float f = mx > m ? fast_exp2(m - mx) : 1.0f;
             m = fmaxf(m, mx);
             l *= f;
-            if (step > 0) {  // (before the first step O is zero)
+            if (step > 0) {  // (before the first step there is no O)
               // O holds still once the other buffer's last PV is done (this
               // one's was before its S was issued)
               if (used_other > 0)
