@@ -146,66 +146,75 @@ __global__ void __launch_bounds__(kSumWarps * 32) summary128_kernel(const Summar
 }
 
 // ------------------------------------------------------------------ any D
-// One CTA per block: D / 8 threads share a token row (4 bytes, 8 channels
-// each), the other threads further rows; integer sums meet in shared memory.
-constexpr int kSumThreads = 256;
-
-__global__ void __launch_bounds__(kSumThreads) summary_kernel(const SummaryArgs a) {
+// One warp per block again, a lane per 4 bytes (8 channels) of a token row and as
+// many rows at once as fit the warp (a power of two). A word's channels are summed
+// as 16-bit halves (32 tokens' worth is 480), the row lanes' sums meet in the
+// first row's, which hold eight channels each from there on.
+__global__ void __launch_bounds__(kSumWarps * 32) summary_kernel(const SummaryArgs a) {
   wait_prior_grid();
   allow_next_grid();
-  __shared__ int sums[4][256];
-  __shared__ float red[kSumThreads / 32];
-  const int tid = threadIdx.x, D = a.D;
-  const int blk = a.first + static_cast<int>(blockIdx.x);
-  const int per_row = D / 8, rows = kSumThreads / per_row;
-  const int piece = tid % per_row, r0 = tid / per_row;
-  for (long u = blockIdx.y; u < a.units; u += gridDim.y) {
-    for (int i = tid; i < a.m * D; i += kSumThreads) sums[i / D][i % D] = 0;
-    __syncthreads();
-    for (int g = 0; g < a.m; ++g) {
-      const long gi = u * a.Gs + blk * a.m + g;
-      if (blk * a.m + g >= a.Gk || r0 >= rows) continue;
-      uint32_t lo = 0u, hi = 0u;  // at most 32 / rows + 1 <= 5 tokens a byte (rows >= 8)
-      for (int t = r0; t < 32; t += rows) {
-        const uint8_t *p = a.k_codes + (gi * 32 + t) * (D / 2) + 4 * piece;
-        const uint32_t x = in_bounds(a.ctl, p, 4) ? *reinterpret_cast<const uint32_t *>(p)
-                                                  : 0x88888888u;
-        lo += x & 0x0F0F0F0Fu;
-        hi += (x >> 4) & 0x0F0F0F0Fu;
-      }
+  const int lane = threadIdx.x & 31, D = a.D;
+  const long per = a.blocks - a.first;
+  const long id = static_cast<long>(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
+  if (id >= per * a.units) return;
+  const long u = id / per;
+  const int blk = a.first + static_cast<int>(id - u * per);
+  const int pieces = D / 8;  // lanes per token row
+  const int rows = pieces > 16 ? 1 : pieces > 8 ? 2 : pieces > 4 ? 4 : 8;
+  const int row = lane / pieces, piece = lane - row * pieces;
+  const bool on = row < rows;
+  float acc[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r0 >= 32) break;
-        atomicAdd(&sums[g][8 * piece + 2 * j], static_cast<int>((lo >> (8 * j)) & 0xffu));
-        atomicAdd(&sums[g][8 * piece + 2 * j + 1], static_cast<int>((hi >> (8 * j)) & 0xffu));
-      }
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int g = 0; g < a.m && blk * a.m + g < a.Gk; ++g) {
+    const long gi = u * a.Gs + blk * a.m + g;
+    const uint8_t *p = a.k_codes + (gi * 32 + row) * (D / 2) + 4 * piece;
+    const float *s = a.k_scales + gi * D + 8 * piece;
+    // the channels' scales are on their way while the codes are summed
+    float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
+    if (row == 0 && in_bounds(a.ctl, s, 32)) {
+      s0 = *reinterpret_cast<const float4 *>(s);
+      s1 = *reinterpret_cast<const float4 *>(s + 4);
     }
-    __syncthreads();
-    const float tokens = static_cast<float>(min(32 * a.m, a.cut - 32 * a.m * blk));
-    float mean = 0.0f;
-    if (tid < D) {
-      float acc = 0.0f;
-      for (int g = 0; g < a.m && blk * a.m + g < a.Gk; ++g) {
-        const float *s = a.k_scales + (u * a.Gs + blk * a.m + g) * D + tid;
-        const float p = __fmul_rn(in_bounds(a.ctl, s, 4) ? *s : 0.0f,
-                                  static_cast<float>(sums[g][tid] - 256));
-        acc = g == 0 ? p : __fadd_rn(acc, p);
-      }
-      mean = __fdiv_rn(acc, tokens);
-    }
-    const float wm = warp_max(fabsf(mean));
-    if ((tid & 31) == 0) red[tid >> 5] = wm;
-    __syncthreads();
-    float mx = red[0];
+    uint32_t sum[4] = {0u, 0u, 0u, 0u};  // sum[k]: channels k (low half) and k + 4
+#pragma unroll 8
+    for (int t = 0; t < 32; t += rows) {
+      const uint8_t *w = p + t * (D / 2);
+      const uint32_t x = on && in_bounds(a.ctl, w, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(w))
+                                                      : 0x88888888u;
 #pragma unroll
-    for (int w = 1; w < kSumThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-    const float scale = __fdiv_rn(mx, 127.0f);
-    const long row = u * a.cap + blk;
-    if (tid < D && in_bounds(a.ctl, a.codes + row * D + tid, 1))
-      a.codes[row * D + tid] = static_cast<int8_t>(int8_code(mean, scale));
-    if (tid == 0 && in_bounds(a.ctl, a.scales + row, 4)) a.scales[row] = scale;
-    __syncthreads();
+      for (int k = 0; k < 4; ++k) sum[k] += (x >> (4 * k)) & 0x000F000Fu;
+    }
+    for (int r = rows / 2; r > 0; r /= 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[k] += __shfl_down_sync(0xffffffffu, sum[k], r * pieces);
+    }
+    const float sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // 32 tokens of code + 8: padding tokens hold code 0
+      const int c = static_cast<int>((sum[i & 3] >> (i < 4 ? 0 : 16)) & 0xffffu) - 256;
+      const float part = __fmul_rn(sc[i], static_cast<float>(c));
+      acc[i] = g == 0 ? part : __fadd_rn(acc[i], part);
+    }
   }
+  const float tokens = static_cast<float>(min(32 * a.m, a.cut - 32 * a.m * blk));
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    acc[i] = __fdiv_rn(acc[i], tokens);
+    mx = row == 0 ? fmaxf(mx, fabsf(acc[i])) : 0.0f;
+  }
+  const float scale = __fdiv_rn(warp_max(mx), 127.0f);
+  const long at = u * a.cap + blk;
+  if (lane == 0 && in_bounds(a.ctl, a.scales + at, 4)) a.scales[at] = scale;
+  int8_t *o = a.codes + at * D + 8 * piece;
+  if (row != 0 || !in_bounds(a.ctl, o, 8)) return;
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    out[i >> 2] |= (static_cast<uint32_t>(int8_code(acc[i], scale)) & 0xffu) << (8 * (i & 3));
+  *reinterpret_cast<uint2 *>(o) = make_uint2(out[0], out[1]);
 }
 
 // ------------------------------------------------------------------ values
@@ -512,20 +521,16 @@ int launch_block_summary(const kvq_cache &c, const kvq_summary &sm, int first, i
   a.cap = sm.cap_blocks;
   a.units = static_cast<long>(d.B) * d.Hkv;
   a.ctl = ctl;
-  if (d.D == 128) {
-    const long warps = a.units * (blocks - first);
-    const dim3 grid(static_cast<unsigned>((warps + kSumWarps - 1) / kSumWarps));
-    if (a.m == 1)
-      launch_dependent(summary128_kernel<1>, grid, dim3(kSumWarps * 32), 0, s, a);
-    else if (a.m == 2)
-      launch_dependent(summary128_kernel<2>, grid, dim3(kSumWarps * 32), 0, s, a);
-    else
-      launch_dependent(summary128_kernel<4>, grid, dim3(kSumWarps * 32), 0, s, a);
-    return 1;
-  }
-  const dim3 grid(static_cast<unsigned>(blocks - first),
-                  static_cast<unsigned>(std::min<long>(a.units, 65535)));
-  launch_dependent(summary_kernel, grid, dim3(kSumThreads), 0, s, a);
+  const long warps = a.units * (blocks - first);
+  const dim3 grid(static_cast<unsigned>((warps + kSumWarps - 1) / kSumWarps)), block(kSumWarps * 32);
+  if (d.D != 128)
+    launch_dependent(summary_kernel, grid, block, 0, s, a);
+  else if (a.m == 1)
+    launch_dependent(summary128_kernel<1>, grid, block, 0, s, a);
+  else if (a.m == 2)
+    launch_dependent(summary128_kernel<2>, grid, block, 0, s, a);
+  else
+    launch_dependent(summary128_kernel<4>, grid, block, 0, s, a);
   return 1;
 }
 
