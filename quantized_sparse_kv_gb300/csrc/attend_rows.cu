@@ -3,14 +3,16 @@
 // tensor-core kernels do not take (fp32 queries, other head dims, fp32 or MXFP8
 // windows).
 //
-// One CTA of 8 warps per (query token, query head, sequence). The row's keys are
-// walked in chunks of 32: the cache's tokens and then the drafted ones (tree), or
-// the listed blocks' groups and then the window (blocks); warp w takes chunks w,
-// w + 8, ... Lane j of a warp scores key j of the chunk against the whole q row in
-// shared memory, the warp keeps an online softmax (running maximum, rescaled sum)
-// and each lane owns D / 32 output features. The warps' states meet in shared
-// memory. Keys a row does not see are never read into a sum, so their contents
-// do not matter. It is bound by its instructions, about 2 D + 100 per key.
+// One CTA of 8 warps per query token, sequence and (up to) four of the query heads
+// that share a KV head, which see the same keys: each key and value is read and
+// dequantized once for all of them. The keys are walked in chunks of 32: the
+// cache's tokens and then the drafted ones (tree), or the listed blocks' groups
+// and then the window (blocks); warp w takes chunks w, w + 8, ... Lane j of a warp
+// scores key j of the chunk against the whole q rows in shared memory, the warp
+// keeps an online softmax per row (running maximum, rescaled sum) and each lane
+// owns D / 32 output features. The warps' states meet in shared memory. Keys a
+// token does not see are never read into a sum, so their contents do not matter.
+// It is bound by its instructions, about (3 + 2.25 rows) D / 4 + 60 a lane and key.
 #include <math_constants.h>
 
 #include "kvq_internal.h"
@@ -57,45 +59,71 @@ __device__ __forceinline__ size_t elem_size(int dtype) {
   return dtype == KVQ_F32 ? 4 : dtype == KVQ_BF16 ? 2 : 1;
 }
 
-// q . (row `row` of a dense [rows][D] tensor)
-template <int D>
-__device__ __forceinline__ float dot_row(const KernelCtl &ctl, const void *p, int dtype, long row,
-                                         const float *q) {
-  float s = 0.0f;
-  if (!in_bounds(ctl, static_cast<const uint8_t *>(p) + row * D * elem_size(dtype),
-                 D * elem_size(dtype)))
-    return s;
-#pragma unroll 8
-  for (int d = 0; d < D; ++d) s = fmaf(q[d], elem(p, dtype, row * D + d), s);
-  return s;
+// s[r] += q[r][d .. d + 3] . (x0 .. x3)
+template <int D, int kRows>
+__device__ __forceinline__ void dot4(float (&s)[kRows], const float (*q)[D], int d, float x0,
+                                     float x1, float x2, float x3) {
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const float4 y = *reinterpret_cast<const float4 *>(&q[r][d]);
+    s[r] = fmaf(y.w, x3, fmaf(y.z, x2, fmaf(y.y, x1, fmaf(y.x, x0, s[r]))));
+  }
 }
 
-// q . K of cache token t
-template <int D>
-__device__ __forceinline__ float dot_cache(const RowsArgs &a, long u, int t, const float *q) {
-  float s = 0.0f;
+// s[r] = q[r] . (row `row` of a dense [rows][D] tensor)
+template <int D, int kRows>
+__device__ __forceinline__ void dot_row(const KernelCtl &ctl, const void *p, int dtype, long row,
+                                        const float (*q)[D], float (&s)[kRows]) {
+  if (!in_bounds(ctl, static_cast<const uint8_t *>(p) + row * D * elem_size(dtype),
+                 D * elem_size(dtype)))
+    return;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    if (dtype == KVQ_F32) {
+      const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + row * D + d);
+      dot4<D, kRows>(s, q, d, x.x, x.y, x.z, x.w);
+    } else {
+      const uint2 x =
+          *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + row * D + d);
+      dot4<D, kRows>(s, q, d, __uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                     __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+    }
+  }
+}
+
+// s[r] = q[r] . K of cache token t
+template <int D, int kRows>
+__device__ __forceinline__ void dot_cache(const RowsArgs &a, long u, int t, const float (*q)[D],
+                                          float (&s)[kRows]) {
   if (t < a.cut) {
     const long g = u * a.Gs + t / kGroup;
     const uint32_t *c =
         reinterpret_cast<const uint32_t *>(a.k_codes + (g * kGroup + t % kGroup) * (D / 2));
     const float *sc = a.k_scales + g * D;
-    if (!in_bounds(a.ctl, c, D / 2) || !in_bounds(a.ctl, sc, D * sizeof(float))) return s;
+    if (!in_bounds(a.ctl, c, D / 2) || !in_bounds(a.ctl, sc, D * sizeof(float))) return;
 #pragma unroll 4
     for (int w = 0; w < D / 8; ++w) {
       const uint32_t x = c[w];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        s = fmaf(q[8 * w + e], nibble(x >> (8 * (e / 2)), e & 1) * sc[8 * w + e], s);
+      for (int h = 0; h < 2; ++h) {
+        const float4 f = *reinterpret_cast<const float4 *>(sc + 8 * w + 4 * h);
+        const uint32_t b0 = x >> (16 * h), b1 = x >> (16 * h + 8);
+        dot4<D, kRows>(s, q, 8 * w + 4 * h, nibble(b0, 0) * f.x, nibble(b0, 1) * f.y,
+                       nibble(b1, 0) * f.z, nibble(b1, 1) * f.w);
+      }
     }
-    return s;
+    return;
   }
   const long row = u * a.Ws + (t - a.cut);
-  if (a.kwin != KVQ_MXFP8) return dot_row<D>(a.ctl, a.k_window, a.kwin, row, q);
+  if (a.kwin != KVQ_MXFP8) return dot_row<D, kRows>(a.ctl, a.k_window, a.kwin, row, q, s);
   const uint8_t *c = static_cast<const uint8_t *>(a.k_window) + row * D;
   const uint8_t *e8 = a.k_e8m0 + row * (D / 32);
-  if (!in_bounds(a.ctl, c, D) || !in_bounds(a.ctl, e8, D / 32)) return s;
-  for (int d = 0; d < D; ++d) s = fmaf(q[d], mxfp8_value(c[d], e8[d / 32]), s);
-  return s;
+  if (!in_bounds(a.ctl, c, D) || !in_bounds(a.ctl, e8, D / 32)) return;
+  for (int d = 0; d < D; d += 4) {
+    const uint8_t e = e8[d / 32];
+    dot4<D, kRows>(s, q, d, mxfp8_value(c[d], e), mxfp8_value(c[d + 1], e),
+                   mxfp8_value(c[d + 2], e), mxfp8_value(c[d + 3], e));
+  }
 }
 
 // Element d of V of cache token t
@@ -115,26 +143,34 @@ __device__ __forceinline__ float v_cache(const RowsArgs &a, long u, int t, int d
   return elem(a.v_window, a.vwin, i);
 }
 
-template <int DPL, bool kTree>
+template <int DPL, bool kTree, int kRows>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a) {
   wait_prior_grid();
   allow_next_grid();
   constexpr int D = 32 * DPL;
-  __shared__ float qs[D];
-  __shared__ float wo[kRowWarps][D], wm[kRowWarps], wl[kRowWarps];
+  __shared__ __align__(16) float qs[kRows][D];
+  __shared__ float wo[kRowWarps][kRows][D], wm[kRowWarps][kRows], wl[kRowWarps][kRows];
   __shared__ int par[KVQ_TREE_MAX];
   __shared__ uint32_t seen[KVQ_TREE_MAX / 32];
   __shared__ int row_ok;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const long kvh = h / a.group;
+  // query token i of sequence b; heads kvh * group + h0 + 0 .. kRows - 1 (below h0 + heads)
+  const int i = blockIdx.x, b = blockIdx.z, per = (a.group + kRows - 1) / kRows;
+  const int kvh = blockIdx.y / per, h0 = (blockIdx.y - kvh * per) * kRows;
+  const int heads = min(kRows, a.group - h0);
   const long u = static_cast<long>(b) * a.Hkv + kvh;
-  const long row = (static_cast<long>(b) * a.Hq + h) * a.n_q + i;
   const size_t qe = elem_size(a.q_dtype), oe = elem_size(a.out_dtype);
-  const bool io_ok =
-      in_bounds(a.ctl, static_cast<const uint8_t *>(a.q) + row * D * qe, D * qe) &&
-      in_bounds(a.ctl, static_cast<uint8_t *>(a.out) + row * D * oe, D * oe);
-  for (int d = tid; d < D; d += kRowWarps * 32) qs[d] = io_ok ? elem(a.q, a.q_dtype, row * D + d) : 0.0f;
+  auto row_of = [&](int r) {
+    return (static_cast<long>(b) * a.Hq + kvh * a.group + h0 + r) * a.n_q + i;
+  };
+  auto q_ok = [&](int r) {
+    return r < heads &&
+           in_bounds(a.ctl, static_cast<const uint8_t *>(a.q) + row_of(r) * D * qe, D * qe);
+  };
+  for (int e = tid; e < kRows * D; e += kRowWarps * 32) {
+    const int r = e / D, d = e % D;
+    qs[r][d] = q_ok(r) ? elem(a.q, a.q_dtype, row_of(r) * D + d) : 0.0f;
+  }
   if (kTree) {
     const int32_t *p = a.parents + static_cast<long>(b) * a.n_q;
     const bool ok = in_bounds(a.ctl, p, sizeof(int32_t) * a.n_q);
@@ -164,15 +200,22 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a) 
     if (bad) flag_error(a.ctl, KVQ_DEV_INDEX);
   }
   if (a.kwin == KVQ_MXFP8) {  // Q takes the same MXFP8 rounding as the K window
-    for (int j = warp; j < DPL; j += kRowWarps)
-      qs[32 * j + lane] = mxfp8_round_warp(qs[32 * j + lane]);
+    for (int j = warp; j < kRows * DPL; j += kRowWarps) {
+      float &x = qs[j / DPL][32 * (j % DPL) + lane];
+      x = mxfp8_round_warp(x);
+    }
   }
   __syncthreads();
   if (kTree && row_ok == 0) return;  // the output of a row without a token stays
 
-  float m = -CUDART_INF_F, l = 0.0f, o[DPL];
+  float m[kRows], l[kRows], o[kRows][DPL];
 #pragma unroll
-  for (int k = 0; k < DPL; ++k) o[k] = 0.0f;
+  for (int r = 0; r < kRows; ++r) {
+    m[r] = -CUDART_INF_F;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) o[r][k] = 0.0f;
+  }
 
   const int32_t *list = nullptr;
   int per_block = 1, list_chunks = 0;
@@ -211,24 +254,54 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a) 
         t = k < a.R ? a.cut + k : -1;
       }
     }
-    float s = -CUDART_INF_F;
-    if (t >= 0) s = dot_cache<D>(a, u, t, qs) * a.scale;
-    if (tj >= 0) s = dot_row<D>(a.ctl, a.k_tree, a.tree_dtype, u * a.n_q + tj, qs) * a.scale;
     const bool live = t >= 0 || tj >= 0;
     const uint32_t lives = __ballot_sync(0xffffffffu, live);
     if (lives == 0u) continue;
-    const float mx = warp_max(s);
-    // (all scores -inf: probabilities against 0 are exp(-inf) = 0)
-    const float m_new = fmaxf(m, mx), ref = m_new == -CUDART_INF_F ? 0.0f : m_new;
-    const float corr = m == -CUDART_INF_F ? 0.0f : expf(m - ref);
-    const float p = live ? expf(s - ref) : 0.0f;
-    l = l * corr + warp_sum(p);
+    float p[kRows];
 #pragma unroll
-    for (int k = 0; k < DPL; ++k) o[k] *= corr;
-    m = m_new;
+    for (int r = 0; r < kRows; ++r) p[r] = 0.0f;
+    if (t >= 0) dot_cache<D, kRows>(a, u, t, qs, p);
+    if (tj >= 0) dot_row<D, kRows>(a.ctl, a.k_tree, a.tree_dtype, u * a.n_q + tj, qs, p);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float s = live ? p[r] * a.scale : -CUDART_INF_F;
+      const float mx = warp_max(s);
+      // (all scores -inf: probabilities against 0 are exp(-inf) = 0)
+      const float m_new = fmaxf(m[r], mx), ref = m_new == -CUDART_INF_F ? 0.0f : m_new;
+      const float corr = m[r] == -CUDART_INF_F ? 0.0f : expf(m[r] - ref);
+      p[r] = live ? expf(s - ref) : 0.0f;
+      l[r] = l[r] * corr + warp_sum(p[r]);
+#pragma unroll
+      for (int k = 0; k < DPL; ++k) o[r][k] *= corr;
+      m[r] = m_new;
+    }
+    // 32 keys of the int4 part in a row: their values' loads overlap
+    const int t0 = __shfl_sync(0xffffffffu, t, 0);
+    const long v0 = u * a.Vs + t0;
+    if (__all_sync(0xffffffffu, t >= 0 && t < a.cut) &&
+        in_bounds(a.ctl, a.v_codes + v0 * (D / 2), 16 * D) &&
+        in_bounds(a.ctl, a.v_scales + v0 * DPL, 128 * DPL)) {
+      const uint8_t *c = a.v_codes + v0 * (D / 2) + lane / 2;
+      const float *sc = a.v_scales + v0 * DPL;
+#pragma unroll 8
+      for (int j = 0; j < 32; ++j) {
+        float pj[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) pj[r] = __shfl_sync(0xffffffffu, p[r], j);
+#pragma unroll
+        for (int k = 0; k < DPL; ++k) {
+          const float v = nibble(c[j * (D / 2) + 16 * k], lane & 1) * sc[j * DPL + k];
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) o[r][k] = fmaf(pj[r], v, o[r][k]);
+        }
+      }
+      continue;
+    }
     for (int j = 0; j < 32; ++j) {
       if (!(lives >> j & 1u)) continue;
-      const float pj = __shfl_sync(0xffffffffu, p, j);
+      float pj[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) pj[r] = __shfl_sync(0xffffffffu, p[r], j);
       const int tt = __shfl_sync(0xffffffffu, t, j), tr = __shfl_sync(0xffffffffu, tj, j);
 #pragma unroll
       for (int k = 0; k < DPL; ++k) {
@@ -242,52 +315,66 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a) 
         } else {
           v = v_cache<D>(a, u, tt, d);
         }
-        o[k] = fmaf(pj, v, o[k]);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) o[r][k] = fmaf(pj[r], v, o[r][k]);
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k < DPL; ++k) wo[warp][lane + 32 * k] = o[k];
-  if (lane == 0) {
-    wm[warp] = m;
-    wl[warp] = l;
+  for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) wo[warp][r][lane + 32 * k] = o[r][k];
+    if (lane == 0) {
+      wm[warp][r] = m[r];
+      wl[warp][r] = l[r];
+    }
   }
   __syncthreads();
-  float mx = -CUDART_INF_F;
+  for (int e = tid; e < kRows * D; e += kRowWarps * 32) {
+    const int r = e / D, d = e % D;
+    const long at = row_of(r) * D;
+    if (!q_ok(r) || !in_bounds(a.ctl, static_cast<uint8_t *>(a.out) + at * oe, D * oe)) continue;
+    float mx = -CUDART_INF_F;
 #pragma unroll
-  for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, wm[w]);
-  if (!io_ok) return;
-  for (int d = tid; d < D; d += kRowWarps * 32) {
+    for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, wm[w][r]);
     float ls = 0.0f, acc = 0.0f;
 #pragma unroll
     for (int w = 0; w < kRowWarps; ++w) {
-      if (wl[w] == 0.0f) continue;  // no key (a NaN sum stays in)
-      const float f = wm[w] == -CUDART_INF_F ? 1.0f : expf(wm[w] - mx);
-      ls += f * wl[w];
-      acc += f * wo[w][d];
+      if (wl[w][r] == 0.0f) continue;  // no key (a NaN sum stays in)
+      const float f = wm[w][r] == -CUDART_INF_F ? 1.0f : expf(wm[w][r] - mx);
+      ls += f * wl[w][r];
+      acc += f * wo[w][r][d];
     }
     const float x = ls == 0.0f ? 0.0f : acc / ls;  // no key at all: zero
     if (a.out_dtype == KVQ_F32)
-      static_cast<float *>(a.out)[row * D + d] = x;
+      static_cast<float *>(a.out)[at + d] = x;
     else
-      static_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(x);
+      static_cast<__nv_bfloat16 *>(a.out)[at + d] = __float2bfloat16_rn(x);
   }
+}
+
+constexpr int kShared = 4;  // query heads of a KV head that share a CTA
+
+template <bool kTree, int kRows>
+int launch_rows_of(const RowsArgs &a, int D, int batch, cudaStream_t s) {
+  const dim3 grid(a.n_q, a.Hkv * ((a.group + kRows - 1) / kRows), batch), block(kRowWarps * 32);
+  switch (D / 32) {
+    case 1: launch_dependent(rows_kernel<1, kTree, kRows>, grid, block, 0, s, a); break;
+    case 2: launch_dependent(rows_kernel<2, kTree, kRows>, grid, block, 0, s, a); break;
+    case 3: launch_dependent(rows_kernel<3, kTree, kRows>, grid, block, 0, s, a); break;
+    case 4: launch_dependent(rows_kernel<4, kTree, kRows>, grid, block, 0, s, a); break;
+    case 5: launch_dependent(rows_kernel<5, kTree, kRows>, grid, block, 0, s, a); break;
+    case 6: launch_dependent(rows_kernel<6, kTree, kRows>, grid, block, 0, s, a); break;
+    case 7: launch_dependent(rows_kernel<7, kTree, kRows>, grid, block, 0, s, a); break;
+    default: launch_dependent(rows_kernel<8, kTree, kRows>, grid, block, 0, s, a); break;
+  }
+  return 1;
 }
 
 template <bool kTree>
 int launch_rows(const RowsArgs &a, int D, int batch, cudaStream_t s) {
-  const dim3 grid(a.n_q, a.Hq, batch), block(kRowWarps * 32);
-  switch (D / 32) {
-    case 1: launch_dependent(rows_kernel<1, kTree>, grid, block, 0, s, a); break;
-    case 2: launch_dependent(rows_kernel<2, kTree>, grid, block, 0, s, a); break;
-    case 3: launch_dependent(rows_kernel<3, kTree>, grid, block, 0, s, a); break;
-    case 4: launch_dependent(rows_kernel<4, kTree>, grid, block, 0, s, a); break;
-    case 5: launch_dependent(rows_kernel<5, kTree>, grid, block, 0, s, a); break;
-    case 6: launch_dependent(rows_kernel<6, kTree>, grid, block, 0, s, a); break;
-    case 7: launch_dependent(rows_kernel<7, kTree>, grid, block, 0, s, a); break;
-    default: launch_dependent(rows_kernel<8, kTree>, grid, block, 0, s, a); break;
-  }
-  return 1;
+  return a.group == 1 ? launch_rows_of<kTree, 1>(a, D, batch, s)
+                      : launch_rows_of<kTree, kShared>(a, D, batch, s);
 }
 
 RowsArgs rows_args(const kvq_cache &c, const void *q, int q_dtype, int Hq, int n_q, float scale,
