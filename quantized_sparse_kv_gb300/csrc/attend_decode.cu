@@ -35,7 +35,9 @@
 // of its tokens exist, 0 for a skipped entry), from list entries the whole warp
 // reads eight items ahead. Everything behind the copies is the same code; with
 // fewer than 8 query heads per KV head the missing rows of the MMA are zero and
-// not stored.
+// not stored. 32 sequences, 32 blocks of 64 and a window of 128 tokens each (25 MB):
+// 14.2 us and 4.7 us for the combine, mostly fixed times (the first item lands after
+// 4-6 us, a CTA has three or four of them).
 //
 // Feature order. Within a thread, features are visited in a fixed permutation
 // (the one that makes a 16-byte row slice of nibbles a ready MMA operand); the

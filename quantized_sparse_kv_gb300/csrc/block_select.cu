@@ -13,7 +13,11 @@
 // group and writes D + 4 per block: memory. Scoring reads D + 4 bytes per
 // block, about 1/40 of the block itself, and needs heads * D / 4 dp4a
 // instructions for it; choosing is a radix selection over one score row and
-// bound by latency.
+// bound by latency. Measured, D = 128, blocks of 64: summaries of 32 x 2 x 131,072
+// tokens (671 MB of codes and scales) 108 us, 6.4 TB/s; their values (17 MB read, 67
+// written) 14 us; scores of 8 heads over 64 x 2,046 blocks (17.3 MB) 9.5 us and the
+// choice of 32 5.3 us. Scores and choice in one kernel (a cluster per query
+// token, scores kept in shared memory) took 6 us longer than the two.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -149,7 +153,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) summary128_kernel(const Summar
 // One warp per block again, a lane per 4 bytes (8 channels) of a token row and as
 // many rows at once as fit the warp (a power of two). A word's channels are summed
 // as 16-bit halves (32 tokens' worth is 480), the row lanes' sums meet in the
-// first row's, which hold eight channels each from there on.
+// first row's, which hold eight channels each from there on. (D = 64, 84 MB: 41.6 us;
+// the kernel above takes 16.8 us for as much at D = 128.)
 __global__ void __launch_bounds__(kSumWarps * 32) summary_kernel(const SummaryArgs a) {
   wait_prior_grid();
   allow_next_grid();

