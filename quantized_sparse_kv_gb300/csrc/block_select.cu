@@ -279,40 +279,17 @@ struct SelectArgs {
 constexpr int kScoreThreads = 128;
 constexpr int kMaxGroup = 64;  // query heads per KV head
 
-// One thread per block of a (unit, query token); q of the G heads as int8 in
-// shared memory, read by broadcast. For D = 128 (k128) a thread's whole block
-// row is in flight while q is rounded, so the two loads' latencies, which are
-// most of the time, overlap; other D read it 16 bytes at a time.
-template <bool k128>
-__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectArgs a) {
-  wait_prior_grid();
-  allow_next_grid();
-  extern __shared__ __align__(16) int8_t qs[];  // [ceil(G / 8) * 8][D]
-  __shared__ float sq[kMaxGroup];
-  const int D = k128 ? 128 : a.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int uq = blockIdx.y;  // unit * n_q + query token
-  const long u = uq / a.n_q;
-  const int iq = uq - static_cast<int>(u) * a.n_q;
-  const int Gp = (a.G + 7) / 8 * 8;
-  const int blk = blockIdx.x * kScoreThreads + threadIdx.x;
-  const long brow = u * a.cap + blk;
-  const bool have = blk < a.blocks && in_bounds(a.ctl, a.codes + brow * D, D) &&
-                    in_bounds(a.ctl, a.scales + brow, 4);
-  const uint4 *kp = reinterpret_cast<const uint4 *>(a.codes + brow * D);
-  uint4 kk[k128 ? 8 : 1];
-  float sb = 0.0f;
-  if (have) {
-    sb = a.scales[brow];
-    if (k128) {
-#pragma unroll
-      for (int c = 0; c < (k128 ? 8 : 1); ++c) kk[c] = kp[c];
-    }
-  }
-  for (int h = warp; h < Gp; h += kScoreThreads / 32) {
+// The rows of q of a (unit, query token) as int8 to shared memory, G heads padded with
+// zeros to a multiple of eight: a warp per row, its largest magnitude first.
+template <int kPer>  // features a lane holds
+__device__ __forceinline__ void round_queries(const SelectArgs &a, long u, int iq, int D,
+                                              int8_t *qs, float *sq) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int h = warp; h < (a.G + 7) / 8 * 8; h += kScoreThreads / 32) {
     const long row = (u * a.G + h) * a.n_q + iq;  // [batch][q_heads][n_q], q head = kv * G + h
-    float x[8], mx = 0.0f;
+    float x[kPer], mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < (k128 ? 4 : 8); ++i) {
+    for (int i = 0; i < kPer; ++i) {
       const int d = lane + 32 * i;
       x[i] = 0.0f;
       if (h < a.G && d < D) {
@@ -327,19 +304,115 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
       mx = fmaxf(mx, fabsf(x[i]));
     }
     const float s = __fdiv_rn(warp_max(mx), 127.0f);
-    if (lane == 0 && h < a.G) sq[h] = s;
+    if (lane == 0) sq[h] = h < a.G ? s : 0.0f;
 #pragma unroll
-    for (int i = 0; i < (k128 ? 4 : 8); ++i)
-      if (lane + 32 * i < D)
-        qs[h * D + lane + 32 * i] = static_cast<int8_t>(int8_code(x[i], s));
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < D) qs[h * D + lane + 32 * i] = static_cast<int8_t>(int8_code(x[i], s));
   }
+}
+
+// D = 128. Eight lanes share a block's row, 16 bytes each, so a warp's load is four
+// whole rows, and a thread's eight rows are in flight while q is rounded. A
+// lane's part of eight heads' codes stays in registers; the eight lanes' sums of a
+// row meet in three exchanges that halve what each keeps, head by head, and three
+// more take the largest score.
+constexpr int kScoreRows = 8;  // blocks per eight lanes
+
+__global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ __align__(16) int8_t qs[kMaxGroup * 128];
+  __shared__ float sq[kMaxGroup];
+  const int lane = threadIdx.x & 31, part = lane & 7;
+  const int uq = blockIdx.y;  // unit * n_q + query token
+  const long u = uq / a.n_q;
+  const int iq = uq - static_cast<int>(u) * a.n_q;
+  // row r of the thread's: block first + r * kScoreThreads / 8
+  const int first = blockIdx.x * kScoreThreads + threadIdx.x / 8;
+  uint4 kk[kScoreRows];
+  float sb[kScoreRows];
+#pragma unroll
+  for (int r = 0; r < kScoreRows; ++r) {
+    const int blk = first + r * (kScoreThreads / 8);
+    const long brow = u * a.cap + blk;
+    const bool have = blk < a.blocks && in_bounds(a.ctl, a.codes + brow * 128, 128) &&
+                      in_bounds(a.ctl, a.scales + brow, 4);
+    kk[r] = have ? *reinterpret_cast<const uint4 *>(a.codes + brow * 128 + 16 * part)
+                 : make_uint4(0u, 0u, 0u, 0u);
+    sb[r] = have ? a.scales[brow] : 0.0f;
+  }
+  round_queries<4>(a, u, iq, 128, qs, sq);
   __syncthreads();
+  float best[kScoreRows];
+#pragma unroll
+  for (int r = 0; r < kScoreRows; ++r) best[r] = -CUDART_INF_F;
+#pragma unroll 1
+  for (int h0 = 0; h0 < a.G; h0 += 8) {
+    int4 q[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      q[h] = *reinterpret_cast<const int4 *>(qs + (h0 + h) * 128 + 16 * part);
+    const float s = sq[h0 + part];  // after the exchanges lane `part` holds head h0 + part
+#pragma unroll
+    for (int r = 0; r < kScoreRows; ++r) {
+      int dot[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        int d = __dp4a(static_cast<int>(kk[r].x), q[h].x, 0);
+        d = __dp4a(static_cast<int>(kk[r].y), q[h].y, d);
+        d = __dp4a(static_cast<int>(kk[r].z), q[h].z, d);
+        dot[h] = __dp4a(static_cast<int>(kk[r].w), q[h].w, d);
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const bool up = part & o;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (h < o) {
+            const int send = up ? dot[h] : dot[h + o], keep = up ? dot[h + o] : dot[h];
+            dot[h] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+      }
+      const float x = __fmul_rn(__fmul_rn(s, sb[r]), static_cast<float>(dot[0]));
+      if (h0 + part < a.G) best[r] = fmaxf(best[r], x);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kScoreRows; ++r) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], o));
+    const int blk = first + r * (kScoreThreads / 8);
+    float *o = a.scores + static_cast<long>(uq) * a.stride + blk;
+    if (part == 0 && blk < a.blocks && in_bounds(a.ctl, o, 4))
+      *o = blk < a.sink ? CUDART_INF_F : best[r];
+  }
+}
+
+// Any D: one thread per block, its row read 16 bytes at a time, q read by broadcast.
+__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  extern __shared__ __align__(16) int8_t qs[];  // [ceil(G / 8) * 8][D]
+  __shared__ float sq[kMaxGroup];
+  const int D = a.D;
+  const int uq = blockIdx.y;  // unit * n_q + query token
+  const long u = uq / a.n_q;
+  const int iq = uq - static_cast<int>(u) * a.n_q;
+  round_queries<8>(a, u, iq, D, qs, sq);
+  __syncthreads();
+  const int blk = blockIdx.x * kScoreThreads + threadIdx.x;
   if (blk >= a.blocks) return;
+  const long brow = u * a.cap + blk;
   float score = -CUDART_INF_F;
-  if (have) {
-    for (int h0 = 0; h0 < Gp; h0 += 8) {
+  if (in_bounds(a.ctl, a.codes + brow * D, D) && in_bounds(a.ctl, a.scales + brow, 4)) {
+    const float sb = a.scales[brow];
+    const uint4 *kp = reinterpret_cast<const uint4 *>(a.codes + brow * D);
+    for (int h0 = 0; h0 < a.G; h0 += 8) {
       int dot[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      auto piece = [&](const uint4 &k, int c) {
+#pragma unroll 4
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 k = kp[c];
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           const int4 q = *reinterpret_cast<const int4 *>(qs + (h0 + h) * D + 16 * c);
@@ -348,13 +421,6 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
           dot[h] = __dp4a(static_cast<int>(k.z), q.z, dot[h]);
           dot[h] = __dp4a(static_cast<int>(k.w), q.w, dot[h]);
         }
-      };
-      if (k128) {
-#pragma unroll
-        for (int c = 0; c < (k128 ? 8 : 1); ++c) piece(kk[c], c);
-      } else {
-#pragma unroll 4
-        for (int c = 0; c < D / 16; ++c) piece(kp[c], c);
       }
 #pragma unroll
       for (int h = 0; h < 8; ++h)
@@ -587,9 +653,9 @@ int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, 
     const size_t smem = static_cast<size_t>((a.G + 7) / 8 * 8) * a.D;
     const dim3 grid((blocks + kScoreThreads - 1) / kScoreThreads, units);
     if (a.D == 128)
-      launch_dependent(block_scores_kernel<true>, grid, dim3(kScoreThreads), smem, s, a);
+      launch_dependent(block_scores128_kernel, grid, dim3(kScoreThreads), 0, s, a);
     else
-      launch_dependent(block_scores_kernel<false>, grid, dim3(kScoreThreads), smem, s, a);
+      launch_dependent(block_scores_kernel, grid, dim3(kScoreThreads), smem, s, a);
     ++launches;
   }
   launch_dependent(select_kernel, dim3(units), dim3(kSelThreads), 0, s, a);
