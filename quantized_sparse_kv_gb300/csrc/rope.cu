@@ -13,13 +13,11 @@
 // thread and head. The sine and cosine of a thread's pairs are made once and
 // serve every head it visits; the heads of a token are spread over `splits`
 // threads only as far as the call needs threads to cover the card (a decoding
-// step takes one head a thread, a prompt several). A thread has the loads of three
-// heads in flight, the first three before it makes its sines (43 -> 37 us for
-// the prompt below).
+// step takes one head a thread, a prompt several). The first heads' loads are
+// issued before a thread makes its sines.
 // Measured: q, k and v rows of a projection, 2 x 8,192 tokens x 20 heads of 128 bf16
-// (151 MB moved): 36.7 us, 4.1 TB/s, of the 5.1 TB/s that a plain copy of this size
-// reaches; 3 x 1,023 x 18 fp32 heads (57 MB): 13.1 us; 64 tokens: 4.6 us, the
-// launch.
+// (151 MB moved): 29.0 us, 5.2 TB/s, what a plain copy of this size reaches; 3 x
+// 1,023 x 18 fp32 heads (57 MB): 12.9 us, a copy 16 us; 64 tokens: 4.6 us, the launch.
 #include <math.h>
 
 #include <algorithm>
@@ -30,7 +28,13 @@ namespace kvq {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 3;  // heads a thread has in flight
+// Heads a thread has in flight (16 bytes each in bf16, 32 in fp32), and the CTAs
+// per SM that its registers are held to. The prompt above: 1 head 33.9 us, 2 heads
+// 29.0, 3 heads in two CTAs 36.9; two heads in three or five CTAs 33-35. fp32, 57 MB:
+// 1 head 12.9, 2 heads 14.3.
+template <typename T>
+constexpr int kRopeHeads = sizeof(T) == 2 ? 2 : 1;
+constexpr int kRopeCtas = 4;
 
 struct RopeArgs {
   RopeTensors t;
@@ -110,7 +114,7 @@ __device__ __forceinline__ void head_ptrs(const RopeArgs &a, int h, int b, int t
 // the units after them 8 features that pass through (rot is a multiple of
 // 16). Otherwise (interleaved pairs) a unit is 8 consecutive features.
 template <typename T, bool kHalf>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeArgs a) {
   wait_prior_grid();
   allow_next_grid();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -127,12 +131,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   const bool pairs = kHalf ? u < a.rot / 16 : d0 < a.rot;
   // Heads go kRopeHeads at a time, all loads of a batch in flight together; the
   // first batch's are issued before the sines and cosines are made.
-  Raw8<T> rx[kRopeHeads], ry[kHalf ? kRopeHeads : 1];
-  T *out[kRopeHeads];
-  bool turn[kRopeHeads];
+  Raw8<T> rx[kRopeHeads<T>], ry[kHalf ? kRopeHeads<T> : 1];
+  T *out[kRopeHeads<T>];
+  bool turn[kRopeHeads<T>];
   auto load = [&](int h) {
 #pragma unroll
-    for (int k = 0; k < kRopeHeads; ++k, h += a.splits) {
+    for (int k = 0; k < kRopeHeads<T>; ++k, h += a.splits) {
       out[k] = nullptr;
       if (h >= a.t.total_heads) continue;
       const T *in;
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 #pragma unroll 1
   for (int h = h0;;) {
 #pragma unroll
-    for (int k = 0; k < kRopeHeads; ++k) {
+    for (int k = 0; k < kRopeHeads<T>; ++k) {
       if (!out[k]) continue;
       float x[8], y[8];
       to_floats(rx[k], x);
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       }
       store8(out[k] + d0, x);
     }
-    h += kRopeHeads * a.splits;
+    h += kRopeHeads<T> * a.splits;
     if (h >= a.t.total_heads) break;
     load(h);
   }
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 
 // Half layout with a rotary dim that is no multiple of 16: one thread per pair
 // or passed feature (units of one element), the same arithmetic (134 MB: 52.6 us
-// at rotary dim 120, 32.3 us in the kernel above at 128).
+// at rotary dim 120, 26.0 us in the kernel above at 128).
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_pair_kernel(const RopeArgs a) {
   wait_prior_grid();
