@@ -11,13 +11,13 @@
 //
 // What bounds them. The summary reads 20 D bytes of K codes and scales per
 // group and writes D + 4 per block: memory. Scoring reads D + 4 bytes per
-// block, about 1/40 of the block itself, and needs heads * D / 4 dp4a
-// instructions for it; choosing is a radix selection over one score row and
-// bound by latency. Measured, D = 128, blocks of 64: summaries of 32 x 2 x 131,072
-// tokens (671 MB of codes and scales) 108 us, 6.4 TB/s; their values (17 MB read, 67
-// written) 14 us; scores of 8 heads over 64 x 2,046 blocks (17.3 MB) 9.5 us and the
-// choice of 32 5.3 us. Scores and choice in one kernel (a cluster per query
-// token, scores kept in shared memory) took 6 us longer than the two.
+// block, about 1/40 of the block itself, for 2 heads * D integer operations;
+// choosing is a radix selection over one score row and bound by latency. Measured,
+// D = 128, blocks of 64: summaries of 32 x 2 x 131,072 tokens (671 MB of codes and
+// scales) 108 us, 6.4 TB/s; their values (17 MB read, 67 written) 14 us; scores of
+// 8 heads over 64 x 2,046 blocks (17.3 MB, cold) 8.1 us and the choice of 32 of them
+// 5.0 us. Scores and choice in one kernel (a cluster per query token, scores kept in
+// shared memory) took 6 us longer than the two.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -311,80 +311,79 @@ __device__ __forceinline__ void round_queries(const SelectArgs &a, long u, int i
   }
 }
 
-// D = 128. Eight lanes share a block's row, 16 bytes each, so a warp's load is four
-// whole rows, and a thread's eight rows are in flight while q is rounded. A
-// lane's part of eight heads' codes stays in registers; the eight lanes' sums of a
-// row meet in three exchanges that halve what each keeps, head by head, and three
-// more take the largest score.
-constexpr int kScoreRows = 8;  // blocks per eight lanes
+// D = 128, on the int8 tensor cores: a warp's MMA takes 16 blocks x 8 heads x 32
+// features, so four of them and four 16-byte loads a lane score 16 blocks. Lane
+// (g, t) holds bytes 16t .. 16t + 15 and 64 + 16t .. of rows g and g + 8 and of head g:
+// the MMA's feature order is permuted the same way on both sides, which a dot
+// product does not see. A warp's two tiles of 16 blocks are in flight while q is
+// rounded. (Byte dot products: a thread per block 34.0 us for select and attend over
+// 32 sequences of 131,072 tokens, eight lanes a block 30.1, this 28.4.)
+constexpr int kScoreTiles = 2;
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 __global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const SelectArgs a) {
   wait_prior_grid();
   allow_next_grid();
   __shared__ __align__(16) int8_t qs[kMaxGroup * 128];
   __shared__ float sq[kMaxGroup];
-  const int lane = threadIdx.x & 31, part = lane & 7;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int uq = blockIdx.y;  // unit * n_q + query token
   const long u = uq / a.n_q;
   const int iq = uq - static_cast<int>(u) * a.n_q;
-  // row r of the thread's: block first + r * kScoreThreads / 8
-  const int first = blockIdx.x * kScoreThreads + threadIdx.x / 8;
-  uint4 kk[kScoreRows];
-  float sb[kScoreRows];
+  const int first = blockIdx.x * kScoreThreads + 16 * kScoreTiles * warp + g;
+  // rows g and g + 8 of each tile: first + 8 r
+  uint4 k[2 * kScoreTiles][2];
+  float sb[2 * kScoreTiles], best[2 * kScoreTiles];
 #pragma unroll
-  for (int r = 0; r < kScoreRows; ++r) {
-    const int blk = first + r * (kScoreThreads / 8);
-    const long brow = u * a.cap + blk;
-    const bool have = blk < a.blocks && in_bounds(a.ctl, a.codes + brow * 128, 128) &&
-                      in_bounds(a.ctl, a.scales + brow, 4);
-    kk[r] = have ? *reinterpret_cast<const uint4 *>(a.codes + brow * 128 + 16 * part)
-                 : make_uint4(0u, 0u, 0u, 0u);
-    sb[r] = have ? a.scales[brow] : 0.0f;
+  for (int r = 0; r < 2 * kScoreTiles; ++r) {
+    const long row = u * a.cap + first + 8 * r;
+    const bool have = first + 8 * r < a.blocks && in_bounds(a.ctl, a.codes + row * 128, 128) &&
+                      in_bounds(a.ctl, a.scales + row, 4);
+    const uint4 *p = reinterpret_cast<const uint4 *>(a.codes + row * 128) + t;
+    k[r][0] = have ? p[0] : make_uint4(0u, 0u, 0u, 0u);
+    k[r][1] = have ? p[4] : make_uint4(0u, 0u, 0u, 0u);
+    sb[r] = have ? a.scales[row] : 0.0f;
+    best[r] = -CUDART_INF_F;
   }
   round_queries<4>(a, u, iq, 128, qs, sq);
   __syncthreads();
-  float best[kScoreRows];
-#pragma unroll
-  for (int r = 0; r < kScoreRows; ++r) best[r] = -CUDART_INF_F;
 #pragma unroll 1
   for (int h0 = 0; h0 < a.G; h0 += 8) {
-    int4 q[8];
+    const uint4 *qp = reinterpret_cast<const uint4 *>(qs + (h0 + g) * 128) + t;
+    const uint4 q0 = qp[0], q1 = qp[4];
+    const float s0 = sq[h0 + 2 * t], s1 = sq[h0 + 2 * t + 1];
+    const bool on0 = h0 + 2 * t < a.G, on1 = h0 + 2 * t + 1 < a.G;
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
-      q[h] = *reinterpret_cast<const int4 *>(qs + (h0 + h) * 128 + 16 * part);
-    const float s = sq[h0 + part];  // after the exchanges lane `part` holds head h0 + part
+    for (int i = 0; i < kScoreTiles; ++i) {
+      const uint4(&lo)[2] = k[2 * i], (&hi)[2] = k[2 * i + 1];
+      int c[4] = {0, 0, 0, 0};
+      mma_s8(c, lo[0].x, hi[0].x, lo[0].y, hi[0].y, q0.x, q0.y);
+      mma_s8(c, lo[0].z, hi[0].z, lo[0].w, hi[0].w, q0.z, q0.w);
+      mma_s8(c, lo[1].x, hi[1].x, lo[1].y, hi[1].y, q1.x, q1.y);
+      mma_s8(c, lo[1].z, hi[1].z, lo[1].w, hi[1].w, q1.z, q1.w);
 #pragma unroll
-    for (int r = 0; r < kScoreRows; ++r) {
-      int dot[8];
-#pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        int d = __dp4a(static_cast<int>(kk[r].x), q[h].x, 0);
-        d = __dp4a(static_cast<int>(kk[r].y), q[h].y, d);
-        d = __dp4a(static_cast<int>(kk[r].z), q[h].z, d);
-        dot[h] = __dp4a(static_cast<int>(kk[r].w), q[h].w, d);
+      for (int r = 0; r < 2; ++r) {
+        const float x0 = __fmul_rn(__fmul_rn(s0, sb[2 * i + r]), static_cast<float>(c[2 * r]));
+        const float x1 = __fmul_rn(__fmul_rn(s1, sb[2 * i + r]), static_cast<float>(c[2 * r + 1]));
+        if (on0) best[2 * i + r] = fmaxf(best[2 * i + r], x0);
+        if (on1) best[2 * i + r] = fmaxf(best[2 * i + r], x1);
       }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        const bool up = part & o;
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (h < o) {
-            const int send = up ? dot[h] : dot[h + o], keep = up ? dot[h + o] : dot[h];
-            dot[h] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
-      }
-      const float x = __fmul_rn(__fmul_rn(s, sb[r]), static_cast<float>(dot[0]));
-      if (h0 + part < a.G) best[r] = fmaxf(best[r], x);
     }
   }
 #pragma unroll
-  for (int r = 0; r < kScoreRows; ++r) {
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], o));
-    const int blk = first + r * (kScoreThreads / 8);
+  for (int r = 0; r < 2 * kScoreTiles; ++r) {
+    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+    const int blk = first + 8 * r;
     float *o = a.scores + static_cast<long>(uq) * a.stride + blk;
-    if (part == 0 && blk < a.blocks && in_bounds(a.ctl, o, 4))
+    if (t == 0 && blk < a.blocks && in_bounds(a.ctl, o, 4))
       *o = blk < a.sink ? CUDART_INF_F : best[r];
   }
 }
