@@ -372,3 +372,30 @@ def test_captured_streams_and_wait(kvq):  # noqa: F811
     assert kvq.read_status(a1.status) == kvq.DEV_TIMEOUT
     a1.status.zero_()
     assert torch.equal(a1.run(), w[0]) and kvq.read_status(a1.status) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("g,nq,n,dt", [(12, 3, 3000, torch.bfloat16), (33, 1, 5000, torch.float32),
+                                       (64, 2, 900, torch.bfloat16), (2, 5, 4100, torch.float32)])
+def test_select_many_heads(kvq, g, nq, n, dt):  # noqa: F811
+    """Head counts that fill eight columns of the scores' MMA several times, or in part."""
+    c = make(kvq, 2, 1, n, 128, 36)
+    s = kvq.BlockSummary(c, 32).update()
+    q = query(2, g, nq, 128, dt)
+    a = kvq.AttendBlocks(c, q, s, 9, n_sink=1)
+    a.run()
+    assert kvq.read_status(a.status) == 0
+    codes, scales = plain_summary(c, 32)
+    assert np.array_equal(a.selected.cpu().numpy(), plain_select(q, codes, scales, 1, 9, 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g", [(64, 1), (64, 3), (96, 6), (224, 5), (256, 9)])
+def test_attend_fp32_kernel_shared_heads(kvq, d, g):  # noqa: F811
+    """Query heads share the fp32 kernel's keys four at a time: whole groups and parts."""
+    c = make(kvq, 2, 2, 500, d, 41)
+    q = query(2, 2 * g, 2, d)
+    a = kvq.AttendBlocks(c, q, kvq.BlockSummary(c, 64).update(), 3, out_dtype="f32")
+    out = a.run()
+    assert kvq.read_status(a.status) == 0 and a.path == "blocks_rows"
+    assert rel(out, plain_attend(c, kvq, q, a.selected, 64)) <= TOL_F32

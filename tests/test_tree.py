@@ -454,3 +454,20 @@ def test_many_runs_agree(kvq, case):
     for _ in range(200):
         differ += (call.run() != first).any()
     assert int(differ) == 0 and kvq.read_status(call.status) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g", [(64, 1), (64, 3), (96, 6), (224, 5), (256, 9)])
+def test_fp32_path_shared_heads(kvq, d, g):
+    """Query heads share the fp32 kernel's keys four at a time: whole groups and parts."""
+    b, hkv, t = 2, 2, 9
+    c = make(kvq, b, hkv, 420, d, 37)
+    q, k, v = inputs(b, g * hkv, hkv, t, d)
+    par = random_tree(b, t, d + g, pad=True)
+    out = torch.full(q.shape, 7.0, device="cuda")
+    a = kvq.AttendTree(c, q, k, v, par, out=out)
+    a.run()
+    assert kvq.read_status(a.status) == 0 and a.path == "tree_rows"
+    compare(out, plain(c, kvq, q, k, v, par), par, TOL_F32)
+    dead = (par == -2)[:, None, :, None].expand_as(out)
+    assert bool((out[dead] == 7.0).all())
