@@ -16,8 +16,8 @@
 // D = 128, blocks of 64: summaries of 32 x 2 x 131,072 tokens (671 MB of codes and
 // scales) 108 us, 6.4 TB/s; their values (17 MB read, 67 written) 14 us; scores of
 // 8 heads over 64 x 2,046 blocks (17.3 MB, cold) 8.1 us and the choice of 32 of them
-// 5.0 us. Scores and choice in one kernel (a cluster per query token, scores kept in
-// shared memory) took 6 us longer than the two.
+// 5.0 us. Scores and choice in one kernel for this many blocks (a cluster per query
+// token, scores kept in shared memory) took 6 us longer than the two.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -281,11 +281,11 @@ constexpr int kMaxGroup = 64;  // query heads per KV head
 
 // The rows of q of a (unit, query token) as int8 to shared memory, G heads padded with
 // zeros to a multiple of eight: a warp per row, its largest magnitude first.
-template <int kPer>  // features a lane holds
+template <int kPer, int kThreads>  // features a lane holds, threads of the CTA
 __device__ __forceinline__ void round_queries(const SelectArgs &a, long u, int iq, int D,
                                               int8_t *qs, float *sq) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int h = warp; h < (a.G + 7) / 8 * 8; h += kScoreThreads / 32) {
+  for (int h = warp; h < (a.G + 7) / 8 * 8; h += kThreads / 32) {
     const long row = (u * a.G + h) * a.n_q + iq;  // [batch][q_heads][n_q], q head = kv * G + h
     float x[kPer], mx = 0.0f;
 #pragma unroll
@@ -328,32 +328,30 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const SelectArgs a) {
-  wait_prior_grid();
-  allow_next_grid();
-  __shared__ __align__(16) int8_t qs[kMaxGroup * 128];
-  __shared__ float sq[kMaxGroup];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int uq = blockIdx.y;  // unit * n_q + query token
-  const long u = uq / a.n_q;
-  const int iq = uq - static_cast<int>(u) * a.n_q;
-  const int first = blockIdx.x * kScoreThreads + 16 * kScoreTiles * warp + g;
-  // rows g and g + 8 of each tile: first + 8 r
+// Rows g and g + 8 of a warp's tiles, blocks first + 8 r.
+struct ScoreRows {
   uint4 k[2 * kScoreTiles][2];
-  float sb[2 * kScoreTiles], best[2 * kScoreTiles];
+  float s[2 * kScoreTiles];
+};
+__device__ __forceinline__ void load_rows(const SelectArgs &a, long u, int first, int t,
+                                          ScoreRows &x) {
 #pragma unroll
   for (int r = 0; r < 2 * kScoreTiles; ++r) {
     const long row = u * a.cap + first + 8 * r;
     const bool have = first + 8 * r < a.blocks && in_bounds(a.ctl, a.codes + row * 128, 128) &&
                       in_bounds(a.ctl, a.scales + row, 4);
     const uint4 *p = reinterpret_cast<const uint4 *>(a.codes + row * 128) + t;
-    k[r][0] = have ? p[0] : make_uint4(0u, 0u, 0u, 0u);
-    k[r][1] = have ? p[4] : make_uint4(0u, 0u, 0u, 0u);
-    sb[r] = have ? a.scales[row] : 0.0f;
-    best[r] = -CUDART_INF_F;
+    x.k[r][0] = have ? p[0] : make_uint4(0u, 0u, 0u, 0u);
+    x.k[r][1] = have ? p[4] : make_uint4(0u, 0u, 0u, 0u);
+    x.s[r] = have ? a.scales[row] : 0.0f;
   }
-  round_queries<4>(a, u, iq, 128, qs, sq);
-  __syncthreads();
+}
+// Their scores (in every lane of a row).
+__device__ __forceinline__ void score_rows(const SelectArgs &a, const ScoreRows &x,
+                                           const int8_t *qs, const float *sq, int first, int g,
+                                           int t, float (&best)[2 * kScoreTiles]) {
+#pragma unroll
+  for (int r = 0; r < 2 * kScoreTiles; ++r) best[r] = -CUDART_INF_F;
 #pragma unroll 1
   for (int h0 = 0; h0 < a.G; h0 += 8) {
     const uint4 *qp = reinterpret_cast<const uint4 *>(qs + (h0 + g) * 128) + t;
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const Se
     const bool on0 = h0 + 2 * t < a.G, on1 = h0 + 2 * t + 1 < a.G;
 #pragma unroll
     for (int i = 0; i < kScoreTiles; ++i) {
-      const uint4(&lo)[2] = k[2 * i], (&hi)[2] = k[2 * i + 1];
+      const uint4(&lo)[2] = x.k[2 * i], (&hi)[2] = x.k[2 * i + 1];
       int c[4] = {0, 0, 0, 0};
       mma_s8(c, lo[0].x, hi[0].x, lo[0].y, hi[0].y, q0.x, q0.y);
       mma_s8(c, lo[0].z, hi[0].z, lo[0].w, hi[0].w, q0.z, q0.w);
@@ -370,8 +368,9 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const Se
       mma_s8(c, lo[1].z, hi[1].z, lo[1].w, hi[1].w, q1.z, q1.w);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float x0 = __fmul_rn(__fmul_rn(s0, sb[2 * i + r]), static_cast<float>(c[2 * r]));
-        const float x1 = __fmul_rn(__fmul_rn(s1, sb[2 * i + r]), static_cast<float>(c[2 * r + 1]));
+        const float sb = x.s[2 * i + r];
+        const float x0 = __fmul_rn(__fmul_rn(s0, sb), static_cast<float>(c[2 * r]));
+        const float x1 = __fmul_rn(__fmul_rn(s1, sb), static_cast<float>(c[2 * r + 1]));
         if (on0) best[2 * i + r] = fmaxf(best[2 * i + r], x0);
         if (on1) best[2 * i + r] = fmaxf(best[2 * i + r], x1);
       }
@@ -381,10 +380,30 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const Se
   for (int r = 0; r < 2 * kScoreTiles; ++r) {
     best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
     best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+    if (first + 8 * r < a.sink) best[r] = CUDART_INF_F;
+  }
+}
+
+__global__ void __launch_bounds__(kScoreThreads) block_scores128_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ __align__(16) int8_t qs[kMaxGroup * 128];
+  __shared__ float sq[kMaxGroup];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int uq = blockIdx.y;  // unit * n_q + query token
+  const long u = uq / a.n_q;
+  const int first = blockIdx.x * kScoreThreads + 16 * kScoreTiles * warp + g;
+  ScoreRows x;
+  load_rows(a, u, first, t, x);
+  round_queries<4, kScoreThreads>(a, u, uq - static_cast<int>(u) * a.n_q, 128, qs, sq);
+  __syncthreads();
+  float best[2 * kScoreTiles];
+  score_rows(a, x, qs, sq, first, g, t, best);
+#pragma unroll
+  for (int r = 0; r < 2 * kScoreTiles; ++r) {
     const int blk = first + 8 * r;
     float *o = a.scores + static_cast<long>(uq) * a.stride + blk;
-    if (t == 0 && blk < a.blocks && in_bounds(a.ctl, o, 4))
-      *o = blk < a.sink ? CUDART_INF_F : best[r];
+    if (t == 0 && blk < a.blocks && in_bounds(a.ctl, o, 4)) *o = best[r];
   }
 }
 
@@ -398,7 +417,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
   const int uq = blockIdx.y;  // unit * n_q + query token
   const long u = uq / a.n_q;
   const int iq = uq - static_cast<int>(u) * a.n_q;
-  round_queries<8>(a, u, iq, D, qs, sq);
+  round_queries<8, kScoreThreads>(a, u, iq, D, qs, sq);
   __syncthreads();
   const int blk = blockIdx.x * kScoreThreads + threadIdx.x;
   if (blk >= a.blocks) return;
@@ -489,24 +508,12 @@ __device__ __forceinline__ void load_keys(const float *sc, int base, int blocks,
   }
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-  wait_prior_grid();
-  allow_next_grid();
+// The k = top_k blocks of the score row sc (k < blocks) to out, by the whole CTA.
+__device__ __forceinline__ void select_row(const SelectArgs &a, const float *sc, int32_t *out) {
   __shared__ int hist[2][256], warp_sums[2][kSelThreads / 32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left, s_whole;
-  const int tid = threadIdx.x;
-  const long uq = blockIdx.x;
-  const float *sc = a.scores + uq * a.stride;
-  int32_t *out = a.selected + uq * a.top_k;
-  const int k = min(a.top_k, a.blocks);
-  if (!in_bounds(a.ctl, out, sizeof(int32_t) * a.top_k)) return;
-  for (int i = k + tid; i < a.top_k; i += kSelThreads) out[i] = -1;
-  if (a.blocks <= a.top_k) {
-    for (int i = tid; i < a.blocks; i += kSelThreads) out[i] = i;
-    return;
-  }
-  if (!in_bounds(a.ctl, sc, sizeof(float) * a.stride)) return;
+  const int tid = threadIdx.x, k = a.top_k;
   constexpr int kPiece = kSelThreads * kSelKeys;
   const bool one = a.blocks <= kPiece;
   uint32_t key[kSelKeys];
@@ -569,6 +576,63 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     written += (total & 0xffff) + min(equal_before + eq_total, left) - min(equal_before, left);
     equal_before += eq_total;
   }
+}
+
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  const long uq = blockIdx.x;
+  const float *sc = a.scores + uq * a.stride;
+  int32_t *out = a.selected + uq * a.top_k;
+  if (!in_bounds(a.ctl, out, sizeof(int32_t) * a.top_k)) return;
+  if (a.blocks <= a.top_k) {  // all of them, then -1
+    for (int i = threadIdx.x; i < a.top_k; i += kSelThreads) out[i] = i < a.blocks ? i : -1;
+    return;
+  }
+  if (!in_bounds(a.ctl, sc, sizeof(float) * a.stride)) return;
+  select_row(a, sc, out);
+}
+
+// Few blocks, D = 128: scores and choice in one CTA per (unit, query token), the
+// scores in shared memory. Against the two kernels (select and attend together, 8
+// heads): 253 blocks of 160 query tokens 24.0 us (25.6), 508 of 64 19.3 (20.4), 510 of 2
+// 13.0 (13.0); 1,016 blocks of 64 21.2 (21.8), of 128 27.2 (28.3), but 1,022 of 2 15.1
+// (13.6) and 2,046 of 64 27.9 (25.9): one CTA's pass over the blocks has to be short, or
+// the card full.
+constexpr int kFewBlocks = 1024;
+__host__ bool few_blocks(long units, int blocks) {
+  return blocks <= (units < 64 ? kFewBlocks / 2 : kFewBlocks);
+}
+
+__global__ void __launch_bounds__(kSelThreads) score_select128_kernel(const SelectArgs a) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ __align__(16) int8_t qs[kMaxGroup * 128];
+  __shared__ __align__(16) float sc[kFewBlocks];
+  __shared__ float sq[kMaxGroup];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int uq = blockIdx.x;  // unit * n_q + query token
+  const long u = uq / a.n_q;
+  int32_t *out = a.selected + static_cast<long>(uq) * a.top_k;
+  if (!in_bounds(a.ctl, out, sizeof(int32_t) * a.top_k)) return;
+  ScoreRows x;
+  int first = 16 * kScoreTiles * warp + g;
+  load_rows(a, u, first, t, x);
+  round_queries<4, kSelThreads>(a, u, uq - static_cast<int>(u) * a.n_q, 128, qs, sq);
+  __syncthreads();
+#pragma unroll 1
+  for (;;) {
+    float best[2 * kScoreTiles];
+    score_rows(a, x, qs, sq, first, g, t, best);
+#pragma unroll
+    for (int r = 0; r < 2 * kScoreTiles; ++r)
+      if (t == 0 && first + 8 * r < a.blocks) sc[first + 8 * r] = best[r];
+    first += kSelThreads / 2 * kScoreTiles;  // 16 blocks a warp and tile
+    if (first - g >= a.blocks) break;
+    load_rows(a, u, first, t, x);
+  }
+  __syncthreads();
+  select_row(a, sc, out);
 }
 
 }  // namespace
@@ -648,6 +712,10 @@ int launch_select_blocks(const kvq_cache &c, const kvq_summary &sm, int blocks, 
   a.ctl = ctl;
   const unsigned units = static_cast<unsigned>(c.batch) * c.kv_heads * n_q;
   int launches = 0;
+  if (blocks > top_k && a.D == 128 && few_blocks(units, blocks)) {
+    launch_dependent(score_select128_kernel, dim3(units), dim3(kSelThreads), 0, s, a);
+    return 1;
+  }
   if (blocks > top_k) {
     const size_t smem = static_cast<size_t>((a.G + 7) / 8 * 8) * a.D;
     const dim3 grid((blocks + kScoreThreads - 1) / kScoreThreads, units);
