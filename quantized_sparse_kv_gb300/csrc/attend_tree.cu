@@ -972,7 +972,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
 // blocks, each over many CTAs): one block per 16 features, its warps take every
 // eighth slot and meet in shared memory.
 constexpr int kCombineWarps = 8;
-constexpr int kWideAbove = 12;  // slots per row block
+// Slots per row block above which kWide is used. Whole calls, wide and not: 9 slots
+// (1 sequence x 1 token, 1,024 keys) 11.3 and 11.9 us, 11 (8 x 8, 8,192) 20.9 and
+// 23.3, 130 (1 x 8, 32,768) 21.6 and 43.7; 6 (16 x 8, 8,200) 32.4 and 31.0.
+constexpr int kWideAbove = 8;
 
 struct RowState {
   float m, l, o[16];
