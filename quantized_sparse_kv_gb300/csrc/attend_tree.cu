@@ -972,10 +972,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
 // blocks, each over many CTAs): one block per 16 features, its warps take every
 // eighth slot and meet in shared memory.
 constexpr int kCombineWarps = 8;
-// Slots per row block above which kWide is used. Whole calls, wide and not: 9 slots
-// (1 sequence x 1 token, 1,024 keys) 11.3 and 11.9 us, 11 (8 x 8, 8,192) 20.9 and
-// 23.3, 130 (1 x 8, 32,768) 21.6 and 43.7; 6 (16 x 8, 8,200) 32.4 and 31.0.
-constexpr int kWideAbove = 8;
+// The narrow form takes a row block's slots one after the other, which the wide one
+// does eight at a time with eight times the CTAs: it pays while those are few. Whole
+// calls in us, wide and narrow, sequences x tokens, keys: 1 x 1, 1,024 11.2, 12.0; 4 x
+// 16, 8,192 19.7, 26.0; 1 x 64, 32,768 29.4, 42.3; 8 x 8, 8,192 21.0, 23.4; 2 x 64,
+// 32,768 42.5, 46.2; but 16 x 8, 8,200 32.5, 31.2; 4 x 64, 8,192 36.0, 32.4; 3 x 100,
+// 16,384 63.1, 58.1.
+__host__ bool wide_combine(int slots, long ctas) { return slots > 3 && 8L * slots > ctas; }
 
 struct RowState {
   float m, l, o[16];
@@ -1168,7 +1171,7 @@ int launch_attend_tree(const kvq_cache &c, const void *q, int Hq, int T, const v
   launch_dependent(tree_kernel, dim3(p.ctas), dim3(kThreads), smem, s, a);
   const unsigned blocks = static_cast<unsigned>(p.units * p.row_blocks);
   const unsigned groups = static_cast<unsigned>(std::min(p.rows, kRowBlock) + 31) / 32;
-  if (p.slots > kWideAbove)
+  if (wide_combine(p.slots, static_cast<long>(blocks) * groups))
     launch_dependent(tree_combine_kernel<true>, dim3(blocks, groups, kD / 16),
                      dim3(kCombineWarps * 32), 0, s, a);
   else
