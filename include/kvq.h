@@ -547,6 +547,8 @@ KVQ_API kvq_status kv_block_values(const kvq_cache *cache, const kvq_summary *su
  * (before the others, n_sink <= top_k). Every step is exact or a single fp32
  * rounding, so the choice is the same whatever the order of the work.
  * q: [batch][q_heads][n_q][D] in q_dtype (F32 or BF16), finite.
+ * The summaries of all n_blocks blocks must be there (kv_block_summary, again
+ * for the new blocks after appends).
  * selected: device int32 [batch][kv_heads][n_q][top_k], the chosen blocks in
  * increasing order, then -1 when the cache has fewer than top_k blocks.
  * workspace/ws_bytes as kv_attend. KVQ_ERR_UNSUPPORTED for q_heads / kv_heads

@@ -834,7 +834,9 @@ class BlockSummary(_Prepared):
 class AttendBlocks(_Prepared):
     """A prepared pair of calls, kv_select_blocks and kv_attend_blocks: each
     query token of a KV head attends the ``top_k`` blocks its summary scores
-    highest and the whole window. ``selected`` (batch, kv_heads, n_q, top_k)
+    highest and the whole window. The summary is the caller's to keep up with the
+    cache (``BlockSummary.update`` after appends that moved groups into the int4
+    part). ``selected`` (batch, kv_heads, n_q, top_k)
     holds the chosen blocks after ``run()``; ``select=False`` attends the lists
     already there (``selected`` may be passed)."""
 
@@ -865,7 +867,9 @@ class AttendBlocks(_Prepared):
             raise ValueError("selected must be int32 (batch, kv_heads, n_q, top_k), dense")
         self.selected = selected
         self.q_dt = F32 if self.q.dtype == torch.float32 else BF16
-        self.out_dt = _dtype(out_dtype) if out_dtype is not None else self.q_dt
+        self.out_dt = (_dtype(out_dtype) if out_dtype is not None else
+                       self.q_dt if out is None else
+                       F32 if out.dtype == torch.float32 else BF16)
         self.out = out if out is not None else torch.empty(
             (b, hq, nq, d), dtype=TORCH_OF[self.out_dt], device=self.q.device)
         if (self.out.shape != self.q.shape or self.out.dtype != TORCH_OF[self.out_dt] or

@@ -399,3 +399,15 @@ def test_attend_fp32_kernel_shared_heads(kvq, d, g):  # noqa: F811
     out = a.run()
     assert kvq.read_status(a.status) == 0 and a.path == "blocks_rows"
     assert rel(out, plain_attend(c, kvq, q, a.selected, 64)) <= TOL_F32
+
+
+@pytest.mark.gpu
+def test_out_decides_the_output_type(kvq):  # noqa: F811
+    c = make(kvq, 1, 2, 300, 128, 44)
+    q = query(1, 16, 1, 128)
+    s = kvq.BlockSummary(c, 32).update()
+    want = kvq.AttendBlocks(c, q, s, 4, out_dtype="f32").run()
+    out = torch.empty(q.shape, device="cuda")
+    assert kvq.AttendBlocks(c, q, s, 4, out=out).run() is out and torch.equal(out, want)
+    with pytest.raises(ValueError):
+        kvq.AttendBlocks(c, q, s, 4, out=out.half())
