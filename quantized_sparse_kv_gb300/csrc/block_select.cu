@@ -152,9 +152,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) summary128_kernel(const Summar
 // ------------------------------------------------------------------ any D
 // One warp per block again, a lane per 4 bytes (8 channels) of a token row and as
 // many rows at once as fit the warp (a power of two). A word's channels are summed
-// as 16-bit halves (32 tokens' worth is 480), the row lanes' sums meet in the
-// first row's, which hold eight channels each from there on. (D = 64, 84 MB: 41.6 us;
-// the kernel above takes 16.8 us for as much at D = 128.)
+// as bytes for 16 tokens (240 at most) and as 16-bit halves from there on, the row
+// lanes' sums meet in the first row's, which hold eight channels each then.
+// (D = 64, 84 MB: 34.2 us; the kernel above takes 16.8 us for as much at D = 128.)
+template <int kRows>  // token rows at once
 __global__ void __launch_bounds__(kSumWarps * 32) summary_kernel(const SummaryArgs a) {
   wait_prior_grid();
   allow_next_grid();
@@ -165,9 +166,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) summary_kernel(const SummaryAr
   const long u = id / per;
   const int blk = a.first + static_cast<int>(id - u * per);
   const int pieces = D / 8;  // lanes per token row
-  const int rows = pieces > 16 ? 1 : pieces > 8 ? 2 : pieces > 4 ? 4 : 8;
   const int row = lane / pieces, piece = lane - row * pieces;
-  const bool on = row < rows;
+  const bool on = row < kRows;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
@@ -182,15 +182,28 @@ __global__ void __launch_bounds__(kSumWarps * 32) summary_kernel(const SummaryAr
       s1 = *reinterpret_cast<const float4 *>(s + 4);
     }
     uint32_t sum[4] = {0u, 0u, 0u, 0u};  // sum[k]: channels k (low half) and k + 4
-#pragma unroll 8
-    for (int t = 0; t < 32; t += rows) {
-      const uint8_t *w = p + t * (D / 2);
-      const uint32_t x = on && in_bounds(a.ctl, w, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(w))
-                                                      : 0x88888888u;
+    constexpr int kTokens = kRows == 1 ? 16 : 32 / kRows;  // of a lane, in bytes
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[k] += (x >> (4 * k)) & 0x000F000Fu;
+    for (int t0 = 0; t0 < 32; t0 += kTokens * kRows) {
+      uint32_t lo = 0u, hi = 0u, x[kTokens];  // bytes: channels 0, 2, 4, 6 and 1, 3, 5, 7
+#pragma unroll
+      for (int t = 0; t < kTokens; ++t) {
+        const uint8_t *w = p + (t0 + t * kRows) * (D / 2);
+        x[t] = on && in_bounds(a.ctl, w, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(w))
+                                            : 0x88888888u;
+      }
+#pragma unroll
+      for (int t = 0; t < kTokens; ++t) {
+        lo += x[t] & 0x0F0F0F0Fu;
+        hi += (x[t] >> 4) & 0x0F0F0F0Fu;
+      }
+      sum[0] += lo & 0x00FF00FFu;
+      sum[1] += hi & 0x00FF00FFu;
+      sum[2] += (lo >> 8) & 0x00FF00FFu;
+      sum[3] += (hi >> 8) & 0x00FF00FFu;
     }
-    for (int r = rows / 2; r > 0; r /= 2) {
+#pragma unroll
+    for (int r = kRows / 2; r > 0; r /= 2) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) sum[k] += __shfl_down_sync(0xffffffffu, sum[k], r * pieces);
     }
@@ -657,8 +670,14 @@ int launch_block_summary(const kvq_cache &c, const kvq_summary &sm, int first, i
   a.ctl = ctl;
   const long warps = a.units * (blocks - first);
   const dim3 grid(static_cast<unsigned>((warps + kSumWarps - 1) / kSumWarps)), block(kSumWarps * 32);
-  if (d.D != 128)
-    launch_dependent(summary_kernel, grid, block, 0, s, a);
+  if (d.D > 128)
+    launch_dependent(summary_kernel<1>, grid, block, 0, s, a);
+  else if (d.D == 96)
+    launch_dependent(summary_kernel<2>, grid, block, 0, s, a);
+  else if (d.D == 64)
+    launch_dependent(summary_kernel<4>, grid, block, 0, s, a);
+  else if (d.D == 32)
+    launch_dependent(summary_kernel<8>, grid, block, 0, s, a);
   else if (a.m == 1)
     launch_dependent(summary128_kernel<1>, grid, block, 0, s, a);
   else if (a.m == 2)
