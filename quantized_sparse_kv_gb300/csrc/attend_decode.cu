@@ -772,8 +772,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__
     float nm = m;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, pm[i]);
-    if (nm == -CUDART_INF_F) continue;
-    const float r = exp2f(m - nm);  // 0 while m is -inf
+    // (no finite score so far: against 0 every weight is 0, and a NaN sum stays one)
+    const float ref = nm == -CUDART_INF_F ? 0.0f : nm;
+    const float r = exp2f(m - ref);  // 0 while m is -inf
     l *= r;
     acc.x *= r;
     acc.y *= r;
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__
     acc.w *= r;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2f(pm[i] - nm);  // 0 for empty and padded slots
+      const float w = exp2f(pm[i] - ref);  // 0 for empty and padded slots
       l += w * pl[i];
       acc.x += w * po[i].x;
       acc.y += w * po[i].y;
@@ -840,8 +841,9 @@ __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
     float nm = m;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, pm[i]);
-    if (nm == -CUDART_INF_F) continue;
-    const float r = exp2f(m - nm);  // 0 while m is -inf
+    // (no finite score so far: against 0 every weight is 0, and a NaN sum stays one)
+    const float ref = nm == -CUDART_INF_F ? 0.0f : nm;
+    const float r = exp2f(m - ref);  // 0 while m is -inf
     l *= r;
     acc.x *= r;
     acc.y *= r;
@@ -849,7 +851,7 @@ __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
     acc.w *= r;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2f(pm[i] - nm);  // 0 for empty and padded slots
+      const float w = exp2f(pm[i] - ref);  // 0 for empty and padded slots
       l += w * pl[i];
       acc.x += w * po[i].x;
       acc.y += w * po[i].y;
