@@ -459,7 +459,8 @@ __device__ __forceinline__ int listed_group(const DecodeArgs &a, int x, int w) {
   const int u = x / a.ipu, j = x - u * a.ipu;
   if (j >= a.Gi) return -1;
   const int gl = kGroupsPerItem * j + w, e = gl / a.gpb, sub = gl - e * a.gpb;
-  if (e >= a.top_k) return -1;
+  // (increasing blocks: entries past the n_blocks-th hold none and are not looked at)
+  if (e >= min(a.top_k, a.n_blocks)) return -1;
   const int32_t *l = a.list + static_cast<long>(u) * a.top_k + e;
   if (!in_bounds(a.ctl, e > 0 ? l - 1 : l, sizeof(int32_t) * (e > 0 ? 2 : 1))) return -1;
   const int blk = *l, prev = e > 0 ? l[-1] : -2;

@@ -1,13 +1,14 @@
-"""Attention over listed blocks where a row or a key holds NaN.
+"""Attention over listed blocks: rows and keys that hold NaN, and long lists.
 
 A row whose scores are NaN is NaN in every kernel, whatever the type of q and
 however many partial results its keys give; rows beside it keep their bits, and
-rows without keys stay zero.
+rows without keys stay zero. Entries of a list past the number of blocks are not
+looked at, wherever they fall among the four groups of an item.
 """
 import pytest
 import torch
 
-from test_blocks import query
+from test_blocks import TOL_DECODE, TOL_F32, plain_attend, query, rel
 from test_tree import kvq, make  # noqa: F401 (fixture)
 
 # b, hkv, n, window, block, blocks listed. Partials of a unit in the decode kernels (bf16 q, on
@@ -93,3 +94,27 @@ def test_a_nan_key_reaches_every_row_of_dense_decoding(kvq, b, n):  # noqa: F811
     assert bool(torch.isnan(out[0, 8:]).all())
     out[0, 8:], want[0, 8:] = 0.0, 0.0
     assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block,blocks", [(64, 11), (64, 1), (32, 9), (32, 10), (32, 11), (128, 3)])
+def test_entries_past_the_number_of_blocks_are_not_looked_at(kvq, dt, block, blocks):  # noqa: F811
+    c = make(kvq, 1, 2, block * blocks, 128, 0)
+    q = query(1, 16, 1, 128, dt)
+    full = list(range(blocks))
+
+    def run(row):
+        sel = torch.tensor([[[row], [row]]], dtype=torch.int32, device="cuda")
+        a = kvq.AttendBlocks(c, q, None, len(row), out_dtype="f32", selected=sel, block=block)
+        out = a.run(select=False)
+        return out.clone(), kvq.read_status(a.status)
+    sel = torch.tensor([[[full], [full]]], dtype=torch.int32)
+    want = plain_attend(c, kvq, q, sel, block)
+    tol = TOL_DECODE if dt == torch.bfloat16 else TOL_F32
+    for tail in ([99], [0], [blocks], [-2, 99, 3, 3], [-1, 0, 5]):
+        out, st = run(full + tail)
+        assert st == 0 and rel(out, want) <= tol, tail
+    # the last entry looked at may still be bad
+    out, st = run(full[:-1] + [blocks, 0, 0, 0])
+    assert st == kvq.DEV_INDEX
