@@ -517,8 +517,9 @@ typedef struct kvq_summary {
  * group and s its scale of a channel: part_g = fl(s * sum c) per 32-token
  * group, the groups' parts added in order in fp32, mean = fl(sum / tokens),
  * scale = fl(max over D of |mean| / 127), code = rint(fl(mean / scale)), ties
- * to even (0 for a zero scale): integers and single fp32 roundings, so the
- * result does not depend on the order of the work. After kv_append moved
+ * to even, held to [-127, 127] (a subnormal scale is rounded coarsely; 0 for a
+ * zero scale): integers and single fp32 roundings, so the result does not
+ * depend on the order of the work. After kv_append moved
  * groups out of the window, the blocks from floor(old cut / block) on are
  * new; first_block >= n_blocks enqueues nothing.
  * KVQ_ERR_ARG: block not 32, 64 or 128, first_block < 0; KVQ_ERR_WORKSPACE:
@@ -540,7 +541,7 @@ KVQ_API kvq_status kv_block_values(const kvq_cache *cache, const kvq_summary *su
 /*
  * kv_select_blocks -- for each query token of each KV head the top_k blocks by
  * a cheap score. Each query row is rounded to int8 (scale s_q = fl(max|q| /
- * 127), code = rint(fl(q / s_q))); a block's score for a head is
+ * 127), code = rint(fl(q / s_q)) held to [-127, 127]); a block's score for a head is
  * fl(fl(s_q * s_b) * d), d the integer product of the codes, and its score
  * for the KV head the largest over the query heads that share it. Equal
  * scores: the lower block first. The first n_sink blocks are always taken

@@ -27,9 +27,10 @@
 namespace kvq {
 namespace {
 
-// fl(x / s) rounded to an integer, 0 for a zero scale.
+// fl(x / s) rounded to an integer in [-127, 127], 0 for a zero scale. |x / s| passes
+// 127.5 only where s = fl(max / 127) is subnormal, rounded by up to a third of itself.
 __device__ __forceinline__ int int8_code(float x, float s) {
-  return s > 0.0f ? __float2int_rn(__fdiv_rn(x, s)) : 0;
+  return s > 0.0f ? max(-127, min(127, __float2int_rn(__fdiv_rn(x, s)))) : 0;
 }
 
 struct SummaryArgs {
