@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mbar_init(smem_u32(&sm.k_empty[i >> 1][i & 1]), 2);
       mbar_init(smem_u32(&sm.v_empty[i >> 1][i & 1]), 2);
     }
-    mbar_init(smem_u32(&sm.q_full), 2 * kBM);
+    mbar_init(smem_u32(&sm.q_full), 2 * kBM + 4);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sm.s_full[i >> 1][i & 1]), 1);
       mbar_init(smem_u32(&sm.p_full[i >> 1][i & 1]), kBM / 32);
@@ -564,12 +564,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     uint32_t other = 0;   // the other buffer's in earlier segments
     bool ok = true;
     uint32_t x = lo;
+    // A segment's queries are announced by the softmax threads and by the four MMA
+    // warps, each of which has seen the announcement before: a warp without a step in a
+    // segment (shared rows, one tile) cannot fall two phases of q_full behind.
+    if (elect_one()) mbar_arrive(smem_u32(&sm.q_full));
+    __syncwarp();
     for (Segment sg; ok && next_segment(a, x, hi, sg); ++seg) {
       const int n = uniform(sg.n);
       const int row0 = kRowBlock * static_cast<int>(sg.rb % static_cast<uint32_t>(a.row_blocks));
       const bool two = uniform(a.rows - row0 > kBM ? 1u : 0u) != 0u;
       const uint32_t qd = q_lo + (two ? g : 0u) * (kTileBytes >> 4);
       if (!spin_wait(abort_flag, smem_u32(&sm.q_full), seg & 1, a.ctl)) break;
+      if (elect_one()) mbar_arrive(smem_u32(&sm.q_full));
+      __syncwarp();
       // Two groups of rows: step s is half s & 1 of tile s / 2, and each half of a
       // stage is freed by both groups. Shared rows: step s is half g of tile s,
       // freed by that group alone, in both arrivals.
