@@ -485,7 +485,10 @@ KVQ_API kvq_status kv_rope(const kvq_rope_tensor *tensors, int32_t n_tensors, in
  * drafted rows converted from bf16 (exact within fp16's normal range, 6e-5 to
  * 65504; larger values, infinite ones too, count as 65504), products and sums
  * in fp32. Scales of the int4 part belong in that range too: smaller ones keep
- * fewer bits, and 7 * scale above 65504 overflows.
+ * fewer bits, and 7 * scale above 65504 overflows. Probabilities are rounded to
+ * fp16 against a reference near the row's maximum: those of keys more than 15.9
+ * nats below the maximum keep fewer than 11 bits, and those of keys more than 23
+ * nats below it may be dropped from the output (the sum keeps them).
  * Other shapes run an fp32 kernel (q_heads and batch <= 65,535).
  */
 #define KVQ_TREE_MAX 256

@@ -35,8 +35,8 @@
 // the hand-overs of the last step run.
 //
 // Precision: fp16 operands (11 bits; K and V are code * scale), fp32 sums and
-// softmax state. P is taken against the reference, raised when 64 keys' P sum
-// to more than 2^12, so P stays below 2^12 in fp16.
+// softmax state. P is rounded to fp16 against a reference that starts 2^9 below the
+// row's maximum and is raised when 64 keys' P sum to more than 61,440 (kRefBias).
 //
 // Feature order: a nibble word gives features (0,4)(1,5)(2,6)(3,7) of eight in
 // pairs without shuffling, so Q, K and V tiles hold every eight features in the
@@ -85,7 +85,14 @@ constexpr int kMaskWords = KVQ_TREE_MAX / 32;
 // scores) and that ending one does (the tail's slower tiles, the output), with two
 // groups of rows and with shared ones (a tile takes 1.8 us, or 1.1 us).
 constexpr int kLeadTwo = 5, kLeadShared = 4, kTrail = 2;
-constexpr float kSumBound = 4096.0f;         // sum of 64 P above which the reference is raised
+// P is fp16, and l its fp32 sum before that rounding: the reference is set 2^kRefBias
+// below the row's maximum, so that keys 15.9 nats below it keep 11 bits of P and keys 23
+// nats below it still count (from a reference at the maximum: 9.7 and 17), and raised when
+// 64 P sum to more than kSumBound, which every P of the 64 then is below (fp16: 65,504).
+// 64 equal scores sum to 2^15. (Raises cost a pass over 64 scores and one over O. The
+// reference at the maximum and a bound of 2^12 in brackets, 16 x 64 tokens over 32,768
+// keys: scores of standard deviation 1 223 us (222), 3 229 (222), 6 248 (232).)
+constexpr float kRefBias = 9.0f, kSumBound = 61440.0f;
 // A partial: O of 256 rows as [32 pieces][256 rows] float4 (a warp's store is
 // consecutive rows of one piece), then (m, l) of the rows.
 constexpr long kPartFloats = kRowBlock * (kD + 2);
@@ -788,9 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         };
         // ---- P over S (32 words over 64 scores). No maximum is taken as long as
         // the 64 keys' sum of P stays below kSumBound, which bounds every P of
-        // it (fp16 holds 2^15); above that (and for a row's first keys) the
-        // step is redone with its maximum as the new reference, and O and l
-        // follow.
+        // it; above that (and for a row's first keys) the step is redone with a
+        // reference from its maximum, and O and l follow.
         bool with_max = __any_sync(0xffffffffu, m == -CUDART_INF_F);
         uint32_t p[32];
         float s;
@@ -813,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
             float mx = -CUDART_INF_F;
 #pragma unroll
             for (int e = 0; e < 32; ++e) mx = fmaxf(fmaxf(mx, v[e]), w[e]);
-            mx *= a.scale_log2;
+            mx = mx * a.scale_log2 - kRefBias;
             const float f = mx > m ? fast_exp2(m - mx) : 1.0f;
             m = fmaxf(m, mx);
             l *= f;

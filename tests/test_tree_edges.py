@@ -1,8 +1,12 @@
-"""kv_attend_tree: hand-overs of short segments (tolerances as in test_tree.py)."""
+"""kv_attend_tree: hand-overs of short segments, one key far above a long flat tail
+(tolerances as in test_tree.py)."""
+import math
+
 import pytest
 import torch
 
-from test_tree import TOL_TENSOR, compare, inputs, kvq, make, plain, random_tree  # noqa: F401 (fixture)
+from test_tree import (TOL_F32, TOL_TENSOR, compare, dequant, inputs, kvq, make, plain,  # noqa: F401 (fixture)
+                       random_tree)
 
 
 @pytest.mark.gpu
@@ -22,3 +26,41 @@ def test_many_short_units_agree(kvq, b, g, n, recent, t):  # noqa: F811
     for _ in range(200):
         differ += (call.run() != first).any()
     assert int(differ) == 0 and kvq.read_status(call.status) == 0
+
+
+def one_key_over_a_flat_tail(kvq, b, n, nats):  # noqa: F811
+    """A cache whose first key stands `nats` above the others, which are all equal, with V = 0
+    there: the output is the tail's sum of V over 2^s + tail. Scores are exact (key 0.875 =
+    7 * 0.125, log2 scale 2^-3, q a bf16 number): s = 128 * 0.875 * q / 8 = 14 q."""
+    k = torch.zeros((b, 2, n, 128), device="cuda", dtype=torch.bfloat16)
+    k[:, :, 0] = 0.875
+    g = torch.Generator(device="cuda").manual_seed(5)
+    v = (1.0 + 0.5 * torch.randn((b, 2, n, 128), generator=g, device="cuda")).bfloat16()
+    v[:, :, 0] = 0.0
+    c = kvq.pack(k, v, 0, "bf16")
+    q = torch.tensor(nats / math.log(2.0) / 14.0).bfloat16().item()
+    return c, q, 2.0 ** (14.0 * q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("nats", [8.0, 12.0, 14.0, 15.0, 16.0, 17.0])
+@pytest.mark.parametrize("t", [1, 32])
+def test_a_key_far_above_a_flat_tail(kvq, dt, nats, t):  # noqa: F811
+    """P is rounded to fp16 against a reference 2^9 below the row's maximum: at 17 nats the tail's
+    P is 2.1e-5, off by 2^-25 / 2.1e-5 = 1.4e-3 of itself at most. With the values' 2^-11 (twice)
+    that stays below 5e-3. The first key's slice holds most of its unit's tail."""
+    b, n = 80 if dt == torch.bfloat16 else 2, 2048
+    c, x, first = one_key_over_a_flat_tail(kvq, b, n, nats)
+    q = torch.full((b, 16, t, 128), x, device="cuda").to(dt)
+    kt = torch.zeros((b, 2, t, 128), device="cuda").to(dt)
+    vt = torch.ones((b, 2, t, 128), device="cuda").to(dt)
+    par = torch.full((b, t), -1, dtype=torch.int32, device="cuda")  # each sees itself alone
+    call = kvq.AttendTree(c, q, kt, vt, par, sm_scale=math.log(2.0) / 8.0, out_dtype="f32")
+    out = call.run()
+    assert kvq.read_status(call.status) == 0
+    _, v = dequant(c, kvq)
+    want = ((v.sum(2) + 1.0) / (first + n)).repeat_interleave(8, 1).unsqueeze(2)  # (the key itself: 1)
+    want = want.expand(out.shape)
+    tol = TOL_TENSOR if dt == torch.bfloat16 else TOL_F32
+    assert float((out.double() - want).norm() / want.norm()) <= tol
