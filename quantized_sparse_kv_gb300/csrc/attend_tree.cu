@@ -91,7 +91,7 @@ constexpr int kLeadTwo = 5, kLeadShared = 4, kTrail = 2;
 // 64 P sum to more than kSumBound, which every P of the 64 then is below (fp16: 65,504).
 // 64 equal scores sum to 2^15. (Raises cost a pass over 64 scores and one over O. The
 // reference at the maximum and a bound of 2^12 in brackets, 16 x 64 tokens over 32,768
-// keys: scores of standard deviation 1 223 us (222), 3 229 (222), 6 248 (232).)
+// keys: scores of standard deviation 1 223 us (222), 2 229 (222), 4 248 (232).)
 constexpr float kRefBias = 9.0f, kSumBound = 61440.0f;
 // A partial: O of 256 rows as [32 pieces][256 rows] float4 (a warp's store is
 // consecutive rows of one piece), then (m, l) of the rows.
