@@ -695,7 +695,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
         sm.red_c[w][h] = c;
         lsum += c * sm.red_l[w][h];
       }
-      sm.red_mx[h] = mx;
+      // (scores that are all NaN leave no maximum and a NaN sum: a finite maximum keeps the
+      // merge from taking the partial for one without keys)
+      sm.red_mx[h] = kList && mx == -CUDART_INF_F && lsum != 0.0f ? 0.0f : mx;
       sm.red_ls[h] = lsum;
     }
     // heads 0-3 live in lanes with t < 2, heads 4-7 in lanes with t >= 2:
@@ -773,9 +775,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__
     float nm = m;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, pm[i]);
-    // (no finite score so far: against 0 every weight is 0, and a NaN sum stays one)
-    const float ref = nm == -CUDART_INF_F ? 0.0f : nm;
-    const float r = exp2f(m - ref);  // 0 while m is -inf
+    if (nm == -CUDART_INF_F) continue;
+    const float r = exp2f(m - nm);  // 0 while m is -inf
     l *= r;
     acc.x *= r;
     acc.y *= r;
@@ -783,7 +784,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs a, OT *__
     acc.w *= r;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2f(pm[i] - ref);  // 0 for empty and padded slots
+      const float w = exp2f(pm[i] - nm);  // 0 for empty and padded slots
       l += w * pl[i];
       acc.x += w * po[i].x;
       acc.y += w * po[i].y;
@@ -842,9 +843,8 @@ __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
     float nm = m;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, pm[i]);
-    // (no finite score so far: against 0 every weight is 0, and a NaN sum stays one)
-    const float ref = nm == -CUDART_INF_F ? 0.0f : nm;
-    const float r = exp2f(m - ref);  // 0 while m is -inf
+    if (nm == -CUDART_INF_F) continue;
+    const float r = exp2f(m - nm);  // 0 while m is -inf
     l *= r;
     acc.x *= r;
     acc.y *= r;
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(256) combine_wide_kernel(const DecodeArgs a,
     acc.w *= r;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2f(pm[i] - ref);  // 0 for empty and padded slots
+      const float w = exp2f(pm[i] - nm);  // 0 for empty and padded slots
       l += w * pl[i];
       acc.x += w * po[i].x;
       acc.y += w * po[i].y;
