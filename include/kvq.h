@@ -577,7 +577,11 @@ KVQ_API kvq_status kv_select_blocks(const kvq_cache *cache, const kvq_summary *s
  * list) are zero. q, out, workspace/ws_bytes as kv_attend.
  * Kernel choice: D = 128, bf16 q, a bf16 window (or none) and at most 8 query
  * heads per KV head run the decode kernels over the listed blocks; other
- * shapes run an fp32 kernel (q_heads and batch <= 65,535).
+ * shapes run an fp32 kernel (q_heads and batch <= 65,535). The decode kernels
+ * round q times the K scales, the int4 values and the probabilities to fp16, the
+ * last against a reference near the row's maximum: those of keys more than 14.5
+ * nats below the maximum may keep fewer than 11 bits, and those of keys more than
+ * 21 nats below it may be dropped from the output.
  */
 KVQ_API kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32_t q_dtype,
                                     int32_t q_heads, int32_t n_q, const int32_t *selected,

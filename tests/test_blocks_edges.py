@@ -3,13 +3,17 @@
 A row whose scores are NaN is NaN in every kernel, whatever the type of q and
 however many partial results its keys give; rows beside it keep their bits, and
 rows without keys stay zero. Entries of a list past the number of blocks are not
-looked at, wherever they fall among the four groups of an item.
+looked at, wherever they fall among the four groups of an item. A key far above all
+others leaves the others' probabilities their bits.
 """
+import math
+
 import pytest
 import torch
 
 from test_blocks import TOL_DECODE, TOL_F32, plain_attend, query, rel
-from test_tree import kvq, make  # noqa: F401 (fixture)
+from test_tree import dequant, kvq, make  # noqa: F401 (fixture)
+from test_tree_edges import one_key_over_a_flat_tail
 
 # b, hkv, n, window, block, blocks listed. Partials of a unit in the decode kernels (bf16 q, on
 # 152 SMs): four; 17, merged by one warp in batches of 16; 65, merged by eight warps in batches
@@ -118,3 +122,25 @@ def test_entries_past_the_number_of_blocks_are_not_looked_at(kvq, dt, block, blo
     # the last entry looked at may still be bad
     out, st = run(full[:-1] + [blocks, 0, 0, 0])
     assert st == kvq.DEV_INDEX
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("nats", [8.0, 12.0, 15.0, 16.0, 17.0, 18.0])
+def test_a_key_far_above_a_flat_tail(kvq, dt, nats):  # noqa: F811
+    """The decode kernels' P is fp16 against a reference 2^7 below a warp's maximum: at 18 nats
+    the tail's P is 1.9e-6 in the warp that holds the first key, off by 2^-25 / 1.9e-6 = 1.6e-2
+    of itself at most. That warp has a quarter of its unit's keys: 4e-3, and at 17 nats 1.4e-3;
+    with the values' roundings (2^-11 twice, random) below 5e-3."""
+    b, n = (128, 2048) if dt == torch.bfloat16 else (2, 2048)
+    c, x, first = one_key_over_a_flat_tail(kvq, b, n, nats)
+    q = torch.full((b, 16, 4, 128), x, device="cuda").to(dt)
+    sel = lists_of(b, 2, 4, n // 64, n // 64)
+    a = kvq.AttendBlocks(c, q, None, n // 64, sm_scale=math.log(2.0) / 8.0, out_dtype="f32",
+                         selected=sel, block=64)
+    out = a.run(select=False)
+    assert kvq.read_status(a.status) == 0
+    _, v = dequant(c, kvq)
+    want = (v.sum(2) / (first + n - 1)).repeat_interleave(8, 1).unsqueeze(2).expand(out.shape)
+    tol = TOL_DECODE if dt == torch.bfloat16 else TOL_F32
+    assert float((out.double() - want).norm() / want.norm()) <= tol
