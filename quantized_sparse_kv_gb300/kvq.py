@@ -804,17 +804,40 @@ class BlockSummary(_Prepared):
         self.struct = KvqSummary(_ptr(self.codes), _ptr(self.scales), block, self.cap_blocks)
         self.ref = ctypes.byref(self.struct)
 
+    # blocks [_from, ...) hold summaries of an int4 part of _cut tokens
+    _from = _cut = 0
+
     @property
     def blocks(self) -> int:
-        return -(-(self.cache.n_tokens - self.cache.recent) // self.block)
+        return -(-self.cache.cut // self.block)
 
     def update(self, first: int = 0) -> "BlockSummary":
         """Recompute the blocks from ``first`` on (all of them by default)."""
         self.run("update", first)
+        self.filled(first)
         return self
+
+    def filled(self, first: int = 0):
+        """Take it that the blocks from ``first`` on hold the cache's summaries: for entries
+        that came another way than by ``update`` (loaded, or kv_block_summary itself)."""
+        cut = self.cache.cut
+        if first >= self.blocks:
+            return
+        # what was there before still holds: all of it, or the blocks that were whole then
+        end = self.blocks if cut == self._cut else min(cut, self._cut) // self.block
+        if not self._from <= first <= end:
+            self._from = first
+        self._cut = cut
+
+    def covers(self, first: int = 0) -> bool:
+        """Whether the blocks from ``first`` on hold summaries of the int4 part as long as it is
+        now. (A cache packed anew in place, at the same length, is not noticed.)"""
+        return self._from <= first and self._cut == self.cache.cut
 
     def values(self, first: int = 0) -> torch.Tensor:
         """The mean keys the codes stand for, fp32 (batch, kv_heads, blocks - first, D)."""
+        if 0 <= first < self.blocks and not self.covers(first):
+            raise ValueError("the summary does not cover the cache: update() it")
         return self.run("values", first)
 
     def _run(self, what: str, first: int):
@@ -836,9 +859,10 @@ class AttendBlocks(_Prepared):
     query token of a KV head attends the ``top_k`` blocks its summary scores
     highest and the whole window. The summary is the caller's to keep up with the
     cache (``BlockSummary.update`` after appends that moved groups into the int4
-    part). ``selected`` (batch, kv_heads, n_q, top_k)
-    holds the chosen blocks after ``run()``; ``select=False`` attends the lists
-    already there (``selected`` may be passed)."""
+    part; a run that would read blocks without a summary raises ValueError).
+    ``selected`` (batch, kv_heads, n_q, top_k) holds the chosen blocks after
+    ``run()``; ``select=False`` attends the lists already there (``selected`` may
+    be passed)."""
 
     def __init__(self, cache: PackedCache, q: torch.Tensor, summary: BlockSummary | None,
                  top_k: int, n_sink: int = 0, sm_scale: float = 0.0, out_dtype=None, out=None,
@@ -905,6 +929,8 @@ class AttendBlocks(_Prepared):
         self.path = None
 
     def _run(self, select: bool = True) -> torch.Tensor:
+        if select and self._select_args and not self.summary.covers():
+            raise ValueError("the summary does not cover the cache: update() it")
         if self.cache.n_tokens != self._n:
             self._reserve()
         if self._copies:
