@@ -624,6 +624,12 @@ class RopePlan:
         self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
 
 
+def _integers(x: torch.Tensor, what: str):
+    """Refuse a tensor whose conversion to int32 would cut fractions off."""
+    if x.is_floating_point() or x.is_complex() or x.dtype == torch.bool:
+        raise TypeError(f"{what} must be whole numbers (int32, or a type that converts to it)")
+
+
 def _static(copies: list, x: torch.Tensor, dtype=None) -> torch.Tensor:
     """x itself when a prepared call can read it in place, else a dense buffer
     (of ``dtype``) that every run() fills from x again. The calls record no
@@ -661,6 +667,7 @@ class Rope(_Prepared):
                  out=None):
         self.lib = load_library()
         self.plan, self.inverse = plan, int(bool(inverse))
+        _integers(positions, "positions")
         src = [x for x in (q, k, v) if x is not None]
         self.device = _one_device(plan.turns, positions, *src, *(out or ()))
         if any(x.dim() != 4 or x.dtype != q.dtype for x in src):
@@ -721,6 +728,7 @@ class AttendTree(_Prepared):
                  out_dtype=None, out=None):
         self.lib = load_library()
         self.cache = cache
+        _integers(parents, "parents")
         self.device = _one_device(cache.k_scales, q, k_tree, v_tree, parents, out)
         self._copies = []
         self.q, self.k, self.v = (_static(self._copies, x) for x in (q, k_tree, v_tree))
