@@ -64,3 +64,22 @@ def test_a_key_far_above_a_flat_tail(kvq, dt, nats, t):  # noqa: F811
     want = want.expand(out.shape)
     tol = TOL_TENSOR if dt == torch.bfloat16 else TOL_F32
     assert float((out.double() - want).norm() / want.norm()) <= tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("b,n,t", [(1, 3000, 1), (2, 700, 5), (2, 700, 40), (24, 260, 20)])
+def test_a_nan_query_row_is_nan_and_stays_alone(kvq, dt, b, n, t):  # noqa: F811
+    """Over one partial and several, shared rows and two groups of them. (The NaN row's warp takes
+    its maxima every step, which moves its neighbours' references: within the tolerance.)"""
+    c = make(kvq, b, 2, n, 128, 70)
+    q, k, v = inputs(b, 16, 2, t, 128, dt)
+    par = random_tree(b, t, 7)
+    want = plain(c, kvq, q, k, v, par)
+    q[-1, 3, t - 1, 17] = torch.nan
+    call = kvq.AttendTree(c, q, k, v, par, out_dtype="f32")
+    out = call.run()
+    assert kvq.read_status(call.status) == 0
+    assert bool(torch.isnan(out[-1, 3, t - 1]).all())
+    out[-1, 3, t - 1], want[-1, 3, t - 1] = 0.0, 0.0
+    compare(out, want, par, TOL_TENSOR if dt == torch.bfloat16 else TOL_F32)
