@@ -483,8 +483,9 @@ KVQ_API kvq_status kv_rope(const kvq_rope_tensor *tensors, int32_t n_tensors, in
  * the tensor cores with fp16 operands: the int4 part as code * scale (the
  * scale and the product each rounded once to fp16, 11 bits), q, window and
  * drafted rows converted from bf16 (exact within fp16's normal range, 6e-5 to
- * 65504; larger values, infinite ones too, count as 65504), products and sums
- * in fp32. Scales of the int4 part belong in that range too: smaller ones keep
+ * 65504; of 2^16 and more q and keys count as NaN, values as infinite), products
+ * and sums in fp32.
+ * Scales of the int4 part belong in that range too: smaller ones keep
  * fewer bits, and 7 * scale above 65504 overflows. Probabilities are rounded to
  * fp16 against a reference near the row's maximum: those of keys more than 15.9
  * nats below the maximum keep fewer than 11 bits, and those of keys more than 23

@@ -104,7 +104,7 @@ struct __align__(1024) TreeSmem {
   int par[KVQ_TREE_MAX];                     // parents of the sequence
   uint32_t seen[KVQ_TREE_MAX][kMaskWords];   // ancestor bits of every drafted token
   uint32_t live[kMaskWords];                 // drafted tokens that exist
-  uint32_t odd_v[kMaskWords];                // drafted tokens with a non-finite V element
+  uint32_t odd_v[kMaskWords];                // drafted tokens with a V element beyond fp16
   float mm[2][kBM], ml[2][kBM];              // row states of the two groups (alternate tiles)
   uint64_t k_full[kStages][2], k_empty[kStages][2], v_full[kStages][2], v_empty[kStages][2];  // [half]
   uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [group][buffer]
@@ -220,18 +220,21 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t b_mn_major, uint32_t n
   return (1u << 4) | (b_mn_major << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Two floats to fp16, values beyond its range (infinities too) clamped to it; NaN
-// stays.
-__device__ __forceinline__ uint32_t pack_h2_sat(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
+// Whether a bf16 (its bits) is beyond fp16: 2^16 and more, infinite, NaN. (bf16's next
+// lower value, 65,280, is an fp16 number.)
+__device__ __forceinline__ bool odd_bf16(uint32_t bits) { return (bits & 0x7fffu) >= 0x4780u; }
 
-// Eight bf16 (four words, natural order) as fp16 in the tiles' feature order.
+// Eight bf16 (four words, natural order) as fp16 in the tiles' feature order. Elements
+// beyond fp16 become infinite, or (kNan: queries and keys) NaN, whose scores are NaN
+// whatever they meet: h + 0 h is h, and NaN where h is infinite.
+template <bool kNan>
 __device__ __forceinline__ uint4 bf8_to_h8(const uint4 &w) {
-  return make_uint4(pack_h2_sat(bf_lo(w.x), bf_lo(w.z)), pack_h2_sat(bf_hi(w.x), bf_hi(w.z)),
-                    pack_h2_sat(bf_lo(w.y), bf_lo(w.w)), pack_h2_sat(bf_hi(w.y), bf_hi(w.w)));
+  auto cvt = [](float lo, float hi) {
+    const __half2 h = as_h2(pack_h2(lo, hi));
+    return as_u32(kNan ? __hfma2(h, __half2half2(__ushort_as_half(0)), h) : h);
+  };
+  return make_uint4(cvt(bf_lo(w.x), bf_lo(w.z)), cvt(bf_hi(w.x), bf_hi(w.z)),
+                    cvt(bf_lo(w.y), bf_lo(w.w)), cvt(bf_hi(w.y), bf_hi(w.w)));
 }
 
 // Place of 16-byte chunk c (0..15, eight features each) of row r in a tile.
@@ -365,8 +368,8 @@ __device__ __forceinline__ void store_raw(const Raw &x, int r, int cb, uint8_t *
 }
 
 // Rows of the tail (window, then drafted tokens) from key k0 on, zeros past
-// its end; non-finite V elements of drafted tokens become zero (they are added
-// for the rows that see them when the output is written).
+// its end; V elements of drafted tokens beyond fp16 become zero (they are added, as
+// infinities or NaN, for the rows that see them when the output is written).
 template <bool kV>
 __device__ __noinline__ void copy_tail(const TreeArgs &a, long u, int k0, int grp, int r, int cb,
                                           uint8_t *tile) {
@@ -387,14 +390,14 @@ __device__ __noinline__ void copy_tail(const TreeArgs &a, long u, int k0, int gr
         uint32_t *e = reinterpret_cast<uint32_t *>(&w[j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u;
-          if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu;
+          if (odd_bf16(e[k])) e[k] &= 0xffff0000u;
+          if (odd_bf16(e[k] >> 16)) e[k] &= 0x0000ffffu;
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4 *>(tile + chunk_at(row, 4 * cb + j)) = bf8_to_h8(w[j]);
+      *reinterpret_cast<uint4 *>(tile + chunk_at(row, 4 * cb + j)) = bf8_to_h8<!kV>(w[j]);
   }
 }
 
@@ -425,8 +428,8 @@ __device__ __forceinline__ bool warp_wait(int *abort_flag, uint32_t bar, uint32_
 }
 
 // Features d0 .. d0 + 31 of a row just written to dst whose seen drafted tokens
-// hold infinities or NaN in V there (zeroed in the tiles): the sum of those is
-// the result. k_lo, k_hi: the tail keys the row's sum covers; step: elements from
+// hold V elements beyond fp16 there (zeroed in the tiles): the sum of those, as
+// infinities or NaN, is the result. k_lo, k_hi: the tail keys the row's sum covers; step: elements from
 // one piece of four features to the next.
 __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &sm, long u, int tok,
                                             int k_lo, int k_hi, int d0, void *dst, int step, bool bf16) {
@@ -436,7 +439,7 @@ __device__ __noinline__ void put_odd_values(const TreeArgs &a, const TreeSmem &s
       if (!((sm.odd_v[j >> 5] & sm.seen[tok][j >> 5]) >> (j & 31) & 1u)) continue;
       const uint16_t *p = a.v_tree + (u * a.T + j) * kD + e;
       const float x = in_bounds(a.ctl, p, 2) ? bf16_to_f32(*p) : 0.0f;
-      if (!(fabsf(x) <= 3.40282347e38f)) s += x;
+      if (!(fabsf(x) < 65536.0f)) s += x * CUDART_INF_F;
     }
     if (s == 0.0f) continue;
     const long at = static_cast<long>(e >> 2) * step + (e & 3);
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const int tail_lo = kBN * max(0, t_lo - a.int4_tiles);        // tail keys of this segment
       const int tail_hi = kBN * (t_lo + n - a.int4_tiles);
       if (has_tail) {
-        // drafted tokens with a non-finite V: a warp per token, four at a time
+        // drafted tokens with a V element beyond fp16: a warp per token, four at a time
         const int j1 = min(a.T, tail_hi - a.R);
         for (int j0 = max(0, tail_lo - a.R) + warp; j0 < j1; j0 += 4 * kSoftWarps) {
           uint2 w[4];
@@ -736,9 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + i * kSoftWarps;
-            const bool odd =
-                (w[i].x & 0x7f80u) == 0x7f80u || (w[i].x & 0x7f800000u) == 0x7f800000u ||
-                (w[i].y & 0x7f80u) == 0x7f80u || (w[i].y & 0x7f800000u) == 0x7f800000u;
+            const bool odd = odd_bf16(w[i].x) || odd_bf16(w[i].x >> 16) || odd_bf16(w[i].y) ||
+                             odd_bf16(w[i].y >> 16);
             if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sm.odd_v[j >> 5], 1u << (j & 31));
           }
         }
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         for (int i = 0; i < 4; ++i) {  // zeros for a row without a token
           const bool on = qt[i] >= 0 && (sm.live[qt[i] >> 5] >> (qt[i] & 31) & 1u);
           *reinterpret_cast<uint4 *>(q_tile + chunk_at(i0 + 2 * i, lane & 15)) =
-              on ? bf8_to_h8(qw[i]) : make_uint4(0u, 0u, 0u, 0u);
+              on ? bf8_to_h8<true>(qw[i]) : make_uint4(0u, 0u, 0u, 0u);
         }
         i0 += 8;
         if (i0 >= q_first + (two ? 32 : 16)) break;
@@ -900,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         part_ml = reinterpret_cast<float2 *>(p + kRowBlock * kD) + (r - row0);
         if (!in_bounds(a.ctl, p, sizeof(float) * kPartFloats)) part = nullptr;
       }
-      bool odd = false;  // a seen drafted token with a non-finite V
+      bool odd = false;  // a seen drafted token with a V element beyond fp16
       if (has_tail) {
 #pragma unroll
         for (int w = 0; w < kMaskWords; ++w) odd |= (sm.odd_v[w] & sm.seen[tok][w]) != 0u;

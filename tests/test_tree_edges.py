@@ -5,8 +5,8 @@ import math
 import pytest
 import torch
 
-from test_tree import (TOL_F32, TOL_TENSOR, compare, dequant, inputs, kvq, make, plain,  # noqa: F401 (fixture)
-                       random_tree)
+from test_tree import (TOL_F32, TOL_TENSOR, ancestors, compare, dequant, inputs,  # noqa: F401 (fixture)
+                       kvq, make, plain, random_tree)
 
 
 @pytest.mark.gpu
@@ -83,3 +83,76 @@ def test_a_nan_query_row_is_nan_and_stays_alone(kvq, dt, b, n, t):  # noqa: F811
     assert bool(torch.isnan(out[-1, 3, t - 1]).all())
     out[-1, 3, t - 1], want[-1, 3, t - 1] = 0.0, 0.0
     compare(out, want, par, TOL_TENSOR if dt == torch.bfloat16 else TOL_F32)
+
+
+BEYOND = [65536.0, -1e5, 3e38, float("inf"), float("-inf"), float("nan")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x", BEYOND)
+@pytest.mark.parametrize("t", [3, 40])
+def test_elements_beyond_fp16_show(kvq, x, t):  # noqa: F811
+    """The tensor-core kernel's operands end at 65,504: what lies beyond makes the rows that see
+    it NaN or infinite, instead of counting as some finite number, and no other row."""
+    b, n, recent = 2, 500, 70
+    q, k, v = inputs(b, 16, 2, t, 128)
+    par = random_tree(b, t, 11)
+    seen = ancestors(par)
+    clean = make(kvq, b, 2, n, 128, recent)
+    want = plain(clean, kvq, q, k, v, par)
+
+    def run(c=clean, q=q, k=k, v=v):
+        call = kvq.AttendTree(c, q, k, v, par, out_dtype="f32")
+        out = call.run()
+        assert kvq.read_status(call.status) == 0 and call.path == "tree_tensor"
+        return out
+
+    def check(out, odd):  # the odd elements are not finite, the rest is what it was
+        assert not bool(torch.isfinite(out[odd]).any())
+        compare(torch.where(odd, 0.0, out), torch.where(odd, 0.0, want), par, TOL_TENSOR)
+    none = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    odd = none.clone()
+    odd[1, 4, t - 1] = True
+    q2 = q.clone()
+    q2[1, 4, t - 1, 100] = x
+    check(run(q=q2), odd)
+    sees = seen[1, :, 1]                                     # rows of sequence 1 that see token 1
+    odd = none.clone()
+    odd[1, 8:, sees] = True
+    k2 = k.clone()
+    k2[1, 1, 1, 7] = x
+    check(run(k=k2), odd)
+    odd = none.clone()
+    odd[1, 8:, sees, 77] = True
+    v2 = v.clone()
+    v2[1, 1, 1, 77] = x
+    out = run(v=v2)
+    check(out, odd)
+    if not math.isnan(x):
+        assert bool((out[odd] == math.copysign(math.inf, x)).all())
+    c = make(kvq, b, 2, n, 128, recent)
+    c.k_window[0, 1, recent - 1, 3] = x
+    odd = none.clone()
+    odd[0, 8:] = True
+    check(run(c=c), odd)
+    c = make(kvq, b, 2, n, 128, recent)
+    c.v_window[0, 1, 0, 3] = x
+    odd = none.clone()
+    odd[0, 8:, :, 3] = True
+    check(run(c=c), odd)
+
+
+@pytest.mark.gpu
+def test_the_largest_fp16_elements_are_exact(kvq):  # noqa: F811
+    """65,280 is bf16's last number below 2^16: values that large are what they are."""
+    b, n, t = 1, 90, 4
+    c = make(kvq, b, 1, n, 128, 90)
+    q, k, v = inputs(b, 8, 1, t, 128)
+    par = random_tree(b, t, 2)
+    v[..., 5] = 65280.0
+    c.v_window[..., 5] = 65280.0
+    c.v_window[..., 6] = -65280.0
+    out, st = kvq.attend_tree(c, q, k, v, par, out_dtype="f32")
+    assert kvq.read_status(st) == 0
+    compare(out, plain(c, kvq, q, k, v, par), par, TOL_TENSOR)
+    assert bool(((out[..., 5] / 65280.0 - 1).abs() <= 2.0 ** -10).all())
