@@ -416,11 +416,11 @@ typedef struct kvq_rope_scaling {
 /*
  * The frequency table of kv_rope: turns[i] = f_i / (2 pi) as a 64-bit binary
  * fraction of a turn, so that pos * turns[i] modulo 2^64 is the phase of any
- * position with no loss at far ones. turns: HOST array of rotary_dim / 2
- * entries (the caller copies it to the device once); *amplitude receives the
- * factor on the rotation. scaling may be NULL (NONE). Host only. KVQ_ERR_ARG
- * for an odd or non-positive rotary_dim, one above 256, base <= 1 or a
- * scaling outside the limits above.
+ * position, to |pos| * 2^-53 turns (the entries are made from doubles). turns:
+ * HOST array of rotary_dim / 2 entries (the caller copies it to the device
+ * once); *amplitude receives the factor on the rotation. scaling may be NULL
+ * (NONE). Host only. KVQ_ERR_ARG for an odd or non-positive rotary_dim, one
+ * above 256, base <= 1 or a scaling outside the limits above.
  */
 KVQ_API kvq_status kvq_rope_turns(int32_t rotary_dim, double base, const kvq_rope_scaling *scaling,
                                   uint64_t *turns, float *amplitude);
@@ -575,7 +575,8 @@ KVQ_API kvq_status kv_select_blocks(const kvq_cache *cache, const kvq_summary *s
  * exceed the entry before it is skipped and flagged KVQ_DEV_DUP (the list's
  * rows are then invalid). Entries past the n_blocks-th are not looked at (a
  * valid list holds -1 there). Rows with no key at all (no window, an empty
- * list) are zero. q, out, workspace/ws_bytes as kv_attend.
+ * list) are zero; a row with an infinite q has no defined value (NaN or zero).
+ * q, out, workspace/ws_bytes as kv_attend.
  * Kernel choice: D = 128, bf16 q, a bf16 window (or none) and at most 8 query
  * heads per KV head run the decode kernels over the listed blocks; other
  * shapes run an fp32 kernel (q_heads and batch <= 65,535). The decode kernels

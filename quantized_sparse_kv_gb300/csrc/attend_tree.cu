@@ -45,12 +45,13 @@
 // What bounds it. Many rows: the tensor pipe and the hand-overs around it. A tile of
 // two groups takes 1.8 us, of which the pipe works 2,560 cycles (a 64-key S step is
 // 8 x 48, its operands' shared-memory reads; a PV step 4 x 64). 16 sequences x 64
-// tokens x 16 heads over 32,768 keys (275 GFLOP): 210 us back to back, 1,310
-// TFLOP/s; without the exponentials it would be 3 % faster, without the softmax 14 %,
-// without the tile stores 9 %. Few rows: packed bytes and fixed times; 16
-// sequences x 8 tokens over 8,200 keys (45 MB): 34.5 us, of which 4.9 us until the
-// first queries are in place, 1.1 us a tile (of 128 rows, half of them used), 2 us
-// the output and about 5 us the merge.
+// tokens x 16 heads over 32,768 keys (275 GFLOP): 212 us on the same inputs back to
+// back, 1,300 TFLOP/s, 223 us on changing ones (1,230); without the exponentials it
+// would be 3 % faster, without the softmax 14 %, without the tile stores 9 %. Few rows:
+// packed bytes and fixed times; 16 sequences x 8 tokens over 8,200 keys (45 MB): 29.9
+// us back to back, 34.4 on changing inputs, of which 4.9 us until the first queries are
+// in place, 1.1 us a tile (of 128 rows, half of them used), 2 us the output and about
+// 5 us the merge.
 // Measured and not kept (16 x 64 tokens, the kernel at that time in brackets): S of
 // a whole tile in one step (N = 128) 268 us (229); Q as the A operand from TMEM, S
 // then 8 x 32 cycles but with one score buffer a group, 264 (213); softmax in

@@ -11,7 +11,7 @@
 //
 // What bounds them. The summary reads 20 D bytes of K codes and scales per
 // group and writes D + 4 per block: memory. Scoring reads D + 4 bytes per
-// block, about 1/40 of the block itself, for 2 heads * D integer operations;
+// block (of 64 tokens at D = 128: 1/78 of its K and V) for 2 heads * D integer operations;
 // choosing is a radix selection over one score row and bound by latency. Measured,
 // D = 128, blocks of 64: summaries of 32 x 2 x 131,072 tokens (671 MB of codes and
 // scales) 108 us, 6.4 TB/s; their values (17 MB read, 67 written) 14 us; scores of
@@ -22,6 +22,7 @@
 
 #include <algorithm>
 
+#include "int4_dequant.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -55,12 +56,6 @@ struct SummaryArgs {
 // with the four channels whose scales it loaded.
 constexpr int kSumWarps = 8;
 
-__device__ __forceinline__ uint32_t prmt_u(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-
 // Sums of the codes of one group in this lane's channels: 32 (lane & 3) +
 // 16 b2 + 8 b3 + 4 b4 + 0..3, b2..b4 the lane's upper bits.
 __device__ __forceinline__ int4 group_sums(const uint4 (&w)[4], int lane) {
@@ -84,8 +79,8 @@ __device__ __forceinline__ int4 group_sums(const uint4 (&w)[4], int lane) {
   const uint32_t l1 = (b3 ? l2[1] : l2[0]) + __shfl_xor_sync(0xffffffffu, b3 ? l2[0] : l2[1], 8);
   const uint32_t h1 = (b3 ? h2[1] : h2[0]) + __shfl_xor_sync(0xffffffffu, b3 ? h2[0] : h2[1], 8);
   // widen: channels (0, 2) and (4, 6) of the word, (1, 3) and (5, 7)
-  const uint32_t la = prmt_u(l1, 0u, 0x4140u), lb = prmt_u(l1, 0u, 0x4342u);
-  const uint32_t ha = prmt_u(h1, 0u, 0x4140u), hb = prmt_u(h1, 0u, 0x4342u);
+  const uint32_t la = prmt(l1, 0u, 0x4140u), lb = prmt(l1, 0u, 0x4342u);
+  const uint32_t ha = prmt(h1, 0u, 0x4140u), hb = prmt(h1, 0u, 0x4342u);
   const uint32_t e = (b4 ? lb : la) + __shfl_xor_sync(0xffffffffu, b4 ? la : lb, 16);
   const uint32_t o = (b4 ? hb : ha) + __shfl_xor_sync(0xffffffffu, b4 ? ha : hb, 16);
   // 32 tokens of code + 8: padding tokens hold code 0

@@ -3,9 +3,10 @@
 // Mathematics. Pair i of a token at position pos turns by 2 pi phi, phi the
 // fraction of pos * f_i / (2 pi). f_i / (2 pi) comes as a 64-bit binary
 // fraction of a turn, so the product modulo 2^64 (ordinary wrapping integer
-// arithmetic, negative positions included) is phi with an error below
-// |pos| * 2^-64 turns: the far positions of a long context lose nothing, and
-// no 64-bit floating point is used. phi goes to fp32 as a signed fraction
+// arithmetic, negative positions included) is phi with the table's error times
+// |pos|: its entries are made from doubles, below 2^-53 turns a position, so the
+// farthest position (2^31) is off by less than 2^-22 turns and one of 2^20 by 2^-33;
+// no 64-bit floating point is used on the device. phi goes to fp32 as a signed fraction
 // (relative error 2^-24) and through sincospif; the two products of a pair are
 // fp32, rounded once to the output type.
 //

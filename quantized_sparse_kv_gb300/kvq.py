@@ -197,9 +197,11 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 class _Prepared:
     """Base of the prepared calls below: ``run()`` issues them on the current
     stream of their tensors' device, with the arguments marshalled once (a
-    decoding step is bound by the host as much as by the GPU). A prepared call
-    has one workspace: runs that may overlap, on several streams or from
-    captured graphs, each need an object of their own."""
+    decoding step is bound by the host as much as by the GPU) and, for calls
+    over a cache, again by the first run after the cache has grown. A captured
+    run replays with the cache's lengths at its capture. A prepared call has
+    one workspace: runs that may overlap, on several streams or from captured
+    graphs, each need an object of their own."""
 
     def run(self, *args, **kw):
         if torch.cuda.current_device() != self.device.index:
@@ -660,7 +662,9 @@ class Rope(_Prepared):
     """A prepared kv_rope call: q (batch, heads, n, D) and optionally k of the
     same batch, n and D, at any strides (views of a projection's rows are read
     in place when their rows start on 16 bytes); ``v`` is only copied to the
-    dense layout. ``run()`` returns the outputs, dense (batch, heads, n, D)."""
+    dense layout. ``positions`` (batch, n): int32 ones are read in place, other
+    integers converted by every run. ``run()`` returns the outputs, dense (batch,
+    heads, n, D)."""
 
     def __init__(self, plan: RopePlan, q: torch.Tensor, k: torch.Tensor | None,
                  positions: torch.Tensor, v: torch.Tensor | None = None, inverse: bool = False,
