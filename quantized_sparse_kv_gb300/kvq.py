@@ -832,9 +832,9 @@ class BlockSummary(_Prepared):
     def filled(self, first: int = 0):
         """Take it that the blocks from ``first`` on hold the cache's summaries: for entries
         that came another way than by ``update`` (loaded, or kv_block_summary itself)."""
-        cut = self.cache.cut
-        if first >= self.blocks:
+        if self.covers(first) or first >= self.blocks:
             return
+        cut = self.cache.cut
         # what was there before still holds: all of it, or the blocks that were whole then
         end = self.blocks if cut == self._cut else min(cut, self._cut) // self.block
         if not self._from <= first <= end:
@@ -848,7 +848,7 @@ class BlockSummary(_Prepared):
 
     def values(self, first: int = 0) -> torch.Tensor:
         """The mean keys the codes stand for, fp32 (batch, kv_heads, blocks - first, D)."""
-        if 0 <= first < self.blocks and not self.covers(first):
+        if not self.covers(first) and 0 <= first < self.blocks:
             raise ValueError("the summary does not cover the cache: update() it")
         return self.run("values", first)
 
