@@ -941,7 +941,8 @@ class AttendBlocks(_Prepared):
         self.path = None
 
     def _run(self, select: bool = True) -> torch.Tensor:
-        if select and self._select_args and not self.summary.covers():
+        if (select and self._select_args and not self.summary.covers() and
+                self.summary.blocks > self.top_k):  # (else every block is taken unread)
             raise ValueError("the summary does not cover the cache: update() it")
         if self.cache.n_tokens != self._n:
             self._reserve()

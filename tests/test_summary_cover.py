@@ -79,3 +79,19 @@ def test_choices_over_missing_summaries_are_refused(kvq):  # noqa: F811
     t.filled()
     b = kvq.AttendBlocks(c, q, t, 3)
     assert torch.equal(b.run(), a.out) and torch.equal(b.selected, a.selected)
+
+
+@pytest.mark.gpu
+def test_no_summary_is_needed_to_take_every_block(kvq):  # noqa: F811
+    c = make(kvq, 1, 2, 704, 128, 64, reserve=(60, 160))     # 10 blocks of 64
+    s = kvq.BlockSummary(c, 64)                              # never updated
+    q = query(1, 16, 1, 128)
+    a = kvq.AttendBlocks(c, q, s, 10)
+    out = a.run()
+    assert kvq.read_status(a.status) == 0
+    assert a.selected[0, 0, 0].tolist() == list(range(10))
+    assert torch.equal(out, kvq.AttendBlocks(c, q, s.update(), 10).run())
+    x = torch.randn((1, 2, 96, 128), device="cuda").bfloat16()
+    kvq.append(c, x, x, 64)                                  # 12 blocks: now there is a choice
+    with pytest.raises(ValueError, match="cover"):
+        a.run()
