@@ -66,8 +66,10 @@ enum {
   KVQ_DEV_DUP = 2,     /* a candidate list holds the same index twice (validate only), or a
                           list of blocks does not increase */
   KVQ_DEV_TIMEOUT = 4, /* a bounded wait ran out; the outputs of that launch are invalid */
-  KVQ_DEV_BOUNDS = 8   /* an address range a kernel derived lay outside the call's buffers
+  KVQ_DEV_BOUNDS = 8,  /* an address range a kernel derived lay outside the call's buffers
                           (checked in the KVQ_DEBUG build, kvq_debug_checks); outputs invalid */
+  KVQ_DEV_PAGES = 16   /* kv_page_tables: a request's new tokens got no pages (none left, or its
+                          row of the table is full); the request stays as it was */
 };
 
 typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1, KVQ_MXFP8 = 2 } kvq_dtype;
@@ -591,13 +593,178 @@ KVQ_API kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32
                                     int32_t out_dtype, void *workspace, size_t *ws_bytes,
                                     int32_t *dev_status, kvq_stream_t stream);
 
+/*
+ * The paged cache: requests of different lengths that come and go, each in a slot.
+ * Request s holds lengths[s] = L tokens. With W = window, the first
+ *   cut(L) = 32 * floor((L - W) / 32) for L >= W, else 0
+ * tokens are int4 groups (the kv_pack rule) in pages of `page` tokens taken from a
+ * pool, and the tokens [cut, L), between W and W + 31 once L >= W, are floats in the
+ * slot's window, a ring of T = floor((W + 63) / 32) tiles of 32 rows: token p lies in
+ * row p % 32 of tile (p / 32) % T. What a token is stored as depends on its request's
+ * tokens alone, not on the steps they came in: every value is first rounded to the
+ * window's type and the groups are made from the rounded values.
+ *
+ * kvq_page_state is shared by the caches of all layers of a model:
+ *   table      [slots][max_pages] int32: entry j of row s is the page that holds tokens
+ *              [j * page, (j + 1) * page) of request s below cut; entries behind a
+ *              request's pages hold nothing.
+ *   lengths    [slots] int32
+ *   free_pages [n_pages] int32: a stack of the pages no request holds, n_free[0] of them
+ *              (the rest of the array is scratch); n_free: 4 int32, only the first used.
+ * An empty state has lengths 0, n_free[0] = n_pages and free_pages any permutation of
+ * the pages. The arrays may be saved and restored by the caller, all together.
+ *
+ * kvq_paged_cache adds one layer's memory, laid out for the attention kernel:
+ *   pool  [n_pages][kv_heads][page / 32][40 * D] bytes: one record per 32-token group
+ *         and head, so that every group is one copy:
+ *           K codes  16 D bytes, [32][D/2] as in kvq_cache
+ *           K scales 4 D bytes, float of channel (D/4) t + 8 i + k (t < 4, i < D/32, k < 8)
+ *                    at [2 i + (k >> 1 & 1)][t][2 (k & 1) + (k >> 2)]
+ *           V codes  16 D bytes: words of 8 codes + 8, word (m, g, t, f), m < 2, g < 8, t < 4,
+ *                    f < D/16; nibbles from the lowest: tokens x, x + 8 of feature y, tokens x,
+ *                    x + 8 of feature y + 8, the same of token x + 1, x = 16 m + 2 t,
+ *                    y = 16 f + g; at [m][f / c][g][t][f % c], c = 4 (2 when D % 64 != 0)
+ *           V scales 4 D bytes, float of (token, 32-feature block b) at
+ *                    [token / 8][token % 8 / 2][b][token % 2]
+ *   ring  [slots][kv_heads][T][2][32 * D] elements of win_dtype (F32 or BF16), K then V:
+ *           K of (row r, channel (D/4) t + 8 i + k) at [r][i ^ x][t][2 (k & 3) + (k >> 2)],
+ *             x = r & 1 when D % 64 == 0, else 0
+ *           V of (row r, feature 32 b + 8 j + g) at [r / 16][r / 8 % 2][b][g][r % 8 / 2][j][r % 2]
+ */
+typedef struct kvq_page_state {
+  int32_t slots;     /* 1 .. KVQ_PAGES_MAX_SLOTS */
+  int32_t n_pages;   /* of the pool */
+  int32_t page;      /* tokens: 32, 64 or 128 */
+  int32_t max_pages; /* of one request */
+  int32_t window;    /* W, 0 .. 65,536 */
+  int32_t *table;
+  int32_t *lengths;
+  int32_t *free_pages;
+  int32_t *n_free;
+} kvq_page_state;
+
+typedef struct kvq_paged_cache {
+  kvq_page_state state;
+  int32_t kv_heads, head_dim, win_dtype;
+  uint8_t *pool;
+  void *ring;
+} kvq_paged_cache;
+
+#define KVQ_PAGES_MAX_SLOTS 8192
+
+/* Sizes in bytes (host only; pointers are not read): sizes[0..5] = table, lengths,
+ * free_pages, n_free, pool, ring. KVQ_ERR_ARG for a shape outside the limits above or a
+ * request that could hold more than 2^31 - 1 tokens. */
+KVQ_API kvq_status kvq_paged_sizes(const kvq_paged_cache *cache, size_t sizes[6]);
+
+/* What kv_page_tables makes of one step: device arrays of the caller's, written by it and
+ * read by kv_append_pages (and by the caller).
+ *   offsets   [slots + 1]: first row of each request's new tokens in the step's tensors
+ *   before    [slots], after [slots]: the requests' lengths
+ *   row_slot  [rows]: the request of each row, -1 for a row of none
+ *   positions [rows]: its token's position (0 for a row of none); what kv_rope takes
+ *   work      [cap_work][2]: (slot, group) of every 32-token group the step writes, in
+ *             the pages or in the windows; cap_work >= kvq_page_work(state, rows)
+ *   counts    [4]: pages free after the step, groups in work, and scratch that has to
+ *             be zero before the first call (it is left zero)
+ */
+typedef struct kvq_page_plan {
+  int32_t rows;
+  int32_t cap_work;
+  int32_t *offsets, *before, *after, *row_slot, *positions, *work, *counts;
+} kvq_page_plan;
+
+/* Entries `work` needs for a step of `rows` token rows; 0 for an invalid state or rows
+ * outside [0, 2^28]. */
+KVQ_API int32_t kvq_page_work(const kvq_page_state *state, int32_t rows);
+
+/*
+ * kv_page_tables -- the tables of one step, built on the GPU from the requests' lengths.
+ * n_new: device int32 [slots]: tokens that each request adds, 0 for one that rests, -1
+ * for one that ends: its pages go back and its length becomes 0. The step's tensors hold
+ * the new tokens of the requests one behind the other in slot order, `plan->rows` rows
+ * in all; rows behind the last request's belong to none.
+ * The pages of ended requests go on top of the free ones (in slot order, each request's
+ * in table order) and requests that grow take theirs from the top (in slot order). A
+ * request whose pages are not there (the sum of the pages asked for by it and the ones
+ * before it exceeds the free ones, or max_pages is exceeded) is flagged KVQ_DEV_PAGES
+ * and stays as it was; its rows belong to none. A request with n_new below -1, more new
+ * tokens than rows are left, or a length that its table cannot hold is flagged
+ * KVQ_DEV_INDEX and stays as it was.
+ * advance != 0: lengths and the free pages become what they are after the step, as the
+ * steps of a model need it (once a step, before the layers' kv_append_pages). advance ==
+ * 0 looks ahead: the plan is the one the step would have (counts[0] >= 0 pages would be
+ * left), and only scratch of the state is written.
+ */
+KVQ_API kvq_status kv_page_tables(const kvq_page_state *state, const int32_t *n_new,
+                                  const kvq_page_plan *plan, int32_t advance,
+                                  int32_t *dev_status, kvq_stream_t stream);
+
+/*
+ * kv_append_pages -- the new tokens' keys and values into one layer's pages and windows,
+ * as the plan of kv_page_tables says; whole groups that leave the windows are quantized.
+ * k_new, v_new: in_dtype (F32 or BF16), element (row, head, d) at [row * stride_row +
+ * head * stride_head + d] (strides in elements, multiples of 16 bytes, >= 0: rows of a
+ * projection are read in place). Rows of none are not read. May be called again with the
+ * same plan, for other layers or, while no token of the step took the window row of
+ * an older one that moved (steps of one token never do), for the same layer.
+ * A page outside the pool is flagged KVQ_DEV_INDEX and not written.
+ */
+typedef struct kvq_page_rows {
+  const void *k_new, *v_new;
+  int64_t k_stride_row, k_stride_head, v_stride_row, v_stride_head;
+} kvq_page_rows;
+KVQ_API kvq_status kv_append_pages(const kvq_paged_cache *cache, const kvq_page_plan *plan,
+                                   const kvq_page_rows *rows, int32_t in_dtype,
+                                   int32_t *dev_status, kvq_stream_t stream);
+
+/*
+ * kv_page_values -- keys and values of listed tokens as attention reads them: code * scale,
+ * or the window's value, rounded to out_dtype (F32 or BF16). row_slot, positions: device
+ * int32 [n_rows]; k, v: [n_rows][kv_heads][D]. A row with slot -1 is left as it was; one
+ * with another slot that does not exist, or a position outside the request, is flagged
+ * KVQ_DEV_INDEX and left as it was. n_rows <= 2^28.
+ */
+KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *row_slot,
+                                  const int32_t *positions, int32_t n_rows, void *k, void *v,
+                                  int32_t out_dtype, int32_t *dev_status, kvq_stream_t stream);
+
+/*
+ * kv_attend_pages -- attention of new tokens, one query row each, over their requests'
+ * pages and windows. q, out: [n_rows][q_heads][D]. row_slot: device int32 [n_rows], the
+ * request of each row, or NULL for row i = request i (n_rows <= slots). positions: device
+ * int32 [n_rows]: row i attends the tokens [0, positions[i]] of its request, so that
+ * several new tokens of one request each see the ones before them; NULL: all tokens of
+ * the request. Lengths are read on the device: a captured call serves every later step.
+ * A row with slot -1 is left as it was (a batch padded to a captured size); one of a
+ * request without tokens is zero. A slot outside [-1, slots), a length that the table
+ * cannot hold or a position outside the request is flagged KVQ_DEV_INDEX and the row left
+ * as it was; a page outside the pool is flagged KVQ_DEV_INDEX and its tokens skipped.
+ * workspace/ws_bytes as kv_attend (they depend on n_rows and q_heads alone). n_rows <=
+ * 65,535; 0 rows are valid.
+ * Kernel choice: D = 64 or 128 with BF16 windows runs on the tensor cores; products of
+ * the int4 part have fp16 operands: q times the K scales (times 4 or 1/4), and
+ * probabilities times the V scales, both rounded to 11 bits, against a reference
+ * that puts the largest product of a tile near 2^7; with V scales between 2^-4 and 2^8
+ * keys more than 11.8 nats below the maximum keep fewer bits, and those more than 18
+ * nats below it may be dropped from the output (the sum keeps them). Scales of V belong
+ * below 2^15, and q * sm_scale * log2(e) times a K scale below 2^14. Other shapes run
+ * an fp32 kernel.
+ */
+KVQ_API kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
+                                   int32_t q_heads, int32_t n_rows, const int32_t *row_slot,
+                                   const int32_t *positions, float sm_scale, void *out,
+                                   int32_t out_dtype, void *workspace, size_t *ws_bytes,
+                                   int32_t *dev_status, kvq_stream_t stream);
+
 /* Number of kernel launches the last successful call on this thread enqueued. */
 KVQ_API int32_t kvq_last_launch_count(void);
 
 /* Name of the kernel family the last successful call on this thread used
  * ("pack", "decode", "chunk_bf16", "chunk_mxfp8", "generic", "candidates",
  * "rope", "tree_tensor", "tree_rows", "block_summary", "block_values",
- * "select_blocks", "blocks_decode", "blocks_rows", ...); a static string. */
+ * "select_blocks", "blocks_decode", "blocks_rows", "page_tables", "append_pages",
+ * "page_values", "pages_tensor", "pages_rows", ...); a static string. */
 KVQ_API const char *kvq_last_path(void);
 
 /*

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "kvq_internal.h"
+#include "paged.cuh"
 
 namespace {
 
@@ -165,6 +166,69 @@ void ctl_add_summary(kvq::KernelCtl &c, const kvq_cache &k, const kvq_summary &s
   const size_t rows = static_cast<size_t>(k.batch) * k.kv_heads * s.cap_blocks;
   ctl_add(c, s.codes, rows * k.head_dim);
   ctl_add(c, s.scales, rows * sizeof(float));
+}
+
+bool page_state_ok(const kvq_page_state &s) {
+  return s.slots >= 1 && s.slots <= KVQ_PAGES_MAX_SLOTS && s.n_pages >= 1 && s.max_pages >= 1 &&
+         (s.page == 32 || s.page == 64 || s.page == 128) && s.window >= 0 && s.window <= 65536 &&
+         static_cast<long>(s.max_pages) * s.page + s.window + 64 <= 0x7fffffffL;
+}
+
+bool paged_ok(const kvq_paged_cache &c) {
+  return page_state_ok(c.state) && c.kv_heads >= 1 && c.head_dim >= 32 && c.head_dim <= 256 &&
+         c.head_dim % 32 == 0 && (c.win_dtype == KVQ_F32 || c.win_dtype == KVQ_BF16);
+}
+
+kvq_status check_page_state(const kvq_page_state *s) {
+  if (!s || !page_state_ok(*s)) return KVQ_ERR_ARG;
+  if (!s->table || !s->lengths || !s->free_pages || !s->n_free) return KVQ_ERR_ARG;
+  if (!aligned16(s->table) || !aligned16(s->lengths) || !aligned16(s->free_pages) ||
+      !aligned16(s->n_free))
+    return KVQ_ERR_ALIGN;
+  return KVQ_OK;
+}
+
+kvq_status check_paged(const kvq_paged_cache *c) {
+  if (!c || !paged_ok(*c)) return KVQ_ERR_ARG;
+  const kvq_status st = check_page_state(&c->state);
+  if (st != KVQ_OK) return st;
+  if (!c->pool || !c->ring) return KVQ_ERR_ARG;
+  if (!aligned16(c->pool) || !aligned16(c->ring)) return KVQ_ERR_ALIGN;
+  return KVQ_OK;
+}
+
+kvq_status check_plan(const kvq_page_state &s, const kvq_page_plan *p) {
+  if (!p || p->rows < 0 || p->rows > (1 << 28) || p->cap_work < 0) return KVQ_ERR_ARG;
+  if (p->cap_work < kvq_page_work(&s, p->rows)) return KVQ_ERR_WORKSPACE;
+  if (!p->offsets || !p->before || !p->after || !p->counts) return KVQ_ERR_ARG;
+  if (p->rows > 0 && (!p->row_slot || !p->positions || !p->work)) return KVQ_ERR_ARG;
+  if (!aligned16(p->offsets) || !aligned16(p->before) || !aligned16(p->after) ||
+      !aligned16(p->row_slot) || !aligned16(p->positions) || !aligned16(p->work) ||
+      !aligned16(p->counts))
+    return KVQ_ERR_ALIGN;
+  return KVQ_OK;
+}
+
+void ctl_add_pages(kvq::KernelCtl &c, const kvq_paged_cache &k) {
+#ifdef KVQ_DEBUG
+  size_t sz[6];
+  if (kvq_paged_sizes(&k, sz) != KVQ_OK) return;
+  ctl_add(c, k.state.table, sz[0]);
+  ctl_add(c, k.state.lengths, sz[1]);
+  ctl_add(c, k.pool, sz[4]);
+  ctl_add(c, k.ring, sz[5]);
+#else
+  (void)c;
+  (void)k;
+#endif
+}
+
+void ctl_add_plan(kvq::KernelCtl &c, const kvq_page_state &s, const kvq_page_plan &p) {
+  ctl_add(c, p.offsets, 4 * (static_cast<size_t>(s.slots) + 1));
+  ctl_add(c, p.before, 4 * static_cast<size_t>(s.slots));
+  ctl_add(c, p.after, 4 * static_cast<size_t>(s.slots));
+  ctl_add(c, p.work, 8 * static_cast<size_t>(p.cap_work));
+  ctl_add(c, p.counts, 16);
 }
 
 }  // namespace
@@ -882,6 +946,170 @@ kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32_t q_dty
   const int n = kvq::launch_block_rows(*cache, q, q_dtype, q_heads, n_q, selected, top_k, block,
                                        blocks, scale, out, out_dtype, ctl, s);
   return finish(n, "blocks_rows");
+}
+
+kvq_status kvq_paged_sizes(const kvq_paged_cache *cache, size_t sizes[6]) {
+  if (!cache || !sizes || !paged_ok(*cache)) return KVQ_ERR_ARG;
+  const kvq_page_state &s = cache->state;
+  const size_t d = static_cast<size_t>(cache->head_dim), h = static_cast<size_t>(cache->kv_heads);
+  const size_t slots = static_cast<size_t>(s.slots), pages = static_cast<size_t>(s.n_pages);
+  sizes[0] = 4 * slots * s.max_pages;
+  sizes[1] = 4 * slots;
+  sizes[2] = 4 * pages;
+  sizes[3] = 16;
+  sizes[4] = pages * h * (s.page / 32) * 40 * d;
+  sizes[5] = slots * h * kvq::paged_tiles(s.window) * 64 * d * elem_bytes(cache->win_dtype);
+  return KVQ_OK;
+}
+
+int32_t kvq_page_work(const kvq_page_state *s, int32_t rows) {
+  if (!s || !page_state_ok(*s) || rows < 0 || rows > (1 << 28)) return 0;
+  // a request with n new tokens writes at most n / 32 groups and its window's tiles, and a
+  // part of a group at either end
+  const int64_t requests = s->slots < rows ? s->slots : rows;
+  return static_cast<int32_t>(rows / 32 + (kvq::paged_tiles(s->window) + 3) * requests);
+}
+
+kvq_status kv_page_tables(const kvq_page_state *state, const int32_t *n_new,
+                          const kvq_page_plan *plan, int32_t advance, int32_t *dev_status,
+                          kvq_stream_t stream) {
+  kvq_status st = check_page_state(state);
+  if (st != KVQ_OK) return st;
+  st = check_plan(*state, plan);
+  if (st != KVQ_OK) return st;
+  if (!n_new) return KVQ_ERR_ARG;
+  if (!aligned16(n_new) || (dev_status && !aligned16(dev_status))) return KVQ_ERR_ALIGN;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  const size_t slots = static_cast<size_t>(state->slots);
+  ctl_add(ctl, state->table, 4 * slots * state->max_pages);
+  ctl_add(ctl, state->lengths, 4 * slots);
+  ctl_add(ctl, state->free_pages, 4 * static_cast<size_t>(state->n_pages));
+  ctl_add(ctl, state->n_free, 16);
+  ctl_add(ctl, n_new, 4 * slots);
+  ctl_add_plan(ctl, *state, *plan);
+  ctl_add(ctl, plan->row_slot, 4 * static_cast<size_t>(plan->rows));
+  ctl_add(ctl, plan->positions, 4 * static_cast<size_t>(plan->rows));
+  const int n = kvq::launch_page_tables(*state, n_new, *plan, advance != 0, ctl, sm_count(),
+                                        reinterpret_cast<cudaStream_t>(stream));
+  return finish(n, "page_tables");
+}
+
+kvq_status kv_append_pages(const kvq_paged_cache *cache, const kvq_page_plan *plan,
+                           const kvq_page_rows *rows, int32_t in_dtype, int32_t *dev_status,
+                           kvq_stream_t stream) {
+  kvq_status st = check_paged(cache);
+  if (st != KVQ_OK) return st;
+  st = check_plan(cache->state, plan);
+  if (st != KVQ_OK) return st;
+  if (!rows || (in_dtype != KVQ_F32 && in_dtype != KVQ_BF16)) return KVQ_ERR_ARG;
+  if (rows->k_stride_row < 0 || rows->k_stride_head < 0 || rows->v_stride_row < 0 ||
+      rows->v_stride_head < 0)
+    return KVQ_ERR_ARG;
+  if (plan->rows == 0) {
+    g_last_launches = 0;
+    g_last_path = "append_pages";
+    return KVQ_OK;
+  }
+  if (!rows->k_new || !rows->v_new) return KVQ_ERR_ARG;
+  const int64_t unit = in_dtype == KVQ_F32 ? 4 : 8;  // elements in 16 bytes
+  if (!aligned16(rows->k_new) || !aligned16(rows->v_new) || rows->k_stride_row % unit ||
+      rows->k_stride_head % unit || rows->v_stride_row % unit || rows->v_stride_head % unit ||
+      (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  if (static_cast<int64_t>(plan->cap_work) * cache->kv_heads > 0x7fffffffL)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  ctl_add_pages(ctl, *cache);
+  ctl_add_plan(ctl, cache->state, *plan);
+  const int64_t n1 = plan->rows - 1, h1 = cache->kv_heads - 1;
+  ctl_add(ctl, rows->k_new,
+          rows_bytes(n1 * rows->k_stride_row + h1 * rows->k_stride_head + cache->head_dim, 1,
+                     in_dtype));
+  ctl_add(ctl, rows->v_new,
+          rows_bytes(n1 * rows->v_stride_row + h1 * rows->v_stride_head + cache->head_dim, 1,
+                     in_dtype));
+  const kvq::PageRows r = {rows->k_new,         rows->v_new,         rows->k_stride_row,
+                           rows->k_stride_head, rows->v_stride_row, rows->v_stride_head,
+                           in_dtype};
+  const int n = kvq::launch_append_pages(kvq::paged_dims(*cache), *plan, r, ctl, sm_count(),
+                                         reinterpret_cast<cudaStream_t>(stream));
+  return finish(n, "append_pages");
+}
+
+kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *row_slot,
+                          const int32_t *positions, int32_t n_rows, void *k, void *v,
+                          int32_t out_dtype, int32_t *dev_status, kvq_stream_t stream) {
+  const kvq_status st = check_paged(cache);
+  if (st != KVQ_OK) return st;
+  if (n_rows < 0 || n_rows > (1 << 28) || (out_dtype != KVQ_F32 && out_dtype != KVQ_BF16))
+    return KVQ_ERR_ARG;
+  if (n_rows == 0) {
+    g_last_launches = 0;
+    g_last_path = "page_values";
+    return KVQ_OK;
+  }
+  if (!row_slot || !positions || !k || !v) return KVQ_ERR_ARG;
+  if (!aligned16(row_slot) || !aligned16(positions) || !aligned16(k) || !aligned16(v) ||
+      (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  ctl_add_pages(ctl, *cache);
+  ctl_add(ctl, row_slot, 4 * static_cast<size_t>(n_rows));
+  ctl_add(ctl, positions, 4 * static_cast<size_t>(n_rows));
+  const size_t bytes = rows_bytes(static_cast<long>(n_rows) * cache->kv_heads, cache->head_dim,
+                                  out_dtype);
+  ctl_add(ctl, k, bytes);
+  ctl_add(ctl, v, bytes);
+  const int n = kvq::launch_page_values(kvq::paged_dims(*cache), row_slot, positions, n_rows, k, v,
+                                        out_dtype, ctl, sm_count(),
+                                        reinterpret_cast<cudaStream_t>(stream));
+  return finish(n, "page_values");
+}
+
+kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
+                           int32_t q_heads, int32_t n_rows, const int32_t *row_slot,
+                           const int32_t *positions, float sm_scale, void *out,
+                           int32_t out_dtype, void *workspace, size_t *ws_bytes,
+                           int32_t *dev_status, kvq_stream_t stream) {
+  const kvq_status st = check_paged(cache);
+  if (st != KVQ_OK) return st;
+  if (!ws_bytes) return KVQ_ERR_ARG;
+  if (q_heads < 1 || q_heads % cache->kv_heads || n_rows < 0 || n_rows > 65535) return KVQ_ERR_ARG;
+  if (!row_slot && n_rows > cache->state.slots) return KVQ_ERR_ARG;
+  if ((q_dtype != KVQ_F32 && q_dtype != KVQ_BF16) ||
+      (out_dtype != KVQ_F32 && out_dtype != KVQ_BF16))
+    return KVQ_ERR_ARG;
+  if (q_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  const kvq::PagedDims d = kvq::paged_dims(*cache);
+  const size_t need = n_rows ? kvq::page_rows_workspace(d, q_heads, n_rows, sms) : 0;
+  if (!workspace) {
+    *ws_bytes = need;
+    return KVQ_OK;
+  }
+  if (*ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (n_rows == 0) {
+    g_last_launches = 0;
+    g_last_path = "pages_rows";
+    return KVQ_OK;
+  }
+  if (!q || !out) return KVQ_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned16(row_slot) ||
+      !aligned16(positions) || (dev_status && !aligned16(dev_status)))
+    return KVQ_ERR_ALIGN;
+  const float scale = resolve_scale(sm_scale, cache->head_dim);
+  kvq::KernelCtl ctl = make_ctl(dev_status);
+  const long rows = static_cast<long>(n_rows) * q_heads;
+  ctl_add_pages(ctl, *cache);
+  ctl_add(ctl, q, rows_bytes(rows, cache->head_dim, q_dtype));
+  ctl_add(ctl, out, rows_bytes(rows, cache->head_dim, out_dtype));
+  ctl_add(ctl, row_slot, 4 * static_cast<size_t>(n_rows));
+  ctl_add(ctl, positions, 4 * static_cast<size_t>(n_rows));
+  ctl_add(ctl, workspace, *ws_bytes);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int n = kvq::launch_page_rows(d, q, q_dtype, q_heads, n_rows, row_slot, positions, scale,
+                                      out, out_dtype, workspace, ctl, sms, s);
+  return finish(n, "pages_rows");
 }
 
 int32_t kvq_last_launch_count(void) { return g_last_launches; }

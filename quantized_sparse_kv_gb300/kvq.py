@@ -19,7 +19,7 @@ TORCH_OF = {F32: torch.float32, BF16: torch.bfloat16}
 
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_ARG", 2: "KVQ_ERR_ALIGN", 3: "KVQ_ERR_UNSUPPORTED",
           4: "KVQ_ERR_WORKSPACE", 5: "KVQ_ERR_CUDA"}
-DEV_INDEX, DEV_DUP, DEV_TIMEOUT, DEV_BOUNDS = 1, 2, 4, 8
+DEV_INDEX, DEV_DUP, DEV_TIMEOUT, DEV_BOUNDS, DEV_PAGES = 1, 2, 4, 8, 16
 # columns of kv_attend_stats (include/kvq.h, KVQ_STAT_*)
 STATS = ("entropy", "support", "top1", "top5", "top10", "zero", "p_zero", "p_tv", "p_sum",
          "qk_tv", "qk_agree")
@@ -65,6 +65,31 @@ class KvqRopeTensor(ctypes.Structure):
 class KvqSummary(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("block", ctypes.c_int32), ("cap_blocks", ctypes.c_int32)]
+
+
+class KvqPageState(ctypes.Structure):
+    _fields_ = [("slots", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p)]
+
+
+class KvqPagedCache(ctypes.Structure):
+    _fields_ = [("state", KvqPageState), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("win_dtype", ctypes.c_int32),
+                ("pool", ctypes.c_void_p), ("ring", ctypes.c_void_p)]
+
+
+class KvqPagePlan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cap_work", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("offsets", "before", "after", "row_slot", "positions",
+                                       "work", "counts")]
+
+
+class KvqPageRows(ctypes.Structure):
+    _fields_ = [("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("k_stride_row", "k_stride_head", "v_stride_row",
+                                      "v_stride_head")]
 
 
 _lib = None
@@ -130,6 +155,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kv_attend_blocks.argtypes = [cp, vp, i32, i32, i32, vp, i32, i32, f32, vp, i32, vp,
                                      ctypes.POINTER(sz), vp, vp]
     lib.kv_attend_blocks.restype = i32
+    pp, st = ctypes.POINTER(KvqPagedCache), ctypes.POINTER(KvqPageState)
+    pl = ctypes.POINTER(KvqPagePlan)
+    lib.kvq_paged_sizes.argtypes = [pp, ctypes.POINTER(sz)]
+    lib.kvq_paged_sizes.restype = i32
+    lib.kvq_page_work.argtypes = [st, i32]
+    lib.kvq_page_work.restype = i32
+    lib.kv_page_tables.argtypes = [st, vp, pl, i32, vp, vp]
+    lib.kv_page_tables.restype = i32
+    lib.kv_append_pages.argtypes = [pp, pl, ctypes.POINTER(KvqPageRows), i32, vp, vp]
+    lib.kv_append_pages.restype = i32
+    lib.kv_page_values.argtypes = [pp, vp, vp, i32, vp, vp, i32, vp, vp]
+    lib.kv_page_values.restype = i32
+    lib.kv_attend_pages.argtypes = [pp, vp, i32, i32, i32, vp, vp, f32, vp, i32, vp,
+                                    ctypes.POINTER(sz), vp, vp]
+    lib.kv_attend_pages.restype = i32
     lib.kvq_last_launch_count.argtypes = []
     lib.kvq_last_launch_count.restype = i32
     lib.kvq_last_path.argtypes = []
@@ -963,3 +1003,279 @@ def attend_blocks(cache: PackedCache, q: torch.Tensor, summary: BlockSummary, to
     a = AttendBlocks(cache, q, summary, top_k, n_sink, sm_scale, out_dtype)
     a.run()
     return a.out, a.selected, a.status
+
+
+# ------------------------------------------------------------------ the paged cache
+PAGES_MAX_SLOTS = 8192   # KVQ_PAGES_MAX_SLOTS
+
+
+class PageState:
+    """What the paged caches of a model's layers share: which pages each request
+    (slot) holds, the requests' lengths and the free pages, all on the device
+    (include/kvq.h, kvq_page_state). ``max_pages`` bounds one request (all pages
+    by default)."""
+
+    def __init__(self, slots: int, n_pages: int, page: int = 64, max_pages: int | None = None,
+                 window: int = 128, device="cuda"):
+        self.slots, self.n_pages, self.page = int(slots), int(n_pages), int(page)
+        self.max_pages = self.n_pages if max_pages is None else int(max_pages)
+        self.window = int(window)
+        self.struct = KvqPageState(self.slots, self.n_pages, self.page, self.max_pages,
+                                   self.window)
+        # (the smallest layer: the shape's limits, before anything is allocated)
+        self._check_shape(KvqPagedCache(self.struct, 1, 32, BF16))
+        i32 = torch.int32
+        self.table = torch.full((self.slots, self.max_pages), -1, dtype=i32, device=device)
+        self.lengths = torch.zeros(self.slots, dtype=i32, device=device)
+        self.free_pages = torch.arange(self.n_pages, dtype=i32, device=device)
+        self.n_free = torch.zeros(4, dtype=i32, device=device)
+        self.n_free[0] = self.n_pages
+        self.device = _one_device(self.table)
+        for name in ("table", "lengths", "free_pages", "n_free"):
+            setattr(self.struct, name, getattr(self, name).data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    @staticmethod
+    def _check_shape(struct: KvqPagedCache) -> list[int]:
+        out = (ctypes.c_size_t * 6)()
+        _check(load_library().kvq_paged_sizes(ctypes.byref(struct), out), "kvq_paged_sizes")
+        return list(out)
+
+    def cut(self, length: int) -> int:
+        """Tokens of a request of this length that are held as int4."""
+        return (length - self.window) // 32 * 32 if length >= self.window else 0
+
+    def pages(self, length: int) -> int:
+        """Pages a request of this length holds."""
+        return -(-self.cut(length) // self.page)
+
+    def restore(self, table=None, lengths=None, free_pages=None, n_free=None) -> "PageState":
+        """Copy saved contents in (None: stays as it is)."""
+        for name, x in (("table", table), ("lengths", lengths), ("free_pages", free_pages),
+                        ("n_free", n_free)):
+            if x is not None:
+                _integers(x, name)
+                if x.shape != getattr(self, name).shape:
+                    raise ValueError(f"{name} must have the shape of the state's")
+                getattr(self, name).copy_(x)
+        return self
+
+
+class PagedCache:
+    """One layer's pages and windows over a PageState (kvq_paged_cache); ``dtype`` is
+    the windows' type, f32 or bf16."""
+
+    def __init__(self, state: PageState, kv_heads: int, head_dim: int, dtype="bf16"):
+        self.state, self.kv_heads, self.head_dim = state, int(kv_heads), int(head_dim)
+        self.win = _dtype(dtype)
+        self.device = state.device
+        self.struct = KvqPagedCache(state.struct, self.kv_heads, self.head_dim, self.win)
+        sizes = PageState._check_shape(self.struct)
+        self.pool = torch.empty(sizes[4], dtype=torch.uint8, device=self.device)
+        self.ring = torch.empty(sizes[5], dtype=torch.uint8, device=self.device)
+        self.struct.pool, self.struct.ring = self.pool.data_ptr(), self.ring.data_ptr()
+        self.ref = ctypes.byref(self.struct)
+
+
+class PageTables(_Prepared):
+    """A prepared kv_page_tables call: ``n_new`` (slots,) says what every request adds
+    (int32 ones are read in place, other integers converted by every run): tokens, 0, or
+    -1 for a request that ends; the step's tensors hold ``rows`` token rows. After
+    ``run()`` it is the step's plan: ``offsets``, ``row_slot``, ``positions`` (what
+    Rope takes as (rows, 1)), ``before``, ``after``, ``free_after``. ``run(advance=False)``
+    looks ahead without moving the state."""
+
+    def __init__(self, state: PageState, n_new: torch.Tensor, rows: int):
+        self.lib = load_library()
+        self.state, self.rows = state, int(rows)
+        _integers(n_new, "n_new")
+        self.device = _one_device(state.table, n_new)
+        if tuple(n_new.shape) != (state.slots,):
+            raise ValueError("n_new must be (slots,)")
+        if not 0 <= self.rows <= 1 << 28:
+            raise ValueError("rows must be in [0, 2^28]")
+        self._copies = []
+        self.n_new = _static(self._copies, n_new, torch.int32)
+        i32, dev = torch.int32, self.device
+        self.offsets = torch.empty(state.slots + 1, dtype=i32, device=dev)
+        self.before = torch.empty(state.slots, dtype=i32, device=dev)
+        self.after = torch.empty(state.slots, dtype=i32, device=dev)
+        self.row_slot = torch.empty(self.rows, dtype=i32, device=dev)
+        self.positions = torch.empty(self.rows, dtype=i32, device=dev)
+        cap = int(self.lib.kvq_page_work(state.ref, self.rows))
+        self.work = torch.empty((cap, 2), dtype=i32, device=dev)
+        self.counts = torch.zeros(4, dtype=i32, device=dev)
+        self.status = new_status(dev)
+        self.struct = KvqPagePlan(self.rows, cap, *(
+            t.data_ptr() or None for t in (self.offsets, self.before, self.after, self.row_slot,
+                                           self.positions, self.work, self.counts)))
+        self.ref = ctypes.byref(self.struct)
+        self._ptrs = (_ptr(self.n_new), _ptr(self.status))
+
+    @property
+    def free_after(self) -> torch.Tensor:
+        """Pages that are free after the step, (1,)."""
+        return self.counts[:1]
+
+    def _run(self, advance: bool = True) -> "PageTables":
+        if self._copies:
+            _refresh(self._copies)
+        n_new, status = self._ptrs
+        _check(self.lib.kv_page_tables(self.state.ref, n_new, self.ref, 1 if advance else 0,
+                                       status, self._raw_stream()), "kv_page_tables")
+        return self
+
+
+def page_tables(state: PageState, n_new: torch.Tensor, rows: int) -> PageTables:
+    """kv_page_tables; returns the step's plan."""
+    return PageTables(state, n_new, rows).run()
+
+
+def _row_view(copies: list, x: torch.Tensor) -> torch.Tensor:
+    """x (rows, heads, D) if its rows can be read in place, else as _static."""
+    unit = 16 // x.element_size()
+    ok = (x.stride(2) == 1 and x.data_ptr() % 16 == 0 and
+          all(s >= 0 and (s % unit == 0 or n == 1) for s, n in zip(x.stride()[:2], x.shape[:2])))
+    return x if ok else _static(copies, x)
+
+
+class AppendPages(_Prepared):
+    """A prepared kv_append_pages call: k, v (rows, kv_heads, D) of the plan's rows, at
+    any strides (views of a projection's rows are read in place when they start on 16
+    bytes). The plan may be run again for every step; one plan serves all layers."""
+
+    def __init__(self, cache: PagedCache, plan: PageTables, k: torch.Tensor, v: torch.Tensor):
+        self.lib = load_library()
+        self.cache, self.plan = cache, plan
+        if plan.state is not cache.state:
+            raise ValueError("the plan is another state's")
+        self.device = _one_device(cache.pool, k, v)
+        if k.dtype not in (torch.float32, torch.bfloat16) or v.dtype != k.dtype:
+            raise TypeError("k and v must both be float32 or bfloat16")
+        shape = (plan.rows, cache.kv_heads, cache.head_dim)
+        if tuple(k.shape) != shape or v.shape != k.shape:
+            raise ValueError("k and v must be (rows, kv_heads, D)")
+        self._copies = []
+        self.k, self.v = (_row_view(self._copies, x.detach()) for x in (k, v))
+        st = [s if n > 1 else 0 for x in (self.k, self.v)
+              for s, n in zip(x.stride()[:2], x.shape[:2])]
+        self.status = new_status(self.device)
+        self.rows = KvqPageRows(self.k.data_ptr() or None, self.v.data_ptr() or None, *st)
+        self._args = (cache.ref, plan.ref, ctypes.byref(self.rows),
+                      F32 if k.dtype == torch.float32 else BF16, _ptr(self.status))
+
+    def _run(self) -> PagedCache:
+        if self._copies:
+            _refresh(self._copies)
+        _check(self.lib.kv_append_pages(*self._args, self._raw_stream()), "kv_append_pages")
+        return self.cache
+
+
+def append_pages(cache: PagedCache, plan: PageTables, k: torch.Tensor,
+                 v: torch.Tensor) -> PagedCache:
+    """kv_append_pages: the plan's new tokens into one layer's cache."""
+    return AppendPages(cache, plan, k, v).run()
+
+
+class PageValues(_Prepared):
+    """A prepared kv_page_values call: keys and values of the tokens (row_slot[i],
+    positions[i]) as attention reads them, two (rows, kv_heads, D) tensors of the windows'
+    type unless ``out_dtype`` says another. A row with slot -1 stays as it was (zeros)."""
+
+    def __init__(self, cache: PagedCache, row_slot: torch.Tensor, positions: torch.Tensor,
+                 out_dtype=None):
+        self.lib = load_library()
+        self.cache = cache
+        _integers(row_slot, "row_slot")
+        _integers(positions, "positions")
+        self.device = _one_device(cache.pool, row_slot, positions)
+        if row_slot.dim() != 1 or positions.shape != row_slot.shape:
+            raise ValueError("row_slot and positions must be (rows,)")
+        self._copies = []
+        self.row_slot = _static(self._copies, row_slot, torch.int32)
+        self.positions = _static(self._copies, positions, torch.int32)
+        n = self.row_slot.numel()
+        dt = _dtype(out_dtype) if out_dtype is not None else cache.win
+        self.k, self.v = (torch.zeros((n, cache.kv_heads, cache.head_dim), dtype=TORCH_OF[dt],
+                                      device=self.device) for _ in range(2))
+        self.status = new_status(self.device)
+        self._args = (cache.ref, _ptr(self.row_slot), _ptr(self.positions), n, _ptr(self.k),
+                      _ptr(self.v), dt, _ptr(self.status))
+
+    def _run(self):
+        if self._copies:
+            _refresh(self._copies)
+        _check(self.lib.kv_page_values(*self._args, self._raw_stream()), "kv_page_values")
+        return self.k, self.v
+
+
+def page_values(cache: PagedCache, row_slot: torch.Tensor, positions: torch.Tensor,
+                out_dtype=None):
+    """kv_page_values; returns (k, v)."""
+    return PageValues(cache, row_slot, positions, out_dtype).run()
+
+
+class AttendPages(_Prepared):
+    """A prepared kv_attend_pages call: q (rows, q_heads, D), one query row per new token;
+    ``row_slot`` (rows,) its request (row i is request i without it; -1: the row of
+    ``out`` stays as it was, zeros unless the caller gives the buffer), ``positions``
+    (rows,) its token's position (without it a row sees its whole request). The plan's
+    ``row_slot`` and ``positions`` are what a step passes. Lengths are read on the device:
+    a captured run serves later steps."""
+
+    def __init__(self, cache: PagedCache, q: torch.Tensor, row_slot: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, sm_scale: float = 0.0, out_dtype=None,
+                 out=None):
+        self.lib = load_library()
+        self.cache = cache
+        self.device = _one_device(cache.pool, q, row_slot, positions, out)
+        if q.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("q must be float32 or bfloat16")
+        if q.dim() != 3 or q.shape[2] != cache.head_dim:
+            raise ValueError("q must be (rows, q_heads, D)")
+        self._copies = []
+        self.q = _static(self._copies, q)
+        n, hq, _ = self.q.shape
+        for name, x in (("row_slot", row_slot), ("positions", positions)):
+            if x is not None:
+                _integers(x, name)
+                if tuple(x.shape) != (n,):
+                    raise ValueError(f"{name} must be (rows,)")
+                x = _static(self._copies, x, torch.int32)
+            setattr(self, name, x)
+        self.q_dt = F32 if q.dtype == torch.float32 else BF16
+        self.out_dt = (_dtype(out_dtype) if out_dtype is not None else
+                       self.q_dt if out is None else
+                       F32 if out.dtype == torch.float32 else BF16)
+        self.out = out if out is not None else torch.zeros(
+            self.q.shape, dtype=TORCH_OF[self.out_dt], device=self.device)
+        if (self.out.shape != self.q.shape or self.out.dtype != TORCH_OF[self.out_dt] or
+                not self.out.is_contiguous()):
+            raise ValueError("out must be a dense tensor of q's shape")
+        self.status = new_status(self.device)
+        self.ws, self._kept = None, []
+        args = (cache.ref, _ptr(self.q), self.q_dt, hq, n, _ptr(self.row_slot),
+                _ptr(self.positions), float(sm_scale or 0.0), _ptr(self.out), self.out_dt)
+        need = ctypes.c_size_t(0)
+        with torch.cuda.device(self.device):
+            _check(self.lib.kv_attend_pages(*args, None, ctypes.byref(need), None, None),
+                   "kv_attend_pages")
+        self._workspace(int(need.value))
+        self._args = (*args, _ptr(self.ws), ctypes.byref(self.ws_bytes), _ptr(self.status))
+        self.path = None
+
+    def _run(self) -> torch.Tensor:
+        if self._copies:
+            _refresh(self._copies)
+        _check(self.lib.kv_attend_pages(*self._args, self._raw_stream()), "kv_attend_pages")
+        if self.path is None:
+            self.path = self.lib.kvq_last_path().decode()
+        return self.out
+
+
+def attend_pages(cache: PagedCache, q: torch.Tensor, row_slot: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, sm_scale: float = 0.0, out_dtype=None):
+    """kv_attend_pages; returns (out, status tensor)."""
+    a = AttendPages(cache, q, row_slot, positions, sm_scale, out_dtype)
+    a.run()
+    return a.out, a.status
