@@ -1082,7 +1082,10 @@ kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t 
   if (q_heads > 65535) return KVQ_ERR_UNSUPPORTED;
   const int sms = sm_count();
   const kvq::PagedDims d = kvq::paged_dims(*cache);
-  const size_t need = n_rows ? kvq::page_rows_workspace(d, q_heads, n_rows, sms) : 0;
+  const bool tensor = kvq::attend_pages_supported(d, q_heads, n_rows);
+  const size_t need = n_rows == 0 ? 0
+                      : tensor    ? kvq::attend_pages_workspace(d, q_heads, n_rows, sms)
+                                  : kvq::page_rows_workspace(d, q_heads, n_rows, sms);
   if (!workspace) {
     *ws_bytes = need;
     return KVQ_OK;
@@ -1090,7 +1093,7 @@ kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t 
   if (*ws_bytes < need) return KVQ_ERR_WORKSPACE;
   if (n_rows == 0) {
     g_last_launches = 0;
-    g_last_path = "pages_rows";
+    g_last_path = tensor ? "pages_tensor" : "pages_rows";
     return KVQ_OK;
   }
   if (!q || !out) return KVQ_ERR_ARG;
@@ -1107,6 +1110,12 @@ kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t 
   ctl_add(ctl, positions, 4 * static_cast<size_t>(n_rows));
   ctl_add(ctl, workspace, *ws_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (tensor) {
+    const int n = kvq::launch_attend_pages(d, q, q_dtype, q_heads, n_rows, row_slot, positions,
+                                           static_cast<float>(scale * kLog2e), out, out_dtype,
+                                           workspace, ctl, sms, s);
+    return finish(n, "pages_tensor");
+  }
   const int n = kvq::launch_page_rows(d, q, q_dtype, q_heads, n_rows, row_slot, positions, scale,
                                       out, out_dtype, workspace, ctl, sms, s);
   return finish(n, "pages_rows");

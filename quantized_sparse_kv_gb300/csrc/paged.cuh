@@ -100,6 +100,11 @@ int launch_append_pages(const PagedDims &d, const kvq_page_plan &p, const PageRo
 int launch_page_values(const PagedDims &d, const int32_t *slot, const int32_t *pos, int n,
                        void *k, void *v, int out_dt, const KernelCtl &ctl, int num_sms,
                        cudaStream_t s);
+bool attend_pages_supported(const PagedDims &d, int Hq, int rows);
+size_t attend_pages_workspace(const PagedDims &d, int Hq, int rows, int num_sms);
+int launch_attend_pages(const PagedDims &d, const void *q, int q_dt, int Hq, int rows,
+                        const int32_t *slot, const int32_t *pos, float scale_log2, void *out,
+                        int out_dt, void *ws, const KernelCtl &ctl, int num_sms, cudaStream_t s);
 int launch_page_rows(const PagedDims &d, const void *q, int q_dt, int Hq, int rows,
                      const int32_t *slot, const int32_t *pos, float scale, void *out, int out_dt,
                      void *ws, const KernelCtl &ctl, int num_sms, cudaStream_t s);

@@ -265,7 +265,8 @@ def test_steps(kvq, slots, pages, page, most, window, hk, group, d, wdt, in_dt, 
         if step % 3 == 2 or step == 13:
             check_values(kvq, cache, model, tokens, wdt, "f32" if step % 2 else "bf16")
             check_attention(kvq, cache, model, tokens, wdt, group, gen,
-                            TOL_TENSOR if tensor else TOL_F32, types[q_dt], rng)
+                            TOL_TENSOR if tensor else TOL_F32, types[q_dt], rng,
+                            "pages_tensor" if tensor else "pages_rows")
     assert max(model.length) > 200
 
 
