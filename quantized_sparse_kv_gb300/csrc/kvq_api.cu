@@ -964,10 +964,7 @@ kvq_status kvq_paged_sizes(const kvq_paged_cache *cache, size_t sizes[6]) {
 
 int32_t kvq_page_work(const kvq_page_state *s, int32_t rows) {
   if (!s || !page_state_ok(*s) || rows < 0 || rows > (1 << 28)) return 0;
-  // a request with n new tokens writes at most n / 32 groups and its window's tiles, and a
-  // part of a group at either end
-  const int64_t requests = s->slots < rows ? s->slots : rows;
-  return static_cast<int32_t>(rows / 32 + (kvq::paged_tiles(s->window) + 3) * requests);
+  return kvq::page_work_bound(s->window, s->slots, rows);
 }
 
 kvq_status kv_page_tables(const kvq_page_state *state, const int32_t *n_new,
@@ -1061,7 +1058,7 @@ kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *row_slot,
   ctl_add(ctl, k, bytes);
   ctl_add(ctl, v, bytes);
   const int n = kvq::launch_page_values(kvq::paged_dims(*cache), row_slot, positions, n_rows, k, v,
-                                        out_dtype, ctl, sm_count(),
+                                        out_dtype, ctl,
                                         reinterpret_cast<cudaStream_t>(stream));
   return finish(n, "page_values");
 }

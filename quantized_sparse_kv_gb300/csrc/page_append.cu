@@ -3,7 +3,19 @@
 //
 // int4 rule of kv_pack ("KV殘差窗口", section 固定預算): scale = fl(amax / 7), code =
 // clamp(rint(fl(x / scale)), -7, 7), K per channel over the 32 tokens of a group, V per
-// token over 32 features.
+// token over 32 features. Values that are bf16 take the reciprocal and one correction step
+// (int4_round.cuh, the same codes), others the division.
+//
+// Append. A CTA of about D threads has one 32-token group of one head. Half of its
+// threads take K: a thread has a pair of channels of all 32 tokens in registers, so the
+// maxima need no exchange and a warp reads whole rows. The others take V: a thread has four
+// features of 16 tokens; eight lanes share a token's 32 features, their maxima meet in
+// three lane exchanges for two tokens at a time. V codes are made from (token, token + 8)
+// pairs of one feature, which is the byte a record's words hold; lanes of features y and
+// y + 8 exchange half of their bytes and each keeps half of the words. The record (40 D
+// bytes) is put together in shared memory and leaves as one bulk copy. All of a thread's
+// loads are issued before the first is used, and several CTAs share an SM: reads in flight
+// are what a prompt's append is bound by.
 #include <algorithm>
 
 #include "int4_round.cuh"
@@ -25,69 +37,296 @@ __device__ __forceinline__ int int4_code(float x, float scale) {
   if (scale == 0.0f) return 0;
   return max(-7, min(7, __float2int_rn(__fdiv_rn(x, scale))));
 }
-
-__device__ __forceinline__ float load_elem(const void *p, size_t i, int dt) {
-  return dt == KVQ_F32 ? static_cast<const float *>(p)[i]
-                       : bf16_to_f32(static_cast<const uint16_t *>(p)[i]);
+// Two codes + 8 as a byte, by the division (out of line: the usual bf16 values do without).
+__device__ __noinline__ uint32_t code_byte_div(float lo, float hi, float s_lo, float s_hi) {
+  return static_cast<uint32_t>(int4_code(lo, s_lo) + 8 + 16 * (int4_code(hi, s_hi) + 8));
 }
+
 __device__ __forceinline__ size_t el_bytes(int dt) { return dt == KVQ_F32 ? 4 : 2; }
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A pair of values as the cache keeps them: bf16 pairs in one register.
+struct PairB {
+  uint32_t w;
+  __device__ __forceinline__ void set(float x, float y) { w = pack_bf2(x, y); }
+  __device__ __forceinline__ float lo() const { return bf_lo(w); }
+  __device__ __forceinline__ float hi() const { return bf_hi(w); }
+};
+struct PairF {
+  float2 f;
+  __device__ __forceinline__ void set(float x, float y) { f = make_float2(x, y); }
+  __device__ __forceinline__ float lo() const { return f.x; }
+  __device__ __forceinline__ float hi() const { return f.y; }
+};
+
+// Types of the step's rows and of the windows.
+template <typename In, typename Win>
+struct Types {
+  static constexpr bool kBf16 = sizeof(Win) == 2;  // the values are bf16
+  using Pair = typename std::conditional<kBf16, PairB, PairF>::type;
+
+  // elements e and e + 1 of a row of the step
+  static __device__ __forceinline__ Pair row2(const AppendPagesArgs &a, const void *rows, size_t e) {
+    const In *p = static_cast<const In *>(rows) + e;
+    Pair x;
+    x.set(0.0f, 0.0f);
+    if (!in_bounds(a.ctl, p, 2 * sizeof(In))) return x;
+    if constexpr (sizeof(In) == 4) {
+      const float2 f = *reinterpret_cast<const float2 *>(p);
+      x.set(f.x, f.y);
+    } else {
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+      if constexpr (kBf16)
+        x.w = w;
+      else
+        x.set(bf_lo(w), bf_hi(w));
+    }
+    return x;
+  }
+  // elements at e0 and e1 of the windows
+  static __device__ __forceinline__ Pair win2(const AppendPagesArgs &a, size_t e0, size_t e1) {
+    const Win *p = static_cast<const Win *>(a.d.ring);
+    Pair x;
+    x.set(0.0f, 0.0f);
+    if (in_bounds(a.ctl, p + e0, sizeof(Win)) && in_bounds(a.ctl, p + e1, sizeof(Win)))
+      x.set(load_f32(p + e0), load_f32(p + e1));
+    return x;
+  }
+};
 
 // One work entry and head: what the step does with 32-token group g of slot s.
 struct GroupWork {
   int s, g, h, before, after, c1, w0, w1, row0;
 };
 
-// Value of token pos, feature d as the cache keeps it (rounded to the window's type).
-template <bool kV>
-__device__ __forceinline__ float source(const AppendPagesArgs &a, const GroupWork &w, int pos,
-                                        int d) {
-  const int D = a.d.D;
-  if (pos < w.before) {
-    const size_t e = a.d.tile_at(w.s, w.h, pos >> 5) +
-                     (kV ? 32 * D + ringv_at(pos & 31, d, D) : ringk_at(pos & 31, d, D));
-    const size_t b = el_bytes(a.d.win_dt);
-    if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.d.ring) + e * b, b)) return 0.0f;
-    return load_elem(a.d.ring, e, a.d.win_dt);
-  }
+__device__ __forceinline__ size_t row_elem(const AppendPagesArgs &a, const GroupWork &w, int pos,
+                                           bool v) {
   const int64_t row = w.row0 + pos - w.before;
-  const void *p = kV ? a.r.v : a.r.k;
-  const size_t e = static_cast<size_t>(row * (kV ? a.r.vsr : a.r.ksr) +
-                                       w.h * (kV ? a.r.vsh : a.r.ksh) + d);
-  const size_t b = el_bytes(a.r.dtype);
-  if (!in_bounds(a.ctl, static_cast<const uint8_t *>(p) + e * b, b)) return 0.0f;
-  const float x = load_elem(p, e, a.r.dtype);
-  return a.d.win_dt == KVQ_F32 ? x : __bfloat162float(__float2bfloat16_rn(x));
+  return static_cast<size_t>(v ? row * a.r.vsr + w.h * a.r.vsh : row * a.r.ksr + w.h * a.r.ksh);
 }
 
-// The new tokens of window group g into its tile.
+// The new tokens of window group g into its tile, eight elements of a row at a time (a
+// tile's K keeps them together, its V has them apart), K and V in turn.
+template <typename In, typename Win>
 __device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const GroupWork &w, int g) {
-  const int D = a.d.D, p0 = max(w.before, 32 * g), p1 = min(w.after, 32 * g + 32);
+  using T = Types<In, Win>;
+  const int D = a.d.D, p0 = max(w.before, 32 * g), p1 = min(w.after, 32 * g + 32), pieces = D / 8;
   const size_t tile = a.d.tile_at(w.s, w.h, g);
-  for (int i = threadIdx.x; i < 2 * D * (p1 - p0); i += blockDim.x) {
-    const int pos = p0 + i / (2 * D), e = i % (2 * D), d = e < D ? e : e - D, r = pos & 31;
-    const float x = e < D ? source<false>(a, w, pos, d) : source<true>(a, w, pos, d);
-    const size_t o = tile + (e < D ? ringk_at(r, d, D) : 32 * D + ringv_at(r, d, D));
-    const size_t b = el_bytes(a.d.win_dt);
-    if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.d.ring) + o * b, b)) continue;
-    if (a.d.win_dt == KVQ_F32)
-      static_cast<float *>(a.d.ring)[o] = x;
-    else
-      static_cast<__nv_bfloat16 *>(a.d.ring)[o] = __float2bfloat16_rn(x);
+  Win *ring = static_cast<Win *>(a.d.ring);
+  for (int i = threadIdx.x; i < 2 * (p1 - p0) * pieces; i += blockDim.x) {
+    const int pos = p0 + i / (2 * pieces), x = i % (2 * pieces), d = 8 * (x % pieces), r = pos & 31;
+    const bool v = x >= pieces;
+    const size_t e = row_elem(a, w, pos, v) + d;
+    typename T::Pair y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = T::row2(a, v ? a.r.v : a.r.k, e + 2 * k);
+    if (v) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        Win *o = ring + tile + 32 * D + ringv_at(r, d + k, D);
+        if (in_bounds(a.ctl, o, sizeof(Win))) store_from_f32(o, k & 1 ? y[k / 2].hi() : y[k / 2].lo());
+      }
+    } else {
+      Win *o = ring + tile + ringk_at(r, d, D);  // order 0 4 1 5 2 6 3 7
+      if (!in_bounds(a.ctl, o, 8 * sizeof(Win))) continue;
+      if constexpr (T::kBf16) {
+        *reinterpret_cast<uint4 *>(o) = make_uint4(
+            __byte_perm(y[0].w, y[2].w, 0x5410), __byte_perm(y[0].w, y[2].w, 0x7632),
+            __byte_perm(y[1].w, y[3].w, 0x5410), __byte_perm(y[1].w, y[3].w, 0x7632));
+      } else {
+        reinterpret_cast<float4 *>(o)[0] = make_float4(y[0].lo(), y[2].lo(), y[0].hi(), y[2].hi());
+        reinterpret_cast<float4 *>(o)[1] = make_float4(y[1].lo(), y[3].lo(), y[1].hi(), y[3].hi());
+      }
+    }
   }
 }
 
-constexpr int kApThreads = 256;
+// K of a group: thread p has channels 2p and 2p + 1.
+template <typename In, typename Win>
+__device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork &w, uint8_t *rec,
+                                       int p) {
+  using T = Types<In, Win>;
+  const int D = a.d.D, t0 = 32 * w.g;
+  if (2 * p >= D) return;
+  typename T::Pair x[32];
+  const size_t tile = a.d.tile_at(w.s, w.h, w.g);
+  const size_t e0 = row_elem(a, w, t0, false) + 2 * p;
+#pragma unroll
+  for (int t = 0; t < 32; ++t) {
+    if (t0 + t < w.before)
+      x[t] = T::win2(a, tile + ringk_at(t, 2 * p, D), tile + ringk_at(t, 2 * p + 1, D));
+    else
+      x[t] = T::row2(a, a.r.k, e0 + static_cast<size_t>(t * a.r.ksr));
+  }
+  float a0, a1;
+  if constexpr (T::kBf16) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int t = 0; t < 32; ++t) m = max_bf16x2(m, x[t].w & 0x7fff7fffu);
+    a0 = bf_lo(m);
+    a1 = bf_hi(m);
+  } else {
+    a0 = a1 = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 32; ++t) {
+      a0 = fmaxf(a0, fabsf(x[t].lo()));
+      a1 = fmaxf(a1, fabsf(x[t].hi()));
+    }
+  }
+  const bool fast = T::kBf16 && recip_ok(a0) && recip_ok(a1);
+  const float s0 = fast ? scale_recip(a0) : int4_scale(a0);
+  const float s1 = fast ? scale_recip(a1) : int4_scale(a1);
+  float *ks = reinterpret_cast<float *>(rec + rec_kscale(D));
+  ks[kscale_at(2 * p, D)] = s0;
+  ks[kscale_at(2 * p + 1, D)] = s1;
+  if (fast) {
+    if constexpr (T::kBf16) {
+      const float r0 = recip_of(s0), r1 = recip_of(s1);
+#pragma unroll
+      for (int t = 0; t < 32; ++t)
+        rec[t * (D / 2) + p] = static_cast<uint8_t>(code_byte_recip(x[t].w, -s0, -s1, r0, r1));
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 32; ++t)
+      rec[t * (D / 2) + p] = static_cast<uint8_t>(code_byte_div(x[t].lo(), x[t].hi(), s0, s1));
+  }
+}
+
+// V of a group: thread i has features 32 b + 4 e .. + 3 of the 16 tokens of half m, i = (m,
+// b, e); every lane of a warp takes part in the exchanges.
+template <typename In, typename Win>
+__device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork &w, uint8_t *rec,
+                                       int i) {
+  using T = Types<In, Win>;
+  const int D = a.d.D, nb = D / 32, m = i / (8 * nb), b = i / 8 % nb, e = i & 7, d0 = 32 * b + 4 * e;
+  const bool live = m < 2;
+  const int t0 = 32 * w.g + 16 * m;
+  typename T::Pair x[16][2];
+  const size_t tile = a.d.tile_at(w.s, w.h, w.g) + 32 * D;
+  const size_t e0 = row_elem(a, w, t0, true) + d0;
+#pragma unroll
+  for (int t = 0; t < 16; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!live)
+        x[t][k].set(0.0f, 0.0f);
+      else if (t0 + t < w.before)
+        x[t][k] = T::win2(a, tile + ringv_at(16 * m + t, d0 + 2 * k, D),
+                          tile + ringv_at(16 * m + t, d0 + 2 * k + 1, D));
+      else
+        x[t][k] = T::row2(a, a.r.v, e0 + static_cast<size_t>(t * a.r.vsr) + 2 * k);
+    }
+  // maxima of tokens 2n and 2n + 1; lane e keeps those of its own two
+  float m0 = 0.0f, m1 = 0.0f;
+  bool fast = T::kBf16;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    float u, v;
+    if constexpr (T::kBf16) {
+      const uint32_t p = max_bf16x2(x[2 * n][0].w & 0x7fff7fffu, x[2 * n][1].w & 0x7fff7fffu);
+      const uint32_t q = max_bf16x2(x[2 * n + 1][0].w & 0x7fff7fffu, x[2 * n + 1][1].w & 0x7fff7fffu);
+      uint32_t y = max_bf16x2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) y = max_bf16x2(y, __shfl_xor_sync(~0u, y, o));
+      u = bf_lo(y);
+      v = bf_hi(y);
+      fast = fast && recip_ok(u) && recip_ok(v);
+    } else {
+      u = fmaxf(fmaxf(fabsf(x[2 * n][0].lo()), fabsf(x[2 * n][0].hi())),
+                fmaxf(fabsf(x[2 * n][1].lo()), fabsf(x[2 * n][1].hi())));
+      v = fmaxf(fmaxf(fabsf(x[2 * n + 1][0].lo()), fabsf(x[2 * n + 1][0].hi())),
+                fmaxf(fabsf(x[2 * n + 1][1].lo()), fabsf(x[2 * n + 1][1].hi())));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        u = fmaxf(u, __shfl_xor_sync(~0u, u, o));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+      }
+    }
+    if (n == e) {
+      m0 = u;
+      m1 = v;
+    }
+  }
+  fast = __all_sync(~0u, fast);
+  const float s0 = fast ? scale_recip(m0) : int4_scale(m0);
+  const float s1 = fast ? scale_recip(m1) : int4_scale(m1);
+  const float r0 = fast ? recip_of(s0) : 0.0f, r1 = fast ? recip_of(s1) : 0.0f;
+  if (live) {
+    float *vs = reinterpret_cast<float *>(rec + rec_vscale(D));
+    vs[vscale_at(16 * m + 2 * e, b, D)] = s0;
+    vs[vscale_at(16 * m + 2 * e + 1, b, D)] = s1;
+  }
+  uint32_t *words = reinterpret_cast<uint32_t *>(rec + rec_vcode(D));
+  const bool upper = e & 2;  // features y + 8
+  const int f = 2 * b + (e >> 2), g0 = 4 * (e & 1) + (upper ? 2 : 0);
+  const int group = (threadIdx.x & 24);  // first of the eight lanes
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    // scales of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+    float s[4], r[4];
+    s[0] = __shfl_sync(~0u, s0, group + t);
+    s[1] = __shfl_sync(~0u, s1, group + t);
+    s[2] = __shfl_sync(~0u, s0, group + t + 4);
+    s[3] = __shfl_sync(~0u, s1, group + t + 4);
+    if (T::kBf16) {
+      r[0] = __shfl_sync(~0u, r0, group + t);
+      r[1] = __shfl_sync(~0u, r1, group + t);
+      r[2] = __shfl_sync(~0u, r0, group + t + 4);
+      r[3] = __shfl_sync(~0u, r1, group + t + 4);
+    }
+    uint32_t c[2][4];  // byte of feature j: tokens 2t + z and 2t + z + 8
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const auto &p = x[2 * t + z][j >> 1], &q = x[2 * t + z + 8][j >> 1];
+        if (T::kBf16 && fast) {
+          if constexpr (T::kBf16)
+            c[z][j] = code_byte_recip(__byte_perm(p.w, q.w, j & 1 ? 0x7632 : 0x5410), -s[z],
+                                      -s[z + 2], r[z], r[z + 2]);
+        } else {
+          c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), s[z], s[z + 2]);
+        }
+      }
+    // bytes: features j, j + 1 of token 2t, then of 2t + 1
+    const uint32_t c01 = __byte_perm(__byte_perm(c[0][0], c[0][1], 0x0040),
+                                     __byte_perm(c[1][0], c[1][1], 0x0040), 0x5410);
+    const uint32_t c23 = __byte_perm(__byte_perm(c[0][2], c[0][3], 0x0040),
+                                     __byte_perm(c[1][2], c[1][3], 0x0040), 0x5410);
+    const uint32_t other = __shfl_xor_sync(~0u, upper ? c01 : c23, 2);
+    const uint32_t lo = upper ? other : c01, hi = upper ? c23 : other;
+    if (live) {
+      words[vword_at(m, g0, t, f, D)] = __byte_perm(lo, hi, 0x6240);
+      words[vword_at(m, g0 + 1, t, f, D)] = __byte_perm(lo, hi, 0x7351);
+    }
+  }
+}
+
+__device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
 
 // A CTA per (group of the work list, head). A group that is packed may have tokens in a
 // tile of the window that the step's new tokens take over: the CTA that packs it writes
 // them too, behind its own reads, and the tile's own entry leaves them to it, so no
 // order between CTAs is needed.
-__global__ void __launch_bounds__(kApThreads) append_pages_kernel(const AppendPagesArgs a) {
-  extern __shared__ float xs[];  // [32][D + 1], then codes
+template <typename In, typename Win>
+__global__ void __launch_bounds__(256) append_pages_kernel(const AppendPagesArgs a) {
+  extern __shared__ __align__(16) uint8_t rec[];
   wait_prior_grid();
   allow_next_grid();
-  const int D = a.d.D, ld = D + 1, T = a.d.tiles, nb = D / 32;
-  uint8_t *codes = reinterpret_cast<uint8_t *>(xs + 32 * ld);  // [32][D]
+  const int T = a.d.tiles, half = blockDim.x / 2;
   int n = 0;
   if (in_bounds(a.ctl, a.counts, 16)) n = min(a.counts[1], a.cap_work);
   for (int it = blockIdx.x; it < n * a.d.Hkv; it += gridDim.x) {
@@ -108,72 +347,35 @@ __global__ void __launch_bounds__(kApThreads) append_pages_kernel(const AppendPa
     if (w.g >= w.c1) {
       // the old group in this tile, if it moves into the pages, has its CTA write here
       const int o = ob - 1 - (((ob - 1 - w.g) % T) + T) % T;
-      if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile(a, w, w.g);
+      if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile<In, Win>(a, w, w.g);
       continue;
     }
     const int32_t *pe = a.d.table + static_cast<size_t>(w.s) * a.d.max_pages +
                         (w.g >> a.d.gpp_log2());
     const int page = in_bounds(a.ctl, pe, 4) ? *pe : -1;
-    uint8_t *rec = nullptr;
-    if (page >= 0 && page < a.d.n_pages)
-      rec = a.d.record_at(page, w.g & ((1 << a.d.gpp_log2()) - 1), w.h);
-    else if (threadIdx.x == 0)
-      flag_error(a.ctl, KVQ_DEV_INDEX);
-    if (rec && !in_bounds(a.ctl, rec, a.d.record())) rec = nullptr;
-    __syncthreads();  // (the staged values of the item before are read)
-    for (int i = threadIdx.x; i < 32 * D; i += kApThreads)
-      xs[i / D * ld + i % D] = source<false>(a, w, 32 * w.g + i / D, i % D);
+    if (static_cast<int>(threadIdx.x) < half)
+      pack_k<In, Win>(a, w, rec, threadIdx.x);
+    else
+      pack_v<In, Win>(a, w, rec, threadIdx.x - half);
     __syncthreads();
-    if (rec) {
-      for (int c = threadIdx.x; c < D; c += kApThreads) {
-        float m = 0.0f;
-        for (int t = 0; t < 32; ++t) m = fmaxf(m, fabsf(xs[t * ld + c]));
-        const float sc = int4_scale(m);
-        reinterpret_cast<float *>(rec + rec_kscale(D))[kscale_at(c, D)] = sc;
-        for (int t = 0; t < 32; ++t)
-          codes[t * D + c] = static_cast<uint8_t>(int4_code(xs[t * ld + c], sc) + 8);
-      }
+    if (threadIdx.x == 0) {
+      uint8_t *dst = page >= 0 && page < a.d.n_pages
+                         ? a.d.record_at(page, w.g & ((1 << a.d.gpp_log2()) - 1), w.h)
+                         : nullptr;
+      if (!dst)
+        flag_error(a.ctl, KVQ_DEV_INDEX);
+      else if (in_bounds(a.ctl, dst, a.d.record()))
+        bulk_s2g(dst, smem_u32(rec), a.d.record());
     }
-    __syncthreads();
-    if (rec)
-      for (int i = threadIdx.x; i < 16 * D; i += kApThreads)
-        rec[i] = codes[2 * i] | codes[2 * i + 1] << 4;
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * D; i += kApThreads)
-      xs[i / D * ld + i % D] = source<true>(a, w, 32 * w.g + i / D, i % D);
-    __syncthreads();
-    if (rec) {
-      for (int i = threadIdx.x; i < 32 * nb; i += kApThreads) {
-        const int t = i / nb, b = i % nb;
-        float m = 0.0f;
-        for (int k = 0; k < 32; ++k) m = fmaxf(m, fabsf(xs[t * ld + 32 * b + k]));
-        const float sc = int4_scale(m);
-        reinterpret_cast<float *>(rec + rec_vscale(D))[vscale_at(t, b, D)] = sc;
-        for (int k = 0; k < 32; ++k)
-          codes[t * D + 32 * b + k] =
-              static_cast<uint8_t>(int4_code(xs[t * ld + 32 * b + k], sc) + 8);
-      }
-    }
-    __syncthreads();
-    if (rec) {
-      for (int i = threadIdx.x; i < 4 * D; i += kApThreads) {
-        const int f = i % (D / 16), t = i / (D / 16) % 4, g = i / (D / 4) % 8, m = i / (2 * D);
-        uint32_t x = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          x |= static_cast<uint32_t>(
-                   codes[(16 * m + 2 * t + (k >> 2) + 8 * (k & 1)) * D + 16 * f + 8 * (k >> 1 & 1) + g])
-               << (4 * k);
-        reinterpret_cast<uint32_t *>(rec + rec_vcode(D))[vword_at(m, g, t, f, D)] = x;
-      }
-    }
-    // the window group that takes over this group's tile
+    // the window group that takes over this group's tile, whose values have all been read
     if (32 * w.g < w.before) {
       const int g = w.w0 + (((w.g - w.w0) % T) + T) % T;
-      __syncthreads();  // every value of the tile has been read
-      if (g < w.w1) write_tile(a, w, g);
+      if (g < w.w1) write_tile<In, Win>(a, w, g);
     }
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncthreads();  // the record is free again
   }
+  if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 struct PageValuesArgs {
@@ -184,72 +386,138 @@ struct PageValuesArgs {
   KernelCtl ctl;
 };
 
-// A thread per (row, head, eight features) of K and V.
+constexpr int kVlRows = 8;  // list rows of one warp
+
+template <typename Out>
+__device__ __forceinline__ void store8(const KernelCtl &ctl, Out *o, const float (&y)[8]) {
+  if (!in_bounds(ctl, o, 8 * sizeof(Out))) return;
+  if constexpr (sizeof(Out) == 4) {
+    reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    *reinterpret_cast<uint4 *>(o) = make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]),
+                                               pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
+  }
+}
+
+// A warp per eight list rows of one head. Lane i < 8 finds row i's record or tile (or
+// that it has none); then the lanes take pieces of eight features of K and of V, their
+// loads ahead of the stores. kD: the head dim, or 0 for one of the others.
+template <typename Out, int kD>
 __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a) {
   wait_prior_grid();
   allow_next_grid();
-  const int D = a.d.D, pieces = a.d.Hkv * D / 8;
-  const long total = static_cast<long>(a.n) * pieces;
-  const long stride = static_cast<long>(gridDim.x) * blockDim.x;
-  for (long i = blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x; i < total; i += stride) {
-    const int row = static_cast<int>(i / pieces), x = static_cast<int>(i - static_cast<long>(row) * pieces);
-    const int h = x / (D / 8), p = x - h * (D / 8), d0 = 8 * p;
-    if (!in_bounds(a.ctl, a.slot + row, 4) || !in_bounds(a.ctl, a.pos + row, 4)) continue;
-    const int s = a.slot[row], pos = a.pos[row];
-    if (s == -1) continue;
-    int len = -1;
-    if (s >= 0 && s < a.d.slots && in_bounds(a.ctl, a.d.lengths + s, 4)) len = a.d.lengths[s];
-    if (!a.d.holds(len) || pos < 0 || pos >= len) {
-      if (x == 0) flag_error(a.ctl, KVQ_DEV_INDEX);
-      continue;
-    }
-    const int g = pos >> 5, r = pos & 31;
-    float k[8], v[8];
-    if (pos < paged_cut(len, a.d.window)) {
-      const int32_t *pe = a.d.table + static_cast<size_t>(s) * a.d.max_pages + (g >> a.d.gpp_log2());
-      const int page = in_bounds(a.ctl, pe, 4) ? *pe : -1;
-      const uint8_t *rec = a.d.record_at(page, g & ((1 << a.d.gpp_log2()) - 1), h);
-      if (page < 0 || page >= a.d.n_pages) {
-        if (x == 0) flag_error(a.ctl, KVQ_DEV_INDEX);
-        continue;
-      }
-      if (!in_bounds(a.ctl, rec, a.d.record())) continue;
-      const uint32_t kw = *reinterpret_cast<const uint32_t *>(rec + r * (D / 2) + 4 * p);
-      const float *ks = reinterpret_cast<const float *>(rec + rec_kscale(D));
-      const uint32_t *vw = reinterpret_cast<const uint32_t *>(rec + rec_vcode(D));
-      const float vs = reinterpret_cast<const float *>(rec + rec_vscale(D))[vscale_at(r, d0 >> 5, D)];
-      // token r, features d0 + g: nibble 4 (r % 2) + 2 (d0 / 8 % 2) + (r / 8 % 2)
-      const int sh = 4 * (4 * (r & 1) + 2 * (p & 1) + (r >> 3 & 1));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        k[j] = (static_cast<int>(kw >> (4 * j) & 15) - 8) * ks[kscale_at(d0 + j, D)];
-        v[j] = (static_cast<int>(vw[vword_at(r >> 4, j, (r & 7) >> 1, d0 >> 4, D)] >> sh & 15) - 8) * vs;
-      }
-    } else {
-      const size_t tile = a.d.tile_at(s, h, g), b = el_bytes(a.d.win_dt);
-      if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.d.ring) + tile * b, 64 * D * b)) continue;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        k[j] = load_elem(a.d.ring, tile + ringk_at(r, d0 + j, D), a.d.win_dt);
-        v[j] = load_elem(a.d.ring, tile + 32 * D + ringv_at(r, d0 + j, D), a.d.win_dt);
-      }
-    }
-    const size_t o = (static_cast<size_t>(row) * a.d.Hkv + h) * D + d0, ob = el_bytes(a.out_dt);
-    for (int z = 0; z < 2; ++z) {
-      void *out = z ? a.v : a.k;
-      const float *y = z ? v : k;
-      if (!in_bounds(a.ctl, static_cast<const uint8_t *>(out) + o * ob, 8 * ob)) continue;
-      if (a.out_dt == KVQ_F32) {
-        float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
-        q[0] = make_float4(y[0], y[1], y[2], y[3]);
-        q[1] = make_float4(y[4], y[5], y[6], y[7]);
+  const int D = kD ? kD : a.d.D, pieces = D / 8, lane = threadIdx.x & 31;
+  const long unit = (blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x) >> 5;
+  const int h = static_cast<int>(unit % a.d.Hkv);
+  const long row0 = unit / a.d.Hkv * kVlRows;
+  if (row0 >= a.n) return;
+  // at: byte offset of the record, or (kind 2) element offset of the tile; kind 0: none
+  size_t at = 0;
+  int kind = 0, r = 0;
+  if (lane < kVlRows && row0 + lane < a.n) {
+    const int32_t *ps = a.slot + row0 + lane, *pp = a.pos + row0 + lane;
+    if (in_bounds(a.ctl, ps, 4) && in_bounds(a.ctl, pp, 4)) {
+      const int s = *ps, pos = *pp;
+      int len = -1;
+      if (s >= 0 && s < a.d.slots && in_bounds(a.ctl, a.d.lengths + s, 4)) len = a.d.lengths[s];
+      const int g = pos >> 5;
+      r = pos & 31;
+      if (s == -1) {
+        kind = 0;
+      } else if (!a.d.holds(len) || pos < 0 || pos >= len) {
+        flag_error(a.ctl, KVQ_DEV_INDEX);
+      } else if (pos < paged_cut(len, a.d.window)) {
+        const int32_t *pe = a.d.table + static_cast<size_t>(s) * a.d.max_pages +
+                            (g >> a.d.gpp_log2());
+        const int page = in_bounds(a.ctl, pe, 4) ? *pe : -1;
+        if (page < 0 || page >= a.d.n_pages) {
+          flag_error(a.ctl, KVQ_DEV_INDEX);
+        } else {
+          const uint8_t *rec = a.d.record_at(page, g & ((1 << a.d.gpp_log2()) - 1), h);
+          at = rec - a.d.pool;
+          kind = in_bounds(a.ctl, rec, 40 * D);
+        }
       } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) =
-            make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]),
-                       pack_bf2(y[6], y[7]));
+        at = a.d.tile_at(s, h, g);
+        const size_t b = el_bytes(a.d.win_dt);
+        kind = in_bounds(a.ctl, static_cast<const uint8_t *>(a.d.ring) + at * b, 64 * D * b) ? 2 : 0;
       }
     }
   }
+  const int passes = kVlRows * pieces / 32;  // D / 32
+#pragma unroll 4
+  for (int ps = 0; ps < passes; ++ps) {
+    const int task = 32 * ps + lane, i = task / pieces, p = task - i * pieces, d0 = 8 * p;
+    const int kd = __shfl_sync(~0u, kind, i), rr = __shfl_sync(~0u, r, i);
+    const size_t off = __shfl_sync(~0u, static_cast<unsigned long long>(at), i);
+    if (kd == 0) continue;
+    float k[8], v[8];
+    if (kd == 1) {
+      const uint8_t *rec = a.d.pool + off;
+      const uint32_t kw = *reinterpret_cast<const uint32_t *>(rec + rr * (D / 2) + 4 * p);
+      // the scales of a piece: channels 0 4 1 5, and 64 bytes on 2 6 3 7
+      const float *ks = reinterpret_cast<const float *>(rec + rec_kscale(D)) + kscale_at(d0, D);
+      const float4 s0 = *reinterpret_cast<const float4 *>(ks);
+      const float4 s1 = *reinterpret_cast<const float4 *>(ks + 16);
+      const float sc[8] = {s0.x, s0.z, s1.x, s1.z, s0.y, s0.w, s1.y, s1.w};
+      const uint32_t *vw = reinterpret_cast<const uint32_t *>(rec + rec_vcode(D)) +
+                           vword_at(rr >> 4, 0, (rr & 7) >> 1, p >> 1, D);
+      const int step = D % 64 == 0 ? 16 : 8;  // words from feature to feature
+      const float vs = reinterpret_cast<const float *>(rec + rec_vscale(D))[vscale_at(rr, d0 >> 5, D)];
+      const int sh = 4 * (4 * (rr & 1) + 2 * (p & 1) + (rr >> 3 & 1));
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = vw[j * step];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        k[j] = (static_cast<int>(kw >> (4 * j) & 15) - 8) * sc[j];
+        v[j] = (static_cast<int>(w[j] >> sh & 15) - 8) * vs;
+      }
+    } else {
+      const size_t ek = off + ringk_at(rr, d0, D), ev = off + 32 * D + ringv_at(rr, d0, D);
+      if (a.d.win_dt == KVQ_F32) {
+        const float *x = static_cast<const float *>(a.d.ring);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          k[j] = x[ek + 2 * (j & 3) + (j >> 2)];
+          v[j] = x[ev + 32 * j];
+        }
+      } else {
+        const uint16_t *x = static_cast<const uint16_t *>(a.d.ring);
+        const uint4 y = *reinterpret_cast<const uint4 *>(x + ek);
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          k[j] = j < 4 ? bf_lo(w[j & 3]) : bf_hi(w[j & 3]);
+          v[j] = bf16_to_f32(x[ev + 32 * j]);
+        }
+      }
+    }
+    const size_t o = (static_cast<size_t>(row0 + i) * a.d.Hkv + h) * D + d0;
+    store8(a.ctl, static_cast<Out *>(a.k) + o, k);
+    store8(a.ctl, static_cast<Out *>(a.v) + o, v);
+  }
+}
+
+template <typename Out>
+void launch_values(const PageValuesArgs &a, cudaStream_t s) {
+  const long units = static_cast<long>((a.n + kVlRows - 1) / kVlRows) * a.d.Hkv;
+  const dim3 grid(static_cast<unsigned>((units + 7) / 8));
+  if (a.d.D == 128)
+    launch_dependent(page_values_kernel<Out, 128>, grid, dim3(256), 0, s, a);
+  else if (a.d.D == 64)
+    launch_dependent(page_values_kernel<Out, 64>, grid, dim3(256), 0, s, a);
+  else
+    launch_dependent(page_values_kernel<Out, 0>, grid, dim3(256), 0, s, a);
+}
+
+template <typename In, typename Win>
+void launch_append_typed(const AppendPagesArgs &a, int num_sms, cudaStream_t s) {
+  const int half = (a.d.D / 2 + 31) / 32 * 32;
+  const long items = static_cast<long>(a.cap_work) * a.d.Hkv;
+  const int grid = static_cast<int>(std::min<long>(items, 8L * num_sms));
+  launch_dependent(append_pages_kernel<In, Win>, dim3(grid), dim3(2 * half), a.d.record(), s, a);
 }
 
 }  // namespace
@@ -264,18 +532,24 @@ int launch_append_pages(const PagedDims &d, const kvq_page_plan &p, const PageRo
   a.after = p.after;
   a.work = p.work;
   a.counts = p.counts;
-  a.cap_work = p.cap_work;
+  // (the entries a step of these rows can fill)
+  a.cap_work = page_work_bound(d.window, d.slots, p.rows);
   a.ctl = ctl;
-  const size_t smem = 32 * (4 * (static_cast<size_t>(d.D) + 1) + d.D);
-  const long items = static_cast<long>(p.cap_work) * d.Hkv;
-  const int grid = static_cast<int>(std::min<long>(items, 6L * num_sms));
-  launch_dependent(append_pages_kernel, dim3(grid), dim3(kApThreads), smem, s, a);
+  if (r.dtype == KVQ_F32) {
+    if (d.win_dt == KVQ_F32)
+      launch_append_typed<float, float>(a, num_sms, s);
+    else
+      launch_append_typed<float, __nv_bfloat16>(a, num_sms, s);
+  } else if (d.win_dt == KVQ_F32) {
+    launch_append_typed<__nv_bfloat16, float>(a, num_sms, s);
+  } else {
+    launch_append_typed<__nv_bfloat16, __nv_bfloat16>(a, num_sms, s);
+  }
   return 1;
 }
 
 int launch_page_values(const PagedDims &d, const int32_t *slot, const int32_t *pos, int n,
-                       void *k, void *v, int out_dt, const KernelCtl &ctl, int num_sms,
-                       cudaStream_t s) {
+                       void *k, void *v, int out_dt, const KernelCtl &ctl, cudaStream_t s) {
   PageValuesArgs a;
   a.d = d;
   a.slot = slot;
@@ -285,9 +559,10 @@ int launch_page_values(const PagedDims &d, const int32_t *slot, const int32_t *p
   a.n = n;
   a.out_dt = out_dt;
   a.ctl = ctl;
-  const long total = static_cast<long>(n) * d.Hkv * d.D / 8;
-  const int grid = static_cast<int>(std::min<long>((total + 255) / 256, 8L * num_sms));
-  launch_dependent(page_values_kernel, dim3(grid), dim3(256), 0, s, a);
+  if (out_dt == KVQ_F32)
+    launch_values<float>(a, s);
+  else
+    launch_values<__nv_bfloat16>(a, s);
   return 1;
 }
 

@@ -3,6 +3,8 @@
 // records and of a window's tiles lie (include/kvq.h, kvq_paged_cache).
 #pragma once
 
+#include <type_traits>
+
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -56,6 +58,15 @@ inline PagedDims paged_dims(const kvq_paged_cache &c) {
   return d;
 }
 
+// Entries of the work list of a step: a request with n new tokens writes at most n / 32
+// groups and its window's tiles and a part of a group at either end, and no more than two
+// groups for each token.
+inline int page_work_bound(int window, int slots, int rows) {
+  const int64_t requests = slots < rows ? slots : rows;
+  const int64_t most = rows / 32 + (paged_tiles(window) + 3) * requests;
+  return static_cast<int>(most < 2 * static_cast<int64_t>(rows) ? most : 2 * static_cast<int64_t>(rows));
+}
+
 // ---- a group's record: byte offsets of its four parts
 __host__ __device__ __forceinline__ int rec_kscale(int D) { return 16 * D; }
 __host__ __device__ __forceinline__ int rec_vcode(int D) { return 20 * D; }
@@ -98,8 +109,7 @@ int launch_page_tables(const kvq_page_state &st, const int32_t *n_new, const kvq
 int launch_append_pages(const PagedDims &d, const kvq_page_plan &p, const PageRows &r,
                         const KernelCtl &ctl, int num_sms, cudaStream_t s);
 int launch_page_values(const PagedDims &d, const int32_t *slot, const int32_t *pos, int n,
-                       void *k, void *v, int out_dt, const KernelCtl &ctl, int num_sms,
-                       cudaStream_t s);
+                       void *k, void *v, int out_dt, const KernelCtl &ctl, cudaStream_t s);
 bool attend_pages_supported(const PagedDims &d, int Hq, int rows);
 size_t attend_pages_workspace(const PagedDims &d, int Hq, int rows, int num_sms);
 int launch_attend_pages(const PagedDims &d, const void *q, int q_dt, int Hq, int rows,
