@@ -663,8 +663,10 @@ KVQ_API kvq_status kvq_paged_sizes(const kvq_paged_cache *cache, size_t sizes[6]
  *   before    [slots], after [slots]: the requests' lengths
  *   row_slot  [rows]: the request of each row, -1 for a row of none
  *   positions [rows]: its token's position (0 for a row of none); what kv_rope takes
- *   work      [cap_work][2]: (slot, group) of every 32-token group the step writes, in
- *             the pages or in the windows; cap_work >= kvq_page_work(state, rows)
+ *   work      [cap_work][8]: of every 32-token group the step writes, in the pages or in
+ *             the windows: slot, group, the page it goes to (-1: the window), its
+ *             request's before, after and first row, and two unused;
+ *             cap_work >= kvq_page_work(state, rows)
  *   counts    [4]: pages free after the step, groups in work, and scratch that has to
  *             be zero before the first call (it is left zero)
  */

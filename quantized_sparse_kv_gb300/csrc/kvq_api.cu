@@ -227,7 +227,7 @@ void ctl_add_plan(kvq::KernelCtl &c, const kvq_page_state &s, const kvq_page_pla
   ctl_add(c, p.offsets, 4 * (static_cast<size_t>(s.slots) + 1));
   ctl_add(c, p.before, 4 * static_cast<size_t>(s.slots));
   ctl_add(c, p.after, 4 * static_cast<size_t>(s.slots));
-  ctl_add(c, p.work, 8 * static_cast<size_t>(p.cap_work));
+  ctl_add(c, p.work, 32 * static_cast<size_t>(p.cap_work));
   ctl_add(c, p.counts, 16);
 }
 

@@ -27,7 +27,7 @@ namespace {
 struct AppendPagesArgs {
   PagedDims d;
   PageRows r;
-  const int32_t *offsets, *before, *after, *work, *counts;
+  const int32_t *work, *counts;
   int cap_work;
   KernelCtl ctl;
 };
@@ -71,9 +71,8 @@ struct Types {
   static constexpr bool kBf16 = sizeof(Win) == 2;  // the values are bf16
   using Pair = typename std::conditional<kBf16, PairB, PairF>::type;
 
-  // elements e and e + 1 of a row of the step
-  static __device__ __forceinline__ Pair row2(const AppendPagesArgs &a, const void *rows, size_t e) {
-    const In *p = static_cast<const In *>(rows) + e;
+  // two elements of a row of the step
+  static __device__ __forceinline__ Pair row2(const AppendPagesArgs &a, const In *p) {
     Pair x;
     x.set(0.0f, 0.0f);
     if (!in_bounds(a.ctl, p, 2 * sizeof(In))) return x;
@@ -89,13 +88,12 @@ struct Types {
     }
     return x;
   }
-  // elements at e0 and e1 of the windows
-  static __device__ __forceinline__ Pair win2(const AppendPagesArgs &a, size_t e0, size_t e1) {
-    const Win *p = static_cast<const Win *>(a.d.ring);
+  // two elements of the windows
+  static __device__ __forceinline__ Pair win2(const AppendPagesArgs &a, const Win *p, const Win *q) {
     Pair x;
     x.set(0.0f, 0.0f);
-    if (in_bounds(a.ctl, p + e0, sizeof(Win)) && in_bounds(a.ctl, p + e1, sizeof(Win)))
-      x.set(load_f32(p + e0), load_f32(p + e1));
+    if (in_bounds(a.ctl, p, sizeof(Win)) && in_bounds(a.ctl, q, sizeof(Win)))
+      x.set(load_f32(p), load_f32(q));
     return x;
   }
 };
@@ -122,10 +120,10 @@ __device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const Group
   for (int i = threadIdx.x; i < 2 * (p1 - p0) * pieces; i += blockDim.x) {
     const int pos = p0 + i / (2 * pieces), x = i % (2 * pieces), d = 8 * (x % pieces), r = pos & 31;
     const bool v = x >= pieces;
-    const size_t e = row_elem(a, w, pos, v) + d;
+    const In *row = static_cast<const In *>(v ? a.r.v : a.r.k) + row_elem(a, w, pos, v) + d;
     typename T::Pair y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = T::row2(a, v ? a.r.v : a.r.k, e + 2 * k);
+    for (int k = 0; k < 4; ++k) y[k] = T::row2(a, row + 2 * k);
     if (v) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -155,14 +153,17 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
   const int D = a.d.D, t0 = 32 * w.g;
   if (2 * p >= D) return;
   typename T::Pair x[32];
-  const size_t tile = a.d.tile_at(w.s, w.h, w.g);
-  const size_t e0 = row_elem(a, w, t0, false) + 2 * p;
+  if (t0 >= w.before) {  // (the usual group of a prompt)
+    const In *row = static_cast<const In *>(a.r.k) + row_elem(a, w, t0, false) + 2 * p;
 #pragma unroll
-  for (int t = 0; t < 32; ++t) {
-    if (t0 + t < w.before)
-      x[t] = T::win2(a, tile + ringk_at(t, 2 * p, D), tile + ringk_at(t, 2 * p + 1, D));
-    else
-      x[t] = T::row2(a, a.r.k, e0 + static_cast<size_t>(t * a.r.ksr));
+    for (int t = 0; t < 32; ++t, row += a.r.ksr) x[t] = T::row2(a, row);
+  } else {
+    const In *row = static_cast<const In *>(a.r.k) + row_elem(a, w, t0, false) + 2 * p;
+    const Win *tile = static_cast<const Win *>(a.d.ring) + a.d.tile_at(w.s, w.h, w.g);
+#pragma unroll
+    for (int t = 0; t < 32; ++t, row += a.r.ksr)
+      x[t] = t0 + t < w.before ? T::win2(a, tile + ringk_at(t, 2 * p, D), tile + ringk_at(t, 2 * p + 1, D))
+                               : T::row2(a, row);
   }
   float a0, a1;
   if constexpr (T::kBf16) {
@@ -209,20 +210,29 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
   const bool live = m < 2;
   const int t0 = 32 * w.g + 16 * m;
   typename T::Pair x[16][2];
-  const size_t tile = a.d.tile_at(w.s, w.h, w.g) + 32 * D;
-  const size_t e0 = row_elem(a, w, t0, true) + d0;
+  const In *row = static_cast<const In *>(a.r.v) + row_elem(a, w, t0, true) + d0;
+  if (!live) {
 #pragma unroll
-  for (int t = 0; t < 16; ++t)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!live)
-        x[t][k].set(0.0f, 0.0f);
-      else if (t0 + t < w.before)
-        x[t][k] = T::win2(a, tile + ringv_at(16 * m + t, d0 + 2 * k, D),
-                          tile + ringv_at(16 * m + t, d0 + 2 * k + 1, D));
-      else
-        x[t][k] = T::row2(a, a.r.v, e0 + static_cast<size_t>(t * a.r.vsr) + 2 * k);
+    for (int t = 0; t < 16; ++t) {
+      x[t][0].set(0.0f, 0.0f);
+      x[t][1].set(0.0f, 0.0f);
     }
+  } else if (t0 >= w.before) {
+#pragma unroll
+    for (int t = 0; t < 16; ++t, row += a.r.vsr) {
+      x[t][0] = T::row2(a, row);
+      x[t][1] = T::row2(a, row + 2);
+    }
+  } else {
+    const Win *tile = static_cast<const Win *>(a.d.ring) + a.d.tile_at(w.s, w.h, w.g) + 32 * D;
+#pragma unroll
+    for (int t = 0; t < 16; ++t, row += a.r.vsr)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        x[t][k] = t0 + t < w.before ? T::win2(a, tile + ringv_at(16 * m + t, d0 + 2 * k, D),
+                                              tile + ringv_at(16 * m + t, d0 + 2 * k + 1, D))
+                                    : T::row2(a, row + 2 * k);
+  }
   // maxima of tokens 2n and 2n + 1; lane e keeps those of its own two
   float m0 = 0.0f, m1 = 0.0f;
   bool fast = T::kBf16;
@@ -322,7 +332,7 @@ __device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes
 // them too, behind its own reads, and the tile's own entry leaves them to it, so no
 // order between CTAs is needed.
 template <typename In, typename Win>
-__global__ void __launch_bounds__(256) append_pages_kernel(const AppendPagesArgs a) {
+__global__ void __launch_bounds__(256, sizeof(Win) == 2 ? 4 : 2) append_pages_kernel(const AppendPagesArgs a) {
   extern __shared__ __align__(16) uint8_t rec[];
   wait_prior_grid();
   allow_next_grid();
@@ -332,14 +342,15 @@ __global__ void __launch_bounds__(256) append_pages_kernel(const AppendPagesArgs
   for (int it = blockIdx.x; it < n * a.d.Hkv; it += gridDim.x) {
     GroupWork w;
     w.h = it % a.d.Hkv;
-    const int32_t *e = a.work + 2 * (it / a.d.Hkv);
-    if (!in_bounds(a.ctl, e, 8)) continue;
-    w.s = e[0];
-    w.g = e[1];
-    if (w.s < 0 || w.s >= a.d.slots) continue;
-    w.before = a.before[w.s];
-    w.after = a.after[w.s];
-    w.row0 = a.offsets[w.s];
+    const int4 *e = reinterpret_cast<const int4 *>(a.work) + 2 * (it / a.d.Hkv);
+    if (!in_bounds(a.ctl, e, 32)) continue;
+    const int4 e0 = e[0], e1 = e[1];
+    w.s = e0.x;
+    w.g = e0.y;
+    const int page = e0.z;
+    w.before = e0.w;
+    w.after = e1.x;
+    w.row0 = e1.y;
     w.c1 = paged_cut(w.after, a.d.window) >> 5;
     w.w0 = max(w.before >> 5, w.c1);
     w.w1 = (w.after + 31) >> 5;
@@ -350,9 +361,6 @@ __global__ void __launch_bounds__(256) append_pages_kernel(const AppendPagesArgs
       if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile<In, Win>(a, w, w.g);
       continue;
     }
-    const int32_t *pe = a.d.table + static_cast<size_t>(w.s) * a.d.max_pages +
-                        (w.g >> a.d.gpp_log2());
-    const int page = in_bounds(a.ctl, pe, 4) ? *pe : -1;
     if (static_cast<int>(threadIdx.x) < half)
       pack_k<In, Win>(a, w, rec, threadIdx.x);
     else
@@ -527,9 +535,6 @@ int launch_append_pages(const PagedDims &d, const kvq_page_plan &p, const PageRo
   AppendPagesArgs a;
   a.d = d;
   a.r = r;
-  a.offsets = p.offsets;
-  a.before = p.before;
-  a.after = p.after;
   a.work = p.work;
   a.counts = p.counts;
   // (the entries a step of these rows can fill)

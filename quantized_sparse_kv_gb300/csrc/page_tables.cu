@@ -74,6 +74,20 @@ __device__ __forceinline__ int clamp_int(long long x) {
   return static_cast<int>(x < 0x7fffffffLL ? x : 0x7fffffffLL);
 }
 
+__device__ __forceinline__ int load_entry(const TablesArgs &a, const int32_t *e) {
+  return in_bounds(a.ctl, e, 4) ? *e : -1;
+}
+
+// The k-th page that the step takes: from the top of the free ones, on which the pages of
+// ended requests (their sums in backp) are put first.
+__device__ __forceinline__ int taken_page(const TablesArgs &a, const int *backp, int k, int n_free,
+                                          long long have) {
+  const long long at = have - 1 - k;
+  if (at < n_free) return load_entry(a, a.free_pages + at);
+  const int j = static_cast<int>(at - n_free), b = find_run(backp, a.S, j);
+  return load_entry(a, a.table + static_cast<size_t>(b) * a.max_pages + (j - backp[b]));
+}
+
 __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
   extern __shared__ int sm[];
   __shared__ long long buf[32];
@@ -219,8 +233,17 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
     const int s = find_run(workp, S, k), e = k - workp[s];
     const int c0 = paged_cut(bef[s], a.window) >> 5, c1 = paged_cut(aft[s], a.window) >> 5;
     const int g = e < c1 - c0 ? c0 + e : max(bef[s] >> 5, c1) + e - (c1 - c0);
-    if (in_bounds(a.ctl, a.work + 2 * k, 8))
-      *reinterpret_cast<int2 *>(a.work + 2 * k) = make_int2(s, g);
+    int page = -1;
+    if (g < c1) {
+      const int j = g >> (a.page_log2 - 5), held = pages_of(a, bef[s]);
+      page = j < held ? load_entry(a, a.table + static_cast<size_t>(s) * a.max_pages + j)
+                      : taken_page(a, backp, takep[s] + j - held, n_free, have);
+    }
+    int4 *o = reinterpret_cast<int4 *>(a.work + 8 * static_cast<size_t>(k));
+    if (in_bounds(a.ctl, o, 32)) {
+      o[0] = make_int4(s, g, page, bef[s]);
+      o[1] = make_int4(aft[s], rowp[s], 0, 0);
+    }
   }
   // pages of ended requests go on top of the free ones
   for (int k = t0; k < n_back; k += step) {
@@ -233,13 +256,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
   // and requests that grow take from the top
   for (int k = t0; k < n_take; k += step) {
     const int s = find_run(takep, S, k);
-    const long long at = have - 1 - k;
-    const int32_t *e = a.free_pages + at;
-    if (at >= n_free) {
-      const int j = static_cast<int>(at - n_free), b = find_run(backp, S, j);
-      e = a.table + static_cast<size_t>(b) * a.max_pages + (j - backp[b]);
-    }
-    const int page = in_bounds(a.ctl, e, 4) ? *e : -1;
+    const int page = taken_page(a, backp, k, n_free, have);
     int32_t *o = a.table + static_cast<size_t>(s) * a.max_pages + pages_of(a, bef[s]) +
                  (k - takep[s]);
     if (in_bounds(a.ctl, o, 4)) *o = page;

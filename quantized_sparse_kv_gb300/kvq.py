@@ -1103,7 +1103,7 @@ class PageTables(_Prepared):
         self.row_slot = torch.empty(self.rows, dtype=i32, device=dev)
         self.positions = torch.empty(self.rows, dtype=i32, device=dev)
         cap = int(self.lib.kvq_page_work(state.ref, self.rows))
-        self.work = torch.empty((cap, 2), dtype=i32, device=dev)
+        self.work = torch.empty((cap, 8), dtype=i32, device=dev)
         self.counts = torch.zeros(4, dtype=i32, device=dev)
         self.status = new_status(dev)
         self.struct = KvqPagePlan(self.rows, cap, *(

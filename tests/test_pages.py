@@ -95,7 +95,13 @@ def check_plan(kvq, state, model, plan, want):
     assert plan.before.tolist() == before and plan.after.tolist() == after
     assert plan.row_slot.tolist() == slot and plan.positions.tolist() == pos
     n = int(plan.counts[1])
-    assert [tuple(w) for w in plan.work[:n].tolist()] == work
+    got = plan.work[:n].tolist()
+    assert [(w[0], w[1]) for w in got] == work
+    table = state.table.tolist()
+    for s, g, page, b, e, row, _, _ in got:
+        assert (b, e, row) == (before[s], after[s], offsets[s])
+        packed = g < model.cut(e) // 32
+        assert page == (table[s][g * 32 // model.page] if packed else -1)
     assert int(plan.free_after) == len(model.free) and int(plan.counts[2]) == 0
 
 
@@ -463,10 +469,15 @@ def test_rows_and_pages_that_do_not_exist(kvq, d, wdt):
         keep = np.r_[0:32, 64:150]
         want = attention64(q[0].double().cpu().numpy(), kk[:, keep], vv[:, keep])
         assert O.rel_l2(got, want) <= TOL_TENSOR
-        again = kvq.AppendPages(cache, plan, k, v)
+    state.table[0, 1] = good
+    # pages outside the pool that a broken table or free list brings into a step
+    for bad in (-1, 20, 1 << 30):
+        state.free_pages.fill_(bad)
+        step = kvq.page_tables(state, torch.tensor([0, 0, 100], device="cuda"), 100)
+        again = kvq.AppendPages(cache, step, k[:100], v[:100])
         again.run()
         assert kvq.read_status(again.status) == kvq.DEV_INDEX
-    state.table[0, 1] = good
+        kvq.page_tables(state, torch.tensor([0, 0, -1], device="cuda"), 0)
 
 
 # ------------------------------------------------------------------ refusals (no GPU)
