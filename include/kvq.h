@@ -706,8 +706,8 @@ KVQ_API kvq_status kv_page_tables(const kvq_page_state *state, const int32_t *n_
  * kv_append_pages -- the new tokens' keys and values into one layer's pages and windows,
  * as the plan of kv_page_tables says; whole groups that leave the windows are quantized.
  * k_new, v_new: in_dtype (F32 or BF16), element (row, head, d) at [row * stride_row +
- * head * stride_head + d] (strides in elements, multiples of 16 bytes, >= 0: rows of a
- * projection are read in place). Rows of none are not read. May be called again with the
+ * head * stride_head + d] (strides in elements, multiples of 16 bytes, 0 .. 2^31 - 1: rows of
+ * a projection are read in place). Rows of none are not read. May be called again with the
  * same plan, for other layers or, while no token of the step took the window row of
  * an older one that moved (steps of one token never do), for the same layer.
  * A page outside the pool is flagged KVQ_DEV_INDEX and not written.

@@ -1013,7 +1013,9 @@ kvq_status kv_append_pages(const kvq_paged_cache *cache, const kvq_page_plan *pl
       rows->k_stride_head % unit || rows->v_stride_row % unit || rows->v_stride_head % unit ||
       (dev_status && !aligned16(dev_status)))
     return KVQ_ERR_ALIGN;
-  if (static_cast<int64_t>(plan->cap_work) * cache->kv_heads > 0x7fffffffL)
+  const int64_t most = 0x7fffffffL;
+  if (static_cast<int64_t>(plan->cap_work) * cache->kv_heads > most || rows->k_stride_row > most ||
+      rows->k_stride_head > most || rows->v_stride_row > most || rows->v_stride_head > most)
     return KVQ_ERR_UNSUPPORTED;
   kvq::KernelCtl ctl = make_ctl(dev_status);
   ctl_add_pages(ctl, *cache);
@@ -1025,8 +1027,12 @@ kvq_status kv_append_pages(const kvq_paged_cache *cache, const kvq_page_plan *pl
   ctl_add(ctl, rows->v_new,
           rows_bytes(n1 * rows->v_stride_row + h1 * rows->v_stride_head + cache->head_dim, 1,
                      in_dtype));
-  const kvq::PageRows r = {rows->k_new,         rows->v_new,         rows->k_stride_row,
-                           rows->k_stride_head, rows->v_stride_row, rows->v_stride_head,
+  const kvq::PageRows r = {rows->k_new,
+                           rows->v_new,
+                           static_cast<int>(rows->k_stride_row),
+                           static_cast<int>(rows->k_stride_head),
+                           static_cast<int>(rows->v_stride_row),
+                           static_cast<int>(rows->v_stride_head),
                            in_dtype};
   const int n = kvq::launch_append_pages(kvq::paged_dims(*cache), *plan, r, ctl, sm_count(),
                                          reinterpret_cast<cudaStream_t>(stream));

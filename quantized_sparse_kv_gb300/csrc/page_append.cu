@@ -10,7 +10,8 @@
 // threads take K: a thread has a pair of channels of all 32 tokens in registers, so the
 // maxima need no exchange and a warp reads whole rows. The others take V: a thread has four
 // features of 16 tokens; eight lanes share a token's 32 features, their maxima meet in
-// three lane exchanges for two tokens at a time. V codes are made from (token, token + 8)
+// three lane exchanges for two tokens at a time and their scales come back through shared
+// memory. V codes are made from (token, token + 8)
 // pairs of one feature, which is the byte a record's words hold; lanes of features y and
 // y + 8 exchange half of their bytes and each keeps half of the words. The record (40 D
 // bytes) is put together in shared memory and leaves as one bulk copy. All of a thread's
@@ -45,10 +46,27 @@ __device__ __noinline__ uint32_t code_byte_div(float lo, float hi, float s_lo, f
 __device__ __forceinline__ size_t el_bytes(int dt) { return dt == KVQ_F32 ? 4 : 2; }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+// The larger magnitudes of two bf16 pairs (with signs that mean nothing).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+// code_byte_recip of two bf16 values given as floats' bits, scales as (negated, reciprocal).
+__device__ __forceinline__ uint32_t code_byte_of(uint32_t lo, uint32_t hi, uint64_t ns, uint64_t r) {
+  uint64_t x, q0, e, q, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo), "r"(hi));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(x), "l"(r));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q0), "l"(ns), "l"(x));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q0));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(q), "l"(0x4B4000084B400008ull));
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y));
+  return hi * 16u + lo;
+}
+__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
 }
 
 // A pair of values as the cache keeps them: bf16 pairs in one register.
@@ -88,6 +106,17 @@ struct Types {
     }
     return x;
   }
+  // four elements of a row
+  static __device__ __forceinline__ void row4(const AppendPagesArgs &a, const In *p, Pair (&x)[2]) {
+    if constexpr (sizeof(In) == 2 && kBf16) {
+      const uint2 w = in_bounds(a.ctl, p, 8) ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
+      x[0].w = w.x;
+      x[1].w = w.y;
+    } else {
+      x[0] = row2(a, p);
+      x[1] = row2(a, p + 2);
+    }
+  }
   // two elements of the windows
   static __device__ __forceinline__ Pair win2(const AppendPagesArgs &a, const Win *p, const Win *q) {
     Pair x;
@@ -106,7 +135,8 @@ struct GroupWork {
 __device__ __forceinline__ size_t row_elem(const AppendPagesArgs &a, const GroupWork &w, int pos,
                                            bool v) {
   const int64_t row = w.row0 + pos - w.before;
-  return static_cast<size_t>(v ? row * a.r.vsr + w.h * a.r.vsh : row * a.r.ksr + w.h * a.r.ksh);
+  return static_cast<size_t>(v ? row * a.r.vsr + static_cast<int64_t>(w.h) * a.r.vsh
+                               : row * a.r.ksr + static_cast<int64_t>(w.h) * a.r.ksh);
 }
 
 // The new tokens of window group g into its tile, eight elements of a row at a time (a
@@ -156,22 +186,22 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
   if (t0 >= w.before) {  // (the usual group of a prompt)
     const In *row = static_cast<const In *>(a.r.k) + row_elem(a, w, t0, false) + 2 * p;
 #pragma unroll
-    for (int t = 0; t < 32; ++t, row += a.r.ksr) x[t] = T::row2(a, row);
+    for (int t = 0; t < 32; ++t) x[t] = T::row2(a, row + static_cast<int64_t>(t) * a.r.ksr);
   } else {
     const In *row = static_cast<const In *>(a.r.k) + row_elem(a, w, t0, false) + 2 * p;
     const Win *tile = static_cast<const Win *>(a.d.ring) + a.d.tile_at(w.s, w.h, w.g);
 #pragma unroll
-    for (int t = 0; t < 32; ++t, row += a.r.ksr)
+    for (int t = 0; t < 32; ++t)
       x[t] = t0 + t < w.before ? T::win2(a, tile + ringk_at(t, 2 * p, D), tile + ringk_at(t, 2 * p + 1, D))
-                               : T::row2(a, row);
+                               : T::row2(a, row + static_cast<int64_t>(t) * a.r.ksr);
   }
   float a0, a1;
   if constexpr (T::kBf16) {
-    uint32_t m = 0u;
+    uint32_t m = x[0].w;
 #pragma unroll
-    for (int t = 0; t < 32; ++t) m = max_bf16x2(m, x[t].w & 0x7fff7fffu);
-    a0 = bf_lo(m);
-    a1 = bf_hi(m);
+    for (int t = 1; t < 32; ++t) m = max_abs2(m, x[t].w);
+    a0 = fabsf(bf_lo(m));
+    a1 = fabsf(bf_hi(m));
   } else {
     a0 = a1 = 0.0f;
 #pragma unroll
@@ -188,10 +218,11 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
   ks[kscale_at(2 * p + 1, D)] = s1;
   if (fast) {
     if constexpr (T::kBf16) {
-      const float r0 = recip_of(s0), r1 = recip_of(s1);
+      const uint64_t ns = pair64(-s0, -s1), r = pair64(recip_of(s0), recip_of(s1));
 #pragma unroll
       for (int t = 0; t < 32; ++t)
-        rec[t * (D / 2) + p] = static_cast<uint8_t>(code_byte_recip(x[t].w, -s0, -s1, r0, r1));
+        rec[t * (D / 2) + p] =
+            static_cast<uint8_t>(code_byte_of(x[t].w << 16, x[t].w & 0xffff0000u, ns, r));
     }
   } else {
 #pragma unroll
@@ -219,35 +250,31 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
     }
   } else if (t0 >= w.before) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t, row += a.r.vsr) {
-      x[t][0] = T::row2(a, row);
-      x[t][1] = T::row2(a, row + 2);
-    }
+    for (int t = 0; t < 16; ++t)
+      T::row4(a, row + static_cast<int64_t>(t) * a.r.vsr, x[t]);
   } else {
     const Win *tile = static_cast<const Win *>(a.d.ring) + a.d.tile_at(w.s, w.h, w.g) + 32 * D;
 #pragma unroll
-    for (int t = 0; t < 16; ++t, row += a.r.vsr)
+    for (int t = 0; t < 16; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         x[t][k] = t0 + t < w.before ? T::win2(a, tile + ringv_at(16 * m + t, d0 + 2 * k, D),
                                               tile + ringv_at(16 * m + t, d0 + 2 * k + 1, D))
-                                    : T::row2(a, row + 2 * k);
+                                    : T::row2(a, row + static_cast<int64_t>(t) * a.r.vsr + 2 * k);
   }
   // maxima of tokens 2n and 2n + 1; lane e keeps those of its own two
   float m0 = 0.0f, m1 = 0.0f;
-  bool fast = T::kBf16;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     float u, v;
     if constexpr (T::kBf16) {
-      const uint32_t p = max_bf16x2(x[2 * n][0].w & 0x7fff7fffu, x[2 * n][1].w & 0x7fff7fffu);
-      const uint32_t q = max_bf16x2(x[2 * n + 1][0].w & 0x7fff7fffu, x[2 * n + 1][1].w & 0x7fff7fffu);
-      uint32_t y = max_bf16x2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
+      const uint32_t p = max_abs2(x[2 * n][0].w, x[2 * n][1].w);
+      const uint32_t q = max_abs2(x[2 * n + 1][0].w, x[2 * n + 1][1].w);
+      uint32_t y = max_abs2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) y = max_bf16x2(y, __shfl_xor_sync(~0u, y, o));
+      for (int o = 1; o < 8; o <<= 1) y = max_abs2(y, __shfl_xor_sync(~0u, y, o));
       u = bf_lo(y);
       v = bf_hi(y);
-      fast = fast && recip_ok(u) && recip_ok(v);
     } else {
       u = fmaxf(fmaxf(fabsf(x[2 * n][0].lo()), fabsf(x[2 * n][0].hi())),
                 fmaxf(fabsf(x[2 * n][1].lo()), fabsf(x[2 * n][1].hi())));
@@ -260,14 +287,25 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
       }
     }
     if (n == e) {
-      m0 = u;
-      m1 = v;
+      m0 = fabsf(u);
+      m1 = fabsf(v);
     }
   }
-  fast = __all_sync(~0u, fast);
+  // (the eight lanes of a token have all of its tokens' maxima between them)
+  const bool fast = __all_sync(~0u, T::kBf16 && recip_ok(m0) && recip_ok(m1));
   const float s0 = fast ? scale_recip(m0) : int4_scale(m0);
   const float s1 = fast ? scale_recip(m1) : int4_scale(m1);
-  const float r0 = fast ? recip_of(s0) : 0.0f, r1 = fast ? recip_of(s1) : 0.0f;
+  // [half and block][t][token 2t or 2t + 1]: -scale of the token and of the one 8 behind it,
+  // then their reciprocals
+  float *aux = reinterpret_cast<float *>(rec + a.d.record()) + (i >> 3) * 32;
+  {
+    float *o = aux + (e & 3) * 8 + (e >> 2);
+    o[0] = -s0;
+    o[4] = -s1;
+    o[2] = fast ? recip_of(s0) : 0.0f;
+    o[6] = fast ? recip_of(s1) : 0.0f;
+  }
+  __syncwarp();
   if (live) {
     float *vs = reinterpret_cast<float *>(rec + rec_vscale(D));
     vs[vscale_at(16 * m + 2 * e, b, D)] = s0;
@@ -276,35 +314,25 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
   uint32_t *words = reinterpret_cast<uint32_t *>(rec + rec_vcode(D));
   const bool upper = e & 2;  // features y + 8
   const int f = 2 * b + (e >> 2), g0 = 4 * (e & 1) + (upper ? 2 : 0);
-  const int group = (threadIdx.x & 24);  // first of the eight lanes
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    // scales of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
-    float s[4], r[4];
-    s[0] = __shfl_sync(~0u, s0, group + t);
-    s[1] = __shfl_sync(~0u, s1, group + t);
-    s[2] = __shfl_sync(~0u, s0, group + t + 4);
-    s[3] = __shfl_sync(~0u, s1, group + t + 4);
-    if (T::kBf16) {
-      r[0] = __shfl_sync(~0u, r0, group + t);
-      r[1] = __shfl_sync(~0u, r1, group + t);
-      r[2] = __shfl_sync(~0u, r0, group + t + 4);
-      r[3] = __shfl_sync(~0u, r1, group + t + 4);
-    }
     uint32_t c[2][4];  // byte of feature j: tokens 2t + z and 2t + z + 8
 #pragma unroll
-    for (int z = 0; z < 2; ++z)
+    for (int z = 0; z < 2; ++z) {
+      const float4 sc = *reinterpret_cast<const float4 *>(aux + 8 * t + 4 * z);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const auto &p = x[2 * t + z][j >> 1], &q = x[2 * t + z + 8][j >> 1];
         if (T::kBf16 && fast) {
           if constexpr (T::kBf16)
-            c[z][j] = code_byte_recip(__byte_perm(p.w, q.w, j & 1 ? 0x7632 : 0x5410), -s[z],
-                                      -s[z + 2], r[z], r[z + 2]);
+            c[z][j] = code_byte_of(j & 1 ? p.w & 0xffff0000u : p.w << 16,
+                                   j & 1 ? q.w & 0xffff0000u : q.w << 16, pair64(sc.x, sc.y),
+                                   pair64(sc.z, sc.w));
         } else {
-          c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), s[z], s[z + 2]);
+          c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y);
         }
       }
+    }
     // bytes: features j, j + 1 of token 2t, then of 2t + 1
     const uint32_t c01 = __byte_perm(__byte_perm(c[0][0], c[0][1], 0x0040),
                                      __byte_perm(c[1][0], c[1][1], 0x0040), 0x5410);
@@ -525,7 +553,8 @@ void launch_append_typed(const AppendPagesArgs &a, int num_sms, cudaStream_t s) 
   const int half = (a.d.D / 2 + 31) / 32 * 32;
   const long items = static_cast<long>(a.cap_work) * a.d.Hkv;
   const int grid = static_cast<int>(std::min<long>(items, 8L * num_sms));
-  launch_dependent(append_pages_kernel<In, Win>, dim3(grid), dim3(2 * half), a.d.record(), s, a);
+  launch_dependent(append_pages_kernel<In, Win>, dim3(grid), dim3(2 * half),
+                   a.d.record() + half / 8 * 128, s, a);
 }
 
 }  // namespace

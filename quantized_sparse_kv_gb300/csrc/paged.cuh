@@ -101,7 +101,7 @@ __host__ __device__ __forceinline__ int ringv_at(int r, int d, int D) {
 // ---- launchers (arguments are already validated)
 struct PageRows {
   const void *k, *v;
-  int64_t ksr, ksh, vsr, vsh;
+  int ksr, ksh, vsr, vsh;  // strides in elements
   int dtype;
 };
 int launch_page_tables(const kvq_page_state &st, const int32_t *n_new, const kvq_page_plan &p,
