@@ -141,10 +141,10 @@ __device__ __forceinline__ size_t row_elem(const AppendPagesArgs &a, const Group
 
 // The new tokens of window group g into its tile, eight elements of a row at a time (a
 // tile's K keeps them together, its V has them apart), K and V in turn.
-template <typename In, typename Win>
+template <typename In, typename Win, int kD>
 __device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const GroupWork &w, int g) {
   using T = Types<In, Win>;
-  const int D = a.d.D, p0 = max(w.before, 32 * g), p1 = min(w.after, 32 * g + 32), pieces = D / 8;
+  const int D = kD ? kD : a.d.D, p0 = max(w.before, 32 * g), p1 = min(w.after, 32 * g + 32), pieces = D / 8;
   const size_t tile = a.d.tile_at(w.s, w.h, g);
   Win *ring = static_cast<Win *>(a.d.ring);
   for (int i = threadIdx.x; i < 2 * (p1 - p0) * pieces; i += blockDim.x) {
@@ -176,11 +176,11 @@ __device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const Group
 }
 
 // K of a group: thread p has channels 2p and 2p + 1.
-template <typename In, typename Win>
+template <typename In, typename Win, int kD>
 __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork &w, uint8_t *rec,
                                        int p) {
   using T = Types<In, Win>;
-  const int D = a.d.D, t0 = 32 * w.g;
+  const int D = kD ? kD : a.d.D, t0 = 32 * w.g;
   if (2 * p >= D) return;
   typename T::Pair x[32];
   if (t0 >= w.before) {  // (the usual group of a prompt)
@@ -233,11 +233,11 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
 
 // V of a group: thread i has features 32 b + 4 e .. + 3 of the 16 tokens of half m, i = (m,
 // b, e); every lane of a warp takes part in the exchanges.
-template <typename In, typename Win>
+template <typename In, typename Win, int kD>
 __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork &w, uint8_t *rec,
                                        int i) {
   using T = Types<In, Win>;
-  const int D = a.d.D, nb = D / 32, m = i / (8 * nb), b = i / 8 % nb, e = i & 7, d0 = 32 * b + 4 * e;
+  const int D = kD ? kD : a.d.D, nb = D / 32, m = i / (8 * nb), b = i / 8 % nb, e = i & 7, d0 = 32 * b + 4 * e;
   const bool live = m < 2;
   const int t0 = 32 * w.g + 16 * m;
   typename T::Pair x[16][2];
@@ -297,7 +297,7 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
   const float s1 = fast ? scale_recip(m1) : int4_scale(m1);
   // [half and block][t][token 2t or 2t + 1]: -scale of the token and of the one 8 behind it,
   // then their reciprocals
-  float *aux = reinterpret_cast<float *>(rec + a.d.record()) + (i >> 3) * 32;
+  float *aux = reinterpret_cast<float *>(rec + 40 * D) + (i >> 3) * 32;
   {
     float *o = aux + (e & 3) * 8 + (e >> 2);
     o[0] = -s0;
@@ -359,7 +359,7 @@ __device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes
 // tile of the window that the step's new tokens take over: the CTA that packs it writes
 // them too, behind its own reads, and the tile's own entry leaves them to it, so no
 // order between CTAs is needed.
-template <typename In, typename Win>
+template <typename In, typename Win, int kD>
 __global__ void __launch_bounds__(256, sizeof(Win) == 2 ? 4 : 2) append_pages_kernel(const AppendPagesArgs a) {
   extern __shared__ __align__(16) uint8_t rec[];
   wait_prior_grid();
@@ -386,13 +386,13 @@ __global__ void __launch_bounds__(256, sizeof(Win) == 2 ? 4 : 2) append_pages_ke
     if (w.g >= w.c1) {
       // the old group in this tile, if it moves into the pages, has its CTA write here
       const int o = ob - 1 - (((ob - 1 - w.g) % T) + T) % T;
-      if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile<In, Win>(a, w, w.g);
+      if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile<In, Win, kD>(a, w, w.g);
       continue;
     }
     if (static_cast<int>(threadIdx.x) < half)
-      pack_k<In, Win>(a, w, rec, threadIdx.x);
+      pack_k<In, Win, kD>(a, w, rec, threadIdx.x);
     else
-      pack_v<In, Win>(a, w, rec, threadIdx.x - half);
+      pack_v<In, Win, kD>(a, w, rec, threadIdx.x - half);
     __syncthreads();
     if (threadIdx.x == 0) {
       uint8_t *dst = page >= 0 && page < a.d.n_pages
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(256, sizeof(Win) == 2 ? 4 : 2) append_pages_ke
     // the window group that takes over this group's tile, whose values have all been read
     if (32 * w.g < w.before) {
       const int g = w.w0 + (((w.g - w.w0) % T) + T) % T;
-      if (g < w.w1) write_tile<In, Win>(a, w, g);
+      if (g < w.w1) write_tile<In, Win, kD>(a, w, g);
     }
     if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncthreads();  // the record is free again
@@ -422,8 +422,9 @@ struct PageValuesArgs {
   KernelCtl ctl;
 };
 
-constexpr int kVlRows = 8;  // list rows of one warp
+constexpr int kVlRows = 16;  // list rows of one warp
 
+// 8 or 16 consecutive values (wide: the address is a multiple of 32 bytes).
 template <typename Out>
 __device__ __forceinline__ void store8(const KernelCtl &ctl, Out *o, const float (&y)[8]) {
   if (!in_bounds(ctl, o, 8 * sizeof(Out))) return;
@@ -435,10 +436,95 @@ __device__ __forceinline__ void store8(const KernelCtl &ctl, Out *o, const float
                                                pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
   }
 }
+template <typename Out>
+__device__ __forceinline__ void store16(const KernelCtl &ctl, Out *o, const float (&lo)[8],
+                                        const float (&hi)[8], bool wide) {
+  if (sizeof(Out) == 4 || !wide) {
+    store8(ctl, o, lo);
+    store8(ctl, o + 8, hi);
+  } else if (in_bounds(ctl, o, 32)) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o),
+                 "r"(pack_bf2(lo[0], lo[1])), "r"(pack_bf2(lo[2], lo[3])),
+                 "r"(pack_bf2(lo[4], lo[5])), "r"(pack_bf2(lo[6], lo[7])),
+                 "r"(pack_bf2(hi[0], hi[1])), "r"(pack_bf2(hi[2], hi[3])),
+                 "r"(pack_bf2(hi[4], hi[5])), "r"(pack_bf2(hi[6], hi[7]))
+                 : "memory");
+  }
+}
 
-// A warp per eight list rows of one head. Lane i < 8 finds row i's record or tile (or
-// that it has none); then the lanes take pieces of eight features of K and of V, their
-// loads ahead of the stores. kD: the head dim, or 0 for one of the others.
+// The scales of eight channels from d0 on, as a record has them: channels 0 4 1 5, and 64
+// bytes on 2 6 3 7.
+__device__ __forceinline__ void load_kscales(const uint8_t *rec, int d0, int D, float (&sc)[8]) {
+  const float *ks = reinterpret_cast<const float *>(rec + rec_kscale(D)) + kscale_at(d0, D);
+  const float4 x = *reinterpret_cast<const float4 *>(ks), y = *reinterpret_cast<const float4 *>(ks + 16);
+  sc[0] = x.x;
+  sc[1] = x.z;
+  sc[2] = y.x;
+  sc[3] = y.z;
+  sc[4] = x.y;
+  sc[5] = x.w;
+  sc[6] = y.y;
+  sc[7] = y.w;
+}
+
+// Tokens [16 m, 16 m + 16) of a record, those with list index i0 + token in [0, 16), to
+// the list rows from row0 on. A lane takes 16 channels of K of every token in its turn
+// and, of V, the eight words of 16 features and four tokens: every byte is read once.
+template <typename Out, int D>
+__device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t *rec, int m, int i0,
+                                          long row0, int h, bool wide, int lane) {
+  constexpr int kChunks = D / 16, kRows = 32 / kChunks;
+  float lo[8], hi[8];
+  const size_t o0 = (static_cast<size_t>(row0) * a.d.Hkv + h) * D;
+  const size_t step = static_cast<size_t>(a.d.Hkv) * D;
+  {
+    const int c = lane & (kChunks - 1), r0 = lane / kChunks;
+    uint2 w[16 / kRows];
+#pragma unroll
+    for (int x = 0; x < 16 / kRows; ++x)
+      w[x] = *reinterpret_cast<const uint2 *>(rec + (16 * m + kRows * x + r0) * (D / 2) + 8 * c);
+    float s0[8], s1[8];
+    load_kscales(rec, 16 * c, D, s0);
+    load_kscales(rec, 16 * c + 8, D, s1);
+#pragma unroll
+    for (int x = 0; x < 16 / kRows; ++x) {
+      const int i = i0 + kRows * x + r0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        lo[j] = (static_cast<int>(w[x].x >> (4 * j) & 15) - 8) * s0[j];
+        hi[j] = (static_cast<int>(w[x].y >> (4 * j) & 15) - 8) * s1[j];
+      }
+      if (i >= 0 && i < kVlRows)
+        store16(a.ctl, static_cast<Out *>(a.k) + o0 + i * step + 16 * c, lo, hi, wide);
+    }
+  }
+  if (lane >= 4 * kChunks) return;
+  const int t = lane >> 2 & 3, f = (lane >> 4) * 4 + (lane & 3);
+  const uint32_t *vw = reinterpret_cast<const uint32_t *>(rec + rec_vcode(D)) + vword_at(m, 0, t, f, D);
+  const float *vs = reinterpret_cast<const float *>(rec + rec_vscale(D));
+  uint32_t w[8];
+#pragma unroll
+  for (int g = 0; g < 8; ++g) w[g] = vw[16 * g];
+  const float2 sa = *reinterpret_cast<const float2 *>(vs + vscale_at(16 * m + 2 * t, f >> 1, D));
+  const float2 sb = *reinterpret_cast<const float2 *>(vs + vscale_at(16 * m + 2 * t + 8, f >> 1, D));
+#pragma unroll
+  for (int z = 0; z < 4; ++z) {  // tokens 2t, 2t + 8, 2t + 1, 2t + 9
+    const int i = i0 + 2 * t + 8 * (z & 1) + (z >> 1), sh = 4 * (z & 1) + 16 * (z >> 1);
+    const float s = z == 0 ? sa.x : z == 1 ? sb.x : z == 2 ? sa.y : sb.y;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      lo[g] = (static_cast<int>(w[g] >> sh & 15) - 8) * s;
+      hi[g] = (static_cast<int>(w[g] >> (sh + 8) & 15) - 8) * s;
+    }
+    if (i >= 0 && i < kVlRows)
+      store16(a.ctl, static_cast<Out *>(a.v) + o0 + i * step + 16 * f, lo, hi, wide);
+  }
+}
+
+// A warp per 16 list rows of one head. Lane i < 16 finds row i's record or tile (or that
+// it has none). Rows that are consecutive int4 tokens of one request (a prefix) are read
+// half a record at a time, others one by one: a token alone touches four times the bytes
+// of its V codes. kD: the head dim, or 0 for one of the others.
 template <typename Out, int kD>
 __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a) {
   wait_prior_grid();
@@ -450,15 +536,15 @@ __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a
   if (row0 >= a.n) return;
   // at: byte offset of the record, or (kind 2) element offset of the tile; kind 0: none
   size_t at = 0;
-  int kind = 0, r = 0;
+  int kind = 0, s = -1, pos = 0;
   if (lane < kVlRows && row0 + lane < a.n) {
     const int32_t *ps = a.slot + row0 + lane, *pp = a.pos + row0 + lane;
     if (in_bounds(a.ctl, ps, 4) && in_bounds(a.ctl, pp, 4)) {
-      const int s = *ps, pos = *pp;
+      s = *ps;
+      pos = *pp;
       int len = -1;
       if (s >= 0 && s < a.d.slots && in_bounds(a.ctl, a.d.lengths + s, 4)) len = a.d.lengths[s];
       const int g = pos >> 5;
-      r = pos & 31;
       if (s == -1) {
         kind = 0;
       } else if (!a.d.holds(len) || pos < 0 || pos >= len) {
@@ -481,27 +567,36 @@ __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a
       }
     }
   }
-  const int passes = kVlRows * pieces / 32;  // D / 32
-#pragma unroll 4
+  if constexpr (kD != 0) {
+    const int s0 = __shfl_sync(~0u, s, 0), p0 = __shfl_sync(~0u, pos, 0);
+    if (__all_sync(~0u, lane >= kVlRows || (kind == 1 && s == s0 && pos == p0 + lane))) {
+      const bool wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 31) == 0;
+      for (int q = p0 >> 4; q <= (p0 + kVlRows - 1) >> 4; ++q) {
+        const int i0 = 16 * q - p0;
+        const size_t off = __shfl_sync(~0u, static_cast<unsigned long long>(at), max(0, i0));
+        read_half<Out, kD>(a, a.d.pool + off, q & 1, i0, row0, h, wide, lane);
+      }
+      return;
+    }
+  }
+  const int passes = kVlRows * pieces / 32;
+#pragma unroll 2
   for (int ps = 0; ps < passes; ++ps) {
     const int task = 32 * ps + lane, i = task / pieces, p = task - i * pieces, d0 = 8 * p;
-    const int kd = __shfl_sync(~0u, kind, i), rr = __shfl_sync(~0u, r, i);
+    const int kd = __shfl_sync(~0u, kind, i), r = __shfl_sync(~0u, pos, i) & 31;
     const size_t off = __shfl_sync(~0u, static_cast<unsigned long long>(at), i);
     if (kd == 0) continue;
     float k[8], v[8];
     if (kd == 1) {
       const uint8_t *rec = a.d.pool + off;
-      const uint32_t kw = *reinterpret_cast<const uint32_t *>(rec + rr * (D / 2) + 4 * p);
-      // the scales of a piece: channels 0 4 1 5, and 64 bytes on 2 6 3 7
-      const float *ks = reinterpret_cast<const float *>(rec + rec_kscale(D)) + kscale_at(d0, D);
-      const float4 s0 = *reinterpret_cast<const float4 *>(ks);
-      const float4 s1 = *reinterpret_cast<const float4 *>(ks + 16);
-      const float sc[8] = {s0.x, s0.z, s1.x, s1.z, s0.y, s0.w, s1.y, s1.w};
+      const uint32_t kw = *reinterpret_cast<const uint32_t *>(rec + r * (D / 2) + 4 * p);
+      float sc[8];
+      load_kscales(rec, d0, D, sc);
       const uint32_t *vw = reinterpret_cast<const uint32_t *>(rec + rec_vcode(D)) +
-                           vword_at(rr >> 4, 0, (rr & 7) >> 1, p >> 1, D);
+                           vword_at(r >> 4, 0, (r & 7) >> 1, p >> 1, D);
       const int step = D % 64 == 0 ? 16 : 8;  // words from feature to feature
-      const float vs = reinterpret_cast<const float *>(rec + rec_vscale(D))[vscale_at(rr, d0 >> 5, D)];
-      const int sh = 4 * (4 * (rr & 1) + 2 * (p & 1) + (rr >> 3 & 1));
+      const float vs = reinterpret_cast<const float *>(rec + rec_vscale(D))[vscale_at(r, d0 >> 5, D)];
+      const int sh = 4 * (4 * (r & 1) + 2 * (p & 1) + (r >> 3 & 1));
       uint32_t w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = vw[j * step];
@@ -511,7 +606,7 @@ __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a
         v[j] = (static_cast<int>(w[j] >> sh & 15) - 8) * vs;
       }
     } else {
-      const size_t ek = off + ringk_at(rr, d0, D), ev = off + 32 * D + ringv_at(rr, d0, D);
+      const size_t ek = off + ringk_at(r, d0, D), ev = off + 32 * D + ringv_at(r, d0, D);
       if (a.d.win_dt == KVQ_F32) {
         const float *x = static_cast<const float *>(a.d.ring);
 #pragma unroll
@@ -548,13 +643,23 @@ void launch_values(const PageValuesArgs &a, cudaStream_t s) {
     launch_dependent(page_values_kernel<Out, 0>, grid, dim3(256), 0, s, a);
 }
 
-template <typename In, typename Win>
-void launch_append_typed(const AppendPagesArgs &a, int num_sms, cudaStream_t s) {
+template <typename In, typename Win, int kD>
+void launch_append_dim(const AppendPagesArgs &a, int num_sms, cudaStream_t s) {
   const int half = (a.d.D / 2 + 31) / 32 * 32;
   const long items = static_cast<long>(a.cap_work) * a.d.Hkv;
   const int grid = static_cast<int>(std::min<long>(items, 8L * num_sms));
-  launch_dependent(append_pages_kernel<In, Win>, dim3(grid), dim3(2 * half),
+  launch_dependent(append_pages_kernel<In, Win, kD>, dim3(grid), dim3(2 * half),
                    a.d.record() + half / 8 * 128, s, a);
+}
+
+template <typename In, typename Win>
+void launch_append_typed(const AppendPagesArgs &a, int num_sms, cudaStream_t s) {
+  if (a.d.D == 128)
+    launch_append_dim<In, Win, 128>(a, num_sms, s);
+  else if (a.d.D == 64)
+    launch_append_dim<In, Win, 64>(a, num_sms, s);
+  else
+    launch_append_dim<In, Win, 0>(a, num_sms, s);
 }
 
 }  // namespace
