@@ -422,7 +422,7 @@ struct PageValuesArgs {
   KernelCtl ctl;
 };
 
-constexpr int kVlRows = 16;  // list rows of one warp
+constexpr int kVlRows = 16;  // list rows of a pair of warps
 
 // 8 or 16 consecutive values (wide: the address is a multiple of 32 bytes).
 template <typename Out>
@@ -468,16 +468,16 @@ __device__ __forceinline__ void load_kscales(const uint8_t *rec, int d0, int D, 
 }
 
 // Tokens [16 m, 16 m + 16) of a record, those with list index i0 + token in [0, 16), to
-// the list rows from row0 on. A lane takes 16 channels of K of every token in its turn
-// and, of V, the eight words of 16 features and four tokens: every byte is read once.
+// the list rows from row0 on: K, or V. A lane takes 16 channels of K of every token in its
+// turn, or the eight words of V of 16 features and four tokens: every byte is read once.
 template <typename Out, int D>
-__device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t *rec, int m, int i0,
-                                          long row0, int h, bool wide, int lane) {
+__device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t *rec, bool v, int m,
+                                          int i0, long row0, int h, bool wide, int lane) {
   constexpr int kChunks = D / 16, kRows = 32 / kChunks;
   float lo[8], hi[8];
   const size_t o0 = (static_cast<size_t>(row0) * a.d.Hkv + h) * D;
   const size_t step = static_cast<size_t>(a.d.Hkv) * D;
-  {
+  if (!v) {
     const int c = lane & (kChunks - 1), r0 = lane / kChunks;
     uint2 w[16 / kRows];
 #pragma unroll
@@ -497,6 +497,7 @@ __device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t
       if (i >= 0 && i < kVlRows)
         store16(a.ctl, static_cast<Out *>(a.k) + o0 + i * step + 16 * c, lo, hi, wide);
     }
+    return;
   }
   if (lane >= 4 * kChunks) return;
   const int t = lane >> 2 & 3, f = (lane >> 4) * 4 + (lane & 3);
@@ -521,17 +522,18 @@ __device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t
   }
 }
 
-// A warp per 16 list rows of one head. Lane i < 16 finds row i's record or tile (or that
+// Two warps per 16 list rows of one head. Lane i < 16 finds row i's record or tile (or that
 // it has none). Rows that are consecutive int4 tokens of one request (a prefix) are read
-// half a record at a time, others one by one: a token alone touches four times the bytes
-// of its V codes. kD: the head dim, or 0 for one of the others.
+// half a record at a time, K by one warp and V by the other; others one by one, eight
+// rows a warp: a token alone touches four times the bytes of its V codes. kD: the head
+// dim, or 0 for one of the others.
 template <typename Out, int kD>
 __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a) {
   wait_prior_grid();
   allow_next_grid();
   const int D = kD ? kD : a.d.D, pieces = D / 8, lane = threadIdx.x & 31;
-  const long unit = (blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x) >> 5;
-  const int h = static_cast<int>(unit % a.d.Hkv);
+  const long unit = (blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x) >> 6;
+  const int h = static_cast<int>(unit % a.d.Hkv), second = threadIdx.x >> 5 & 1;
   const long row0 = unit / a.d.Hkv * kVlRows;
   if (row0 >= a.n) return;
   // at: byte offset of the record, or (kind 2) element offset of the tile; kind 0: none
@@ -574,15 +576,16 @@ __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a
       for (int q = p0 >> 4; q <= (p0 + kVlRows - 1) >> 4; ++q) {
         const int i0 = 16 * q - p0;
         const size_t off = __shfl_sync(~0u, static_cast<unsigned long long>(at), max(0, i0));
-        read_half<Out, kD>(a, a.d.pool + off, q & 1, i0, row0, h, wide, lane);
+        read_half<Out, kD>(a, a.d.pool + off, second, q & 1, i0, row0, h, wide, lane);
       }
       return;
     }
   }
-  const int passes = kVlRows * pieces / 32;
-#pragma unroll 2
+  const int passes = pieces / 4;
+#pragma unroll 4
   for (int ps = 0; ps < passes; ++ps) {
-    const int task = 32 * ps + lane, i = task / pieces, p = task - i * pieces, d0 = 8 * p;
+    const int task = 32 * ps + lane, r8 = task / pieces, p = task - r8 * pieces, d0 = 8 * p;
+    const int i = 8 * second + r8;
     const int kd = __shfl_sync(~0u, kind, i), r = __shfl_sync(~0u, pos, i) & 31;
     const size_t off = __shfl_sync(~0u, static_cast<unsigned long long>(at), i);
     if (kd == 0) continue;
@@ -634,7 +637,7 @@ __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a
 template <typename Out>
 void launch_values(const PageValuesArgs &a, cudaStream_t s) {
   const long units = static_cast<long>((a.n + kVlRows - 1) / kVlRows) * a.d.Hkv;
-  const dim3 grid(static_cast<unsigned>((units + 7) / 8));
+  const dim3 grid(static_cast<unsigned>((units + 3) / 4));
   if (a.d.D == 128)
     launch_dependent(page_values_kernel<Out, 128>, grid, dim3(256), 0, s, a);
   else if (a.d.D == 64)
