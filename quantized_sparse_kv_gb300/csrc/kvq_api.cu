@@ -1014,7 +1014,7 @@ kvq_status kv_append_pages(const kvq_paged_cache *cache, const kvq_page_plan *pl
       (dev_status && !aligned16(dev_status)))
     return KVQ_ERR_ALIGN;
   const int64_t most = 0x7fffffffL;
-  if (static_cast<int64_t>(plan->cap_work) * cache->kv_heads > most || rows->k_stride_row > most ||
+  if (2 * static_cast<int64_t>(plan->cap_work) * cache->kv_heads > most || rows->k_stride_row > most ||
       rows->k_stride_head > most || rows->v_stride_row > most || rows->v_stride_head > most)
     return KVQ_ERR_UNSUPPORTED;
   kvq::KernelCtl ctl = make_ctl(dev_status);

@@ -6,15 +6,14 @@
 // token over 32 features. Values that are bf16 take the reciprocal and one correction step
 // (int4_round.cuh, the same codes), others the division.
 //
-// Append. A CTA of about D threads has one 32-token group of one head. Half of its
-// threads take K: a thread has a pair of channels of all 32 tokens in registers, so the
-// maxima need no exchange and a warp reads whole rows. The others take V: a thread has four
-// features of 16 tokens; eight lanes share a token's 32 features, their maxima meet in
+// Append. A CTA of about D / 2 threads has K or V of one 32-token group of one head. For
+// K a thread has a pair of channels of all 32 tokens in registers, so the maxima need no
+// exchange and a warp reads whole rows. For V a thread has four features of 16 tokens; eight lanes share a token's 32 features, their maxima meet in
 // three lane exchanges for two tokens at a time and their scales come back through shared
 // memory. V codes are made from (token, token + 8)
 // pairs of one feature, which is the byte a record's words hold; lanes of features y and
-// y + 8 exchange half of their bytes and each keeps half of the words. The record (40 D
-// bytes) is put together in shared memory and leaves as one bulk copy. All of a thread's
+// y + 8 exchange half of their bytes and each keeps half of the words. Each half of
+// the record (20 D bytes) is put together in shared memory and leaves as one bulk copy. All of a thread's
 // loads are issued before the first is used, and several CTAs share an SM: reads in flight
 // are what a prompt's append is bound by.
 #include <algorithm>
@@ -139,17 +138,17 @@ __device__ __forceinline__ size_t row_elem(const AppendPagesArgs &a, const Group
                                : row * a.r.ksr + static_cast<int64_t>(w.h) * a.r.ksh);
 }
 
-// The new tokens of window group g into its tile, eight elements of a row at a time (a
-// tile's K keeps them together, its V has them apart), K and V in turn.
+// K or V of the new tokens of window group g into its tile, eight elements of a row at a
+// time (a tile's K keeps them together, its V has them apart).
 template <typename In, typename Win, int kD>
-__device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const GroupWork &w, int g) {
+__device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const GroupWork &w, bool v,
+                                           int g) {
   using T = Types<In, Win>;
   const int D = kD ? kD : a.d.D, p0 = max(w.before, 32 * g), p1 = min(w.after, 32 * g + 32), pieces = D / 8;
   const size_t tile = a.d.tile_at(w.s, w.h, g);
   Win *ring = static_cast<Win *>(a.d.ring);
-  for (int i = threadIdx.x; i < 2 * (p1 - p0) * pieces; i += blockDim.x) {
-    const int pos = p0 + i / (2 * pieces), x = i % (2 * pieces), d = 8 * (x % pieces), r = pos & 31;
-    const bool v = x >= pieces;
+  for (int i = threadIdx.x; i < (p1 - p0) * pieces; i += blockDim.x) {
+    const int pos = p0 + i / pieces, d = 8 * (i % pieces), r = pos & 31;
     const In *row = static_cast<const In *>(v ? a.r.v : a.r.k) + row_elem(a, w, pos, v) + d;
     typename T::Pair y[4];
 #pragma unroll
@@ -175,7 +174,7 @@ __device__ __forceinline__ void write_tile(const AppendPagesArgs &a, const Group
   }
 }
 
-// K of a group: thread p has channels 2p and 2p + 1.
+// K of a group, the first half of its record: thread p has channels 2p and 2p + 1.
 template <typename In, typename Win, int kD>
 __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork &w, uint8_t *rec,
                                        int p) {
@@ -231,7 +230,7 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
   }
 }
 
-// V of a group: thread i has features 32 b + 4 e .. + 3 of the 16 tokens of half m, i = (m,
+// V of a group, the second half of its record: thread i has features 32 b + 4 e .. + 3 of the 16 tokens of half m, i = (m,
 // b, e); every lane of a warp takes part in the exchanges.
 template <typename In, typename Win, int kD>
 __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork &w, uint8_t *rec,
@@ -297,7 +296,7 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
   const float s1 = fast ? scale_recip(m1) : int4_scale(m1);
   // [half and block][t][token 2t or 2t + 1]: -scale of the token and of the one 8 behind it,
   // then their reciprocals
-  float *aux = reinterpret_cast<float *>(rec + 40 * D) + (i >> 3) * 32;
+  float *aux = reinterpret_cast<float *>(rec + 20 * D) + (i >> 3) * 32;
   {
     float *o = aux + (e & 3) * 8 + (e >> 2);
     o[0] = -s0;
@@ -307,11 +306,11 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
   }
   __syncwarp();
   if (live) {
-    float *vs = reinterpret_cast<float *>(rec + rec_vscale(D));
+    float *vs = reinterpret_cast<float *>(rec + rec_vscale(D) - rec_vcode(D));
     vs[vscale_at(16 * m + 2 * e, b, D)] = s0;
     vs[vscale_at(16 * m + 2 * e + 1, b, D)] = s1;
   }
-  uint32_t *words = reinterpret_cast<uint32_t *>(rec + rec_vcode(D));
+  uint32_t *words = reinterpret_cast<uint32_t *>(rec);
   const bool upper = e & 2;  // features y + 8
   const int f = 2 * b + (e >> 2), g0 = 4 * (e & 1) + (upper ? 2 : 0);
 #pragma unroll
@@ -355,24 +354,27 @@ __device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// A CTA per (group of the work list, head). A group that is packed may have tokens in a
-// tile of the window that the step's new tokens take over: the CTA that packs it writes
-// them too, behind its own reads, and the tile's own entry leaves them to it, so no
-// order between CTAs is needed.
+// A CTA per (group of the work list, head, K or V). A group that is packed may have
+// tokens in a tile of the window that the step's new tokens take over: the CTA that packs
+// it writes them too, behind its own reads, and the tile's own entry leaves them to it, so
+// no order between CTAs is needed.
 template <typename In, typename Win, int kD>
-__global__ void __launch_bounds__(256, sizeof(Win) == 2 ? 4 : 2) append_pages_kernel(const AppendPagesArgs a) {
+__global__ void __launch_bounds__(128, sizeof(Win) == 2 ? 8 : 4)
+    append_pages_kernel(const AppendPagesArgs a) {
   extern __shared__ __align__(16) uint8_t rec[];
   wait_prior_grid();
   allow_next_grid();
-  const int T = a.d.tiles, half = blockDim.x / 2;
+  const int T = a.d.tiles, D = kD ? kD : a.d.D;
   int n = 0;
   if (in_bounds(a.ctl, a.counts, 16)) n = min(a.counts[1], a.cap_work);
-  for (int it = blockIdx.x; it < n * a.d.Hkv; it += gridDim.x) {
+  for (int it = blockIdx.x; it < 2 * n * a.d.Hkv; it += gridDim.x) {
     GroupWork w;
-    w.h = it % a.d.Hkv;
-    const int4 *e = reinterpret_cast<const int4 *>(a.work) + 2 * (it / a.d.Hkv);
-    if (!in_bounds(a.ctl, e, 32)) continue;
-    const int4 e0 = e[0], e1 = e[1];
+    const bool v = it & 1;
+    const int e = (it >> 1) / a.d.Hkv;
+    w.h = (it >> 1) - e * a.d.Hkv;
+    const int4 *p = reinterpret_cast<const int4 *>(a.work) + 2 * static_cast<size_t>(e);
+    if (!in_bounds(a.ctl, p, 32)) continue;
+    const int4 e0 = p[0], e1 = p[1];
     w.s = e0.x;
     w.g = e0.y;
     const int page = e0.z;
@@ -382,31 +384,31 @@ __global__ void __launch_bounds__(256, sizeof(Win) == 2 ? 4 : 2) append_pages_ke
     w.c1 = paged_cut(w.after, a.d.window) >> 5;
     w.w0 = max(w.before >> 5, w.c1);
     w.w1 = (w.after + 31) >> 5;
-    const int c0 = paged_cut(w.before, a.d.window) >> 5, ob = (w.before + 31) >> 5;
     if (w.g >= w.c1) {
       // the old group in this tile, if it moves into the pages, has its CTA write here
+      const int c0 = paged_cut(w.before, a.d.window) >> 5, ob = (w.before + 31) >> 5;
       const int o = ob - 1 - (((ob - 1 - w.g) % T) + T) % T;
-      if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile<In, Win, kD>(a, w, w.g);
+      if (!(ob > c0 && o >= c0 && o < w.c1)) write_tile<In, Win, kD>(a, w, v, w.g);
       continue;
     }
-    if (static_cast<int>(threadIdx.x) < half)
-      pack_k<In, Win, kD>(a, w, rec, threadIdx.x);
+    if (v)
+      pack_v<In, Win, kD>(a, w, rec, threadIdx.x);
     else
-      pack_v<In, Win, kD>(a, w, rec, threadIdx.x - half);
+      pack_k<In, Win, kD>(a, w, rec, threadIdx.x);
     __syncthreads();
     if (threadIdx.x == 0) {
-      uint8_t *dst = page >= 0 && page < a.d.n_pages
-                         ? a.d.record_at(page, w.g & ((1 << a.d.gpp_log2()) - 1), w.h)
-                         : nullptr;
+      uint8_t *dst = nullptr;
+      if (page >= 0 && page < a.d.n_pages)
+        dst = a.d.record_at(page, w.g & ((1 << a.d.gpp_log2()) - 1), w.h) + (v ? rec_vcode(D) : 0);
       if (!dst)
         flag_error(a.ctl, KVQ_DEV_INDEX);
-      else if (in_bounds(a.ctl, dst, a.d.record()))
-        bulk_s2g(dst, smem_u32(rec), a.d.record());
+      else if (in_bounds(a.ctl, dst, 20 * D))
+        bulk_s2g(dst, smem_u32(rec), 20 * D);
     }
     // the window group that takes over this group's tile, whose values have all been read
     if (32 * w.g < w.before) {
       const int g = w.w0 + (((w.g - w.w0) % T) + T) % T;
-      if (g < w.w1) write_tile<In, Win, kD>(a, w, g);
+      if (g < w.w1) write_tile<In, Win, kD>(a, w, v, g);
     }
     if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncthreads();  // the record is free again
@@ -648,11 +650,11 @@ void launch_values(const PageValuesArgs &a, cudaStream_t s) {
 
 template <typename In, typename Win, int kD>
 void launch_append_dim(const AppendPagesArgs &a, int num_sms, cudaStream_t s) {
-  const int half = (a.d.D / 2 + 31) / 32 * 32;
-  const long items = static_cast<long>(a.cap_work) * a.d.Hkv;
-  const int grid = static_cast<int>(std::min<long>(items, 8L * num_sms));
-  launch_dependent(append_pages_kernel<In, Win, kD>, dim3(grid), dim3(2 * half),
-                   a.d.record() + half / 8 * 128, s, a);
+  const int threads = (a.d.D / 2 + 31) / 32 * 32;
+  const long items = 2L * a.cap_work * a.d.Hkv;
+  const int grid = static_cast<int>(std::min<long>(items, 16L * num_sms));
+  launch_dependent(append_pages_kernel<In, Win, kD>, dim3(grid), dim3(threads),
+                   20 * a.d.D + threads * 16, s, a);
 }
 
 template <typename In, typename Win>
