@@ -633,7 +633,7 @@ KVQ_API kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32
  */
 typedef struct kvq_page_state {
   int32_t slots;     /* 1 .. KVQ_PAGES_MAX_SLOTS */
-  int32_t n_pages;   /* of the pool */
+  int32_t n_pages;   /* of the pool, 1 .. 2^28 */
   int32_t page;      /* tokens: 32, 64 or 128 */
   int32_t max_pages; /* of one request */
   int32_t window;    /* W, 0 .. 65,536 */
@@ -660,6 +660,7 @@ KVQ_API kvq_status kvq_paged_sizes(const kvq_paged_cache *cache, size_t sizes[6]
 /* What kv_page_tables makes of one step: device arrays of the caller's, written by it and
  * read by kv_append_pages (and by the caller).
  *   offsets   [slots + 1]: first row of each request's new tokens in the step's tensors
+ *             (sums above 2^30 are 2^30)
  *   before    [slots], after [slots]: the requests' lengths
  *   row_slot  [rows]: the request of each row, -1 for a row of none
  *   positions [rows]: its token's position (0 for a row of none); what kv_rope takes

@@ -176,6 +176,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B (no accumulator to clear)
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 template <int D>
 struct State {
   float o[D / 16][4];  // 2^-24 O^T: tile f, features 16f + g and + 8, heads 2t and 2t + 1
@@ -237,14 +246,18 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
   // exponent of the largest V scale (a NaN counts as large)
   int ev;
   {
-    const int lane = 4 * g + t;
-    float x = fmaxf(vs[lane], vs[lane + 32]);
-    if (D == 128) x = fmaxf(x, fmaxf(vs[lane + 64], vs[lane + 96]));
+    float x;
+    if constexpr (D == 128) {
+      const float4 y = reinterpret_cast<const float4 *>(vs)[4 * g + t];
+      x = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+    } else {
+      const float2 y = reinterpret_cast<const float2 *>(vs)[4 * g + t];
+      x = fmaxf(y.x, y.y);
+    }
     ev = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(x)) >> 23) - 127;
     ev = max(-4, min(8, ev));
   }
-  float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-  float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float s[2][4], e[4];
   uint32_t w[2][2][NB];
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
@@ -265,11 +278,18 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
     }
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    mma_f16(e, kLo8, kLo8, kHi8, kHi8, bq[2 * i][0], bq[2 * i][1]);
+    if (i == 0)
+      mma_f16_first(e, kLo8, kLo8, kHi8, kHi8, bq[0][0], bq[0][1]);
+    else
+      mma_f16(e, kLo8, kLo8, kHi8, kHi8, bq[2 * i][0], bq[2 * i][1]);
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const uint32_t x = w[mt][0][i], y = w[mt][1][i];
-      mma_f16(s[mt], x & kLoMask, y & kLoMask, x & kHiMask, y & kHiMask, bq[2 * i][0], bq[2 * i][1]);
+      if (i == 0)
+        mma_f16_first(s[mt], x & kLoMask, y & kLoMask, x & kHiMask, y & kHiMask, bq[0][0], bq[0][1]);
+      else
+        mma_f16(s[mt], x & kLoMask, y & kLoMask, x & kHiMask, y & kHiMask, bq[2 * i][0],
+                bq[2 * i][1]);
     }
     mma_f16(e, kLo8, kLo8, kHi8, kHi8, bq[2 * i + 1][0], bq[2 * i + 1][1]);
 #pragma unroll
@@ -456,6 +476,17 @@ __device__ __forceinline__ bool aborted(const Smem<D> &sm) {
   return *reinterpret_cast<const volatile int *>(&sm.abort_flag) != 0;
 }
 
+// A row that attends nothing: its units are finished; zeros if it is a row at all.
+template <int D>
+__device__ __noinline__ void no_items(const AttendPagesArgs &a, int row, bool zero) {
+  for (int u = row * units_per_row(a); u < (row + 1) * units_per_row(a); ++u)
+    if (in_bounds(a.ctl, a.first + u, 4)) a.first[u] = -1;
+  const size_t b = a.out_dt == KVQ_F32 ? 4 : 2, bytes = static_cast<size_t>(a.Hq) * D * b;
+  uint8_t *o = static_cast<uint8_t *>(a.out) + row * bytes;
+  if (!zero || !in_bounds(a.ctl, o, bytes)) return;
+  for (size_t i = 0; i < bytes; i += 16) *reinterpret_cast<uint4 *>(o + i) = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // This CTA's slice of the items; row0 and at0 say where it starts.
 template <int D>
 __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm, long long &lo,
@@ -464,7 +495,12 @@ __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm
   const int warp = threadIdx.x >> 5;
   const int r0 = min(a.rows, static_cast<int>(threadIdx.x) * per), r1 = min(a.rows, r0 + per);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += row_items(row_info(a, r, blockIdx.x == 0));
+  RowInfo info = {-1, -1, 0};
+  for (int r = r0; r < r1; ++r) {
+    info = row_info(a, r, blockIdx.x == 0);
+    mine += row_items(info);
+    if (info.n <= 0 && r % a.ctas == static_cast<int>(blockIdx.x)) no_items<D>(a, r, info.n == 0);
+  }
   long long v = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -500,9 +536,12 @@ __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm
     }
   }
   __syncthreads();
-  if (lo < hi)
+  if (per == 1) {
+    if (lo < hi && r0 < r1 && r0 >= sm.row0) sm.row[r0 - sm.row0] = info;
+  } else if (lo < hi) {
     for (int i = threadIdx.x; i < kRowsHeld && sm.row0 + i < a.rows; i += kThreads)
       sm.row[i] = row_info(a, sm.row0 + i, false);
+  }
   __syncthreads();
 }
 
@@ -688,7 +727,7 @@ __device__ __forceinline__ void close_unit(const AttendPagesArgs &a, Smem<D> &sm
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(const AttendPagesArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(const __grid_constant__ AttendPagesArgs a) {
   constexpr int kStages = Cfg<D>::kStages;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
@@ -727,16 +766,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
     bool stop = false;
     for (; k < end; ++k, ++at.j) {
       const int s = k % kStages;
-      stop = aborted(sm);
-      if (!stop && !mbar_wait(smem_u32(&sm.full[s]), static_cast<uint32_t>((k / kStages) & 1),
-                              a.ctl.wait_limit_ns)) {
-        if (lane == 0) {
-          flag_error(a.ctl, KVQ_DEV_TIMEOUT);
+      const uint32_t bar = smem_u32(&sm.full[s]), par = static_cast<uint32_t>((k / kStages) & 1);
+      if (!__all_sync(~0u, mbar_try_wait(bar, par))) {
+        stop = aborted(sm) || !mbar_wait(bar, par, a.ctl.wait_limit_ns);
+        stop = __any_sync(~0u, stop);
+        if (stop) {
+          if (lane == 0 && !aborted(sm)) flag_error(a.ctl, KVQ_DEV_TIMEOUT);
           *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+          break;
         }
-        stop = true;
       }
-      if (stop) break;
       const uint8_t *stage = sm.stage[s];
       if (at.j < at.int4) {
         const int valid = sm.valid[s][warp];
@@ -759,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
   }
 }
 
-// Joins a unit's partials, and writes the zeros of rows without tokens. kWarps warps per
+// Joins the partials of a unit that several CTAs had. kWarps warps per
 // head take every kWarps-th partial; with one warp a head a CTA has all of a unit's heads.
 template <int D, int kWarps>
 __global__ void __launch_bounds__(256) attend_pages_join_kernel(const AttendPagesArgs a) {
@@ -773,16 +812,14 @@ __global__ void __launch_bounds__(256) attend_pages_join_kernel(const AttendPage
   const int kvh = hc / a.chunks, chunk = hc - kvh * a.chunks;
   const int h = kWarps == 1 ? warp : static_cast<int>(blockIdx.y), w0 = kWarps == 1 ? 0 : warp;
   if (h >= min(kApHeads, a.G - kApHeads * chunk)) return;
-  const RowInfo r = row_info(a, row, false);
-  if (r.n < 0) return;
+  if (!in_bounds(a.ctl, a.first + unit, 4) || !in_bounds(a.ctl, a.last + unit, 4)) return;
+  const int c0 = a.first[unit], c1 = a.last[unit];
+  if (c0 < 0) return;                   // finished by its CTA, or a row that attends nothing
+  if (c1 < c0 || c1 >= a.ctas) return;  // (not written: a wait ran out)
   float m = kNone, l = 0.0f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  if (r.n > 0) {
-    if (!in_bounds(a.ctl, a.first + unit, 4) || !in_bounds(a.ctl, a.last + unit, 4)) return;
-    const int c0 = a.first[unit], c1 = a.last[unit];
-    if (c0 < 0) return;  // finished by its CTA
-    if (c1 < c0 || c1 >= a.ctas) return;  // (not written: a wait ran out)
+  {
     const int n = c1 - c0 + 1;
     const float *base = a.part + (static_cast<size_t>(c0) + unit) * (kApHeads * kPart) + h * kPart;
     constexpr size_t kSlot = kApHeads * kPart;
@@ -839,8 +876,6 @@ __global__ void __launch_bounds__(256) attend_pages_join_kernel(const AttendPage
         for (int v = 0; v < V; ++v) acc[v] = fmaf(x, sm_o[w][32 * v + lane], acc[v]);
       }
     }
-  } else if (w0) {
-    return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t o = (static_cast<size_t>(row) * a.Hq + kvh * a.G + kApHeads * chunk + h) * D;

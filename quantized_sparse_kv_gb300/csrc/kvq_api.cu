@@ -169,7 +169,8 @@ void ctl_add_summary(kvq::KernelCtl &c, const kvq_cache &k, const kvq_summary &s
 }
 
 bool page_state_ok(const kvq_page_state &s) {
-  return s.slots >= 1 && s.slots <= KVQ_PAGES_MAX_SLOTS && s.n_pages >= 1 && s.max_pages >= 1 &&
+  return s.slots >= 1 && s.slots <= KVQ_PAGES_MAX_SLOTS && s.n_pages >= 1 &&
+         s.n_pages <= (1 << 28) && s.max_pages >= 1 &&
          (s.page == 32 || s.page == 64 || s.page == 128) && s.window >= 0 && s.window <= 65536 &&
          static_cast<long>(s.max_pages) * s.page + s.window + 64 <= 0x7fffffffL;
 }

@@ -1082,7 +1082,7 @@ class PageTables(_Prepared):
     (int32 ones are read in place, other integers converted by every run): tokens, 0, or
     -1 for a request that ends; the step's tensors hold ``rows`` token rows. After
     ``run()`` it is the step's plan: ``offsets``, ``row_slot``, ``positions`` (what
-    Rope takes as (rows, 1)), ``before``, ``after``, ``free_after``. ``run(advance=False)``
+    Rope takes as (rows, 1)), ``before``, ``after``, ``free_after`` (1,). ``run(advance=False)``
     looks ahead without moving the state."""
 
     def __init__(self, state: PageState, n_new: torch.Tensor, rows: int):
@@ -1110,19 +1110,16 @@ class PageTables(_Prepared):
             t.data_ptr() or None for t in (self.offsets, self.before, self.after, self.row_slot,
                                            self.positions, self.work, self.counts)))
         self.ref = ctypes.byref(self.struct)
-        self._ptrs = (_ptr(self.n_new), _ptr(self.status))
-
-    @property
-    def free_after(self) -> torch.Tensor:
-        """Pages that are free after the step, (1,)."""
-        return self.counts[:1]
+        self.free_after = self.counts[:1]
+        # (arguments without and with advance)
+        self._args = [(state.ref, _ptr(self.n_new), self.ref, advance, _ptr(self.status))
+                      for advance in (0, 1)]
 
     def _run(self, advance: bool = True) -> "PageTables":
         if self._copies:
             _refresh(self._copies)
-        n_new, status = self._ptrs
-        _check(self.lib.kv_page_tables(self.state.ref, n_new, self.ref, 1 if advance else 0,
-                                       status, self._raw_stream()), "kv_page_tables")
+        _check(self.lib.kv_page_tables(*self._args[bool(advance)], self._raw_stream()),
+               "kv_page_tables")
         return self
 
 

@@ -59,7 +59,7 @@ class Model:
                 self.table[s], self.length[s] = [], 0
         have = len(self.free)
         for s, n in enumerate(n_new):
-            offsets.append(min(first, 2 ** 31 - 1))
+            offsets.append(min(first, 2 ** 30))
             if n < -1:
                 flags |= 1
             if n <= 0:
@@ -84,7 +84,7 @@ class Model:
             c1 = self.cut(end) // 32
             work += [(s, g) for g in range(self.cut(before[s]) // 32, c1)]
             work += [(s, g) for g in range(max(before[s] // 32, c1), -(-end // 32))]
-        offsets.append(min(first, 2 ** 31 - 1))
+        offsets.append(min(first, 2 ** 30))
         return offsets, before, list(self.length), slot, pos, work, flags
 
 
@@ -504,7 +504,7 @@ def host_plan(kvq, rows=10, cap=None, **kw):
     return kvq.KvqPagePlan(rows, 1000 if cap is None else cap, *f.values())
 
 
-BAD_STATES = [dict(slots=0), dict(slots=8193), dict(n_pages=0), dict(page=16), dict(page=96),
+BAD_STATES = [dict(slots=0), dict(slots=8193), dict(n_pages=0), dict(n_pages=(1 << 28) + 1), dict(page=16), dict(page=96),
               dict(max_pages=0), dict(window=-1), dict(window=65537), dict(max_pages=1 << 26)]
 
 
