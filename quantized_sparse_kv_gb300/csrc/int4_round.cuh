@@ -89,6 +89,17 @@ __host__ __device__ __forceinline__ uint32_t code8_recip(float x, float s, float
   return bits_of(add_rn(q, 12582920.0f));  // 1.5 * 2^23 + 8
 }
 
+// For any fp32 value: code + 8 in bits 0-3 of c (bits 4-7 zero), for |x| <= amax with
+// recip_ok(amax), s = fl(amax / 7) and r = fl(1 / s) -- unless the answer is false. The
+// product fl(x r) is off the true quotient by at most 2^-23 of it and fl(x / s) by 2^-24, so
+// for quotients below 7.5 the two are within 1.4e-6: both round to one integer where the
+// product is further than 5e-6 from halfway between two. (A NaN r is answered false.)
+__host__ __device__ __forceinline__ bool code8_clear(float x, float r, uint32_t &c) {
+  const float q = mul_rn(x, r), y = add_rn(q, 12582920.0f);
+  c = bits_of(y);
+  return fabsf(add_rn(q, -add_rn(y, -12582920.0f))) < 0.499995f;
+}
+
 // One code byte from a pair of bf16 values (the low half of w in the low
 // nibble), each with its own scale: on the device the four operations run
 // on both halves at once as packed f32x2 instructions (per half the same

@@ -3,8 +3,9 @@
 //
 // int4 rule of kv_pack ("KV殘差窗口", section 固定預算): scale = fl(amax / 7), code =
 // clamp(rint(fl(x / scale)), -7, 7), K per channel over the 32 tokens of a group, V per
-// token over 32 features. Values that are bf16 take the reciprocal and one correction step
-// (int4_round.cuh, the same codes), others the division.
+// token over 32 features. Values that are bf16 take the reciprocal and one correction step,
+// others the reciprocal where the code is clear, else the division (int4_round.cuh: the
+// same codes).
 //
 // Append. A CTA of about D / 2 threads has K or V of one 32-token group of one head. For
 // K a thread has a pair of channels of all 32 tokens in registers, so the maxima need no
@@ -40,6 +41,18 @@ __device__ __forceinline__ int int4_code(float x, float scale) {
 // Two codes + 8 as a byte, by the division (out of line: the usual bf16 values do without).
 __device__ __noinline__ uint32_t code_byte_div(float lo, float hi, float s_lo, float s_hi) {
   return static_cast<uint32_t>(int4_code(lo, s_lo) + 8 + 16 * (int4_code(hi, s_hi) + 8));
+}
+
+// The same without a division where the codes are clear (r: reciprocals of the scales, NaN for
+// one that has none to be used).
+__device__ __forceinline__ uint32_t code_byte_f32(float lo, float hi, float s_lo, float s_hi,
+                                                  float r_lo, float r_hi) {
+  uint32_t a, b;
+  const bool ok = code8_clear(lo, r_lo, a) & code8_clear(hi, r_hi, b);
+  return ok ? b * 16u + a : code_byte_div(lo, hi, s_lo, s_hi);
+}
+__device__ __forceinline__ float recip_or_nan(float amax, float s) {
+  return recip_ok(amax) ? recip_of(s) : __int_as_float(0x7fc00000);
 }
 
 __device__ __forceinline__ size_t el_bytes(int dt) { return dt == KVQ_F32 ? 4 : 2; }
@@ -224,9 +237,11 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
             static_cast<uint8_t>(code_byte_of(x[t].w << 16, x[t].w & 0xffff0000u, ns, r));
     }
   } else {
+    const float r0 = recip_or_nan(a0, s0), r1 = recip_or_nan(a1, s1);
 #pragma unroll
     for (int t = 0; t < 32; ++t)
-      rec[t * (D / 2) + p] = static_cast<uint8_t>(code_byte_div(x[t].lo(), x[t].hi(), s0, s1));
+      rec[t * (D / 2) + p] =
+          static_cast<uint8_t>(code_byte_f32(x[t].lo(), x[t].hi(), s0, s1, r0, r1));
   }
 }
 
@@ -301,8 +316,8 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
     float *o = aux + (e & 3) * 8 + (e >> 2);
     o[0] = -s0;
     o[4] = -s1;
-    o[2] = fast ? recip_of(s0) : 0.0f;
-    o[6] = fast ? recip_of(s1) : 0.0f;
+    o[2] = recip_or_nan(m0, s0);
+    o[6] = recip_or_nan(m1, s1);
   }
   __syncwarp();
   if (live) {
@@ -328,7 +343,8 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
                                    j & 1 ? q.w & 0xffff0000u : q.w << 16, pair64(sc.x, sc.y),
                                    pair64(sc.z, sc.w));
         } else {
-          c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y);
+          c[z][j] = code_byte_f32(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y,
+                                  sc.z, sc.w);
         }
       }
     }
