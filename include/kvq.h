@@ -747,12 +747,11 @@ KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *r
  * 65,535; 0 rows are valid.
  * Kernel choice: D = 64 or 128 with BF16 windows runs on the tensor cores; products of
  * the int4 part have fp16 operands: q times the K scales (times 4 or 1/4), and
- * probabilities times the V scales, both rounded to 11 bits, against a reference
- * that puts the largest product of a tile near 2^7; with V scales between 2^-4 and 2^8
- * keys more than 11.8 nats below the maximum keep fewer bits, and those more than 18
- * nats below it may be dropped from the output (the sum keeps them). Scales of V belong
- * below 2^15, and q * sm_scale * log2(e) times a K scale below 2^14. Other shapes run
- * an fp32 kernel.
+ * probabilities times the V scales, both rounded to 11 bits, against a reference that puts
+ * the largest product of a tile near 2^7: keys more than 11.8 nats below the maximum may
+ * keep fewer bits, and those more than 18 nats below it may be dropped from the output
+ * (the sum keeps them). q * sm_scale * log2(e) times a K scale belongs below 2^14. Other
+ * shapes run an fp32 kernel.
  */
 KVQ_API kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
                                    int32_t q_heads, int32_t n_rows, const int32_t *row_slot,

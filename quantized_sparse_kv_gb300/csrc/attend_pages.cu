@@ -32,7 +32,8 @@
 // Softmax in the log2 domain, fp32 state. The reference of a head is raised only when
 // score + log2(largest V scale of the group) exceeds it by more than kBias + kLazy, to
 // kBias below, so products P * scale stay within fp16 (below 2^12) and keep 11 bits
-// down to 2^-17 of the largest, whatever the magnitude of V.
+// down to 2^-17 of the largest, whatever the magnitude of V (scales that fp16 would not
+// hold well give a power of two to P).
 #include <algorithm>
 
 #include "int4_dequant.cuh"
@@ -229,10 +230,30 @@ __device__ __forceinline__ void raise(State<D> &st, float mx0, float mx1) {
 
 constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
-// One int4 group: 32 tokens, `valid` of them attended (kFull: all).
-template <int D, bool kFull>
+// Exponent of a group's largest V scale (a NaN counts as large).
+template <int D>
+__device__ __forceinline__ int scale_exponent(const uint8_t *rec, int lane) {
+  const float *vs = reinterpret_cast<const float *>(rec + rec_vscale(D));
+  float x;
+  if constexpr (D == 128) {
+    const float4 y = reinterpret_cast<const float4 *>(vs)[lane];
+    x = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+  } else {
+    const float2 y = reinterpret_cast<const float2 *>(vs)[lane];
+    x = fmaxf(y.x, y.y);
+  }
+  const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(x)) >> 23) - 127;
+  return max(-24, min(40, e));
+}
+// Scales outside [2^-4, 2^9) are taken there by 2^-far, which P has instead.
+__device__ __forceinline__ int far_of(int ev) { return ev - max(-4, min(8, ev)); }
+
+// One int4 group: 32 tokens, `valid` of them attended, ev the exponent of its V scales.
+// kUsual: all are attended and far_of(ev) is 0.
+template <int D, bool kUsual>
 __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
-                                         const uint32_t (&qh)[D / 32][4], int valid, int g, int t) {
+                                         const uint32_t (&qh)[D / 32][4], int valid, int ev, int g,
+                                         int t) {
   constexpr int NB = D / 32;
   const float *ks = reinterpret_cast<const float *>(rec + rec_kscale(D)) + 4 * t;
   const float *vs = reinterpret_cast<const float *>(rec + rec_vscale(D));
@@ -242,20 +263,6 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
     const float4 s = *reinterpret_cast<const float4 *>(ks + 16 * i);
     bq[i][0] = as_u32(__hmul2(as_h2(qh[i >> 1][2 * (i & 1)]), __floats2half2_rn(s.x, s.y)));
     bq[i][1] = as_u32(__hmul2(as_h2(qh[i >> 1][2 * (i & 1) + 1]), __floats2half2_rn(s.z, s.w)));
-  }
-  // exponent of the largest V scale (a NaN counts as large)
-  int ev;
-  {
-    float x;
-    if constexpr (D == 128) {
-      const float4 y = reinterpret_cast<const float4 *>(vs)[4 * g + t];
-      x = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-    } else {
-      const float2 y = reinterpret_cast<const float2 *>(vs)[4 * g + t];
-      x = fmaxf(y.x, y.y);
-    }
-    ev = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(x)) >> 23) - 127;
-    ev = max(-4, min(8, ev));
   }
   float s[2][4], e[4];
   uint32_t w[2][2][NB];
@@ -305,25 +312,33 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       s[mt][k] += e[k & 1];
-      if (!kFull && 16 * mt + 8 * (k >> 1) + g >= valid) s[mt][k] = -INFINITY;
+      if (!kUsual && 16 * mt + 8 * (k >> 1) + g >= valid) s[mt][k] = -INFINITY;
     }
     mx0 = fmaxf(mx0, fmaxf(s[mt][0], s[mt][2]));
     mx1 = fmaxf(mx1, fmaxf(s[mt][1], s[mt][3]));
   }
   constexpr float kUnit = 4194304.0f;  // 2^22: low nibbles 2^-24 times 4, high ones 2^-20 / 4
   raise(st, fmaf(mx0, kUnit, static_cast<float>(ev)), fmaf(mx1, kUnit, static_cast<float>(ev)));
+  const int far = kUsual ? 0 : far_of(ev);
+  const float shift = kUsual ? 0.0f : static_cast<float>(far);
+  const float back = kUsual ? 1.0f : __int_as_float((127 - far) << 23);  // 2^-far
   float sum[2] = {0.0f, 0.0f}, sum16[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      s[mt][k] = fast_exp2(fmaf(s[mt][k], kUnit, -st.m[k]));
-      s[mt][k + 2] = fast_exp2(fmaf(s[mt][k + 2], kUnit, -st.m[k] - 4.0f));
+      s[mt][k] = fast_exp2(fmaf(s[mt][k], kUnit, shift - st.m[k]));
+      s[mt][k + 2] = fast_exp2(fmaf(s[mt][k + 2], kUnit, shift - 4.0f - st.m[k]));
       sum[k] += s[mt][k];
       sum16[k] += s[mt][k + 2];
     }
 #pragma unroll
-  for (int k = 0; k < 2; ++k) st.l[k] += fmaf(sum16[k], 16.0f, sum[k]);
+  for (int k = 0; k < 2; ++k) {
+    if (kUsual)
+      st.l[k] += fmaf(sum16[k], 16.0f, sum[k]);
+    else
+      st.l[k] = fmaf(fmaf(sum16[k], 16.0f, sum[k]), back, st.l[k]);
+  }
 
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
@@ -335,7 +350,11 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
 #pragma unroll
       for (int f = 0; f < NB; f += 2) {
         float4 x = *reinterpret_cast<const float4 *>(vs + ((2 * mt + ps) * 4 + t) * 2 * NB + 2 * f);
-        if (!kFull) {  // (their P is 0, their scale may be anything)
+        if (!kUsual) {  // (the P of tokens not attended is 0, their scale may be anything)
+          x.x *= back;
+          x.y *= back;
+          x.z *= back;
+          x.w *= back;
           const int tok = 16 * mt + 8 * ps + 2 * t;
           if (tok >= valid) x.x = x.z = 0.0f;
           if (tok + 1 >= valid) x.y = x.w = 0.0f;
@@ -780,10 +799,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
       if (at.j < at.int4) {
         const int valid = sm.valid[s][warp];
         const uint8_t *rec = stage + warp * Cfg<D>::kRecord;
-        if (valid >= 32)
-          do_group<D, true>(st, rec, qh, 32, g, t);
+        const int ev = scale_exponent<D>(rec, lane);
+        if (valid >= 32 && far_of(ev) == 0)
+          do_group<D, true>(st, rec, qh, 32, ev, g, t);
         else if (valid > 0)
-          do_group<D, false>(st, rec, qh, valid, g, t);
+          do_group<D, false>(st, rec, qh, valid, ev, g, t);
       } else if ((warp >> 1) == (at.j & 1)) {
         const int valid = sm.valid[s][0] - 16 * (warp & 1);
         if (valid > 0)
