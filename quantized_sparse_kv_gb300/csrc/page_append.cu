@@ -236,6 +236,10 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
         rec[t * (D / 2) + p] =
             static_cast<uint8_t>(code_byte_of(x[t].w << 16, x[t].w & 0xffff0000u, ns, r));
     }
+  } else if constexpr (T::kBf16) {
+#pragma unroll
+    for (int t = 0; t < 32; ++t)
+      rec[t * (D / 2) + p] = static_cast<uint8_t>(code_byte_div(x[t].lo(), x[t].hi(), s0, s1));
   } else {
     const float r0 = recip_or_nan(a0, s0), r1 = recip_or_nan(a1, s1);
 #pragma unroll
@@ -316,8 +320,13 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
     float *o = aux + (e & 3) * 8 + (e >> 2);
     o[0] = -s0;
     o[4] = -s1;
-    o[2] = recip_or_nan(m0, s0);
-    o[6] = recip_or_nan(m1, s1);
+    if (T::kBf16) {
+      o[2] = fast ? recip_of(s0) : 0.0f;
+      o[6] = fast ? recip_of(s1) : 0.0f;
+    } else {
+      o[2] = recip_or_nan(m0, s0);
+      o[6] = recip_or_nan(m1, s1);
+    }
   }
   __syncwarp();
   if (live) {
@@ -342,6 +351,8 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
             c[z][j] = code_byte_of(j & 1 ? p.w & 0xffff0000u : p.w << 16,
                                    j & 1 ? q.w & 0xffff0000u : q.w << 16, pair64(sc.x, sc.y),
                                    pair64(sc.z, sc.w));
+        } else if constexpr (T::kBf16) {
+          c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y);
         } else {
           c[z][j] = code_byte_f32(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y,
                                   sc.z, sc.w);
@@ -507,6 +518,7 @@ __device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t
 #pragma unroll
     for (int x = 0; x < 16 / kRows; ++x) {
       const int i = i0 + kRows * x + r0;
+      if (i0 + kRows * x <= -kRows || i0 + kRows * x >= kVlRows) continue;  // (none of them)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         lo[j] = (static_cast<int>(w[x].x >> (4 * j) & 15) - 8) * s0[j];
@@ -530,6 +542,7 @@ __device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t
   for (int z = 0; z < 4; ++z) {  // tokens 2t, 2t + 8, 2t + 1, 2t + 9
     const int i = i0 + 2 * t + 8 * (z & 1) + (z >> 1), sh = 4 * (z & 1) + 16 * (z >> 1);
     const float s = z == 0 ? sa.x : z == 1 ? sb.x : z == 2 ? sa.y : sb.y;
+    if (i - 2 * t < -6 || i - 2 * t >= kVlRows) continue;
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       lo[g] = (static_cast<int>(w[g] >> sh & 15) - 8) * s;
@@ -544,9 +557,10 @@ __device__ __forceinline__ void read_half(const PageValuesArgs &a, const uint8_t
 // it has none). Rows that are consecutive int4 tokens of one request (a prefix) are read
 // half a record at a time, K by one warp and V by the other; others one by one, eight
 // rows a warp: a token alone touches four times the bytes of its V codes. kD: the head
-// dim, or 0 for one of the others.
+// dim, or 0 for one of the others. 56 registers: 112,000 rows of two heads (two thirds of the
+// list's runs start inside a half record) 31.9 us, with 64 33.1; 16,384 rows 5.8 us and 5.7.
 template <typename Out, int kD>
-__global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a) {
+__global__ void __launch_bounds__(128, 9) page_values_kernel(const PageValuesArgs a) {
   wait_prior_grid();
   allow_next_grid();
   const int D = kD ? kD : a.d.D, pieces = D / 8, lane = threadIdx.x & 31;
@@ -655,13 +669,13 @@ __global__ void __launch_bounds__(256) page_values_kernel(const PageValuesArgs a
 template <typename Out>
 void launch_values(const PageValuesArgs &a, cudaStream_t s) {
   const long units = static_cast<long>((a.n + kVlRows - 1) / kVlRows) * a.d.Hkv;
-  const dim3 grid(static_cast<unsigned>((units + 3) / 4));
+  const dim3 grid(static_cast<unsigned>((units + 1) / 2));
   if (a.d.D == 128)
-    launch_dependent(page_values_kernel<Out, 128>, grid, dim3(256), 0, s, a);
+    launch_dependent(page_values_kernel<Out, 128>, grid, dim3(128), 0, s, a);
   else if (a.d.D == 64)
-    launch_dependent(page_values_kernel<Out, 64>, grid, dim3(256), 0, s, a);
+    launch_dependent(page_values_kernel<Out, 64>, grid, dim3(128), 0, s, a);
   else
-    launch_dependent(page_values_kernel<Out, 0>, grid, dim3(256), 0, s, a);
+    launch_dependent(page_values_kernel<Out, 0>, grid, dim3(128), 0, s, a);
 }
 
 template <typename In, typename Win, int kD>
