@@ -541,8 +541,15 @@ __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm
   // whose partial would be missing)
   const long long n = min(total, static_cast<long long>(a.ctas));
   const long long c = min(static_cast<long long>(blockIdx.x), n);
-  lo = n ? total * c / n : 0;
-  hi = n ? total * min(c + 1, n) / n : 0;
+  if (total < (1 << 22) && a.ctas < 1024) {  // (products of 32 bits: a shorter division)
+    const unsigned t32 = static_cast<unsigned>(total), n32 = max(1u, static_cast<unsigned>(n));
+    const unsigned c32 = static_cast<unsigned>(c);
+    lo = t32 * c32 / n32;
+    hi = t32 * min(c32 + 1, static_cast<unsigned>(n)) / n32;
+  } else {
+    lo = total * c / n;
+    hi = total * min(c + 1, n) / n;
+  }
   if (lo < hi && base <= lo && lo < base + mine * upr) {
     for (int r = r0; r < r1; ++r) {
       const long long n = static_cast<long long>(row_items(row_info(a, r, false))) * upr;
