@@ -34,6 +34,11 @@
 // kBias below, so products P * scale stay within fp16 (below 2^12) and keep 11 bits
 // down to 2^-17 of the largest, whatever the magnitude of V (scales that fp16 would not
 // hold well give a power of two to P).
+//
+// 64 requests of 16 to 32 thousand tokens, 16 heads over 2 (510 MB): 94 us, 5.4 TB/s, of which
+// 2.2 us until a CTA has its slice, 6 until its first item, 6.1 TB/s then (the copies without
+// the arithmetic 6.7), 10 between the first CTA's end and the last's, 4 the join. One request
+// of 700 tokens: 9.1 us.
 #include <algorithm>
 
 #include "int4_dequant.cuh"

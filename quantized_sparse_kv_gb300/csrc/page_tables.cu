@@ -8,6 +8,9 @@
 // binary search over the sums; the tables of a decoding step are one CTA. Nothing is
 // ordered by atomics, so the tables are a function of the inputs. The lengths and the
 // count of free pages are written by the CTA that is the last to have read them.
+//
+// 64 requests of a decoding step: 4.0 us, a launch and a row of dependent steps (two loads,
+// three sums, a search, a write). 1,024 requests with 24 prompts, 99,151 rows: 6.7 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -215,8 +218,9 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
     }
   }
 
+  // Rows, groups and pages, each from another thread on: those of one kind are few, and a
+  // thread that has one of each would wait for four chains of loads in a row.
   const int t0 = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
-  // rows
   for (int r = t0; r < a.rows; r += step) {
     int slot = -1, pos = 0;
     if (r < rowp[S]) {
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
     if (in_bounds(a.ctl, a.positions + r, 4)) a.positions[r] = pos;
   }
   // groups to write: those that are packed, then those of the window
-  for (int k = t0; k < n_work; k += step) {
+  for (int k = step - 1 - t0; k < n_work; k += step) {
     const int s = find_run(workp, S, k), e = k - workp[s];
     const int c0 = paged_cut(bef[s], a.window) >> 5, c1 = paged_cut(aft[s], a.window) >> 5;
     const int g = e < c1 - c0 ? c0 + e : max(bef[s] >> 5, c1) + e - (c1 - c0);
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
     }
   }
   // pages of ended requests go on top of the free ones
-  for (int k = t0; k < n_back; k += step) {
+  for (int k = (t0 + step / 2) % step; k < n_back; k += step) {
     const int s = find_run(backp, S, k);
     const int32_t *e = a.table + static_cast<size_t>(s) * a.max_pages + (k - backp[s]);
     if (n_free + k < a.n_pages && in_bounds(a.ctl, e, 4) &&
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
       a.free_pages[n_free + k] = *e;
   }
   // and requests that grow take from the top
-  for (int k = t0; k < n_take; k += step) {
+  for (int k = (t0 + step / 4) % step; k < n_take; k += step) {
     const int s = find_run(takep, S, k);
     const int page = taken_page(a, backp, k, n_free, have);
     int32_t *o = a.table + static_cast<size_t>(s) * a.max_pages + pages_of(a, bef[s]) +
@@ -306,9 +310,9 @@ int launch_page_tables(const kvq_page_state &st, const int32_t *n_new, const kvq
   a.cap_work = p.cap_work;
   a.advance = advance;
   a.ctl = ctl;
-  // (1,024 slots and 99,151 rows: 8.9 us with 512 threads, 9.4 with 256, 10.0 with 1,024)
+  // (1,024 slots: 512 threads 0.5 us faster than 256, 1.1 than 1,024)
   const int threads = st.slots <= 256 ? 256 : 512;
-  const int grid = std::max(1, std::min(num_sms, (p.rows + 2 * threads - 1) / (2 * threads)));
+  const int grid = std::max(1, std::min(num_sms, (p.rows + threads - 1) / threads));
   const size_t smem = sizeof(int) * (6 * static_cast<size_t>(st.slots) + 4);
   if (smem > 48 * 1024) opt_in_smem(page_tables_kernel, smem);
   launch_dependent(page_tables_kernel, dim3(grid), dim3(threads), smem, s, a);
