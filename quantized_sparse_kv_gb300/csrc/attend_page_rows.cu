@@ -54,6 +54,15 @@ __device__ __forceinline__ float *part_of(const PageRowsArgs &a, int row, int hc
                       (kPrHeads * (a.d.D + 2));
 }
 
+__device__ __forceinline__ void store_out(const PageRowsArgs &a, size_t o, float y) {
+  const size_t b = a.out_dt == KVQ_F32 ? 4 : 2;
+  if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.out) + o * b, b)) return;
+  if (a.out_dt == KVQ_F32)
+    static_cast<float *>(a.out)[o] = y;
+  else
+    static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(y);
+}
+
 __global__ void __launch_bounds__(kPrThreads) page_rows_kernel(const PageRowsArgs a) {
   extern __shared__ float sm[];
   wait_prior_grid();
@@ -151,6 +160,17 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_kernel(const PageRowsArg
       }
     }
   }
+  if (a.splits == 1) {  // the row's only share
+    __syncthreads();
+    if (warp < nh && lane == 0) corr[warp] = l == 0.0f ? 0.0f : 1.0f / l;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = threadIdx.x + k * kPrThreads;
+      if (i < nh * D) store_out(a, (static_cast<size_t>(row) * a.Hq + h0) * D + i, acc[k] * corr[i / D]);
+    }
+    return;
+  }
   float *part = part_of(a, row, hc, blockIdx.z);
   if (!in_bounds(a.ctl, part, sizeof(float) * kPrHeads * (D + 2))) return;
 #pragma unroll
@@ -189,12 +209,7 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_combine_kernel(const Pag
       l += lz != lz ? lz : c * lz;
     }
     y = l == 0.0f ? 0.0f : y / l;
-    const size_t o = (static_cast<size_t>(row) * a.Hq + h0) * D + i, b = a.out_dt == KVQ_F32 ? 4 : 2;
-    if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.out) + o * b, b)) continue;
-    if (a.out_dt == KVQ_F32)
-      static_cast<float *>(a.out)[o] = y;
-    else
-      static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(y);
+    store_out(a, (static_cast<size_t>(row) * a.Hq + h0) * D + i, y);
   }
 }
 
@@ -209,8 +224,9 @@ int row_splits(const PagedDims &d, int Hq, int rows, int num_sms) {
 
 size_t page_rows_workspace(const PagedDims &d, int Hq, int rows, int num_sms) {
   const int chunks = (Hq / d.Hkv + kPrHeads - 1) / kPrHeads;
-  return sizeof(float) * rows * d.Hkv * chunks * row_splits(d, Hq, rows, num_sms) * kPrHeads *
-         (static_cast<size_t>(d.D) + 2);
+  const int splits = row_splits(d, Hq, rows, num_sms);
+  if (splits == 1) return 0;
+  return sizeof(float) * rows * d.Hkv * chunks * splits * kPrHeads * (static_cast<size_t>(d.D) + 2);
 }
 
 int launch_page_rows(const PagedDims &d, const void *q, int q_dt, int Hq, int rows,
@@ -236,6 +252,7 @@ int launch_page_rows(const PagedDims &d, const void *q, int q_dt, int Hq, int ro
   opt_in_smem(page_rows_kernel, smem);
   const dim3 grid(rows, d.Hkv * a.chunks, a.splits);
   launch_dependent(page_rows_kernel, grid, dim3(kPrThreads), smem, s, a);
+  if (a.splits == 1) return 1;
   launch_dependent(page_rows_combine_kernel, dim3(rows, d.Hkv * a.chunks), dim3(kPrThreads), 0, s,
                    a);
   return 2;

@@ -70,8 +70,10 @@ struct AttendPagesArgs {
   const void *q;
   void *out;
   const int32_t *slot, *pos;
-  int32_t *first, *last;  // [unit]: CTAs of its first and last item; first = -1: finished
-  float *part;            // [CTA + unit][8][kPart]
+  // [unit]: partial of its first item and CTA of its last one; first = -1: finished
+  int32_t *first, *last;
+  // [CTA][2][8][kPart]: only the first and the last unit of a slice can have others' items
+  float *part;
   float scale_log2;
   int q_dt, out_dt, rows, Hq, G, chunks, ctas;
   KernelCtl ctl;
@@ -663,11 +665,12 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32));
 }
 
-// The four warps' states of a unit: finished (whole) or left as this CTA's partial.
+// The four warps' states of a unit: finished (whole) or left as this CTA's partial (`later`:
+// of a unit behind its first).
 template <int D>
 __device__ __forceinline__ void close_unit(const AttendPagesArgs &a, Smem<D> &sm, State<D> &st,
-                                           int row, int hc, bool starts, bool ends, int warp,
-                                           int g, int t) {
+                                           int row, int hc, bool later, bool starts, bool ends,
+                                           int warp, int g, int t) {
   const int unit = row * units_per_row(a) + hc;
   float l0 = st.l[0], l1 = st.l[1];
 #pragma unroll
@@ -709,13 +712,14 @@ __device__ __forceinline__ void close_unit(const AttendPagesArgs &a, Smem<D> &sm
     sm.red_ls[h] = ls;
   }
   const bool whole = starts && ends;
-  float *part = a.part + (static_cast<size_t>(blockIdx.x) + unit) * (kApHeads * Cfg<D>::kPart);
+  const int slot = 2 * blockIdx.x + later;
+  float *part = a.part + static_cast<size_t>(slot) * (kApHeads * Cfg<D>::kPart);
   const bool part_ok = whole || in_bounds(a.ctl, part, sizeof(float) * kApHeads * Cfg<D>::kPart);
   const int kvh = hc / a.chunks, chunk = hc - kvh * a.chunks;
   const int nh = min(kApHeads, a.G - kApHeads * chunk);
   const size_t out0 = (static_cast<size_t>(row) * a.Hq + kvh * a.G + kApHeads * chunk) * D;
   if (threadIdx.x == 0 && in_bounds(a.ctl, a.first + unit, 4) && in_bounds(a.ctl, a.last + unit, 4)) {
-    if (starts) a.first[unit] = whole ? -1 : static_cast<int>(blockIdx.x);
+    if (starts) a.first[unit] = whole ? -1 : slot;
     if (ends) a.last[unit] = blockIdx.x;
   }
   for (int half = 0; half < 2; ++half) {
@@ -824,7 +828,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
     }
-    close_unit(a, sm, st, at.row, at.hc, starts, ends, warp, g, t);
+    // (a unit that starts in the slice, but not with it, is a later one)
+    close_unit(a, sm, st, at.row, at.hc, starts && k > at.j, starts, ends, warp, g, t);
     if (stop || aborted(sm)) break;
     if (ends) at.next_unit(a, sm);
   }
@@ -845,24 +850,27 @@ __global__ void __launch_bounds__(256) attend_pages_join_kernel(const AttendPage
   const int h = kWarps == 1 ? warp : static_cast<int>(blockIdx.y), w0 = kWarps == 1 ? 0 : warp;
   if (h >= min(kApHeads, a.G - kApHeads * chunk)) return;
   if (!in_bounds(a.ctl, a.first + unit, 4) || !in_bounds(a.ctl, a.last + unit, 4)) return;
-  const int c0 = a.first[unit], c1 = a.last[unit];
-  if (c0 < 0) return;                   // finished by its CTA, or a row that attends nothing
+  const int slot0 = a.first[unit], c0 = slot0 >> 1, c1 = a.last[unit];
+  if (slot0 < 0) return;                // finished by its CTA, or a row that attends nothing
   if (c1 < c0 || c1 >= a.ctas) return;  // (not written: a wait ran out)
   float m = kNone, l = 0.0f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
   {
     const int n = c1 - c0 + 1;
-    const float *base = a.part + (static_cast<size_t>(c0) + unit) * (kApHeads * kPart) + h * kPart;
+    // its partials: slot0, and the first one of every CTA behind
     constexpr size_t kSlot = kApHeads * kPart;
-    if (!in_bounds(a.ctl, base, sizeof(float) * ((n - 1) * kSlot + kPart))) return;
+    const float *parts = a.part + h * kPart;
+    if (!in_bounds(a.ctl, parts + slot0 * kSlot, sizeof(float) * kPart) ||
+        !in_bounds(a.ctl, parts + 2 * c0 * kSlot, sizeof(float) * (2 * (n - 1) * kSlot + kPart)))
+      return;
     constexpr int kBatch = 8;
     for (int i0 = w0; i0 < n; i0 += kWarps * kBatch) {
       float pm[kBatch], pl[kBatch], po[kBatch][V];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int c = i0 + kWarps * i;
-        const float *p = base + static_cast<size_t>(min(c, n - 1)) * kSlot;
+        const float *p = parts + (c == 0 ? slot0 : 2 * (c0 + min(c, n - 1))) * kSlot;
         const float2 ml = *reinterpret_cast<const float2 *>(p + D);
         pm[i] = c < n ? ml.x : -INFINITY;
         pl[i] = c < n ? ml.y : 0.0f;
@@ -962,7 +970,7 @@ bool attend_pages_supported(const PagedDims &d, int Hq, int rows) {
 size_t attend_pages_workspace(const PagedDims &d, int Hq, int rows, int num_sms) {
   const size_t units = static_cast<size_t>(rows) * d.Hkv * chunks_of(d, Hq);
   return (8 * units + 15) / 16 * 16 +
-         sizeof(float) * (units + grid_of(d, Hq, rows, num_sms)) * kApHeads * (d.D + 4);
+         sizeof(float) * 2 * grid_of(d, Hq, rows, num_sms) * kApHeads * (d.D + 4);
 }
 
 int launch_attend_pages(const PagedDims &d, const void *q, int q_dt, int Hq, int rows,
