@@ -83,7 +83,7 @@ __device__ __forceinline__ int find_run(const int *sum, int n, int k) {
 }
 
 __device__ __forceinline__ int pages_of(const TablesArgs &a, int len) {
-  return (paged_cut(len, a.window) + (1 << a.page_log2) - 1) >> a.page_log2;
+  return paged_pages(len, a.window, a.page_log2);
 }
 
 __device__ __forceinline__ bool holds(const TablesArgs &a, int len) {

@@ -13,6 +13,11 @@ __host__ __device__ __forceinline__ int paged_cut(int len, int window) {
   return len >= window ? ((len - window) >> 5) << 5 : 0;
 }
 __host__ __device__ __forceinline__ int paged_tiles(int window) { return (window + 63) >> 5; }
+// Pages that hold a request's int4 tokens (unsigned: any length may be asked about).
+__host__ __device__ __forceinline__ int paged_pages(int len, int window, int page_log2) {
+  const uint32_t cut = static_cast<uint32_t>(paged_cut(len, window));
+  return static_cast<int>((cut + (1u << page_log2) - 1u) >> page_log2);
+}
 
 // Shape and arrays of one layer's cache, as kernels take them.
 struct PagedDims {
@@ -27,8 +32,7 @@ struct PagedDims {
   __host__ __device__ __forceinline__ int record() const { return 40 * D; }
   // whether a table row can hold a request of this length
   __host__ __device__ __forceinline__ bool holds(int len) const {
-    return len >= 0 &&
-           (paged_cut(len, window) + (1 << page_log2) - 1) >> page_log2 <= max_pages;
+    return len >= 0 && paged_pages(len, window, page_log2) <= max_pages;
   }
   // record of group g (of its page) and head h
   __host__ __device__ __forceinline__ uint8_t *record_at(int page, int sub, int h) const {
