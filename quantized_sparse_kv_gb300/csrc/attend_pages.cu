@@ -133,6 +133,7 @@ struct __align__(16) Smem {
   RowInfo row[kRowsHeld];
   long long sums[kConsumers + 1];
   int row0, abort_flag;
+  int quit;  // abort_flag as all consumers see it at the end of a unit
   int at0;  // items of row0 before the slice
 };
 
@@ -708,6 +709,8 @@ __device__ __forceinline__ void close_unit(const AttendPagesArgs &a, Smem<D> &sm
       sm.red_c[w][h] = c * 16777216.0f;  // O is held times 2^-24
       ls += c * sm.red_l[w][h];
     }
+    // (between two barriers: a warp that gave up waiting did so before the first)
+    if (h == 0) sm.quit = aborted(sm);
     sm.red_mx[h] = mx;
     sm.red_ls[h] = ls;
   }
@@ -798,14 +801,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
     const bool starts = at.j == 0;
     const int end = min(n_items, k + at.items - at.j);
     const bool ends = end - k == at.items - at.j;
-    bool stop = false;
     for (; k < end; ++k, ++at.j) {
       const int s = k % kStages;
       const uint32_t bar = smem_u32(&sm.full[s]), par = static_cast<uint32_t>((k / kStages) & 1);
       if (!__all_sync(~0u, mbar_try_wait(bar, par))) {
-        stop = aborted(sm) || !mbar_wait(bar, par, a.ctl.wait_limit_ns);
-        stop = __any_sync(~0u, stop);
-        if (stop) {
+        const bool stop = aborted(sm) || !mbar_wait(bar, par, a.ctl.wait_limit_ns);
+        if (__any_sync(~0u, stop)) {
           if (lane == 0 && !aborted(sm)) flag_error(a.ctl, KVQ_DEV_TIMEOUT);
           *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
           break;
@@ -830,7 +831,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
     }
     // (a unit that starts in the slice, but not with it, is a later one)
     close_unit(a, sm, st, at.row, at.hc, starts && k > at.j, starts, ends, warp, g, t);
-    if (stop || aborted(sm)) break;
+    // the four warps leave together, as each unit's end has barriers for all of them
+    if (sm.quit) break;
     if (ends) at.next_unit(a, sm);
   }
 }

@@ -288,3 +288,29 @@ def test_both_builds_agree(tmp_path):
             assert int(rel[name]) == 0 and int(dbg[name]) == 0, name
         else:
             assert rel[name].tobytes() == dbg[name].tobytes(), name
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_at_any_item_end_the_call(kvq):  # noqa: F811
+    # slices of several units each, whose ends are where the warps of a CTA meet
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    d, rows = 64, 3000
+    k = torch.randn((150, 1, d), generator=gen, device="cuda").bfloat16()
+    v = torch.randn((150, 1, d), generator=gen, device="cuda").bfloat16()
+    cache, values = one_request(kvq, 150, k, v, 40, 1, d)
+    q = torch.randn((rows, 3, d), generator=gen, device="cuda").bfloat16()
+    call = kvq.AttendPages(cache, q, torch.zeros(rows, dtype=torch.int32, device="cuda"),
+                           out_dtype="f32")
+    for item in [*range(24), 3 * rows - 1]:
+        kvq.debug_set(2_000_000, item)  # 2 ms
+        try:
+            call.run()
+            assert kvq.read_status(call.status) & kvq.DEV_TIMEOUT
+        finally:
+            kvq.debug_set(0, -1)
+        call.status.zero_()
+    got = call.run()
+    assert kvq.read_status(call.status) == 0
+    for i in (0, 1, rows - 1):
+        want = attention64(q[i].double().cpu().numpy(), *values)
+        assert O.rel_l2(got[i].double().cpu().numpy(), want) <= TOL_TENSOR
