@@ -645,7 +645,9 @@ typedef struct kvq_page_state {
 
 typedef struct kvq_paged_cache {
   kvq_page_state state;
-  int32_t kv_heads, head_dim, win_dtype;
+  int32_t kv_heads; /* 1 .. 65,535 */
+  int32_t head_dim; /* 32 .. 256, a multiple of 32 */
+  int32_t win_dtype;
   uint8_t *pool;
   void *ring;
 } kvq_paged_cache;

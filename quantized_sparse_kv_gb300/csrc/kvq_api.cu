@@ -175,9 +175,10 @@ bool page_state_ok(const kvq_page_state &s) {
          static_cast<long>(s.max_pages) * s.page + s.window + 64 <= 0x7fffffffL;
 }
 
+// (with these limits the sizes fit 64 bits)
 bool paged_ok(const kvq_paged_cache &c) {
-  return page_state_ok(c.state) && c.kv_heads >= 1 && c.head_dim >= 32 && c.head_dim <= 256 &&
-         c.head_dim % 32 == 0 && (c.win_dtype == KVQ_F32 || c.win_dtype == KVQ_BF16);
+  return page_state_ok(c.state) && c.kv_heads >= 1 && c.kv_heads <= 65535 &&
+         c.head_dim >= 32 && c.head_dim <= 256 && c.head_dim % 32 == 0 && (c.win_dtype == KVQ_F32 || c.win_dtype == KVQ_BF16);
 }
 
 kvq_status check_page_state(const kvq_page_state *s) {
@@ -1053,6 +1054,7 @@ kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *row_slot,
     return KVQ_OK;
   }
   if (!row_slot || !positions || !k || !v) return KVQ_ERR_ARG;
+  if (static_cast<long>(n_rows) * cache->kv_heads > 1L << 34) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(row_slot) || !aligned16(positions) || !aligned16(k) || !aligned16(v) ||
       (dev_status && !aligned16(dev_status)))
     return KVQ_ERR_ALIGN;

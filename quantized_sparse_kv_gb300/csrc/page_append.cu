@@ -398,13 +398,13 @@ __global__ void __launch_bounds__(128, sizeof(Win) == 2 ? 8 : 4)
   wait_prior_grid();
   allow_next_grid();
   const int T = a.d.tiles, D = kD ? kD : a.d.D;
-  int n = 0;
-  if (in_bounds(a.ctl, a.counts, 16)) n = min(a.counts[1], a.cap_work);
-  for (int it = blockIdx.x; it < 2 * n * a.d.Hkv; it += gridDim.x) {
+  unsigned items = 0;
+  if (in_bounds(a.ctl, a.counts, 16)) items = 2u * max(0, min(a.counts[1], a.cap_work)) * a.d.Hkv;
+  for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {  // (up to 2^31 of them)
     GroupWork w;
     const bool v = it & 1;
-    const int e = (it >> 1) / a.d.Hkv;
-    w.h = (it >> 1) - e * a.d.Hkv;
+    const int e = static_cast<int>((it >> 1) / a.d.Hkv);
+    w.h = static_cast<int>((it >> 1) - static_cast<unsigned>(e) * a.d.Hkv);
     const int4 *p = reinterpret_cast<const int4 *>(a.work) + 2 * static_cast<size_t>(e);
     if (!in_bounds(a.ctl, p, 32)) continue;
     const int4 e0 = p[0], e1 = p[1];

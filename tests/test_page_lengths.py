@@ -5,6 +5,7 @@ pages of cut(L) are at most max_pages) for lengths at both ends of 32 bits and a
 every limit, whatever an array of lengths contains. On the GPU: such lengths are flagged
 and nothing is read or written for them.
 """
+import ctypes
 import os
 import shutil
 import subprocess
@@ -93,3 +94,23 @@ def test_lengths_that_no_table_holds_are_flagged(kvq, page, d, wdt):  # noqa: F8
         vals.run()
         assert kvq.read_status(vals.status) == kvq.DEV_INDEX
         assert bool((vals.k[0] == 0).all()) and bool((vals.k[1] != 0).any())
+
+
+def test_sizes_that_64_bits_do_not_hold_are_refused(kvq):  # noqa: F811
+    lib = kvq.load_library()
+    sizes = (ctypes.c_size_t * 6)()
+    state = kvq.KvqPageState(8192, 1 << 28, 128, 1000, 65536)
+    # the largest that is taken, then one whose pool would have 2^64 bytes and more
+    assert lib.kvq_paged_sizes(ctypes.byref(kvq.KvqPagedCache(state, 65535, 256, 0)), sizes) == 0
+    assert sizes[4] == (1 << 28) * 65535 * 4 * 40 * 256
+    assert sizes[5] == 8192 * 65535 * 2049 * 2 * 32 * 256 * 4
+    for heads in (65536, 1 << 30, (1 << 31) - 1):
+        assert lib.kvq_paged_sizes(ctypes.byref(kvq.KvqPagedCache(state, heads, 256, 0)), sizes) == 1
+
+
+def test_more_values_than_a_grid_has_blocks_are_refused(kvq):  # noqa: F811
+    lib, addr = kvq.load_library(), 1 << 20
+    state = kvq.KvqPageState(4, 10, 64, 5, 128, addr, addr, addr, addr)
+    cache = kvq.KvqPagedCache(state, 65, 128, 1, addr, addr)
+    assert lib.kv_page_values(ctypes.byref(cache), addr, addr, 1 << 28, addr, addr, 1, None,
+                              None) == 3
