@@ -356,7 +356,6 @@ struct __align__(16) DecodeSmem {
   uint64_t full[kStages];
   uint64_t empty[kStages];
   int abort_flag;
-  int quit;  // abort_flag as all consumers see it at the end of a unit
   int valid[kStages][kConsumers];   // kList: tokens of each group of the item
 };
 
@@ -638,8 +637,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
     q_from_raw<kList>(a, u, g, t, qraw, qh);
     const int u_end = min(hi, (u + 1) * a.ipu) - lo;  // CTA-relative end of unit u
     int j = lo + k - u * a.ipu;                        // item index within unit u
+    bool aborted = false;
     for (; k < u_end; ++k, ++j) {
-      if (aborted_flag(sm)) break;
+      if (aborted_flag(sm)) {
+        aborted = true;
+        break;
+      }
       const int s = k % kStages;
       if (!mbar_wait(smem_u32(&sm.full[s]), static_cast<uint32_t>((k / kStages) & 1),
                      a.ctl.wait_limit_ns)) {
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
           flag_error(a.ctl, KVQ_DEV_TIMEOUT);
           *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
         }
-        __syncwarp();
+        aborted = true;
         break;
       }
       const uint8_t *stg = sm.stage[s];
@@ -704,8 +707,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
       // (scores that are all NaN leave no maximum and a NaN sum: a finite maximum keeps the
       // merge from taking the partial for one without keys)
       sm.red_mx[h] = kList && mx == -CUDART_INF_F && lsum != 0.0f ? 0.0f : mx;
-      // (between two barriers: a warp that gave up waiting did so before the first)
-      if (h == 0) sm.quit = aborted_flag(sm);
       sm.red_ls[h] = lsum;
     }
     // heads 0-3 live in lanes with t < 2, heads 4-7 in lanes with t >= 2:
@@ -741,8 +742,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32));
     }
-    // the four warps leave together, as each unit's end has barriers for all of them
-    if (sm.quit) break;
+    if (aborted || aborted_flag(sm)) {
+      // Another warp may have looked before the flag was set and go on to the next unit:
+      // it finds this one at the barriers of every unit left (five each).
+      for (++u; u * a.ipu < hi; ++u)
+        for (int i = 0; i < 5; ++i) asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32));
+      break;
+    }
   }
 }
 
