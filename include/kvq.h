@@ -613,6 +613,9 @@ KVQ_API kvq_status kv_attend_blocks(const kvq_cache *cache, const void *q, int32
  *              (the rest of the array is scratch); n_free: 4 int32, only the first used.
  * An empty state has lengths 0, n_free[0] = n_pages and free_pages any permutation of
  * the pages. The arrays may be saved and restored by the caller, all together.
+ * Calls on a state and its caches are ordered by the caller (one stream, or events): a
+ * step's kv_page_tables and kv_append_pages do not overlap calls that read the lengths,
+ * pages or windows. Calls that only read may overlap, with a workspace each.
  *
  * kvq_paged_cache adds one layer's memory, laid out for the attention kernel:
  *   pool  [n_pages][kv_heads][page / 32][40 * D] bytes: one record per 32-token group
@@ -745,15 +748,16 @@ KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *r
  * request without tokens is zero. A slot outside [-1, slots), a length that the table
  * cannot hold or a position outside the request is flagged KVQ_DEV_INDEX and the row left
  * as it was; a page outside the pool is flagged KVQ_DEV_INDEX and its tokens skipped.
- * workspace/ws_bytes as kv_attend (they depend on n_rows and q_heads alone). n_rows <=
- * 65,535; 0 rows are valid.
+ * workspace/ws_bytes as kv_attend (the size depends on n_rows, q_heads and the cache's shape
+ * alone). n_rows <= 65,535; 0 rows are valid.
  * Kernel choice: D = 64 or 128 with BF16 windows runs on the tensor cores; products of
  * the int4 part have fp16 operands: q times the K scales (times 4 or 1/4), and
  * probabilities times the V scales, both rounded to 11 bits, against a reference that puts
  * the largest product of a tile near 2^7: keys more than 11.8 nats below the maximum may
  * keep fewer bits, and those more than 18 nats below it may be dropped from the output
- * (the sum keeps them). q * sm_scale * log2(e) times a K scale belongs below 2^14. Other
- * shapes run an fp32 kernel.
+ * (the sum keeps them). q * sm_scale * log2(e), a K scale and their product belong below
+ * 2^14 (either factor below 2^-12 has an absolute error of up to 2^-23). Other shapes run an
+ * fp32 kernel.
  */
 KVQ_API kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
                                    int32_t q_heads, int32_t n_rows, const int32_t *row_slot,

@@ -607,7 +607,7 @@ __device__ __forceinline__ void load_item(const AttendPagesArgs &a, Smem<D> &sm,
         flag_error(a.ctl, KVQ_DEV_INDEX);
       }
     }
-  } else if (w == 0) {
+  } else if (w == 0 && at.j < at.items) {
     const int g = (at.r.cut >> 5) + at.j - at.int4;
     src = static_cast<const uint8_t *>(a.d.ring) + 2 * a.d.tile_at(at.r.slot, kvh, g);
     bytes = 128 * D;
@@ -777,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
       mbar_init(smem_u32(&sm.empty[s]), kConsumers);
     }
     sm.abort_flag = 0;
+    sm.row0 = sm.at0 = 0;
     fence_mbar_init();
   }
   wait_prior_grid();
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
   Walk at = {};
   at.start(a, sm);
   int k = 0;
-  while (k < n_items) {
+  while (k < n_items && at.row < a.rows) {  // (the rows end first only if lengths changed)
     reset(st);
     load_q<D>(a, at.row, at.hc, g, t, qh);
     const bool starts = at.j == 0;
