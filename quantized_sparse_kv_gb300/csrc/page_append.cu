@@ -18,11 +18,11 @@
 // copy. All of a thread's loads are issued before the first is used, and 16 CTAs share an
 // SM at 64 registers.
 //
-// 112,000 rows of two heads, D = 128 (151 MB in and out): 34.6 us, 4.4 TB/s; the loads of
+// 112,000 rows of two heads, D = 128 (151 MB in and out): 33.9 us, 4.5 TB/s; the loads of
 // 32 warps an SM and 1.3 thousand instructions a half group, half of the issue slots, overlap
 // in part. Rows staged in shared memory a group ahead (49 us, 42 without as it was then), 16
 // values a thread (38) and 80 registers (56) were slower. One token of each of 64 requests:
-// 4.6 us, of which the launch is 2.
+// 4.5 us, of which the launch is 2 and a group that completes the rest.
 #include <algorithm>
 
 #include "int4_round.cuh"
@@ -143,6 +143,33 @@ struct Types {
       x.set(load_f32(p), load_f32(q));
     return x;
   }
+  // K of channels c and c + 1 (c even) of window row r. bf16: one load of channels k, k + 4,
+  // k + 1, k + 5, which lie together.
+  static __device__ __forceinline__ Pair win_k(const AppendPagesArgs &a, const Win *tile, int r, int c,
+                                               int D) {
+    if constexpr (kBf16) {
+      Pair x;
+      const Win *p = tile + ringk_at(r, c & ~4, D);
+      const uint2 y = in_bounds(a.ctl, p, 8) ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
+      x.w = __byte_perm(y.x, y.y, c & 4 ? 0x7632 : 0x5410);
+      return x;
+    } else {
+      return win2(a, tile + ringk_at(r, c, D), tile + ringk_at(r, c + 1, D));
+    }
+  }
+  // V of features d and d + 1 of window rows r and r + 1 (r even), bf16: one load a feature,
+  // whose tokens lie in pairs.
+  static __device__ __forceinline__ void win_v(const AppendPagesArgs &a, const Win *tile, int r, int d,
+                                               int D, Pair &t0, Pair &t1) {
+    const Win *p = tile + ringv_at(r, d, D), *q = tile + ringv_at(r, d + 1, D);
+    uint32_t y = 0, z = 0;
+    if (in_bounds(a.ctl, p, 4) && in_bounds(a.ctl, q, 4)) {
+      y = *reinterpret_cast<const uint32_t *>(p);
+      z = *reinterpret_cast<const uint32_t *>(q);
+    }
+    t0.w = __byte_perm(y, z, 0x5410);
+    t1.w = __byte_perm(y, z, 0x7632);
+  }
 };
 
 // One work entry and head: what the step does with 32-token group g of slot s.
@@ -210,7 +237,7 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
     const Win *tile = static_cast<const Win *>(a.d.ring) + a.d.tile_at(w.s, w.h, w.g);
 #pragma unroll
     for (int t = 0; t < 32; ++t)
-      x[t] = t0 + t < w.before ? T::win2(a, tile + ringk_at(t, 2 * p, D), tile + ringk_at(t, 2 * p + 1, D))
+      x[t] = t0 + t < w.before ? T::win_k(a, tile, t, 2 * p, D)
                                : T::row2(a, row + static_cast<int64_t>(t) * a.r.ksr);
   }
   float a0, a1;
@@ -278,13 +305,28 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
       T::row4(a, row + static_cast<int64_t>(t) * a.r.vsr, x[t]);
   } else {
     const Win *tile = static_cast<const Win *>(a.d.ring) + a.d.tile_at(w.s, w.h, w.g) + 32 * D;
+    if constexpr (T::kBf16) {
+      // (the window has both tokens of a pair, written or not)
 #pragma unroll
-    for (int t = 0; t < 16; ++t)
+      for (int t = 0; t < 16; t += 2)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        x[t][k] = t0 + t < w.before ? T::win2(a, tile + ringv_at(16 * m + t, d0 + 2 * k, D),
-                                              tile + ringv_at(16 * m + t, d0 + 2 * k + 1, D))
-                                    : T::row2(a, row + static_cast<int64_t>(t) * a.r.vsr + 2 * k);
+        for (int k = 0; k < 2; ++k) {
+          if (t0 + t < w.before)
+            T::win_v(a, tile, 16 * m + t, d0 + 2 * k, D, x[t][k], x[t + 1][k]);
+          else
+            x[t][k] = T::row2(a, row + static_cast<int64_t>(t) * a.r.vsr + 2 * k);
+          if (t0 + t + 1 >= w.before)
+            x[t + 1][k] = T::row2(a, row + static_cast<int64_t>(t + 1) * a.r.vsr + 2 * k);
+        }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          x[t][k] = t0 + t < w.before ? T::win2(a, tile + ringv_at(16 * m + t, d0 + 2 * k, D),
+                                                tile + ringv_at(16 * m + t, d0 + 2 * k + 1, D))
+                                      : T::row2(a, row + static_cast<int64_t>(t) * a.r.vsr + 2 * k);
+    }
   }
   // maxima of tokens 2n and 2n + 1; lane e keeps those of its own two
   float m0 = 0.0f, m1 = 0.0f;
