@@ -9,8 +9,13 @@
 // ordered by atomics, so the tables are a function of the inputs. The lengths and the
 // count of free pages are written by the CTA that is the last to have read them.
 //
-// 64 requests of a decoding step: 4.0 us, a launch and a row of dependent steps (two loads,
-// three sums, a search, a write). 1,024 requests with 24 prompts, 99,151 rows: 6.7 us.
+// Who is served depends on the sums themselves (the rows and the pages that are left). When
+// there are rows and pages for all that is asked for, as in the usual step, one sum of
+// four numbers says it; only else two more follow, of what the requests before were granted.
+//
+// 64 requests of a decoding step: 3.3 us (3.8 with three sums), a launch and a row of
+// dependent steps (two loads, a sum, a search, a write). 1,024 requests with 24 prompts, 99,151
+// rows: 6.2 us (6.7).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -31,41 +36,41 @@ struct TablesArgs {
 constexpr uint32_t kMost = 1u << 30;
 __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return min(a + b, kMost); }
 
-// Exclusive sums of two numbers over the block's threads and, in ta and tb, the sums of all.
-// One barrier: every call has a buffer of its own.
+// Exclusive sums of N numbers over the block's threads and, in t, the sums of all. One
+// barrier: every call has a buffer of its own.
+template <int N>
 struct SumBuffer {
-  uint32_t a[32], b[32];
+  uint32_t x[N][32];
 };
-__device__ __forceinline__ void block_sums(uint32_t &a, uint32_t &b, uint32_t &ta, uint32_t &tb,
-                                           SumBuffer &buf) {
+template <int N>
+__device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (&t)[N], SumBuffer<N> &buf) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const auto scan = [lane](uint32_t &x, uint32_t &y) {
+  const auto scan = [lane](uint32_t (&y)[N]) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t p = __shfl_up_sync(~0u, x, o), q = __shfl_up_sync(~0u, y, o);
-      if (lane >= o) {
-        x = add(x, p);
-        y = add(y, q);
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t p = __shfl_up_sync(~0u, y[i], o);
+        if (lane >= o) y[i] = add(y[i], p);
       }
-    }
   };
-  scan(a, b);
-  if (lane == 31) {
-    buf.a[warp] = a;
-    buf.b[warp] = b;
+  scan(x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (lane == 31) buf.x[i][warp] = x[i];
+    x[i] = __shfl_up_sync(~0u, x[i], 1);
+    if (lane == 0) x[i] = 0;
   }
-  a = __shfl_up_sync(~0u, a, 1);
-  b = __shfl_up_sync(~0u, b, 1);
-  if (lane == 0) a = b = 0;
   __syncthreads();
-  uint32_t wa = lane < warps ? buf.a[lane] : 0, wb = lane < warps ? buf.b[lane] : 0;
-  scan(wa, wb);
-  ta = __shfl_sync(~0u, wa, 31);
-  tb = __shfl_sync(~0u, wb, 31);
-  const uint32_t pa = __shfl_sync(~0u, wa, max(warp - 1, 0)), pb = __shfl_sync(~0u, wb, max(warp - 1, 0));
-  if (warp) {
-    a = add(a, pa);
-    b = add(b, pb);
+  uint32_t w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = lane < warps ? buf.x[i][lane] : 0;
+  scan(w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    t[i] = __shfl_sync(~0u, w[i], 31);
+    const uint32_t p = __shfl_sync(~0u, w[i], max(warp - 1, 0));
+    if (warp) x[i] = add(x[i], p);
   }
 }
 
@@ -97,6 +102,28 @@ __device__ __forceinline__ int groups_of(const TablesArgs &a, int len, int end) 
   return c1 - c0 + max(0, ((end + 31) >> 5) - max(len >> 5, c1));
 }
 
+// The length that a request of n new tokens asks for: its own when it rests or cannot be
+// served whatever the others ask for (bit: why).
+__device__ __forceinline__ int asked(const TablesArgs &a, int len, int n, int &bit) {
+  bit = 0;
+  if (n <= 0) return n == -1 ? 0 : len;
+  const uint32_t grown = static_cast<uint32_t>(len) + static_cast<uint32_t>(n);
+  if (!holds(a, len))
+    bit = KVQ_DEV_INDEX;
+  else if (grown > 0x7fffffffu || pages_of(a, static_cast<int>(grown)) > a.max_pages)
+    bit = KVQ_DEV_PAGES;
+  return bit ? len : static_cast<int>(grown);
+}
+// Sums that are taken of the requests: rows, pages that come back, pages asked for, groups.
+__device__ __forceinline__ void count(const TablesArgs &a, int len, int n, int end, uint32_t (&x)[4]) {
+  x[0] = add(x[0], min(static_cast<uint32_t>(max(n, 0)), kMost));
+  if (n == -1) x[1] = add(x[1], pages_of(a, len));
+  if (end > len) {
+    x[2] = add(x[2], pages_of(a, end) - pages_of(a, len));
+    x[3] = add(x[3], groups_of(a, len, end));
+  }
+}
+
 __device__ __forceinline__ int load_entry(const TablesArgs &a, const int32_t *e) {
   return in_bounds(a.ctl, e, 4) ? *e : -1;
 }
@@ -113,7 +140,9 @@ __device__ __forceinline__ int taken_page(const TablesArgs &a, const int *backp,
 
 __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
   extern __shared__ int sm[];
-  __shared__ SumBuffer buf[3];
+  __shared__ SumBuffer<4> buf4;
+  __shared__ SumBuffer<1> buf1;
+  __shared__ SumBuffer<2> buf2;
   __shared__ int last;
   const int S = a.S;
   int *rowp = sm, *takep = rowp + S + 1, *backp = takep + S + 1, *workp = backp + S + 1;
@@ -124,8 +153,8 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
   allow_next_grid();
 
   // what each request asks for: aft[s] holds n_new until it is decided
-  uint32_t rows = 0, rows_total, back = 0, back_total;
-  int n_free = 0;
+  uint32_t x[4] = {0, 0, 0, 0}, total[4];
+  int n_free = 0, bit;
   if (in_bounds(a.ctl, a.n_free, 4)) n_free = min(max(a.n_free[0], 0), a.n_pages);
   for (int s = s0; s < s1; ++s) {
     int len = 0, n = 0;
@@ -137,70 +166,78 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a) {
     }
     bef[s] = len;
     aft[s] = n;
-    rows = add(rows, min(static_cast<uint32_t>(max(n, 0)), kMost));
-    if (n == -1) back = add(back, pages_of(a, len));
+    count(a, len, n, asked(a, len, n, bit), x);
   }
-  block_sums(rows, back, rows_total, back_total, buf[0]);
-  if (threadIdx.x == 0) {
-    rowp[S] = rows_total;
-    backp[S] = back_total;
-  }
-  uint32_t take = 0, take_total, none = 0, none_total;
-  for (int s = s0; s < s1; ++s) {
-    const int n = aft[s], len = bef[s];
-    rowp[s] = rows;
-    backp[s] = back;
-    rows = add(rows, min(static_cast<uint32_t>(max(n, 0)), kMost));
-    if (n == -1) back = add(back, pages_of(a, len));
-    if (n > 0) {
-      int bit = 0;
-      const long long grown = static_cast<long long>(len) + n;
-      if (rows > static_cast<uint32_t>(a.rows) || !holds(a, len))
-        bit = KVQ_DEV_INDEX;
-      else if (grown > 0x7fffffffLL || pages_of(a, static_cast<int>(grown)) > a.max_pages)
-        bit = KVQ_DEV_PAGES;
-      if (bit) {
-        if (blockIdx.x == 0) flag_error(a.ctl, bit);
-        aft[s] = 0;
-      } else {
-        take = add(take, pages_of(a, static_cast<int>(grown)) - pages_of(a, len));
+  block_sums(x, total, buf4);
+  const uint32_t have = min(n_free + total[1], kMost - 1);
+  int n_back = total[1], n_take = total[2], work_total = total[3];
+  if (total[0] <= static_cast<uint32_t>(a.rows) && total[2] <= have) {
+    // the usual step: there are rows and pages for all
+    for (int s = s0; s < s1; ++s) {
+      const int n = aft[s], len = bef[s], end = asked(a, len, n, bit);
+      if (bit && blockIdx.x == 0) flag_error(a.ctl, bit);
+      rowp[s] = x[0];
+      backp[s] = x[1];
+      takep[s] = x[2];
+      workp[s] = x[3];
+      count(a, len, n, end, x);
+      aft[s] = end;
+    }
+  } else {
+    uint32_t take[1] = {0}, take_total[1];
+    for (int s = s0; s < s1; ++s) {
+      const int n = aft[s], len = bef[s];
+      rowp[s] = x[0];
+      backp[s] = x[1];
+      count(a, len, n, len, x);
+      if (n > 0) {
+        const int end = asked(a, len, n, bit);
+        if (x[0] > static_cast<uint32_t>(a.rows)) bit = KVQ_DEV_INDEX;
+        if (bit) {
+          if (blockIdx.x == 0) flag_error(a.ctl, bit);
+          aft[s] = 0;
+        } else {
+          take[0] = add(take[0], pages_of(a, end) - pages_of(a, len));
+        }
       }
     }
-  }
-  // pages: served while the sum of what is asked for does not pass what there is
-  const uint32_t have = min(n_free + back_total, kMost - 1);
-  block_sums(take, none, take_total, none_total, buf[1]);
-  uint32_t served = 0, served_total, work = 0, work_total;
-  for (int s = s0; s < s1; ++s) {
-    const int n = aft[s], len = bef[s];
-    takep[s] = min(take, have);
-    int end = n == -1 ? 0 : len;
-    if (n > 0) {
-      const int need = pages_of(a, len + n) - pages_of(a, len);
-      take = add(take, need);
-      if (need > 0 && take > have) {
-        if (blockIdx.x == 0) flag_error(a.ctl, KVQ_DEV_PAGES);
-      } else {
-        end = len + n;
-        served = add(served, need);
-        work = add(work, groups_of(a, len, end));
+    // pages: served while the sum of what is asked for does not pass what there is
+    block_sums(take, take_total, buf1);
+    uint32_t y[2] = {0, 0}, served[2];  // pages, groups
+    for (int s = s0; s < s1; ++s) {
+      const int n = aft[s], len = bef[s];
+      takep[s] = min(take[0], have);
+      int end = n == -1 ? 0 : len;
+      if (n > 0) {
+        const int need = pages_of(a, len + n) - pages_of(a, len);
+        take[0] = add(take[0], need);
+        if (need > 0 && take[0] > have) {
+          if (blockIdx.x == 0) flag_error(a.ctl, KVQ_DEV_PAGES);
+        } else {
+          end = len + n;
+          y[0] = add(y[0], need);
+          y[1] = add(y[1], groups_of(a, len, end));
+        }
       }
+      aft[s] = end;
     }
-    aft[s] = end;
-  }
-  // (requests that were refused come behind the served ones in the sum of pages)
-  block_sums(served, work, served_total, work_total, buf[2]);
-  for (int s = s0; s < s1; ++s) {
-    workp[s] = work;
-    work = add(work, groups_of(a, bef[s], aft[s]));
+    // (requests that were refused come behind the served ones in the sum of pages)
+    block_sums(y, served, buf2);
+    for (int s = s0; s < s1; ++s) {
+      workp[s] = y[1];
+      y[1] = add(y[1], groups_of(a, bef[s], aft[s]));
+    }
+    n_take = served[0];
+    work_total = served[1];
   }
   if (threadIdx.x == 0) {
+    rowp[S] = total[0];
+    backp[S] = n_back;
+    takep[S] = n_take;
     workp[S] = work_total;
-    takep[S] = served_total;
   }
   __syncthreads();
-  const int n_work = min(static_cast<int>(work_total), a.cap_work);
-  const int n_back = back_total, n_take = served_total;
+  const int n_work = min(work_total, a.cap_work);
 
   // the state is read: the CTA that is the last to have done so moves it on. (Its count
   // comes back while the tables are written.)
