@@ -51,7 +51,10 @@ constexpr int kApHeads = 8;
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kRowsHeld = 192;  // rows of a slice whose lengths are held in shared memory
+// Rows whose lengths are held in shared memory: all, up to a row a thread, else the first of the
+// slice.
+constexpr int kRowsHeld = 192;
+static_assert(kRowsHeld >= kThreads);
 constexpr float kBias = 7.0f, kLazy = 4.0f;
 constexpr float kNone = -1e30f;  // a reference below every score
 // -8 as the codes are read: low nibbles 2^-24, high nibbles 2^-20
@@ -132,7 +135,8 @@ struct __align__(16) Smem {
   int valid[Cfg<D>::kStages][kConsumers];
   RowInfo row[kRowsHeld];
   long long sums[kConsumers + 1];
-  int row0, abort_flag;
+  int row0, held0;  // first row of the slice, and the first one held
+  int abort_flag;
   int quit;  // abort_flag as all consumers see it at the end of a unit
   int at0;  // items of row0 before the slice
 };
@@ -144,7 +148,7 @@ struct Walk {
 
   template <int D>
   __device__ __forceinline__ void load(const AttendPagesArgs &a, const Smem<D> &sm) {
-    const int i = row - sm.row0;
+    const int i = row - sm.held0;
     if (row >= a.rows)
       r = RowInfo{-1, -1, 0};
     else
@@ -535,6 +539,7 @@ __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm
     if (lane >= o) v += y;
   }
   if (lane == 31) sm.sums[warp] = v;
+  if (per == 1 && r0 < r1) sm.row[r0] = info;  // (all rows: no more than the threads)
   __syncthreads();
   long long base = v - mine, total = 0;
 #pragma unroll
@@ -558,11 +563,18 @@ __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm
     lo = total * c / n;
     hi = total * min(c + 1, n) / n;
   }
-  if (lo < hi && base <= lo && lo < base + mine * upr) {
+  if (per == 1) {
+    if (lo < hi && base <= lo && lo < base + mine * upr) {
+      sm.row0 = r0;
+      sm.at0 = static_cast<int>(lo - base);
+    }
+  } else if (lo < hi && base <= lo && lo < base + mine * upr) {
     for (int r = r0; r < r1; ++r) {
-      const long long n = static_cast<long long>(row_items(row_info(a, r, false))) * upr;
+      const long long n =
+          static_cast<long long>(row_items(row_info(a, r, false))) * upr;
       if (lo < base + n) {
         sm.row0 = r;
+        sm.held0 = r;
         sm.at0 = static_cast<int>(lo - base);
         break;
       }
@@ -570,12 +582,9 @@ __device__ __forceinline__ void find_slice(const AttendPagesArgs &a, Smem<D> &sm
     }
   }
   __syncthreads();
-  if (per == 1) {
-    if (lo < hi && r0 < r1 && r0 >= sm.row0) sm.row[r0 - sm.row0] = info;
-  } else if (lo < hi) {
-    for (int i = threadIdx.x; i < kRowsHeld && sm.row0 + i < a.rows; i += kThreads)
-      sm.row[i] = row_info(a, sm.row0 + i, false);
-  }
+  if (per == 1 || lo >= hi) return;
+  for (int i = threadIdx.x; i < kRowsHeld && sm.row0 + i < a.rows; i += kThreads)
+    sm.row[i] = row_info(a, sm.row0 + i, false);
   __syncthreads();
 }
 
@@ -627,15 +636,19 @@ __device__ __forceinline__ void run_loader(const AttendPagesArgs &a, Smem<D> &sm
   Walk at = {}, ahead;
   at.start(a, sm);
   ahead = at;  // this lane's item of the next eight
+  int pages = page_of(a, ahead, w), later = -1;
+  // the first item's copies are issued before the others' pages are looked up (0.5 us of a call)
+  if (lane < 4 && lo != a.ctl.drop_item) load_item(a, sm, at, pages, w, 0);
   for (int i = 0; i < (lane >> 2) && i + 1 < n_items; ++i) ahead.next(a, sm);
-  int pages = (lane >> 2) < n_items ? page_of(a, ahead, w) : -1, later = -1;
-  int k = 0;
+  if (lane >= 4) pages = (lane >> 2) < n_items ? page_of(a, ahead, w) : -1;
+  at.next(a, sm);
+  int k = 1;
   for (; k < n_items; ++k) {
     const int st = k % kStages;
-    if ((k & 7) == 0) {
-      if (k) pages = later;
+    if ((k & 7) == 0) pages = later;
+    if ((k & 7) == 3) {  // (not before the first stages are on their way: 1.5 us of a call)
       later = -1;
-      if (k + 8 + (lane >> 2) < n_items) {
+      if (k + 5 + (lane >> 2) < n_items) {
         for (int i = 0; i < 8; ++i) ahead.next(a, sm);
         later = page_of(a, ahead, w);
       }
@@ -777,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
       mbar_init(smem_u32(&sm.empty[s]), kConsumers);
     }
     sm.abort_flag = 0;
-    sm.row0 = sm.at0 = 0;
+    sm.row0 = sm.held0 = sm.at0 = 0;
     fence_mbar_init();
   }
   wait_prior_grid();
