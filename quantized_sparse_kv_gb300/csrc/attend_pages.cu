@@ -596,10 +596,26 @@ __device__ __forceinline__ int page_of(const AttendPagesArgs &a, const Walk &at,
   return in_bounds(a.ctl, e, 4) ? *e : -1;
 }
 
+// bulk_g2s of what is read once: such lines leave the L2 first (1.1 to 1.5 us of a call of 84 MB
+// and more; no change where several units read the same bytes and for one short request).
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_g2s_policy(uint32_t dst, const void *src, uint32_t bytes,
+                                                uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], "
+      "%2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // Lane w's share of an item into a stage.
 template <int D>
 __device__ __forceinline__ void load_item(const AttendPagesArgs &a, Smem<D> &sm, const Walk &at,
-                                          int page, int w, int st) {
+                                          int page, int w, int st, uint64_t policy) {
   const uint32_t dst = smem_u32(sm.stage[st]), bar = smem_u32(&sm.full[st]);
   const int kvh = at.hc / a.chunks;
   int valid = 0;
@@ -625,7 +641,7 @@ __device__ __forceinline__ void load_item(const AttendPagesArgs &a, Smem<D> &sm,
   if (bytes && !in_bounds(a.ctl, src, bytes)) bytes = valid = 0;
   sm.valid[st][w] = valid;
   mbar_arrive_expect_tx(bar, bytes);
-  if (bytes) bulk_g2s(dst + w * Cfg<D>::kRecord, src, bytes, bar);
+  if (bytes) bulk_g2s_policy(dst + w * Cfg<D>::kRecord, src, bytes, bar, policy);
 }
 
 template <int D>
@@ -633,12 +649,13 @@ __device__ __forceinline__ void run_loader(const AttendPagesArgs &a, Smem<D> &sm
                                            int n_items, int lane) {
   constexpr int kStages = Cfg<D>::kStages;
   const int w = lane & 3;
+  const uint64_t policy = read_once_policy();
   Walk at = {}, ahead;
   at.start(a, sm);
   ahead = at;  // this lane's item of the next eight
   int pages = page_of(a, ahead, w), later = -1;
   // the first item's copies are issued before the others' pages are looked up (0.5 us of a call)
-  if (lane < 4 && lo != a.ctl.drop_item) load_item(a, sm, at, pages, w, 0);
+  if (lane < 4 && lo != a.ctl.drop_item) load_item(a, sm, at, pages, w, 0, policy);
   for (int i = 0; i < (lane >> 2) && i + 1 < n_items; ++i) ahead.next(a, sm);
   if (lane >= 4) pages = (lane >> 2) < n_items ? page_of(a, ahead, w) : -1;
   at.next(a, sm);
@@ -664,7 +681,7 @@ __device__ __forceinline__ void run_loader(const AttendPagesArgs &a, Smem<D> &sm
       }
     }
     if (__any_sync(~0u, !go || aborted(sm))) break;
-    if (lane < 4 && lo + k != a.ctl.drop_item) load_item(a, sm, at, page, w, st);
+    if (lane < 4 && lo + k != a.ctl.drop_item) load_item(a, sm, at, page, w, st, policy);
     at.next(a, sm);
   }
   // copies still in flight must land before the CTA ends
