@@ -35,10 +35,11 @@
 // down to 2^-17 of the largest, whatever the magnitude of V (scales that fp16 would not
 // hold well give a power of two to P).
 //
-// 64 requests of 16 to 32 thousand tokens, 16 heads over 2 (510 MB): 94 us, 5.4 TB/s, of which
-// 2.2 us until a CTA has its slice, 6 until its first item, 6.1 TB/s then (the copies without
-// the arithmetic 6.7), 10 between the first CTA's end and the last's, 4 the join. One request
-// of 700 tokens: 9.1 us.
+// 64 requests of 16 to 32 thousand tokens, 16 heads over 2 (510 MB): 90.7 us, 5.6 TB/s, of which
+// 1.5 us until a CTA has its slice, 3.8 until its first item, 6.5 TB/s then until the first
+// CTAs end; 10 lie between the mean and the last CTA's end (the first CTA of an SM is
+// ahead of its third), 3 are the join. One request of 700 tokens: 8.5 us. D = 64 is bound by the
+// MMAs and their operands (336 MB: 84 us; with four CTAs per SM 87, with five 107).
 #include <algorithm>
 
 #include "int4_dequant.cuh"
