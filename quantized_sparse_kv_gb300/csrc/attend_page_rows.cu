@@ -4,11 +4,14 @@
 //
 // A CTA takes one query row, up to eight query heads of one KV head and an equal share of
 // the row's 32-token groups; each group's keys and values are staged in shared memory as
-// floats. Warp h scores head h (lane = token) and keeps its running maximum and sum; then
-// every thread adds the group's values to its elements of the output. A second kernel
-// merges the shares' partial results. Codes are decoded a word of eight at a time (element by
-// element 4.3 ms instead of 2.1): 64 requests of 24 thousand tokens, 16 heads over 2, D = 128,
-// fp32 windows, 2.1 ms (84 us for as many on the tensor cores).
+// floats, a word of eight codes at a time. A warp has an eighth of the channels of all
+// scores (lane = token), so that K is read once for the heads; the parts meet in shared
+// memory, where warp h takes head h's maximum and sum. A warp then has four of the tokens
+// of the output, all heads in registers over all groups, and the warps' sums meet at the end. A
+// second kernel merges the shares, a lane a share. The fp32 products and the latency
+// of the staging at 16 warps per SM bound it: 64 requests of 24 thousand tokens, 16 heads over 2,
+// D = 128, fp32 windows: 1.74 ms (codes one by one and K read by every head 4.3; the tensor
+// cores, with bf16 windows, 0.09); 8 of 8 thousand, D = 256: 174 us (573).
 #include <math_constants.h>
 
 #include <algorithm>
@@ -19,7 +22,10 @@ namespace kvq {
 namespace {
 
 constexpr int kPrThreads = 256;
+constexpr int kPrWarps = kPrThreads / 32;
 constexpr int kPrHeads = 8;
+constexpr int kPrSplits = 64;  // shares of a row at most: two a lane of the merge
+static_assert(kPrHeads <= kPrWarps);
 
 struct PageRowsArgs {
   PagedDims d;
@@ -83,23 +89,35 @@ __device__ __forceinline__ void stage_group(const PageRowsArgs &a, const uint8_t
     o[0] = make_float4(code(0) * x.x, code(1) * x.z, code(2) * y.x, code(3) * y.z);
     o[1] = make_float4(code(4) * x.y, code(5) * x.w, code(6) * y.y, code(7) * y.w);
   }
-  for (int i = threadIdx.x; i < 4 * D; i += kPrThreads) {
-    const int lane = i >> cl & 31, mf = i >> (cl + 5), m = mf / fw;
-    const int f = ((mf - m * fw) << cl) + (i & ((1 << cl) - 1));
-    const int x = 16 * m + 2 * (lane & 3), y = 16 * f + (lane >> 2);
-    const uint32_t w = vw[i];
-    const float2 sa = *reinterpret_cast<const float2 *>(vscale + vscale_at(x, f >> 1, D));
-    const float2 sb = *reinterpret_cast<const float2 *>(vscale + vscale_at(x + 8, f >> 1, D));
-    const auto code = [w](int j) { return static_cast<float>(static_cast<int>(w >> (4 * j) & 15) - 8); };
-    float *o = vs + x * ld + y;
-    o[0] = code(0) * sa.x;
-    o[8] = code(2) * sa.x;
-    o[8 * ld] = code(1) * sb.x;
-    o[8 * ld + 8] = code(3) * sb.x;
-    o[ld] = code(4) * sa.y;
-    o[ld + 8] = code(6) * sa.y;
-    o[9 * ld] = code(5) * sb.y;
-    o[9 * ld + 8] = code(7) * sb.y;
+  // (a lane takes the words it has side by side: stores of a warp fall into 32 banks)
+  for (int i = threadIdx.x; i < 4 * D >> cl; i += kPrThreads) {
+    const int lane = i & 31, mf = i >> 5, m = mf / fw, f0 = (mf - m * fw) << cl;
+    const int x = 16 * m + 2 * (lane & 3);
+    uint32_t w[4];
+    if (cl == 2) {
+      const uint4 u = reinterpret_cast<const uint4 *>(vw)[i];
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = reinterpret_cast<const uint2 *>(vw)[i];
+      w[0] = u.x, w[1] = u.y, w[2] = w[3] = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= 1 << cl) break;
+      const int f = f0 + k;
+      const float2 sa = *reinterpret_cast<const float2 *>(vscale + vscale_at(x, f >> 1, D));
+      const float2 sb = *reinterpret_cast<const float2 *>(vscale + vscale_at(x + 8, f >> 1, D));
+      const auto code = [&](int j) { return static_cast<float>(static_cast<int>(w[k] >> (4 * j) & 15) - 8); };
+      float *o = vs + x * ld + 16 * f + (lane >> 2);
+      o[0] = code(0) * sa.x;
+      o[8] = code(2) * sa.x;
+      o[8 * ld] = code(1) * sb.x;
+      o[8 * ld + 8] = code(3) * sb.x;
+      o[ld] = code(4) * sa.y;
+      o[ld + 8] = code(6) * sa.y;
+      o[9 * ld] = code(5) * sb.y;
+      o[9 * ld + 8] = code(7) * sb.y;
+    }
   }
 }
 
@@ -144,13 +162,15 @@ __device__ __forceinline__ void stage_tile(const PageRowsArgs &a, size_t tile, f
   }
 }
 
-__global__ void __launch_bounds__(kPrThreads) page_rows_kernel(const PageRowsArgs a) {
+// kCols: float4 columns of the output a lane has (2 for D > 128).
+template <int kCols>
+__global__ void __launch_bounds__(kPrThreads, 2) page_rows_kernel(const PageRowsArgs a) {
   extern __shared__ __align__(16) float sm[];
   wait_prior_grid();
   allow_next_grid();
   const int D = a.d.D, ld = D + 4, gl = a.d.gpp_log2();
   float *ks = sm, *vs = ks + 32 * ld, *qs = vs + 32 * ld, *ps = qs + kPrHeads * D;
-  float *corr = ps + kPrHeads * 32;
+  float *red = ps + kPrHeads * 32, *corr = red + kPrWarps * kPrHeads * 32;
   const int row = blockIdx.x, hc = blockIdx.y, kvh = hc / a.chunks, chunk = hc % a.chunks;
   const int h0 = kvh * a.G + kPrHeads * chunk, nh = min(kPrHeads, a.G - kPrHeads * chunk);
   int s;
@@ -167,12 +187,13 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_kernel(const PageRowsArg
                             : bf16_to_f32(static_cast<const uint16_t *>(a.q)[e]);
     qs[i] = x * a.scale_log2;
   }
-  // a thread's output: features 4 c .. 4 c + 3 of head `slot`, and of the one `slots` behind it
-  const int cols = D / 4, slots = kPrThreads / cols, slot = threadIdx.x / cols;
-  const int c = threadIdx.x - slot * cols;
-  float acc[2][4];
+  // of the tokens 4 warp .. 4 warp + 3 of every group: features 4 (lane + 32 k) and on
+  const int cols = D / 4;
+  float acc[kCols][kPrHeads][4];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
+  for (int k = 0; k < kCols; ++k)
+#pragma unroll
+    for (int h = 0; h < kPrHeads; ++h) acc[k][h][0] = acc[k][h][1] = acc[k][h][2] = acc[k][h][3] = 0.0f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float m = -CUDART_INF_F, l = 0.0f;
   for (int g = g0; g < g1; ++g) {
@@ -202,19 +223,31 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_kernel(const PageRowsArg
     else
       stage_tile<uint16_t>(a, tile, ks, vs, ld);
     __syncthreads();
-    if (warp < nh) {
-      const float4 *q4 = reinterpret_cast<const float4 *>(qs + warp * D);
+    {  // a warp's eighth of the channels of every score; lane = token
+      float x[kPrHeads];
+#pragma unroll
+      for (int h = 0; h < kPrHeads; ++h) x[h] = 0.0f;
+      const int c0 = warp * (cols / kPrWarps);
       const float4 *k4 = reinterpret_cast<const float4 *>(ks + lane * ld);
-      float x0 = 0.0f, x1 = 0.0f, x2 = 0.0f, x3 = 0.0f;
-#pragma unroll 8
-      for (int d = 0; d < cols; ++d) {
-        const float4 q = q4[d], k = k4[d];
-        x0 = fmaf(q.x, k.x, x0);
-        x1 = fmaf(q.y, k.y, x1);
-        x2 = fmaf(q.z, k.z, x2);
-        x3 = fmaf(q.w, k.w, x3);
+      const float4 *q4 = reinterpret_cast<const float4 *>(qs);
+      for (int d = c0; d < c0 + cols / kPrWarps; ++d) {
+        const float4 k = k4[d];
+#pragma unroll
+        for (int h = 0; h < kPrHeads; ++h) {
+          if (h >= nh) break;
+          const float4 q = q4[h * cols + d];
+          x[h] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, x[h]))));
+        }
       }
-      float x = (x0 + x1) + (x2 + x3);
+#pragma unroll
+      for (int h = 0; h < kPrHeads; ++h)
+        if (h < nh) red[(warp * kPrHeads + h) * 32 + lane] = x[h];
+    }
+    __syncthreads();
+    if (warp < nh) {  // a head's scores; lane = token
+      float x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kPrWarps; ++w) x += red[(w * kPrHeads + warp) * 32 + lane];
       if (lane >= valid) x = -CUDART_INF_F;
       const float mx = fmaxf(m, warp_max(x));
       const float ref = mx == -CUDART_INF_F ? 0.0f : mx;
@@ -225,51 +258,61 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_kernel(const PageRowsArg
       if (lane == 0) corr[warp] = f;
     }
     __syncthreads();
+    float4 p[kPrHeads];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int h = slot + k * slots;
-      if (slot >= slots || h >= nh) break;
+    for (int h = 0; h < kPrHeads; ++h) {
+      if (h >= nh) break;
+      p[h] = *reinterpret_cast<const float4 *>(ps + h * 32 + 4 * warp);
       const float f = corr[h];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) acc[k][z] *= f;
-      const float *ph = ps + h * 32, *v0 = vs + 4 * c;
-      const auto add = [&](float p, int r) {
-        const float4 v = *reinterpret_cast<const float4 *>(v0 + r * ld);
-        acc[k][0] = fmaf(p, v.x, acc[k][0]);
-        acc[k][1] = fmaf(p, v.y, acc[k][1]);
-        acc[k][2] = fmaf(p, v.z, acc[k][2]);
-        acc[k][3] = fmaf(p, v.w, acc[k][3]);
-      };
-      int r = 0;
-      for (; r + 4 <= valid; r += 4) {
-        const float4 p = *reinterpret_cast<const float4 *>(ph + r);
-        add(p.x, r);
-        add(p.y, r + 1);
-        add(p.z, r + 2);
-        add(p.w, r + 3);
+      for (int k = 0; k < kCols; ++k)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) acc[k][h][z] *= f;
+    }
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+      if (lane + 32 * k >= cols) break;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int r = 4 * warp + t;
+        if (r >= valid) break;  // (what is staged there may be anything)
+        const float4 v = *reinterpret_cast<const float4 *>(vs + r * ld + 4 * (lane + 32 * k));
+#pragma unroll
+        for (int h = 0; h < kPrHeads; ++h) {
+          if (h >= nh) break;
+          const float y = t == 0 ? p[h].x : t == 1 ? p[h].y : t == 2 ? p[h].z : p[h].w;
+          acc[k][h][0] = fmaf(y, v.x, acc[k][h][0]);
+          acc[k][h][1] = fmaf(y, v.y, acc[k][h][1]);
+          acc[k][h][2] = fmaf(y, v.z, acc[k][h][2]);
+          acc[k][h][3] = fmaf(y, v.w, acc[k][h][3]);
+        }
       }
-      for (; r < valid; ++r) add(ph[r], r);
     }
   }
-  if (a.splits == 1) {  // the row's only share
-    __syncthreads();
-    if (warp < nh && lane == 0) corr[warp] = l == 0.0f ? 0.0f : 1.0f / l;
-    __syncthreads();
+  // the warps' sums meet in the space of K and V, [warp][head][D]
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    if (lane + 32 * k >= cols) break;
+#pragma unroll
+    for (int h = 0; h < kPrHeads; ++h)
+      if (h < nh)
+        *reinterpret_cast<float4 *>(sm + (warp * kPrHeads + h) * D + 4 * (lane + 32 * k)) =
+            make_float4(acc[k][h][0], acc[k][h][1], acc[k][h][2], acc[k][h][3]);
   }
+  if (warp < nh && lane == 0) corr[warp] = l == 0.0f ? 0.0f : 1.0f / l;
+  __syncthreads();
   float *part = part_of(a, row, hc, blockIdx.z);
   if (a.splits > 1 && !in_bounds(a.ctl, part, sizeof(float) * kPrHeads * (D + 2))) return;
+  for (int i = threadIdx.x; i < nh * D; i += kPrThreads) {
+    float y = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int h = slot + k * slots;
-    if (slot >= slots || h >= nh) break;
-#pragma unroll
-    for (int z = 0; z < 4; ++z) {
-      const int d = 4 * c + z;
-      if (a.splits == 1)
-        store_out(a, (static_cast<size_t>(row) * a.Hq + h0 + h) * D + d, acc[k][z] * corr[h]);
-      else
-        part[h * (D + 2) + d] = acc[k][z];
-    }
+    for (int w = 0; w < kPrWarps; ++w) y += sm[w * kPrHeads * D + i];
+    const int h = i / D;
+    if (a.splits == 1)  // the row's only share
+      store_out(a, (static_cast<size_t>(row) * a.Hq + h0) * D + i, y * corr[h]);
+    else
+      part[h * (D + 2) + i - h * D] = y;
   }
   if (a.splits > 1 && warp < nh && lane == 0) {
     part[warp * (D + 2) + D] = m;
@@ -286,23 +329,41 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_combine_kernel(const Pag
   int s;
   const int n = row_tokens(a, row, s, false);
   if (n < 0) return;
+  __shared__ float weight[kPrHeads][kPrSplits], inv[kPrHeads];
+  const float *p = part_of(a, row, hc, 0);
+  const size_t step = kPrHeads * (D + 2);
+  if (!in_bounds(a.ctl, p, sizeof(float) * a.splits * step)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < nh) {  // a head's weights; lane = share
+    const float *ph = p + warp * (D + 2) + D;
+    float pm[2], pl[2], mx = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int z = lane + 32 * k;
+      pm[k] = z < a.splits ? ph[z * step] : -CUDART_INF_F;
+      pl[k] = z < a.splits ? ph[z * step + 1] : 0.0f;
+      mx = fmaxf(mx, pm[k]);
+    }
+    mx = warp_max(mx);
+    if (mx == -CUDART_INF_F) mx = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // (a share without keys has m = -inf and weight 0; one of NaN scores keeps its NaN)
+      const float c = pl[k] != pl[k] ? pl[k] : exp2f(pm[k] - mx);
+      weight[warp][lane + 32 * k] = c;
+      l += c * pl[k];
+    }
+    l = warp_sum(l);
+    if (lane == 0) inv[warp] = l == 0.0f ? 0.0f : 1.0f / l;
+  }
+  __syncthreads();
   for (int i = threadIdx.x; i < nh * D; i += kPrThreads) {
     const int h = i / D, d = i - h * D;
-    const float *p = part_of(a, row, hc, 0) + h * (D + 2);
-    const size_t step = kPrHeads * (D + 2);
-    if (!in_bounds(a.ctl, p, sizeof(float) * ((a.splits - 1) * step + D + 2))) return;
-    float m = -CUDART_INF_F;
-    for (int z = 0; z < a.splits; ++z) m = fmaxf(m, p[z * step + D]);
-    if (m == -CUDART_INF_F) m = 0.0f;
-    float y = 0.0f, l = 0.0f;
-    for (int z = 0; z < a.splits; ++z) {
-      // (a share without keys has m = -inf and weight 0; one of NaN scores keeps its NaN)
-      const float c = exp2f(p[z * step + D] - m), lz = p[z * step + D + 1];
-      y += lz != lz ? lz : c * p[z * step + d];
-      l += lz != lz ? lz : c * lz;
-    }
-    y = l == 0.0f ? 0.0f : y / l;
-    store_out(a, (static_cast<size_t>(row) * a.Hq + h0) * D + i, y);
+    const float *pd = p + h * (D + 2) + d;
+    float y = 0.0f;
+#pragma unroll 16
+    for (int z = 0; z < a.splits; ++z) y = fmaf(weight[h][z], pd[z * step], y);
+    store_out(a, (static_cast<size_t>(row) * a.Hq + h0) * D + i, y * inv[h]);
   }
 }
 
@@ -310,7 +371,7 @@ __global__ void __launch_bounds__(kPrThreads) page_rows_combine_kernel(const Pag
 int row_splits(const PagedDims &d, int Hq, int rows, int num_sms) {
   const int chunks = (Hq / d.Hkv + kPrHeads - 1) / kPrHeads;
   const long units = static_cast<long>(rows) * d.Hkv * chunks;
-  return static_cast<int>(std::max<long>(1, std::min<long>(64, 4L * num_sms / std::max(1L, units))));
+  return static_cast<int>(std::max<long>(1, std::min<long>(kPrSplits, 4L * num_sms / std::max(1L, units))));
 }
 
 }  // namespace
@@ -340,10 +401,12 @@ int launch_page_rows(const PagedDims &d, const void *q, int q_dt, int Hq, int ro
   a.chunks = (a.G + kPrHeads - 1) / kPrHeads;
   a.splits = row_splits(d, Hq, rows, num_sms);
   a.ctl = ctl;
-  const size_t smem = sizeof(float) * (64 * (static_cast<size_t>(d.D) + 4) + kPrHeads * (d.D + 33));
-  opt_in_smem(page_rows_kernel, smem);
+  const size_t smem = sizeof(float) * (64 * (static_cast<size_t>(d.D) + 4) + kPrHeads * (d.D + 33) +
+                                       32 * kPrWarps * kPrHeads);
+  auto *const kernel = d.D > 128 ? page_rows_kernel<2> : page_rows_kernel<1>;
+  opt_in_smem(kernel, smem);
   const dim3 grid(rows, d.Hkv * a.chunks, a.splits);
-  launch_dependent(page_rows_kernel, grid, dim3(kPrThreads), smem, s, a);
+  launch_dependent(kernel, grid, dim3(kPrThreads), smem, s, a);
   if (a.splits == 1) return 1;
   launch_dependent(page_rows_combine_kernel, dim3(rows, d.Hkv * a.chunks), dim3(kPrThreads), 0, s,
                    a);

@@ -314,3 +314,29 @@ def test_waits_that_run_out_at_any_item_end_the_call(kvq):  # noqa: F811
     for i in (0, 1, rows - 1):
         want = attention64(q[i].double().cpu().numpy(), *values)
         assert O.rel_l2(got[i].double().cpu().numpy(), want) <= TOL_TENSOR
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("rows,group", [(2, 1), (2, 11), (700, 3)])
+def test_the_fp32_kernel_at_every_head_dim(kvq, d, rows, group):  # noqa: F811
+    # few rows share a request's groups among CTAs, many have one each; the last row of a
+    # request is NaN and is attended by the first query row alone
+    gen = torch.Generator(device="cuda").manual_seed(d + rows)
+    n = 391
+    k = torch.randn((n, 2, d), generator=gen, device="cuda")
+    v = torch.randn((n, 2, d), generator=gen, device="cuda")
+    v[n - 1] = float("nan")
+    cache, (kk, vv) = one_request(kvq, n, k, v, 50, 2, d, "f32", 32)
+    q = torch.randn((rows, 2 * group, d), generator=gen, device="cuda")
+    pos = torch.randint(0, n - 1, (rows,), generator=gen, device="cuda").int()
+    pos[0], pos[1] = n - 1, n - 2
+    slot = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    call = kvq.AttendPages(cache, q, slot, pos)
+    got = call.run().double().cpu().numpy()
+    assert kvq.read_status(call.status) == 0 and call.path == "pages_rows"
+    assert np.isnan(got[0]).all() and not np.isnan(got[1:]).any()
+    for i in {1, rows // 2, rows - 1}:
+        p = int(pos[i]) + 1
+        want = attention64(q[i].double().cpu().numpy(), kk[:, :p], vv[:, :p])
+        assert O.rel_l2(got[i], want) <= TOL_F32
