@@ -639,19 +639,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
     int j = lo + k - u * a.ipu;                        // item index within unit u
     bool aborted = false;
     for (; k < u_end; ++k, ++j) {
-      if (aborted_flag(sm)) {
-        aborted = true;
-        break;
-      }
       const int s = k % kStages;
-      if (!mbar_wait(smem_u32(&sm.full[s]), static_cast<uint32_t>((k / kStages) & 1),
-                     a.ctl.wait_limit_ns)) {
-        if (lane == 0) {
-          flag_error(a.ctl, KVQ_DEV_TIMEOUT);
-          *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+      const uint32_t bar = smem_u32(&sm.full[s]), par = static_cast<uint32_t>((k / kStages) & 1);
+      if (!__all_sync(0xffffffffu, mbar_try_wait(bar, par))) {
+        // (each lane's clock ends its own wait: the warp answers as one)
+        const bool stop = aborted_flag(sm) || !mbar_wait(bar, par, a.ctl.wait_limit_ns);
+        if (__any_sync(0xffffffffu, stop)) {
+          if (lane == 0) {
+            flag_error(a.ctl, KVQ_DEV_TIMEOUT);
+            *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+          }
+          aborted = true;
+          break;
         }
-        aborted = true;
-        break;
       }
       const uint8_t *stg = sm.stage[s];
       if (j < a.Gi) {
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32));
     }
-    if (aborted || aborted_flag(sm)) {
+    if (__any_sync(0xffffffffu, aborted || aborted_flag(sm))) {
       // Another warp may have looked before the flag was set and go on to the next unit:
       // it finds this one at the barriers of every unit left (five each).
       for (++u; u * a.ipu < hi; ++u)
