@@ -58,6 +58,15 @@ int launch_pack(const void *k, const void *v, int in_dtype, const kvq_cache &c,
 // tokens become int4 and the window becomes R_new rows.
 int launch_append(const kvq_cache &c, const void *k_new, const void *v_new, int in_dtype,
                   int n_new, int m, int R_new, const KernelCtl &ctl, cudaStream_t s);
+// Its CTAs: a thread per channel pair and slice of a group's 32 tokens, in as many equal
+// slices as there are threads for (a power of two; with 48, 80, 96 or 112 pairs some
+// threads have none).
+constexpr int kAppendThreads = 256;
+__host__ __device__ constexpr int append_slices(int D) {
+  int n = 1;
+  while (n * D <= kAppendThreads) n *= 2;
+  return n;
+}
 
 // attend_generic.cu: fp32 CUDA-core attention for any supported shape.
 int launch_attend_generic(const kvq_cache &c, const void *q, int q_dtype, int Hq, int n_q,

@@ -697,7 +697,6 @@ __device__ __forceinline__ void seq8(const AppendArgs &a, const void *win, const
   for (int e = 0; e < 8; ++e) x[e] = 0.0f;
 }
 
-constexpr int kAppendThreads = 256;
 // 8-element pieces of a 32-token group per thread: 32 * D / 8 / 256, D <= 256
 constexpr int kStagePieces = 4;
 
@@ -740,11 +739,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_migrate_kernel(const Ap
   __syncthreads();
   // K: thread (pair p, slice q) takes channels 2p, 2p + 1 over tokens
   // q * tq .. q * tq + tq - 1; the per-channel maxima meet in shared memory.
+  // (Threads behind the last slice have no tokens.)
   __shared__ float2 kmax[kAppendThreads];
-  const int np = D / 2, nq = kAppendThreads / np, tq = kGroup / nq;
+  const int np = D / 2, nq = append_slices(D), tq = kGroup / nq;
   const int p = threadIdx.x % np, q = threadIdx.x / np;
+  const int t1 = q < nq ? q * tq + tq : 0;
   float a0 = 0.0f, a1 = 0.0f;
-  for (int t = q * tq; t < q * tq + tq; ++t) {
+  for (int t = q * tq; t < t1; ++t) {
     a0 = fmaxf(a0, fabsf(xs[t * ld + 2 * p]));
     a1 = fmaxf(a1, fabsf(xs[t * ld + 2 * p + 1]));
   }
@@ -759,7 +760,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_migrate_kernel(const Ap
     a.k_scales[grp * D + 2 * p] = s0;
     a.k_scales[grp * D + 2 * p + 1] = s1;
   }
-  for (int t = q * tq; t < q * tq + tq; ++t)
+  for (int t = q * tq; t < t1; ++t)
     if (in_bounds(a.ctl, a.k_codes + (grp * kGroup + t) * (D / 2) + p, 1))
       a.k_codes[(grp * kGroup + t) * (D / 2) + p] = static_cast<uint8_t>(
         (int4_code(xs[t * ld + 2 * p], s0) + 8) | ((int4_code(xs[t * ld + 2 * p + 1], s1) + 8) << 4));
