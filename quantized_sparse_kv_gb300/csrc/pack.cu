@@ -345,7 +345,7 @@ __device__ __forceinline__ void pack_v_tile(const uint8_t *tile, int vw, int lan
     m[i] = max_bf16x2(max_bf16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
                       max_bf16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
   const uint32_t mm = max_bf16x2(max_bf16x2(m[0], m[1]), max_bf16x2(m[2], m[3]));
-  const float amax = fmaxf(bf_lo(mm), bf_hi(mm));
+  const float amax = fmaxf(fmaxf(bf_lo(mm), bf_hi(mm)), 0.0f);  // (of NaNs alone: 0)
   const long row = row0 + t;
   uint8_t *dst = v_codes + row * 64 + 16 * j;
   float *scale = v_scales + row * 4 + j;

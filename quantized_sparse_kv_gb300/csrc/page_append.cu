@@ -245,8 +245,8 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
     uint32_t m = x[0].w;
 #pragma unroll
     for (int t = 1; t < 32; ++t) m = max_abs2(m, x[t].w);
-    a0 = fabsf(bf_lo(m));
-    a1 = fabsf(bf_hi(m));
+    a0 = fmaxf(fabsf(bf_lo(m)), 0.0f);  // (of NaNs alone: 0)
+    a1 = fmaxf(fabsf(bf_hi(m)), 0.0f);
   } else {
     a0 = a1 = 0.0f;
 #pragma unroll
@@ -353,8 +353,8 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
       }
     }
     if (n == e) {
-      m0 = fabsf(u);
-      m1 = fabsf(v);
+      m0 = fmaxf(fabsf(u), 0.0f);  // (of NaNs alone: 0)
+      m1 = fmaxf(fabsf(v), 0.0f);
     }
   }
   // (the eight lanes of a token have all of its tokens' maxima between them)
