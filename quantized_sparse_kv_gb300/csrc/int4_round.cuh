@@ -100,30 +100,43 @@ __host__ __device__ __forceinline__ bool code8_clear(float x, float r, uint32_t 
   return fabsf(add_rn(q, -add_rn(y, -12582920.0f))) < 0.499995f;
 }
 
-// One code byte from a pair of bf16 values (the low half of w in the low
-// nibble), each with its own scale: on the device the four operations run
-// on both halves at once as packed f32x2 instructions (per half the same
-// IEEE operations); ns = -s.
-__host__ __device__ __forceinline__ uint32_t code_byte_recip(uint32_t w, float ns_lo, float ns_hi,
-                                                             float r_lo, float r_hi) {
-  uint32_t lo_bits = w << 16, hi_bits = w & 0xffff0000u;
+__host__ __device__ __forceinline__ uint64_t pair64(float lo, float hi) {
 #ifdef __CUDA_ARCH__
-  uint64_t x, ns, r, q0, e, q, y;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo_bits), "r"(hi_bits));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(ns) : "f"(ns_lo), "f"(ns_hi));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r_lo), "f"(r_hi));
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
+#else
+  return static_cast<uint64_t>(bits_of(hi)) << 32 | bits_of(lo);
+#endif
+}
+
+// One code byte, in bits 0-7 of the result, from the bits of two floats (lo in the low nibble),
+// each with its own scale; ns = (-s_lo, -s_hi) and r = (r_lo, r_hi) as pair64. On the device
+// the four operations run on both at once as packed f32x2 instructions (per half the same IEEE
+// operations). The low half is masked: a NaN's sum has every bit set, and would borrow from
+// the high nibble.
+__host__ __device__ __forceinline__ uint32_t code_byte_pair(uint32_t lo, uint32_t hi, uint64_t ns,
+                                                            uint64_t r) {
+#ifdef __CUDA_ARCH__
+  uint64_t x, q0, e, q, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo), "r"(hi));
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(x), "l"(r));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q0), "l"(ns), "l"(x));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q0));
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(q), "l"(0x4B4000084B400008ull));
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo_bits), "=r"(hi_bits) : "l"(y));
-  return hi_bits * 16u + lo_bits;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y));
 #else
-  float lo, hi;
-  memcpy(&lo, &lo_bits, 4);
-  memcpy(&hi, &hi_bits, 4);
-  return (code8_recip(hi, -ns_hi, r_hi) * 16u + code8_recip(lo, -ns_lo, r_lo)) & 0xffu;
+  const auto sum = [](uint32_t x, uint32_t s, uint32_t i) {
+    float f[3];
+    const uint32_t u[3] = {x, s ^ 0x80000000u, i};
+    memcpy(f, u, 12);
+    const uint32_t y = code8_recip(f[0], f[1], f[2]);
+    return (y & 0x7fffffffu) > 0x7f800000u ? 0x7fffffffu : y;  // the device's NaN
+  };
+  lo = sum(lo, static_cast<uint32_t>(ns), static_cast<uint32_t>(r));
+  hi = sum(hi, static_cast<uint32_t>(ns >> 32), static_cast<uint32_t>(r >> 32));
 #endif
+  return hi * 16u + (lo & 15u);
 }
 
 }  // namespace kvq

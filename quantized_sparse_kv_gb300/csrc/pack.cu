@@ -297,12 +297,12 @@ __device__ __forceinline__ void pack_k_quarter(const uint8_t *tile, int kw, int 
     return;
   }
   const float s0 = scale_recip(a0), s1 = scale_recip(a1);
-  const float r0 = recip_of(s0), r1 = recip_of(s1);
+  const uint64_t ns = pair64(-s0, -s1), r = pair64(recip_of(s0), recip_of(s1));
   if (h == 0 && in_bounds(ctl, scales, 2 * sizeof(float)))
     *reinterpret_cast<float2 *>(scales) = make_float2(s0, s1);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint32_t b = code_byte_recip(x[i], -s0, -s1, r0, r1);
+    const uint32_t b = code_byte_pair(x[i] << 16, x[i] & 0xffff0000u, ns, r);
     if (in_bounds(ctl, dst + i * 64, 1)) dst[i * 64] = static_cast<uint8_t>(b);
   }
 }
@@ -353,14 +353,15 @@ __device__ __forceinline__ void pack_v_tile(const uint8_t *tile, int vw, int lan
     pack_v_group_div(src, amax, t < valid, dst, scale, ctl);
     return;
   }
-  const float s = scale_recip(amax), r = recip_of(s);
+  const float s = scale_recip(amax);
+  const uint64_t ns = pair64(-s, -s), r = pair64(recip_of(s), recip_of(s));
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
     uint32_t b[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) b[q] = code_byte_recip(e[q], -s, -s, r, r);
+    for (int q = 0; q < 4; ++q) b[q] = code_byte_pair(e[q] << 16, e[q] & 0xffff0000u, ns, r);
     o[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
   // o[i] holds 16-byte piece (i + rot) & 3: rotate back by rot

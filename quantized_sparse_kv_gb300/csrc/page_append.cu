@@ -18,7 +18,7 @@
 // copy. All of a thread's loads are issued before the first is used, and 16 CTAs share an
 // SM at 64 registers.
 //
-// 112,000 rows of two heads, D = 128 (151 MB in and out): 33.9 us, 4.5 TB/s; the loads of
+// 112,000 rows of two heads, D = 128 (151 MB in and out): 34.6 us, 4.4 TB/s; the loads of
 // 32 warps an SM and 1.3 thousand instructions a half group, half of the issue slots, overlap
 // in part. Rows staged in shared memory a group ahead (49 us, 42 without as it was then), 16
 // values a thread (38) and 80 registers (56) were slower. One token of each of 64 requests:
@@ -70,23 +70,6 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// code_byte_recip of two bf16 values given as floats' bits, scales as (negated, reciprocal).
-__device__ __forceinline__ uint32_t code_byte_of(uint32_t lo, uint32_t hi, uint64_t ns, uint64_t r) {
-  uint64_t x, q0, e, q, y;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo), "r"(hi));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(x), "l"(r));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q0), "l"(ns), "l"(x));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q0));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(q), "l"(0x4B4000084B400008ull));
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y));
-  return hi * 16u + lo;
-}
-__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
-  uint64_t x;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
-  return x;
-}
-
 // A pair of values as the cache keeps them: bf16 pairs in one register.
 struct PairB {
   uint32_t w;
@@ -267,7 +250,7 @@ __device__ __forceinline__ void pack_k(const AppendPagesArgs &a, const GroupWork
 #pragma unroll
       for (int t = 0; t < 32; ++t)
         rec[t * (D / 2) + p] =
-            static_cast<uint8_t>(code_byte_of(x[t].w << 16, x[t].w & 0xffff0000u, ns, r));
+            static_cast<uint8_t>(code_byte_pair(x[t].w << 16, x[t].w & 0xffff0000u, ns, r));
     }
   } else if constexpr (T::kBf16) {
 #pragma unroll
@@ -396,9 +379,9 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
         const auto &p = x[2 * t + z][j >> 1], &q = x[2 * t + z + 8][j >> 1];
         if (T::kBf16 && fast) {
           if constexpr (T::kBf16)
-            c[z][j] = code_byte_of(j & 1 ? p.w & 0xffff0000u : p.w << 16,
-                                   j & 1 ? q.w & 0xffff0000u : q.w << 16, pair64(sc.x, sc.y),
-                                   pair64(sc.z, sc.w));
+            c[z][j] = code_byte_pair(j & 1 ? p.w & 0xffff0000u : p.w << 16,
+                                     j & 1 ? q.w & 0xffff0000u : q.w << 16, pair64(sc.x, sc.y),
+                                     pair64(sc.z, sc.w));
         } else if constexpr (T::kBf16) {
           c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y);
         } else {
