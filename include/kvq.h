@@ -756,8 +756,9 @@ KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *r
  * the largest product of a tile near 2^7: keys more than 11.8 nats below the maximum may
  * keep fewer bits, and those more than 18 nats below it may be dropped from the output
  * (the sum keeps them). q * sm_scale * log2(e), a K scale and their product belong below
- * 2^14 (either factor below 2^-12 has an absolute error of up to 2^-23). Other shapes run an
- * fp32 kernel.
+ * 2^14 (either factor below 2^-12 has an absolute error of up to 2^-23). Tokens
+ * that a row does not attend have no part in it, whatever they hold (but that the tokens of a
+ * group share its K scales). Other shapes run an fp32 kernel.
  */
 KVQ_API kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
                                    int32_t q_heads, int32_t n_rows, const int32_t *row_slot,

@@ -243,19 +243,26 @@ __device__ __forceinline__ void raise(State<D> &st, float mx0, float mx1) {
 
 constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
-// Exponent of a group's largest V scale (a NaN counts as large).
+// Exponent of the largest V scale of a group's first `valid` tokens (a NaN counts as large):
+// those that are not attended set no reference, whatever they hold.
 template <int D>
-__device__ __forceinline__ int scale_exponent(const uint8_t *rec, int lane) {
+__device__ __forceinline__ int scale_exponent(const uint8_t *rec, int valid, int lane) {
   const float *vs = reinterpret_cast<const float *>(rec + rec_vscale(D));
-  float x;
+  float x, y;  // of tokens lane & ~1 and the one behind it
   if constexpr (D == 128) {
-    const float4 y = reinterpret_cast<const float4 *>(vs)[lane];
-    x = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+    const float4 z = reinterpret_cast<const float4 *>(vs)[lane];
+    x = fmaxf(z.x, z.z);
+    y = fmaxf(z.y, z.w);
   } else {
-    const float2 y = reinterpret_cast<const float2 *>(vs)[lane];
-    x = fmaxf(y.x, y.y);
+    const float2 z = reinterpret_cast<const float2 *>(vs)[lane];
+    x = z.x;
+    y = z.y;
   }
-  const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(x)) >> 23) - 127;
+  if (valid < 32) {
+    if ((lane & ~1) >= valid) x = 0.0f;
+    if ((lane | 1) >= valid) y = 0.0f;
+  }
+  const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(fmaxf(x, y))) >> 23) - 127;
   return max(-24, min(40, e));
 }
 // Scales outside [2^-4, 2^9) are taken there by 2^-far, which P has instead.
@@ -848,11 +855,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
       if (at.j < at.int4) {
         const int valid = sm.valid[s][warp];
         const uint8_t *rec = stage + warp * Cfg<D>::kRecord;
-        const int ev = scale_exponent<D>(rec, lane);
+        const int ev = scale_exponent<D>(rec, 32, lane);
         if (valid >= 32 && far_of(ev) == 0)
           do_group<D, true>(st, rec, qh, 32, ev, g, t);
         else if (valid > 0)
-          do_group<D, false>(st, rec, qh, valid, ev, g, t);
+          do_group<D, false>(st, rec, qh, valid, scale_exponent<D>(rec, valid, lane), g, t);
       } else if ((warp >> 1) == (at.j & 1)) {
         const int valid = sm.valid[s][0] - 16 * (warp & 1);
         if (valid > 0)
