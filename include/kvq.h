@@ -752,10 +752,12 @@ KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *r
  * alone). n_rows <= 65,535; 0 rows are valid.
  * Kernel choice: D = 64 or 128 with BF16 windows runs on the tensor cores; products of
  * the int4 part have fp16 operands: q times the K scales (times 4 or 1/4), and
- * probabilities times the V scales, both rounded to 11 bits, against a reference that puts
- * the largest product of a tile near 2^7: keys more than 11.8 nats below the maximum may
- * keep fewer bits, and those more than 18 nats below it may be dropped from the output
- * (the sum keeps them). q * sm_scale * log2(e), a K scale and their product belong below
+ * probabilities times the V scales, both rounded to 11 bits. The reference of the
+ * probabilities puts the largest product of a key's probability and its 32-token group's
+ * largest V scale near 2^7, whatever the size of the values: keys whose product lies more than
+ * 11.8 nats below the largest may keep fewer bits, as may V scales below 2^-10 of their
+ * group's largest, and keys more than 18 nats below may be dropped from the output (the
+ * sum keeps them). q * sm_scale * log2(e), a K scale and their product belong below
  * 2^14 (either factor below 2^-12 has an absolute error of up to 2^-23). Tokens
  * that a row does not attend have no part in it, whatever they hold (but that the tokens of a
  * group share its K scales). Other shapes run an fp32 kernel.

@@ -31,9 +31,10 @@
 //
 // Softmax in the log2 domain, fp32 state. The reference of a head is raised only when
 // score + log2(largest V scale of the group) exceeds it by more than kBias + kLazy, to
-// kBias below, so products P * scale stay within fp16 (below 2^12) and keep 11 bits
-// down to 2^-17 of the largest, whatever the magnitude of V (scales that fp16 would not
-// hold well give a power of two to P).
+// kBias below. Products P * scale stay within fp16 (below 2^12), and P and the products
+// keep 11 bits down to 2^-17 of the largest, the scales down to 2^-10 of their group's: scales of
+// 2 and more, or below 2^-4, give a power of two to P, so that P has the same range of
+// exponents whatever the magnitude of V.
 //
 // 64 requests of 16 to 32 thousand tokens, 16 heads over 2 (510 MB): 90.7 us, 5.6 TB/s, of which
 // 1.5 us until a CTA has its slice, 3.8 until its first item, 6.5 TB/s then until the first
@@ -265,12 +266,15 @@ __device__ __forceinline__ int scale_exponent(const uint8_t *rec, int valid, int
   const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(fmaxf(x, y))) >> 23) - 127;
   return max(-24, min(40, e));
 }
-// Scales outside [2^-4, 2^9) are taken there by 2^-far, which P has instead.
-__device__ __forceinline__ int far_of(int ev) { return ev - max(-4, min(8, ev)); }
+// Scales outside [2^-4, 2) are taken there by 2^-far, which P has instead: P of the reference
+// is 2^7 to 2^15 then, and the smallest of its 11-bit values is 17 binades below.
+__device__ __forceinline__ int far_of(int ev) { return ev - max(-4, min(0, ev)); }
 
 // One int4 group: 32 tokens, `valid` of them attended, ev the exponent of its V scales.
-// kUsual: all are attended and far_of(ev) is 0.
-template <int D, bool kUsual>
+// kUsual: all are attended and far_of(ev) is 0. kScaled: all are attended. (64 requests of 24,576
+// tokens: 90 us with values of 0.5 to 14 at most in a group, 93 with larger or smaller ones.)
+enum GroupKind { kUsual, kScaled, kAny };
+template <int D, GroupKind kKind>
 __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
                                          const uint32_t (&qh)[D / 32][4], int valid, int ev, int g,
                                          int t) {
@@ -332,16 +336,16 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       s[mt][k] += e[k & 1];
-      if (!kUsual && 16 * mt + 8 * (k >> 1) + g >= valid) s[mt][k] = -INFINITY;
+      if (kKind == kAny && 16 * mt + 8 * (k >> 1) + g >= valid) s[mt][k] = -INFINITY;
     }
     mx0 = fmaxf(mx0, fmaxf(s[mt][0], s[mt][2]));
     mx1 = fmaxf(mx1, fmaxf(s[mt][1], s[mt][3]));
   }
   constexpr float kUnit = 4194304.0f;  // 2^22: low nibbles 2^-24 times 4, high ones 2^-20 / 4
   raise(st, fmaf(mx0, kUnit, static_cast<float>(ev)), fmaf(mx1, kUnit, static_cast<float>(ev)));
-  const int far = kUsual ? 0 : far_of(ev);
-  const float shift = kUsual ? 0.0f : static_cast<float>(far);
-  const float back = kUsual ? 1.0f : __int_as_float((127 - far) << 23);  // 2^-far
+  const int far = kKind == kUsual ? 0 : far_of(ev);
+  const float shift = kKind == kUsual ? 0.0f : static_cast<float>(far);
+  const float back = kKind == kUsual ? 1.0f : __int_as_float((127 - far) << 23);  // 2^-far
   float sum[2] = {0.0f, 0.0f}, sum16[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
@@ -354,7 +358,7 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
     }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (kUsual)
+    if (kKind == kUsual)
       st.l[k] += fmaf(sum16[k], 16.0f, sum[k]);
     else
       st.l[k] = fmaf(fmaf(sum16[k], 16.0f, sum[k]), back, st.l[k]);
@@ -370,11 +374,13 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
 #pragma unroll
       for (int f = 0; f < NB; f += 2) {
         float4 x = *reinterpret_cast<const float4 *>(vs + ((2 * mt + ps) * 4 + t) * 2 * NB + 2 * f);
-        if (!kUsual) {  // (the P of tokens not attended is 0, their scale may be anything)
+        if (kKind != kUsual) {
           x.x *= back;
           x.y *= back;
           x.z *= back;
           x.w *= back;
+        }
+        if (kKind == kAny) {  // (the P of tokens not attended is 0, their scale may be anything)
           const int tok = 16 * mt + 8 * ps + 2 * t;
           if (tok >= valid) x.x = x.z = 0.0f;
           if (tok + 1 >= valid) x.y = x.w = 0.0f;
@@ -857,9 +863,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
         const uint8_t *rec = stage + warp * Cfg<D>::kRecord;
         const int ev = scale_exponent<D>(rec, 32, lane);
         if (valid >= 32 && far_of(ev) == 0)
-          do_group<D, true>(st, rec, qh, 32, ev, g, t);
+          do_group<D, kUsual>(st, rec, qh, 32, ev, g, t);
+        else if (valid >= 32)
+          do_group<D, kScaled>(st, rec, qh, 32, ev, g, t);
         else if (valid > 0)
-          do_group<D, false>(st, rec, qh, valid, scale_exponent<D>(rec, valid, lane), g, t);
+          do_group<D, kAny>(st, rec, qh, valid, scale_exponent<D>(rec, valid, lane), g, t);
       } else if ((warp >> 1) == (at.j & 1)) {
         const int valid = sm.valid[s][0] - 16 * (warp & 1);
         if (valid > 0)

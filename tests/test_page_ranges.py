@@ -1,5 +1,5 @@
-"""kv_attend_pages on the tensor cores where magnitudes lie apart: tokens behind a row's
-position. Against 64-bit attention over
+"""kv_attend_pages on the tensor cores where magnitudes lie apart: keys far above the others
+under values of any size, tokens behind a row's position. Against 64-bit attention over
 the dequantized values; TOL_TENSOR as derived in test_pages.py (six roundings of 2^-11), which
 holds wherever probabilities and scales keep their 11 bits.
 """
@@ -11,6 +11,46 @@ torch = pytest.importorskip("torch")
 from oracle import kvq_oracle as O  # noqa: E402
 from test_pages import TOL_TENSOR, attention64, kvq  # noqa: E402,F401
 from test_pages_edges import one_request  # noqa: E402
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("each_warp", [False, True])
+@pytest.mark.parametrize("size", [0.05, 1.0, 30.0, 500.0, 3000.0, 1e5])
+def test_keys_far_above_the_others(kvq, d, each_warp, size):  # noqa: F811
+    # Sink keys 11.5 nats above the rest, with zero values, one or one in each of the groups of
+    # an item: the output is the others', which keep 11 bits down to 11.8 nats below. Channel 0
+    # alone makes the sinks' scores, so that the others differ by a tenth of a nat at most.
+    # A sink's score is one product of three factors rounded to 11 bits (q times the scale, the K
+    # scale, their product; 2^-11 each, relative): 11.5 * 3 * 2^-11 = 0.017 nats. It scales the
+    # sum of the probabilities, and with it all of the output alike, by no more than 1.7 %; what
+    # is left of the difference without that common factor is the others' own, TOL_TENSOR.
+    gen = torch.Generator(device="cuda").manual_seed(d + int(size))
+    n = 512
+    sinks = [5, 41, 77, 124] if each_warp else [77]
+    q = torch.randn((2, 8, d), generator=gen, device="cuda") * 0.02
+    q[:, :, 0] = 4.0
+    k = torch.randn((n, 1, d), generator=gen, device="cuda")
+    k[:, :, 0] = 0.0
+    k[sinks, 0, 0] = 11.5 * d ** 0.5 / 4.0
+    v = torch.randn((n, 1, d), generator=gen, device="cuda") * size
+    v[sinks] = 0.0
+    q, k, v = q.bfloat16(), k.bfloat16(), v.bfloat16()
+    cache, values = one_request(kvq, n, k, v, 0, 1, d)
+    a = np.einsum("td,rhd->rht", values[0][0], q.double().cpu().numpy()) / np.sqrt(d)
+    rest = np.delete(a, sinks, axis=2)
+    gap = a[:, :, sinks].max(2) - rest.min(2), a[:, :, sinks].min(2) - rest.max(2)
+    assert gap[0].max() < 11.8 and gap[1].min() > 11.0
+    call = kvq.AttendPages(cache, q, torch.zeros(2, dtype=torch.int32, device="cuda"),
+                           out_dtype="f32")
+    got = call.run().double().cpu().numpy()
+    assert kvq.read_status(call.status) == 0 and call.path == "pages_tensor"
+    for i in range(2):
+        want = attention64(q[i].double().cpu().numpy(), *values)
+        for h in range(8):
+            common = (got[i, h] @ want[h]) / (want[h] @ want[h])
+            assert abs(common - 1.0) <= 0.017 + TOL_TENSOR, (i, h)
+            assert O.rel_l2(got[i, h], common * want[h]) <= TOL_TENSOR, (i, h)
 
 
 @pytest.mark.gpu
