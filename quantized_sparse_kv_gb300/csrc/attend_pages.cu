@@ -244,6 +244,13 @@ __device__ __forceinline__ void raise(State<D> &st, float mx0, float mx1) {
 
 constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
+// Exponents of V scales that are told apart. Their span keeps the sum of a head, which is held
+// against a reference that counts the scales, within fp32: the weight of groups at one end against
+// groups at the other is lost (2^-126) only where it is below 2^-20 of theirs. Scales above
+// 2^kMaxExp have 2^4 of room in the products, those below 2^kMinExp lose no bits until 2^-58.
+constexpr int kMinExp = -48, kMaxExp = 52;
+__device__ __forceinline__ int held_exponent(int e) { return max(kMinExp, min(kMaxExp, e)); }
+
 // Exponent of the largest V scale of a group's first `valid` tokens (a NaN counts as large):
 // those that are not attended set no reference, whatever they hold.
 template <int D>
@@ -264,7 +271,7 @@ __device__ __forceinline__ int scale_exponent(const uint8_t *rec, int valid, int
     if ((lane | 1) >= valid) y = 0.0f;
   }
   const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(fmaxf(x, y))) >> 23) - 127;
-  return max(-24, min(40, e));
+  return held_exponent(e);
 }
 // Scales outside [2^-4, 2) are taken there by 2^-far, which P has instead: P of the reference
 // is 2^7 to 2^15 then, and the smallest of its 11-bit values is 17 binades below.

@@ -1,5 +1,6 @@
-"""kv_attend_pages on the tensor cores where magnitudes lie apart: keys far above the others
-under values of any size, tokens behind a row's position. Against 64-bit attention over
+"""kv_attend_pages on the tensor cores where magnitudes lie apart or end: keys far above the
+others under values of any size, tokens behind a row's position, values at both ends of the
+range that the header states. Against 64-bit attention over
 the dequantized values; TOL_TENSOR as derived in test_pages.py (six roundings of 2^-11), which
 holds wherever probabilities and scales keep their 11 bits.
 """
@@ -10,7 +11,7 @@ torch = pytest.importorskip("torch")
 
 from oracle import kvq_oracle as O  # noqa: E402
 from test_pages import TOL_TENSOR, attention64, kvq  # noqa: E402,F401
-from test_pages_edges import one_request  # noqa: E402
+from test_pages_edges import check_rows, one_request  # noqa: E402
 
 
 @pytest.mark.gpu
@@ -76,3 +77,36 @@ def test_tokens_behind_the_position_have_no_part(kvq, d, size):  # noqa: F811
         assert kvq.read_status(call.status) == 0 and call.path == "pages_tensor"
         want = attention64(q[0].double().cpu().numpy(), kk[:, :last + 1], vv[:, :last + 1])
         assert O.rel_l2(got[0], want) <= TOL_TENSOR, last
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1e-16, 1e-12, 1e-9, 1e10, 1e13, 1e16, 1e17])
+@pytest.mark.parametrize("window", [0, 64])
+def test_values_at_the_ends_of_the_range(kvq, d, size, window):  # noqa: F811
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    n = 640
+    k = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    v = (torch.randn((n, 1, d), generator=gen, device="cuda") * size).bfloat16()
+    # (every group's largest value is within the header's 2.4e-17 and 5e17)
+    most = v.abs().view(n, d // 32, 32).amax(-1)
+    assert 2.4e-17 < float(most.min()) and float(most.max()) < 5e17
+    cache, values = one_request(kvq, n, k, v, window, 1, d)
+    q = torch.randn((3, 8, d), generator=gen, device="cuda").bfloat16()
+    check_rows(kvq, cache, values, q, TOL_TENSOR)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_both_ends_in_one_request(kvq, d):  # noqa: F811
+    # the sum of the probabilities keeps the weight of groups whose values do not show
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    n = 1024
+    size = torch.ones(n, device="cuda")
+    size[:300], size[300:332], size[400:500], size[700:710] = 1e-16, 0.0, 1e-8, 1e17
+    k = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    v = (torch.randn((n, 1, d), generator=gen, device="cuda") * size[:, None, None]).bfloat16()
+    for order in (slice(None), torch.arange(n - 1, -1, -1, device="cuda")):
+        cache, values = one_request(kvq, n, k[order], v[order], 64, 1, d)
+        q = torch.randn((2, 8, d), generator=gen, device="cuda").bfloat16()
+        check_rows(kvq, cache, values, q, TOL_TENSOR)
