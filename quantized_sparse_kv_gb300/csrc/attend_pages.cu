@@ -242,6 +242,11 @@ __device__ __forceinline__ void raise(State<D> &st, float mx0, float mx1) {
   }
 }
 
+// A pair of fp16 with zeros for NaNs.
+__device__ __forceinline__ uint32_t no_nan(uint32_t x) {
+  return x & __heq2_mask(as_h2(x), as_h2(x));
+}
+
 constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
 // Exponents of V scales that are told apart. Their span keeps the sum of a head, which is held
@@ -251,35 +256,41 @@ constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 constexpr int kMinExp = -48, kMaxExp = 52;
 __device__ __forceinline__ int held_exponent(int e) { return max(kMinExp, min(kMaxExp, e)); }
 
-// Exponent of the largest V scale of a group's first `valid` tokens (a NaN counts as large):
-// those that are not attended set no reference, whatever they hold.
-template <int D>
+constexpr int kTopExp = 55;
+constexpr float kNoScale = 72057594037927936.0f;  // 2^(kTopExp + 1): from there on infinite
+
+// Exponent of the largest V scale of a group's first `valid` tokens. Those that are not attended
+// set no reference, whatever they hold. kSome: nor do scales from kNoScale on, whose values
+// are NaN (else such a scale is answered by its exponent).
+template <int D, bool kSome>
 __device__ __forceinline__ int scale_exponent(const uint8_t *rec, int valid, int lane) {
-  const float *vs = reinterpret_cast<const float *>(rec + rec_vscale(D));
-  float x, y;  // of tokens lane & ~1 and the one behind it
+  constexpr int V = D / 32;  // a lane's scales are of tokens lane & ~1 and the one behind it, in turn
+  float x[V];
+  const float *vs = reinterpret_cast<const float *>(rec + rec_vscale(D)) + V * lane;
   if constexpr (D == 128) {
-    const float4 z = reinterpret_cast<const float4 *>(vs)[lane];
-    x = fmaxf(z.x, z.z);
-    y = fmaxf(z.y, z.w);
+    const float4 z = *reinterpret_cast<const float4 *>(vs);
+    x[0] = z.x, x[1] = z.y, x[2] = z.z, x[3] = z.w;
   } else {
-    const float2 z = reinterpret_cast<const float2 *>(vs)[lane];
-    x = z.x;
-    y = z.y;
+    const float2 z = *reinterpret_cast<const float2 *>(vs);
+    x[0] = z.x, x[1] = z.y;
   }
-  if (valid < 32) {
-    if ((lane & ~1) >= valid) x = 0.0f;
-    if ((lane | 1) >= valid) y = 0.0f;
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (kSome && ((lane & ~1) + (i & 1) >= valid || !(x[i] < kNoScale))) x[i] = 0.0f;
+    m = fmaxf(m, x[i]);
   }
-  const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(fmaxf(x, y))) >> 23) - 127;
-  return held_exponent(e);
+  const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(m)) >> 23) - 127;
+  return kSome ? held_exponent(e) : e;
 }
 // Scales outside [2^-4, 2) are taken there by 2^-far, which P has instead: P of the reference
 // is 2^7 to 2^15 then, and the smallest of its 11-bit values is 17 binades below.
 __device__ __forceinline__ int far_of(int ev) { return ev - max(-4, min(0, ev)); }
 
 // One int4 group: 32 tokens, `valid` of them attended, ev the exponent of its V scales.
-// kUsual: all are attended and far_of(ev) is 0. kScaled: all are attended. (64 requests of 24,576
-// tokens: 90 us with values of 0.5 to 14 at most in a group, 93 with larger or smaller ones.)
+// kUsual: all are attended and far_of(ev) is 0. kScaled: all are attended and no scale reaches
+// kNoScale. (64 requests of 24,576 tokens: 90 us with values of 0.5 to 14 at most in a group, 93
+// with larger or smaller ones.)
 enum GroupKind { kUsual, kScaled, kAny };
 template <int D, GroupKind kKind>
 __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
@@ -381,13 +392,17 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
 #pragma unroll
       for (int f = 0; f < NB; f += 2) {
         float4 x = *reinterpret_cast<const float4 *>(vs + ((2 * mt + ps) * 4 + t) * 2 * NB + 2 * f);
-        if (kKind != kUsual) {
+        if (kKind == kScaled) {
           x.x *= back;
           x.y *= back;
           x.z *= back;
           x.w *= back;
-        }
-        if (kKind == kAny) {  // (the P of tokens not attended is 0, their scale may be anything)
+        } else if (kKind == kAny) {  // (the P of tokens not attended is 0, their scale may be anything)
+          const float bad = __int_as_float(0x7fffffff);
+          x.x = x.x < kNoScale ? x.x * back : bad;
+          x.y = x.y < kNoScale ? x.y * back : bad;
+          x.z = x.z < kNoScale ? x.z * back : bad;
+          x.w = x.w < kNoScale ? x.w * back : bad;
           const int tok = 16 * mt + 8 * ps + 2 * t;
           if (tok >= valid) x.x = x.z = 0.0f;
           if (tok + 1 >= valid) x.y = x.w = 0.0f;
@@ -397,8 +412,9 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
         b[ps][f + 1] = as_u32(__hmul2(as_h2(p), __floats2half2_rn(x.z, x.w)));
       }
 #pragma unroll
-    for (int f = 0; f < NB; ++f)
-      mma_f16(st.c, g == f ? kLo8 : 0u, 0u, g == f ? kHi8 : 0u, 0u, b[0][f], b[1][f]);
+    for (int f = 0; f < NB; ++f)  // (a NaN is in its block's O; here it would reach every row)
+      mma_f16(st.c, g == f ? kLo8 : 0u, 0u, g == f ? kHi8 : 0u, 0u,
+              kKind == kAny ? no_nan(b[0][f]) : b[0][f], kKind == kAny ? no_nan(b[1][f]) : b[1][f]);
 #pragma unroll
     for (int c = 0; c < NB / 2; ++c) {
       const uint4 x = *reinterpret_cast<const uint4 *>(
@@ -868,13 +884,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_pages_kernel(cons
       if (at.j < at.int4) {
         const int valid = sm.valid[s][warp];
         const uint8_t *rec = stage + warp * Cfg<D>::kRecord;
-        const int ev = scale_exponent<D>(rec, 32, lane);
+        const int ev = scale_exponent<D, false>(rec, 32, lane);
         if (valid >= 32 && far_of(ev) == 0)
           do_group<D, kUsual>(st, rec, qh, 32, ev, g, t);
-        else if (valid >= 32)
-          do_group<D, kScaled>(st, rec, qh, 32, ev, g, t);
+        else if (valid >= 32 && ev <= kTopExp)
+          do_group<D, kScaled>(st, rec, qh, 32, held_exponent(ev), g, t);
         else if (valid > 0)
-          do_group<D, kAny>(st, rec, qh, valid, scale_exponent<D>(rec, valid, lane), g, t);
+          do_group<D, kAny>(st, rec, qh, valid, scale_exponent<D, true>(rec, valid, lane), g, t);
       } else if ((warp >> 1) == (at.j & 1)) {
         const int valid = sm.valid[s][0] - 16 * (warp & 1);
         if (valid > 0)

@@ -1,6 +1,6 @@
 """kv_attend_pages on the tensor cores where magnitudes lie apart or end: keys far above the
 others under values of any size, tokens behind a row's position, values at both ends of the
-range that the header states. Against 64-bit attention over
+range that the header states, infinities in pages. Against 64-bit attention over
 the dequantized values; TOL_TENSOR as derived in test_pages.py (six roundings of 2^-11), which
 holds wherever probabilities and scales keep their 11 bits.
 """
@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import kvq_oracle as O  # noqa: E402
-from test_pages import TOL_TENSOR, attention64, kvq  # noqa: E402,F401
+from test_pages import TOL_F32, TOL_TENSOR, attention64, kvq  # noqa: E402,F401
 from test_pages_edges import check_rows, one_request  # noqa: E402
 
 
@@ -110,3 +110,34 @@ def test_both_ends_in_one_request(kvq, d):  # noqa: F811
         cache, values = one_request(kvq, n, k[order], v[order], 64, 1, d)
         q = torch.randn((2, 8, d), generator=gen, device="cuda").bfloat16()
         check_rows(kvq, cache, values, q, TOL_TENSOR)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,wdt", [(64, "bf16"), (128, "bf16"), (96, "f32")])
+@pytest.mark.parametrize("size", [float("inf"), float("-inf"), 1e30])
+def test_infinite_values_in_the_pages_stay_in_their_features(kvq, d, wdt, size):  # noqa: F811
+    # an infinite value's group has an infinite scale and code 0: NaN for its 32 features, and
+    # nothing else. (On the tensor cores a scale of 2^56 and more counts as one.)
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    n = 320
+    k = torch.randn((n, 2, d), generator=gen, device="cuda").bfloat16()
+    v = torch.randn((n, 2, d), generator=gen, device="cuda").bfloat16()
+    v[77, 1, 40] = size
+    v[200, 1, 33] = -size
+    q = torch.randn((3, 8, d), generator=gen, device="cuda").bfloat16()
+    with np.errstate(all="ignore"):
+        cache, (kk, vv) = one_request(kvq, n, k, v, 0, 2, d, wdt)
+    vv[:, :, 32:64] = 0.0
+    call = kvq.AttendPages(cache, q, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                           torch.tensor([n - 1, 76, 150], dtype=torch.int32, device="cuda"),
+                           out_dtype="f32")
+    got = call.run().double().cpu().numpy()
+    assert kvq.read_status(call.status) == 0
+    for i, m in enumerate((n, 77, 151)):
+        want = attention64(q[i].double().cpu().numpy(), kk[:, :m], vv[:, :m])
+        bad = np.zeros((8, d), bool)
+        if m > 77 and (wdt == "bf16" or np.isinf(size)):
+            bad[4:, 32:64] = True
+        assert (np.isnan(got[i])[:, 32:64] == bad[:, 32:64]).all(), i
+        got[i][:, 32:64] = 0.0
+        assert O.rel_l2(got[i], want) <= (TOL_TENSOR if wdt == "bf16" else TOL_F32), i
