@@ -761,7 +761,10 @@ KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *r
  * 2^14 (either factor below 2^-12 has an absolute error of up to 2^-23). The largest
  * value of 32 features of a token in the int4 part belongs between 2.4e-17 and 5e17 (or is
  * zero): smaller ones keep fewer bits, and larger or infinite ones make those 32 features NaN
- * in the rows that attend the token. Tokens
+ * in the rows that attend the token. Infinite
+ * keys and values in the window give what the formula gives (a score of -inf leaves its token
+ * out, +inf has no softmax: NaN; an infinite value is infinite in the output), but where q
+ * rounds to zero. Tokens
  * that a row does not attend have no part in it, whatever they hold (but that the tokens of a
  * group share its K scales). Other shapes run an fp32 kernel.
  */

@@ -431,8 +431,18 @@ __device__ __forceinline__ void do_group(State<D> &st, const uint8_t *rec,
   }
 }
 
-// 16 tokens of a bf16 window tile (half 0 or 1), `valid` of them attended. q and P are
-// split into two bf16 parts each (16 bits), K and V are exact.
+// x and y as two pairs of bf16 whose sum they are, q exactly and P to 15 bits. The parts of a
+// number have its sign and are zero only if it is, so that infinite keys and values come
+// out as products with the number itself.
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+  constexpr float kBelow = 1.0f - 0.0078125f;
+  const uint32_t u = __float_as_uint(x * kBelow), v = __float_as_uint(y * kBelow);
+  hi = __byte_perm(u, v, 0x7632);
+  lo = pack_bf2(x - __uint_as_float(u & 0xffff0000u), y - __uint_as_float(v & 0xffff0000u));
+}
+
+// 16 tokens of a bf16 window tile (half 0 or 1), `valid` of them attended. q (the 11 bits that
+// the int4 part has of it) and P are split into two bf16 parts each, K and V are exact.
 template <int D>
 __device__ __forceinline__ void do_window(State<D> &st, const uint16_t *tile, int half,
                                           const uint32_t (&qh)[D / 32][4], int valid, int g, int t) {
@@ -450,8 +460,7 @@ __device__ __forceinline__ void do_window(State<D> &st, const uint16_t *tile, in
       float2 f = __half22float2(as_h2(qh[i][j]));
       f.x *= j & 1 ? 4.0f : 0.25f;
       f.y *= j & 1 ? 4.0f : 0.25f;
-      hi[j] = pack_bf2(f.x, f.y);
-      lo[j] = pack_bf2(f.x - bf_lo(hi[j]), f.y - bf_hi(hi[j]));
+      split(f.x, f.y, hi[j], lo[j]);
     }
     mma_bf16(s, a.x, b.x, a.y, b.y, hi[0], hi[1]);
     mma_bf16(s, a.x, b.x, a.y, b.y, lo[0], lo[1]);
@@ -465,9 +474,9 @@ __device__ __forceinline__ void do_window(State<D> &st, const uint16_t *tile, in
   for (int k = 0; k < 4; ++k) s[k] = fast_exp2(s[k] - st.m[k & 1] - 24.0f);
   st.l[0] = fmaf(s[0] + s[2], 16777216.0f, st.l[0]);
   st.l[1] = fmaf(s[1] + s[3], 16777216.0f, st.l[1]);
-  const uint32_t xh0 = pack_bf2(s[0], s[1]), xh1 = pack_bf2(s[2], s[3]);
-  const uint32_t xl0 = pack_bf2(s[0] - bf_lo(xh0), s[1] - bf_hi(xh0));
-  const uint32_t xl1 = pack_bf2(s[2] - bf_lo(xh1), s[3] - bf_hi(xh1));
+  uint32_t xh0, xl0, xh1, xl1;
+  split(s[0], s[1], xh0, xl0);
+  split(s[2], s[3], xh1, xl1);
   const uint32_t bh0 = movmatrix_t(xh0), bh1 = movmatrix_t(xh1);
   const uint32_t bl0 = movmatrix_t(xl0), bl1 = movmatrix_t(xl1);
   // tokens that are not attended: their rows may hold anything

@@ -1,6 +1,6 @@
 """kv_attend_pages on the tensor cores where magnitudes lie apart or end: keys far above the
 others under values of any size, tokens behind a row's position, values at both ends of the
-range that the header states, infinities in pages. Against 64-bit attention over
+range that the header states, infinities in pages and windows. Against 64-bit attention over
 the dequantized values; TOL_TENSOR as derived in test_pages.py (six roundings of 2^-11), which
 holds wherever probabilities and scales keep their 11 bits.
 """
@@ -141,3 +141,58 @@ def test_infinite_values_in_the_pages_stay_in_their_features(kvq, d, wdt, size):
         assert (np.isnan(got[i])[:, 32:64] == bad[:, 32:64]).all(), i
         got[i][:, 32:64] = 0.0
         assert O.rel_l2(got[i], want) <= (TOL_TENSOR if wdt == "bf16" else TOL_F32), i
+
+
+def with_infinities(d, wdt, gen):
+    """Window keys and values with infinities under queries of known signs; what the 64-bit
+    definition makes of them."""
+    n, window = 200, 100
+    k = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    v = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    q = torch.randn((1, 4, d), generator=gen, device="cuda").bfloat16()
+    return n, window, k, v, q
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,wdt", [(64, "bf16"), (128, "bf16"), (96, "f32"), (96, "bf16")])
+@pytest.mark.parametrize("at", [100, 130, 199])
+def test_infinite_values_in_the_window(kvq, d, wdt, at):  # noqa: F811
+    gen = torch.Generator(device="cuda").manual_seed(d + at)
+    n, window, k, v, q = with_infinities(d, wdt, gen)
+    v[at, 0, 3], v[at, 0, 9] = float("inf"), float("-inf")
+    v[at, 0, 20], v[at - 3 if at > 100 else at + 3, 0, 20] = float("inf"), float("-inf")
+    cache, (kk, vv) = one_request(kvq, n, k, v, window, 1, d, wdt)
+    out, status = kvq.attend_pages(cache, q, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                   out_dtype="f32")
+    assert kvq.read_status(status) == 0
+    got = out[0].double().cpu().numpy()
+    assert (got[:, 3] == np.inf).all() and (got[:, 9] == -np.inf).all()
+    assert np.isnan(got[:, 20]).all()
+    keep = [i for i in range(d) if i not in (3, 9, 20)]
+    want = attention64(q[0].double().cpu().numpy(), kk, np.where(np.isfinite(vv), vv, 0.0))
+    assert O.rel_l2(got[:, keep], want[:, keep]) <= (TOL_TENSOR if wdt == "bf16" else TOL_F32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,wdt", [(64, "bf16"), (128, "bf16"), (96, "f32"), (96, "bf16")])
+@pytest.mark.parametrize("at", [100, 130, 199])
+@pytest.mark.parametrize("same", [False, True])
+def test_infinite_keys_in_the_window(kvq, d, wdt, at, same):  # noqa: F811
+    # a score of -inf leaves the token out, one of +inf or of both infinities has no softmax
+    gen = torch.Generator(device="cuda").manual_seed(d + at)
+    n, window, k, v, q = with_infinities(d, wdt, gen)
+    q[0, :, 5] = torch.tensor([1.0, -1.0, 0.37, -1e-3], device="cuda").bfloat16()
+    q[0, :, 17] = q[0, :, 5] if same else -q[0, :, 5]
+    k[at, 0, 5], k[at, 0, 17] = float("-inf"), float("-inf")
+    cache, (kk, vv) = one_request(kvq, n, k, v, window, 1, d, wdt)
+    out, status = kvq.attend_pages(cache, q, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                   out_dtype="f32")
+    assert kvq.read_status(status) == 0
+    got = out[0].double().cpu().numpy()
+    rest = np.delete(np.arange(n), at)
+    want = attention64(q[0].double().cpu().numpy(), kk[:, rest], vv[:, rest])
+    for h in range(4):
+        if same and h in (0, 2):
+            assert O.rel_l2(got[h], want[h]) <= (TOL_TENSOR if wdt == "bf16" else TOL_F32), h
+        else:
+            assert np.isnan(got[h]).all(), h
