@@ -110,13 +110,12 @@ __host__ __device__ __forceinline__ uint64_t pair64(float lo, float hi) {
 #endif
 }
 
-// One code byte, in bits 0-7 of the result, from the bits of two floats (lo in the low nibble),
-// each with its own scale; ns = (-s_lo, -s_hi) and r = (r_lo, r_hi) as pair64. On the device
-// the four operations run on both at once as packed f32x2 instructions (per half the same IEEE
-// operations). The low half is masked: a NaN's sum has every bit set, and would borrow from
-// the high nibble.
-__host__ __device__ __forceinline__ uint32_t code_byte_pair(uint32_t lo, uint32_t hi, uint64_t ns,
-                                                            uint64_t r) {
+// code + 8 in bits 0-3, of two floats given by their bits, in their places; each has its own
+// scale, ns = (-s_lo, -s_hi) and r = (r_lo, r_hi) as pair64. On the device the four operations
+// run on both at once as packed f32x2 instructions (per half the same IEEE operations).
+// Bits 4-7 are zero but for a NaN, whose sum has every bit set.
+__host__ __device__ __forceinline__ void code8_pair(uint32_t &lo, uint32_t &hi, uint64_t ns,
+                                                    uint64_t r) {
 #ifdef __CUDA_ARCH__
   uint64_t x, q0, e, q, y;
   asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo), "r"(hi));
@@ -136,7 +135,13 @@ __host__ __device__ __forceinline__ uint32_t code_byte_pair(uint32_t lo, uint32_
   lo = sum(lo, static_cast<uint32_t>(ns), static_cast<uint32_t>(r));
   hi = sum(hi, static_cast<uint32_t>(ns >> 32), static_cast<uint32_t>(r >> 32));
 #endif
-  return hi * 16u + (lo & 15u);
+}
+
+// One code byte of them, in bits 0-7 of the result, lo in the low nibble.
+__host__ __device__ __forceinline__ uint32_t code_byte_pair(uint32_t lo, uint32_t hi, uint64_t ns,
+                                                            uint64_t r) {
+  code8_pair(lo, hi, ns, r);
+  return hi * 16u + (lo & 15u);  // (a NaN in lo would borrow from the high nibble)
 }
 
 }  // namespace kvq

@@ -15,10 +15,11 @@
 // (token, token + 8) pairs of one feature, which is the byte a record's words hold; lanes of
 // features y and y + 8 exchange half of their bytes and each keeps half of the words. Each
 // half of the record (20 D bytes) is put together in shared memory and leaves as one bulk
-// copy. All of a thread's loads are issued before the first is used, and 16 CTAs share an
-// SM at 64 registers.
+// copy. All of a thread's loads are issued before the first is used, and with bf16 windows 16
+// CTAs share an SM at 64 registers, for which the compiler spills 44 bytes a thread (12 at D =
+// 64, 36 at other head dims; 28 to 124 with fp32 rows); with fp32 windows eight at 128.
 //
-// 112,000 rows of two heads, D = 128 (151 MB in and out): 34.6 us, 4.4 TB/s; the loads of
+// 112,000 rows of two heads, D = 128 (151 MB in and out): 33.3 us, 4.5 TB/s; the loads of
 // 32 warps an SM and 1.3 thousand instructions a half group, half of the issue slots, overlap
 // in part. Rows staged in shared memory a group ahead (49 us, 42 without as it was then), 16
 // values a thread (38) and 80 registers (56) were slower. One token of each of 64 requests:
@@ -70,6 +71,11 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// The lowest bytes of four words.
+__device__ __forceinline__ uint32_t four_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
 // A pair of values as the cache keeps them: bf16 pairs in one register.
 struct PairB {
   uint32_t w;
@@ -370,31 +376,47 @@ __device__ __forceinline__ void pack_v(const AppendPagesArgs &a, const GroupWork
   const int f = 2 * b + (e >> 2), g0 = 4 * (e & 1) + (upper ? 2 : 0);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    uint32_t c[2][4];  // byte of feature j: tokens 2t + z and 2t + z + 8
+    // bytes: features j, j + 1 of token 2t, then of 2t + 1; low nibbles are the tokens
+    // themselves, high ones those 8 behind
+    uint32_t c01 = 0, c23 = 0;
+    if constexpr (T::kBf16) {
+      if (fast) {  // (low and high codes apart: one mask for four bytes)
+        uint32_t lo[2][4], hi[2][4];
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const float4 sc = *reinterpret_cast<const float4 *>(aux + 8 * t + 4 * z);
+        for (int z = 0; z < 2; ++z) {
+          const float4 sc = *reinterpret_cast<const float4 *>(aux + 8 * t + 4 * z);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const auto &p = x[2 * t + z][j >> 1], &q = x[2 * t + z + 8][j >> 1];
-        if (T::kBf16 && fast) {
-          if constexpr (T::kBf16)
-            c[z][j] = code_byte_pair(j & 1 ? p.w & 0xffff0000u : p.w << 16,
-                                     j & 1 ? q.w & 0xffff0000u : q.w << 16, pair64(sc.x, sc.y),
-                                     pair64(sc.z, sc.w));
-        } else if constexpr (T::kBf16) {
-          c[z][j] = code_byte_div(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y);
-        } else {
-          c[z][j] = code_byte_f32(j & 1 ? p.hi() : p.lo(), j & 1 ? q.hi() : q.lo(), -sc.x, -sc.y,
-                                  sc.z, sc.w);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t p = x[2 * t + z][j >> 1].w, q = x[2 * t + z + 8][j >> 1].w;
+            lo[z][j] = j & 1 ? p & 0xffff0000u : p << 16;
+            hi[z][j] = j & 1 ? q & 0xffff0000u : q << 16;
+            code8_pair(lo[z][j], hi[z][j], pair64(sc.x, sc.y), pair64(sc.z, sc.w));
+          }
         }
+        c01 = (four_bytes(hi[0][0], hi[0][1], hi[1][0], hi[1][1]) << 4 & 0xf0f0f0f0u) |
+              (four_bytes(lo[0][0], lo[0][1], lo[1][0], lo[1][1]) & 0x0f0f0f0fu);
+        c23 = (four_bytes(hi[0][2], hi[0][3], hi[1][2], hi[1][3]) << 4 & 0xf0f0f0f0u) |
+              (four_bytes(lo[0][2], lo[0][3], lo[1][2], lo[1][3]) & 0x0f0f0f0fu);
       }
     }
-    // bytes: features j, j + 1 of token 2t, then of 2t + 1
-    const uint32_t c01 = __byte_perm(__byte_perm(c[0][0], c[0][1], 0x0040),
-                                     __byte_perm(c[1][0], c[1][1], 0x0040), 0x5410);
-    const uint32_t c23 = __byte_perm(__byte_perm(c[0][2], c[0][3], 0x0040),
-                                     __byte_perm(c[1][2], c[1][3], 0x0040), 0x5410);
+    if (!fast) {
+      uint32_t c[2][4];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const float4 sc = *reinterpret_cast<const float4 *>(aux + 8 * t + 4 * z);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const auto &p = x[2 * t + z][j >> 1], &q = x[2 * t + z + 8][j >> 1];
+          const float y0 = j & 1 ? p.hi() : p.lo(), y8 = j & 1 ? q.hi() : q.lo();
+          if constexpr (T::kBf16)
+            c[z][j] = code_byte_div(y0, y8, -sc.x, -sc.y);
+          else
+            c[z][j] = code_byte_f32(y0, y8, -sc.x, -sc.y, sc.z, sc.w);
+        }
+      }
+      c01 = four_bytes(c[0][0], c[0][1], c[1][0], c[1][1]);
+      c23 = four_bytes(c[0][2], c[0][3], c[1][2], c[1][3]);
+    }
     const uint32_t other = __shfl_xor_sync(~0u, upper ? c01 : c23, 2);
     const uint32_t lo = upper ? other : c01, hi = upper ? c23 : other;
     if (live) {
