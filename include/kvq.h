@@ -750,23 +750,27 @@ KVQ_API kvq_status kv_page_values(const kvq_paged_cache *cache, const int32_t *r
  * as it was; a page outside the pool is flagged KVQ_DEV_INDEX and its tokens skipped.
  * workspace/ws_bytes as kv_attend (the size depends on n_rows, q_heads and the cache's shape
  * alone). n_rows <= 65,535; 0 rows are valid.
- * Kernel choice: D = 64 or 128 with BF16 windows runs on the tensor cores; products of
- * the int4 part have fp16 operands: q times the K scales (times 4 or 1/4), and
- * probabilities times the V scales, both rounded to 11 bits. The reference of the
- * probabilities puts the largest product of a key's probability and its 32-token group's
- * largest V scale near 2^7, whatever the size of the values: keys whose product lies more than
- * 11.8 nats below the largest may keep fewer bits, as may V scales below 2^-10 of their
- * group's largest, and keys more than 18 nats below may be dropped from the output (the
- * sum keeps them). q * sm_scale * log2(e), a K scale and their product belong below
- * 2^14 (either factor below 2^-12 has an absolute error of up to 2^-23). The largest
- * value of 32 features of a token in the int4 part belongs between 2.4e-17 and 5e17 (or is
- * zero): smaller ones keep fewer bits, and larger or infinite ones make those 32 features NaN
- * in the rows that attend the token. Infinite
- * keys and values in the window give what the formula gives (a score of -inf leaves its token
- * out, +inf has no softmax: NaN; an infinite value is infinite in the output), but where q
- * rounds to zero. Tokens
- * that a row does not attend have no part in it, whatever they hold (but that the tokens of a
- * group share its K scales). Other shapes run an fp32 kernel.
+ * Kernel choice: D = 64 or 128 with BF16 windows runs on the tensor cores, other shapes an
+ * fp32 kernel. Either reads a request's cache once for every row and every eight query
+ * heads of a KV head. On the tensor cores:
+ *   Roundings to 11 bits, fp16's: q * sm_scale * log2(e), F32 q too; a K scale; their
+ *   product (times 4 or 1/4); a probability; a V scale; their product. In the window the
+ *   rounded q is used as well, probabilities keep 15 bits, keys and values all. Sums are fp32.
+ *   q * sm_scale * log2(e), a K scale and their product belong below 2^14 (either factor
+ *   below 2^-12 has an absolute error of up to 2^-23).
+ *   The reference of the probabilities puts the largest product of a key's probability and
+ *   its 32-token group's largest V scale near 2^7, whatever the size of the values: keys
+ *   whose product lies more than 11.8 nats below the largest may keep fewer bits, as may V
+ *   scales below 2^-10 of their group's largest, and keys more than 18 nats below may be
+ *   dropped from the output (the sum keeps them).
+ *   The largest of 32 features of a token's values in the int4 part belongs between 2.4e-17
+ *   and 5e17 (or is zero): smaller ones keep fewer bits, and larger or infinite ones make those
+ *   32 features NaN in the rows that attend the token.
+ *   Infinite keys and values in the window give what the formula gives (a score of -inf
+ *   leaves its token out, one of +inf makes the row NaN, an infinite value is infinite in the
+ *   output), but where q rounds to zero.
+ * Tokens that a row does not attend have no part in it, whatever they hold (but that the
+ * tokens of a group share its K scales). A row whose scores are all -inf is zero.
  */
 KVQ_API kvq_status kv_attend_pages(const kvq_paged_cache *cache, const void *q, int32_t q_dtype,
                                    int32_t q_heads, int32_t n_rows, const int32_t *row_slot,

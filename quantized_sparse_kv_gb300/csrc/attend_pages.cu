@@ -1,11 +1,12 @@
 // kv_attend_pages on the tensor cores: one query row per new token over the pages and the
 // window of its request, split over the length and joined (D = 64 or 128, bf16 windows).
 //
-// Work split. A unit is (query row, KV head, up to eight of its query heads). Its items
-// are its int4 groups taken four at a time, then its window tiles of 32 tokens. The items
-// of all units lie end to end and the persistent grid (three CTAs per SM) takes equal
-// contiguous slices, whatever the requests' lengths are; each CTA finds its slice from the
-// lengths itself (one sum over the rows), so nothing about them is known to the host. A
+// Work split. A unit is (query row, KV head, up to eight of its query heads: the columns of an
+// MMA; a KV head with more is read once for every eight, and a request with several rows once
+// for each). Its items are its int4 groups taken four at a time, then its window tiles of 32
+// tokens. The items of all units lie end to end and the persistent grid (three CTAs per SM)
+// takes equal contiguous slices, whatever the requests' lengths are; each CTA finds its slice
+// from the lengths itself (one sum over the rows), so nothing about them is known to the host. A
 // unit that one CTA has from end to end is finished there; the others leave a partial
 // (maximum, sum, output before the division) per CTA, which a second kernel joins.
 //
@@ -25,9 +26,15 @@
 //
 // P V: V codes as stored (a record's words hold the four operand registers of one MMA),
 // features as rows, tokens as the inner dimension. The V scale of a (token, 32 features) is
-// multiplied into P, one copy of P per 32 features, 16 products instead of 128; the 8s come
-// off through a tile of row sums of those copies. The upper nibbles' factor 1/16 is
-// in the exponent of the second half of P.
+// multiplied into P, one copy of P per 32 features: at D = 128 16 packed products a lane and
+// group, where scaling the group's 4,096 values would take 64. The 8s come off through a tile of
+// row sums of those copies. The upper nibbles' factor 1/16 is in the exponent of the second
+// half of P.
+//
+// Roundings, each to the 11 bits of an fp16 operand: q * scale (also of fp32 q, and for the
+// window), a K scale, their product; P, a V scale, their product. P of the window keeps 15
+// bits. The sums are fp32. (A window part with 16 bits of q would need its own copy of it: 32
+// registers of 128 that are all taken.)
 //
 // Softmax in the log2 domain, fp32 state. The reference of a head is raised only when
 // score + log2(largest V scale of the group) exceeds it by more than kBias + kLazy, to

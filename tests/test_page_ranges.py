@@ -196,3 +196,21 @@ def test_infinite_keys_in_the_window(kvq, d, wdt, at, same):  # noqa: F811
             assert O.rel_l2(got[h], want[h]) <= (TOL_TENSOR if wdt == "bf16" else TOL_F32), h
         else:
             assert np.isnan(got[h]).all(), h
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,wdt", [(64, "bf16"), (128, "bf16"), (96, "f32"), (96, "bf16")])
+def test_a_row_whose_scores_are_all_minus_infinity_is_zero(kvq, d, wdt):  # noqa: F811
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    n = 45
+    k = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    v = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    q = torch.randn((2, 2, d), generator=gen, device="cuda").bfloat16()
+    q[:, 0, 7], q[:, 1, 7] = 0.5, -0.5
+    k[:, 0, 7] = float("-inf")
+    cache, _ = one_request(kvq, n, k, v, 100, 1, d, wdt)
+    out, status = kvq.attend_pages(cache, q, torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                   torch.tensor([n - 1, 3], dtype=torch.int32, device="cuda"),
+                                   out_dtype="f32")
+    assert kvq.read_status(status) == 0
+    assert bool((out[:, 0] == 0).all()) and bool(out[:, 1].isnan().all())
