@@ -20,7 +20,7 @@
 // 64, 36 at other head dims; 28 to 124 with fp32 rows); with fp32 windows eight at 128.
 //
 // 112,000 rows of two heads, D = 128 (151 MB in and out): 33.3 us, 4.5 TB/s; the loads of
-// 32 warps an SM and 1.3 thousand instructions a half group, half of the issue slots, overlap
+// 32 warps an SM and 1.4 thousand instructions a half group, half of the issue slots, overlap
 // in part. Rows staged in shared memory a group ahead (49 us, 42 without as it was then), 16
 // values a thread (38) and 80 registers (56) were slower. One token of each of 64 requests:
 // 4.5 us, of which the launch is 2 and a group that completes the rest.
