@@ -242,6 +242,23 @@ __device__ __forceinline__ float range_sum(const float (&v)[32], int lo, int hi)
   return a + b;
 }
 
+// A bounded wait of a whole warp, whose lanes get one answer: each lane's own clock ends its
+// wait, so some may see a phase complete that others have given up. (Out of line behind a
+// first try: 0.3 % of a chunk attention's time; inlined 1.5 and 2.5, bf16 and MXFP8.)
+__device__ __noinline__ bool wait_on_as_one(int *abort_flag, uint32_t bar, uint32_t parity,
+                                            int32_t *dev_status, uint64_t limit_ns) {
+  const bool ok = mbar_wait(bar, parity, limit_ns);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (dev_status) atomicOr(dev_status, KVQ_DEV_TIMEOUT);
+  *reinterpret_cast<volatile int *>(abort_flag) = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait_as_one(int *abort_flag, uint32_t bar, uint32_t parity,
+                                            const KernelCtl &ctl) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on_as_one(abort_flag, bar, parity, ctl.dev_status, ctl.wait_limit_ns);
+}
+
 // 32 columns of the pass: P = 2^(s * scale + neg_m) for the valid ones (0
 // beyond), raw maximum, P to shared memory as bf16, the chunk's sum. Region
 // sums: byte c of offs is the offset of the one region bound inside chunk c
@@ -664,7 +681,7 @@ __device__ __forceinline__ void chunk_body(const CUtensorMap &tm_q, const CUtens
     bool ok = true;
     for (int i = 0; i < my_tiles; ++i) {
       const int j = 2 * i + g;
-      if (!wait_or_abort(abort_flag, smem_u32(&sm.s_full[g]), i & 1, a.ctl)) {
+      if (!wait_as_one(abort_flag, smem_u32(&sm.s_full[g]), i & 1, a.ctl)) {
         ok = false;
         break;
       }
@@ -673,7 +690,7 @@ __device__ __forceinline__ void chunk_body(const CUtensorMap &tm_q, const CUtens
       const int t0 = j * BN;
       // O_g += P V of the previous tile must be done before P_g is rewritten
       // or O_g is rescaled
-      if (i >= 1 && !wait_or_abort(abort_flag, smem_u32(&sm.o_done[g]), (i - 1) & 1, a.ctl)) {
+      if (i >= 1 && !wait_as_one(abort_flag, smem_u32(&sm.o_done[g]), (i - 1) & 1, a.ctl)) {
         ok = false;
         break;
       }
@@ -771,7 +788,7 @@ __device__ __forceinline__ void chunk_body(const CUtensorMap &tm_q, const CUtens
     // merges both groups' O for half of the columns (group g: 64g .. 64g + 63)
     const bool mine_ok =
         ok && (my_tiles == 0 ||
-               wait_or_abort(abort_flag, smem_u32(&sm.o_done[g]), (my_tiles - 1) & 1, a.ctl));
+               wait_as_one(abort_flag, smem_u32(&sm.o_done[g]), (my_tiles - 1) & 1, a.ctl));
     // A group's last PV is issued after the last QK, so once it has completed
     // no MMA reads Q or K stage 0 any more and the group may write over them.
     MergeState *ms = reinterpret_cast<MergeState *>(sm.q);
@@ -790,7 +807,7 @@ __device__ __forceinline__ void chunk_body(const CUtensorMap &tm_q, const CUtens
     const int other_tiles = (nt - other + 1) >> 1;
     if (mine_ok &&
         (other_tiles == 0 ||
-         wait_or_abort(abort_flag, smem_u32(&sm.o_done[other]), (other_tiles - 1) & 1, a.ctl))) {
+         wait_as_one(abort_flag, smem_u32(&sm.o_done[other]), (other_tiles - 1) & 1, a.ctl))) {
       tc_fence_after();
       const bool have_b = nt > 1;  // group B processed at least one tile (group A always)
       const float ma = ms[0].m[row], mb = have_b ? ms[1].m[row] : -CUDART_INF_F;

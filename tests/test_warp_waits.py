@@ -71,8 +71,8 @@ def test_the_reader_tells_them_apart():
         assert unvoted_waits(good) == [], good
 
 
-@pytest.mark.parametrize("name", ["attend_decode.cu", "attend_pages.cu", "attend_tree.cu",
-                                  "pack.cu"])
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC)
+                                        if f.endswith(".cu") and f != "attend_candidates.cu"))
 def test_a_warp_leaves_a_wait_as_one(name):
     with open(os.path.join(CSRC, name)) as f:
         assert unvoted_waits(f.read()) == []
