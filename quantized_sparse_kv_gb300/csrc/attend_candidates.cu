@@ -968,7 +968,9 @@ __global__ void __launch_bounds__(kUThreads, 2) cand_union_kernel(const UnionArg
     const int m0 = 16 * warp, mi = lane >> 3, rr = lane & 7;
     for (int r = 0; r < rounds; ++r) {
       const int st = r & 1;
-      if (!mbar_wait(smem_u32(&sm.full[st]), (r >> 1) & 1, a.ctl.wait_limit_ns)) {
+      // (the warp answers as one: each lane's own clock ends its wait)
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), (r >> 1) & 1,
+                                             a.ctl.wait_limit_ns))) {
         flag_error(a.ctl, KVQ_DEV_TIMEOUT);
         break;
       }

@@ -71,11 +71,14 @@ def test_the_reader_tells_them_apart():
         assert unvoted_waits(good) == [], good
 
 
-@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC)
-                                        if f.endswith(".cu") and f != "attend_candidates.cu"))
+# (the candidate union's loaders wait for slots of a thread's own, with nothing warp-wide behind)
+OWN = {"attend_candidates.cu": 1}
+
+
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC) if f.endswith(".cu")))
 def test_a_warp_leaves_a_wait_as_one(name):
     with open(os.path.join(CSRC, name)) as f:
-        assert unvoted_waits(f.read()) == []
+        assert len(unvoted_waits(f.read())) == OWN.get(name, 0)
 
 
 @pytest.mark.gpu
