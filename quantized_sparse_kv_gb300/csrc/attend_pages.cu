@@ -66,6 +66,7 @@ constexpr int kRowsHeld = 192;
 static_assert(kRowsHeld >= kThreads);
 constexpr float kBias = 7.0f, kLazy = 4.0f;
 constexpr float kNone = -1e30f;  // a reference below every score
+constexpr float kHeld = 16777216.0f;  // 2^24: O is held times its inverse until it is divided
 // -8 as the codes are read: low nibbles 2^-24, high nibbles 2^-20
 constexpr uint32_t kLo8 = 0x80088008u, kHi8 = 0x80808080u;
 
@@ -209,7 +210,7 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
 }
 template <int D>
 struct State {
-  float o[D / 16][4];  // 2^-24 O^T: tile f, features 16f + g and + 8, heads 2t and 2t + 1
+  float o[D / 16][4];  // O^T / kHeld: tile f, features 16f + g and + 8, heads 2t and 2t + 1
   float c[4];          // the 8s of row block g (< D / 32): c[0], c[1] for heads 2t, 2t + 1
   float m[2], l[2];
 };
@@ -479,8 +480,8 @@ __device__ __forceinline__ void do_window(State<D> &st, const uint16_t *tile, in
   raise(st, fmaxf(s[0], s[2]), fmaxf(s[1], s[3]));
 #pragma unroll
   for (int k = 0; k < 4; ++k) s[k] = fast_exp2(s[k] - st.m[k & 1] - 24.0f);
-  st.l[0] = fmaf(s[0] + s[2], 16777216.0f, st.l[0]);
-  st.l[1] = fmaf(s[1] + s[3], 16777216.0f, st.l[1]);
+  st.l[0] = fmaf(s[0] + s[2], kHeld, st.l[0]);
+  st.l[1] = fmaf(s[1] + s[3], kHeld, st.l[1]);
   uint32_t xh0, xl0, xh1, xl1;
   split(s[0], s[1], xh0, xl0);
   split(s[2], s[3], xh1, xl1);
@@ -789,7 +790,7 @@ __device__ __forceinline__ void close_unit(const AttendPagesArgs &a, Smem<D> &sm
 #pragma unroll
     for (int w = 0; w < kConsumers; ++w) {
       const float c = exp2f(sm.red_m[w][h] - mx);
-      sm.red_c[w][h] = c * 16777216.0f;  // O is held times 2^-24
+      sm.red_c[w][h] = c;
       ls += c * sm.red_l[w][h];
     }
     // (between two barriers: a warp that gave up waiting did so before the first)
@@ -828,7 +829,7 @@ __device__ __forceinline__ void close_unit(const AttendPagesArgs &a, Smem<D> &sm
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) acc += sm.red_c[w][h] * sm.red_o[w][hh][d];
       if (whole) {
-        const float ls = sm.red_ls[h], y = ls == 0.0f ? 0.0f : acc / ls;
+        const float ls = sm.red_ls[h], y = ls == 0.0f ? 0.0f : acc / ls * kHeld;
         const size_t o = out0 + static_cast<size_t>(h) * D + d, b = a.out_dt == KVQ_F32 ? 4 : 2;
         if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.out) + o * b, b)) continue;
         if (a.out_dt == KVQ_F32)
@@ -1005,7 +1006,7 @@ __global__ void __launch_bounds__(256) attend_pages_join_kernel(const AttendPage
       }
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = l == 0.0f ? 0.0f : kHeld / l;
   const size_t o = (static_cast<size_t>(row) * a.Hq + kvh * a.G + kApHeads * chunk + h) * D;
   const size_t b = a.out_dt == KVQ_F32 ? 4 : 2;
   if (!in_bounds(a.ctl, static_cast<const uint8_t *>(a.out) + o * b, D * b)) return;

@@ -214,3 +214,17 @@ def test_a_row_whose_scores_are_all_minus_infinity_is_zero(kvq, d, wdt):  # noqa
                                    out_dtype="f32")
     assert kvq.read_status(status) == 0
     assert bool((out[:, 0] == 0).all()) and bool(out[:, 1].isnan().all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [100, 3900])
+@pytest.mark.parametrize("size", [1e-25, 1e25, 1e36])
+def test_values_of_any_magnitude_in_the_window(kvq, d, n, size):  # noqa: F811
+    # (one CTA's unit, and one whose partials are joined)
+    gen = torch.Generator(device="cuda").manual_seed(d + n)
+    k = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+    v = (torch.randn((n, 1, d), generator=gen, device="cuda") * size).bfloat16()
+    cache, values = one_request(kvq, n, k, v, 4000, 1, d)
+    q = torch.randn((2, 8, d), generator=gen, device="cuda").bfloat16()
+    check_rows(kvq, cache, values, q, TOL_TENSOR)
