@@ -32,9 +32,8 @@
 // half of P.
 //
 // Roundings, each to the 11 bits of an fp16 operand: q * scale (also of fp32 q, and for the
-// window), a K scale, their product; P, a V scale, their product. P of the window keeps 15
-// bits. The sums are fp32. (A window part with 16 bits of q would need its own copy of it: 32
-// registers of 128 that are all taken.)
+// window, which has no copy of q of its own), a K scale, their product; P, a V scale, their
+// product. P of the window keeps 15 bits. The sums are fp32.
 //
 // Softmax in the log2 domain, fp32 state. The reference of a head is raised only when
 // score + log2(largest V scale of the group) exceeds it by more than kBias + kLazy, to
